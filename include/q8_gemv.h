@@ -316,6 +316,115 @@ q8_status q8_repack_f16(const void *blocks, int K, int N, int8_t *q, float *s);
  * |r| <= 127 and r * d == w exactly.  Any failure returns Q8_ERR_NOT_Q8_0 (q and s then hold no meaning). */
 q8_status q8_quantize(const double *w, int K, int N, int8_t *q, float *s);
 
+/* ---------------------------------------------------------------------------------------------------------------
+ * Between the q/k/v products and the output projection: a paged key-value cache, the rotation and the append that
+ * fill it, and the attention that reads it.  No counterpart on the pages beyond their key-value rows ("plan.rs"); the
+ * formulas are stated with each call.
+ * ------------------------------------------------------------------------------------------------------------- */
+
+/* A paged key-value cache.  A page holds `page_size` consecutive tokens of one request for all its heads:
+ *   bf16 (k_scale and v_scale NULL):  k, v  bf16 [pages][heads][page_size][dim]
+ *   Q8_0 (both given):                k, v  int8 of that shape, and fp32 k_scale, v_scale
+ *                                     [pages][heads][page_size][dim / 32]: value = code * scale, the form of
+ *                                     q8_quantize_act taken over each 32 values of a head (1.125 bytes a value)
+ * page_stride is the number of values from one page to the next (heads * page_size * dim when pages are dense, more
+ * when several caches share an allocation); the scales' pages are page_stride / 32 apart.
+ *   dim 64 or 128; page_size a positive multiple of 16; page_stride a multiple of dim, at least heads * page_size *
+ *   dim; k, v and the scales 16-byte aligned.
+ * A token's slot is page * page_size + its offset in the page.  A block table is int32 [requests][table_width] (rows
+ * table_pitch apart): entry i of a request is the page of its tokens i * page_size and on.  An entry outside
+ * [0, pages) names no page: attention sees no token there.  Offsets are 64-bit throughout. */
+typedef struct {
+    void *k, *v;
+    float *k_scale, *v_scale;
+    int64_t page_stride;
+    int pages, heads, page_size, dim;
+} q8_kv_cache;
+
+/* The most requests one call takes. */
+#define Q8_MAX_REQUESTS 16384
+
+/* Block tables and slot maps of one step, from the requests' lengths, on the device.  For request r with cached[r]
+ * tokens in the cache and fresh[r] new ones (negative lengths count as 0):
+ *   have = ceil(cached / page_size), want = min(table_width, ceil((cached + fresh) / page_size)),
+ *   need = max(0, want - have), base = the sum of the requests' needs before r,
+ *   table[r][have + i] = free_pages[head + base + i] for i < need (-1 where that index is not below n_free),
+ *   lens[r] = cached + fresh, row_start[r] = the sum of fresh before r (row_start[R] = the total),
+ *   and the row row_start[r] + i of the step's `rows` rows, i < fresh:
+ *   positions = cached + i, slots = table[r][position / page_size] * page_size + position % page_size, or -1 where
+ *   that entry is missing (beyond table_width, or the free list ran out).
+ * Rows past the total are padding: positions and slots -1 (q8_rope_append skips them), so a step captured in a graph
+ * can keep a fixed row count.  next_head = head + the sum of the needs: it passes n_free when the list ran out.
+ *   cached, fresh  device, int32 [R], 1 <= R <= Q8_MAX_REQUESTS      free_pages  device, int32 [n_free] (may be NULL
+ *   head           device, int32 [1], or NULL for 0                                  when n_free is 0)
+ *   table          device, int32 [R][table_width], rows table_pitch apart (entries below `have` read, new ones written)
+ *   lens int32 [R], row_start int32 [R + 1], positions int32 [rows], slots int64 [rows], next_head int32 [1]: device,
+ *   written; none may overlap an input or another output.  The sums must stay below 2^31.
+ * Errors: Q8_ERR_ARG (NULL pointers, overlaps), Q8_ERR_SHAPE (R, page_size, table_width, table_pitch < table_width,
+ * rows < 0, n_free < 0), Q8_ERR_ALIGN (a pointer not aligned to its type), Q8_ERR_CUDA. */
+q8_status q8_kv_slots(const int *cached, const int *fresh, int R, int page_size, const int *free_pages, int n_free,
+                      const int *head, int *table, int table_width, int table_pitch, int rows, int *lens,
+                      int *row_start, int *positions, int64_t *slots, int *next_head, q8_stream_t stream);
+
+/* Flags of q8_rope_append. */
+#define Q8_ROPE_INTERLEAVED 1u /* rotate the pairs (2i, 2i + 1); without it the halves (i, i + rotary_dim / 2) */
+
+/* Norms of q and k per head, the rotation to their positions, and the write of k and v into the cache, in one pass
+ * over the fp32 outputs of the q/k/v products.  For each head's `dim` values x of row t:
+ *   u = x / sqrt(mean(x^2) + eps) * gamma          (q with q_gamma, k with k_gamma; u = x where gamma is NULL)
+ *   (a, b) -> (a cos - b sin, a sin + b cos)       on the rotary_dim / 2 pairs of u's first rotary_dim values, with
+ *   cos = table[position][i], sin = table[position][rotary_dim / 2 + i] for pair i
+ * q is rounded to bf16 into q_out; k (normed, rotated) and v (as it is) are written at the row's slot in the cache's
+ * type: bf16, or codes and scales by the rule of q8_quantize_act taken on the fp32 values.
+ *   q          device, fp32 [rows][ldq], heads at column head * dim (q_heads of them); k, v likewise (cache->heads)
+ *   q_gamma, k_gamma  device, fp32 [dim], or NULL        table  device, fp32 [max_positions][rotary_dim], or NULL
+ *   positions  device, int32 [rows]    slots  device, int64 [rows]     when rotary_dim is 0
+ *   q_out      device, bf16 [rows][ldo] (written)
+ *   1 <= rows <= 65535; rotary_dim a multiple of 8, 0 .. dim; ldq, ldk, ldv multiples of 4, ldo of 8; all pointers 16-byte aligned
+ *   (positions 4, slots 8, gammas 16)
+ * A row with a negative position is padding: its q is written as zeros and nothing goes to the cache.  A row with a
+ * slot outside the cache writes nothing to it.  A position past the table gives NaN in the rotated values.  Two rows
+ * with one slot leave either's values there.
+ * Errors: Q8_ERR_ARG (NULL pointers, unknown flags, eps < 0 or not finite, q_out overlapping an input or the cache),
+ * Q8_ERR_SHAPE, Q8_ERR_ALIGN, Q8_ERR_CUDA. */
+q8_status q8_rope_append(const float *q, int ldq, const float *k, int ldk, const float *v, int ldv,
+                         const float *q_gamma, const float *k_gamma, float eps, const float *table, int max_positions,
+                         int rotary_dim, const int *positions, const int64_t *slots, void *q_out, int ldo,
+                         const q8_kv_cache *cache, int rows, int q_heads, unsigned int flags, q8_stream_t stream);
+
+/* Bytes of device workspace the attention calls take: a constant.  The caller zeroes it once before its first use
+ * (the calls leave its counters at zero) and gives calls that may overlap on the GPU one each. */
+int64_t q8_attn_workspace_bytes(void);
+
+/* Attention of one new token a request over the paged cache (grouped heads: query head h reads cache head
+ * h / (q_heads / cache->heads)):
+ *   out[r] = sum_j w_j v_j,   w = softmax over the visible j of scale * (q[r] . k_j)
+ * where request r's token has position p = lens[r] - 1 and key j < lens[r] is visible when
+ *   window == 0, or p - j < window, or j < sinks
+ * and its page is in the table.  A row that sees nothing (lens[r] <= 0) gets zeros.  Scores, softmax statistics and
+ * sums are fp32; the result is rounded once to bf16.  What is not visible is not read into the result, whatever its
+ * bits.
+ *   q, out  device, bf16 [R][ldq], [R][ldo]: heads at column head * dim; q_heads a multiple of cache->heads
+ *   block_table  device, int32 [R][table_width], rows table_pitch apart      lens  device, int32 [R]
+ *   window >= 0, sinks >= 0 (ignored when window is 0); scale finite
+ *   workspace  device, q8_attn_workspace_bytes() bytes, 16-byte aligned
+ * A long cache is split over the SMs and its parts joined in a fixed order: results do not depend on timing.
+ * Errors: Q8_ERR_ARG (NULL pointers, a scale not finite, out overlapping an input, window or sinks < 0),
+ * Q8_ERR_SHAPE (R outside 1..Q8_MAX_REQUESTS, heads, dims, widths or pitches), Q8_ERR_ALIGN, Q8_ERR_CUDA. */
+q8_status q8_attn_decode(const void *q, int ldq, const q8_kv_cache *cache, const int *block_table, int table_width,
+                         int table_pitch, const int *lens, void *out, int ldo, int R, int q_heads, float scale,
+                         int window, int sinks, void *workspace, q8_stream_t stream);
+
+/* Attention of a chunk of new tokens, rows row_start[r] .. row_start[r + 1] - 1 being request r's last
+ * n = row_start[r + 1] - row_start[r] tokens: row row_start[r] + i has position p = lens[r] - n + i and sees key j <= p
+ * by the rule of q8_attn_decode (window, sinks, missing pages).  The chunk's own keys are in the cache already.
+ *   q, out  device, bf16 [rows][ldq], [rows][ldo]      row_start  device, int32 [R + 1], ascending from 0, at most rows
+ * Rows past row_start[R] are padding and get zeros, as do rows that see nothing.  Other arguments, errors: as
+ * q8_attn_decode; rows >= 1. */
+q8_status q8_attn_prefill(const void *q, int ldq, const q8_kv_cache *cache, const int *block_table, int table_width,
+                          int table_pitch, const int *lens, const int *row_start, void *out, int ldo, int rows, int R,
+                          int q_heads, float scale, int window, int sinks, void *workspace, q8_stream_t stream);
+
 /* Reads the device fault word of the current device: nonzero when a kernel's bounded wait on a pipeline barrier ran
  * out (bit 0: a consumer waited about two seconds for a stage's data; bit 1: the producer waited as long for a free
  * stage; bit 2: a wait of the prefill GEMM ran out) and the kernel finished early -- that call's outputs are then

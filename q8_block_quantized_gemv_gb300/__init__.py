@@ -10,6 +10,9 @@ C++ host code (repack, quantize).  PyTorch supplies device memory and streams.  
 * :func:`quantize_act` -- ``q8_quantize_act``: the quantized form of an activation (int8 values and an fp32 scale per
   32, "plan.rs" ``QBLOCK``); every product function takes the :class:`QuantAct` it returns in place of bf16 x
   (``Q8_FLAG_Q8_ACT``, tiled weights);
+* :class:`KVCache`, :func:`kv_slots`, :func:`rope_table`, :func:`rope_append`, :func:`attn_decode`,
+  :func:`attn_prefill` -- what lies between the q/k/v products and the output projection: a paged key-value cache
+  (bf16 or Q8_0), its block tables and slots, the append with norms and rotation, and the attention over it;
 * :func:`repack` -- ``q8_repack``: 36-byte checkpoint blocks -> (q, s) on the host;
 * :func:`quantize` -- ``q8_quantize``: the Q8_0 rule of "from_q8.rs" ``quantize`` on the host.
 
@@ -63,6 +66,12 @@ SIGNATURES = {
     "q8_plan_glu_launches": (_I, [_I, _I, _I, ctypes.c_uint]),
     "q8_set_tuning": (_I, [_I, _I]),
     "q8_get_tuning": (_I, [_I]),
+    "q8_kv_slots": (_I, [_P, _P, _I, _I, _P, _I, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P, _P]),
+    "q8_rope_append": (_I, [_P, _I, _P, _I, _P, _I, _P, _P, ctypes.c_float, _P, _I, _I, _P, _P, _P, _I, _P, _I, _I,
+                            ctypes.c_uint, _P]),
+    "q8_attn_workspace_bytes": (ctypes.c_int64, []),
+    "q8_attn_decode": (_I, [_P, _I, _P, _P, _I, _I, _P, _P, _I, _I, _I, ctypes.c_float, _I, _I, _P, _P]),
+    "q8_attn_prefill": (_I, [_P, _I, _P, _P, _I, _I, _P, _P, _P, _I, _I, _I, _I, ctypes.c_float, _I, _I, _P, _P]),
 }
 
 
@@ -444,6 +453,237 @@ def gemv_residual_norm_noalloc(x, q, s, N: int, residual, gamma, eps: float, h, 
                                                N, _flags(constant_weights, True, x), _stream_handle(stream)),
            "q8_gemv_residual_norm_noalloc")
     return h, out_bf16
+
+
+class _KV(ctypes.Structure):
+    _fields_ = [("k", _P), ("v", _P), ("k_scale", _P), ("v_scale", _P), ("page_stride", ctypes.c_int64),
+                ("pages", _I), ("heads", _I), ("page_size", _I), ("dim", _I)]
+
+
+FLAG_ROPE_INTERLEAVED = 1
+
+
+class KVCache:
+    """A paged key-value cache (q8_kv_cache): k and v, CUDA tensors [pages, heads, page_size, dim], bfloat16, or int8
+    with k_scale and v_scale, float32 [pages, heads, page_size, dim / 32].  Pages may be apart (views of a larger
+    allocation), everything inside a page is contiguous.  :meth:`empty` allocates one."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        import torch
+        q8 = k_scale is not None
+        if k.dim() != 4 or k.shape != v.shape:
+            raise ValueError("k and v must be [pages, heads, page_size, dim]")
+        pages, heads, page_size, dim = k.shape
+        dense = heads * page_size * dim
+        stride = k.stride(0) if pages > 1 else dense
+        for x, shape, ps in ((k, k.shape, stride), (v, k.shape, stride)) + (
+                ((k_scale, (*k.shape[:3], dim // Q8_BLOCK), stride // Q8_BLOCK),
+                 (v_scale, (*k.shape[:3], dim // Q8_BLOCK), stride // Q8_BLOCK)) if q8 or v_scale is not None else ()):
+            if x is None or not x.is_cuda or x.device != k.device or tuple(x.shape) != tuple(shape):
+                raise ValueError("k, v and the scales must be CUDA tensors of one device, the scales [..., dim / 32]")
+            if pages and not x[0].is_contiguous() or (pages > 1 and x.stride(0) != ps):
+                raise ValueError("a page must be contiguous, and the pages of k, v and the scales equally far apart")
+        want = torch.int8 if q8 else torch.bfloat16
+        if k.dtype != want or v.dtype != want or (q8 and (k_scale.dtype, v_scale.dtype) != (torch.float32,) * 2):
+            raise TypeError("k and v must be bfloat16, or int8 with float32 scales")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.pages, self.heads, self.page_size, self.dim, self.device = pages, heads, page_size, dim, k.device
+        self._c = _KV(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if q8 else None,
+                      v_scale.data_ptr() if q8 else None, stride, pages, heads, page_size, dim)
+        self._ref = ctypes.addressof(self._c)
+
+    @classmethod
+    def empty(cls, pages: int, heads: int, page_size: int, dim: int, dtype: str = "bf16", device="cuda"):
+        """A zeroed cache of the given type, "bf16" or "q8"."""
+        import torch
+        shape = (pages, heads, page_size, dim)
+        if dtype == "bf16":
+            return cls(*(torch.zeros(shape, dtype=torch.bfloat16, device=device) for _ in range(2)))
+        if dtype != "q8":
+            raise ValueError("dtype must be \"bf16\" or \"q8\"")
+        sshape = (pages, heads, page_size, dim // Q8_BLOCK)
+        return cls(*(torch.zeros(shape, dtype=torch.int8, device=device) for _ in range(2)),
+                   *(torch.zeros(sshape, dtype=torch.float32, device=device) for _ in range(2)))
+
+
+def _ints(name, t, n=None):
+    import torch
+    if not t.is_cuda or t.dtype != torch.int32 or not t.is_contiguous() or (n is not None and t.numel() != n):
+        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor" + (f" of {n} values" if n is not None else ""))
+    return t.data_ptr()
+
+
+def _table_of(table, R):
+    import torch
+    if not table.is_cuda or table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != R or \
+            (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError(f"the block table must be an int32 CUDA tensor [{R}, width] with unit column stride")
+    return table.data_ptr(), table.shape[1], table.stride(0) if R > 1 else table.shape[1]
+
+
+def kv_slots(cached, fresh, table, free_pages, page_size: int, rows: int, head=None, stream=None, out=None):
+    """Block tables and slot maps of one step (q8_kv_slots): request r has cached[r] tokens in the cache and fresh[r]
+    new ones (int32 [R]); new pages come from free_pages[head:] and are written into ``table`` (int32 [R, width]) in
+    place.  Returns a dict of CUDA tensors: table, lens int32 [R], row_start int32 [R + 1], positions int32 [rows],
+    slots int64 [rows] (rows past the total: -1), head int32 [1], the next step's.  ``out``: such a dict to write."""
+    import torch
+    R = cached.numel()
+    c, f = _ints("cached", cached), _ints("fresh", fresh, R)
+    t, width, pitch = _table_of(table, R)
+    if out is None:
+        dev = cached.device
+        new = torch.empty((2 * R + 2 + rows,), dtype=torch.int32, device=dev)
+        out = {"table": table, "lens": new[:R], "row_start": new[R:2 * R + 1], "positions": new[2 * R + 2:],
+               "slots": torch.empty((rows,), dtype=torch.int64, device=dev), "head": new[2 * R + 1:2 * R + 2]}
+    elif out["slots"].dtype != torch.int64 or out["slots"].numel() != rows or not out["slots"].is_contiguous() \
+            or not out["slots"].is_cuda or out["table"] is not table:
+        raise ValueError("out must hold this table and contiguous CUDA tensors of the sizes kv_slots returns")
+    _check(lib().q8_kv_slots(c, f, R, page_size, _ints("free_pages", free_pages), free_pages.numel(),
+                             None if head is None else _ints("head", head, 1), t, width, pitch, rows,
+                             _ints("lens", out["lens"], R), _ints("row_start", out["row_start"], R + 1),
+                             _ints("positions", out["positions"], rows), out["slots"].data_ptr(),
+                             _ints("head", out["head"], 1), _stream_handle(stream)), "q8_kv_slots")
+    return out
+
+
+def rope_table(positions: int, rotary_dim: int, base: float = 10000.0, scaling=None, device="cuda"):
+    """The rotation table of q8_rope_append: fp32 [positions, rotary_dim], row p holding cos(p f_i) for the
+    rotary_dim / 2 pairs i, then sin(p f_i), with f_i = base ** (-2 i / rotary_dim); computed in fp64 on the host, so
+    the angles of long positions keep their precision.  ``scaling`` stretches it for contexts longer than trained:
+
+    * ("linear", s): positions divided by s (position interpolation);
+    * ("ntk", s): base times s ** (rotary_dim / (rotary_dim - 2)): the slowest pair is stretched by s, the fastest kept;
+    * ("parts", s, trained[, fast, slow[, amplitude]]): pair by pair, by the turns trained * f_i / (2 pi) it makes over
+      the trained length: more than ``fast`` (32) turns keep f_i, fewer than ``slow`` (1) take f_i / s, a linear ramp
+      over the pair index between; cos and sin times ``amplitude`` (0.1 ln s + 1)."""
+    import torch
+    if rotary_dim % 2 or rotary_dim < 2 or positions < 1:
+        raise ValueError("rotary_dim must be even and positive, positions at least 1")
+    i = np.arange(rotary_dim // 2, dtype=np.float64)
+    amplitude = 1.0
+    kind = scaling[0] if scaling else None
+    if kind == "ntk":
+        base = base * float(scaling[1]) ** (rotary_dim / (rotary_dim - 2)) if rotary_dim > 2 else base
+    f = base ** (-2.0 * i / rotary_dim)
+    if kind == "linear":
+        f = f / float(scaling[1])
+    elif kind == "parts":
+        s, trained = float(scaling[1]), float(scaling[2])
+        fast, slow = (float(scaling[3]), float(scaling[4])) if len(scaling) > 4 else (32.0, 1.0)
+        amplitude = float(scaling[5]) if len(scaling) > 5 else 0.1 * np.log(s) + 1.0 if s > 1 else 1.0
+        at = [rotary_dim * np.log(trained / (2 * np.pi * turns)) / (2 * np.log(base)) for turns in (fast, slow)]
+        low, high = max(np.floor(at[0]), 0.0), min(np.ceil(at[1]), rotary_dim - 1.0)
+        ramp = np.clip((i - low) / max(high - low, 1e-3), 0.0, 1.0)
+        f = f * (1.0 - ramp) + f / s * ramp
+    elif kind not in (None, "ntk"):
+        raise ValueError(f"unknown scaling {scaling[0]!r}")
+    angle = np.arange(positions, dtype=np.float64)[:, None] * f
+    both = np.concatenate([np.cos(angle), np.sin(angle)], axis=1) * amplitude
+    return torch.from_numpy(both.astype(np.float32)).to(device)
+
+
+def _rows2(name, x, dtype, cols):
+    if not x.is_cuda or x.dtype != dtype or x.dim() != 2 or x.shape[1] < cols or x.stride(1) != 1:
+        raise ValueError(f"{name} must be a 2-D {dtype} CUDA tensor of at least {cols} columns, unit column stride")
+    return x.data_ptr(), x.stride(0) if x.shape[0] > 1 else x.shape[1]
+
+
+def rope_append(q, k, v, cache: KVCache, positions, slots, table=None, q_heads: int | None = None,
+                interleaved: bool = False, q_gamma=None, k_gamma=None, eps: float = 1e-6, out=None, stream=None):
+    """Norms of q and k per head, their rotation, and the append of k and v to the cache (q8_rope_append).  q, k, v:
+    the products' fp32 outputs [rows, >= heads * dim] (q_heads defaults to q's columns / dim); positions int32 [rows],
+    slots int64 [rows] (:func:`kv_slots`); ``table``: :func:`rope_table`, its width the rotated part of a head (None:
+    no rotation).  Returns q, bf16 [rows, q_heads * dim]."""
+    import torch
+    dim = cache.dim
+    if q_heads is None:
+        q_heads = q.shape[1] // dim
+    rows, n = q.shape[0], q_heads * dim
+    qp, ldq = _rows2("q", q, torch.float32, max(n, 1))
+    kp, ldk = _rows2("k", k, torch.float32, cache.heads * dim)
+    vp, ldv = _rows2("v", v, torch.float32, cache.heads * dim)
+    if k.shape[0] != rows or v.shape[0] != rows:
+        raise ValueError("q, k and v must have the same rows")
+    if not slots.is_cuda or slots.dtype != torch.int64 or slots.numel() != rows or not slots.is_contiguous():
+        raise ValueError("slots must be a contiguous int64 CUDA tensor of one value a row")
+    pos = _ints("positions", positions, rows)
+    for g in (q_gamma, k_gamma):
+        if g is not None and (not g.is_cuda or g.dtype != torch.float32 or g.numel() != dim or not g.is_contiguous()):
+            raise ValueError("a gamma must be a contiguous fp32 CUDA tensor of dim values")
+    if table is not None and (not table.is_cuda or table.dtype != torch.float32 or table.dim() != 2
+                              or not table.is_contiguous()):
+        raise ValueError("table must be a contiguous fp32 CUDA tensor [positions, rotary_dim]")
+    if out is None:
+        out = torch.empty((rows, n), dtype=torch.bfloat16, device=q.device)
+    elif out.shape[0] != rows:
+        raise ValueError("out must have q's rows")
+    op, ldo = _rows2("out", out, torch.bfloat16, max(n, 1))
+    if rows == 0:
+        return out
+    _check(lib().q8_rope_append(qp, ldq, kp, ldk, vp, ldv, None if q_gamma is None else q_gamma.data_ptr(),
+                                None if k_gamma is None else k_gamma.data_ptr(), float(eps),
+                                None if table is None else table.data_ptr(), 0 if table is None else table.shape[0],
+                                0 if table is None else table.shape[1], pos, slots.data_ptr(), op, ldo, cache._ref,
+                                rows, q_heads, FLAG_ROPE_INTERLEAVED if interleaved else 0, _stream_handle(stream)),
+           "q8_rope_append")
+    return out
+
+
+def attn_workspace(device="cuda"):
+    """A zeroed workspace for attn_decode and attn_prefill (q8_attn_workspace_bytes); keep one per stream."""
+    import torch
+    return torch.zeros((int(lib().q8_attn_workspace_bytes()),), dtype=torch.uint8, device=device)
+
+
+def _attn(q, cache, R, table, lens, q_heads, scale, out, workspace):
+    import torch
+    if q_heads is None:
+        q_heads = q.shape[1] // cache.dim
+    n = q_heads * cache.dim
+    qp, ldq = _rows2("q", q, torch.bfloat16, max(n, 1))
+    tp, width, pitch = _table_of(table, R)
+    if out is None:
+        out = torch.empty((q.shape[0], n), dtype=torch.bfloat16, device=q.device)
+    elif out.shape[0] != q.shape[0]:
+        raise ValueError("out must have q's rows")
+    op, ldo = _rows2("out", out, torch.bfloat16, max(n, 1))
+    if workspace is None:
+        workspace = attn_workspace(q.device)
+    elif not workspace.is_cuda or not workspace.is_contiguous() or \
+            workspace.numel() * workspace.element_size() < lib().q8_attn_workspace_bytes():
+        raise ValueError("workspace must come from attn_workspace")
+    scale = float(cache.dim ** -0.5 if scale is None else scale)
+    return (qp, ldq, cache._ref, tp, width, pitch, _ints("lens", lens, R)), (op, ldo), q_heads, scale, out, workspace
+
+
+def attn_decode(q, cache: KVCache, table, lens, q_heads: int | None = None, scale: float | None = None,
+                window: int = 0, sinks: int = 0, out=None, workspace=None, stream=None):
+    """Attention of one new token a request over its pages (q8_attn_decode): q bf16 [R, >= q_heads * dim], block table
+    int32 [R, width], lens int32 [R] (the new token included; 0: an idle row, which gets zeros).  ``window``: keys that
+    far back or more are hidden (0: none), but for the first ``sinks``.  ``scale`` defaults to dim ** -0.5.
+    ``workspace``: :func:`attn_workspace`, one per stream (None: allocated and zeroed for this call).  Returns bf16
+    [R, q_heads * dim], the output projection's activation."""
+    R = q.shape[0]
+    a, o, q_heads, scale, out, workspace = _attn(q, cache, R, table, lens, q_heads, scale, out, workspace)
+    if R == 0:
+        return out
+    _check(lib().q8_attn_decode(*a, *o, R, q_heads, scale, window, sinks, workspace.data_ptr(),
+                                _stream_handle(stream)), "q8_attn_decode")
+    return out
+
+
+def attn_prefill(q, cache: KVCache, table, lens, row_start, q_heads: int | None = None, scale: float | None = None,
+                 window: int = 0, sinks: int = 0, out=None, workspace=None, stream=None):
+    """Causal attention of a chunk of new tokens over the pages (q8_attn_prefill): rows row_start[r] .. row_start[r+1]
+    of q are the last tokens of request r, whose keys are in the cache already; row_start int32 [R + 1], lens int32
+    [R].  Rows past row_start[R] get zeros.  Other arguments as :func:`attn_decode`."""
+    R = lens.numel()
+    a, o, q_heads, scale, out, workspace = _attn(q, cache, R, table, lens, q_heads, scale, out, workspace)
+    if q.shape[0] == 0:
+        return out
+    _check(lib().q8_attn_prefill(*a, _ints("row_start", row_start, R + 1), *o, q.shape[0], R, q_heads, scale, window,
+                                 sinks, workspace.data_ptr(), _stream_handle(stream)), "q8_attn_prefill")
+    return out
 
 
 def residual_norm_launches() -> int:
