@@ -3,8 +3,10 @@
 #include <cuda_bf16.h>
 #include <math.h>
 
+#include <atomic>
+
+#include "q8_attn.h"
 #include "q8_device.cuh"
-#include "q8_kv.h"
 
 namespace q8 {
 namespace {
@@ -132,9 +134,21 @@ q8_status attn_args(AttnArgs *a, const void *q, int ldq, const q8_kv_cache *c, c
 }
 
 }  // namespace
+
+cudaError_t sm_count_of_device(int *sms) {
+    static std::atomic<int> cache[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64 && (*sms = cache[dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+    e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess && dev >= 0 && dev < 64) cache[dev].store(*sms, std::memory_order_relaxed);
+    return e;
+}
+
 }  // namespace q8
 
-extern "C" int64_t q8_attn_workspace_bytes(void) { return 64ll << 20; }
+extern "C" int64_t q8_attn_workspace_bytes(void) { return q8::kAttnWorkspaceBytes; }
 
 extern "C" q8_status q8_attn_decode(const void *q, int ldq, const q8_kv_cache *cache, const int *block_table,
                                     int table_width, int table_pitch, const int *lens, void *out, int ldo, int R,
@@ -144,7 +158,7 @@ extern "C" q8_status q8_attn_decode(const void *q, int ldq, const q8_kv_cache *c
     q8_status st = q8::attn_args(&a, q, ldq, cache, block_table, table_width, table_pitch, lens, nullptr, out, ldo, R,
                                  R, q_heads, scale, window, sinks, workspace);
     if (st != Q8_OK) return st;
-    const cudaError_t e = q8::launch_rows(a, cache->dim, q8::kv_is_q8(cache), (cudaStream_t)stream);
+    const cudaError_t e = q8::launch_attn_decode(a, cache->dim, q8::kv_is_q8(cache), (cudaStream_t)stream);
     return e == cudaSuccess ? Q8_OK : q8::kv_cuda_fail(e);
 }
 

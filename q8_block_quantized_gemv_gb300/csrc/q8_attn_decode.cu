@@ -1,0 +1,721 @@
+// q8_attn_decode: attention of one new token a request over the paged cache, split over the cache's length and joined.
+//
+// Every visible key and value is read once for all query heads of its cache head, 4 flops a byte and head: HBM bounds
+// the kernel until contexts are so short that latency does.  So the work is cut by bytes, not by requests: the visible
+// tokens of all (request, cache head) items in a row are a list of 16-token units, and each CTA (one per SM) takes an
+// equal contiguous span of it, computed on the device from lens.  Its 8 warps take the span's units in turn, each
+// with a ring of its own in shared memory filled by cp.async (prefetch runs on across items; no CTA barrier but at an
+// item's end), a running maximum and sum, and accumulators in registers.
+//
+// Products run transposed on mma.sync m16n8k16, as 16 tokens (or 16 of the head's values) by 8 query heads: a unit's
+// S^T = K Q^T, then O^T += V^T P^T, so up to 8 heads sharing a cache head cost what one does.  tcgen05 has nothing to
+// add: its smallest tile is 64 rows, and one to 16 query rows leave the tensor pipe nearly idle either way.
+//
+// At an item's end the warps' parts are summed through shared memory in warp order.  An item that crosses spans
+// leaves parts in the workspace; the CTA that arrives last (a counter per first CTA, left at zero) adds them in span
+// order, so the result does not depend on who was last.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include "q8_attn.h"
+#include "q8_device.cuh"
+
+namespace q8 {
+namespace {
+
+constexpr int kUnit = 16;  // tokens of a unit; a page holds whole units
+constexpr int kMinSpan = 16;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kSlack = 8.0f;  // log2: the running maximum moves when a score passes it by more than this
+
+template <int D, bool Q8, int NT> struct Cfg {
+    static constexpr int kWarps = Q8 && NT == 1 ? 12 : 8;
+    static constexpr int kRow = Q8 ? D : 2 * D;                    // bytes of a token's values
+    static constexpr int kVals = kUnit * kRow;                     // of a unit, K or V
+    static constexpr int kScales = Q8 ? kUnit * (D / 32) * 4 : 0;  // of a unit, K or V
+    static constexpr int kStage = 2 * (kVals + kScales);
+    static constexpr int kPart = NT * 8 * D * 4 + NT * 8 * 8;      // a warp's O, then its (m, l)
+    static constexpr int kFit = (226 * 1024 - kWarps * kPart) / (kWarps * kStage);
+    static constexpr int kStages = kFit > 6 ? 6 : kFit;
+    static constexpr int kSmem = kWarps * (kStages * kStage + kPart);
+    static_assert(kStages >= 2, "");
+};
+
+__device__ __forceinline__ uint32_t saddr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp8(uint32_t dst, const void *src, bool ok) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(ok ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t transposed8x8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// d = a b + c, c the same for both token halves.
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0,
+                                        float c1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %11, %10, %11};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+}
+template <int N> __device__ __forceinline__ void load_scales(float (&d)[N], const unsigned char *p) {
+    if (N == 4) {
+        const float4 v = *reinterpret_cast<const float4 *>(p);
+        d[0] = v.x; d[1] = v.y; d[N - 2] = v.z; d[N - 1] = v.w;
+    } else {
+        const float2 v = *reinterpret_cast<const float2 *>(p);
+        d[0] = v.x; d[1] = v.y;
+    }
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+// What a request's token sees, as units: [0, us) hold its sinks, [ul, ul + n - us) the rest.
+struct Seen {
+    int end;      // keys [0, end) exist
+    int lo;       // keys [lo, end) are in the window
+    int us, ul, n;
+};
+__device__ __forceinline__ Seen seen_of(const AttnArgs &a, int len) {
+    Seen s;
+    s.end = min(max(len, 0), a.width * a.page_size);
+    s.lo = a.window ? min(max(len - a.window, 0), s.end) : 0;
+    const int sinks = a.window ? min(a.sinks, s.lo) : 0;
+    s.us = (sinks + kUnit - 1) / kUnit;
+    s.ul = max(s.lo / kUnit, s.us);
+    s.n = s.us + max(0, (s.end + kUnit - 1) / kUnit - s.ul);
+    return s;
+}
+
+// A place in the list of units: item (r, tile) begins at unit `start` of the list and has s.n units.
+struct Cursor {
+    int r, tile;
+    long long start;
+    Seen s;
+    __device__ __forceinline__ void next(const AttnArgs &a, int tiles) {
+        start += s.n;
+        if (++tile == tiles) {
+            tile = 0;
+            do {
+                ++r;
+                s = seen_of(a, r < a.R ? a.lens[r] : 0x7FFFFFFF);  // past the end: units without end stop the walk
+            } while (r < a.R && s.n == 0);
+        }
+    }
+};
+
+// A stored int8 word (q, four bytes) flipped to q + 128; bytes E and E + 1 as the fp16 pair q + 1152: each byte in the
+// low mantissa of 1024.
+template <int E> __device__ __forceinline__ uint32_t biased_f16x2(uint32_t flipped) {
+    uint32_t p;
+    asm("prmt.b32 %0, %1, 0x64646464, %2;" : "=r"(p) : "r"(flipped), "n"(E == 0 ? 0x4140 : 0x4342));
+    return p;
+}
+// The exact fp16 pair of q.
+template <int E> __device__ __forceinline__ uint32_t codes_f16x2(uint32_t flipped) {
+    const uint32_t p = biased_f16x2<E>(flipped);
+    const __half2 v = __hsub2(*reinterpret_cast<const __half2 *>(&p), __half2half2(__ushort_as_half(0x6480)));
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+// The codes' bytes E of two tokens' flipped words interleaved as {a_E, b_E, a_E+1, b_E+1}, for codes_f16x2.
+template <int E> __device__ __forceinline__ uint32_t interleave(uint32_t a, uint32_t b) {
+    uint32_t p;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(p) : "r"(a), "r"(b), "n"(E == 0 ? 0x5140 : 0x7362));
+    return p;
+}
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+// x / d for x < 2^27 as (x * mul) >> shift.  mul = ceil(2^shift / d) with 2^shift >= 2^27 d is off by less than one
+// part in 2^27, so the quotient is exact, and x * mul < 2^56.
+struct UnitDiv {
+    unsigned mul;
+    int shift;
+};
+inline UnitDiv unit_div(int d) {
+    int log = 0;
+    while ((1ll << log) < d) ++log;
+    return {(unsigned)(((1ull << (27 + log)) + d - 1) / d), 27 + log};
+}
+
+template <int D, bool Q8, int NT>
+__global__ void __launch_bounds__(32 * Cfg<D, Q8, NT>::kWarps, 1) attn_decode_kernel(AttnArgs a, int tiles_a_head, UnitDiv div) {
+    using C = Cfg<D, Q8, NT>;
+    constexpr int W = C::kWarps;
+    constexpr int KS = D / 16;       // k-steps of S, value tiles of O
+    constexpr int NB = D / 32;       // quantized blocks of a head
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ long long s_scan[W + 2];
+    __shared__ int s_first[2];
+    __shared__ int s_last;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    const int tiles = a.kv_heads * tiles_a_head;  // items a request
+    unsigned char *ring = smem + warp * (C::kStages * C::kStage);
+    unsigned char *parts = smem + W * C::kStages * C::kStage;
+    const uint32_t ring_s = saddr(ring);
+    // The page of unit u of a request, u / (page_size / 16): u below 2^27, times the rounded-up reciprocal.
+    auto unit_page = [&](int u) { return (int)(((unsigned long long)(unsigned)u * div.mul) >> div.shift); };
+
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    // ---- the list's length and this CTA's span of it ----
+    const int each = (a.R + 32 * W - 1) / (32 * W);
+    const int ra = min(a.R, tid * each), rb = min(a.R, ra + each);
+    long long mine = 0;
+    for (int r = ra; r < rb; ++r) mine += seen_of(a, a.lens[r]).n;
+    long long upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+    }
+    if (lane == 31) s_scan[warp] = upto;
+    __syncthreads();
+    long long before = upto - mine, total = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        if (w < warp) before += s_scan[w];
+        total += s_scan[w];
+    }
+    total *= tiles;
+    const long long span = max((total + gridDim.x - 1) / gridDim.x, (long long)kMinSpan);
+    const long long b0 = span * blockIdx.x, b1 = min(total, b0 + span);
+    if (b0 < b1) {
+        if (before * tiles <= b0 && b0 < (before + mine) * tiles) {  // exactly one thread: the request of unit b0
+            int r = ra;
+            for (;; ++r) {
+                const int n = seen_of(a, a.lens[r]).n;
+                if (b0 < (before + n) * tiles) break;
+                before += n;
+            }
+            s_first[0] = r;
+            s_scan[W] = before * tiles;
+        }
+        __syncthreads();
+        Cursor c;  // the item being computed; p runs ahead of it, filling the ring
+        c.r = s_first[0];
+        c.s = seen_of(a, a.lens[c.r]);
+        c.tile = (int)((b0 - s_scan[W]) / c.s.n);
+        c.start = s_scan[W] + (long long)c.tile * c.s.n;
+        Cursor p = c;
+
+        // ---- the ring: the warp's next unit into stage `slot`; zeros where no token is visible ----
+        const int mine_n = b1 - b0 > warp ? (int)((b1 - b0 - warp + W - 1) / W) : 0;  // this warp's units
+        int todo = mine_n;
+        long long pi = b0 + warp - p.start;  // the next unit to request, within p's item
+        int page_ahead = -1, unit_ahead = 0;
+        auto look_up = [&]() {  // p, unit_ahead and page_ahead for the next request
+            if (todo == 0) return;
+            while (pi >= p.s.n) {
+                pi -= p.s.n;
+                p.next(a, tiles);
+            }
+            unit_ahead = (int)pi < p.s.us ? (int)pi : p.s.ul + ((int)pi - p.s.us);
+            page_ahead = a.table[(size_t)p.r * a.pitch + unit_page(unit_ahead)];
+        };
+        constexpr int CH = C::kRow / 16;  // 16-byte chunks a row
+        constexpr int RP = 32 / CH;       // rows a pass of the warp's lanes
+        // Where this lane's chunk goes in its row: chunks (bf16) or 32-byte groups (codes) are spread over the banks by
+        // bits of the row, as the reads below want them; the rows of a lane's passes agree in those bits or step by 4.
+        const int ch = lane % CH, row0 = lane / CH;
+        int slot = 0;
+        unsigned there_bits = 0;  // bit: the stage's unit lies on a page
+        auto request = [&]() {
+            if (todo > 0) {
+                const bool there = page_ahead >= 0 && page_ahead < a.pages;
+                const int j0 = unit_ahead * kUnit;
+                const int in_page = unit_ahead - unit_page(unit_ahead) * (a.page_size / kUnit);
+                there_bits = (there_bits & ~(1u << slot)) | ((there ? 1u : 0u) << slot);
+                const long long at = there ? (long long)page_ahead * a.page_stride +
+                    ((long long)(p.tile / tiles_a_head) * a.page_size + in_page * kUnit) * D : 0;
+                const uint32_t dst = ring_s + slot * C::kStage;
+                const unsigned char *kp = static_cast<const unsigned char *>(a.k) + at * (Q8 ? 1 : 2) + lane * 16;
+                const unsigned char *vp = static_cast<const unsigned char *>(a.v) + at * (Q8 ? 1 : 2) + lane * 16;
+                const bool whole = there && j0 + kUnit <= p.s.end && (j0 >= p.s.lo || j0 + kUnit <= a.sinks);
+#pragma unroll
+                for (int x = 0; x < kUnit / RP; ++x) {
+                    const int row = x * RP + row0;
+                    int kc, vc;
+                    if (!Q8) {
+                        kc = vc = ch ^ (row & 7);
+                    } else if (D == 128) {
+                        kc = ch ^ ((row & 3) << 1);
+                        vc = ch ^ (((row >> 1) & 3) << 1);
+                    } else {
+                        kc = ch ^ (((row >> 1) & 1) << 1);
+                        vc = ch ^ (((row >> 2) & 1) << 1);
+                    }
+                    const uint32_t kd = dst + row * C::kRow + kc * 16, vd = dst + C::kVals + row * C::kRow + vc * 16;
+                    if (whole) {
+                        cp16(kd, kp + x * 512);
+                        cp16(vd, vp + x * 512);
+                    } else {
+                        const int j = j0 + row;
+                        const bool ok = there && j < p.s.end && (j >= p.s.lo || j < a.sinks);
+                        cp16(kd, ok ? kp + x * 512 : a.k, ok);
+                        cp16(vd, ok ? vp + x * 512 : a.v, ok);
+                    }
+                }
+                if (Q8) {  // 16 rows of NB scales, K on lanes 0-15 and V on 16-31
+                    const int row = lane & 15, j = j0 + row;
+                    const bool ok = there && j < p.s.end && (j >= p.s.lo || j < a.sinks);
+                    const float *src = lane < 16 ? a.ks : a.vs;
+                    const uint32_t to = dst + 2 * C::kVals + (lane < 16 ? 0 : C::kScales) + row * NB * 4;
+                    if (NB == 4) cp16(to, ok ? src + at / 32 + row * NB : src, ok);
+                    else cp8(to, ok ? src + at / 32 + row * NB : src, ok);
+                }
+                --todo;
+                pi += W;
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            slot = slot + 1 == C::kStages ? 0 : slot + 1;
+            look_up();
+        };
+        look_up();
+#pragma unroll
+        for (int x = 0; x < C::kStages - 1; ++x) request();
+
+        long long ci = b0 + warp - c.start;  // the next unit to compute, within c's item
+        int stage = 0;
+        while (c.start < b1) {
+            const int seg = (int)min((long long)c.s.n, b1 - c.start);  // c's units end here, or at the span's end
+            const int kv_head = c.tile / tiles_a_head;
+            const int head0 = kv_head * a.group + (c.tile % tiles_a_head) * (8 * NT);
+            const int heads = min(8 * NT, (kv_head + 1) * a.group - head0);
+            // ---- this item's queries as B fragments (8 heads a tile; absent heads are zeros) ----
+            uint32_t qf[NT][KS][2];
+            float off[NT][Q8 ? NB : 1][2];
+            float sc[NT][2];  // scale * log2(e) of this lane's two heads (2t, 2t + 1)
+            float m[NT][2], l[NT][2], o[NT][KS][4];
+            // Over a Q8_0 cache o's 32 values of block b are in units of unit[b], a power of two that follows the
+            // largest value scale met: the weights p * scale / unit then stay within fp16's range.
+            float unit[Q8 ? NB : 1], per_unit[Q8 ? NB : 1];
+#pragma unroll
+            for (int b = 0; b < (Q8 ? NB : 1); ++b) unit[b] = per_unit[b] = 0.0f;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const uint16_t *qr = a.q + (size_t)c.r * a.ldq + (size_t)(head0 + 8 * n + g) * D;
+                const bool ok = 8 * n + g < heads;
+                if (!Q8) {
+#pragma unroll
+                    for (int k = 0; k < KS; ++k)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+                            qf[n][k][x] = ok ? *reinterpret_cast<const uint32_t *>(qr + 16 * k + 8 * x + 2 * t) : 0u;
+                    sc[n][0] = sc[n][1] = a.scale * kLog2e;
+                } else {
+                    // The keys are exact fp16 integers, so q is taken in fp16 too, exactly: scaled by a power of two
+                    // to a largest magnitude in [2^9, 2^10) (values 2^-23 of the largest and smaller lose bits that
+                    // fp32 sums would not hold).  Lane t holds values 8t .. 8t + 7 of each 32, as the keys' lanes do.
+                    uint32_t mx = 0u;
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        uint4 v = ok ? *reinterpret_cast<const uint4 *>(qr + 32 * b + 8 * t) : make_uint4(0, 0, 0, 0);
+                        qf[n][2 * b][0] = v.x; qf[n][2 * b][1] = v.y; qf[n][2 * b + 1][0] = v.z; qf[n][2 * b + 1][1] = v.w;
+                        const uint32_t vv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            mx = max(mx, max(vv[e] & 0x7FFFu, (vv[e] >> 16) & 0x7FFFu));
+                    }
+                    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                    mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                    // exponent field of the largest; subnormals count as the smallest normal
+                    const int ex = min(max((int)(mx >> 7), 1), 254);
+                    const int up = min(127 + 9 - ex, 126);  // q * 2^up
+                    const float f = __uint_as_float((uint32_t)(up + 127) << 23);
+#pragma unroll
+                    for (int k = 0; k < KS; ++k)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const uint32_t v = qf[n][k][x];
+                            const __half2 h = __floats2half2_rn(__uint_as_float(v << 16) * f,
+                                                                __uint_as_float(v & 0xFFFF0000u) * f);
+                            qf[n][k][x] = *reinterpret_cast<const uint32_t *>(&h);
+                        }
+                    // The keys enter as code + 1152 (one instruction a pair): each block's sum begins at -1152 times the
+                    // sum of its fp16 queries.  The detour costs fp32 about 2^-24 * 1152 sum |q| a block, some 20
+                    // times the rounding of the plain sum and 1e-5 of a score.
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        float sum = 0.0f;
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const uint32_t v = qf[n][2 * b + (x >> 1)][x & 1];
+                            const float2 f2 = __half22float2(*reinterpret_cast<const __half2 *>(&v));
+                            sum += f2.x + f2.y;
+                        }
+                        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+                            off[n][b][x] = -1152.0f * __shfl_sync(0xffffffffu, sum, (2 * t + x) * 4);
+                    }
+                    const float back = __uint_as_float((uint32_t)(127 - up) << 23);  // 2^-up
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+                        sc[n][x] = __shfl_sync(0xffffffffu, back, (2 * t + x) * 4) * (a.scale * kLog2e);
+                }
+                m[n][0] = m[n][1] = -INFINITY;
+                l[n][0] = l[n][1] = 0.0f;
+#pragma unroll
+                for (int k = 0; k < KS; ++k)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) o[n][k][x] = 0.0f;
+            }
+            // ---- this warp's units of the item ----
+            for (; ci < seg; ci += W) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
+                __syncwarp();  // every lane's copies of the stage have landed; the stage read last is free
+                request();
+                const uint32_t kst = ring_s + stage * C::kStage, vst = kst + C::kVals;
+                const unsigned char *st = ring + stage * C::kStage;
+                const bool there = (there_bits >> stage) & 1u;
+                stage = stage + 1 == C::kStages ? 0 : stage + 1;
+                float s[NT][4];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+                if (!Q8) {
+#pragma unroll
+                    for (int k = 0; k < KS; ++k) {
+                        uint32_t kf[4];
+                        const int row = lane & 15;
+                        ldsm4(kf, kst + row * C::kRow + (((2 * k + (lane >> 4)) ^ (row & 7)) << 4));
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) mma_bf16(s[n], kf, qf[n][k][0], qf[n][k][1]);
+                    }
+                } else {
+                    float d0[NB], d1[NB];
+                    load_scales<NB>(d0, st + 2 * C::kVals + g * NB * 4);
+                    load_scales<NB>(d1, st + 2 * C::kVals + (g + 8) * NB * 4);
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        // values 8t .. 8t + 7 of rows g and g + 8; their 32-byte groups are spread over the banks
+                        const int grp = D == 128 ? b ^ (g & 3) : b ^ ((g >> 1) & 1);
+                        const uint2 r0 = *reinterpret_cast<const uint2 *>(st + g * C::kRow + grp * 32 + t * 8);
+                        const uint2 r1 = *reinterpret_cast<const uint2 *>(st + (g + 8) * C::kRow + grp * 32 + t * 8);
+                        const uint32_t x0 = r0.x ^ 0x80808080u, y0 = r0.y ^ 0x80808080u;
+                        const uint32_t x1 = r1.x ^ 0x80808080u, y1 = r1.y ^ 0x80808080u;
+                        const uint32_t f0[4] = {biased_f16x2<0>(x0), biased_f16x2<0>(x1), biased_f16x2<2>(x0),
+                                                biased_f16x2<2>(x1)};
+                        const uint32_t f1[4] = {biased_f16x2<0>(y0), biased_f16x2<0>(y1), biased_f16x2<2>(y0),
+                                                biased_f16x2<2>(y1)};
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            float z[4];
+                            mma_f16(z, f0, qf[n][2 * b][0], qf[n][2 * b][1], off[n][b][0], off[n][b][1]);
+                            mma_f16(z, f1, qf[n][2 * b + 1][0], qf[n][2 * b + 1][1]);
+                            s[n][0] = fmaf(d0[b], z[0], s[n][0]);
+                            s[n][1] = fmaf(d0[b], z[1], s[n][1]);
+                            s[n][2] = fmaf(d1[b], z[2], s[n][2]);
+                            s[n][3] = fmaf(d1[b], z[3], s[n][3]);
+                        }
+                    }
+                }
+                // ---- scores of tokens g (s[0], s[1]) and g + 8 (s[2], s[3]) for heads 2t, 2t + 1 ----
+                const int i = (int)ci, u = i < c.s.us ? i : c.s.ul + (i - c.s.us);
+                const int j0 = u * kUnit;
+                const int ja = j0 + g, jb = ja + 8;
+                const bool va = there && ja < c.s.end && (ja >= c.s.lo || ja < a.sinks);
+                const bool vb = there && jb < c.s.end && (jb >= c.s.lo || jb < a.sinks);
+                bool above = false;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    s[n][0] = va ? s[n][0] * sc[n][0] : -INFINITY;
+                    s[n][1] = va ? s[n][1] * sc[n][1] : -INFINITY;
+                    s[n][2] = vb ? s[n][2] * sc[n][0] : -INFINITY;
+                    s[n][3] = vb ? s[n][3] * sc[n][1] : -INFINITY;
+                    above = above || fmaxf(s[n][0], s[n][2]) > m[n][0] + kSlack ||
+                            fmaxf(s[n][1], s[n][3]) > m[n][1] + kSlack;
+                }
+                if (__any_sync(0xffffffffu, above)) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            float mx = fmaxf(s[n][x], s[n][x + 2]);
+#pragma unroll
+                            for (int sh = 4; sh < 32; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
+                            mx = fmaxf(mx, m[n][x]);
+                            const float f = mx == m[n][x] ? 1.0f : ex2(m[n][x] - mx);
+                            m[n][x] = mx;
+                            l[n][x] *= f;
+#pragma unroll
+                            for (int k = 0; k < KS; ++k) {
+                                o[n][k][x] *= f;
+                                o[n][k][x + 2] *= f;
+                            }
+                        }
+                }
+                float p[NT][4];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const float m0 = m[n][0] == -INFINITY ? 0.0f : m[n][0], m1 = m[n][1] == -INFINITY ? 0.0f : m[n][1];
+                    p[n][0] = ex2(s[n][0] - m0);
+                    p[n][1] = ex2(s[n][1] - m1);
+                    p[n][2] = ex2(s[n][2] - m0);
+                    p[n][3] = ex2(s[n][3] - m1);
+                    l[n][0] += p[n][0] + p[n][2];
+                    l[n][1] += p[n][1] + p[n][3];
+                }
+                // ---- O^T += V^T P^T ----
+                if (!Q8) {
+                    uint32_t pf[NT][2];  // weights rounded to bf16, v's type, for the product; their sum is fp32
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        pf[n][0] = transposed8x8(bf16x2(p[n][0], p[n][1]));
+                        pf[n][1] = transposed8x8(bf16x2(p[n][2], p[n][3]));
+                    }
+#pragma unroll
+                    for (int k = 0; k < KS; ++k) {
+                        uint32_t vf[4];
+                        const int row = (lane & 7) + ((lane >> 4) << 3);
+                        ldsm4t(vf, vst + row * C::kRow + (((2 * k + ((lane >> 3) & 1)) ^ (row & 7)) << 4));
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) mma_bf16(o[n][k], vf, pf[n][0], pf[n][1]);
+                    }
+                } else {
+                    // The codes are exact in fp16; the tokens' scales go to the weights, p * scale / unit, rounded to
+                    // fp16 (11 bits; below 2^-14 of the unit they lose bits that do not reach the result).
+                    const unsigned char *vb8 = st + C::kVals;
+                    float da[NB], db[NB];
+                    load_scales<NB>(da, st + 2 * C::kVals + C::kScales + g * NB * 4);
+                    load_scales<NB>(db, st + 2 * C::kVals + C::kScales + (g + 8) * NB * 4);
+                    bool big = false;
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        big = big || fabsf(da[b]) > 4.0f * unit[b] || fabsf(db[b]) > 4.0f * unit[b];
+                    }
+                    if (__any_sync(0xffffffffu, big)) {
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) {
+                            float mx = fmaxf(fabsf(da[b]), fabsf(db[b]));
+#pragma unroll
+                            for (int sh = 4; sh < 32; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
+                            if (mx > 4.0f * unit[b]) {
+                                // the power of two at or below the largest scale, within what has a reciprocal
+                                const float now = __uint_as_float(
+                                    min(max(__float_as_uint(mx) & 0x7F800000u, 0x01000000u), 0x7E000000u));
+                                const float f = unit[b] * (1.0f / now);
+#pragma unroll
+                                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                    for (int x = 0; x < 4; ++x) {
+                                        o[n][2 * b][x] *= f;
+                                        o[n][2 * b + 1][x] *= f;
+                                    }
+                                unit[b] = now;
+                                per_unit[b] = 1.0f / now;
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        // values 4g .. 4g + 3 of tokens 2t, 2t + 1, 2t + 8, 2t + 9
+                        uint32_t w[4];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const int row = 2 * t + (x & 1) + 8 * (x >> 1);
+                            const int grp = D == 128 ? b ^ ((row >> 1) & 3) : b ^ ((row >> 2) & 1);
+                            w[x] = *reinterpret_cast<const uint32_t *>(vb8 + row * C::kRow + grp * 32 + g * 4) ^ 0x80808080u;
+                        }
+                        const uint32_t lo0 = interleave<0>(w[0], w[1]), lo1 = interleave<2>(w[0], w[1]);
+                        const uint32_t hi0 = interleave<0>(w[2], w[3]), hi1 = interleave<2>(w[2], w[3]);
+                        const uint32_t v0[4] = {codes_f16x2<0>(lo0), codes_f16x2<2>(lo0), codes_f16x2<0>(hi0),
+                                                codes_f16x2<2>(hi0)};
+                        const uint32_t v1[4] = {codes_f16x2<0>(lo1), codes_f16x2<2>(lo1), codes_f16x2<0>(hi1),
+                                                codes_f16x2<2>(hi1)};
+                        const float fa = da[b] * per_unit[b], fb = db[b] * per_unit[b];
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            const uint32_t q0 = transposed8x8(f16x2(p[n][0] * fa, p[n][1] * fa));
+                            const uint32_t q1 = transposed8x8(f16x2(p[n][2] * fb, p[n][3] * fb));
+                            mma_f16(o[n][2 * b], v0, q0, q1);
+                            mma_f16(o[n][2 * b + 1], v1, q0, q1);
+                        }
+                    }
+                }
+            }
+            // ---- the item's end: the warps' parts through shared memory ----
+            float *po = reinterpret_cast<float *>(parts + warp * C::kPart);
+            float2 *pml = reinterpret_cast<float2 *>(parts + warp * C::kPart + NT * 8 * D * 4);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+#pragma unroll
+                    for (int sh = 4; sh < 32; sh <<= 1) l[n][x] += __shfl_xor_sync(0xffffffffu, l[n][x], sh);
+                    float *row = po + (8 * n + 2 * t + x) * D;
+                    if (!Q8) {
+#pragma unroll
+                        for (int k = 0; k < KS; ++k) {
+                            row[16 * k + g] = o[n][k][x];
+                            row[16 * k + g + 8] = o[n][k][x + 2];
+                        }
+                    } else {
+#pragma unroll
+                        for (int b = 0; b < NB; ++b)
+                            *reinterpret_cast<float4 *>(row + 32 * b + 4 * g) = make_float4(
+                                o[n][2 * b][x] * unit[b], o[n][2 * b][x + 2] * unit[b], o[n][2 * b + 1][x] * unit[b],
+                                o[n][2 * b + 1][x + 2] * unit[b]);
+                    }
+                    if (g == 0) pml[8 * n + 2 * t + x] = make_float2(m[n][x], l[n][x]);
+                }
+            __syncthreads();
+            const long long end = c.start + c.s.n;
+            const int c0 = (int)(c.start / span), c1 = (int)((end - 1) / span);  // the CTAs that share the item
+            float *base = reinterpret_cast<float *>(a.work + kAttnCounterBytes);
+            // four values of one head a thread and pass
+            constexpr int PASS = NT * 8 * (D / 4);
+            for (int e = tid; e < PASS; e += 32 * W) {
+                const int h = e / (D / 4), d4 = e % (D / 4);
+                float mx = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < W; ++w)
+                    mx = fmaxf(mx, reinterpret_cast<const float2 *>(parts + w * C::kPart + NT * 8 * D * 4)[h].x);
+                float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                float sum = 0.0f;
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    const float2 ml = reinterpret_cast<const float2 *>(parts + w * C::kPart + NT * 8 * D * 4)[h];
+                    const float f = ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : 1.0f) : ex2(ml.x - mx);
+                    const float4 v = *reinterpret_cast<const float4 *>(parts + w * C::kPart + (h * D + 4 * d4) * 4);
+                    sum = fmaf(ml.y, f, sum);
+                    acc.x = fmaf(v.x, f, acc.x);
+                    acc.y = fmaf(v.y, f, acc.y);
+                    acc.z = fmaf(v.z, f, acc.z);
+                    acc.w = fmaf(v.w, f, acc.w);
+                }
+                if (c0 == c1) {
+                    if (h < heads) {
+                        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                        *reinterpret_cast<uint2 *>(a.out + (size_t)c.r * a.ldo + (size_t)(head0 + h) * D + 4 * d4) =
+                            make_uint2(bf16x2(acc.x * inv, acc.y * inv), bf16x2(acc.z * inv, acc.w * inv));
+                    }
+                } else {
+                    float *part = base + ((long long)blockIdx.x * 2 + (c.start >= b0)) * kDecodePartFloats;
+                    *reinterpret_cast<float4 *>(part + h * D + 4 * d4) = acc;
+                    if (d4 == 0) *reinterpret_cast<float2 *>(part + kDecodeHeads * 128 + 2 * h) = make_float2(mx, sum);
+                }
+            }
+            if (c0 != c1) {
+                // ---- an item shared with other CTAs: whoever arrives last adds the parts, in span order ----
+                int *count = reinterpret_cast<int *>(a.work) + c0;
+                __threadfence();
+                __syncthreads();
+                if (tid == 0) {
+                    const int seen = atomicAdd(count, 1);
+                    s_last = seen == c1 - c0;
+                    if (s_last) *count = 0;
+                }
+                __syncthreads();
+                if (s_last) {
+                    __threadfence();
+                    for (int e = tid; e < PASS; e += 32 * W) {
+                        const int h = e / (D / 4), d4 = e % (D / 4);
+                        if (h >= heads) continue;
+                        float mx = -INFINITY, sum = 0.0f;
+                        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        for (int x = c0; x <= c1; ++x) {
+                            const float *part = base + ((long long)x * 2 + (x == c0)) * kDecodePartFloats;
+                            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(part + kDecodeHeads * 128 + 2 * h));
+                            const float4 v = __ldcg(reinterpret_cast<const float4 *>(part + h * D + 4 * d4));
+                            const float nm = fmaxf(mx, ml.x);
+                            const float fa = mx == nm ? 1.0f : ex2(mx - nm);
+                            const float fb = ml.x == nm ? 1.0f : ex2(ml.x - nm);
+                            mx = nm;
+                            sum = sum * fa + ml.y * fb;
+                            acc.x = acc.x * fa + v.x * fb;
+                            acc.y = acc.y * fa + v.y * fb;
+                            acc.z = acc.z * fa + v.z * fb;
+                            acc.w = acc.w * fa + v.w * fb;
+                        }
+                        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                        *reinterpret_cast<uint2 *>(a.out + (size_t)c.r * a.ldo + (size_t)(head0 + h) * D + 4 * d4) =
+                            make_uint2(bf16x2(acc.x * inv, acc.y * inv), bf16x2(acc.z * inv, acc.w * inv));
+                    }
+                }
+            }
+            __syncthreads();  // the parts are free for the next item
+            if (c.start + seg == b1) break;
+            ci -= c.s.n;
+            c.next(a, tiles);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    }
+    // ---- rows that see nothing ----
+    for (int r = blockIdx.x; r < a.R; r += gridDim.x)
+        if (seen_of(a, a.lens[r]).n == 0)
+            for (int e = tid; e < a.heads * D / 8; e += 32 * W)
+                *reinterpret_cast<uint4 *>(a.out + (size_t)r * a.ldo + 8 * e) = make_uint4(0u, 0u, 0u, 0u);
+}
+
+template <int D, bool Q8, int NT> cudaError_t launch_one(const AttnArgs &a, int sms, cudaStream_t stream) {
+    using C = Cfg<D, Q8, NT>;
+    cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<D, Q8, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         C::kSmem);
+    if (e != cudaSuccess) return e;
+    const int tiles_a_head = (a.group + 8 * NT - 1) / (8 * NT);
+    return kv_launch(attn_decode_kernel<D, Q8, NT>, dim3((unsigned)sms, 1, 1), 32 * C::kWarps, C::kSmem, stream, a,
+                     tiles_a_head, unit_div(a.page_size / kUnit));
+}
+
+}  // namespace
+
+cudaError_t launch_attn_decode(const AttnArgs &a, int dim, bool q8, cudaStream_t stream) {
+    int sms = 0;
+    cudaError_t e = sm_count_of_device(&sms);
+    if (e != cudaSuccess) return e;
+    if (sms > kAttnMaxCtas) sms = kAttnMaxCtas;
+    const bool wide = a.group > 8;  // 16 query heads a pass over the keys instead of 8
+    if (dim == 128) {
+        if (q8) return wide ? launch_one<128, true, 2>(a, sms, stream) : launch_one<128, true, 1>(a, sms, stream);
+        return wide ? launch_one<128, false, 2>(a, sms, stream) : launch_one<128, false, 1>(a, sms, stream);
+    }
+    if (q8) return wide ? launch_one<64, true, 2>(a, sms, stream) : launch_one<64, true, 1>(a, sms, stream);
+    return wide ? launch_one<64, false, 2>(a, sms, stream) : launch_one<64, false, 1>(a, sms, stream);
+}
+
+}  // namespace q8
