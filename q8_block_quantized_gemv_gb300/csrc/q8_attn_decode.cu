@@ -69,6 +69,18 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
                  : "r"(a)
                  : "memory");
 }
+// 16 tokens by 32 codes, transposed: lane (g, t) gets tokens 4t .. 4t + 3 of codes g, g + 8, g + 16 and g + 24.
+__device__ __forceinline__ void ldsm8t(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a)
+                 : "memory");
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+    return v;
+}
 __device__ __forceinline__ uint32_t transposed8x8(uint32_t x) {
     uint32_t y;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -94,19 +106,28 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
 }
-template <int N> __device__ __forceinline__ void load_scales(float (&d)[N], const unsigned char *p) {
-    if (N == 4) {
-        const float4 v = *reinterpret_cast<const float4 *>(p);
-        d[0] = v.x; d[1] = v.y; d[N - 2] = v.z; d[N - 1] = v.w;
-    } else {
-        const float2 v = *reinterpret_cast<const float2 *>(p);
-        d[0] = v.x; d[1] = v.y;
-    }
+template <int N> __device__ __forceinline__ void load_scales(float (&d)[N], uint32_t a) {
+    if (N == 4)
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(d[0]), "=f"(d[1]), "=f"(d[N - 2]), "=f"(d[N - 1]) : "r"(a) : "memory");
+    else
+        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(d[0]), "=f"(d[1]) : "r"(a) : "memory");
 }
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     uint32_t d;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
     return d;
+}
+
+// Where 16-byte chunk `ch` of a token's row goes in its stage.  The bf16 rows and the codes' values are read by
+// (transposing) matrix loads, eight rows of one chunk at a time; the codes' keys by 8-byte loads of 32-byte groups from
+// the rows ta of four consecutive g (row ta + 2 keeps its place).  Either way the rows read together land on different banks.
+template <int D, bool Q8> __device__ __forceinline__ int key_chunk(int row, int ch) {
+    if (!Q8) return ch ^ (row & 7);
+    return D == 128 ? ch ^ (((row & 1) | ((row >> 1) & 2)) << 1) : ch ^ (((row >> 2) & 1) << 1);
+}
+template <int D, bool Q8> __device__ __forceinline__ int value_chunk(int row, int ch) {
+    return Q8 && D == 64 ? ch ^ ((row >> 1) & 3) : ch ^ (row & 7);
 }
 
 // What a request's token sees, as units: [0, us) hold its sinks, [ul, ul + n - us) the rest.
@@ -156,12 +177,6 @@ template <int E> __device__ __forceinline__ uint32_t codes_f16x2(uint32_t flippe
     const __half2 v = __hsub2(*reinterpret_cast<const __half2 *>(&p), __half2half2(__ushort_as_half(0x6480)));
     return *reinterpret_cast<const uint32_t *>(&v);
 }
-// The codes' bytes E of two tokens' flipped words interleaved as {a_E, b_E, a_E+1, b_E+1}, for codes_f16x2.
-template <int E> __device__ __forceinline__ uint32_t interleave(uint32_t a, uint32_t b) {
-    uint32_t p;
-    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(p) : "r"(a), "r"(b), "n"(E == 0 ? 0x5140 : 0x7362));
-    return p;
-}
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
     uint32_t d;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
@@ -195,8 +210,6 @@ __global__ void __launch_bounds__(32 * Cfg<D, Q8, NT>::kWarps, 1) attn_decode_ke
     unsigned char *ring = smem + warp * (C::kStages * C::kStage);
     unsigned char *parts = smem + W * C::kStages * C::kStage;
     const uint32_t ring_s = saddr(ring);
-    // The page of unit u of a request, u / (page_size / 16): u below 2^27, times the rounded-up reciprocal.
-    auto unit_page = [&](int u) { return (int)(((unsigned long long)(unsigned)u * div.mul) >> div.shift); };
 
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -243,69 +256,81 @@ __global__ void __launch_bounds__(32 * Cfg<D, Q8, NT>::kWarps, 1) attn_decode_ke
         Cursor p = c;
 
         // ---- the ring: the warp's next unit into stage `slot`; zeros where no token is visible ----
-        const int mine_n = b1 - b0 > warp ? (int)((b1 - b0 - warp + W - 1) / W) : 0;  // this warp's units
-        int todo = mine_n;
-        long long pi = b0 + warp - p.start;  // the next unit to request, within p's item
-        int page_ahead = -1, unit_ahead = 0;
-        auto look_up = [&]() {  // p, unit_ahead and page_ahead for the next request
+        int todo = b1 - b0 > warp ? (int)((b1 - b0 - warp + W - 1) / W) : 0;  // this warp's units
+        int pi = (int)(b0 + warp - p.start);                                  // the next one, within p's item
+        const int *table_row = nullptr;  // of p's item, and its cache head's first value in a page
+        int head_at = 0;
+        auto place = [&]() {
+            table_row = a.table + (size_t)p.r * a.pitch;
+            head_at = (p.tile / tiles_a_head) * a.page_size * D;
+        };
+        place();
+        int page_ahead = -1, unit_ahead = 0, at_ahead = 0;
+        auto look_up = [&]() {  // where the next request finds its unit
             if (todo == 0) return;
-            while (pi >= p.s.n) {
-                pi -= p.s.n;
-                p.next(a, tiles);
+            if (pi >= p.s.n) {
+                do {
+                    pi -= p.s.n;
+                    p.next(a, tiles);
+                } while (pi >= p.s.n);
+                place();
             }
-            unit_ahead = (int)pi < p.s.us ? (int)pi : p.s.ul + ((int)pi - p.s.us);
-            page_ahead = a.table[(size_t)p.r * a.pitch + unit_page(unit_ahead)];
+            unit_ahead = pi < p.s.us ? pi : p.s.ul + (pi - p.s.us);
+            const int page = (int)(((unsigned long long)(unsigned)unit_ahead * div.mul) >> div.shift);
+            page_ahead = table_row[page];
+            at_ahead = head_at + (unit_ahead * kUnit - page * a.page_size) * D;
         };
         constexpr int CH = C::kRow / 16;  // 16-byte chunks a row
         constexpr int RP = 32 / CH;       // rows a pass of the warp's lanes
-        // Where this lane's chunk goes in its row: chunks (bf16) or 32-byte groups (codes) are spread over the banks by
-        // bits of the row, as the reads below want them; the rows of a lane's passes agree in those bits or step by 4.
+        constexpr int NX = kUnit / RP;    // passes
         const int ch = lane % CH, row0 = lane / CH;
+        uint32_t kd[NX], vd[NX];  // where this lane's chunks go in a stage
+#pragma unroll
+        for (int x = 0; x < NX; ++x) {
+            const int row = x * RP + row0;
+            kd[x] = ring_s + row * C::kRow + key_chunk<D, Q8>(row, ch) * 16;
+            vd[x] = ring_s + C::kVals + row * C::kRow + value_chunk<D, Q8>(row, ch) * 16;
+        }
+        const unsigned char *const kl = static_cast<const unsigned char *>(a.k) + lane * 16;
+        const unsigned char *const vl = static_cast<const unsigned char *>(a.v) + lane * 16;
+        const unsigned char *const sl =
+            reinterpret_cast<const unsigned char *>(lane < 16 ? a.ks : a.vs) + (lane & 15) * (NB * 4);
+        const uint32_t sd = ring_s + 2 * C::kVals + lane * (NB * 4);  // K's scales on lanes 0-15, V's on 16-31
         int slot = 0;
-        unsigned there_bits = 0;  // bit: the stage's unit lies on a page
+        unsigned whole_bits = 0;  // bit: the stage's unit lies on a page and all its tokens are visible
+        unsigned there_bits = 0;  // bit: it lies on a page
         auto request = [&]() {
             if (todo > 0) {
-                const bool there = page_ahead >= 0 && page_ahead < a.pages;
+                const bool there = (unsigned)page_ahead < (unsigned)a.pages;
                 const int j0 = unit_ahead * kUnit;
-                const int in_page = unit_ahead - unit_page(unit_ahead) * (a.page_size / kUnit);
-                there_bits = (there_bits & ~(1u << slot)) | ((there ? 1u : 0u) << slot);
-                const long long at = there ? (long long)page_ahead * a.page_stride +
-                    ((long long)(p.tile / tiles_a_head) * a.page_size + in_page * kUnit) * D : 0;
-                const uint32_t dst = ring_s + slot * C::kStage;
-                const unsigned char *kp = static_cast<const unsigned char *>(a.k) + at * (Q8 ? 1 : 2) + lane * 16;
-                const unsigned char *vp = static_cast<const unsigned char *>(a.v) + at * (Q8 ? 1 : 2) + lane * 16;
                 const bool whole = there && j0 + kUnit <= p.s.end && (j0 >= p.s.lo || j0 + kUnit <= a.sinks);
+                const unsigned bit = 1u << slot;
+                there_bits = there ? there_bits | bit : there_bits & ~bit;
+                whole_bits = whole ? whole_bits | bit : whole_bits & ~bit;
+                const long long at = there ? page_ahead * a.page_stride + at_ahead : 0;
+                const uint32_t dst = slot * C::kStage;
+                const unsigned char *kp = kl + at * (Q8 ? 1 : 2), *vp = vl + at * (Q8 ? 1 : 2);
+                if (whole) {
 #pragma unroll
-                for (int x = 0; x < kUnit / RP; ++x) {
-                    const int row = x * RP + row0;
-                    int kc, vc;
-                    if (!Q8) {
-                        kc = vc = ch ^ (row & 7);
-                    } else if (D == 128) {
-                        kc = ch ^ ((row & 3) << 1);
-                        vc = ch ^ (((row >> 1) & 3) << 1);
-                    } else {
-                        kc = ch ^ (((row >> 1) & 1) << 1);
-                        vc = ch ^ (((row >> 2) & 1) << 1);
+                    for (int x = 0; x < NX; ++x) {
+                        cp16(dst + kd[x], kp + x * 512);
+                        cp16(dst + vd[x], vp + x * 512);
                     }
-                    const uint32_t kd = dst + row * C::kRow + kc * 16, vd = dst + C::kVals + row * C::kRow + vc * 16;
-                    if (whole) {
-                        cp16(kd, kp + x * 512);
-                        cp16(vd, vp + x * 512);
-                    } else {
-                        const int j = j0 + row;
+                } else {
+#pragma unroll
+                    for (int x = 0; x < NX; ++x) {
+                        const int j = j0 + x * RP + row0;
                         const bool ok = there && j < p.s.end && (j >= p.s.lo || j < a.sinks);
-                        cp16(kd, ok ? kp + x * 512 : a.k, ok);
-                        cp16(vd, ok ? vp + x * 512 : a.v, ok);
+                        cp16(dst + kd[x], ok ? kp + x * 512 : a.k, ok);
+                        cp16(dst + vd[x], ok ? vp + x * 512 : a.v, ok);
                     }
                 }
-                if (Q8) {  // 16 rows of NB scales, K on lanes 0-15 and V on 16-31
-                    const int row = lane & 15, j = j0 + row;
-                    const bool ok = there && j < p.s.end && (j >= p.s.lo || j < a.sinks);
-                    const float *src = lane < 16 ? a.ks : a.vs;
-                    const uint32_t to = dst + 2 * C::kVals + (lane < 16 ? 0 : C::kScales) + row * NB * 4;
-                    if (NB == 4) cp16(to, ok ? src + at / 32 + row * NB : src, ok);
-                    else cp8(to, ok ? src + at / 32 + row * NB : src, ok);
+                if (Q8) {
+                    const int j = j0 + (lane & 15);
+                    const bool ok = whole || (there && j < p.s.end && (j >= p.s.lo || j < a.sinks));
+                    const void *src = ok ? static_cast<const void *>(sl + at / 8) : a.ks;
+                    if (NB == 4) cp16(dst + sd, src, ok);
+                    else cp8(dst + sd, src, ok);
                 }
                 --todo;
                 pi += W;
@@ -318,7 +343,18 @@ __global__ void __launch_bounds__(32 * Cfg<D, Q8, NT>::kWarps, 1) attn_decode_ke
 #pragma unroll
         for (int x = 0; x < C::kStages - 1; ++x) request();
 
-        long long ci = b0 + warp - c.start;  // the next unit to compute, within c's item
+        // Where this lane reads in a stage.  Over a Q8_0 cache rows g and g + 8 of the score product are tokens ta and
+        // ta + 2, so that the weights come out in the token order of the transposed codes.
+        const int ta = 4 * (g >> 1) + (g & 1);
+        uint32_t kr[NB], vr[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            kr[b] = ring_s + ta * C::kRow + key_chunk<D, true>(ta, 2 * b) * 16 + t * 8;
+            const int row = lane & 15;
+            vr[b] = ring_s + C::kVals + row * C::kRow + value_chunk<D, true>(row, 2 * b + (lane >> 4)) * 16;
+        }
+        const uint32_t sr = ring_s + 2 * C::kVals + ta * (NB * 4);
+        int ci = (int)(b0 + warp - c.start);  // the next unit to compute, within c's item
         int stage = 0;
         while (c.start < b1) {
             const int seg = (int)min((long long)c.s.n, b1 - c.start);  // c's units end here, or at the span's end
@@ -410,32 +446,30 @@ __global__ void __launch_bounds__(32 * Cfg<D, Q8, NT>::kWarps, 1) attn_decode_ke
                 asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
                 __syncwarp();  // every lane's copies of the stage have landed; the stage read last is free
                 request();
-                const uint32_t kst = ring_s + stage * C::kStage, vst = kst + C::kVals;
-                const unsigned char *st = ring + stage * C::kStage;
-                const bool there = (there_bits >> stage) & 1u;
+                const uint32_t at = stage * C::kStage;
+                const bool whole = (whole_bits >> stage) & 1u, there = (there_bits >> stage) & 1u;
                 stage = stage + 1 == C::kStages ? 0 : stage + 1;
+                // ---- s = q k: rows of tokens ja (s[0], s[1]) and jb (s[2], s[3]), heads 2t and 2t + 1 ----
                 float s[NT][4];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
                 if (!Q8) {
+                    const int row = lane & 15;
+                    const uint32_t base = ring_s + at + row * C::kRow;
 #pragma unroll
                     for (int k = 0; k < KS; ++k) {
                         uint32_t kf[4];
-                        const int row = lane & 15;
-                        ldsm4(kf, kst + row * C::kRow + (((2 * k + (lane >> 4)) ^ (row & 7)) << 4));
+                        ldsm4(kf, base + (((2 * k + (lane >> 4)) ^ (row & 7)) << 4));
 #pragma unroll
                         for (int n = 0; n < NT; ++n) mma_bf16(s[n], kf, qf[n][k][0], qf[n][k][1]);
                     }
                 } else {
                     float d0[NB], d1[NB];
-                    load_scales<NB>(d0, st + 2 * C::kVals + g * NB * 4);
-                    load_scales<NB>(d1, st + 2 * C::kVals + (g + 8) * NB * 4);
+                    load_scales<NB>(d0, at + sr);
+                    load_scales<NB>(d1, at + sr + 2 * NB * 4);
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        // values 8t .. 8t + 7 of rows g and g + 8; their 32-byte groups are spread over the banks
-                        const int grp = D == 128 ? b ^ (g & 3) : b ^ ((g >> 1) & 1);
-                        const uint2 r0 = *reinterpret_cast<const uint2 *>(st + g * C::kRow + grp * 32 + t * 8);
-                        const uint2 r1 = *reinterpret_cast<const uint2 *>(st + (g + 8) * C::kRow + grp * 32 + t * 8);
+                    for (int b = 0; b < NB; ++b) {  // lane t: codes 8t .. 8t + 7 of the block
+                        const uint2 r0 = lds64(at + kr[b]), r1 = lds64(at + kr[b] + 2 * C::kRow);
                         const uint32_t x0 = r0.x ^ 0x80808080u, y0 = r0.y ^ 0x80808080u;
                         const uint32_t x1 = r1.x ^ 0x80808080u, y1 = r1.y ^ 0x80808080u;
                         const uint32_t f0[4] = {biased_f16x2<0>(x0), biased_f16x2<0>(x1), biased_f16x2<2>(x0),
@@ -454,22 +488,30 @@ __global__ void __launch_bounds__(32 * Cfg<D, Q8, NT>::kWarps, 1) attn_decode_ke
                         }
                     }
                 }
-                // ---- scores of tokens g (s[0], s[1]) and g + 8 (s[2], s[3]) for heads 2t, 2t + 1 ----
-                const int i = (int)ci, u = i < c.s.us ? i : c.s.ul + (i - c.s.us);
-                const int j0 = u * kUnit;
-                const int ja = j0 + g, jb = ja + 8;
-                const bool va = there && ja < c.s.end && (ja >= c.s.lo || ja < a.sinks);
-                const bool vb = there && jb < c.s.end && (jb >= c.s.lo || jb < a.sinks);
-                bool above = false;
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    s[n][0] = va ? s[n][0] * sc[n][0] : -INFINITY;
-                    s[n][1] = va ? s[n][1] * sc[n][1] : -INFINITY;
-                    s[n][2] = vb ? s[n][2] * sc[n][0] : -INFINITY;
-                    s[n][3] = vb ? s[n][3] * sc[n][1] : -INFINITY;
-                    above = above || fmaxf(s[n][0], s[n][2]) > m[n][0] + kSlack ||
-                            fmaxf(s[n][1], s[n][3]) > m[n][1] + kSlack;
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) s[n][x] *= sc[n][x & 1];
+                if (!whole) {
+                    const int u = ci < c.s.us ? ci : c.s.ul + (ci - c.s.us);
+                    const int ja = u * kUnit + (Q8 ? ta : g), jb = ja + (Q8 ? 2 : 8);
+                    const bool va = there && ja < c.s.end && (ja >= c.s.lo || ja < a.sinks);
+                    const bool vb = there && jb < c.s.end && (jb >= c.s.lo || jb < a.sinks);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) s[n][x] = (x < 2 ? va : vb) ? s[n][x] : -INFINITY;
                 }
+                // ---- weights p = 2^(s - m) ----
+                float p[NT][4];
+                bool above = !whole;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        p[n][x] = s[n][x] - m[n][x & 1];
+                        above = above || p[n][x] > kSlack;
+                    }
                 if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
@@ -487,16 +529,15 @@ __global__ void __launch_bounds__(32 * Cfg<D, Q8, NT>::kWarps, 1) attn_decode_ke
                                 o[n][k][x] *= f;
                                 o[n][k][x + 2] *= f;
                             }
+                            const float m0 = mx == -INFINITY ? 0.0f : mx;  // nothing seen yet: weights 0
+                            p[n][x] = s[n][x] - m0;
+                            p[n][x + 2] = s[n][x + 2] - m0;
                         }
                 }
-                float p[NT][4];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    const float m0 = m[n][0] == -INFINITY ? 0.0f : m[n][0], m1 = m[n][1] == -INFINITY ? 0.0f : m[n][1];
-                    p[n][0] = ex2(s[n][0] - m0);
-                    p[n][1] = ex2(s[n][1] - m1);
-                    p[n][2] = ex2(s[n][2] - m0);
-                    p[n][3] = ex2(s[n][3] - m1);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) p[n][x] = ex2(p[n][x]);
                     l[n][0] += p[n][0] + p[n][2];
                     l[n][1] += p[n][1] + p[n][3];
                 }
@@ -508,26 +549,24 @@ __global__ void __launch_bounds__(32 * Cfg<D, Q8, NT>::kWarps, 1) attn_decode_ke
                         pf[n][0] = transposed8x8(bf16x2(p[n][0], p[n][1]));
                         pf[n][1] = transposed8x8(bf16x2(p[n][2], p[n][3]));
                     }
+                    const int row = (lane & 7) + ((lane >> 4) << 3);
+                    const uint32_t base = ring_s + at + C::kVals + row * C::kRow;
 #pragma unroll
                     for (int k = 0; k < KS; ++k) {
                         uint32_t vf[4];
-                        const int row = (lane & 7) + ((lane >> 4) << 3);
-                        ldsm4t(vf, vst + row * C::kRow + (((2 * k + ((lane >> 3) & 1)) ^ (row & 7)) << 4));
+                        ldsm4t(vf, base + (((2 * k + ((lane >> 3) & 1)) ^ (row & 7)) << 4));
 #pragma unroll
                         for (int n = 0; n < NT; ++n) mma_bf16(o[n][k], vf, pf[n][0], pf[n][1]);
                     }
                 } else {
                     // The codes are exact in fp16; the tokens' scales go to the weights, p * scale / unit, rounded to
                     // fp16 (11 bits; below 2^-14 of the unit they lose bits that do not reach the result).
-                    const unsigned char *vb8 = st + C::kVals;
                     float da[NB], db[NB];
-                    load_scales<NB>(da, st + 2 * C::kVals + C::kScales + g * NB * 4);
-                    load_scales<NB>(db, st + 2 * C::kVals + C::kScales + (g + 8) * NB * 4);
+                    load_scales<NB>(da, at + sr + C::kScales);
+                    load_scales<NB>(db, at + sr + C::kScales + 2 * NB * 4);
                     bool big = false;
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        big = big || fabsf(da[b]) > 4.0f * unit[b] || fabsf(db[b]) > 4.0f * unit[b];
-                    }
+                    for (int b = 0; b < NB; ++b) big = big || fmaxf(fabsf(da[b]), fabsf(db[b])) > 4.0f * unit[b];
                     if (__any_sync(0xffffffffu, big)) {
 #pragma unroll
                         for (int b = 0; b < NB; ++b) {
@@ -553,20 +592,14 @@ __global__ void __launch_bounds__(32 * Cfg<D, Q8, NT>::kWarps, 1) attn_decode_ke
                     }
 #pragma unroll
                     for (int b = 0; b < NB; ++b) {
-                        // values 4g .. 4g + 3 of tokens 2t, 2t + 1, 2t + 8, 2t + 9
                         uint32_t w[4];
+                        ldsm8t(w, at + vr[b]);
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const int row = 2 * t + (x & 1) + 8 * (x >> 1);
-                            const int grp = D == 128 ? b ^ ((row >> 1) & 3) : b ^ ((row >> 2) & 1);
-                            w[x] = *reinterpret_cast<const uint32_t *>(vb8 + row * C::kRow + grp * 32 + g * 4) ^ 0x80808080u;
-                        }
-                        const uint32_t lo0 = interleave<0>(w[0], w[1]), lo1 = interleave<2>(w[0], w[1]);
-                        const uint32_t hi0 = interleave<0>(w[2], w[3]), hi1 = interleave<2>(w[2], w[3]);
-                        const uint32_t v0[4] = {codes_f16x2<0>(lo0), codes_f16x2<2>(lo0), codes_f16x2<0>(hi0),
-                                                codes_f16x2<2>(hi0)};
-                        const uint32_t v1[4] = {codes_f16x2<0>(lo1), codes_f16x2<2>(lo1), codes_f16x2<0>(hi1),
-                                                codes_f16x2<2>(hi1)};
+                        for (int x = 0; x < 4; ++x) w[x] ^= 0x80808080u;
+                        const uint32_t v0[4] = {codes_f16x2<0>(w[0]), codes_f16x2<0>(w[1]), codes_f16x2<2>(w[0]),
+                                                codes_f16x2<2>(w[1])};
+                        const uint32_t v1[4] = {codes_f16x2<0>(w[2]), codes_f16x2<0>(w[3]), codes_f16x2<2>(w[2]),
+                                                codes_f16x2<2>(w[3])};
                         const float fa = da[b] * per_unit[b], fb = db[b] * per_unit[b];
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
@@ -588,18 +621,11 @@ __global__ void __launch_bounds__(32 * Cfg<D, Q8, NT>::kWarps, 1) attn_decode_ke
 #pragma unroll
                     for (int sh = 4; sh < 32; sh <<= 1) l[n][x] += __shfl_xor_sync(0xffffffffu, l[n][x], sh);
                     float *row = po + (8 * n + 2 * t + x) * D;
-                    if (!Q8) {
 #pragma unroll
-                        for (int k = 0; k < KS; ++k) {
-                            row[16 * k + g] = o[n][k][x];
-                            row[16 * k + g + 8] = o[n][k][x + 2];
-                        }
-                    } else {
-#pragma unroll
-                        for (int b = 0; b < NB; ++b)
-                            *reinterpret_cast<float4 *>(row + 32 * b + 4 * g) = make_float4(
-                                o[n][2 * b][x] * unit[b], o[n][2 * b][x + 2] * unit[b], o[n][2 * b + 1][x] * unit[b],
-                                o[n][2 * b + 1][x + 2] * unit[b]);
+                    for (int k = 0; k < KS; ++k) {
+                        const float f = Q8 ? unit[Q8 ? k / 2 : 0] : 1.0f;
+                        row[16 * k + g] = o[n][k][x] * f;
+                        row[16 * k + g + 8] = o[n][k][x + 2] * f;
                     }
                     if (g == 0) pml[8 * n + 2 * t + x] = make_float2(m[n][x], l[n][x]);
                 }
