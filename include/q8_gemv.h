@@ -329,8 +329,8 @@ q8_status q8_quantize(const double *w, int K, int N, int8_t *q, float *s);
  *                                     q8_quantize_act taken over each 32 values of a head (1.125 bytes a value)
  * page_stride is the number of values from one page to the next (heads * page_size * dim when pages are dense, more
  * when several caches share an allocation); the scales' pages are page_stride / 32 apart.
- *   dim 64 or 128; page_size a positive multiple of 16; page_stride a multiple of dim, at least heads * page_size *
- *   dim; k, v and the scales 16-byte aligned.
+ *   dim 64 or 128; page_size a positive multiple of 16; page_stride a multiple of 128, at least heads * page_size *
+ *   dim, pages * page_stride at most 2^38; k, v and the scales 16-byte aligned.
  * A token's slot is page * page_size + its offset in the page.  A block table is int32 [requests][table_width] (rows
  * table_pitch apart): entry i of a request is the page of its tokens i * page_size and on.  An entry outside
  * [0, pages) names no page: attention sees no token there.  Offsets are 64-bit throughout. */
@@ -427,7 +427,8 @@ q8_status q8_attn_prefill(const void *q, int ldq, const q8_kv_cache *cache, cons
 
 /* Reads the device fault word of the current device: nonzero when a kernel's bounded wait on a pipeline barrier ran
  * out (bit 0: a consumer waited about two seconds for a stage's data; bit 1: the producer waited as long for a free
- * stage; bit 2: a wait of the prefill GEMM ran out) and the kernel finished early -- that call's outputs are then
+ * stage; bit 2: a wait of the prefill GEMM ran out; bit 3: one of q8_attn_prefill, whose workspace has to be
+ * zeroed again) and the kernel finished early -- that call's outputs are then
  * wrong.  Synchronous with respect to the
  * device.  `clear` != 0 resets the word to 0.  Returns Q8_ERR_ARG for a NULL `fault`, Q8_ERR_CUDA on a CUDA error. */
 q8_status q8_device_fault(unsigned int *fault, int clear);

@@ -6,6 +6,7 @@
 #include <atomic>
 
 #include "../../include/q8_gemv.h"
+#include "q8_attn.h"
 #include "q8_launch.h"
 
 namespace q8 {
@@ -645,11 +646,12 @@ extern "C" q8_status q8_gemv_residual_norm(const void *x, const int8_t *q, const
 
 extern "C" q8_status q8_device_fault(unsigned int *fault, int clear) {
     if (!fault) return Q8_ERR_ARG;
-    unsigned gemm = 0;
+    unsigned gemm = 0, attn = 0;
     cudaError_t e = q8::read_fault_word(fault, clear != 0);
     if (e == cudaSuccess) e = q8::read_gemm_fault(&gemm, clear != 0);
+    if (e == cudaSuccess) e = q8::read_attn_fault(&attn, clear != 0);
     if (e != cudaSuccess) return cuda_fail(e);
-    *fault |= gemm;
+    *fault |= gemm | attn;
     return Q8_OK;
 }
 

@@ -1,0 +1,1054 @@
+// q8_attn_prefill: causal attention of a chunk of new tokens over the paged cache, on the 5th-generation tensor cores.
+//
+// 4 dim flops a visible (query row, key) pair against 4 dim bytes a key: from some hundred rows the tensor cores bound
+// it, so the kernel is built around keeping them fed.  A work item is 256 query rows of one cache head -- the tokens'
+// rows with the heads that share the cache head packed beside each other, so shared heads fill tiles as tokens do --
+// held as two 128-row tiles that take turns: while the softmax warps work on one tile's scores, the tensor cores
+// compute the other's.  For each 128-key tile:
+//     S = Q K^T (tcgen05.mma, both operands in shared memory, fp32 S in tensor memory)
+//     P = 2^(S scale log2(e) - m), rounded to 16 bits, written over S in tensor memory
+//     O += P V (P read from tensor memory, V from shared memory, fp32 O in tensor memory)
+// with a running m that only moves when a score passes it by 2^8 (then the row's O is rescaled in place).
+//
+// Warps: 0-3 and 4-7 the softmax of tiles A and B, one row a thread; 8 issues the MMAs; 9 requests keys and values;
+// the rest load Q and prepare values:
+//   bf16 cache: K and V tiles arrive by TMA straight in the MMA's 128-byte swizzle; the helpers (two warps) look through
+//     the V tiles that some row does not see whole, and clear what nobody sees;
+//   Q8_0 cache: codes and scales arrive by bulk copies, and the helpers (four warps) turn them into fp16 operands,
+//     code * scale / unit with one power of two `unit` a tile, and Q into fp16 with one a row: 11 significant bits.
+//     (bf16 operands would cost the scores and values 8-bit roundings: measured 0.0029 against 0.0017 relative error.)
+//
+// The tiles of all items are one list, cut into equal spans, one for each CTA (one CTA per SM); an item that crosses
+// spans leaves fp32 parts in the workspace, which the CTA that arrives last adds in span order.
+//
+// A weight of zero times a value that is not finite is NaN, so a value that one row sees and another of its tile does
+// not must not reach the MMA unless finite: such values are cleared, and the rows that do see them get them added at
+// the end (a rare, slow walk).
+//
+// Every wait is bounded (about two seconds); one that runs out records a fault, and the CTA drains and returns.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cudaTypedefs.h>
+#include <math.h>
+
+#include "q8_attn.h"
+#include "q8_device.cuh"
+
+namespace q8 {
+namespace {
+
+constexpr int kTile = 128;   // keys of a tile, and rows of a query tile
+constexpr int kRows = 256;   // query rows of an item
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kSlack = 8.0f;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kHelpWarp = 10;
+constexpr unsigned kTmemColumns = 512;
+constexpr uint32_t kColO = 256;  // S of tiles A and B at columns 0 and 128, O from here
+constexpr unsigned kFaultAttnWait = 8u;
+
+__device__ unsigned int g_attn_fault = 0;
+
+template <int D, bool Q8> struct Cfg {
+    static constexpr int kSub = D / 64;                    // 128-byte-wide column blocks of an operand
+    static constexpr int kOp = kSub * kTile * 128;         // bytes of a K, V or Q operand tile
+    static constexpr int kRaw = Q8 ? kTile * D + kTile * (D / 32) * 4 : 0;
+    static constexpr int kSlots = Q8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 10);
+    static constexpr int kRawSlots = Q8 ? (D == 128 ? 3 : 4) : 0;
+    static constexpr int kHelpers = Q8 ? 4 : 2;            // warps
+    static constexpr int kThreads = 32 * (kHelpWarp + kHelpers);
+    static constexpr int kRing = 2 * kOp;                  // after Q's two tiles
+    static constexpr int kRawAt = kRing + kSlots * kOp;
+    static constexpr int kCtl = kRawAt + kRawSlots * kRaw;
+    static constexpr int kSmem = kCtl + (Q8 ? 4096 : 2048);
+    static_assert(kSmem <= 226 * 1024, "");
+};
+
+// Control block in shared memory.
+template <int D, bool Q8> struct Control {
+    using C = Cfg<D, Q8>;
+    uint64_t full[10], ready[10], empty[10];   // operand ring: landed, usable, free
+    uint64_t raw_full[4], raw_empty[4];        // raw ring (Q8_0)
+    uint64_t q_full, q_empty, drain;
+    uint64_t s_full[2], p_ready[2], o_full[2], joined, decided;
+    // Of key tile number n of this CTA at n & 7 (no role is more than five tiles behind the requests):
+    unsigned pages[8];  // bits: which 16-token groups lie on a page
+    float unit[2][8];   // Q8_0: log2 of the keys' and the values' unit
+    uint32_t tmem;
+    int abort, poison, last;
+    int first_r, first_qt;
+    long long first_start;
+    long long scan[20];
+    float qscale[2][Q8 ? kRows : 1];  // Q8_0: the powers of two that undo the rows' fp16 scaling, by segment parity
+};
+static_assert(sizeof(Control<128, true>) <= 4096 && sizeof(Control<128, false>) <= 2048, "");
+
+__device__ __forceinline__ uint32_t saddr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void bar_init(uint64_t *bar, unsigned n) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(saddr(bar)), "r"(n) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(saddr(bar)) : "memory");
+}
+__device__ __forceinline__ void bar_arrive_tx(uint64_t *bar, unsigned bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(saddr(bar)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint64_t *bar, unsigned parity) {
+    uint32_t done;
+    asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(done)
+                 : "r"(saddr(bar)), "r"(parity)
+                 : "memory");
+    return done != 0;
+}
+__device__ __forceinline__ uint64_t now_ns() {
+    uint64_t t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+// Wait for a phase of `bar`; false when the CTA is aborting, or after about two seconds (which starts the abort).
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, unsigned parity, volatile int *abort) {
+    if (bar_try(bar, parity)) return true;
+    const uint64_t t0 = now_ns();
+    for (unsigned n = 1;; ++n) {
+        if (bar_try(bar, parity)) return true;
+        if ((n & 63u) == 0) {
+            if (*abort) return false;
+            if (now_ns() - t0 > 2000000000ull) {
+                *abort = 1;
+                atomicOr(&g_attn_fault, kFaultAttnWait);
+                return false;
+            }
+        }
+    }
+}
+// The same for a whole warp, one answer for all lanes.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, unsigned parity, volatile int *abort) {
+    return __all_sync(0xffffffffu, bar_wait(bar, parity, abort));
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void commit(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(saddr(bar))
+                 : "memory");
+}
+// Shared-memory matrix descriptor, 128-byte swizzle (layout 2).  K-major operands (Q, K): rows of 128 bytes, groups of
+// 8 rows 1024 bytes apart.  MN-major (V): 64 values of dim in 128 bytes, groups of 8 keys 1024 bytes apart, the next
+// 64 values `lead` bytes on.
+__device__ __forceinline__ uint64_t desc128(uint32_t addr, uint32_t lead) {
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
+        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+__device__ __forceinline__ void tm_ld32(uint32_t a, uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(a));
+}
+__device__ __forceinline__ void tm_st32(uint32_t a, const uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(a),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+__device__ __forceinline__ void tm_st16(uint32_t a, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(a),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+__device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void bulk(uint32_t dst, const void *src, unsigned bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(saddr(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void tma3(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
+            "r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(saddr(bar))
+        : "memory");
+}
+
+struct PrefillArgs {
+    AttnArgs a;
+    int run;  // consecutive tokens of a tile that lie on one page wherever they start: gcd(page_size, 128)
+};
+
+// 256 query rows of one cache head: packed row x is token (256 qt + x) / group of the request, head (256 qt + x) %
+// group of those that share the cache head.  Its key tiles are [0, us) for the sinks and [ul, ul + n - us).
+struct Item {
+    int r, qt, h;
+    long long start;  // of its tiles in the list
+    int row0, tokens, pos0, rows;
+    int p_min, p_max, end, lo, us, ul, n;
+
+    __device__ __forceinline__ int tile(int i) const { return i < us ? i : ul + (i - us); }
+    // Whether some row of the item does not see all of tile u, pages aside.
+    __device__ __forceinline__ bool partial(const AttnArgs &a, int u) const {
+        const int j0 = u * kTile;
+        return j0 + kTile > end || j0 + kTile - 1 > p_min ||
+               (a.window && p_max - j0 >= a.window && j0 + kTile > a.sinks);
+    }
+};
+// Key tiles that rows at positions p_min .. p_max visit.
+__device__ __forceinline__ void span_of(const AttnArgs &a, Item &x) {
+    x.end = min(max(x.p_max + 1, 0), a.width * a.page_size);
+    x.lo = a.window ? min(max(x.p_min - a.window + 1, 0), x.end) : 0;
+    const int sinks = a.window ? min(a.sinks, x.lo) : 0;
+    x.us = (sinks + kTile - 1) / kTile;
+    x.ul = max(x.lo / kTile, x.us);
+    x.n = x.us + max(0, (x.end + kTile - 1) / kTile - x.ul);
+}
+__device__ __forceinline__ void request_of(const AttnArgs &a, Item &x) {
+    const int t0 = min(max(a.row_start[x.r], 0), a.rows), t1 = min(max(a.row_start[x.r + 1], t0), a.rows);
+    x.row0 = t0;
+    x.tokens = t1 - t0;
+    x.pos0 = max(a.lens[x.r], 0) - x.tokens;
+}
+__device__ __forceinline__ int q_tiles(const AttnArgs &a, int tokens) {
+    return (int)(((long long)tokens * a.group + kRows - 1) / kRows);
+}
+__device__ __forceinline__ void q_tile_of(const AttnArgs &a, Item &x) {
+    const long long first = (long long)x.qt * kRows, all = (long long)x.tokens * a.group;
+    x.rows = (int)min((long long)kRows, all - first);
+    x.p_min = x.pos0 + (int)(first / a.group);
+    x.p_max = x.pos0 + (int)((first + x.rows - 1) / a.group);
+    span_of(a, x);
+}
+__device__ __forceinline__ void next_item(const AttnArgs &a, Item &x) {
+    x.start += x.n;
+    if (++x.h < a.kv_heads) return;
+    x.h = 0;
+    do {
+        if (++x.qt >= q_tiles(a, x.tokens)) {
+            do {
+                if (++x.r >= a.R) return;  // never reached: the walk ends within the list
+                request_of(a, x);
+            } while (x.tokens == 0);
+            x.qt = 0;
+        }
+        q_tile_of(a, x);
+    } while (x.n == 0);
+}
+
+// Whether the row at position p sees key j (pages aside).
+__device__ __forceinline__ bool sees(const AttnArgs &a, int p, int j) {
+    return j <= p && (!a.window || p - j < a.window || j < a.sinks);
+}
+
+// Values that are not finite in tiles that only some rows see were cleared before the MMA; add them to the rows that
+// do see them.  o: 32 of the row's values from column c0.
+template <int D, bool Q8>
+__device__ __noinline__ void add_nonfinite(const AttnArgs &a, const Item it, int i0, int i1, int p, int c0, float *o) {
+    for (int i = i0; i < i1; ++i) {
+        const int u = it.tile(i);
+        for (int c = 0; c < kTile; ++c) {
+            const int j = u * kTile + c;
+            if (j >= it.end) break;
+            if (!sees(a, p, j)) continue;
+            const int page = a.table[(size_t)it.r * a.pitch + j / a.page_size];
+            if (page < 0 || page >= a.pages) continue;
+            // only tiles that some row does not see whole were cleared
+            bool cleared = it.partial(a, u);
+            for (int b = 0; b < kTile / 16 && !cleared; ++b) {
+                const int pg = a.table[(size_t)it.r * a.pitch + (u * kTile + 16 * b) / a.page_size];
+                cleared = pg < 0 || pg >= a.pages;
+            }
+            if (!cleared) break;
+            const long long at =
+                (long long)page * a.page_stride + ((long long)it.h * a.page_size + j % a.page_size) * D + c0;
+            for (int d = 0; d < 32; ++d) {
+                float v;
+                if (Q8) v = (float)static_cast<const signed char *>(a.v)[at + d] * a.vs[(at + d) / 32];
+                else v = __uint_as_float((uint32_t)static_cast<const uint16_t *>(a.v)[at + d] << 16);
+                if (!(fabsf(v) < INFINITY)) o[d] += v;
+            }
+        }
+    }
+}
+
+template <int D, bool Q8>
+__global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
+    prefill_kernel(const __grid_constant__ PrefillArgs pa, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+    using C = Cfg<D, Q8>;
+    const AttnArgs &a = pa.a;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    Control<D, Q8> &ctl = *reinterpret_cast<Control<D, Q8> *>(smem + C::kCtl);
+    volatile int *abort = &ctl.abort;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    if (tid == 0) {
+        for (int i = 0; i < C::kSlots; ++i) {
+            bar_init(&ctl.full[i], 1);
+            bar_init(&ctl.ready[i], C::kHelpers);
+            bar_init(&ctl.empty[i], 1);
+        }
+        for (int i = 0; i < C::kRawSlots; ++i) {
+            bar_init(&ctl.raw_full[i], 1);
+            bar_init(&ctl.raw_empty[i], C::kHelpers);
+        }
+        bar_init(&ctl.q_full, C::kHelpers);
+        bar_init(&ctl.q_empty, 1);
+        bar_init(&ctl.drain, 1);
+        bar_init(&ctl.joined, 256);
+        bar_init(&ctl.decided, 1);
+        for (int i = 0; i < 2; ++i) {
+            bar_init(&ctl.s_full[i], 1);
+            bar_init(&ctl.p_ready[i], 128);
+            bar_init(&ctl.o_full[i], 1);
+        }
+        ctl.abort = 0;
+        ctl.poison = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&ctl.tmem)),
+                     "r"(kTmemColumns)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    // ---- the list and this CTA's span: query tiles of each request, then key tiles of each query tile ----
+    int *qsum = reinterpret_cast<int *>(smem);  // [R + 1] exclusive sums (the operands come later)
+    constexpr int T = C::kThreads;
+    long long total = 0, b0 = 0, b1 = 0, span = 1;
+    {
+        const int each = (a.R + T - 1) / T, ra = min(a.R, tid * each), rb = min(a.R, ra + each);
+        Item x;
+        int mine = 0;
+        for (x.r = ra; x.r < rb; ++x.r) {
+            request_of(a, x);
+            mine += q_tiles(a, x.tokens);
+        }
+        int upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
+        }
+        if (lane == 31) ctl.scan[warp] = upto;
+        __syncthreads();
+        int before = upto - mine, tiles = 0;
+        for (int w = 0; w < T / 32; ++w) {
+            if (w < warp) before += (int)ctl.scan[w];
+            tiles += (int)ctl.scan[w];
+        }
+        for (x.r = ra; x.r < rb; ++x.r) {
+            request_of(a, x);
+            qsum[x.r] = before;
+            before += q_tiles(a, x.tokens);
+        }
+        if (tid == 0) qsum[a.R] = tiles;
+        __syncthreads();
+        // this thread's query tiles of all of them
+        const int qe = (tiles + T - 1) / T, qa = min(tiles, tid * qe), qb = min(tiles, qa + qe);
+        long long keys = 0;
+        auto seek = [&](int q) {  // x at query tile q of the list
+            int lo = 0, hi = a.R - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (qsum[mid] <= q) lo = mid; else hi = mid - 1;
+            }
+            x.r = lo;
+            x.qt = q - qsum[lo];
+            request_of(a, x);
+            q_tile_of(a, x);
+        };
+        for (int q = qa; q < qb; ++q) {
+            seek(q);
+            keys += x.n;
+        }
+        long long sum = keys;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += y;
+        }
+        __syncthreads();  // every thread has read scan
+        if (lane == 31) ctl.scan[warp] = sum;
+        __syncthreads();
+        long long ahead = sum - keys;
+        for (int w = 0; w < T / 32; ++w) {
+            if (w < warp) ahead += ctl.scan[w];
+            total += ctl.scan[w];
+        }
+        total *= a.kv_heads;
+        span = max((total + gridDim.x - 1) / gridDim.x, 4ll);
+        b0 = span * blockIdx.x;
+        b1 = min(total, b0 + span);
+        if (b0 < b1 && ahead * a.kv_heads <= b0 && b0 < (ahead + keys) * a.kv_heads) {
+            for (int q = qa;; ++q) {  // exactly one thread holds unit b0
+                seek(q);
+                if (b0 < (ahead + x.n) * a.kv_heads) break;
+                ahead += x.n;
+            }
+            ctl.first_r = x.r;
+            ctl.first_qt = x.qt;
+            ctl.first_start = ahead * a.kv_heads;
+        }
+    }
+    fence_before();
+    fence_async();
+    __syncthreads();  // also: qsum is read, the operands may land over it
+    fence_after();
+    const uint32_t tmem = ctl.tmem;
+    const bool work = b0 < b1;
+
+    Item it;
+    if (work) {
+        it.r = ctl.first_r;
+        it.qt = ctl.first_qt;
+        request_of(a, it);
+        q_tile_of(a, it);
+        it.h = (int)((b0 - ctl.first_start) / it.n);
+        it.start = ctl.first_start + (long long)it.h * it.n;
+    }
+    // An item's tiles [i0, i1) fall into this span.
+#define Q8_EACH_SEGMENT                                                                   \
+    for (int i0 = work ? (int)(b0 - it.start) : 0, i1 = 0, more = work;                   \
+         more && (i1 = (int)min((long long)it.n, b1 - it.start), true);                   \
+         more = it.start + it.n < b1, more ? (next_item(a, it), i0 = 0) : 0)
+
+    if (warp == kLoadWarp) {
+        // ---- keys and values: lane i requests run i of each tile ----
+        const int runs = kTile / pa.run, per = pa.run / 16;
+        unsigned cnt = 0;
+        bool ok = true;
+        Q8_EACH_SEGMENT {
+            if (!ok) break;
+            const int *row = a.table + (size_t)it.r * a.pitch;
+            int page = -1, off = 0;
+            auto look = [&](int i) {
+                const int j = it.tile(i) * kTile + lane * pa.run;
+                page = -1;
+                if (lane < runs && j < it.end) {
+                    page = row[j / a.page_size];
+                    off = j % a.page_size;
+                }
+            };
+            look(i0);
+            for (int i = i0; i < i1 && ok; ++i) {
+                const bool there = page >= 0 && page < a.pages;
+                const unsigned got = __ballot_sync(0xffffffffu, there);
+                unsigned groups = 0;  // a bit for each 16 tokens
+                for (int b = 0; b < runs; ++b)
+                    if (got >> b & 1u) groups |= ((1u << per) - 1u) << (b * per);
+                const int mypage = page, myoff = off;
+                if (i + 1 < i1) look(i + 1);
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv, ++cnt) {
+                    const unsigned slots = Q8 ? C::kRawSlots : C::kSlots;
+                    const unsigned s = cnt % slots, turn = cnt / slots;
+                    uint64_t *full = Q8 ? &ctl.raw_full[s] : &ctl.full[s];
+                    if (cnt >= slots && !warp_wait(Q8 ? &ctl.raw_empty[s] : &ctl.empty[s], (turn - 1) & 1, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) {
+                        if (kv == 0) ctl.pages[(cnt >> 1) & 7] = groups;
+                        const unsigned bytes = __popc(groups) * 16 * (Q8 ? D + D / 32 * 4 : 2 * D);
+                        bar_arrive_tx(full, bytes);
+                    }
+                    __syncwarp();
+                    if (there) {
+                        if (!Q8) {
+                            const uint32_t dst = saddr(smem + C::kRing + s * C::kOp) + lane * pa.run * 128;
+#pragma unroll
+                            for (int sub = 0; sub < C::kSub; ++sub)
+                                tma3(dst + sub * kTile * 128, kv ? &vmap : &kmap, 64 * sub, it.h * a.page_size + myoff,
+                                     mypage, full);
+                        } else {
+                            const long long at = (long long)mypage * a.page_stride +
+                                                 ((long long)it.h * a.page_size + myoff) * D;
+                            const uint32_t dst = saddr(smem + C::kRawAt + s * C::kRaw);
+                            bulk(dst + lane * pa.run * D, static_cast<const signed char *>(kv ? a.v : a.k) + at,
+                                 pa.run * D, full);
+                            bulk(dst + kTile * D + lane * pa.run * (D / 32) * 4, (kv ? a.vs : a.ks) + at / 32,
+                                 pa.run * (D / 32) * 4, full);
+                        }
+                    }
+                }
+            }
+        }
+        if (!ok) {  // the copies in flight land before the shared memory goes
+            const unsigned slots = Q8 ? C::kRawSlots : C::kSlots;
+            for (unsigned c = cnt > slots ? cnt - slots : 0; c < cnt; ++c) {
+                const uint64_t t0 = now_ns();
+                while (!bar_try(Q8 ? &ctl.raw_full[c % slots] : &ctl.full[c % slots], (c / slots) & 1) &&
+                       now_ns() - t0 < 2000000000ull) {
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        // ---- the MMAs (one thread) ----
+        if (lane == 0) {
+            constexpr uint32_t fmt = Q8 ? 0u : 1u;  // fp16 or bf16 operands
+            const uint32_t id_s = (1u << 4) | (fmt << 7) | (fmt << 10) | (a.scale < 0.0f ? 1u << 13 : 0u) |
+                                  ((kTile >> 3) << 17) | ((kTile >> 4) << 24);
+            constexpr uint32_t id_o = (1u << 4) | (fmt << 7) | (fmt << 10) | (1u << 16) | ((D >> 3) << 17) |
+                                      ((kTile >> 4) << 24);
+            const uint32_t q_at = saddr(smem), ring = saddr(smem + C::kRing);
+            unsigned cnt = 0, seg = 0, pcnt[2] = {0, 0};
+            bool ok = true;
+            auto scores = [&](int x, unsigned s) {  // S of tile x with the keys in slot s
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t o = (k / 4) * kTile * 128 + (k % 4) * 32;
+                    mma_ss(tmem + x * kTile, desc128(q_at + x * C::kOp + o, 16), desc128(ring + s * C::kOp + o, 16), id_s,
+                           k > 0);
+                }
+                commit(&ctl.s_full[x]);
+            };
+            Q8_EACH_SEGMENT {
+                if (!ok) break;
+                const int nx = it.rows > kTile ? 2 : 1;
+                if (!(ok = bar_wait(&ctl.q_full, seg & 1, abort))) break;
+                auto usable = [&](unsigned c, bool value) {
+                    const unsigned s = c % C::kSlots, par = (c / C::kSlots) & 1;
+                    return bar_wait(Q8 || value ? &ctl.ready[s] : &ctl.full[s], par, abort);
+                };
+                const unsigned c0 = cnt;
+                if (!(ok = usable(c0, false))) break;
+                fence_after();
+                for (int x = 0; x < nx; ++x) scores(x, c0 % C::kSlots);
+                commit(&ctl.empty[c0 % C::kSlots]);
+                if (i1 - i0 == 1) commit(&ctl.q_empty);
+                for (int i = i0; i < i1 && ok; ++i) {
+                    const unsigned cv = c0 + 2 * (i - i0) + 1, ck = cv + 1;
+                    const bool last = i + 1 == i1;
+                    if (!(ok = usable(cv, true))) break;
+                    for (int x = 0; x < nx; ++x) {
+                        if (!(ok = bar_wait(&ctl.p_ready[x], pcnt[x] & 1, abort))) break;
+                        ++pcnt[x];
+                        fence_after();
+#pragma unroll
+                        for (int k = 0; k < kTile / 16; ++k)
+                            mma_ts(tmem + kColO + x * 128, tmem + x * kTile + k * 8,
+                                   desc128(ring + (cv % C::kSlots) * C::kOp + k * 2048, kTile * 128), id_o,
+                                   i > i0 || k > 0);
+                        if (last) commit(&ctl.o_full[x]);
+                        if (x == nx - 1) commit(&ctl.empty[cv % C::kSlots]);
+                        if (!last) {
+                            if (x == 0) {
+                                if (!(ok = usable(ck, false))) break;
+                                fence_after();
+                            }
+                            scores(x, ck % C::kSlots);
+                            if (x == nx - 1) {
+                                commit(&ctl.empty[ck % C::kSlots]);
+                                if (i + 2 == i1) commit(&ctl.q_empty);
+                            }
+                        }
+                    }
+                }
+                cnt = c0 + 2 * (i1 - i0);
+                ++seg;
+            }
+        }
+        __syncwarp();
+    } else if (warp >= kHelpWarp) {
+        // ---- Q, and what the tiles need before the MMAs ----
+        const int ht = tid - 32 * kHelpWarp;
+        constexpr int HT = 32 * C::kHelpers;
+        unsigned cnt = 0, seg = 0;
+        bool ok = true;
+        Q8_EACH_SEGMENT {
+            if (!ok) break;
+            if (seg && !(ok = warp_wait(&ctl.q_empty, (seg - 1) & 1, abort))) break;
+            // Q: row x's 16-byte chunk c at chunk c ^ (x & 7) of its 128 bytes (the 128-byte swizzle)
+            constexpr int CH = D / 8;
+            const long long first = (long long)it.qt * kRows;
+            if (!Q8) {
+                for (int e = ht; e < kRows * CH; e += HT) {
+                    const int x = e / CH, c = e % CH;
+                    const bool live = x < it.rows;
+                    const int rho = live ? (int)((first + x) / a.group) : 0;
+                    const int gh = live ? (int)((first + x) - (long long)rho * a.group) : 0;
+                    const uint16_t *src = a.q + (size_t)(it.row0 + rho) * a.ldq + (size_t)(it.h * a.group + gh) * D + 8 * c;
+                    const uint32_t dst = saddr(smem) + (x / kTile) * C::kOp + (c / 8) * kTile * 128 + (x % kTile) * 128 +
+                                         (((c & 7) ^ (x & 7)) << 4);
+                    cp16(dst, live ? src : a.q, live);
+                }
+                asm volatile("cp.async.wait_all;" ::: "memory");
+            } else {
+                for (int e0 = 0; e0 < kRows * CH; e0 += HT * 4) {
+                    uint4 v[4];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const int e = e0 + y * HT + ht, x = e / CH, c = e % CH;
+                        v[y] = make_uint4(0u, 0u, 0u, 0u);
+                        if (x < it.rows) {
+                            const int rho = (int)((first + x) / a.group);
+                            const int gh = (int)((first + x) - (long long)rho * a.group);
+                            v[y] = *reinterpret_cast<const uint4 *>(a.q + (size_t)(it.row0 + rho) * a.ldq +
+                                                                    (size_t)(it.h * a.group + gh) * D + 8 * c);
+                        }
+                    }
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const int e = e0 + y * HT + ht, x = e / CH, c = e % CH;
+                        uint32_t w[4] = {v[y].x, v[y].y, v[y].z, v[y].w};
+                        uint32_t mx = 0u;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) mx = max(mx, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
+#pragma unroll
+                        for (int o = 1; o < CH; o <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                        // times a power of two that takes the row's largest magnitude to [2^9, 2^10)
+                        const int ex = min(max((int)(mx >> 7), 1), 254), up = min(127 + 9 - ex, 126);
+                        const float f = __uint_as_float((uint32_t)(up + 127) << 23);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            w[k] = f16x2(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xFFFF0000u) * f);
+                        *reinterpret_cast<uint4 *>(smem + (x / kTile) * C::kOp + (c / 8) * kTile * 128 +
+                                                   (x % kTile) * 128 + (((c & 7) ^ (x & 7)) << 4)) =
+                            make_uint4(w[0], w[1], w[2], w[3]);
+                        if (c == 0) ctl.qscale[seg & 1][Q8 ? x : 0] = __uint_as_float((uint32_t)(127 - up) << 23);
+                    }
+                }
+            }
+            fence_async();
+            __syncwarp();
+            if (lane == 0) bar_arrive(&ctl.q_full);
+            int v_ex = 0;
+            for (int i = i0; i < i1 && ok; ++i) {
+                const int u = it.tile(i), j0 = u * kTile;
+                // a key that some row of the item may see
+                auto live = [&](int c, unsigned groups) {
+                    const int j = j0 + c;
+                    return (groups >> (c >> 4) & 1u) && j < it.end && (j >= it.lo || j < a.sinks);
+                };
+                for (int kv = 0; kv < 2 && ok; ++kv, ++cnt) {
+                    const unsigned s = cnt % C::kSlots, par = (cnt / C::kSlots) & 1;
+                    unsigned char *op = smem + C::kRing + s * C::kOp;
+                    if (!Q8) {
+                        if (!(ok = warp_wait(&ctl.full[s], par, abort))) break;
+                        const unsigned groups = ctl.pages[(cnt >> 1) & 7];
+                        if (kv && (groups != 0xFFu || it.partial(a, u))) {
+                            bool found = false;
+                            for (int e = ht; e < kTile * CH; e += HT) {
+                                const int c = e / CH, ch = e % CH;
+                                uint4 *at = reinterpret_cast<uint4 *>(op + (ch / 8) * kTile * 128 + c * 128 + (ch % 8) * 16);
+                                if (!live(c, groups)) {
+                                    *at = make_uint4(0u, 0u, 0u, 0u);
+                                    continue;
+                                }
+                                uint4 v = *at;
+                                uint32_t w[4] = {v.x, v.y, v.z, v.w}, bad = 0u;
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) bad |= ((w[k] & 0x7FFF7FFFu) + 0x00800080u) & 0x80008000u;
+                                if (bad) {
+                                    found = true;
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) {
+                                        const uint32_t b = ((w[k] & 0x7FFF7FFFu) + 0x00800080u) & 0x80008000u;
+                                        w[k] &= ~((b >> 15) * 0xFFFFu);
+                                    }
+                                    *at = make_uint4(w[0], w[1], w[2], w[3]);
+                                }
+                            }
+                            if (found) *(volatile int *)&ctl.poison = 1;
+                            fence_async();
+                        }
+                        __syncwarp();
+                        if (lane == 0) bar_arrive(&ctl.ready[s]);
+                        continue;
+                    }
+                    // Q8_0: codes and scales to fp16
+                    const unsigned rs = cnt % (C::kRawSlots ? C::kRawSlots : 1);
+                    const unsigned rpar = (cnt / (C::kRawSlots ? C::kRawSlots : 1)) & 1;
+                    if (cnt >= (unsigned)C::kSlots && !(ok = warp_wait(&ctl.empty[s], par ^ 1, abort))) break;
+                    if (!(ok = warp_wait(&ctl.raw_full[rs], rpar, abort))) break;
+                    const unsigned char *raw = smem + C::kRawAt + rs * C::kRaw;
+                    const float *scl = reinterpret_cast<const float *>(raw + kTile * D);
+                    const unsigned groups = ctl.pages[(cnt >> 1) & 7];
+                    const bool part = groups != 0xFFu || it.partial(a, u);
+                    constexpr int NB = D / 32;
+                    float mx = 0.0f;  // the tile's largest finite scale: every warp looks for itself
+#pragma unroll
+                    for (int y = 0; y < kTile * NB / 32; ++y) {
+                        const int e = y * 32 + lane;
+                        const float f = fabsf(scl[e]);
+                        if (f < INFINITY && (!part || live(e / NB, groups))) mx = fmaxf(mx, f);
+                    }
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                    // The values' unit only grows within a segment, and neither is below 2^-63, so that a tile of
+                    // zeros does not take the row sums, which are kept apart from the units, out of fp32's range.
+                    int ex = min(max((int)(__float_as_uint(mx) >> 23), 64), 252);
+                    if (kv) ex = v_ex = max(v_ex, ex);
+                    const float down = __uint_as_float((uint32_t)(254 - ex) << 23);  // 2^-(ex - 127)
+                    bool found = false;
+                    constexpr int RC = D / 16;  // 16-code chunks a row
+#pragma unroll 4
+                    for (int e = ht; e < kTile * RC; e += HT) {
+                        const int c = e / RC, ch = e % RC;
+                        float f = scl[c * NB + ch / 2] * down;
+                        uint4 v = *reinterpret_cast<const uint4 *>(raw + c * D + ch * 16);
+                        if (part) {
+                            const bool see = live(c, groups);
+                            if (!see || (kv && !(fabsf(f) < INFINITY))) {
+                                found = found || see;
+                                v = make_uint4(0u, 0u, 0u, 0u);
+                                f = 0.0f;
+                            }
+                        }
+                        const __half2 f2 = __float2half2_rn(f);
+                        const uint32_t w[4] = {v.x ^ 0x80808080u, v.y ^ 0x80808080u, v.z ^ 0x80808080u, v.w ^ 0x80808080u};
+                        uint32_t h[8];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                const uint32_t b = __byte_perm(w[k], 0x64646464u, y ? 0x4342 : 0x4140);
+                                const __half2 q = __hmul2(__hsub2(*reinterpret_cast<const __half2 *>(&b),
+                                                                  __half2half2(__ushort_as_half(0x6480))), f2);
+                                h[2 * k + y] = *reinterpret_cast<const uint32_t *>(&q);
+                            }
+                        unsigned char *to = op + (ch / 4) * kTile * 128 + c * 128;
+                        const int d0 = ((2 * ch) & 7) ^ (c & 7), d1 = ((2 * ch + 1) & 7) ^ (c & 7);
+                        const bool swap = (ch >> 2) & 1;  // the two halves of a quarter warp write different banks
+                        const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+                        *reinterpret_cast<uint4 *>(to + (swap ? d1 : d0) * 16) = swap ? hi : lo;
+                        *reinterpret_cast<uint4 *>(to + (swap ? d0 : d1) * 16) = swap ? lo : hi;
+                    }
+                    if (found) *(volatile int *)&ctl.poison = 1;
+                    if (ht == 0) ctl.unit[kv][(cnt >> 1) & 7] = (float)(ex - 127);
+                    fence_async();
+                    __syncwarp();
+                    if (lane == 0) {
+                        bar_arrive(&ctl.raw_empty[rs]);
+                        bar_arrive(&ctl.ready[s]);
+                    }
+                }
+            }
+            ++seg;
+        }
+        __syncwarp();
+    } else {
+        // ---- softmax: thread = row of tile x ----
+        const int x = warp >> 2, quarter = warp & 3;
+        const int rx = x * kTile + quarter * 32 + lane;  // packed row within the item
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        const uint32_t ts = tmem + lanes + x * kTile, to = tmem + lanes + kColO + x * 128;
+        constexpr float kLeast = 1.17549435e-38f;  // a factor of 0 would make NaN of a hidden score's -inf
+        const float sc0 = fmaxf(fabsf(a.scale) * kLog2e, kLeast);
+        unsigned cnt = 0, scnt = 0, ocnt = 0, shared = 0, seg = 0;
+        bool ok = true;
+        Q8_EACH_SEGMENT {
+            if (!ok) break;
+            const bool active = x == 0 || it.rows > kTile;
+            const bool row_live = rx < it.rows;
+            const long long rho = (long long)it.qt * kRows + rx;
+            const int tok = (int)(rho / a.group), gh = (int)(rho - (long long)tok * a.group);
+            const int p = it.pos0 + tok;
+            float M = -INFINITY, l = 0.0f;
+            if (active) {
+                float sc = sc0;
+                for (int i = i0; i < i1 && ok; ++i) {
+                    const unsigned ck = cnt + 2 * (i - i0), at = (ck >> 1) & 7;
+                    if (!(ok = warp_wait(&ctl.s_full[x], scnt & 1, abort))) break;
+                    ++scnt;
+                    fence_after();
+                    float shift = 0.0f;  // log2 of the values' unit (Q8_0)
+                    const unsigned groups = *(volatile unsigned *)&ctl.pages[at];
+                    if (Q8) {
+                        const unsigned cv = ck + 1;
+                        if (!(ok = warp_wait(&ctl.ready[cv % C::kSlots], (cv / C::kSlots) & 1, abort))) break;
+                        const float back = *(volatile float *)&ctl.qscale[seg & 1][Q8 ? rx : 0];
+                        sc = fmaxf(sc0 * back * ex2(*(volatile float *)&ctl.unit[0][at]), kLeast);
+                        shift = *(volatile float *)&ctl.unit[1][at];
+                    }
+                    const int u = it.tile(i), j0 = u * kTile;
+                    const bool part = groups != 0xFFu || it.partial(a, u);
+                    // columns [c_lo, c_hi] and [0, c_sink) are visible
+                    const int c_hi = min(p, it.end - 1) - j0;
+                    const int c_lo = a.window ? max(p - a.window + 1 - j0, 0) : 0, c_sink = a.window ? a.sinks - j0 : 0;
+                    auto hide = [&](uint32_t (&v)[32], int c0) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            const int c = c0 + k;
+                            const bool see = c <= c_hi && (c >= c_lo || c < c_sink) && (groups >> (c >> 4) & 1u);
+                            if (!see) v[k] = 0xFF800000u;
+                        }
+                    };
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int c0 = 0; c0 < kTile; c0 += 32) {
+                        uint32_t v[32];
+                        tm_ld32(ts + c0, v);
+                        tm_wait_ld();
+                        if (part) hide(v, c0);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) mx = fmaxf(mx, __uint_as_float(v[k]));
+                    }
+                    mx = mx == -INFINITY ? mx : fmaf(mx, sc, shift);
+                    const bool above = mx > M + kSlack || (M == -INFINITY && mx > M);
+                    if (__any_sync(0xffffffffu, above)) {
+                        const float now = above ? mx : M;
+                        const float f = above ? ex2(M - now) : 1.0f;  // 0 from -inf
+                        M = now;
+                        l *= f;
+                        if (i > i0) {
+#pragma unroll 1
+                            for (int c0 = 0; c0 < D; c0 += 32) {
+                                uint32_t v[32];
+                                tm_ld32(to + c0, v);
+                                tm_wait_ld();
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * f);
+                                tm_st32(to + c0, v);
+                            }
+                        }
+                    }
+                    const float off = shift - (M == -INFINITY ? 0.0f : M);
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int c0 = 0; c0 < kTile; c0 += 32) {
+                        uint32_t v[32], w[16];
+                        tm_ld32(ts + c0, v);
+                        tm_wait_ld();
+                        if (part) hide(v, c0);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            const float p0 = ex2(fmaf(__uint_as_float(v[2 * k]), sc, off));
+                            const float p1 = ex2(fmaf(__uint_as_float(v[2 * k + 1]), sc, off));
+                            sum += p0 + p1;
+                            w[k] = Q8 ? f16x2(p0, p1) : bf16x2(p0, p1);
+                        }
+                        tm_st16(ts + c0 / 2, w);
+                    }
+                    l += Q8 ? sum * ex2(-shift) : sum;
+                    tm_wait_st();
+                    fence_before();
+                    bar_arrive(&ctl.p_ready[x]);
+                }
+                if (ok) ok = warp_wait(&ctl.o_full[x], ocnt++ & 1, abort);
+                fence_after();
+            }
+            cnt += 2 * (i1 - i0);
+            ++seg;
+            // ---- the segment's end ----
+            const long long last_unit = it.start + it.n - 1;
+            const int c0 = (int)(it.start / span), c1 = (int)(last_unit / span);
+            const bool poison = *(volatile int *)&ctl.poison != 0;
+            float *base = reinterpret_cast<float *>(a.work + kPrefillPartAt);
+            uint16_t *orow = a.out + (size_t)(it.row0 + (row_live ? tok : 0)) * a.ldo + (size_t)(it.h * a.group + (row_live ? gh : 0)) * D;
+            if (active && ok) {
+                const float inv = c0 == c1 ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
+                float *part = base + ((long long)blockIdx.x * 2 + (it.start >= b0)) * kPrefillPartFloats;
+#pragma unroll 1
+                for (int cc = 0; cc < D; cc += 32) {
+                    uint32_t v[32];
+                    tm_ld32(to + cc, v);
+                    tm_wait_ld();
+                    float o[32];
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] = __uint_as_float(v[k]) * inv;
+                    if (poison && row_live) {
+                        float extra[32];
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) extra[k] = o[k];
+                        add_nonfinite<D, Q8>(a, it, i0, i1, p, cc, extra);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] = extra[k];
+                    }
+                    if (c0 == c1) {
+                        if (row_live) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                *reinterpret_cast<uint4 *>(orow + cc + 8 * k) =
+                                    make_uint4(bf16x2(o[8 * k], o[8 * k + 1]), bf16x2(o[8 * k + 2], o[8 * k + 3]),
+                                               bf16x2(o[8 * k + 4], o[8 * k + 5]), bf16x2(o[8 * k + 6], o[8 * k + 7]));
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            *reinterpret_cast<float4 *>(part + ((cc / 4 + k) * kRows + rx) * 4) =
+                                make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                    }
+                }
+                if (c0 != c1)
+                    *reinterpret_cast<float2 *>(part + kRows * 128 + 2 * rx) = make_float2(M, l);
+            }
+            fence_before();
+            if (c0 != c1 && ok) {
+                // ---- shared with other CTAs: the last to arrive adds the parts in span order ----
+                __threadfence();
+                bar_arrive(&ctl.joined);
+                if (tid == 0 && bar_wait(&ctl.joined, shared & 1, abort)) {
+                    int *count = reinterpret_cast<int *>(a.work + kPrefillCounterAt) + c0;
+                    __threadfence();
+                    const int seen = atomicAdd(count, 1);
+                    ctl.last = seen == c1 - c0;
+                    if (seen == c1 - c0) *count = 0;
+                    __threadfence();
+                    bar_arrive(&ctl.decided);
+                }
+                ok = warp_wait(&ctl.decided, shared++ & 1, abort);
+                if (ok && *(volatile int *)&ctl.last && active && row_live) {
+                    __threadfence();
+                    float m2 = -INFINITY, l2 = 0.0f;
+                    for (int y = c0; y <= c1; ++y)
+                        m2 = fmaxf(m2, __ldcg(base + ((long long)y * 2 + (y == c0)) * kPrefillPartFloats + kRows * 128 + 2 * rx));
+                    for (int y = c0; y <= c1; ++y) {
+                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(
+                            base + ((long long)y * 2 + (y == c0)) * kPrefillPartFloats + kRows * 128 + 2 * rx));
+                        l2 += ml.y * (ml.x == m2 ? 1.0f : ex2(ml.x - m2));
+                    }
+                    const float inv = l2 == 0.0f ? 0.0f : 1.0f / l2;
+#pragma unroll 1
+                    for (int cc = 0; cc < D / 4; cc += 2) {
+                        float4 o0 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), o1 = o0;
+                        for (int y = c0; y <= c1; ++y) {
+                            const float *part = base + ((long long)y * 2 + (y == c0)) * kPrefillPartFloats;
+                            const float m1 = __ldcg(part + kRows * 128 + 2 * rx);
+                            const float f = m1 == m2 ? 1.0f : ex2(m1 - m2);
+                            const float4 v0 = __ldcg(reinterpret_cast<const float4 *>(part + (cc * kRows + rx) * 4));
+                            const float4 v1 = __ldcg(reinterpret_cast<const float4 *>(part + ((cc + 1) * kRows + rx) * 4));
+                            o0.x = fmaf(v0.x, f, o0.x); o0.y = fmaf(v0.y, f, o0.y);
+                            o0.z = fmaf(v0.z, f, o0.z); o0.w = fmaf(v0.w, f, o0.w);
+                            o1.x = fmaf(v1.x, f, o1.x); o1.y = fmaf(v1.y, f, o1.y);
+                            o1.z = fmaf(v1.z, f, o1.z); o1.w = fmaf(v1.w, f, o1.w);
+                        }
+                        *reinterpret_cast<uint4 *>(orow + 4 * cc) =
+                            make_uint4(bf16x2(o0.x * inv, o0.y * inv), bf16x2(o0.z * inv, o0.w * inv),
+                                       bf16x2(o1.x * inv, o1.y * inv), bf16x2(o1.z * inv, o1.w * inv));
+                    }
+                }
+            }
+        }
+    }
+#undef Q8_EACH_SEGMENT
+
+    // ---- drain: every MMA issued is done (o_full was waited for), unless the CTA aborted ----
+    fence_before();
+    __syncthreads();
+    if (*abort && tid == 32 * kMmaWarp) {
+        commit(&ctl.drain);
+        const uint64_t t0 = now_ns();
+        while (!bar_try(&ctl.drain, 0) && now_ns() - t0 < 2000000000ull) {
+        }
+    }
+    __syncthreads();
+    fence_after();
+    if (warp == 0)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemColumns) : "memory");
+    // ---- rows that see nothing: padding, and rows before the first key ----
+    for (int row = blockIdx.x * T + tid; row < a.rows; row += gridDim.x * T) {
+        int lo = 0, hi = a.R;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (a.row_start[mid] <= row) lo = mid; else hi = mid - 1;
+        }
+        Item x;
+        x.n = 0;
+        if (lo < a.R) {
+            x.r = lo;
+            request_of(a, x);
+            x.p_min = x.p_max = x.pos0 + (row - x.row0);
+            span_of(a, x);
+        }
+        if (x.n == 0)
+            for (int e = 0; e < a.heads * D / 8; ++e)
+                *reinterpret_cast<uint4 *>(a.out + (size_t)row * a.ldo + 8 * e) = make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                            cudaSuccess && q == cudaDriverEntryPointSuccess;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ok ? p : nullptr);
+    }();
+    return fn;
+}
+
+// A bf16 cache's keys or values as [pages][heads * page_size][dim], boxes of `run` tokens by 64 values, 128-byte swizzle.
+bool encode_cache(CUtensorMap *map, const AttnArgs &a, const void *p, int dim, int run) {
+    const PFN_cuTensorMapEncodeTiled_v12000 encode = encode_fn();
+    if (!encode) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)a.kv_heads * a.page_size, (cuuint64_t)a.pages};
+    cuuint64_t strides[2] = {(cuuint64_t)dim * 2, (cuuint64_t)a.page_stride * 2};
+    cuuint32_t box[3] = {64, (cuuint32_t)run, 1}, step[3] = {1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(p), dims, strides, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool Q8> cudaError_t launch_one(const AttnArgs &a, int sms, cudaStream_t stream) {
+    using C = Cfg<D, Q8>;
+    cudaError_t e = cudaFuncSetAttribute(prefill_kernel<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    PrefillArgs pa = {a, 16};
+    while (pa.run < kTile && a.page_size % (2 * pa.run) == 0) pa.run *= 2;
+    CUtensorMap kmap = {}, vmap = {};
+    if (!Q8 && (!encode_cache(&kmap, a, a.k, D, pa.run) || !encode_cache(&vmap, a, a.v, D, pa.run)))
+        return cudaErrorNotSupported;
+    return kv_launch(prefill_kernel<D, Q8>, dim3((unsigned)sms, 1, 1), C::kThreads, C::kSmem, stream, pa, kmap, vmap);
+}
+
+}  // namespace
+
+cudaError_t read_attn_fault(unsigned *out, bool clear) {
+    cudaError_t e = cudaMemcpyFromSymbol(out, g_attn_fault, sizeof(unsigned));
+    if (e != cudaSuccess || !clear) return e;
+    const unsigned zero = 0;
+    return cudaMemcpyToSymbol(g_attn_fault, &zero, sizeof(unsigned));
+}
+
+cudaError_t launch_attn_prefill(const AttnArgs &a, int dim, bool q8, cudaStream_t stream) {
+    int sms = 0;
+    cudaError_t e = sm_count_of_device(&sms);
+    if (e != cudaSuccess) return e;
+    if (sms > kAttnMaxCtas) sms = kAttnMaxCtas;
+    if (dim == 128) return q8 ? launch_one<128, true>(a, sms, stream) : launch_one<128, false>(a, sms, stream);
+    return q8 ? launch_one<64, true>(a, sms, stream) : launch_one<64, false>(a, sms, stream);
+}
+
+}  // namespace q8

@@ -252,7 +252,7 @@ q8_status kv_check_cache(const q8_kv_cache *c) {
         return Q8_ERR_SHAPE;
     if ((int64_t)c->heads * c->page_size > 0x7FFFFFFFll / c->dim) return Q8_ERR_SHAPE;
     const int64_t dense = (int64_t)c->heads * c->page_size * c->dim;
-    if (c->page_stride < dense || c->page_stride % c->dim != 0 || c->page_stride > (1ll << 40) / c->pages)
+    if (c->page_stride < dense || c->page_stride % 128 != 0 || c->page_stride > (1ll << 38) / c->pages)
         return Q8_ERR_SHAPE;
     if (!kv_aligned(c->k, 16) || !kv_aligned(c->v, 16) || !kv_aligned(c->k_scale, 16) || !kv_aligned(c->v_scale, 16))
         return Q8_ERR_ALIGN;
