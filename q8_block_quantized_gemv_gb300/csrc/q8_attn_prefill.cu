@@ -45,6 +45,7 @@ constexpr float kSlack = 8.0f;
 constexpr int kMmaWarp = 8, kLoadWarp = 9, kHelpWarp = 10;
 constexpr unsigned kTmemColumns = 512;
 constexpr uint32_t kColO = 256;  // S of tiles A and B at columns 0 and 128, O from here
+constexpr uint32_t kColP = 64;   // the weights (16 bits) over the upper half of their scores
 constexpr unsigned kFaultAttnWait = 8u;
 
 __device__ unsigned int g_attn_fault = 0;
@@ -108,13 +109,14 @@ __device__ __forceinline__ uint64_t now_ns() {
 }
 // Wait for a phase of `bar`; false when the CTA is aborting, or after about two seconds (which starts the abort).
 __device__ __forceinline__ bool bar_wait(uint64_t *bar, unsigned parity, volatile int *abort) {
-    if (bar_try(bar, parity)) return true;
-    const uint64_t t0 = now_ns();
+    uint64_t t0 = 0;  // the timer is slow to read: looked at once in a long while
     for (unsigned n = 1;; ++n) {
         if (bar_try(bar, parity)) return true;
-        if ((n & 63u) == 0) {
+        if ((n & 255u) == 0) {
             if (*abort) return false;
-            if (now_ns() - t0 > 2000000000ull) {
+            const uint64_t t = now_ns();
+            if (!t0) t0 = t;
+            if (t - t0 > 2000000000ull) {
                 *abort = 1;
                 atomicOr(&g_attn_fault, kFaultAttnWait);
                 return false;
@@ -159,6 +161,14 @@ __device__ __forceinline__ void tm_ld32(uint32_t a, uint32_t (&v)[32]) {
           "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
         : "r"(a));
 }
+__device__ __forceinline__ void tm_ld16(uint32_t a, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(a));
+}
 __device__ __forceinline__ void tm_st32(uint32_t a, const uint32_t (&v)[32]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
@@ -183,6 +193,25 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float max32(const uint32_t (&v)[32]) {
+    float a = max3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
+    float b = max3(__uint_as_float(v[3]), __uint_as_float(v[4]), __uint_as_float(v[5]));
+#pragma unroll
+    for (int k = 6; k < 30; k += 4) {
+        a = max3(a, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+        b = max3(b, __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
+    }
+    return max3(a, b, fmaxf(__uint_as_float(v[30]), __uint_as_float(v[31])));
+}
+// The lowest n of 32 bits (none for n <= 0, all for n >= 32).
+__device__ __forceinline__ uint32_t bits_below(int n) {
+    return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u;
 }
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     uint32_t d;
@@ -212,7 +241,8 @@ __device__ __forceinline__ void tma3(uint32_t dst, const CUtensorMap *map, int x
 
 struct PrefillArgs {
     AttnArgs a;
-    int run;  // consecutive tokens of a tile that lie on one page wherever they start: gcd(page_size, 128)
+    int run;             // consecutive tokens of a tile that lie on one page wherever they start: gcd(page_size, 128)
+    unsigned group_mul;  // ceil(2^31 / group): y / group = y * group_mul >> 31 for y < 2^15 (group < 2^15)
 };
 
 // 256 query rows of one cache head: packed row x is token (256 qt + x) / group of the request, head (256 qt + x) %
@@ -221,6 +251,7 @@ struct Item {
     int r, qt, h;
     long long start;  // of its tiles in the list
     int row0, tokens, pos0, rows;
+    int tok0, gh0;  // of packed row 0
     int p_min, p_max, end, lo, us, ul, n;
 
     __device__ __forceinline__ int tile(int i) const { return i < us ? i : ul + (i - us); }
@@ -252,9 +283,17 @@ __device__ __forceinline__ int q_tiles(const AttnArgs &a, int tokens) {
 __device__ __forceinline__ void q_tile_of(const AttnArgs &a, Item &x) {
     const long long first = (long long)x.qt * kRows, all = (long long)x.tokens * a.group;
     x.rows = (int)min((long long)kRows, all - first);
-    x.p_min = x.pos0 + (int)(first / a.group);
+    x.tok0 = (int)(first / a.group);
+    x.gh0 = (int)(first - (long long)x.tok0 * a.group);
+    x.p_min = x.pos0 + x.tok0;
     x.p_max = x.pos0 + (int)((first + x.rows - 1) / a.group);
     span_of(a, x);
+}
+// Packed row x of the item: its token and its head among those that share the cache head.
+__device__ __forceinline__ int2 row_of(const PrefillArgs &pa, const Item &it, int x) {
+    const unsigned y = (unsigned)(it.gh0 + x);
+    const int t = (int)(((unsigned long long)y * pa.group_mul) >> 31);
+    return make_int2(it.tok0 + t, (int)y - t * pa.a.group);
 }
 __device__ __forceinline__ void next_item(const AttnArgs &a, Item &x) {
     x.start += x.n;
@@ -436,7 +475,6 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
     fence_after();
     const uint32_t tmem = ctl.tmem;
     const bool work = b0 < b1;
-
     Item it;
     if (work) {
         it.r = ctl.first_r;
@@ -567,7 +605,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                         fence_after();
 #pragma unroll
                         for (int k = 0; k < kTile / 16; ++k)
-                            mma_ts(tmem + kColO + x * 128, tmem + x * kTile + k * 8,
+                            mma_ts(tmem + kColO + x * 128, tmem + x * kTile + kColP + k * 8,
                                    desc128(ring + (cv % C::kSlots) * C::kOp + k * 2048, kTile * 128), id_o,
                                    i > i0 || k > 0);
                         if (last) commit(&ctl.o_full[x]);
@@ -601,14 +639,12 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
             if (seg && !(ok = warp_wait(&ctl.q_empty, (seg - 1) & 1, abort))) break;
             // Q: row x's 16-byte chunk c at chunk c ^ (x & 7) of its 128 bytes (the 128-byte swizzle)
             constexpr int CH = D / 8;
-            const long long first = (long long)it.qt * kRows;
             if (!Q8) {
                 for (int e = ht; e < kRows * CH; e += HT) {
                     const int x = e / CH, c = e % CH;
                     const bool live = x < it.rows;
-                    const int rho = live ? (int)((first + x) / a.group) : 0;
-                    const int gh = live ? (int)((first + x) - (long long)rho * a.group) : 0;
-                    const uint16_t *src = a.q + (size_t)(it.row0 + rho) * a.ldq + (size_t)(it.h * a.group + gh) * D + 8 * c;
+                    const int2 at = row_of(pa, it, x);
+                    const uint16_t *src = a.q + (size_t)(it.row0 + at.x) * a.ldq + (it.h * a.group + at.y) * D + 8 * c;
                     const uint32_t dst = saddr(smem) + (x / kTile) * C::kOp + (c / 8) * kTile * 128 + (x % kTile) * 128 +
                                          (((c & 7) ^ (x & 7)) << 4);
                     cp16(dst, live ? src : a.q, live);
@@ -622,10 +658,9 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                         const int e = e0 + y * HT + ht, x = e / CH, c = e % CH;
                         v[y] = make_uint4(0u, 0u, 0u, 0u);
                         if (x < it.rows) {
-                            const int rho = (int)((first + x) / a.group);
-                            const int gh = (int)((first + x) - (long long)rho * a.group);
-                            v[y] = *reinterpret_cast<const uint4 *>(a.q + (size_t)(it.row0 + rho) * a.ldq +
-                                                                    (size_t)(it.h * a.group + gh) * D + 8 * c);
+                            const int2 at = row_of(pa, it, x);
+                            v[y] = *reinterpret_cast<const uint4 *>(a.q + (size_t)(it.row0 + at.x) * a.ldq +
+                                                                    (it.h * a.group + at.y) * D + 8 * c);
                         }
                     }
 #pragma unroll
@@ -782,9 +817,8 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
             if (!ok) break;
             const bool active = x == 0 || it.rows > kTile;
             const bool row_live = rx < it.rows;
-            const long long rho = (long long)it.qt * kRows + rx;
-            const int tok = (int)(rho / a.group), gh = (int)(rho - (long long)tok * a.group);
-            const int p = it.pos0 + tok;
+            const int2 me = row_of(pa, it, rx);
+            const int tok = me.x, gh = me.y, p = it.pos0 + tok;
             float M = -INFINITY, l = 0.0f;
             if (active) {
                 float sc = sc0;
@@ -807,24 +841,34 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                     // columns [c_lo, c_hi] and [0, c_sink) are visible
                     const int c_hi = min(p, it.end - 1) - j0;
                     const int c_lo = a.window ? max(p - a.window + 1 - j0, 0) : 0, c_sink = a.window ? a.sinks - j0 : 0;
-                    auto hide = [&](uint32_t (&v)[32], int c0) {
+                    if (part) {  // hidden scores become -inf in place
+#pragma unroll 1
+                        for (int c0 = 0; c0 < kTile; c0 += 32) {
+                            uint32_t v[32];
+                            tm_ld32(ts + c0, v);
+                            // bits: columns c0 .. of this row that it sees
+                            const uint32_t up = bits_below(c_hi + 1 - c0);
+                            uint32_t see = up & (~bits_below(c_lo - c0) | bits_below(c_sink - c0));
+                            see &= ((groups >> (c0 / 16) & 1u) ? 0xFFFFu : 0u) |
+                                   ((groups >> (c0 / 16 + 1) & 1u) ? 0xFFFF0000u : 0u);
+                            tm_wait_ld();
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            const int c = c0 + k;
-                            const bool see = c <= c_hi && (c >= c_lo || c < c_sink) && (groups >> (c >> 4) & 1u);
-                            if (!see) v[k] = 0xFF800000u;
+                            for (int k = 0; k < 32; ++k) v[k] = (see >> k & 1u) ? v[k] : 0xFF800000u;
+                            tm_st32(ts + c0, v);
                         }
-                    };
-                    float mx = -INFINITY;
-#pragma unroll
-                    for (int c0 = 0; c0 < kTile; c0 += 32) {
-                        uint32_t v[32];
-                        tm_ld32(ts + c0, v);
-                        tm_wait_ld();
-                        if (part) hide(v, c0);
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) mx = fmaxf(mx, __uint_as_float(v[k]));
+                        tm_wait_st();
                     }
+                    // Two looks at the row: its maximum, then the weights.  The upper half of the scores stays in
+                    // registers between them; the weights go over it, so that the lower half can be read again.
+                    uint32_t v[2][32], w2[2][32];
+                    tm_ld32(ts, w2[0]);
+                    tm_ld32(ts + 32, w2[1]);
+                    tm_wait_ld();
+                    tm_ld32(ts + 64, v[0]);
+                    tm_ld32(ts + 96, v[1]);
+                    float mx = max3(max32(w2[0]), max32(w2[1]), -INFINITY);
+                    tm_wait_ld();
+                    mx = max3(mx, max32(v[0]), max32(v[1]));
                     mx = mx == -INFINITY ? mx : fmaf(mx, sc, shift);
                     const bool above = mx > M + kSlack || (M == -INFINITY && mx > M);
                     if (__any_sync(0xffffffffu, above)) {
@@ -834,33 +878,48 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                         l *= f;
                         if (i > i0) {
 #pragma unroll 1
-                            for (int c0 = 0; c0 < D; c0 += 32) {
-                                uint32_t v[32];
-                                tm_ld32(to + c0, v);
+                            for (int c0 = 0; c0 < D; c0 += 16) {
+                                uint32_t w[16];
+                                tm_ld16(to + c0, w);
                                 tm_wait_ld();
 #pragma unroll
-                                for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * f);
-                                tm_st32(to + c0, v);
+                                for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) * f);
+                                tm_st16(to + c0, w);
                             }
                         }
                     }
                     const float off = shift - (M == -INFINITY ? 0.0f : M);
-                    float sum = 0.0f;
-#pragma unroll
-                    for (int c0 = 0; c0 < kTile; c0 += 32) {
-                        uint32_t v[32], w[16];
-                        tm_ld32(ts + c0, v);
-                        tm_wait_ld();
-                        if (part) hide(v, c0);
+                    unsigned long long sc2, off2, sum2 = 0ull;
+                    asm("mov.b64 %0, {%1, %1};" : "=l"(sc2) : "f"(sc));
+                    asm("mov.b64 %0, {%1, %1};" : "=l"(off2) : "f"(off));
+                    auto weights = [&](const uint32_t (&r)[32], uint32_t col) {
+                        uint32_t w[16];
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
-                            const float p0 = ex2(fmaf(__uint_as_float(v[2 * k]), sc, off));
-                            const float p1 = ex2(fmaf(__uint_as_float(v[2 * k + 1]), sc, off));
-                            sum += p0 + p1;
+                            unsigned long long e;
+                            float p0, p1;
+                            asm("{\n .reg .b64 s;\n mov.b64 s, {%1, %2};\n fma.rn.f32x2 %0, s, %3, %4;\n}"
+                                : "=l"(e) : "r"(r[2 * k]), "r"(r[2 * k + 1]), "l"(sc2), "l"(off2));
+                            asm("mov.b64 {%0, %1}, %2;" : "=f"(p0), "=f"(p1) : "l"(e));
+                            p0 = ex2(p0);
+                            p1 = ex2(p1);
+                            asm("{\n .reg .b64 s;\n mov.b64 s, {%1, %2};\n add.rn.f32x2 %0, %0, s;\n}"
+                                : "+l"(sum2) : "f"(p0), "f"(p1));
                             w[k] = Q8 ? f16x2(p0, p1) : bf16x2(p0, p1);
                         }
-                        tm_st16(ts + c0 / 2, w);
-                    }
+                        tm_st16(ts + kColP + col, w);
+                    };
+                    weights(v[0], 32);
+                    tm_ld32(ts, v[0]);
+                    weights(v[1], 48);
+                    tm_wait_ld();
+                    tm_ld32(ts + 32, v[1]);
+                    weights(v[0], 0);
+                    tm_wait_ld();
+                    weights(v[1], 16);
+                    float sum, sum_hi;
+                    asm("mov.b64 {%0, %1}, %2;" : "=f"(sum), "=f"(sum_hi) : "l"(sum2));
+                    sum += sum_hi;
                     l += Q8 ? sum * ex2(-shift) : sum;
                     tm_wait_st();
                     fence_before();
@@ -876,7 +935,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
             const int c0 = (int)(it.start / span), c1 = (int)(last_unit / span);
             const bool poison = *(volatile int *)&ctl.poison != 0;
             float *base = reinterpret_cast<float *>(a.work + kPrefillPartAt);
-            uint16_t *orow = a.out + (size_t)(it.row0 + (row_live ? tok : 0)) * a.ldo + (size_t)(it.h * a.group + (row_live ? gh : 0)) * D;
+            uint16_t *orow = a.out + (size_t)(it.row0 + (row_live ? tok : 0)) * a.ldo + (it.h * a.group + (row_live ? gh : 0)) * D;
             if (active && ok) {
                 const float inv = c0 == c1 ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
                 float *part = base + ((long long)blockIdx.x * 2 + (it.start >= b0)) * kPrefillPartFloats;
@@ -1025,7 +1084,7 @@ template <int D, bool Q8> cudaError_t launch_one(const AttnArgs &a, int sms, cud
     using C = Cfg<D, Q8>;
     cudaError_t e = cudaFuncSetAttribute(prefill_kernel<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    PrefillArgs pa = {a, 16};
+    PrefillArgs pa = {a, 16, (unsigned)(((1ll << 31) + a.group - 1) / a.group)};
     while (pa.run < kTile && a.page_size % (2 * pa.run) == 0) pa.run *= 2;
     CUtensorMap kmap = {}, vmap = {};
     if (!Q8 && (!encode_cache(&kmap, a, a.k, D, pa.run) || !encode_cache(&vmap, a, a.v, D, pa.run)))
