@@ -420,7 +420,7 @@ q8_status q8_attn_decode(const void *q, int ldq, const q8_kv_cache *cache, const
  * by the rule of q8_attn_decode (window, sinks, missing pages).  The chunk's own keys are in the cache already.
  *   q, out  device, bf16 [rows][ldq], [rows][ldo]      row_start  device, int32 [R + 1], ascending from 0, at most rows
  * Rows past row_start[R] are padding and get zeros, as do rows that see nothing.  Other arguments, errors: as
- * q8_attn_decode; rows >= 1. */
+ * q8_attn_decode; 1 <= rows <= 2^24, q_heads at most 128 times cache->heads. */
 q8_status q8_attn_prefill(const void *q, int ldq, const q8_kv_cache *cache, const int *block_table, int table_width,
                           int table_pitch, const int *lens, const int *row_start, void *out, int ldo, int rows, int R,
                           int q_heads, float scale, int window, int sinks, void *workspace, q8_stream_t stream);

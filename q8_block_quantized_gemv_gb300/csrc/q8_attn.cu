@@ -77,6 +77,7 @@ extern "C" q8_status q8_attn_prefill(const void *q, int ldq, const q8_kv_cache *
     q8_status st = q8::attn_args(&a, q, ldq, cache, block_table, table_width, table_pitch, lens, row_start, out, ldo,
                                  rows, R, q_heads, scale, window, sinks, workspace);
     if (st != Q8_OK) return st;
+    if (a.group > 128) return Q8_ERR_SHAPE;  // a query tile holds whole tokens
     const cudaError_t e = q8::launch_attn_prefill(a, cache->dim, q8::kv_is_q8(cache), (cudaStream_t)stream);
     return e == cudaSuccess ? Q8_OK : q8::kv_cuda_fail(e);
 }

@@ -1,9 +1,9 @@
 // q8_attn_prefill: causal attention of a chunk of new tokens over the paged cache, on the 5th-generation tensor cores.
 //
 // 4 dim flops a visible (query row, key) pair against 4 dim bytes a key: from some hundred rows the tensor cores bound
-// it, so the kernel is built around keeping them fed.  A work item is 256 query rows of one cache head -- the tokens'
-// rows with the heads that share the cache head packed beside each other, so shared heads fill tiles as tokens do --
-// held as two 128-row tiles that take turns: while the softmax warps work on one tile's scores, the tensor cores
+// it, so the kernel is built around keeping them fed.  A work item is two 128-row query tiles of one cache head -- the
+// tokens' rows with the heads that share the cache head packed beside each other, whole tokens to a tile, so shared
+// heads fill tiles as tokens do -- that take turns: while the softmax warps work on one tile's scores, the tensor cores
 // compute the other's.  For each 128-key tile:
 //     S = Q K^T (tcgen05.mma, both operands in shared memory, fp32 S in tensor memory)
 //     P = 2^(S scale log2(e) - m), rounded to 16 bits, written over S in tensor memory
@@ -40,6 +40,8 @@ namespace {
 
 constexpr int kTile = 128;   // keys of a tile, and rows of a query tile
 constexpr int kRows = 256;   // query rows of an item
+constexpr int kItemCost = 2; // what an item costs beside its tiles, in tiles: loading Q, the pipe's fill, the epilogue
+constexpr int kMinSpan = 4 + kItemCost;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;
 constexpr int kMmaWarp = 8, kLoadWarp = 9, kHelpWarp = 10;
@@ -70,8 +72,8 @@ template <int D, bool Q8> struct Control {
     using C = Cfg<D, Q8>;
     uint64_t full[10], ready[10], empty[10];   // operand ring: landed, usable, free
     uint64_t raw_full[4], raw_empty[4];        // raw ring (Q8_0)
-    uint64_t q_full, q_empty, drain;
-    uint64_t s_full[2], p_ready[2], o_full[2], joined, decided;
+    uint64_t q_raw, q_full, q_empty, drain;  // q_raw: landed, before the conversion (Q8_0)
+    uint64_t s_full[2], p_ready[2][2], o_full[2], joined, decided;  // p_ready: the tile's upper and lower 64 keys
     // Of key tile number n of this CTA at n & 7 (no role is more than five tiles behind the requests):
     unsigned pages[8];  // bits: which 16-token groups lie on a page
     float unit[2][8];   // Q8_0: log2 of the keys' and the values' unit
@@ -223,9 +225,6 @@ __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
     return d;
 }
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool ok) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
-}
 __device__ __forceinline__ void bulk(uint32_t dst, const void *src, unsigned bytes, uint64_t *bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                  "l"(src), "r"(bytes), "r"(saddr(bar))
@@ -241,18 +240,20 @@ __device__ __forceinline__ void tma3(uint32_t dst, const CUtensorMap *map, int x
 
 struct PrefillArgs {
     AttnArgs a;
-    int run;             // consecutive tokens of a tile that lie on one page wherever they start: gcd(page_size, 128)
-    unsigned group_mul;  // ceil(2^31 / group): y / group = y * group_mul >> 31 for y < 2^15 (group < 2^15)
+    int run;         // consecutive tokens of a tile that lie on one page wherever they start: gcd(page_size, 128)
+    int tile_tokens; // tokens of a query tile: 128 / group
 };
 
-// 256 query rows of one cache head: packed row x is token (256 qt + x) / group of the request, head (256 qt + x) %
-// group of those that share the cache head.  Its key tiles are [0, us) for the sinks and [ul, ul + n - us).
+// Two query tiles of one cache head: tokens tok0 .. tok0 + tokens - 1 of request r, the first tile_tokens of them in
+// tile A, the rest in B; row y of a tile is token y / group, head y % group of those that share the cache head.  The
+// item's key tiles are [0, us) for the sinks and [ul, ul + n - us); tile A visits the first n_a of them.  In the list
+// an item takes kItemCost + n places, the tiles last.
 struct Item {
     int r, qt, h;
-    long long start;  // of its tiles in the list
-    int row0, tokens, pos0, rows;
-    int tok0, gh0;  // of packed row 0
-    int p_min, p_max, end, lo, us, ul, n;
+    long long start;  // of its tiles in the list, the fixed cost behind it
+    int row0, all, pos0;  // the request's first row, its rows, the position of its first row
+    int tok0, tokens;
+    int p_min, p_max, end, lo, us, ul, n, n_a;
 
     __device__ __forceinline__ int tile(int i) const { return i < us ? i : ul + (i - us); }
     // Whether some row of the item does not see all of tile u, pages aside.
@@ -274,40 +275,36 @@ __device__ __forceinline__ void span_of(const AttnArgs &a, Item &x) {
 __device__ __forceinline__ void request_of(const AttnArgs &a, Item &x) {
     const int t0 = min(max(a.row_start[x.r], 0), a.rows), t1 = min(max(a.row_start[x.r + 1], t0), a.rows);
     x.row0 = t0;
-    x.tokens = t1 - t0;
-    x.pos0 = max(a.lens[x.r], 0) - x.tokens;
+    x.all = t1 - t0;
+    x.pos0 = max(a.lens[x.r], 0) - x.all;
 }
-__device__ __forceinline__ int q_tiles(const AttnArgs &a, int tokens) {
-    return (int)(((long long)tokens * a.group + kRows - 1) / kRows);
+__device__ __forceinline__ int q_tiles(const PrefillArgs &pa, int tokens) {
+    return (tokens + 2 * pa.tile_tokens - 1) / (2 * pa.tile_tokens);
 }
-__device__ __forceinline__ void q_tile_of(const AttnArgs &a, Item &x) {
-    const long long first = (long long)x.qt * kRows, all = (long long)x.tokens * a.group;
-    x.rows = (int)min((long long)kRows, all - first);
-    x.tok0 = (int)(first / a.group);
-    x.gh0 = (int)(first - (long long)x.tok0 * a.group);
+__device__ __forceinline__ void q_tile_of(const PrefillArgs &pa, Item &x) {
+    x.tok0 = x.qt * 2 * pa.tile_tokens;
+    x.tokens = min(2 * pa.tile_tokens, x.all - x.tok0);
     x.p_min = x.pos0 + x.tok0;
-    x.p_max = x.pos0 + (int)((first + x.rows - 1) / a.group);
-    span_of(a, x);
+    x.p_max = x.p_min + x.tokens - 1;
+    span_of(pa.a, x);
+    // tiles up to the one of tile A's last key
+    const int last = (x.p_min + min(pa.tile_tokens, x.tokens) - 1) / kTile;
+    x.n_a = min(x.n, max(1, last < x.ul ? min(last + 1, x.us) : x.us + last - x.ul + 1));
 }
-// Packed row x of the item: its token and its head among those that share the cache head.
-__device__ __forceinline__ int2 row_of(const PrefillArgs &pa, const Item &it, int x) {
-    const unsigned y = (unsigned)(it.gh0 + x);
-    const int t = (int)(((unsigned long long)y * pa.group_mul) >> 31);
-    return make_int2(it.tok0 + t, (int)y - t * pa.a.group);
-}
-__device__ __forceinline__ void next_item(const AttnArgs &a, Item &x) {
-    x.start += x.n;
-    if (++x.h < a.kv_heads) return;
+__device__ __forceinline__ long long cost_of(const Item &x) { return x.n ? x.n + kItemCost : 0; }
+__device__ __forceinline__ void next_item(const PrefillArgs &pa, Item &x) {
+    x.start += x.n + kItemCost;
+    if (++x.h < pa.a.kv_heads) return;
     x.h = 0;
     do {
-        if (++x.qt >= q_tiles(a, x.tokens)) {
+        if (++x.qt >= q_tiles(pa, x.all)) {
             do {
-                if (++x.r >= a.R) return;  // never reached: the walk ends within the list
-                request_of(a, x);
-            } while (x.tokens == 0);
+                if (++x.r >= pa.a.R) return;  // never reached: the walk ends within the list
+                request_of(pa.a, x);
+            } while (x.all == 0);
             x.qt = 0;
         }
-        q_tile_of(a, x);
+        q_tile_of(pa, x);
     } while (x.n == 0);
 }
 
@@ -349,7 +346,8 @@ __device__ __noinline__ void add_nonfinite(const AttnArgs &a, const Item it, int
 
 template <int D, bool Q8>
 __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
-    prefill_kernel(const __grid_constant__ PrefillArgs pa, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+    prefill_kernel(const __grid_constant__ PrefillArgs pa, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                   const __grid_constant__ CUtensorMap qmap) {
     using C = Cfg<D, Q8>;
     const AttnArgs &a = pa.a;
     extern __shared__ __align__(1024) unsigned char smem[];
@@ -367,14 +365,16 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
             bar_init(&ctl.raw_full[i], 1);
             bar_init(&ctl.raw_empty[i], C::kHelpers);
         }
-        bar_init(&ctl.q_full, C::kHelpers);
+        bar_init(&ctl.q_raw, 1);
+        bar_init(&ctl.q_full, Q8 ? C::kHelpers : 1);
         bar_init(&ctl.q_empty, 1);
         bar_init(&ctl.drain, 1);
         bar_init(&ctl.joined, 256);
         bar_init(&ctl.decided, 1);
         for (int i = 0; i < 2; ++i) {
             bar_init(&ctl.s_full[i], 1);
-            bar_init(&ctl.p_ready[i], 128);
+            bar_init(&ctl.p_ready[i][0], 4);
+            bar_init(&ctl.p_ready[i][1], 4);
             bar_init(&ctl.o_full[i], 1);
         }
         ctl.abort = 0;
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
         int mine = 0;
         for (x.r = ra; x.r < rb; ++x.r) {
             request_of(a, x);
-            mine += q_tiles(a, x.tokens);
+            mine += q_tiles(pa, x.all);
         }
         int upto = mine;
 #pragma unroll
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
         for (x.r = ra; x.r < rb; ++x.r) {
             request_of(a, x);
             qsum[x.r] = before;
-            before += q_tiles(a, x.tokens);
+            before += q_tiles(pa, x.all);
         }
         if (tid == 0) qsum[a.R] = tiles;
         __syncthreads();
@@ -434,11 +434,11 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
             x.r = lo;
             x.qt = q - qsum[lo];
             request_of(a, x);
-            q_tile_of(a, x);
+            q_tile_of(pa, x);
         };
         for (int q = qa; q < qb; ++q) {
             seek(q);
-            keys += x.n;
+            keys += cost_of(x);
         }
         long long sum = keys;
 #pragma unroll
@@ -455,14 +455,14 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
             total += ctl.scan[w];
         }
         total *= a.kv_heads;
-        span = max((total + gridDim.x - 1) / gridDim.x, 4ll);
+        span = max((total + gridDim.x - 1) / gridDim.x, (long long)kMinSpan);
         b0 = span * blockIdx.x;
         b1 = min(total, b0 + span);
         if (b0 < b1 && ahead * a.kv_heads <= b0 && b0 < (ahead + keys) * a.kv_heads) {
             for (int q = qa;; ++q) {  // exactly one thread holds unit b0
                 seek(q);
-                if (b0 < (ahead + x.n) * a.kv_heads) break;
-                ahead += x.n;
+                if (b0 < (ahead + cost_of(x)) * a.kv_heads) break;
+                ahead += cost_of(x);
             }
             ctl.first_r = x.r;
             ctl.first_qt = x.qt;
@@ -480,23 +480,46 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
         it.r = ctl.first_r;
         it.qt = ctl.first_qt;
         request_of(a, it);
-        q_tile_of(a, it);
-        it.h = (int)((b0 - ctl.first_start) / it.n);
-        it.start = ctl.first_start + (long long)it.h * it.n;
+        q_tile_of(pa, it);
+        it.h = (int)((b0 - ctl.first_start) / cost_of(it));
+        it.start = ctl.first_start + it.h * cost_of(it) + kItemCost;
     }
-    // An item's tiles [i0, i1) fall into this span.
-#define Q8_EACH_SEGMENT                                                                   \
-    for (int i0 = work ? (int)(b0 - it.start) : 0, i1 = 0, more = work;                   \
-         more && (i1 = (int)min((long long)it.n, b1 - it.start), true);                   \
-         more = it.start + it.n < b1, more ? (next_item(a, it), i0 = 0) : 0)
+    // An item's tiles [i0, i1) that fall into this span; none of the last item's when only its fixed cost does.
+    int i0 = 0, i1 = 0;
+    auto segment = [&]() {
+        i0 = (int)max(0ll, b0 - it.start);
+        i1 = (int)min((long long)it.n, b1 - it.start);
+    };
+    bool more = work;
+    if (more) segment();
+    auto advance = [&]() {
+        more = it.start + it.n < b1;
+        if (more) {
+            next_item(pa, it);
+            segment();
+            more = i1 > 0;
+        }
+    };
 
     if (warp == kLoadWarp) {
         // ---- keys and values: lane i requests run i of each tile ----
         const int runs = kTile / pa.run, per = pa.run / 16;
-        unsigned cnt = 0;
+        unsigned cnt = 0, seg = 0;
         bool ok = true;
-        Q8_EACH_SEGMENT {
+        for (; more; advance()) {
             if (!ok) break;
+            if (seg && !(ok = warp_wait(&ctl.q_empty, (seg - 1) & 1, abort))) break;
+            ++seg;
+            if (lane == 0) {  // Q: boxes of 64 values, the cache head's heads, a tile's tokens
+                uint64_t *bar = Q8 ? &ctl.q_raw : &ctl.q_full;
+                const int nx = it.tokens > pa.tile_tokens ? 2 : 1;
+                bar_arrive_tx(bar, (unsigned)(nx * C::kSub * 128 * a.group * pa.tile_tokens));
+                for (int x = 0; x < nx; ++x)
+                    for (int sub = 0; sub < C::kSub; ++sub)
+                        tma3(saddr(smem) + x * C::kOp + sub * kTile * 128, &qmap, 64 * sub, it.h * a.group,
+                             it.row0 + it.tok0 + x * pa.tile_tokens, bar);
+            }
+            __syncwarp();
             const int *row = a.table + (size_t)it.r * a.pitch;
             int page = -1, off = 0;
             auto look = [&](int i) {
@@ -559,6 +582,9 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                        now_ns() - t0 < 2000000000ull) {
                 }
             }
+            const uint64_t t0 = now_ns();
+            while (seg && !bar_try(Q8 ? &ctl.q_raw : &ctl.q_full, (seg - 1) & 1) && now_ns() - t0 < 2000000000ull) {
+            }
         }
         __syncwarp();
     } else if (warp == kMmaWarp) {
@@ -581,9 +607,9 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                 }
                 commit(&ctl.s_full[x]);
             };
-            Q8_EACH_SEGMENT {
+            for (; more; advance()) {
                 if (!ok) break;
-                const int nx = it.rows > kTile ? 2 : 1;
+                const int lim[2] = {min(i1, it.n_a), it.tokens > pa.tile_tokens ? i1 : 0};  // each tile's last, plus 1
                 if (!(ok = bar_wait(&ctl.q_full, seg & 1, abort))) break;
                 auto usable = [&](unsigned c, bool value) {
                     const unsigned s = c % C::kSlots, par = (c / C::kSlots) & 1;
@@ -592,35 +618,42 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                 const unsigned c0 = cnt;
                 if (!(ok = usable(c0, false))) break;
                 fence_after();
-                for (int x = 0; x < nx; ++x) scores(x, c0 % C::kSlots);
+                for (int x = 0; x < 2; ++x)
+                    if (i0 < lim[x]) scores(x, c0 % C::kSlots);
                 commit(&ctl.empty[c0 % C::kSlots]);
                 if (i1 - i0 == 1) commit(&ctl.q_empty);
                 for (int i = i0; i < i1 && ok; ++i) {
                     const unsigned cv = c0 + 2 * (i - i0) + 1, ck = cv + 1;
-                    const bool last = i + 1 == i1;
+                    const bool next = i + 1 < i1;
                     if (!(ok = usable(cv, true))) break;
-                    for (int x = 0; x < nx; ++x) {
-                        if (!(ok = bar_wait(&ctl.p_ready[x], pcnt[x] & 1, abort))) break;
-                        ++pcnt[x];
-                        fence_after();
+                    for (int x = 0; x < 2; ++x) {
+                        if (i < lim[x]) {
 #pragma unroll
-                        for (int k = 0; k < kTile / 16; ++k)
-                            mma_ts(tmem + kColO + x * 128, tmem + x * kTile + kColP + k * 8,
-                                   desc128(ring + (cv % C::kSlots) * C::kOp + k * 2048, kTile * 128), id_o,
-                                   i > i0 || k > 0);
-                        if (last) commit(&ctl.o_full[x]);
-                        if (x == nx - 1) commit(&ctl.empty[cv % C::kSlots]);
-                        if (!last) {
-                            if (x == 0) {
-                                if (!(ok = usable(ck, false))) break;
+                            for (int half = 0; half < 2; ++half) {  // the upper keys' weights come first
+                                if (!(ok = bar_wait(&ctl.p_ready[x][half], pcnt[x] & 1, abort))) break;
                                 fence_after();
+#pragma unroll
+                                for (int k = 0; k < kTile / 32; ++k) {
+                                    const int ks = (half ? 0 : kTile / 32) + k;
+                                    mma_ts(tmem + kColO + x * 128, tmem + x * kTile + kColP + ks * 8,
+                                           desc128(ring + (cv % C::kSlots) * C::kOp + ks * 2048, kTile * 128), id_o,
+                                           i > i0 || half > 0 || k > 0);
+                                }
                             }
-                            scores(x, ck % C::kSlots);
-                            if (x == nx - 1) {
-                                commit(&ctl.empty[ck % C::kSlots]);
-                                if (i + 2 == i1) commit(&ctl.q_empty);
-                            }
+                            if (!ok) break;
+                            ++pcnt[x];
+                            if (i + 1 == lim[x]) commit(&ctl.o_full[x]);
                         }
+                        if (x == (i < lim[1] ? 1 : 0)) commit(&ctl.empty[cv % C::kSlots]);  // after its last use
+                        if (next && x == 0) {
+                            if (!(ok = usable(ck, false))) break;
+                            fence_after();
+                        }
+                        if (i + 1 < lim[x]) scores(x, ck % C::kSlots);
+                    }
+                    if (next && ok) {
+                        commit(&ctl.empty[ck % C::kSlots]);
+                        if (i + 2 == i1) commit(&ctl.q_empty);
                     }
                 }
                 cnt = c0 + 2 * (i1 - i0);
@@ -634,60 +667,36 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
         constexpr int HT = 32 * C::kHelpers;
         unsigned cnt = 0, seg = 0;
         bool ok = true;
-        Q8_EACH_SEGMENT {
+        for (; more; advance()) {
             if (!ok) break;
-            if (seg && !(ok = warp_wait(&ctl.q_empty, (seg - 1) & 1, abort))) break;
-            // Q: row x's 16-byte chunk c at chunk c ^ (x & 7) of its 128 bytes (the 128-byte swizzle)
-            constexpr int CH = D / 8;
-            if (!Q8) {
+            constexpr int CH = D / 8;  // 16-byte chunks of an operand row
+            if (Q8) {  // Q to fp16, in place
+                if (!(ok = warp_wait(&ctl.q_raw, seg & 1, abort))) break;
+#pragma unroll 4
                 for (int e = ht; e < kRows * CH; e += HT) {
                     const int x = e / CH, c = e % CH;
-                    const bool live = x < it.rows;
-                    const int2 at = row_of(pa, it, x);
-                    const uint16_t *src = a.q + (size_t)(it.row0 + at.x) * a.ldq + (it.h * a.group + at.y) * D + 8 * c;
-                    const uint32_t dst = saddr(smem) + (x / kTile) * C::kOp + (c / 8) * kTile * 128 + (x % kTile) * 128 +
-                                         (((c & 7) ^ (x & 7)) << 4);
-                    cp16(dst, live ? src : a.q, live);
+                    uint4 *at = reinterpret_cast<uint4 *>(smem + (x / kTile) * C::kOp + (c / 8) * kTile * 128 +
+                                                          (x % kTile) * 128 + (((c & 7) ^ (x & 7)) << 4));
+                    const uint4 v = *at;
+                    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t mx = 0u;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) mx = max(mx, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
+#pragma unroll
+                    for (int o = 1; o < CH; o <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                    // times a power of two that takes the row's largest magnitude to [2^9, 2^10)
+                    const int ex = min(max((int)(mx >> 7), 1), 254), up = min(127 + 9 - ex, 126);
+                    const float f = __uint_as_float((uint32_t)(up + 127) << 23);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        w[k] = f16x2(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xFFFF0000u) * f);
+                    *at = make_uint4(w[0], w[1], w[2], w[3]);
+                    if (c == 0) ctl.qscale[seg & 1][Q8 ? x : 0] = __uint_as_float((uint32_t)(127 - up) << 23);
                 }
-                asm volatile("cp.async.wait_all;" ::: "memory");
-            } else {
-                for (int e0 = 0; e0 < kRows * CH; e0 += HT * 4) {
-                    uint4 v[4];
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        const int e = e0 + y * HT + ht, x = e / CH, c = e % CH;
-                        v[y] = make_uint4(0u, 0u, 0u, 0u);
-                        if (x < it.rows) {
-                            const int2 at = row_of(pa, it, x);
-                            v[y] = *reinterpret_cast<const uint4 *>(a.q + (size_t)(it.row0 + at.x) * a.ldq +
-                                                                    (it.h * a.group + at.y) * D + 8 * c);
-                        }
-                    }
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        const int e = e0 + y * HT + ht, x = e / CH, c = e % CH;
-                        uint32_t w[4] = {v[y].x, v[y].y, v[y].z, v[y].w};
-                        uint32_t mx = 0u;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) mx = max(mx, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
-#pragma unroll
-                        for (int o = 1; o < CH; o <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                        // times a power of two that takes the row's largest magnitude to [2^9, 2^10)
-                        const int ex = min(max((int)(mx >> 7), 1), 254), up = min(127 + 9 - ex, 126);
-                        const float f = __uint_as_float((uint32_t)(up + 127) << 23);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            w[k] = f16x2(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xFFFF0000u) * f);
-                        *reinterpret_cast<uint4 *>(smem + (x / kTile) * C::kOp + (c / 8) * kTile * 128 +
-                                                   (x % kTile) * 128 + (((c & 7) ^ (x & 7)) << 4)) =
-                            make_uint4(w[0], w[1], w[2], w[3]);
-                        if (c == 0) ctl.qscale[seg & 1][Q8 ? x : 0] = __uint_as_float((uint32_t)(127 - up) << 23);
-                    }
-                }
+                fence_async();
+                __syncwarp();
+                if (lane == 0) bar_arrive(&ctl.q_full);
             }
-            fence_async();
-            __syncwarp();
-            if (lane == 0) bar_arrive(&ctl.q_full);
             int v_ex = 0;
             for (int i = i0; i < i1 && ok; ++i) {
                 const int u = it.tile(i), j0 = u * kTile;
@@ -806,23 +815,25 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
     } else {
         // ---- softmax: thread = row of tile x ----
         const int x = warp >> 2, quarter = warp & 3;
-        const int rx = x * kTile + quarter * 32 + lane;  // packed row within the item
+        const int y = quarter * 32 + lane, rx = x * kTile + y;
+        const int tok = x * pa.tile_tokens + y / a.group, gh = y % a.group;  // of this row: the item's token, the head
+        const bool whole_row = y < pa.tile_tokens * a.group;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         const uint32_t ts = tmem + lanes + x * kTile, to = tmem + lanes + kColO + x * 128;
         constexpr float kLeast = 1.17549435e-38f;  // a factor of 0 would make NaN of a hidden score's -inf
         const float sc0 = fmaxf(fabsf(a.scale) * kLog2e, kLeast);
         unsigned cnt = 0, scnt = 0, ocnt = 0, shared = 0, seg = 0;
         bool ok = true;
-        Q8_EACH_SEGMENT {
+        for (; more; advance()) {
             if (!ok) break;
-            const bool active = x == 0 || it.rows > kTile;
-            const bool row_live = rx < it.rows;
-            const int2 me = row_of(pa, it, rx);
-            const int tok = me.x, gh = me.y, p = it.pos0 + tok;
+            const int lim = x == 0 ? min(i1, it.n_a) : it.tokens > pa.tile_tokens ? i1 : 0;
+            const bool active = i0 < lim;
+            const bool row_live = whole_row && tok < it.tokens;
+            const int p = it.p_min + tok;
             float M = -INFINITY, l = 0.0f;
             if (active) {
                 float sc = sc0;
-                for (int i = i0; i < i1 && ok; ++i) {
+                for (int i = i0; i < lim && ok; ++i) {
                     const unsigned ck = cnt + 2 * (i - i0), at = (ck >> 1) & 7;
                     if (!(ok = warp_wait(&ctl.s_full[x], scnt & 1, abort))) break;
                     ++scnt;
@@ -912,6 +923,10 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                     weights(v[0], 32);
                     tm_ld32(ts, v[0]);
                     weights(v[1], 48);
+                    tm_wait_st();
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(&ctl.p_ready[x][0]);
                     tm_wait_ld();
                     tm_ld32(ts + 32, v[1]);
                     weights(v[0], 0);
@@ -923,7 +938,8 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                     l += Q8 ? sum * ex2(-shift) : sum;
                     tm_wait_st();
                     fence_before();
-                    bar_arrive(&ctl.p_ready[x]);
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(&ctl.p_ready[x][1]);
                 }
                 if (ok) ok = warp_wait(&ctl.o_full[x], ocnt++ & 1, abort);
                 fence_after();
@@ -935,10 +951,10 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
             const int c0 = (int)(it.start / span), c1 = (int)(last_unit / span);
             const bool poison = *(volatile int *)&ctl.poison != 0;
             float *base = reinterpret_cast<float *>(a.work + kPrefillPartAt);
-            uint16_t *orow = a.out + (size_t)(it.row0 + (row_live ? tok : 0)) * a.ldo + (it.h * a.group + (row_live ? gh : 0)) * D;
+            uint16_t *orow = a.out + (size_t)(it.row0 + it.tok0 + (row_live ? tok : 0)) * a.ldo + (it.h * a.group + gh) * D;
+            float *part = base + ((long long)blockIdx.x * 2 + (it.start >= b0)) * kPrefillPartFloats;
             if (active && ok) {
                 const float inv = c0 == c1 ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
-                float *part = base + ((long long)blockIdx.x * 2 + (it.start >= b0)) * kPrefillPartFloats;
 #pragma unroll 1
                 for (int cc = 0; cc < D; cc += 32) {
                     uint32_t v[32];
@@ -970,9 +986,8 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                                 make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
                     }
                 }
-                if (c0 != c1)
-                    *reinterpret_cast<float2 *>(part + kRows * 128 + 2 * rx) = make_float2(M, l);
             }
+            if (c0 != c1) *reinterpret_cast<float2 *>(part + kRows * 128 + 2 * rx) = make_float2(M, l);
             fence_before();
             if (c0 != c1 && ok) {
                 // ---- shared with other CTAs: the last to arrive adds the parts in span order ----
@@ -988,40 +1003,49 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                     bar_arrive(&ctl.decided);
                 }
                 ok = warp_wait(&ctl.decided, shared++ & 1, abort);
-                if (ok && *(volatile int *)&ctl.last && active && row_live) {
+                if (ok && *(volatile int *)&ctl.last && row_live) {
                     __threadfence();
                     float m2 = -INFINITY, l2 = 0.0f;
-                    for (int y = c0; y <= c1; ++y)
-                        m2 = fmaxf(m2, __ldcg(base + ((long long)y * 2 + (y == c0)) * kPrefillPartFloats + kRows * 128 + 2 * rx));
-                    for (int y = c0; y <= c1; ++y) {
+                    for (int z = c0; z <= c1; ++z)
+                        m2 = fmaxf(m2, __ldcg(base + ((long long)z * 2 + (z == c0)) * kPrefillPartFloats + kRows * 128 + 2 * rx));
+                    for (int z = c0; z <= c1; ++z) {
                         const float2 ml = __ldcg(reinterpret_cast<const float2 *>(
-                            base + ((long long)y * 2 + (y == c0)) * kPrefillPartFloats + kRows * 128 + 2 * rx));
+                            base + ((long long)z * 2 + (z == c0)) * kPrefillPartFloats + kRows * 128 + 2 * rx));
                         l2 += ml.y * (ml.x == m2 ? 1.0f : ex2(ml.x - m2));
                     }
                     const float inv = l2 == 0.0f ? 0.0f : 1.0f / l2;
 #pragma unroll 1
-                    for (int cc = 0; cc < D / 4; cc += 2) {
-                        float4 o0 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), o1 = o0;
-                        for (int y = c0; y <= c1; ++y) {
-                            const float *part = base + ((long long)y * 2 + (y == c0)) * kPrefillPartFloats;
-                            const float m1 = __ldcg(part + kRows * 128 + 2 * rx);
+                    for (int cc = 0; cc < D / 4; cc += 8) {  // 32 values at a time: eight loads in flight
+                        float4 o[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
+                        for (int z = c0; z <= c1; ++z) {
+                            const float *from = base + ((long long)z * 2 + (z == c0)) * kPrefillPartFloats;
+                            const float m1 = __ldcg(from + kRows * 128 + 2 * rx);
+                            const bool none = m1 == -INFINITY;  // a part that saw nothing has no O
                             const float f = m1 == m2 ? 1.0f : ex2(m1 - m2);
-                            const float4 v0 = __ldcg(reinterpret_cast<const float4 *>(part + (cc * kRows + rx) * 4));
-                            const float4 v1 = __ldcg(reinterpret_cast<const float4 *>(part + ((cc + 1) * kRows + rx) * 4));
-                            o0.x = fmaf(v0.x, f, o0.x); o0.y = fmaf(v0.y, f, o0.y);
-                            o0.z = fmaf(v0.z, f, o0.z); o0.w = fmaf(v0.w, f, o0.w);
-                            o1.x = fmaf(v1.x, f, o1.x); o1.y = fmaf(v1.y, f, o1.y);
-                            o1.z = fmaf(v1.z, f, o1.z); o1.w = fmaf(v1.w, f, o1.w);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                const float4 v = none ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
+                                                      : __ldcg(reinterpret_cast<const float4 *>(from + ((cc + k) * kRows + rx) * 4));
+                                o[k].x = fmaf(v.x, f, o[k].x);
+                                o[k].y = fmaf(v.y, f, o[k].y);
+                                o[k].z = fmaf(v.z, f, o[k].z);
+                                o[k].w = fmaf(v.w, f, o[k].w);
+                            }
                         }
-                        *reinterpret_cast<uint4 *>(orow + 4 * cc) =
-                            make_uint4(bf16x2(o0.x * inv, o0.y * inv), bf16x2(o0.z * inv, o0.w * inv),
-                                       bf16x2(o1.x * inv, o1.y * inv), bf16x2(o1.z * inv, o1.w * inv));
+#pragma unroll
+                        for (int k = 0; k < 8; k += 2)
+                            *reinterpret_cast<uint4 *>(orow + 4 * (cc + k)) =
+                                make_uint4(bf16x2(o[k].x * inv, o[k].y * inv), bf16x2(o[k].z * inv, o[k].w * inv),
+                                           bf16x2(o[k + 1].x * inv, o[k + 1].y * inv),
+                                           bf16x2(o[k + 1].z * inv, o[k + 1].w * inv));
                     }
                 }
             }
         }
     }
-#undef Q8_EACH_SEGMENT
 
     // ---- drain: every MMA issued is done (o_full was waited for), unless the CTA aborted ----
     fence_before();
@@ -1068,13 +1092,12 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
-// A bf16 cache's keys or values as [pages][heads * page_size][dim], boxes of `run` tokens by 64 values, 128-byte swizzle.
-bool encode_cache(CUtensorMap *map, const AttnArgs &a, const void *p, int dim, int run) {
+// A map of 16-bit values [dims[2]][dims[1]][dims[0]], boxes of 64 x b1 x b2 values, 128-byte swizzle.
+bool encode_boxes(CUtensorMap *map, const void *p, const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2], int b1,
+                  int b2) {
     const PFN_cuTensorMapEncodeTiled_v12000 encode = encode_fn();
     if (!encode) return false;
-    cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)a.kv_heads * a.page_size, (cuuint64_t)a.pages};
-    cuuint64_t strides[2] = {(cuuint64_t)dim * 2, (cuuint64_t)a.page_stride * 2};
-    cuuint32_t box[3] = {64, (cuuint32_t)run, 1}, step[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {64, (cuuint32_t)b1, (cuuint32_t)b2}, step[3] = {1, 1, 1};
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(p), dims, strides, box, step,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -1084,12 +1107,19 @@ template <int D, bool Q8> cudaError_t launch_one(const AttnArgs &a, int sms, cud
     using C = Cfg<D, Q8>;
     cudaError_t e = cudaFuncSetAttribute(prefill_kernel<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    PrefillArgs pa = {a, 16, (unsigned)(((1ll << 31) + a.group - 1) / a.group)};
+    PrefillArgs pa = {a, 16, kTile / a.group};
     while (pa.run < kTile && a.page_size % (2 * pa.run) == 0) pa.run *= 2;
-    CUtensorMap kmap = {}, vmap = {};
-    if (!Q8 && (!encode_cache(&kmap, a, a.k, D, pa.run) || !encode_cache(&vmap, a, a.v, D, pa.run)))
+    // K and V as [pages][heads * page_size][dim], boxes of `run` tokens; Q as [rows][heads][dim], boxes of a tile's
+    // tokens and their heads.
+    CUtensorMap kmap = {}, vmap = {}, qmap = {};
+    const cuuint64_t kd[3] = {D, (cuuint64_t)a.kv_heads * a.page_size, (cuuint64_t)a.pages};
+    const cuuint64_t ks[2] = {D * 2, (cuuint64_t)a.page_stride * 2};
+    const cuuint64_t qd[3] = {D, (cuuint64_t)a.heads, (cuuint64_t)a.rows}, qs[2] = {D * 2, (cuuint64_t)a.ldq * 2};
+    if (!encode_boxes(&qmap, a.q, qd, qs, a.group, pa.tile_tokens) ||
+        (!Q8 && (!encode_boxes(&kmap, a.k, kd, ks, pa.run, 1) || !encode_boxes(&vmap, a.v, kd, ks, pa.run, 1))))
         return cudaErrorNotSupported;
-    return kv_launch(prefill_kernel<D, Q8>, dim3((unsigned)sms, 1, 1), C::kThreads, C::kSmem, stream, pa, kmap, vmap);
+    return kv_launch(prefill_kernel<D, Q8>, dim3((unsigned)sms, 1, 1), C::kThreads, C::kSmem, stream, pa, kmap, vmap,
+                     qmap);
 }
 
 }  // namespace
