@@ -8,7 +8,8 @@
 //     S = Q K^T (tcgen05.mma, both operands in shared memory, fp32 S in tensor memory)
 //     P = 2^(S scale log2(e) - m), rounded to 16 bits, written over S in tensor memory
 //     O += P V (P read from tensor memory, V from shared memory, fp32 O in tensor memory)
-// with a running m that only moves when a score passes it by 2^8 (then the row's O is rescaled in place).
+// with a running m that only moves when weights against it grow past what their type and the sums take (2^15 in fp16,
+// 2^60 in bf16; then the row's O is rescaled in place).
 //
 // Warps: 0-3 and 4-7 the softmax of tiles A and B, one row a thread; 8 issues the MMAs; 9 requests keys and values;
 // the rest load Q and prepare values:
@@ -32,6 +33,8 @@
 #include <cudaTypedefs.h>
 #include <math.h>
 
+#include <atomic>
+
 #include "q8_attn.h"
 #include "q8_device.cuh"
 
@@ -43,7 +46,6 @@ constexpr int kRows = 256;   // query rows of an item
 constexpr int kItemCost = 2; // what an item costs beside its tiles, in tiles: loading Q, the pipe's fill, the epilogue
 constexpr int kMinSpan = 4 + kItemCost;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kSlack = 8.0f;
 constexpr int kMmaWarp = 8, kLoadWarp = 9, kHelpWarp = 10;
 constexpr unsigned kTmemColumns = 512;
 constexpr uint32_t kColO = 256;  // S of tiles A and B at columns 0 and 128, O from here
@@ -73,7 +75,7 @@ template <int D, bool Q8> struct Control {
     uint64_t full[10], ready[10], empty[10];   // operand ring: landed, usable, free
     uint64_t raw_full[4], raw_empty[4];        // raw ring (Q8_0)
     uint64_t q_raw, q_full, q_empty, drain;  // q_raw: landed, before the conversion (Q8_0)
-    uint64_t s_full[2], p_ready[2][2], o_full[2], joined, decided;  // p_ready: the tile's upper and lower 64 keys
+    uint64_t s_full[2], p_ready[2], o_full[2], joined, decided;
     // Of key tile number n of this CTA at n & 7 (no role is more than five tiles behind the requests):
     unsigned pages[8];  // bits: which 16-token groups lie on a page
     float unit[2][8];   // Q8_0: log2 of the keys' and the values' unit
@@ -238,29 +240,50 @@ __device__ __forceinline__ void tma3(uint32_t dst, const CUtensorMap *map, int x
         : "memory");
 }
 
+// The same into every CTA of the cluster whose bit is set: the same place, completing the same barrier of each.
+__device__ __forceinline__ void tma3_multicast(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar,
+                                               unsigned mask) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%2, "
+        "%3, %4}], [%5], %6;" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(saddr(bar)), "h"((uint16_t)mask)
+        : "memory");
+}
+__device__ __forceinline__ void commit_multicast(uint64_t *bar, unsigned mask) {
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            saddr(bar)),
+        "h"((uint16_t)mask)
+        : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 struct PrefillArgs {
     AttnArgs a;
     int run;         // consecutive tokens of a tile that lie on one page wherever they start: gcd(page_size, 128)
     int tile_tokens; // tokens of a query tile: 128 / group
 };
 
-// Two query tiles of one cache head: tokens tok0 .. tok0 + tokens - 1 of request r, the first tile_tokens of them in
-// tile A, the rest in B; row y of a tile is token y / group, head y % group of those that share the cache head.  The
-// item's key tiles are [0, us) for the sinks and [ul, ul + n - us); tile A visits the first n_a of them.  In the list
-// an item takes kItemCost + n places, the tiles last.
+// 2 CL query tiles of one cache head, two for each CTA of a cluster: tokens tok0 .. tok0 + tokens - 1 of request r,
+// tile_tokens to a tile; row y of a tile is token y / group, head y % group of those that share the cache head.  The
+// item's key tiles are [0, us) for the sinks and [ul, ul + n - us).  In the list an item takes kItemCost + n places, the
+// tiles last.
 struct Item {
     int r, qt, h;
     long long start;  // of its tiles in the list, the fixed cost behind it
     int row0, all, pos0;  // the request's first row, its rows, the position of its first row
     int tok0, tokens;
-    int p_min, p_max, end, lo, us, ul, n, n_a;
+    int p_min, p_max, end, lo, us, ul, n;
 
     __device__ __forceinline__ int tile(int i) const { return i < us ? i : ul + (i - us); }
     // Whether some row of the item does not see all of tile u, pages aside.
-    __device__ __forceinline__ bool partial(const AttnArgs &a, int u) const {
+    __device__ __forceinline__ bool partial(const AttnArgs &a, int u) const { return partial(a, u, p_min, p_max); }
+    // The same for its rows at positions p0 .. p1.
+    __device__ __forceinline__ bool partial(const AttnArgs &a, int u, int p0, int p1) const {
         const int j0 = u * kTile;
-        return j0 + kTile > end || j0 + kTile - 1 > p_min ||
-               (a.window && p_max - j0 >= a.window && j0 + kTile > a.sinks);
+        return j0 + kTile > end || j0 + kTile - 1 > p0 || (a.window && p1 - j0 >= a.window && j0 + kTile > a.sinks);
     }
 };
 // Key tiles that rows at positions p_min .. p_max visit.
@@ -278,33 +301,51 @@ __device__ __forceinline__ void request_of(const AttnArgs &a, Item &x) {
     x.all = t1 - t0;
     x.pos0 = max(a.lens[x.r], 0) - x.all;
 }
-__device__ __forceinline__ int q_tiles(const PrefillArgs &pa, int tokens) {
-    return (tokens + 2 * pa.tile_tokens - 1) / (2 * pa.tile_tokens);
+template <int CL> __device__ __forceinline__ int q_tiles(const PrefillArgs &pa, int tokens) {
+    return (tokens + 2 * CL * pa.tile_tokens - 1) / (2 * CL * pa.tile_tokens);
 }
-__device__ __forceinline__ void q_tile_of(const PrefillArgs &pa, Item &x) {
-    x.tok0 = x.qt * 2 * pa.tile_tokens;
-    x.tokens = min(2 * pa.tile_tokens, x.all - x.tok0);
+template <int CL> __device__ __forceinline__ void q_tile_of(const PrefillArgs &pa, Item &x) {
+    x.tok0 = x.qt * 2 * CL * pa.tile_tokens;
+    x.tokens = min(2 * CL * pa.tile_tokens, x.all - x.tok0);
     x.p_min = x.pos0 + x.tok0;
     x.p_max = x.p_min + x.tokens - 1;
     span_of(pa.a, x);
-    // tiles up to the one of tile A's last key
-    const int last = (x.p_min + min(pa.tile_tokens, x.tokens) - 1) / kTile;
-    x.n_a = min(x.n, max(1, last < x.ul ? min(last + 1, x.us) : x.us + last - x.ul + 1));
+}
+// The item's key tiles that its query tile t visits within a segment [i0, i1): first .. last without us .. skip - 1,
+// which are in no row's window; none if last < first.
+struct Visit {
+    int first, last, us, skip;
+    __device__ __forceinline__ bool operator()(int i) const { return i >= first && i <= last && (i < us || i >= skip); }
+};
+__device__ __forceinline__ Visit visit_of(const PrefillArgs &pa, const Item &x, int t, int i0, int i1) {
+    Visit v = {0, -1, x.us, x.us};
+    const int a = t * pa.tile_tokens, b = min(a + pa.tile_tokens, x.tokens);  // its tokens
+    if (a >= b) return v;
+    const int hi = (x.p_min + b - 1) / kTile;  // the tile of its last key
+    const int lim = min(x.n, max(1, hi < x.ul ? min(hi + 1, x.us) : x.us + hi - x.ul + 1));
+    if (pa.a.window) {  // sinks may reach past us, where the item's first rows see all tiles anyway
+        v.us = max(x.us, min(x.us + (min(pa.a.sinks, x.end) + kTile - 1) / kTile - x.ul, lim));
+        v.skip = max(v.us, min(x.us + max(x.p_min + a - pa.a.window + 1, 0) / kTile - x.ul, lim - 1));
+    }
+    v.first = i0 >= v.us && i0 < v.skip ? v.skip : i0;
+    v.last = min(lim, i1) - 1;
+    if (v.last >= v.us && v.last < v.skip) v.last = v.us - 1;
+    return v;
 }
 __device__ __forceinline__ long long cost_of(const Item &x) { return x.n ? x.n + kItemCost : 0; }
-__device__ __forceinline__ void next_item(const PrefillArgs &pa, Item &x) {
+template <int CL> __device__ __forceinline__ void next_item(const PrefillArgs &pa, Item &x) {
     x.start += x.n + kItemCost;
     if (++x.h < pa.a.kv_heads) return;
     x.h = 0;
     do {
-        if (++x.qt >= q_tiles(pa, x.all)) {
+        if (++x.qt >= q_tiles<CL>(pa, x.all)) {
             do {
                 if (++x.r >= pa.a.R) return;  // never reached: the walk ends within the list
                 request_of(pa.a, x);
             } while (x.all == 0);
             x.qt = 0;
         }
-        q_tile_of(pa, x);
+        q_tile_of<CL>(pa, x);
     } while (x.n == 0);
 }
 
@@ -344,7 +385,7 @@ __device__ __noinline__ void add_nonfinite(const AttnArgs &a, const Item it, int
     }
 }
 
-template <int D, bool Q8>
+template <int D, bool Q8, int CL>
 __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
     prefill_kernel(const __grid_constant__ PrefillArgs pa, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                    const __grid_constant__ CUtensorMap qmap) {
@@ -354,12 +395,13 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
     Control<D, Q8> &ctl = *reinterpret_cast<Control<D, Q8> *>(smem + C::kCtl);
     volatile int *abort = &ctl.abort;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = CL == 1 ? 0 : (int)(blockIdx.x % CL), group_id = blockIdx.x / CL;  // in its cluster; the cluster
 
     if (tid == 0) {
         for (int i = 0; i < C::kSlots; ++i) {
             bar_init(&ctl.full[i], 1);
             bar_init(&ctl.ready[i], C::kHelpers);
-            bar_init(&ctl.empty[i], 1);
+            bar_init(&ctl.empty[i], CL);  // every CTA that the copies go to
         }
         for (int i = 0; i < C::kRawSlots; ++i) {
             bar_init(&ctl.raw_full[i], 1);
@@ -373,8 +415,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
         bar_init(&ctl.decided, 1);
         for (int i = 0; i < 2; ++i) {
             bar_init(&ctl.s_full[i], 1);
-            bar_init(&ctl.p_ready[i][0], 4);
-            bar_init(&ctl.p_ready[i][1], 4);
+            bar_init(&ctl.p_ready[i], 4);
             bar_init(&ctl.o_full[i], 1);
         }
         ctl.abort = 0;
@@ -400,7 +441,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
         int mine = 0;
         for (x.r = ra; x.r < rb; ++x.r) {
             request_of(a, x);
-            mine += q_tiles(pa, x.all);
+            mine += q_tiles<CL>(pa, x.all);
         }
         int upto = mine;
 #pragma unroll
@@ -418,7 +459,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
         for (x.r = ra; x.r < rb; ++x.r) {
             request_of(a, x);
             qsum[x.r] = before;
-            before += q_tiles(pa, x.all);
+            before += q_tiles<CL>(pa, x.all);
         }
         if (tid == 0) qsum[a.R] = tiles;
         __syncthreads();
@@ -434,7 +475,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
             x.r = lo;
             x.qt = q - qsum[lo];
             request_of(a, x);
-            q_tile_of(pa, x);
+            q_tile_of<CL>(pa, x);
         };
         for (int q = qa; q < qb; ++q) {
             seek(q);
@@ -455,8 +496,8 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
             total += ctl.scan[w];
         }
         total *= a.kv_heads;
-        span = max((total + gridDim.x - 1) / gridDim.x, (long long)kMinSpan);
-        b0 = span * blockIdx.x;
+        span = max((total + gridDim.x / CL - 1) / (gridDim.x / CL), (long long)kMinSpan);
+        b0 = span * group_id;
         b1 = min(total, b0 + span);
         if (b0 < b1 && ahead * a.kv_heads <= b0 && b0 < (ahead + keys) * a.kv_heads) {
             for (int q = qa;; ++q) {  // exactly one thread holds unit b0
@@ -472,6 +513,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
     fence_before();
     fence_async();
     __syncthreads();  // also: qsum is read, the operands may land over it
+    if (CL > 1) cluster_sync();  // in every CTA of the cluster, its barriers set up
     fence_after();
     const uint32_t tmem = ctl.tmem;
     const bool work = b0 < b1;
@@ -480,7 +522,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
         it.r = ctl.first_r;
         it.qt = ctl.first_qt;
         request_of(a, it);
-        q_tile_of(pa, it);
+        q_tile_of<CL>(pa, it);
         it.h = (int)((b0 - ctl.first_start) / cost_of(it));
         it.start = ctl.first_start + it.h * cost_of(it) + kItemCost;
     }
@@ -495,7 +537,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
     auto advance = [&]() {
         more = it.start + it.n < b1;
         if (more) {
-            next_item(pa, it);
+            next_item<CL>(pa, it);
             segment();
             more = i1 > 0;
         }
@@ -512,12 +554,13 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
             ++seg;
             if (lane == 0) {  // Q: boxes of 64 values, the cache head's heads, a tile's tokens
                 uint64_t *bar = Q8 ? &ctl.q_raw : &ctl.q_full;
-                const int nx = it.tokens > pa.tile_tokens ? 2 : 1;
+                const int mine = it.tokens - rank * 2 * pa.tile_tokens;  // this CTA's tokens
+                const int nx = mine > pa.tile_tokens ? 2 : mine > 0 ? 1 : 0;
                 bar_arrive_tx(bar, (unsigned)(nx * C::kSub * 128 * a.group * pa.tile_tokens));
                 for (int x = 0; x < nx; ++x)
                     for (int sub = 0; sub < C::kSub; ++sub)
                         tma3(saddr(smem) + x * C::kOp + sub * kTile * 128, &qmap, 64 * sub, it.h * a.group,
-                             it.row0 + it.tok0 + x * pa.tile_tokens, bar);
+                             it.row0 + it.tok0 + (2 * rank + x) * pa.tile_tokens, bar);
             }
             __syncwarp();
             const int *row = a.table + (size_t)it.r * a.pitch;
@@ -554,13 +597,18 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                         bar_arrive_tx(full, bytes);
                     }
                     __syncwarp();
-                    if (there) {
+                    // each CTA of the cluster requests its share of the runs, for all of them
+                    if (there && (CL == 1 || lane * CL / runs == rank)) {
                         if (!Q8) {
                             const uint32_t dst = saddr(smem + C::kRing + s * C::kOp) + lane * pa.run * 128;
 #pragma unroll
                             for (int sub = 0; sub < C::kSub; ++sub)
-                                tma3(dst + sub * kTile * 128, kv ? &vmap : &kmap, 64 * sub, it.h * a.page_size + myoff,
-                                     mypage, full);
+                                if (CL == 1)
+                                    tma3(dst + sub * kTile * 128, kv ? &vmap : &kmap, 64 * sub,
+                                         it.h * a.page_size + myoff, mypage, full);
+                                else
+                                    tma3_multicast(dst + sub * kTile * 128, kv ? &vmap : &kmap, 64 * sub,
+                                                   it.h * a.page_size + myoff, mypage, full, (1u << CL) - 1u);
                         } else {
                             const long long at = (long long)mypage * a.page_stride +
                                                  ((long long)it.h * a.page_size + myoff) * D;
@@ -595,64 +643,67 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                                   ((kTile >> 3) << 17) | ((kTile >> 4) << 24);
             constexpr uint32_t id_o = (1u << 4) | (fmt << 7) | (fmt << 10) | (1u << 16) | ((D >> 3) << 17) |
                                       ((kTile >> 4) << 24);
-            const uint32_t q_at = saddr(smem), ring = saddr(smem + C::kRing);
+            // One thread feeds the tensor pipe, so an MMA has to be a few instructions: descriptors are a constant and
+            // an address in 16-byte units, and steps along K are additions to it.
+            const uint64_t q_desc = desc128(saddr(smem), 16), k_desc = desc128(saddr(smem + C::kRing), 16);
+            const uint64_t v_desc = desc128(saddr(smem + C::kRing), kTile * 128);
             unsigned cnt = 0, seg = 0, pcnt[2] = {0, 0};
             bool ok = true;
             auto scores = [&](int x, unsigned s) {  // S of tile x with the keys in slot s
+                const uint64_t qd = q_desc + (unsigned)(x * (C::kOp >> 4)), kd = k_desc + s * (C::kOp >> 4);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t o = (k / 4) * kTile * 128 + (k % 4) * 32;
-                    mma_ss(tmem + x * kTile, desc128(q_at + x * C::kOp + o, 16), desc128(ring + s * C::kOp + o, 16), id_s,
-                           k > 0);
+                    const unsigned o = ((k / 4) * kTile * 128 + (k % 4) * 32) >> 4;
+                    mma_ss(tmem + x * kTile, qd + o, kd + o, id_s, k > 0);
                 }
                 commit(&ctl.s_full[x]);
             };
             for (; more; advance()) {
                 if (!ok) break;
-                const int lim[2] = {min(i1, it.n_a), it.tokens > pa.tile_tokens ? i1 : 0};  // each tile's last, plus 1
+                const Visit vis[2] = {visit_of(pa, it, 2 * rank, i0, i1), visit_of(pa, it, 2 * rank + 1, i0, i1)};
                 if (!(ok = bar_wait(&ctl.q_full, seg & 1, abort))) break;
                 auto usable = [&](unsigned c, bool value) {
                     const unsigned s = c % C::kSlots, par = (c / C::kSlots) & 1;
                     return bar_wait(Q8 || value ? &ctl.ready[s] : &ctl.full[s], par, abort);
                 };
+                auto release = [&](unsigned c) {  // the slot is free once the MMAs so far are done
+                    if (CL == 1) commit(&ctl.empty[c % C::kSlots]);
+                    else commit_multicast(&ctl.empty[c % C::kSlots], (1u << CL) - 1u);
+                };
                 const unsigned c0 = cnt;
                 if (!(ok = usable(c0, false))) break;
                 fence_after();
+#pragma unroll
                 for (int x = 0; x < 2; ++x)
-                    if (i0 < lim[x]) scores(x, c0 % C::kSlots);
-                commit(&ctl.empty[c0 % C::kSlots]);
+                    if (vis[x](i0)) scores(x, c0 % C::kSlots);
+                release(c0);
                 if (i1 - i0 == 1) commit(&ctl.q_empty);
                 for (int i = i0; i < i1 && ok; ++i) {
                     const unsigned cv = c0 + 2 * (i - i0) + 1, ck = cv + 1;
                     const bool next = i + 1 < i1;
                     if (!(ok = usable(cv, true))) break;
+                    const uint64_t vd = v_desc + (cv % C::kSlots) * (C::kOp >> 4);
+#pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        if (i < lim[x]) {
+                        if (vis[x](i)) {
+                            if (!(ok = bar_wait(&ctl.p_ready[x], pcnt[x] & 1, abort))) break;
+                            fence_after();
 #pragma unroll
-                            for (int half = 0; half < 2; ++half) {  // the upper keys' weights come first
-                                if (!(ok = bar_wait(&ctl.p_ready[x][half], pcnt[x] & 1, abort))) break;
-                                fence_after();
-#pragma unroll
-                                for (int k = 0; k < kTile / 32; ++k) {
-                                    const int ks = (half ? 0 : kTile / 32) + k;
-                                    mma_ts(tmem + kColO + x * 128, tmem + x * kTile + kColP + ks * 8,
-                                           desc128(ring + (cv % C::kSlots) * C::kOp + ks * 2048, kTile * 128), id_o,
-                                           i > i0 || half > 0 || k > 0);
-                                }
-                            }
-                            if (!ok) break;
+                            for (int k = 0; k < kTile / 16; ++k)
+                                mma_ts(tmem + kColO + x * 128, tmem + x * kTile + kColP + k * 8, vd + (k * 2048 >> 4),
+                                       id_o, i > vis[x].first || k > 0);
                             ++pcnt[x];
-                            if (i + 1 == lim[x]) commit(&ctl.o_full[x]);
+                            if (i == vis[x].last) commit(&ctl.o_full[x]);
                         }
-                        if (x == (i < lim[1] ? 1 : 0)) commit(&ctl.empty[cv % C::kSlots]);  // after its last use
+                        if (x == 1) release(cv);
                         if (next && x == 0) {
                             if (!(ok = usable(ck, false))) break;
                             fence_after();
                         }
-                        if (i + 1 < lim[x]) scores(x, ck % C::kSlots);
+                        if (next && vis[x](i + 1)) scores(x, ck % C::kSlots);
                     }
                     if (next && ok) {
-                        commit(&ctl.empty[ck % C::kSlots]);
+                        release(ck);
                         if (i + 2 == i1) commit(&ctl.q_empty);
                     }
                 }
@@ -816,24 +867,29 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
         // ---- softmax: thread = row of tile x ----
         const int x = warp >> 2, quarter = warp & 3;
         const int y = quarter * 32 + lane, rx = x * kTile + y;
-        const int tok = x * pa.tile_tokens + y / a.group, gh = y % a.group;  // of this row: the item's token, the head
+        const int tok = (2 * rank + x) * pa.tile_tokens + y / a.group, gh = y % a.group;  // of this row: the item's token, the head
         const bool whole_row = y < pa.tile_tokens * a.group;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         const uint32_t ts = tmem + lanes + x * kTile, to = tmem + lanes + kColO + x * 128;
+        // The largest sum of a row's 128 weights: below fp16's largest value, and for bf16 weights, which have fp32's
+        // range, far below where a row's sums could overflow.
+        constexpr float kMostSum = Q8 ? 32768.0f : 1.15292150e18f;  // 2^15, 2^60
         constexpr float kLeast = 1.17549435e-38f;  // a factor of 0 would make NaN of a hidden score's -inf
         const float sc0 = fmaxf(fabsf(a.scale) * kLog2e, kLeast);
         unsigned cnt = 0, scnt = 0, ocnt = 0, shared = 0, seg = 0;
         bool ok = true;
         for (; more; advance()) {
             if (!ok) break;
-            const int lim = x == 0 ? min(i1, it.n_a) : it.tokens > pa.tile_tokens ? i1 : 0;
-            const bool active = i0 < lim;
+            const Visit vis = visit_of(pa, it, 2 * rank + x, i0, i1);
+            const bool active = vis.first <= vis.last;
+            const bool mine = it.tokens > 2 * rank * pa.tile_tokens;  // this CTA has rows of the item
             const bool row_live = whole_row && tok < it.tokens;
-            const int p = it.p_min + tok;
-            float M = -INFINITY, l = 0.0f;
+            const int p = it.p_min + tok, p0 = it.p_min + (2 * rank + x) * pa.tile_tokens;  // of the row, the tile
+            float M = row_live ? -INFINITY : 0.0f, l = 0.0f;  // rows beyond the item's ask for nothing
             if (active) {
                 float sc = sc0;
-                for (int i = i0; i < lim && ok; ++i) {
+                for (int i = vis.first; i <= vis.last && ok; ++i) {
+                    if (!vis(i)) continue;
                     const unsigned ck = cnt + 2 * (i - i0), at = (ck >> 1) & 7;
                     if (!(ok = warp_wait(&ctl.s_full[x], scnt & 1, abort))) break;
                     ++scnt;
@@ -848,7 +904,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                         shift = *(volatile float *)&ctl.unit[1][at];
                     }
                     const int u = it.tile(i), j0 = u * kTile;
-                    const bool part = groups != 0xFFu || it.partial(a, u);
+                    const bool part = groups != 0xFFu || it.partial(a, u, p0, p0 + pa.tile_tokens - 1);
                     // columns [c_lo, c_hi] and [0, c_sink) are visible
                     const int c_hi = min(p, it.end - 1) - j0;
                     const int c_lo = a.window ? max(p - a.window + 1 - j0, 0) : 0, c_sink = a.window ? a.sinks - j0 : 0;
@@ -869,42 +925,13 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                         }
                         tm_wait_st();
                     }
-                    // Two looks at the row: its maximum, then the weights.  The upper half of the scores stays in
-                    // registers between them; the weights go over it, so that the lower half can be read again.
-                    uint32_t v[2][32], w2[2][32];
-                    tm_ld32(ts, w2[0]);
-                    tm_ld32(ts + 32, w2[1]);
-                    tm_wait_ld();
-                    tm_ld32(ts + 64, v[0]);
-                    tm_ld32(ts + 96, v[1]);
-                    float mx = max3(max32(w2[0]), max32(w2[1]), -INFINITY);
-                    tm_wait_ld();
-                    mx = max3(mx, max32(v[0]), max32(v[1]));
-                    mx = mx == -INFINITY ? mx : fmaf(mx, sc, shift);
-                    const bool above = mx > M + kSlack || (M == -INFINITY && mx > M);
-                    if (__any_sync(0xffffffffu, above)) {
-                        const float now = above ? mx : M;
-                        const float f = above ? ex2(M - now) : 1.0f;  // 0 from -inf
-                        M = now;
-                        l *= f;
-                        if (i > i0) {
-#pragma unroll 1
-                            for (int c0 = 0; c0 < D; c0 += 16) {
-                                uint32_t w[16];
-                                tm_ld16(to + c0, w);
-                                tm_wait_ld();
-#pragma unroll
-                                for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) * f);
-                                tm_st16(to + c0, w);
-                            }
-                        }
-                    }
-                    const float off = shift - (M == -INFINITY ? 0.0f : M);
-                    unsigned long long sc2, off2, sum2 = 0ull;
+                    // The weights are taken against the running maximum as it stands: a row's maximum is only looked
+                    // for where their sum shows that a score passed it too far (or there is none yet).
+                    unsigned long long sc2, off2, sum2;
                     asm("mov.b64 %0, {%1, %1};" : "=l"(sc2) : "f"(sc));
-                    asm("mov.b64 %0, {%1, %1};" : "=l"(off2) : "f"(off));
-                    auto weights = [&](const uint32_t (&r)[32], uint32_t col) {
-                        uint32_t w[16];
+                    float sum;
+                    uint32_t w[4][16];
+                    auto weights = [&](const uint32_t (&r)[32], uint32_t (&to)[16]) {
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
                             unsigned long long e;
@@ -916,30 +943,62 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                             p1 = ex2(p1);
                             asm("{\n .reg .b64 s;\n mov.b64 s, {%1, %2};\n add.rn.f32x2 %0, %0, s;\n}"
                                 : "+l"(sum2) : "f"(p0), "f"(p1));
-                            w[k] = Q8 ? f16x2(p0, p1) : bf16x2(p0, p1);
+                            to[k] = Q8 ? f16x2(p0, p1) : bf16x2(p0, p1);
                         }
-                        tm_st16(ts + kColP + col, w);
                     };
-                    weights(v[0], 32);
-                    tm_ld32(ts, v[0]);
-                    weights(v[1], 48);
-                    tm_wait_st();
-                    fence_before();
-                    __syncwarp();
-                    if (lane == 0) bar_arrive(&ctl.p_ready[x][0]);
-                    tm_wait_ld();
-                    tm_ld32(ts + 32, v[1]);
-                    weights(v[0], 0);
-                    tm_wait_ld();
-                    weights(v[1], 16);
-                    float sum, sum_hi;
-                    asm("mov.b64 {%0, %1}, %2;" : "=f"(sum), "=f"(sum_hi) : "l"(sum2));
-                    sum += sum_hi;
+                    for (int again = __any_sync(0xffffffffu, M == -INFINITY) ? 1 : 0;; again = 1) {
+                        if (again) {
+                            float mx = -INFINITY;
+#pragma unroll 1
+                            for (int c0 = 0; c0 < kTile; c0 += 32) {
+                                uint32_t v[32];
+                                tm_ld32(ts + c0, v);
+                                tm_wait_ld();
+                                mx = fmaxf(mx, max32(v));
+                            }
+                            mx = mx == -INFINITY ? mx : fmaf(mx, sc, shift);
+                            const float now = fmaxf(M, mx), f = now == M ? 1.0f : ex2(M - now);  // 0 from -inf
+                            M = now;
+                            l *= f;
+                            if (i > vis.first) {
+#pragma unroll 1
+                                for (int c0 = 0; c0 < D; c0 += 16) {
+                                    uint32_t o[16];
+                                    tm_ld16(to + c0, o);
+                                    tm_wait_ld();
+#pragma unroll
+                                    for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                                    tm_st16(to + c0, o);
+                                }
+                            }
+                        }
+                        const float off = shift - (M == -INFINITY ? 0.0f : M);
+                        asm("mov.b64 %0, {%1, %1};" : "=l"(off2) : "f"(off));
+                        sum2 = 0ull;
+                        uint32_t va[32], vb[32];
+                        tm_ld32(ts, va);
+                        tm_ld32(ts + 32, vb);
+                        tm_wait_ld();
+                        weights(va, w[0]);
+                        tm_ld32(ts + 64, va);
+                        weights(vb, w[1]);
+                        tm_wait_ld();
+                        tm_ld32(ts + 96, vb);
+                        weights(va, w[2]);
+                        tm_wait_ld();
+                        weights(vb, w[3]);
+                        float sum_hi;
+                        asm("mov.b64 {%0, %1}, %2;" : "=f"(sum), "=f"(sum_hi) : "l"(sum2));
+                        sum += sum_hi;
+                        if (again || !__any_sync(0xffffffffu, row_live && sum > kMostSum)) break;
+                    }
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) tm_st16(ts + kColP + 16 * y, w[y]);
                     l += Q8 ? sum * ex2(-shift) : sum;
                     tm_wait_st();
                     fence_before();
                     __syncwarp();
-                    if (lane == 0) bar_arrive(&ctl.p_ready[x][1]);
+                    if (lane == 0) bar_arrive(&ctl.p_ready[x]);
                 }
                 if (ok) ok = warp_wait(&ctl.o_full[x], ocnt++ & 1, abort);
                 fence_after();
@@ -987,14 +1046,14 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                     }
                 }
             }
-            if (c0 != c1) *reinterpret_cast<float2 *>(part + kRows * 128 + 2 * rx) = make_float2(M, l);
+            if (c0 != c1 && mine) *reinterpret_cast<float2 *>(part + kRows * 128 + 2 * rx) = make_float2(M, l);
             fence_before();
-            if (c0 != c1 && ok) {
+            if (c0 != c1 && mine && ok) {
                 // ---- shared with other CTAs: the last to arrive adds the parts in span order ----
                 __threadfence();
                 bar_arrive(&ctl.joined);
                 if (tid == 0 && bar_wait(&ctl.joined, shared & 1, abort)) {
-                    int *count = reinterpret_cast<int *>(a.work + kPrefillCounterAt) + c0;
+                    int *count = reinterpret_cast<int *>(a.work + kPrefillCounterAt) + c0 * CL + rank;
                     __threadfence();
                     const int seen = atomicAdd(count, 1);
                     ctl.last = seen == c1 - c0;
@@ -1007,10 +1066,10 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                     __threadfence();
                     float m2 = -INFINITY, l2 = 0.0f;
                     for (int z = c0; z <= c1; ++z)
-                        m2 = fmaxf(m2, __ldcg(base + ((long long)z * 2 + (z == c0)) * kPrefillPartFloats + kRows * 128 + 2 * rx));
+                        m2 = fmaxf(m2, __ldcg(base + ((long long)(z * CL + rank) * 2 + (z == c0)) * kPrefillPartFloats + kRows * 128 + 2 * rx));
                     for (int z = c0; z <= c1; ++z) {
                         const float2 ml = __ldcg(reinterpret_cast<const float2 *>(
-                            base + ((long long)z * 2 + (z == c0)) * kPrefillPartFloats + kRows * 128 + 2 * rx));
+                            base + ((long long)(z * CL + rank) * 2 + (z == c0)) * kPrefillPartFloats + kRows * 128 + 2 * rx));
                         l2 += ml.y * (ml.x == m2 ? 1.0f : ex2(ml.x - m2));
                     }
                     const float inv = l2 == 0.0f ? 0.0f : 1.0f / l2;
@@ -1021,7 +1080,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                         for (int k = 0; k < 8; ++k) o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 2
                         for (int z = c0; z <= c1; ++z) {
-                            const float *from = base + ((long long)z * 2 + (z == c0)) * kPrefillPartFloats;
+                            const float *from = base + ((long long)(z * CL + rank) * 2 + (z == c0)) * kPrefillPartFloats;
                             const float m1 = __ldcg(from + kRows * 128 + 2 * rx);
                             const bool none = m1 == -INFINITY;  // a part that saw nothing has no O
                             const float f = m1 == m2 ? 1.0f : ex2(m1 - m2);
@@ -1058,6 +1117,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
     }
     __syncthreads();
     fence_after();
+    if (CL > 1) cluster_sync();  // nothing of the others' copies or commits is on its way here any more
     if (warp == 0)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemColumns) : "memory");
     // ---- rows that see nothing: padding, and rows before the first key ----
@@ -1103,12 +1163,13 @@ bool encode_boxes(CUtensorMap *map, const void *p, const cuuint64_t (&dims)[3], 
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool Q8> cudaError_t launch_one(const AttnArgs &a, int sms, cudaStream_t stream) {
+template <int D, bool Q8, int CL> cudaError_t launch_one(const AttnArgs &a, int sms, cudaStream_t stream) {
     using C = Cfg<D, Q8>;
-    cudaError_t e = cudaFuncSetAttribute(prefill_kernel<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    const auto kernel = prefill_kernel<D, Q8, CL>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     PrefillArgs pa = {a, 16, kTile / a.group};
-    while (pa.run < kTile && a.page_size % (2 * pa.run) == 0) pa.run *= 2;
+    while (pa.run < kTile / CL && a.page_size % (2 * pa.run) == 0) pa.run *= 2;
     // K and V as [pages][heads * page_size][dim], boxes of `run` tokens; Q as [rows][heads][dim], boxes of a tile's
     // tokens and their heads.
     CUtensorMap kmap = {}, vmap = {}, qmap = {};
@@ -1118,8 +1179,36 @@ template <int D, bool Q8> cudaError_t launch_one(const AttnArgs &a, int sms, cud
     if (!encode_boxes(&qmap, a.q, qd, qs, a.group, pa.tile_tokens) ||
         (!Q8 && (!encode_boxes(&kmap, a.k, kd, ks, pa.run, 1) || !encode_boxes(&vmap, a.v, kd, ks, pa.run, 1))))
         return cudaErrorNotSupported;
-    return kv_launch(prefill_kernel<D, Q8>, dim3((unsigned)sms, 1, 1), C::kThreads, C::kSmem, stream, pa, kmap, vmap,
-                     qmap);
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(C::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CL;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CL > 1 ? 2 : 1;
+    cfg.gridDim = dim3((unsigned)sms, 1, 1);
+    if (CL > 1) {  // as many clusters as are resident at once (asked once a device)
+        static std::atomic<int> cache[64];
+        int dev = 0, n = 0;
+        e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) n = cache[dev].load(std::memory_order_relaxed);
+        if (n == 0) {
+            cfg.gridDim = dim3(CL, 1, 1);
+            e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+            if (e != cudaSuccess) return e;
+            if (n < 1) return cudaErrorNotSupported;
+            if (n > sms / CL) n = sms / CL;
+            if (dev < 64) cache[dev].store(n, std::memory_order_relaxed);
+        }
+        cfg.gridDim = dim3((unsigned)(n * CL), 1, 1);
+    }
+    return cudaLaunchKernelEx(&cfg, kernel, pa, kmap, vmap, qmap);
 }
 
 }  // namespace
@@ -1136,8 +1225,12 @@ cudaError_t launch_attn_prefill(const AttnArgs &a, int dim, bool q8, cudaStream_
     cudaError_t e = sm_count_of_device(&sms);
     if (e != cudaSuccess) return e;
     if (sms > kAttnMaxCtas) sms = kAttnMaxCtas;
-    if (dim == 128) return q8 ? launch_one<128, true>(a, sms, stream) : launch_one<128, false>(a, sms, stream);
-    return q8 ? launch_one<64, true>(a, sms, stream) : launch_one<64, false>(a, sms, stream);
+    if (q8) return dim == 128 ? launch_one<128, true, 1>(a, sms, stream) : launch_one<64, true, 1>(a, sms, stream);
+    // Two CTAs share each key and value tile (each requests half of it for both) where requests fill their four query
+    // tiles on average.
+    if ((long long)a.rows * a.group >= 4ll * kTile * a.R)
+        return dim == 128 ? launch_one<128, false, 2>(a, sms, stream) : launch_one<64, false, 2>(a, sms, stream);
+    return dim == 128 ? launch_one<128, false, 1>(a, sms, stream) : launch_one<64, false, 1>(a, sms, stream);
 }
 
 }  // namespace q8
