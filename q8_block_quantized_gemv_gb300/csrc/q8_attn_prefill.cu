@@ -128,9 +128,16 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, unsigned parity, volatil
         }
     }
 }
-// The same for a whole warp, one answer for all lanes.
+// The same for a whole warp, one answer for all lanes; the first look is a few instructions.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, unsigned parity, volatile int *abort) {
-    return __all_sync(0xffffffffu, bar_wait(bar, parity, abort));
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p, q;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " vote.sync.all.pred q, p, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}"
+        : "=r"(done)
+        : "r"(saddr(bar)), "r"(parity)
+        : "memory");
+    return done ? true : __all_sync(0xffffffffu, bar_wait(bar, parity, abort));
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -142,18 +149,35 @@ __device__ __forceinline__ void commit(uint64_t *bar) {
 // Shared-memory matrix descriptor, 128-byte swizzle (layout 2).  K-major operands (Q, K): rows of 128 bytes, groups of
 // 8 rows 1024 bytes apart.  MN-major (V): 64 values of dim in 128 bytes, groups of 8 keys 1024 bytes apart, the next
 // 64 values `lead` bytes on.
-__device__ __forceinline__ uint64_t desc128(uint32_t addr, uint32_t lead) {
-    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-           (1ull << 46) | (2ull << 61);
+constexpr uint64_t desc128_high = ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+__device__ __forceinline__ uint32_t desc128_low(uint32_t addr, uint32_t lead) {
+    return ((addr & 0x3FFFFu) >> 4) | ((lead >> 4) << 16);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
-                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+// One lane of a converged warp.  The warp that issues MMAs runs its loop with all lanes, so that addresses and
+// descriptors stay in uniform registers, and picks a lane for the instructions themselves: inside a one-lane branch
+// each MMA moved its operands over anew, 67 to 85 clocks of issue for 64 of work.
+__device__ __forceinline__ bool elect() {
+    uint32_t one;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(one));
+    return one != 0;
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// A value that all lanes hold, so that the compiler knows it.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+// Descriptors come as their low words; the high ones are desc128's constant.
+constexpr uint32_t kDescHigh = (uint32_t)(desc128_high >> 32);
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
-        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+        "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.b32 p, %4, 0;\n mov.b64 da, {%1, %5};\n"
+        " mov.b64 db, {%2, %5};\n tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 db;\n setp.ne.b32 p, %4, 0;\n mov.b64 db, {%2, %5};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
+        : "memory");
 }
 __device__ __forceinline__ void tm_ld32(uint32_t a, uint32_t (&v)[32]) {
     asm volatile(
@@ -394,7 +418,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
     extern __shared__ __align__(1024) unsigned char smem[];
     Control<D, Q8> &ctl = *reinterpret_cast<Control<D, Q8> *>(smem + C::kCtl);
     volatile int *abort = &ctl.abort;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = (int)uniform(tid >> 5);
     const int rank = CL == 1 ? 0 : (int)(blockIdx.x % CL), group_id = blockIdx.x / CL;  // in its cluster; the cluster
 
     if (tid == 0) {
@@ -515,7 +539,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
     __syncthreads();  // also: qsum is read, the operands may land over it
     if (CL > 1) cluster_sync();  // in every CTA of the cluster, its barriers set up
     fence_after();
-    const uint32_t tmem = ctl.tmem;
+    const uint32_t tmem = uniform(ctl.tmem);
     const bool work = b0 < b1;
     Item it;
     if (work) {
@@ -636,80 +660,76 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
         }
         __syncwarp();
     } else if (warp == kMmaWarp) {
-        // ---- the MMAs (one thread) ----
-        if (lane == 0) {
-            constexpr uint32_t fmt = Q8 ? 0u : 1u;  // fp16 or bf16 operands
-            const uint32_t id_s = (1u << 4) | (fmt << 7) | (fmt << 10) | (a.scale < 0.0f ? 1u << 13 : 0u) |
-                                  ((kTile >> 3) << 17) | ((kTile >> 4) << 24);
-            constexpr uint32_t id_o = (1u << 4) | (fmt << 7) | (fmt << 10) | (1u << 16) | ((D >> 3) << 17) |
-                                      ((kTile >> 4) << 24);
-            // One thread feeds the tensor pipe, so an MMA has to be a few instructions: descriptors are a constant and
-            // an address in 16-byte units, and steps along K are additions to it.
-            const uint64_t q_desc = desc128(saddr(smem), 16), k_desc = desc128(saddr(smem + C::kRing), 16);
-            const uint64_t v_desc = desc128(saddr(smem + C::kRing), kTile * 128);
-            unsigned cnt = 0, seg = 0, pcnt[2] = {0, 0};
-            bool ok = true;
-            auto scores = [&](int x, unsigned s) {  // S of tile x with the keys in slot s
-                const uint64_t qd = q_desc + (unsigned)(x * (C::kOp >> 4)), kd = k_desc + s * (C::kOp >> 4);
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const unsigned o = ((k / 4) * kTile * 128 + (k % 4) * 32) >> 4;
-                    mma_ss(tmem + x * kTile, qd + o, kd + o, id_s, k > 0);
+        // ---- the MMAs ----
+        // The tensor cores run what is queued while this warp looks at barriers, as long as a batch follows a batch: O
+        // of one key tile and S of the next for tile A, the same for B, each issued in one go, and the waits for
+        // what the next batches need between them.
+        constexpr uint32_t fmt = Q8 ? 0u : 1u;  // fp16 or bf16 operands
+        const uint32_t id_s = (1u << 4) | (fmt << 7) | (fmt << 10) | (a.scale < 0.0f ? 1u << 13 : 0u) |
+                              ((kTile >> 3) << 17) | ((kTile >> 4) << 24);
+        constexpr uint32_t id_o = (1u << 4) | (fmt << 7) | (fmt << 10) | (1u << 16) | ((D >> 3) << 17) |
+                                  ((kTile >> 4) << 24);
+        const uint32_t q_desc = desc128_low(saddr(smem), 16), k_desc = desc128_low(saddr(smem + C::kRing), 16);
+        const uint32_t v_desc = desc128_low(saddr(smem + C::kRing), kTile * 128);
+        unsigned slot = 0, phase = 0, seg = 0, pcnt[2] = {0, 0};  // of the ring: the next use
+        bool ok = true;
+        auto release = [&](unsigned slot) {  // the slot is free once the MMAs so far are done
+            if (CL == 1) commit(&ctl.empty[slot]);
+            else commit_multicast(&ctl.empty[slot], (1u << CL) - 1u);
+        };
+        for (; more; advance()) {
+            const Visit vis[2] = {visit_of(pa, it, 2 * rank, i0, i1), visit_of(pa, it, 2 * rank + 1, i0, i1)};
+            if (!(ok = warp_wait(&ctl.q_full, seg & 1, abort))) break;
+            for (int i = i0 - 1; i < i1 && ok; ++i) {
+                const bool has_v = i >= i0, has_k = i + 1 < i1;
+                unsigned sk = 0, sv = 0;
+                if (has_v) {
+                    sv = slot;
+                    if (!(ok = warp_wait(&ctl.ready[sv], phase, abort))) break;
+                    if (++slot == C::kSlots) { slot = 0; phase ^= 1; }
                 }
-                commit(&ctl.s_full[x]);
-            };
-            for (; more; advance()) {
-                if (!ok) break;
-                const Visit vis[2] = {visit_of(pa, it, 2 * rank, i0, i1), visit_of(pa, it, 2 * rank + 1, i0, i1)};
-                if (!(ok = bar_wait(&ctl.q_full, seg & 1, abort))) break;
-                auto usable = [&](unsigned c, bool value) {
-                    const unsigned s = c % C::kSlots, par = (c / C::kSlots) & 1;
-                    return bar_wait(Q8 || value ? &ctl.ready[s] : &ctl.full[s], par, abort);
-                };
-                auto release = [&](unsigned c) {  // the slot is free once the MMAs so far are done
-                    if (CL == 1) commit(&ctl.empty[c % C::kSlots]);
-                    else commit_multicast(&ctl.empty[c % C::kSlots], (1u << CL) - 1u);
-                };
-                const unsigned c0 = cnt;
-                if (!(ok = usable(c0, false))) break;
-                fence_after();
+                if (has_k) {
+                    sk = slot;
+                    if (!(ok = warp_wait(Q8 ? &ctl.ready[sk] : &ctl.full[sk], phase, abort))) break;
+                    if (++slot == C::kSlots) { slot = 0; phase ^= 1; }
+                }
+                sv = uniform(sv);
+                sk = uniform(sk);
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
-                    if (vis[x](i0)) scores(x, c0 % C::kSlots);
-                release(c0);
-                if (i1 - i0 == 1) commit(&ctl.q_empty);
-                for (int i = i0; i < i1 && ok; ++i) {
-                    const unsigned cv = c0 + 2 * (i - i0) + 1, ck = cv + 1;
-                    const bool next = i + 1 < i1;
-                    if (!(ok = usable(cv, true))) break;
-                    const uint64_t vd = v_desc + (cv % C::kSlots) * (C::kOp >> 4);
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        if (vis[x](i)) {
-                            if (!(ok = bar_wait(&ctl.p_ready[x], pcnt[x] & 1, abort))) break;
-                            fence_after();
+                for (int x = 0; x < 2; ++x) {
+                    const bool do_o = has_v && vis[x](i), do_s = has_k && vis[x](i + 1);
+                    const uint32_t more_o = i > vis[x].first;
+                    if (do_o && !(ok = warp_wait(&ctl.p_ready[x], pcnt[x]++ & 1, abort))) break;
+                    fence_after();
+                    if (elect()) {
+                        if (do_o) {
+                            const uint32_t vd = v_desc + sv * (C::kOp >> 4);
 #pragma unroll
                             for (int k = 0; k < kTile / 16; ++k)
                                 mma_ts(tmem + kColO + x * 128, tmem + x * kTile + kColP + k * 8, vd + (k * 2048 >> 4),
-                                       id_o, i > vis[x].first || k > 0);
-                            ++pcnt[x];
+                                       id_o, k > 0 ? 1u : more_o);
                             if (i == vis[x].last) commit(&ctl.o_full[x]);
                         }
-                        if (x == 1) release(cv);
-                        if (next && x == 0) {
-                            if (!(ok = usable(ck, false))) break;
-                            fence_after();
+                        if (do_s) {
+                            const uint32_t qd = q_desc + x * (C::kOp >> 4), kd = k_desc + sk * (C::kOp >> 4);
+#pragma unroll
+                            for (int k = 0; k < D / 16; ++k) {
+                                const unsigned o = ((k / 4) * kTile * 128 + (k % 4) * 32) >> 4;
+                                mma_ss(tmem + x * kTile, qd + o, kd + o, id_s, k > 0);
+                            }
+                            commit(&ctl.s_full[x]);
                         }
-                        if (next && vis[x](i + 1)) scores(x, ck % C::kSlots);
+                        if (x == 1) {
+                            if (has_v) release(sv);
+                            if (has_k) release(sk);
+                            if (i + 2 == i1) commit(&ctl.q_empty);
+                        }
                     }
-                    if (next && ok) {
-                        release(ck);
-                        if (i + 2 == i1) commit(&ctl.q_empty);
-                    }
+                    __syncwarp();
                 }
-                cnt = c0 + 2 * (i1 - i0);
-                ++seg;
             }
+            if (!ok) break;
+            ++seg;
         }
         __syncwarp();
     } else if (warp >= kHelpWarp) {
