@@ -33,8 +33,6 @@
 #include <cudaTypedefs.h>
 #include <math.h>
 
-#include <atomic>
-
 #include "q8_attn.h"
 #include "q8_device.cuh"
 
@@ -43,8 +41,6 @@ namespace {
 
 constexpr int kTile = 128;   // keys of a tile, and rows of a query tile
 constexpr int kRows = 256;   // query rows of an item
-constexpr int kItemCost = 2; // what an item costs beside its tiles, in tiles: loading Q, the pipe's fill, the epilogue
-constexpr int kMinSpan = 4 + kItemCost;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMmaWarp = 8, kLoadWarp = 9, kHelpWarp = 10;
 constexpr unsigned kTmemColumns = 512;
@@ -62,6 +58,9 @@ template <int D, bool Q8> struct Cfg {
     static constexpr int kRawSlots = Q8 ? (D == 128 ? 3 : 4) : 0;
     static constexpr int kHelpers = Q8 ? 4 : 2;            // warps
     static constexpr int kThreads = 32 * (kHelpWarp + kHelpers);
+    // What an item costs beside its tiles, in tiles: loading Q, the pipe's fill and drain, the epilogue.  Without it the
+    // CTAs of a long prompt's first rows, 44 short items each, took 835,000 clocks where the others took 740,000.
+    static constexpr int kItemCost = Q8 ? 2 : 4;
     static constexpr int kRing = 2 * kOp;                  // after Q's two tiles
     static constexpr int kRawAt = kRing + kSlots * kOp;
     static constexpr int kCtl = kRawAt + kRawSlots * kRaw;
@@ -72,7 +71,8 @@ template <int D, bool Q8> struct Cfg {
 // Control block in shared memory.
 template <int D, bool Q8> struct Control {
     using C = Cfg<D, Q8>;
-    uint64_t full[10], ready[10], empty[10];   // operand ring: landed, usable, free
+    uint64_t full[10], ready[10];              // operand ring: landed, usable
+    uint64_t step[8];                          // a step's MMAs are done, and with them what it used is free
     uint64_t raw_full[4], raw_empty[4];        // raw ring (Q8_0)
     uint64_t q_raw, q_full, q_empty, drain;  // q_raw: landed, before the conversion (Q8_0)
     uint64_t s_full[2], p_ready[2], o_full[2], joined, decided;
@@ -138,6 +138,18 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, unsigned parity, volati
         : "r"(saddr(bar)), "r"(parity)
         : "memory");
     return done ? true : __all_sync(0xffffffffu, bar_wait(bar, parity, abort));
+}
+// Whether three phases are complete: the looks overlap.
+__device__ __forceinline__ bool look3(uint64_t *b0, unsigned p0, uint64_t *b1, unsigned p1, uint64_t *b2, unsigned p2) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p, q, r;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n mbarrier.try_wait.parity.shared::cta.b64 r, [%5], %6;\n"
+        " and.pred p, p, q;\n and.pred p, p, r;\n vote.sync.all.pred q, p, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}"
+        : "=r"(done)
+        : "r"(saddr(b0)), "r"(p0), "r"(saddr(b1)), "r"(p1), "r"(saddr(b2)), "r"(p2)
+        : "memory");
+    return done != 0;
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -264,36 +276,35 @@ __device__ __forceinline__ void tma3(uint32_t dst, const CUtensorMap *map, int x
         : "memory");
 }
 
-// The same into every CTA of the cluster whose bit is set: the same place, completing the same barrier of each.
-__device__ __forceinline__ void tma3_multicast(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar,
-                                               unsigned mask) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%2, "
-        "%3, %4}], [%5], %6;" ::"r"(dst),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(saddr(bar)), "h"((uint16_t)mask)
-        : "memory");
-}
-__device__ __forceinline__ void commit_multicast(uint64_t *bar, unsigned mask) {
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-            saddr(bar)),
-        "h"((uint16_t)mask)
-        : "memory");
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+// 32 values of an output row; wide: 32-byte stores, whole sectors (every row 32-byte aligned).
+__device__ __forceinline__ void store_row(uint16_t *p, const float (&o)[32], bool wide) {
+    uint32_t w[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) w[k] = bf16x2(o[2 * k], o[2 * k + 1]);
+    if (wide) {
+#pragma unroll
+        for (int k = 0; k < 16; k += 8)
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p + 2 * k), "r"(w[k]),
+                         "r"(w[k + 1]), "r"(w[k + 2]), "r"(w[k + 3]), "r"(w[k + 4]), "r"(w[k + 5]), "r"(w[k + 6]),
+                         "r"(w[k + 7])
+                         : "memory");
+    } else {
+#pragma unroll
+        for (int k = 0; k < 16; k += 4)
+            *reinterpret_cast<uint4 *>(p + 2 * k) = make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
+    }
 }
 
 struct PrefillArgs {
     AttnArgs a;
     int run;         // consecutive tokens of a tile that lie on one page wherever they start: gcd(page_size, 128)
     int tile_tokens; // tokens of a query tile: 128 / group
+    int item_cost;   // in key tiles
 };
 
-// 2 CL query tiles of one cache head, two for each CTA of a cluster: tokens tok0 .. tok0 + tokens - 1 of request r,
-// tile_tokens to a tile; row y of a tile is token y / group, head y % group of those that share the cache head.  The
-// item's key tiles are [0, us) for the sinks and [ul, ul + n - us).  In the list an item takes kItemCost + n places, the
-// tiles last.
+// Two query tiles of one cache head: tokens tok0 .. tok0 + tokens - 1 of request r, tile_tokens to a tile; row y of a tile is token y / group, head y % group of those that share the cache head.  The
+// item's key tiles are [0, us) for the sinks and [ul, ul + n - us).  In the list
+// an item takes item_cost + n places, the tiles last.
 struct Item {
     int r, qt, h;
     long long start;  // of its tiles in the list, the fixed cost behind it
@@ -319,18 +330,19 @@ __device__ __forceinline__ void span_of(const AttnArgs &a, Item &x) {
     x.ul = max(x.lo / kTile, x.us);
     x.n = x.us + max(0, (x.end + kTile - 1) / kTile - x.ul);
 }
-__device__ __forceinline__ void request_of(const AttnArgs &a, Item &x) {
-    const int t0 = min(max(a.row_start[x.r], 0), a.rows), t1 = min(max(a.row_start[x.r + 1], t0), a.rows);
+__device__ __forceinline__ void request_of(const int *row_start, const int *lens, int rows, Item &x) {
+    const int t0 = min(max(row_start[x.r], 0), rows), t1 = min(max(row_start[x.r + 1], t0), rows);
     x.row0 = t0;
     x.all = t1 - t0;
-    x.pos0 = max(a.lens[x.r], 0) - x.all;
+    x.pos0 = max(lens[x.r], 0) - x.all;
 }
-template <int CL> __device__ __forceinline__ int q_tiles(const PrefillArgs &pa, int tokens) {
-    return (tokens + 2 * CL * pa.tile_tokens - 1) / (2 * CL * pa.tile_tokens);
+__device__ __forceinline__ void request_of(const AttnArgs &a, Item &x) { request_of(a.row_start, a.lens, a.rows, x); }
+__device__ __forceinline__ int q_tiles(const PrefillArgs &pa, int tokens) {
+    return (tokens + 2 * pa.tile_tokens - 1) / (2 * pa.tile_tokens);
 }
-template <int CL> __device__ __forceinline__ void q_tile_of(const PrefillArgs &pa, Item &x) {
-    x.tok0 = x.qt * 2 * CL * pa.tile_tokens;
-    x.tokens = min(2 * CL * pa.tile_tokens, x.all - x.tok0);
+__device__ __forceinline__ void q_tile_of(const PrefillArgs &pa, Item &x) {
+    x.tok0 = x.qt * 2 * pa.tile_tokens;
+    x.tokens = min(2 * pa.tile_tokens, x.all - x.tok0);
     x.p_min = x.pos0 + x.tok0;
     x.p_max = x.p_min + x.tokens - 1;
     span_of(pa.a, x);
@@ -356,20 +368,22 @@ __device__ __forceinline__ Visit visit_of(const PrefillArgs &pa, const Item &x, 
     if (v.last >= v.us && v.last < v.skip) v.last = v.us - 1;
     return v;
 }
-__device__ __forceinline__ long long cost_of(const Item &x) { return x.n ? x.n + kItemCost : 0; }
-template <int CL> __device__ __forceinline__ void next_item(const PrefillArgs &pa, Item &x) {
-    x.start += x.n + kItemCost;
+__device__ __forceinline__ long long cost_of(const PrefillArgs &pa, const Item &x) {
+    return x.n ? x.n + pa.item_cost : 0;
+}
+__device__ __forceinline__ void next_item(const PrefillArgs &pa, Item &x) {
+    x.start += x.n + pa.item_cost;
     if (++x.h < pa.a.kv_heads) return;
     x.h = 0;
     do {
-        if (++x.qt >= q_tiles<CL>(pa, x.all)) {
+        if (++x.qt >= q_tiles(pa, x.all)) {
             do {
                 if (++x.r >= pa.a.R) return;  // never reached: the walk ends within the list
                 request_of(pa.a, x);
             } while (x.all == 0);
             x.qt = 0;
         }
-        q_tile_of<CL>(pa, x);
+        q_tile_of(pa, x);
     } while (x.n == 0);
 }
 
@@ -409,7 +423,7 @@ __device__ __noinline__ void add_nonfinite(const AttnArgs &a, const Item it, int
     }
 }
 
-template <int D, bool Q8, int CL>
+template <int D, bool Q8>
 __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
     prefill_kernel(const __grid_constant__ PrefillArgs pa, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                    const __grid_constant__ CUtensorMap qmap) {
@@ -419,14 +433,12 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
     Control<D, Q8> &ctl = *reinterpret_cast<Control<D, Q8> *>(smem + C::kCtl);
     volatile int *abort = &ctl.abort;
     const int tid = threadIdx.x, lane = tid & 31, warp = (int)uniform(tid >> 5);
-    const int rank = CL == 1 ? 0 : (int)(blockIdx.x % CL), group_id = blockIdx.x / CL;  // in its cluster; the cluster
-
     if (tid == 0) {
         for (int i = 0; i < C::kSlots; ++i) {
             bar_init(&ctl.full[i], 1);
             bar_init(&ctl.ready[i], C::kHelpers);
-            bar_init(&ctl.empty[i], CL);  // every CTA that the copies go to
         }
+        for (int i = 0; i < 8; ++i) bar_init(&ctl.step[i], 1);
         for (int i = 0; i < C::kRawSlots; ++i) {
             bar_init(&ctl.raw_full[i], 1);
             bar_init(&ctl.raw_empty[i], C::kHelpers);
@@ -460,12 +472,18 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
     constexpr int T = C::kThreads;
     long long total = 0, b0 = 0, b1 = 0, span = 1;
     {
+        int *starts = qsum + a.R + 1, *lens = starts + a.R + 1;  // copies: what follows looks at them over and over
+        for (int r = tid; r <= a.R; r += T) {
+            starts[r] = a.row_start[r];
+            if (r < a.R) lens[r] = a.lens[r];
+        }
+        __syncthreads();
         const int each = (a.R + T - 1) / T, ra = min(a.R, tid * each), rb = min(a.R, ra + each);
         Item x;
         int mine = 0;
         for (x.r = ra; x.r < rb; ++x.r) {
-            request_of(a, x);
-            mine += q_tiles<CL>(pa, x.all);
+            request_of(starts, lens, a.rows, x);
+            mine += q_tiles(pa, x.all);
         }
         int upto = mine;
 #pragma unroll
@@ -481,9 +499,9 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
             tiles += (int)ctl.scan[w];
         }
         for (x.r = ra; x.r < rb; ++x.r) {
-            request_of(a, x);
+            request_of(starts, lens, a.rows, x);
             qsum[x.r] = before;
-            before += q_tiles<CL>(pa, x.all);
+            before += q_tiles(pa, x.all);
         }
         if (tid == 0) qsum[a.R] = tiles;
         __syncthreads();
@@ -498,12 +516,12 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
             }
             x.r = lo;
             x.qt = q - qsum[lo];
-            request_of(a, x);
-            q_tile_of<CL>(pa, x);
+            request_of(starts, lens, a.rows, x);
+            q_tile_of(pa, x);
         };
         for (int q = qa; q < qb; ++q) {
             seek(q);
-            keys += cost_of(x);
+            keys += cost_of(pa, x);
         }
         long long sum = keys;
 #pragma unroll
@@ -520,14 +538,14 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
             total += ctl.scan[w];
         }
         total *= a.kv_heads;
-        span = max((total + gridDim.x / CL - 1) / (gridDim.x / CL), (long long)kMinSpan);
-        b0 = span * group_id;
+        span = max((total + gridDim.x - 1) / gridDim.x, 4ll + C::kItemCost);
+        b0 = span * blockIdx.x;
         b1 = min(total, b0 + span);
         if (b0 < b1 && ahead * a.kv_heads <= b0 && b0 < (ahead + keys) * a.kv_heads) {
             for (int q = qa;; ++q) {  // exactly one thread holds unit b0
                 seek(q);
-                if (b0 < (ahead + cost_of(x)) * a.kv_heads) break;
-                ahead += cost_of(x);
+                if (b0 < (ahead + cost_of(pa, x)) * a.kv_heads) break;
+                ahead += cost_of(pa, x);
             }
             ctl.first_r = x.r;
             ctl.first_qt = x.qt;
@@ -537,7 +555,6 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
     fence_before();
     fence_async();
     __syncthreads();  // also: qsum is read, the operands may land over it
-    if (CL > 1) cluster_sync();  // in every CTA of the cluster, its barriers set up
     fence_after();
     const uint32_t tmem = uniform(ctl.tmem);
     const bool work = b0 < b1;
@@ -546,9 +563,9 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
         it.r = ctl.first_r;
         it.qt = ctl.first_qt;
         request_of(a, it);
-        q_tile_of<CL>(pa, it);
-        it.h = (int)((b0 - ctl.first_start) / cost_of(it));
-        it.start = ctl.first_start + it.h * cost_of(it) + kItemCost;
+        q_tile_of(pa, it);
+        it.h = (int)((b0 - ctl.first_start) / cost_of(pa, it));
+        it.start = ctl.first_start + it.h * cost_of(pa, it) + pa.item_cost;
     }
     // An item's tiles [i0, i1) that fall into this span; none of the last item's when only its fixed cost does.
     int i0 = 0, i1 = 0;
@@ -561,12 +578,22 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
     auto advance = [&]() {
         more = it.start + it.n < b1;
         if (more) {
-            next_item<CL>(pa, it);
+            next_item(pa, it);
             segment();
             more = i1 > 0;
         }
     };
 
+    // Who fills the operand ring waits for the step that used a slot's last contents: key tile i is used in step i - i0 of
+    // its segment, its values in the next.  Lane s remembers slot s's step.
+    unsigned steps = 0, last_step = 0;
+    auto slot_free = [&](unsigned s) {
+        const unsigned n = __shfl_sync(0xffffffffu, last_step, s);
+        return warp_wait(&ctl.step[n & 7], (n >> 3) & 1, abort);
+    };
+    auto slot_used = [&](unsigned s, unsigned step) {
+        if (lane == (int)s) last_step = step;
+    };
     if (warp == kLoadWarp) {
         // ---- keys and values: lane i requests run i of each tile ----
         const int runs = kTile / pa.run, per = pa.run / 16;
@@ -578,13 +605,12 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
             ++seg;
             if (lane == 0) {  // Q: boxes of 64 values, the cache head's heads, a tile's tokens
                 uint64_t *bar = Q8 ? &ctl.q_raw : &ctl.q_full;
-                const int mine = it.tokens - rank * 2 * pa.tile_tokens;  // this CTA's tokens
-                const int nx = mine > pa.tile_tokens ? 2 : mine > 0 ? 1 : 0;
+                const int nx = it.tokens > pa.tile_tokens ? 2 : 1;
                 bar_arrive_tx(bar, (unsigned)(nx * C::kSub * 128 * a.group * pa.tile_tokens));
                 for (int x = 0; x < nx; ++x)
                     for (int sub = 0; sub < C::kSub; ++sub)
                         tma3(saddr(smem) + x * C::kOp + sub * kTile * 128, &qmap, 64 * sub, it.h * a.group,
-                             it.row0 + it.tok0 + (2 * rank + x) * pa.tile_tokens, bar);
+                             it.row0 + it.tok0 + x * pa.tile_tokens, bar);
             }
             __syncwarp();
             const int *row = a.table + (size_t)it.r * a.pitch;
@@ -611,28 +637,25 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                     const unsigned slots = Q8 ? C::kRawSlots : C::kSlots;
                     const unsigned s = cnt % slots, turn = cnt / slots;
                     uint64_t *full = Q8 ? &ctl.raw_full[s] : &ctl.full[s];
-                    if (cnt >= slots && !warp_wait(Q8 ? &ctl.raw_empty[s] : &ctl.empty[s], (turn - 1) & 1, abort)) {
-                        ok = false;
-                        break;
+                    if (cnt >= slots) {
+                        if (Q8) ok = warp_wait(&ctl.raw_empty[s], (turn - 1) & 1, abort);
+                        else ok = slot_free(s);
+                        if (!ok) break;
                     }
+                    if (!Q8) slot_used(s, steps + (i - i0) + kv);
                     if (lane == 0) {
                         if (kv == 0) ctl.pages[(cnt >> 1) & 7] = groups;
                         const unsigned bytes = __popc(groups) * 16 * (Q8 ? D + D / 32 * 4 : 2 * D);
                         bar_arrive_tx(full, bytes);
                     }
                     __syncwarp();
-                    // each CTA of the cluster requests its share of the runs, for all of them
-                    if (there && (CL == 1 || lane * CL / runs == rank)) {
+                    if (there) {
                         if (!Q8) {
                             const uint32_t dst = saddr(smem + C::kRing + s * C::kOp) + lane * pa.run * 128;
 #pragma unroll
                             for (int sub = 0; sub < C::kSub; ++sub)
-                                if (CL == 1)
-                                    tma3(dst + sub * kTile * 128, kv ? &vmap : &kmap, 64 * sub,
-                                         it.h * a.page_size + myoff, mypage, full);
-                                else
-                                    tma3_multicast(dst + sub * kTile * 128, kv ? &vmap : &kmap, 64 * sub,
-                                                   it.h * a.page_size + myoff, mypage, full, (1u << CL) - 1u);
+                                tma3(dst + sub * kTile * 128, kv ? &vmap : &kmap, 64 * sub, it.h * a.page_size + myoff,
+                                     mypage, full);
                         } else {
                             const long long at = (long long)mypage * a.page_stride +
                                                  ((long long)it.h * a.page_size + myoff) * D;
@@ -645,6 +668,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                     }
                 }
             }
+            steps += i1 - i0 + 1;
         }
         if (!ok) {  // the copies in flight land before the shared memory goes
             const unsigned slots = Q8 ? C::kRawSlots : C::kSlots;
@@ -671,35 +695,31 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                                   ((kTile >> 4) << 24);
         const uint32_t q_desc = desc128_low(saddr(smem), 16), k_desc = desc128_low(saddr(smem + C::kRing), 16);
         const uint32_t v_desc = desc128_low(saddr(smem + C::kRing), kTile * 128);
-        unsigned slot = 0, phase = 0, seg = 0, pcnt[2] = {0, 0};  // of the ring: the next use
+        unsigned slot = 0, phase = 0, seg = 0, steps = 0, pcnt[2] = {0, 0};  // slot, phase: of the ring's next use
         bool ok = true;
-        auto release = [&](unsigned slot) {  // the slot is free once the MMAs so far are done
-            if (CL == 1) commit(&ctl.empty[slot]);
-            else commit_multicast(&ctl.empty[slot], (1u << CL) - 1u);
-        };
         for (; more; advance()) {
-            const Visit vis[2] = {visit_of(pa, it, 2 * rank, i0, i1), visit_of(pa, it, 2 * rank + 1, i0, i1)};
+            const Visit vis[2] = {visit_of(pa, it, 0, i0, i1), visit_of(pa, it, 1, i0, i1)};
             if (!(ok = warp_wait(&ctl.q_full, seg & 1, abort))) break;
             for (int i = i0 - 1; i < i1 && ok; ++i) {
                 const bool has_v = i >= i0, has_k = i + 1 < i1;
-                unsigned sk = 0, sv = 0;
-                if (has_v) {
-                    sv = slot;
-                    if (!(ok = warp_wait(&ctl.ready[sv], phase, abort))) break;
-                    if (++slot == C::kSlots) { slot = 0; phase ^= 1; }
+                const unsigned sv = uniform(slot), vphase = phase;
+                if (has_v && ++slot == C::kSlots) { slot = 0; phase ^= 1; }
+                const unsigned sk = has_v ? (sv + 1 == C::kSlots ? 0 : sv + 1) : sv, kphase = phase;
+                if (has_k && ++slot == C::kSlots) { slot = 0; phase ^= 1; }
+                uint64_t *const vbar = &ctl.ready[sv], *const kbar = Q8 ? &ctl.ready[sk] : &ctl.full[sk];
+                // values, keys and tile A's weights in one look where all are wanted
+                const bool all = has_v && has_k && vis[0](i);
+                if (!all || !look3(vbar, vphase, kbar, kphase, &ctl.p_ready[0], pcnt[0] & 1)) {
+                    if (has_v && !(ok = warp_wait(vbar, vphase, abort))) break;
+                    if (has_k && !(ok = warp_wait(kbar, kphase, abort))) break;
+                    if (has_v && vis[0](i) && !(ok = warp_wait(&ctl.p_ready[0], pcnt[0] & 1, abort))) break;
                 }
-                if (has_k) {
-                    sk = slot;
-                    if (!(ok = warp_wait(Q8 ? &ctl.ready[sk] : &ctl.full[sk], phase, abort))) break;
-                    if (++slot == C::kSlots) { slot = 0; phase ^= 1; }
-                }
-                sv = uniform(sv);
-                sk = uniform(sk);
+                if (has_v && vis[0](i)) ++pcnt[0];
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     const bool do_o = has_v && vis[x](i), do_s = has_k && vis[x](i + 1);
                     const uint32_t more_o = i > vis[x].first;
-                    if (do_o && !(ok = warp_wait(&ctl.p_ready[x], pcnt[x]++ & 1, abort))) break;
+                    if (x == 1 && do_o && !(ok = warp_wait(&ctl.p_ready[1], pcnt[1]++ & 1, abort))) break;
                     fence_after();
                     if (elect()) {
                         if (do_o) {
@@ -720,13 +740,13 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                             commit(&ctl.s_full[x]);
                         }
                         if (x == 1) {
-                            if (has_v) release(sv);
-                            if (has_k) release(sk);
+                            commit(&ctl.step[steps & 7]);
                             if (i + 2 == i1) commit(&ctl.q_empty);
                         }
                     }
                     __syncwarp();
                 }
+                ++steps;
             }
             if (!ok) break;
             ++seg;
@@ -815,7 +835,8 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                     // Q8_0: codes and scales to fp16
                     const unsigned rs = cnt % (C::kRawSlots ? C::kRawSlots : 1);
                     const unsigned rpar = (cnt / (C::kRawSlots ? C::kRawSlots : 1)) & 1;
-                    if (cnt >= (unsigned)C::kSlots && !(ok = warp_wait(&ctl.empty[s], par ^ 1, abort))) break;
+                    if (cnt >= (unsigned)C::kSlots && !(ok = slot_free(s))) break;
+                    slot_used(s, steps + (i - i0) + kv);
                     if (!(ok = warp_wait(&ctl.raw_full[rs], rpar, abort))) break;
                     const unsigned char *raw = smem + C::kRawAt + rs * C::kRaw;
                     const float *scl = reinterpret_cast<const float *>(raw + kTile * D);
@@ -880,6 +901,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                     }
                 }
             }
+            steps += i1 - i0 + 1;
             ++seg;
         }
         __syncwarp();
@@ -887,7 +909,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
         // ---- softmax: thread = row of tile x ----
         const int x = warp >> 2, quarter = warp & 3;
         const int y = quarter * 32 + lane, rx = x * kTile + y;
-        const int tok = (2 * rank + x) * pa.tile_tokens + y / a.group, gh = y % a.group;  // of this row: the item's token, the head
+        const int tok = x * pa.tile_tokens + y / a.group, gh = y % a.group;  // of this row: the item's token, the head
         const bool whole_row = y < pa.tile_tokens * a.group;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         const uint32_t ts = tmem + lanes + x * kTile, to = tmem + lanes + kColO + x * 128;
@@ -900,11 +922,10 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
         bool ok = true;
         for (; more; advance()) {
             if (!ok) break;
-            const Visit vis = visit_of(pa, it, 2 * rank + x, i0, i1);
+            const Visit vis = visit_of(pa, it, x, i0, i1);
             const bool active = vis.first <= vis.last;
-            const bool mine = it.tokens > 2 * rank * pa.tile_tokens;  // this CTA has rows of the item
             const bool row_live = whole_row && tok < it.tokens;
-            const int p = it.p_min + tok, p0 = it.p_min + (2 * rank + x) * pa.tile_tokens;  // of the row, the tile
+            const int p = it.p_min + tok, p0 = it.p_min + x * pa.tile_tokens;  // of the row, the tile
             float M = row_live ? -INFINITY : 0.0f, l = 0.0f;  // rows beyond the item's ask for nothing
             if (active) {
                 float sc = sc0;
@@ -1028,6 +1049,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
             // ---- the segment's end ----
             const long long last_unit = it.start + it.n - 1;
             const int c0 = (int)(it.start / span), c1 = (int)(last_unit / span);
+            const bool wide = (((uintptr_t)a.out | (uintptr_t)(2 * a.ldo)) & 31) == 0;
             const bool poison = *(volatile int *)&ctl.poison != 0;
             float *base = reinterpret_cast<float *>(a.work + kPrefillPartAt);
             uint16_t *orow = a.out + (size_t)(it.row0 + it.tok0 + (row_live ? tok : 0)) * a.ldo + (it.h * a.group + gh) * D;
@@ -1051,13 +1073,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                         for (int k = 0; k < 32; ++k) o[k] = extra[k];
                     }
                     if (c0 == c1) {
-                        if (row_live) {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                *reinterpret_cast<uint4 *>(orow + cc + 8 * k) =
-                                    make_uint4(bf16x2(o[8 * k], o[8 * k + 1]), bf16x2(o[8 * k + 2], o[8 * k + 3]),
-                                               bf16x2(o[8 * k + 4], o[8 * k + 5]), bf16x2(o[8 * k + 6], o[8 * k + 7]));
-                        }
+                        if (row_live) store_row(orow + cc, o, wide);
                     } else {
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
@@ -1066,14 +1082,14 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                     }
                 }
             }
-            if (c0 != c1 && mine) *reinterpret_cast<float2 *>(part + kRows * 128 + 2 * rx) = make_float2(M, l);
+            if (c0 != c1) *reinterpret_cast<float2 *>(part + kRows * 128 + 2 * rx) = make_float2(M, l);
             fence_before();
-            if (c0 != c1 && mine && ok) {
+            if (c0 != c1 && ok) {
                 // ---- shared with other CTAs: the last to arrive adds the parts in span order ----
                 __threadfence();
                 bar_arrive(&ctl.joined);
                 if (tid == 0 && bar_wait(&ctl.joined, shared & 1, abort)) {
-                    int *count = reinterpret_cast<int *>(a.work + kPrefillCounterAt) + c0 * CL + rank;
+                    int *count = reinterpret_cast<int *>(a.work + kPrefillCounterAt) + c0;
                     __threadfence();
                     const int seen = atomicAdd(count, 1);
                     ctl.last = seen == c1 - c0;
@@ -1084,42 +1100,39 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                 ok = warp_wait(&ctl.decided, shared++ & 1, abort);
                 if (ok && *(volatile int *)&ctl.last && row_live) {
                     __threadfence();
-                    float m2 = -INFINITY, l2 = 0.0f;
-                    for (int z = c0; z <= c1; ++z)
-                        m2 = fmaxf(m2, __ldcg(base + ((long long)(z * CL + rank) * 2 + (z == c0)) * kPrefillPartFloats + kRows * 128 + 2 * rx));
-                    for (int z = c0; z <= c1; ++z) {
-                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(
-                            base + ((long long)(z * CL + rank) * 2 + (z == c0)) * kPrefillPartFloats + kRows * 128 + 2 * rx));
-                        l2 += ml.y * (ml.x == m2 ? 1.0f : ex2(ml.x - m2));
-                    }
-                    const float inv = l2 == 0.0f ? 0.0f : 1.0f / l2;
+                    constexpr int J = Q8 ? 32 : 64;  // columns at a time: J / 4 loads in flight, J sums
 #pragma unroll 1
-                    for (int cc = 0; cc < D / 4; cc += 8) {  // 32 values at a time: eight loads in flight
-                        float4 o[8];
+                    for (int cc = 0; cc < D; cc += J) {
+                        float o[J], m2 = -INFINITY, l2 = 0.0f;
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 2
+                        for (int k = 0; k < J; ++k) o[k] = 0.0f;
+#pragma unroll 1
                         for (int z = c0; z <= c1; ++z) {
-                            const float *from = base + ((long long)(z * CL + rank) * 2 + (z == c0)) * kPrefillPartFloats;
-                            const float m1 = __ldcg(from + kRows * 128 + 2 * rx);
-                            const bool none = m1 == -INFINITY;  // a part that saw nothing has no O
-                            const float f = m1 == m2 ? 1.0f : ex2(m1 - m2);
+                            const float *from = base + ((long long)z * 2 + (z == c0)) * kPrefillPartFloats;
+                            const float2 ml = __ldcg(reinterpret_cast<const float2 *>(from + kRows * 128 + 2 * rx));
+                            float4 v[J / 4];
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                const float4 v = none ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
-                                                      : __ldcg(reinterpret_cast<const float4 *>(from + ((cc + k) * kRows + rx) * 4));
-                                o[k].x = fmaf(v.x, f, o[k].x);
-                                o[k].y = fmaf(v.y, f, o[k].y);
-                                o[k].z = fmaf(v.z, f, o[k].z);
-                                o[k].w = fmaf(v.w, f, o[k].w);
+                            for (int k = 0; k < J / 4; ++k)
+                                v[k] = __ldcg(reinterpret_cast<const float4 *>(from + ((cc / 4 + k) * kRows + rx) * 4));
+                            const float now = fmaxf(m2, ml.x);
+                            const float fa = m2 == now ? 1.0f : ex2(m2 - now), fb = ml.x == now ? 1.0f : ex2(ml.x - now);
+                            m2 = now;
+                            l2 = l2 * fa + ml.y * fb;
+                            const bool none = ml.x == -INFINITY;  // a part that saw nothing has no O
+#pragma unroll
+                            for (int k = 0; k < J / 4; ++k) {
+                                o[4 * k] = fmaf(none ? 0.0f : v[k].x, fb, o[4 * k] * fa);
+                                o[4 * k + 1] = fmaf(none ? 0.0f : v[k].y, fb, o[4 * k + 1] * fa);
+                                o[4 * k + 2] = fmaf(none ? 0.0f : v[k].z, fb, o[4 * k + 2] * fa);
+                                o[4 * k + 3] = fmaf(none ? 0.0f : v[k].w, fb, o[4 * k + 3] * fa);
                             }
                         }
+                        const float inv = l2 == 0.0f ? 0.0f : 1.0f / l2;
 #pragma unroll
-                        for (int k = 0; k < 8; k += 2)
-                            *reinterpret_cast<uint4 *>(orow + 4 * (cc + k)) =
-                                make_uint4(bf16x2(o[k].x * inv, o[k].y * inv), bf16x2(o[k].z * inv, o[k].w * inv),
-                                           bf16x2(o[k + 1].x * inv, o[k + 1].y * inv),
-                                           bf16x2(o[k + 1].z * inv, o[k + 1].w * inv));
+                        for (int k = 0; k < J; ++k) o[k] *= inv;
+#pragma unroll
+                        for (int k = 0; k < J; k += 32)
+                            store_row(orow + cc + k, *reinterpret_cast<const float(*)[32]>(o + k), wide);
                     }
                 }
             }
@@ -1137,7 +1150,6 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
     }
     __syncthreads();
     fence_after();
-    if (CL > 1) cluster_sync();  // nothing of the others' copies or commits is on its way here any more
     if (warp == 0)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemColumns) : "memory");
     // ---- rows that see nothing: padding, and rows before the first key ----
@@ -1183,13 +1195,12 @@ bool encode_boxes(CUtensorMap *map, const void *p, const cuuint64_t (&dims)[3], 
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool Q8, int CL> cudaError_t launch_one(const AttnArgs &a, int sms, cudaStream_t stream) {
+template <int D, bool Q8> cudaError_t launch_one(const AttnArgs &a, int sms, cudaStream_t stream) {
     using C = Cfg<D, Q8>;
-    const auto kernel = prefill_kernel<D, Q8, CL>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    cudaError_t e = cudaFuncSetAttribute(prefill_kernel<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    PrefillArgs pa = {a, 16, kTile / a.group};
-    while (pa.run < kTile / CL && a.page_size % (2 * pa.run) == 0) pa.run *= 2;
+    PrefillArgs pa = {a, 16, kTile / a.group, C::kItemCost};
+    while (pa.run < kTile && a.page_size % (2 * pa.run) == 0) pa.run *= 2;
     // K and V as [pages][heads * page_size][dim], boxes of `run` tokens; Q as [rows][heads][dim], boxes of a tile's
     // tokens and their heads.
     CUtensorMap kmap = {}, vmap = {}, qmap = {};
@@ -1199,36 +1210,8 @@ template <int D, bool Q8, int CL> cudaError_t launch_one(const AttnArgs &a, int 
     if (!encode_boxes(&qmap, a.q, qd, qs, a.group, pa.tile_tokens) ||
         (!Q8 && (!encode_boxes(&kmap, a.k, kd, ks, pa.run, 1) || !encode_boxes(&vmap, a.v, kd, ks, pa.run, 1))))
         return cudaErrorNotSupported;
-    cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(C::kThreads, 1, 1);
-    cfg.dynamicSmemBytes = C::kSmem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = CL;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = CL > 1 ? 2 : 1;
-    cfg.gridDim = dim3((unsigned)sms, 1, 1);
-    if (CL > 1) {  // as many clusters as are resident at once (asked once a device)
-        static std::atomic<int> cache[64];
-        int dev = 0, n = 0;
-        e = cudaGetDevice(&dev);
-        if (e != cudaSuccess) return e;
-        if (dev < 64) n = cache[dev].load(std::memory_order_relaxed);
-        if (n == 0) {
-            cfg.gridDim = dim3(CL, 1, 1);
-            e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
-            if (e != cudaSuccess) return e;
-            if (n < 1) return cudaErrorNotSupported;
-            if (n > sms / CL) n = sms / CL;
-            if (dev < 64) cache[dev].store(n, std::memory_order_relaxed);
-        }
-        cfg.gridDim = dim3((unsigned)(n * CL), 1, 1);
-    }
-    return cudaLaunchKernelEx(&cfg, kernel, pa, kmap, vmap, qmap);
+    return kv_launch(prefill_kernel<D, Q8>, dim3((unsigned)sms, 1, 1), C::kThreads, C::kSmem, stream, pa, kmap, vmap,
+                     qmap);
 }
 
 }  // namespace
@@ -1245,12 +1228,8 @@ cudaError_t launch_attn_prefill(const AttnArgs &a, int dim, bool q8, cudaStream_
     cudaError_t e = sm_count_of_device(&sms);
     if (e != cudaSuccess) return e;
     if (sms > kAttnMaxCtas) sms = kAttnMaxCtas;
-    if (q8) return dim == 128 ? launch_one<128, true, 1>(a, sms, stream) : launch_one<64, true, 1>(a, sms, stream);
-    // Two CTAs share each key and value tile (each requests half of it for both) where requests fill their four query
-    // tiles on average.
-    if ((long long)a.rows * a.group >= 4ll * kTile * a.R)
-        return dim == 128 ? launch_one<128, false, 2>(a, sms, stream) : launch_one<64, false, 2>(a, sms, stream);
-    return dim == 128 ? launch_one<128, false, 1>(a, sms, stream) : launch_one<64, false, 1>(a, sms, stream);
+    if (dim == 128) return q8 ? launch_one<128, true>(a, sms, stream) : launch_one<128, false>(a, sms, stream);
+    return q8 ? launch_one<64, true>(a, sms, stream) : launch_one<64, false>(a, sms, stream);
 }
 
 }  // namespace q8
