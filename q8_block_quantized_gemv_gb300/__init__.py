@@ -130,6 +130,22 @@ def _stream_handle(stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+_raw_stream = None
+
+
+def _stream_of(stream, device):
+    """The handle of ``stream``, or of the device's current stream: torch's own look-up where it has it, a tenth of the
+    time that making a Stream object for it takes."""
+    global _raw_stream
+    if stream is not None:
+        return _stream_handle(stream)
+    if _raw_stream is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda index: torch.cuda.current_stream(index).cuda_stream)
+    return _raw_stream(device.index)
+
+
 def tiled_n(N: int) -> int:
     return lib().q8_tiled_n(N)
 
@@ -515,10 +531,11 @@ def _ints(name, t, n=None):
 
 def _table_of(table, R):
     import torch
-    if not table.is_cuda or table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != R or \
-            (table.shape[1] > 1 and table.stride(1) != 1):
+    shape = table.shape
+    if not table.is_cuda or table.dtype != torch.int32 or len(shape) != 2 or shape[0] != R or \
+            (shape[1] > 1 and table.stride(1) != 1):
         raise ValueError(f"the block table must be an int32 CUDA tensor [{R}, width] with unit column stride")
-    return table.data_ptr(), table.shape[1], table.stride(0) if R > 1 else table.shape[1]
+    return table.data_ptr(), shape[1], table.stride(0) if R > 1 else shape[1]
 
 
 def kv_slots(cached, fresh, table, free_pages, page_size: int, rows: int, head=None, stream=None, out=None):
@@ -530,19 +547,27 @@ def kv_slots(cached, fresh, table, free_pages, page_size: int, rows: int, head=N
     R = cached.numel()
     c, f = _ints("cached", cached), _ints("fresh", fresh, R)
     t, width, pitch = _table_of(table, R)
+    dev = cached.device
     if out is None:
-        dev = cached.device
-        new = torch.empty((2 * R + 2 + rows,), dtype=torch.int32, device=dev)
-        out = {"table": table, "lens": new[:R], "row_start": new[R:2 * R + 1], "positions": new[2 * R + 2:],
-               "slots": torch.empty((rows,), dtype=torch.int64, device=dev), "head": new[2 * R + 1:2 * R + 2]}
-    elif out["slots"].dtype != torch.int64 or out["slots"].numel() != rows or not out["slots"].is_contiguous() \
-            or not out["slots"].is_cuda or out["table"] is not table:
-        raise ValueError("out must hold this table and contiguous CUDA tensors of the sizes kv_slots returns")
-    _check(lib().q8_kv_slots(c, f, R, page_size, _ints("free_pages", free_pages), free_pages.numel(),
-                             None if head is None else _ints("head", head, 1), t, width, pitch, rows,
-                             _ints("lens", out["lens"], R), _ints("row_start", out["row_start"], R + 1),
-                             _ints("positions", out["positions"], rows), out["slots"].data_ptr(),
-                             _ints("head", out["head"], 1), _stream_handle(stream)), "q8_kv_slots")
+        i32 = torch.int32  # tensors of their own: cheaper than views of one
+        lens, starts = torch.empty(R, dtype=i32, device=dev), torch.empty(R + 1, dtype=i32, device=dev)
+        positions, next_head = torch.empty(rows, dtype=i32, device=dev), torch.empty(1, dtype=i32, device=dev)
+        slots = torch.empty(rows, dtype=torch.int64, device=dev)
+        out = {"table": table, "lens": lens, "row_start": starts, "positions": positions, "slots": slots,
+               "head": next_head}
+        lp, sp, pp, hp = lens.data_ptr(), starts.data_ptr(), positions.data_ptr(), next_head.data_ptr()
+    else:
+        slots = out["slots"]
+        if slots.dtype != torch.int64 or slots.numel() != rows or not slots.is_contiguous() or not slots.is_cuda \
+                or out["table"] is not table:
+            raise ValueError("out must hold this table and contiguous CUDA tensors of the sizes kv_slots returns")
+        lp, sp = _ints("lens", out["lens"], R), _ints("row_start", out["row_start"], R + 1)
+        hp, pp = _ints("head", out["head"], 1), _ints("positions", out["positions"], rows)
+    st = lib().q8_kv_slots(c, f, R, page_size, _ints("free_pages", free_pages), free_pages.numel(),
+                           None if head is None else _ints("head", head, 1), t, width, pitch, rows, lp, sp, pp,
+                           slots.data_ptr(), hp, _stream_of(stream, dev))
+    if st:
+        raise Q8Error(st, "q8_kv_slots")
     return out
 
 
@@ -583,9 +608,10 @@ def rope_table(positions: int, rotary_dim: int, base: float = 10000.0, scaling=N
 
 
 def _rows2(name, x, dtype, cols):
-    if not x.is_cuda or x.dtype != dtype or x.dim() != 2 or x.shape[1] < cols or x.stride(1) != 1:
+    shape = x.shape
+    if not x.is_cuda or x.dtype != dtype or len(shape) != 2 or shape[1] < cols or x.stride(1) != 1:
         raise ValueError(f"{name} must be a 2-D {dtype} CUDA tensor of at least {cols} columns, unit column stride")
-    return x.data_ptr(), x.stride(0) if x.shape[0] > 1 else x.shape[1]
+    return x.data_ptr(), x.stride(0) if shape[0] > 1 else shape[1]
 
 
 def rope_append(q, k, v, cache: KVCache, positions, slots, table=None, q_heads: int | None = None,
@@ -595,65 +621,77 @@ def rope_append(q, k, v, cache: KVCache, positions, slots, table=None, q_heads: 
     slots int64 [rows] (:func:`kv_slots`); ``table``: :func:`rope_table`, its width the rotated part of a head (None:
     no rotation).  Returns q, bf16 [rows, q_heads * dim]."""
     import torch
-    dim = cache.dim
+    dim, f32 = cache.dim, torch.float32
     if q_heads is None:
         q_heads = q.shape[1] // dim
-    rows, n = q.shape[0], q_heads * dim
-    qp, ldq = _rows2("q", q, torch.float32, max(n, 1))
-    kp, ldk = _rows2("k", k, torch.float32, cache.heads * dim)
-    vp, ldv = _rows2("v", v, torch.float32, cache.heads * dim)
+    rows, n, m = q.shape[0], q_heads * dim, cache.heads * dim
+    qp, ldq = _rows2("q", q, f32, max(n, 1))
+    kp, ldk = _rows2("k", k, f32, m)
+    vp, ldv = _rows2("v", v, f32, m)
     if k.shape[0] != rows or v.shape[0] != rows:
         raise ValueError("q, k and v must have the same rows")
     if not slots.is_cuda or slots.dtype != torch.int64 or slots.numel() != rows or not slots.is_contiguous():
         raise ValueError("slots must be a contiguous int64 CUDA tensor of one value a row")
     pos = _ints("positions", positions, rows)
     for g in (q_gamma, k_gamma):
-        if g is not None and (not g.is_cuda or g.dtype != torch.float32 or g.numel() != dim or not g.is_contiguous()):
+        if g is not None and (not g.is_cuda or g.dtype != f32 or g.numel() != dim or not g.is_contiguous()):
             raise ValueError("a gamma must be a contiguous fp32 CUDA tensor of dim values")
-    if table is not None and (not table.is_cuda or table.dtype != torch.float32 or table.dim() != 2
-                              or not table.is_contiguous()):
-        raise ValueError("table must be a contiguous fp32 CUDA tensor [positions, rotary_dim]")
+    tp, limit, rot = None, 0, 0
+    if table is not None:
+        if not table.is_cuda or table.dtype != f32 or table.dim() != 2 or not table.is_contiguous():
+            raise ValueError("table must be a contiguous fp32 CUDA tensor [positions, rotary_dim]")
+        tp, (limit, rot) = table.data_ptr(), table.shape
     if out is None:
         out = torch.empty((rows, n), dtype=torch.bfloat16, device=q.device)
-    elif out.shape[0] != rows:
-        raise ValueError("out must have q's rows")
-    op, ldo = _rows2("out", out, torch.bfloat16, max(n, 1))
+        op, ldo = out.data_ptr(), n
+    else:
+        if out.shape[0] != rows:
+            raise ValueError("out must have q's rows")
+        op, ldo = _rows2("out", out, torch.bfloat16, max(n, 1))
     if rows == 0:
         return out
-    _check(lib().q8_rope_append(qp, ldq, kp, ldk, vp, ldv, None if q_gamma is None else q_gamma.data_ptr(),
-                                None if k_gamma is None else k_gamma.data_ptr(), float(eps),
-                                None if table is None else table.data_ptr(), 0 if table is None else table.shape[0],
-                                0 if table is None else table.shape[1], pos, slots.data_ptr(), op, ldo, cache._ref,
-                                rows, q_heads, FLAG_ROPE_INTERLEAVED if interleaved else 0, _stream_handle(stream)),
-           "q8_rope_append")
+    st = lib().q8_rope_append(qp, ldq, kp, ldk, vp, ldv, None if q_gamma is None else q_gamma.data_ptr(),
+                              None if k_gamma is None else k_gamma.data_ptr(), eps, tp, limit, rot, pos,
+                              slots.data_ptr(), op, ldo, cache._ref, rows, q_heads,
+                              FLAG_ROPE_INTERLEAVED if interleaved else 0, _stream_of(stream, cache.device))
+    if st:
+        raise Q8Error(st, "q8_rope_append")
     return out
+
+
+_workspace_bytes = 0
 
 
 def attn_workspace(device="cuda"):
     """A zeroed workspace for attn_decode and attn_prefill (q8_attn_workspace_bytes); keep one per stream."""
     import torch
-    return torch.zeros((int(lib().q8_attn_workspace_bytes()),), dtype=torch.uint8, device=device)
+    global _workspace_bytes
+    _workspace_bytes = int(lib().q8_attn_workspace_bytes())
+    return torch.zeros((_workspace_bytes,), dtype=torch.uint8, device=device)
 
 
 def _attn(q, cache, R, table, lens, q_heads, scale, out, workspace):
     import torch
+    shape = q.shape
     if q_heads is None:
-        q_heads = q.shape[1] // cache.dim
+        q_heads = shape[1] // cache.dim
     n = q_heads * cache.dim
     qp, ldq = _rows2("q", q, torch.bfloat16, max(n, 1))
     tp, width, pitch = _table_of(table, R)
     if out is None:
-        out = torch.empty((q.shape[0], n), dtype=torch.bfloat16, device=q.device)
-    elif out.shape[0] != q.shape[0]:
-        raise ValueError("out must have q's rows")
-    op, ldo = _rows2("out", out, torch.bfloat16, max(n, 1))
+        out = torch.empty((shape[0], n), dtype=torch.bfloat16, device=q.device)
+        op, ldo = out.data_ptr(), n
+    else:
+        if out.shape[0] != shape[0]:
+            raise ValueError("out must have q's rows")
+        op, ldo = _rows2("out", out, torch.bfloat16, max(n, 1))
     if workspace is None:
         workspace = attn_workspace(q.device)
     elif not workspace.is_cuda or not workspace.is_contiguous() or \
-            workspace.numel() * workspace.element_size() < lib().q8_attn_workspace_bytes():
+            workspace.nbytes < (_workspace_bytes or lib().q8_attn_workspace_bytes()):
         raise ValueError("workspace must come from attn_workspace")
-    scale = float(cache.dim ** -0.5 if scale is None else scale)
-    return (qp, ldq, cache._ref, tp, width, pitch, _ints("lens", lens, R)), (op, ldo), q_heads, scale, out, workspace
+    return (qp, ldq, cache._ref, tp, width, pitch, _ints("lens", lens, R), op, ldo, q_heads,
+            cache.dim ** -0.5 if scale is None else scale, out, workspace)
 
 
 def attn_decode(q, cache: KVCache, table, lens, q_heads: int | None = None, scale: float | None = None,
@@ -664,11 +702,14 @@ def attn_decode(q, cache: KVCache, table, lens, q_heads: int | None = None, scal
     ``workspace``: :func:`attn_workspace`, one per stream (None: allocated and zeroed for this call).  Returns bf16
     [R, q_heads * dim], the output projection's activation."""
     R = q.shape[0]
-    a, o, q_heads, scale, out, workspace = _attn(q, cache, R, table, lens, q_heads, scale, out, workspace)
+    qp, ldq, kv, tp, width, pitch, lp, op, ldo, q_heads, scale, out, workspace = \
+        _attn(q, cache, R, table, lens, q_heads, scale, out, workspace)
     if R == 0:
         return out
-    _check(lib().q8_attn_decode(*a, *o, R, q_heads, scale, window, sinks, workspace.data_ptr(),
-                                _stream_handle(stream)), "q8_attn_decode")
+    st = lib().q8_attn_decode(qp, ldq, kv, tp, width, pitch, lp, op, ldo, R, q_heads, scale, window, sinks,
+                              workspace.data_ptr(), _stream_of(stream, cache.device))
+    if st:
+        raise Q8Error(st, "q8_attn_decode")
     return out
 
 
@@ -677,12 +718,16 @@ def attn_prefill(q, cache: KVCache, table, lens, row_start, q_heads: int | None 
     """Causal attention of a chunk of new tokens over the pages (q8_attn_prefill): rows row_start[r] .. row_start[r+1]
     of q are the last tokens of request r, whose keys are in the cache already; row_start int32 [R + 1], lens int32
     [R].  Rows past row_start[R] get zeros.  Other arguments as :func:`attn_decode`."""
-    R = lens.numel()
-    a, o, q_heads, scale, out, workspace = _attn(q, cache, R, table, lens, q_heads, scale, out, workspace)
-    if q.shape[0] == 0:
+    R, rows = lens.numel(), q.shape[0]
+    qp, ldq, kv, tp, width, pitch, lp, op, ldo, q_heads, scale, out, workspace = \
+        _attn(q, cache, R, table, lens, q_heads, scale, out, workspace)
+    if rows == 0:
         return out
-    _check(lib().q8_attn_prefill(*a, _ints("row_start", row_start, R + 1), *o, q.shape[0], R, q_heads, scale, window,
-                                 sinks, workspace.data_ptr(), _stream_handle(stream)), "q8_attn_prefill")
+    st = lib().q8_attn_prefill(qp, ldq, kv, tp, width, pitch, lp, _ints("row_start", row_start, R + 1), op, ldo, rows,
+                               R, q_heads, scale, window, sinks, workspace.data_ptr(),
+                               _stream_of(stream, cache.device))
+    if st:
+        raise Q8Error(st, "q8_attn_prefill")
     return out
 
 

@@ -26,6 +26,7 @@ namespace {
 
 constexpr int kUnit = 16;  // tokens of a unit; a page holds whole units
 constexpr int kMinSpan = 16;
+constexpr int kWholeUnits = 64;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;  // log2: the running maximum moves when a score passes it by more than this
 
@@ -203,7 +204,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, Q8, NT>::kWarps, 1) attn_decode_ke
     constexpr int NB = D / 32;       // quantized blocks of a head
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ long long s_scan[W + 2];
-    __shared__ int s_first[2];
+    __shared__ int s_first[1];
     __shared__ int s_last;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int tiles = a.kv_heads * tiles_a_head;  // items a request
@@ -214,6 +215,22 @@ __global__ void __launch_bounds__(32 * Cfg<D, Q8, NT>::kWarps, 1) attn_decode_ke
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
+    long long span, b0, b1;  // the CTA's span [b0, b1) of the list
+    Cursor c;                // the item being computed
+    // ---- few short items: one a CTA, nothing to join ----
+    // Splitting an item costs its CTAs a round through memory to hand their parts over, some 3 us; 64 units are 8 a
+    // warp.  (32 heads of one request of 203 tokens: 11.5 us split, 5.2 us whole.)
+    bool whole_items = (long long)a.R * tiles <= gridDim.x;
+    if (whole_items)  // at most a request a thread: a.R <= gridDim.x < the block
+        whole_items = !__syncthreads_or(tid < a.R && seen_of(a, a.lens[tid]).n > kWholeUnits);
+    if (whole_items) {
+        span = 1ll << 40;
+        c.r = min((int)blockIdx.x / tiles, a.R - 1);
+        c.tile = blockIdx.x % tiles;
+        c.start = b0 = 0;
+        c.s = seen_of(a, a.lens[c.r]);
+        b1 = (int)blockIdx.x < a.R * tiles ? c.s.n : 0;
+    } else {
     // ---- the list's length and this CTA's span of it ----
     const int each = (a.R + 32 * W - 1) / (32 * W);
     const int ra = min(a.R, tid * each), rb = min(a.R, ra + each);
@@ -234,8 +251,9 @@ __global__ void __launch_bounds__(32 * Cfg<D, Q8, NT>::kWarps, 1) attn_decode_ke
         total += s_scan[w];
     }
     total *= tiles;
-    const long long span = max((total + gridDim.x - 1) / gridDim.x, (long long)kMinSpan);
-    const long long b0 = span * blockIdx.x, b1 = min(total, b0 + span);
+    span = max((total + gridDim.x - 1) / gridDim.x, (long long)kMinSpan);
+    b0 = span * blockIdx.x;
+    b1 = min(total, b0 + span);
     if (b0 < b1) {
         if (before * tiles <= b0 && b0 < (before + mine) * tiles) {  // exactly one thread: the request of unit b0
             int r = ra;
@@ -248,12 +266,14 @@ __global__ void __launch_bounds__(32 * Cfg<D, Q8, NT>::kWarps, 1) attn_decode_ke
             s_scan[W] = before * tiles;
         }
         __syncthreads();
-        Cursor c;  // the item being computed; p runs ahead of it, filling the ring
         c.r = s_first[0];
         c.s = seen_of(a, a.lens[c.r]);
         c.tile = (int)((b0 - s_scan[W]) / c.s.n);
         c.start = s_scan[W] + (long long)c.tile * c.s.n;
-        Cursor p = c;
+    }
+    }
+    if (b0 < b1) {
+        Cursor p = c;  // runs ahead of c, filling the ring
 
         // ---- the ring: the warp's next unit into stage `slot`; zeros where no token is visible ----
         int todo = b1 - b0 > warp ? (int)((b1 - b0 - warp + W - 1) / W) : 0;  // this warp's units
@@ -720,8 +740,8 @@ __global__ void __launch_bounds__(32 * Cfg<D, Q8, NT>::kWarps, 1) attn_decode_ke
 
 template <int D, bool Q8, int NT> cudaError_t launch_one(const AttnArgs &a, int sms, cudaStream_t stream) {
     using C = Cfg<D, Q8, NT>;
-    cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<D, Q8, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         C::kSmem);
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t e = kv_allow_smem(attn_decode_kernel<D, Q8, NT>, C::kSmem, &allowed);
     if (e != cudaSuccess) return e;
     const int tiles_a_head = (a.group + 8 * NT - 1) / (8 * NT);
     return kv_launch(attn_decode_kernel<D, Q8, NT>, dim3((unsigned)sms, 1, 1), 32 * C::kWarps, C::kSmem, stream, a,

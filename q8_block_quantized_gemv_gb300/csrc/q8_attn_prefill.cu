@@ -1197,7 +1197,8 @@ bool encode_boxes(CUtensorMap *map, const void *p, const cuuint64_t (&dims)[3], 
 
 template <int D, bool Q8> cudaError_t launch_one(const AttnArgs &a, int sms, cudaStream_t stream) {
     using C = Cfg<D, Q8>;
-    cudaError_t e = cudaFuncSetAttribute(prefill_kernel<D, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t e = kv_allow_smem(prefill_kernel<D, Q8>, C::kSmem, &allowed);
     if (e != cudaSuccess) return e;
     PrefillArgs pa = {a, 16, kTile / a.group, C::kItemCost};
     while (pa.run < kTile && a.page_size % (2 * pa.run) == 0) pa.run *= 2;

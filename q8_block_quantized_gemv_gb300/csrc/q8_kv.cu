@@ -110,10 +110,11 @@ __global__ void __launch_bounds__(kSlotThreads) slots_kernel(SlotArgs a) {
 
 // ---- append ---------------------------------------------------------------------------------------------------------
 //
-// One pass over the fp32 outputs of the q/k/v products: 4 bytes read and 2 (bf16) or 1.125 (Q8_0) written a value, a
-// handful of operations each, so memory bounds it once there are enough rows, and latency before that.  A head's dim
-// values sit on dim / 4 lanes, four a lane, so the norm's sum and the amax of 32 values are shuffles and the partner
-// of a half-layout pair is rotary_dim / 8 lanes away.
+// One pass over the fp32 outputs of the q/k/v products: 4 bytes read and 2 (bf16) or 1.125 (Q8_0) written a value, so
+// memory bounds it once there are enough rows, and latency before that -- if a value costs few enough instructions.
+// A lane holds eight values of a head, as two chunks of four: with the half layout a chunk and its partner rotary_dim
+// / 2 on, so that the rotation needs no other lane; otherwise two neighbours.  (Four values a lane and shuffles for the
+// partners took twice the instructions: 82 us for 8191 rows of 32 + 2 x 8 heads, 55 us now.)
 struct AppendArgs {
     const float *q, *k, *v, *qg, *kg, *table;
     const int *positions;
@@ -126,7 +127,8 @@ struct AppendArgs {
     int ldq, ldk, ldv, ldo, max_pos, rot, rows, q_heads, kv_heads, page;
 };
 
-constexpr int kAppendWarps = 8;
+constexpr int kAppendWarps = 4;
+constexpr long long kAppendWide = 1ll << 21;  // values
 
 __device__ __forceinline__ uint2 pack_bf16x4(float4 v) {
     const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
@@ -136,112 +138,199 @@ __device__ __forceinline__ uint2 pack_bf16x4(float4 v) {
     return o;
 }
 
-// D: the head's dim; HALF / pairs; Q8: the cache's type.  A group of D / 4 lanes takes one head of one row.
-template <int D, bool INTERLEAVED, bool Q8>
+// D: the head's dim; PAIRS: neighbours (2i, 2i + 1) turn, not halves; Q8: the cache's type; N: heads of its row a group
+// of D / 8 lanes takes, all requested before the first is used.
+template <int D, bool PAIRS, bool Q8, int N>
 __global__ void __launch_bounds__(32 * kAppendWarps) append_kernel(AppendArgs a) {
-    constexpr int L = D / 4;        // lanes a head
-    constexpr int G = 32 / L;       // heads a warp takes at once
+    constexpr int L = D / 8;   // lanes a head
+    constexpr int G = 32 / L;  // heads a warp takes at once
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31, sub = lane % L, warp = threadIdx.x >> 5;
-    const int t = blockIdx.y;
     const int total = a.q_heads + 2 * a.kv_heads;
-    const int head = (blockIdx.x * kAppendWarps + warp) * G + lane / L;
-    const bool live = head < total;
+    const unsigned per_row = (unsigned)(total + G * N - 1) / (G * N);  // warps a row
+    const unsigned id = blockIdx.x * kAppendWarps + warp;
+    const int t = (int)(id / per_row);
+    if (t >= a.rows) return;
+    const int head0 = (int)(id - t * per_row) * (G * N) + lane / L;  // then every G-th
     const int pos = a.positions[t];
     const long long slot = a.slots[t];
-    const bool is_q = head < a.q_heads, is_k = !is_q && head < a.q_heads + a.kv_heads;
-    const int h = is_q ? head : (is_k ? head - a.q_heads : head - a.q_heads - a.kv_heads);
-    const int d0 = 4 * sub;
-    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (live && pos >= 0) {
-        const float *src = is_q ? a.q + (size_t)t * a.ldq : (is_k ? a.k + (size_t)t * a.ldk : a.v + (size_t)t * a.ldv);
-        x = *reinterpret_cast<const float4 *>(src + (size_t)h * D + d0);
+    // this lane's two chunks of four values: c, a pair's first, turns with d, its second
+    const int p8 = a.rot / 8;  // chunk pairs that turn (halves)
+    const int c = PAIRS ? 2 * sub : (sub < p8 ? sub : 2 * sub), d = PAIRS ? c + 1 : (sub < p8 ? sub + p8 : c + 1);
+    float4 in[N][2];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const int head = head0 + n * G;
+        in[n][0] = in[n][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (head < total && pos >= 0) {
+            const float *src = head < a.q_heads ? a.q + (size_t)t * a.ldq + head * D
+                               : head < a.q_heads + a.kv_heads
+                                   ? a.k + (size_t)t * a.ldk + (head - a.q_heads) * D
+                                   : a.v + (size_t)t * a.ldv + (head - a.q_heads - a.kv_heads) * D;
+            in[n][0] = __ldcs(reinterpret_cast<const float4 *>(src) + c);
+            in[n][1] = __ldcs(reinterpret_cast<const float4 *>(src) + d);
+        }
     }
-    float cs[4] = {1.0f, 1.0f, 1.0f, 1.0f}, sn[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    const int half = a.rot / 2;
-    const bool turned = live && pos >= 0 && d0 < a.rot && (is_q || is_k);
-    if (turned) {
-        if (pos < a.max_pos) {
-            const float *row = a.table + (size_t)pos * a.rot;
-            if (INTERLEAVED) {
-                const float2 c = *reinterpret_cast<const float2 *>(row + 2 * sub);
-                const float2 s = *reinterpret_cast<const float2 *>(row + half + 2 * sub);
-                cs[0] = cs[1] = c.x; cs[2] = cs[3] = c.y;
-                sn[0] = sn[1] = s.x; sn[2] = sn[3] = s.y;
-            } else {
-                const int i = d0 < half ? d0 : d0 - half;
-                const float4 c = *reinterpret_cast<const float4 *>(row + i);
-                const float4 s = *reinterpret_cast<const float4 *>(row + half + i);
-                cs[0] = c.x; cs[1] = c.y; cs[2] = c.z; cs[3] = c.w;
-                sn[0] = s.x; sn[1] = s.y; sn[2] = s.z; sn[3] = s.w;
-            }
+    // cos and sin: of the chunk's four pairs (halves), or of each chunk's two (pairs: in x, y of cs[0] and cs[1])
+    float4 cs[2], sn[2];
+    cs[0] = cs[1] = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+    sn[0] = sn[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (pos >= 0 && (PAIRS ? 4 * c < a.rot : sub < p8)) {
+        const float *row = a.table + (size_t)pos * a.rot;
+        const float nan = __uint_as_float(0x7FC00000u);
+        if (pos >= a.max_pos) {
+            cs[0] = cs[1] = sn[0] = sn[1] = make_float4(nan, nan, nan, nan);
+        } else if (PAIRS) {  // rotary_dim is a multiple of 8: both chunks turn or neither
+            const float4 cv = *reinterpret_cast<const float4 *>(row + 2 * c);
+            const float4 sv = *reinterpret_cast<const float4 *>(row + a.rot / 2 + 2 * c);
+            cs[0] = make_float4(cv.x, cv.y, 0.0f, 0.0f);
+            cs[1] = make_float4(cv.z, cv.w, 0.0f, 0.0f);
+            sn[0] = make_float4(sv.x, sv.y, 0.0f, 0.0f);
+            sn[1] = make_float4(sv.z, sv.w, 0.0f, 0.0f);
         } else {
+            cs[0] = *reinterpret_cast<const float4 *>(row + 4 * c);
+            sn[0] = *reinterpret_cast<const float4 *>(row + a.rot / 2 + 4 * c);
+        }
+    }
+    const bool turns = PAIRS ? 4 * c < a.rot : sub < p8;
+    const bool placed = pos >= 0 && slot >= 0 && slot < a.n_slots;
+    const long long page = placed ? slot / a.page : 0;
+    const long long place = placed ? page * a.page_stride + (slot - page * a.page) * D : 0;  // of head 0
+    const float4 one = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+    const bool norms = a.qg || a.kg;
+    float4 gq[2] = {one, one}, gk[2] = {one, one};
+    if (a.qg) {
+        gq[0] = reinterpret_cast<const float4 *>(a.qg)[c];
+        gq[1] = reinterpret_cast<const float4 *>(a.qg)[d];
+    }
+    if (a.kg) {
+        gk[0] = reinterpret_cast<const float4 *>(a.kg)[c];
+        gk[1] = reinterpret_cast<const float4 *>(a.kg)[d];
+    }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) cs[e] = sn[e] = __uint_as_float(0x7FC00000u);
-        }
-    }
-    const float *gamma = is_q ? a.qg : a.kg;
-    if (a.qg || a.kg) {  // uniform across the launch: every lane takes the shuffles
-        float ss = fmaf(x.x, x.x, fmaf(x.y, x.y, fmaf(x.z, x.z, x.w * x.w)));
+    for (int n = 0; n < N; ++n) {
+        const int head = head0 + n * G;
+        const bool live = head < total;
+        const bool is_q = head < a.q_heads, is_k = !is_q && head < a.q_heads + a.kv_heads;
+        const int h = is_q ? head : (is_k ? head - a.q_heads : head - a.q_heads - a.kv_heads);
+        float4 x = in[n][0], y = in[n][1];
+        if (norms) {  // uniform across the launch: every lane takes the shuffles
+            float ss = fmaf(x.x, x.x, fmaf(x.y, x.y, fmaf(x.z, x.z, x.w * x.w))) +
+                       fmaf(y.x, y.x, fmaf(y.y, y.y, fmaf(y.z, y.z, y.w * y.w)));
 #pragma unroll
-        for (int o = 1; o < L; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (live && (is_q || is_k) && gamma) {
-            const float rs = 1.0f / sqrtf(ss / (float)D + a.eps);
-            const float4 g = *reinterpret_cast<const float4 *>(gamma + d0);
-            x.x = x.x * rs * g.x; x.y = x.y * rs * g.y; x.z = x.z * rs * g.z; x.w = x.w * rs * g.w;
+            for (int o = 1; o < L; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            if ((is_q && a.qg) || (is_k && a.kg)) {
+                const float rs = rsqrtf(ss * (1.0f / D) + a.eps);
+                const float4 g0 = is_q ? gq[0] : gk[0], g1 = is_q ? gq[1] : gk[1];
+                x.x *= rs * g0.x; x.y *= rs * g0.y; x.z *= rs * g0.z; x.w *= rs * g0.w;
+                y.x *= rs * g1.x; y.y *= rs * g1.y; y.z *= rs * g1.z; y.w *= rs * g1.w;
+            }
         }
-    }
-    if (INTERLEAVED) {
-        if (turned) {
-            const float4 y = x;
-            x.x = y.x * cs[0] - y.y * sn[0]; x.y = y.x * sn[1] + y.y * cs[1];
-            x.z = y.z * cs[2] - y.w * sn[2]; x.w = y.z * sn[3] + y.w * cs[3];
+        if (turns && (is_q || is_k)) {
+            const float4 u = x, v = y;
+            if (PAIRS) {
+                x.x = u.x * cs[0].x - u.y * sn[0].x; x.y = u.x * sn[0].x + u.y * cs[0].x;
+                x.z = u.z * cs[0].y - u.w * sn[0].y; x.w = u.z * sn[0].y + u.w * cs[0].y;
+                y.x = v.x * cs[1].x - v.y * sn[1].x; y.y = v.x * sn[1].x + v.y * cs[1].x;
+                y.z = v.z * cs[1].y - v.w * sn[1].y; y.w = v.z * sn[1].y + v.w * cs[1].y;
+            } else {
+                x.x = u.x * cs[0].x - v.x * sn[0].x; y.x = u.x * sn[0].x + v.x * cs[0].x;
+                x.y = u.y * cs[0].y - v.y * sn[0].y; y.y = u.y * sn[0].y + v.y * cs[0].y;
+                x.z = u.z * cs[0].z - v.z * sn[0].z; y.z = u.z * sn[0].z + v.z * cs[0].z;
+                x.w = u.w * cs[0].w - v.w * sn[0].w; y.w = u.w * sn[0].w + v.w * cs[0].w;
+            }
         }
-    } else {
-        const bool first = d0 < half;
-        const int far = first ? sub + half / 4 : sub - half / 4;
-        const int from = (lane - sub) + (d0 < a.rot ? far : sub);
-        float4 y;
-        y.x = __shfl_sync(0xffffffffu, x.x, from); y.y = __shfl_sync(0xffffffffu, x.y, from);
-        y.z = __shfl_sync(0xffffffffu, x.z, from); y.w = __shfl_sync(0xffffffffu, x.w, from);
-        if (turned) {
-            const float sg = first ? -1.0f : 1.0f;
-            x.x = x.x * cs[0] + sg * (y.x * sn[0]); x.y = x.y * cs[1] + sg * (y.y * sn[1]);
-            x.z = x.z * cs[2] + sg * (y.z * sn[2]); x.w = x.w * cs[3] + sg * (y.w * sn[3]);
+        if (is_q) {
+            uint2 *to = reinterpret_cast<uint2 *>(a.qo + (size_t)t * a.ldo + h * D);
+            if (PAIRS) {
+                const uint2 lo = pack_bf16x4(x), hi = pack_bf16x4(y);
+                *reinterpret_cast<uint4 *>(to + c) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+            } else {
+                to[c] = pack_bf16x4(x);
+                to[d] = pack_bf16x4(y);
+            }
         }
-    }
-    if (is_q) {
-        if (live) *reinterpret_cast<uint2 *>(a.qo + (size_t)t * a.ldo + (size_t)h * D + d0) = pack_bf16x4(x);
-    }
-    const bool write = live && !is_q && pos >= 0 && slot >= 0 && slot < a.n_slots;
-    const long long page = write ? slot / a.page : 0, off = write ? slot - page * a.page : 0;
-    const long long base = page * a.page_stride + ((long long)h * a.page + off) * D;
-    if (Q8) {
-        uint32_t mx = max(max(__float_as_uint(x.x) & 0x7FFFFFFFu, __float_as_uint(x.y) & 0x7FFFFFFFu),
-                          max(__float_as_uint(x.z) & 0x7FFFFFFFu, __float_as_uint(x.w) & 0x7FFFFFFFu));
+        const bool write = live && !is_q && placed;
+        const long long base = place + (long long)h * a.page * D;
+        if (Q8) {
+            const auto most = [](float4 v) {
+                return max(max(__float_as_uint(v.x) & 0x7FFFFFFFu, __float_as_uint(v.y) & 0x7FFFFFFFu),
+                           max(__float_as_uint(v.z) & 0x7FFFFFFFu, __float_as_uint(v.w) & 0x7FFFFFFFu));
+            };
+            uint32_t m0 = most(x), m1 = most(y);  // of the chunks, then of their blocks of eight chunks
+            if (PAIRS) {
+                m0 = max(m0, m1);
+                m0 = max(m0, __shfl_xor_sync(0xffffffffu, m0, 1));
+                m0 = m1 = max(m0, __shfl_xor_sync(0xffffffffu, m0, 2));
+            } else if (a.rot % 64 == 0 && a.rot == D) {  // eight lanes' chunks are a block, first and second alike
 #pragma unroll
-        for (int o = 1; o < 8; o <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        if (write) {
-            const float d = act_scale(mx), inv = act_inv(d);
-            const uint32_t codes = act_code(x.x, d, inv, mx) | (act_code(x.y, d, inv, mx) << 8) |
-                                   (act_code(x.z, d, inv, mx) << 16) | (act_code(x.w, d, inv, mx) << 24);
-            *reinterpret_cast<uint32_t *>(static_cast<unsigned char *>(is_k ? a.kc : a.vc) + base + d0) = codes;
-            if ((sub & 7) == 0) (is_k ? a.ks : a.vs)[(base + d0) / kBlock] = d;
+                for (int o = 1; o < 8; o <<= 1) {
+                    m0 = max(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+                    m1 = max(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+                }
+            } else {  // gather the eight chunks of each block from the lanes that hold them
+                uint32_t b0 = 0u, b1 = 0u;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        const int k = ((w ? d : c) & ~7) + e;  // chunk; its lane, and whether it is the second there
+                        const int from = k < p8 ? k : (k < 2 * p8 ? k - p8 : k >> 1);
+                        const bool second = k < 2 * p8 ? k >= p8 : (k & 1) != 0;
+                        const uint32_t f = __shfl_sync(0xffffffffu, m0, lane - sub + from);
+                        const uint32_t g = __shfl_sync(0xffffffffu, m1, lane - sub + from);
+                        (w ? b1 : b0) = max(w ? b1 : b0, second ? g : f);
+                    }
+                }
+                m0 = b0;
+                m1 = b1;
+            }
+            if (write) {
+                unsigned char *codes = static_cast<unsigned char *>(is_k ? a.kc : a.vc) + base;
+                float *scales = (is_k ? a.ks : a.vs) + base / kBlock;
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    const float4 v = w ? y : x;
+                    const uint32_t m = w ? m1 : m0;
+                    const int k = w ? d : c;
+                    const float s = act_scale(m), inv = act_inv(s);
+                    *reinterpret_cast<uint32_t *>(codes + 4 * k) =
+                        act_code(v.x, s, inv, m) | (act_code(v.y, s, inv, m) << 8) | (act_code(v.z, s, inv, m) << 16) |
+                        (act_code(v.w, s, inv, m) << 24);
+                    if ((k & 7) == 0) scales[k >> 3] = s;
+                }
+            }
+        } else if (write) {
+            uint2 *to = reinterpret_cast<uint2 *>(static_cast<uint16_t *>(is_k ? a.kc : a.vc) + base);
+            if (PAIRS) {
+                const uint2 lo = pack_bf16x4(x), hi = pack_bf16x4(y);
+                *reinterpret_cast<uint4 *>(to + c) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+            } else {
+                to[c] = pack_bf16x4(x);
+                to[d] = pack_bf16x4(y);
+            }
         }
-    } else if (write) {
-        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(is_k ? a.kc : a.vc) + base + d0) = pack_bf16x4(x);
     }
 }
 
+template <int D, bool I, bool Q8> cudaError_t launch_append_type(const AppendArgs &a, cudaStream_t stream) {
+    const int total = a.q_heads + 2 * a.kv_heads;
+    const auto grid = [&](int n) {
+        const long long per = (256 / D) * n, warps = a.rows * ((total + per - 1) / per);
+        return dim3((unsigned)((warps + kAppendWarps - 1) / kAppendWarps), 1, 1);
+    };
+    // One head a lane group while the rows are few (latency: all of it in flight at once anyway), four once there are
+    // enough to fill the SMs several times.
+    if ((long long)a.rows * total * D < kAppendWide)
+        return kv_launch(append_kernel<D, I, Q8, 1>, grid(1), 32 * kAppendWarps, 0, stream, a);
+    return kv_launch(append_kernel<D, I, Q8, 4>, grid(4), 32 * kAppendWarps, 0, stream, a);
+}
+
 template <int D> cudaError_t launch_append(const AppendArgs &a, bool interleaved, bool q8, cudaStream_t stream) {
-    const int total = a.q_heads + 2 * a.kv_heads, per = kAppendWarps * (128 / D);
-    const dim3 grid((unsigned)((total + per - 1) / per), (unsigned)a.rows, 1);
-    if (interleaved)
-        return q8 ? kv_launch(append_kernel<D, true, true>, grid, 32 * kAppendWarps, 0, stream, a)
-                  : kv_launch(append_kernel<D, true, false>, grid, 32 * kAppendWarps, 0, stream, a);
-    return q8 ? kv_launch(append_kernel<D, false, true>, grid, 32 * kAppendWarps, 0, stream, a)
-              : kv_launch(append_kernel<D, false, false>, grid, 32 * kAppendWarps, 0, stream, a);
+    if (interleaved || a.rot == 0)
+        return q8 ? launch_append_type<D, true, true>(a, stream) : launch_append_type<D, true, false>(a, stream);
+    return q8 ? launch_append_type<D, false, true>(a, stream) : launch_append_type<D, false, false>(a, stream);
 }
 
 }  // namespace
@@ -296,9 +385,8 @@ extern "C" q8_status q8_kv_slots(const int *cached, const int *fresh, int R, int
     const SlotArgs a = {cached, fresh, free_pages, head, table, lens, row_start, positions, next_head,
                         reinterpret_cast<long long *>(slots), R, page_size, n_free, table_width, table_pitch, rows};
     const size_t smem = (size_t)(R + 1) * 8;
-    cudaError_t e = cudaSuccess;
-    if (smem > 40 * 1024)
-        e = cudaFuncSetAttribute(slots_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t e = smem > 40 * 1024 ? kv_allow_smem(slots_kernel, (Q8_MAX_REQUESTS + 1) * 8, &allowed) : cudaSuccess;
     if (e != cudaSuccess) return kv_cuda_fail(e);
     const int most = rows > R + 1 ? rows : R + 1;
     int ctas = (most + kSlotThreads - 1) / kSlotThreads;

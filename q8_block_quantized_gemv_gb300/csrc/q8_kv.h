@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/q8_gemv.h"
 
 namespace q8 {
@@ -41,6 +43,20 @@ struct AttnArgs {
     int window, sinks;
     unsigned char *work;  // the caller's workspace
 };
+
+// Let `kernel` take `smem` bytes of dynamic shared memory, asked once a device: the attribute stays, and asking takes
+// about as long as a launch.  `done` is the kernel's own, a bit a device.
+template <typename Kernel>
+inline cudaError_t kv_allow_smem(Kernel kernel, int smem, std::atomic<uint64_t> *done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+    if (done->load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 // Launch with programmatic dependent launch: the kernel waits (griddepcontrol.wait) before it reads anything.
 template <typename Kernel, typename... Args>
