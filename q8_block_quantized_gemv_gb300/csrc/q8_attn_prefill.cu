@@ -843,12 +843,20 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                     const unsigned groups = ctl.pages[(cnt >> 1) & 7];
                     const bool part = groups != 0xFFu || it.partial(a, u);
                     constexpr int NB = D / 32;
-                    float mx = 0.0f;  // the tile's largest finite scale: every warp looks for itself
+                    float mx = 0.0f;  // the tile's largest finite scale: every warp looks for itself, four at a time
 #pragma unroll
-                    for (int y = 0; y < kTile * NB / 32; ++y) {
-                        const int e = y * 32 + lane;
-                        const float f = fabsf(scl[e]);
-                        if (f < INFINITY && (!part || live(e / NB, groups))) mx = fmaxf(mx, f);
+                    for (int y = 0; y < kTile * NB / 128; ++y) {
+                        const int e = (y * 32 + lane) * 4;
+                        const float4 f = *reinterpret_cast<const float4 *>(scl + e);
+                        float m = fmaxf(fmaxf(fabsf(f.x), fabsf(f.y)), fmaxf(fabsf(f.z), fabsf(f.w)));
+                        if (part || !(m < INFINITY)) {  // one by one, what somebody sees and is finite
+                            m = 0.0f;
+                            const float g[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                            for (int w = 0; w < 4; ++w)
+                                if (fabsf(g[w]) < INFINITY && (!part || live((e + w) / NB, groups))) m = fmaxf(m, fabsf(g[w]));
+                        }
+                        mx = fmaxf(mx, m);
                     }
 #pragma unroll
                     for (int o = 1; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -858,14 +866,23 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                     if (kv) ex = v_ex = max(v_ex, ex);
                     const float down = __uint_as_float((uint32_t)(254 - ex) << 23);  // 2^-(ex - 127)
                     bool found = false;
-                    constexpr int RC = D / 16;  // 16-code chunks a row
-#pragma unroll 4
-                    for (int e = ht; e < kTile * RC; e += HT) {
-                        const int c = e / RC, ch = e % RC;
-                        float f = scl[c * NB + ch / 2] * down;
-                        uint4 v = *reinterpret_cast<const uint4 *>(raw + c * D + ch * 16);
+                    // Thread ht takes 16 codes of rows r0, r0 + HT / RC, ...: a step of whole swizzle periods, so that
+                    // all addresses are its first ones plus constants.
+                    constexpr int RC = D / 16, RS = HT / RC;  // chunks of 16 codes a row, rows a pass
+                    static_assert(RS % 8 == 0 && kTile % RS == 0, "");
+                    const int ch = ht % RC, r0 = ht / RC;
+                    const unsigned char *src = raw + r0 * D + ch * 16;
+                    const float *sc = scl + r0 * NB + ch / 2;
+                    unsigned char *to = op + (ch / 4) * kTile * 128 + r0 * 128;
+                    const bool swap = (ch >> 2) & 1;  // the two halves of a quarter warp write different banks
+                    const int da = (((2 * ch) & 7) ^ (r0 & 7)) * 16, db = da ^ 16;
+                    unsigned char *first = to + (swap ? db : da), *second = to + (swap ? da : db);
+#pragma unroll
+                    for (int y = 0; y < kTile / RS; ++y) {
+                        float f = sc[y * RS * NB] * down;
+                        uint4 v = *reinterpret_cast<const uint4 *>(src + y * RS * D);
                         if (part) {
-                            const bool see = live(c, groups);
+                            const bool see = live(r0 + y * RS, groups);
                             if (!see || (kv && !(fabsf(f) < INFINITY))) {
                                 found = found || see;
                                 v = make_uint4(0u, 0u, 0u, 0u);
@@ -878,18 +895,15 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
 #pragma unroll
-                            for (int y = 0; y < 2; ++y) {
-                                const uint32_t b = __byte_perm(w[k], 0x64646464u, y ? 0x4342 : 0x4140);
+                            for (int z = 0; z < 2; ++z) {
+                                const uint32_t b = __byte_perm(w[k], 0x64646464u, z ? 0x4342 : 0x4140);
                                 const __half2 q = __hmul2(__hsub2(*reinterpret_cast<const __half2 *>(&b),
                                                                   __half2half2(__ushort_as_half(0x6480))), f2);
-                                h[2 * k + y] = *reinterpret_cast<const uint32_t *>(&q);
+                                h[2 * k + z] = *reinterpret_cast<const uint32_t *>(&q);
                             }
-                        unsigned char *to = op + (ch / 4) * kTile * 128 + c * 128;
-                        const int d0 = ((2 * ch) & 7) ^ (c & 7), d1 = ((2 * ch + 1) & 7) ^ (c & 7);
-                        const bool swap = (ch >> 2) & 1;  // the two halves of a quarter warp write different banks
                         const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-                        *reinterpret_cast<uint4 *>(to + (swap ? d1 : d0) * 16) = swap ? hi : lo;
-                        *reinterpret_cast<uint4 *>(to + (swap ? d0 : d1) * 16) = swap ? lo : hi;
+                        *reinterpret_cast<uint4 *>(first + y * RS * 128) = swap ? hi : lo;
+                        *reinterpret_cast<uint4 *>(second + y * RS * 128) = swap ? lo : hi;
                     }
                     if (found) *(volatile int *)&ctl.poison = 1;
                     if (ht == 0) ctl.unit[kv][(cnt >> 1) & 7] = (float)(ex - 127);
