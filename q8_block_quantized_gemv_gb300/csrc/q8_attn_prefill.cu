@@ -44,7 +44,6 @@ constexpr int kRows = 256;   // query rows of an item
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMmaWarp = 8, kLoadWarp = 9, kHelpWarp = 10;
 constexpr unsigned kTmemColumns = 512;
-constexpr uint32_t kColO = 256;  // S of tiles A and B at columns 0 and 128, O from here
 constexpr uint32_t kColP = 64;   // the weights (16 bits) over the upper half of their scores
 constexpr unsigned kFaultAttnWait = 8u;
 
@@ -52,6 +51,11 @@ __device__ unsigned int g_attn_fault = 0;
 
 template <int D, bool Q8> struct Cfg {
     static constexpr int kSub = D / 64;                    // 128-byte-wide column blocks of an operand
+    // Tensor memory: score buffers of 128 columns, then the tiles' O.  With two buffers a tile's next scores follow its
+    // last weights, which lie over the last scores.  Heads of 64 leave room for a third: the jobs A, B, A, B ... take the
+    // buffers in turn, and a tile's next scores are there before its softmax is done with the last.
+    static constexpr int kBufs = D == 64 ? 3 : 2;
+    static constexpr uint32_t kColO = kBufs * 128;
     static constexpr int kOp = kSub * kTile * 128;         // bytes of a K, V or Q operand tile
     static constexpr int kRaw = Q8 ? kTile * D + kTile * (D / 32) * 4 : 0;
     static constexpr int kSlots = Q8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 10);
@@ -75,7 +79,8 @@ template <int D, bool Q8> struct Control {
     uint64_t step[8];                          // a step's MMAs are done, and with them what it used is free
     uint64_t raw_full[4], raw_empty[4];        // raw ring (Q8_0)
     uint64_t q_raw, q_full, q_empty, drain;  // q_raw: landed, before the conversion (Q8_0)
-    uint64_t s_full[2], p_ready[2], o_full[2], joined, decided;
+    uint64_t s_full[3], p_ready[3];            // by score buffer: scores computed, weights written
+    uint64_t o_full[2], joined, decided;
     // Of key tile number n of this CTA at n & 7 (no role is more than five tiles behind the requests):
     unsigned pages[8];  // bits: which 16-token groups lie on a page
     float unit[2][8];   // Q8_0: log2 of the keys' and the values' unit
@@ -347,27 +352,6 @@ __device__ __forceinline__ void q_tile_of(const PrefillArgs &pa, Item &x) {
     x.p_max = x.p_min + x.tokens - 1;
     span_of(pa.a, x);
 }
-// The item's key tiles that its query tile t visits within a segment [i0, i1): first .. last without us .. skip - 1,
-// which are in no row's window; none if last < first.
-struct Visit {
-    int first, last, us, skip;
-    __device__ __forceinline__ bool operator()(int i) const { return i >= first && i <= last && (i < us || i >= skip); }
-};
-__device__ __forceinline__ Visit visit_of(const PrefillArgs &pa, const Item &x, int t, int i0, int i1) {
-    Visit v = {0, -1, x.us, x.us};
-    const int a = t * pa.tile_tokens, b = min(a + pa.tile_tokens, x.tokens);  // its tokens
-    if (a >= b) return v;
-    const int hi = (x.p_min + b - 1) / kTile;  // the tile of its last key
-    const int lim = min(x.n, max(1, hi < x.ul ? min(hi + 1, x.us) : x.us + hi - x.ul + 1));
-    if (pa.a.window) {  // sinks may reach past us, where the item's first rows see all tiles anyway
-        v.us = max(x.us, min(x.us + (min(pa.a.sinks, x.end) + kTile - 1) / kTile - x.ul, lim));
-        v.skip = max(v.us, min(x.us + max(x.p_min + a - pa.a.window + 1, 0) / kTile - x.ul, lim - 1));
-    }
-    v.first = i0 >= v.us && i0 < v.skip ? v.skip : i0;
-    v.last = min(lim, i1) - 1;
-    if (v.last >= v.us && v.last < v.skip) v.last = v.us - 1;
-    return v;
-}
 __device__ __forceinline__ long long cost_of(const PrefillArgs &pa, const Item &x) {
     return x.n ? x.n + pa.item_cost : 0;
 }
@@ -449,11 +433,11 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
         bar_init(&ctl.drain, 1);
         bar_init(&ctl.joined, 256);
         bar_init(&ctl.decided, 1);
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < C::kBufs; ++i) {
             bar_init(&ctl.s_full[i], 1);
             bar_init(&ctl.p_ready[i], 4);
-            bar_init(&ctl.o_full[i], 1);
         }
+        for (int i = 0; i < 2; ++i) bar_init(&ctl.o_full[i], 1);
         ctl.abort = 0;
         ctl.poison = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -685,9 +669,8 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
         __syncwarp();
     } else if (warp == kMmaWarp) {
         // ---- the MMAs ----
-        // The tensor cores run what is queued while this warp looks at barriers, as long as a batch follows a batch: O
-        // of one key tile and S of the next for tile A, the same for B, each issued in one go, and the waits for
-        // what the next batches need between them.
+        // The tensor cores work on what is queued while this warp looks at barriers, as long as a batch follows a batch.  A
+        // turn is a batch: the O of a job, and the S that its score buffer (with three, the one behind it) is free for.
         constexpr uint32_t fmt = Q8 ? 0u : 1u;  // fp16 or bf16 operands
         const uint32_t id_s = (1u << 4) | (fmt << 7) | (fmt << 10) | (a.scale < 0.0f ? 1u << 13 : 0u) |
                               ((kTile >> 3) << 17) | ((kTile >> 4) << 24);
@@ -695,57 +678,125 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                                   ((kTile >> 4) << 24);
         const uint32_t q_desc = desc128_low(saddr(smem), 16), k_desc = desc128_low(saddr(smem + C::kRing), 16);
         const uint32_t v_desc = desc128_low(saddr(smem + C::kRing), kTile * 128);
-        unsigned slot = 0, phase = 0, seg = 0, steps = 0, pcnt[2] = {0, 0};  // slot, phase: of the ring's next use
+        constexpr int AHEAD = C::kBufs - 1;  // key tiles that A's scores are ahead of its O
+        unsigned seg = 0, steps = 0, pbits = 0;              // pbits: the weight barriers' phases
+        unsigned kslot = 0, kphase = 0, vslot = 1, vphase = 0;  // of the next keys to wait for, the next values
+        unsigned jobs = 0;                                   // the buffer of A's next O
         bool ok = true;
-        for (; more; advance()) {
-            const Visit vis[2] = {visit_of(pa, it, 0, i0, i1), visit_of(pa, it, 1, i0, i1)};
-            if (!(ok = warp_wait(&ctl.q_full, seg & 1, abort))) break;
-            for (int i = i0 - 1; i < i1 && ok; ++i) {
-                const bool has_v = i >= i0, has_k = i + 1 < i1;
-                const unsigned sv = uniform(slot), vphase = phase;
-                if (has_v && ++slot == C::kSlots) { slot = 0; phase ^= 1; }
-                const unsigned sk = has_v ? (sv + 1 == C::kSlots ? 0 : sv + 1) : sv, kphase = phase;
-                if (has_k && ++slot == C::kSlots) { slot = 0; phase ^= 1; }
-                uint64_t *const vbar = &ctl.ready[sv], *const kbar = Q8 ? &ctl.ready[sk] : &ctl.full[sk];
-                // values, keys and tile A's weights in one look where all are wanted
-                const bool all = has_v && has_k && vis[0](i);
-                if (!all || !look3(vbar, vphase, kbar, kphase, &ctl.p_ready[0], pcnt[0] & 1)) {
-                    if (has_v && !(ok = warp_wait(vbar, vphase, abort))) break;
-                    if (has_k && !(ok = warp_wait(kbar, kphase, abort))) break;
-                    if (has_v && vis[0](i) && !(ok = warp_wait(&ctl.p_ready[0], pcnt[0] & 1, abort))) break;
-                }
-                if (has_v && vis[0](i)) ++pcnt[0];
+        auto two_on = [](unsigned &slot, unsigned &phase) {
+            slot += 2;
+            if (slot >= C::kSlots) {
+                slot -= C::kSlots;
+                phase ^= 1;
+            }
+        };
+        auto key_bar = [&]() { return Q8 ? &ctl.ready[kslot] : &ctl.full[kslot]; };
+        auto issue_s = [&](int x, unsigned b, unsigned slot) {  // one lane
+            const uint32_t qd = q_desc + x * (C::kOp >> 4), kd = k_desc + slot * (C::kOp >> 4);
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const bool do_o = has_v && vis[x](i), do_s = has_k && vis[x](i + 1);
-                    const uint32_t more_o = i > vis[x].first;
-                    if (x == 1 && do_o && !(ok = warp_wait(&ctl.p_ready[1], pcnt[1]++ & 1, abort))) break;
+            for (int k = 0; k < D / 16; ++k) {
+                const unsigned o = ((k / 4) * kTile * 128 + (k % 4) * 32) >> 4;
+                mma_ss(tmem + b * kTile, qd + o, kd + o, id_s, k > 0);
+            }
+            commit(&ctl.s_full[b]);
+        };
+        auto issue_o = [&](int x, unsigned b, unsigned slot, uint32_t more_o) {
+            const uint32_t vd = v_desc + slot * (C::kOp >> 4);
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k)
+                mma_ts(tmem + C::kColO + x * D, tmem + b * kTile + kColP + k * 8, vd + (k * 2048 >> 4), id_o,
+                       k > 0 ? 1u : more_o);
+        };
+        auto buffer = [](unsigned j) { return C::kBufs == 2 ? j & 1u : (j >= 6 ? j - 6 : j >= 3 ? j - 3 : j); };
+        for (; more; advance()) {
+            const bool two = it.tokens > pa.tile_tokens;  // tile B has rows
+            if (!(ok = warp_wait(&ctl.q_full, seg & 1, abort))) break;
+            // the first scores
+            unsigned key1 = 0;  // slot of the keys that B's next scores need
+            for (int n = 0; n < AHEAD && i0 + n < i1; ++n) {
+                if (!(ok = warp_wait(key_bar(), kphase, abort))) break;
+                key1 = uniform(kslot);
+                two_on(kslot, kphase);
+                const unsigned b = uniform(jobs);
+                fence_after();
+                if (elect()) {
+                    issue_s(0, buffer(b + 2 * n), key1);
+                    if (n == 0 && two) issue_s(1, buffer(b + 1), key1);
+                    if (n + 1 == AHEAD || i0 + n + 1 == i1) {
+                        commit(&ctl.step[steps & 7]);
+                        if (i1 - i0 == 1) commit(&ctl.q_empty);
+                    }
+                }
+                __syncwarp();
+            }
+            if (!ok) break;
+            ++steps;
+            for (int i = i0; i < i1; ++i) {
+                const unsigned u = uniform(vslot | (jobs << 8)), vs = u & 255u, ba = u >> 8, bb = buffer(ba + 1);
+                const uint32_t more_o = i > i0;
+                // ---- A ----
+                {
+                    const bool keys = C::kBufs == 2 && i + 1 < i1;  // two buffers: A's next scores in this turn
+                    uint64_t *const pbar = &ctl.p_ready[ba], *const kbar = keys ? key_bar() : pbar;
+                    const unsigned pp = pbits >> ba & 1u, kp = keys ? kphase : pp;
+                    if (!look3(pbar, pp, &ctl.ready[vs], vphase, kbar, kp)) {
+                        if (!(ok = warp_wait(&ctl.ready[vs], vphase, abort))) break;
+                        if (!(ok = warp_wait(kbar, kp, abort))) break;
+                        if (!(ok = warp_wait(pbar, pp, abort))) break;
+                    }
+                    pbits ^= 1u << ba;
+                    if (keys) {
+                        key1 = uniform(kslot);
+                        two_on(kslot, kphase);
+                    }
                     fence_after();
                     if (elect()) {
-                        if (do_o) {
-                            const uint32_t vd = v_desc + sv * (C::kOp >> 4);
-#pragma unroll
-                            for (int k = 0; k < kTile / 16; ++k)
-                                mma_ts(tmem + kColO + x * 128, tmem + x * kTile + kColP + k * 8, vd + (k * 2048 >> 4),
-                                       id_o, k > 0 ? 1u : more_o);
-                            if (i == vis[x].last) commit(&ctl.o_full[x]);
-                        }
-                        if (do_s) {
-                            const uint32_t qd = q_desc + x * (C::kOp >> 4), kd = k_desc + sk * (C::kOp >> 4);
-#pragma unroll
-                            for (int k = 0; k < D / 16; ++k) {
-                                const unsigned o = ((k / 4) * kTile * 128 + (k % 4) * 32) >> 4;
-                                mma_ss(tmem + x * kTile, qd + o, kd + o, id_s, k > 0);
-                            }
-                            commit(&ctl.s_full[x]);
-                        }
-                        if (x == 1) {
-                            commit(&ctl.step[steps & 7]);
-                            if (i + 2 == i1) commit(&ctl.q_empty);
+                        issue_o(0, ba, vs, more_o);
+                        if (i + 1 == i1) commit(&ctl.o_full[0]);
+                        if (C::kBufs == 2) {
+                            if (keys) issue_s(0, ba, key1);
+                        } else if (two && i + 1 < i1) {
+                            issue_s(1, ba, key1);
                         }
                     }
                     __syncwarp();
                 }
+                // ---- B ----
+                {
+                    const bool keys = C::kBufs == 3 && i + 2 < i1;  // three: A's scores of the tile after the next
+                    if (two || keys) {
+                        uint64_t *const kbar = keys ? key_bar() : &ctl.p_ready[bb], *const pbar = two ? &ctl.p_ready[bb] : kbar;
+                        const unsigned kp = keys ? kphase : pbits >> bb & 1u, pp = two ? pbits >> bb & 1u : kp;
+                        if (!look3(pbar, pp, kbar, kp, pbar, pp)) {
+                            if (!(ok = warp_wait(kbar, kp, abort))) break;
+                            if (!(ok = warp_wait(pbar, pp, abort))) break;
+                        }
+                        if (two) pbits ^= 1u << bb;
+                    }
+                    unsigned key2 = 0;
+                    if (keys) {
+                        key2 = uniform(kslot);
+                        two_on(kslot, kphase);
+                    }
+                    fence_after();
+                    if (elect()) {
+                        if (two) {
+                            issue_o(1, bb, vs, more_o);
+                            if (i + 1 == i1) commit(&ctl.o_full[1]);
+                        }
+                        if (C::kBufs == 2) {
+                            if (two && i + 1 < i1) issue_s(1, bb, key1);
+                        } else if (keys) {
+                            issue_s(0, bb, key2);
+                        }
+                        commit(&ctl.step[steps & 7]);
+                        if (i + 2 == i1) commit(&ctl.q_empty);
+                    }
+                    __syncwarp();
+                    if (keys) key1 = key2;
+                }
+                two_on(vslot, vphase);
+                if (C::kBufs == 3) jobs = buffer(jobs + 2);
                 ++steps;
             }
             if (!ok) break;
@@ -926,28 +977,31 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
         const int tok = x * pa.tile_tokens + y / a.group, gh = y % a.group;  // of this row: the item's token, the head
         const bool whole_row = y < pa.tile_tokens * a.group;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        const uint32_t ts = tmem + lanes + x * kTile, to = tmem + lanes + kColO + x * 128;
+        const uint32_t to = tmem + lanes + C::kColO + x * D;
         // The largest sum of a row's 128 weights: below fp16's largest value, and for bf16 weights, which have fp32's
         // range, far below where a row's sums could overflow.
         constexpr float kMostSum = Q8 ? 32768.0f : 1.15292150e18f;  // 2^15, 2^60
         constexpr float kLeast = 1.17549435e-38f;  // a factor of 0 would make NaN of a hidden score's -inf
         const float sc0 = fmaxf(fabsf(a.scale) * kLog2e, kLeast);
-        unsigned cnt = 0, scnt = 0, ocnt = 0, shared = 0, seg = 0;
+        unsigned cnt = 0, ocnt = 0, shared = 0, seg = 0;
+        unsigned job = 0, sbits = 0;  // the buffer of A's next scores; the score barriers' phases
         bool ok = true;
         for (; more; advance()) {
             if (!ok) break;
-            const Visit vis = visit_of(pa, it, x, i0, i1);
-            const bool active = vis.first <= vis.last;
+            const bool two = it.tokens > pa.tile_tokens, active = x == 0 || two;
             const bool row_live = whole_row && tok < it.tokens;
             const int p = it.p_min + tok, p0 = it.p_min + x * pa.tile_tokens;  // of the row, the tile
             float M = row_live ? -INFINITY : 0.0f, l = 0.0f;  // rows beyond the item's ask for nothing
             if (active) {
                 float sc = sc0;
-                for (int i = vis.first; i <= vis.last && ok; ++i) {
-                    if (!vis(i)) continue;
+                for (int i = i0; i < i1 && ok; ++i) {
+                    const unsigned ba = job, bb = C::kBufs == 2 ? 1u : (job == 2 ? 0u : job + 1);
+                    const unsigned b = x ? bb : ba, parity = sbits >> b & 1u;
+                    sbits ^= (1u << ba) ^ (two ? 1u << bb : 0u);
+                    if (C::kBufs == 3) job = job == 0 ? 2u : job - 1;  // two on
+                    const uint32_t ts = tmem + lanes + b * kTile;
                     const unsigned ck = cnt + 2 * (i - i0), at = (ck >> 1) & 7;
-                    if (!(ok = warp_wait(&ctl.s_full[x], scnt & 1, abort))) break;
-                    ++scnt;
+                    if (!(ok = warp_wait(&ctl.s_full[b], parity, abort))) break;
                     fence_after();
                     float shift = 0.0f;  // log2 of the values' unit (Q8_0)
                     const unsigned groups = *(volatile unsigned *)&ctl.pages[at];
@@ -1015,7 +1069,14 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                             const float now = fmaxf(M, mx), f = now == M ? 1.0f : ex2(M - now);  // 0 from -inf
                             M = now;
                             l *= f;
-                            if (i > vis.first) {
+                            if (i > i0) {
+                                // With three buffers these scores may have come before the last tile's O: it is at
+                                // rest once that tile's turns are done.
+                                if (C::kBufs == 3) {
+                                    const unsigned n = steps + (i - i0);
+                                    if (!(ok = warp_wait(&ctl.step[n & 7], (n >> 3) & 1, abort))) break;
+                                    fence_after();
+                                }
 #pragma unroll 1
                                 for (int c0 = 0; c0 < D; c0 += 16) {
                                     uint32_t o[16];
@@ -1053,11 +1114,20 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                     tm_wait_st();
                     fence_before();
                     __syncwarp();
-                    if (lane == 0) bar_arrive(&ctl.p_ready[x]);
+                    if (lane == 0) bar_arrive(&ctl.p_ready[b]);
                 }
                 if (ok) ok = warp_wait(&ctl.o_full[x], ocnt++ & 1, abort);
                 fence_after();
+            } else {
+                // Tile B without rows keeps count of the buffers, and does not run ahead: a barrier tells a phase from the
+                // one before it, not from the one before that.
+                for (int i = i0; i < i1; ++i) {
+                    sbits ^= 1u << job;
+                    if (C::kBufs == 3) job = job == 0 ? 2u : job - 1;
+                }
+                ok = warp_wait(&ctl.o_full[0], seg & 1, abort);
             }
+            steps += i1 - i0 + 1;
             cnt += 2 * (i1 - i0);
             ++seg;
             // ---- the segment's end ----
