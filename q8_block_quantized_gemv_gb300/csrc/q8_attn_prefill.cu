@@ -82,7 +82,9 @@ template <int D, bool Q8> struct Control {
     uint64_t s_full[3], p_ready[3];            // by score buffer: scores computed, weights written
     uint64_t o_full[2], joined, decided;
     // Of key tile number n of this CTA at n & 7 (no role is more than five tiles behind the requests):
-    unsigned pages[8];  // bits: which 16-token groups lie on a page
+    // its first key, and bits: which 16-token groups lie on a page (0-7); whether some row of tile A (8) or B (9) does
+    // not see all of it
+    int2 tile[8];
     float unit[2][8];   // Q8_0: log2 of the keys' and the values' unit
     uint32_t tmem;
     int abort, poison, last;
@@ -298,6 +300,12 @@ __device__ __forceinline__ void store_row(uint16_t *p, const float (&o)[32], boo
         for (int k = 0; k < 16; k += 4)
             *reinterpret_cast<uint4 *>(p + 2 * k) = make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
     }
+}
+
+__device__ __forceinline__ int2 tile_info(const int2 *p) {
+    int2 v;
+    asm volatile("ld.shared.v2.s32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(saddr(p)) : "memory");
+    return v;
 }
 
 struct PrefillArgs {
@@ -628,7 +636,13 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                     }
                     if (!Q8) slot_used(s, steps + (i - i0) + kv);
                     if (lane == 0) {
-                        if (kv == 0) ctl.pages[(cnt >> 1) & 7] = groups;
+                        if (kv == 0) {
+                            const int u = it.tile(i), pb = it.p_min + pa.tile_tokens;
+                            const bool gone = groups != 0xFFu;
+                            ctl.tile[(cnt >> 1) & 7] = make_int2(
+                                u * kTile, (int)groups | (gone || it.partial(a, u, it.p_min, pb - 1) ? 256 : 0) |
+                                               (gone || it.partial(a, u, pb, pb + pa.tile_tokens - 1) ? 512 : 0));
+                        }
                         const unsigned bytes = __popc(groups) * 16 * (Q8 ? D + D / 32 * 4 : 2 * D);
                         bar_arrive_tx(full, bytes);
                     }
@@ -852,7 +866,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                     unsigned char *op = smem + C::kRing + s * C::kOp;
                     if (!Q8) {
                         if (!(ok = warp_wait(&ctl.full[s], par, abort))) break;
-                        const unsigned groups = ctl.pages[(cnt >> 1) & 7];
+                        const unsigned groups = ctl.tile[(cnt >> 1) & 7].y & 255u;
                         if (kv && (groups != 0xFFu || it.partial(a, u))) {
                             bool found = false;
                             for (int e = ht; e < kTile * CH; e += HT) {
@@ -891,7 +905,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                     if (!(ok = warp_wait(&ctl.raw_full[rs], rpar, abort))) break;
                     const unsigned char *raw = smem + C::kRawAt + rs * C::kRaw;
                     const float *scl = reinterpret_cast<const float *>(raw + kTile * D);
-                    const unsigned groups = ctl.pages[(cnt >> 1) & 7];
+                    const unsigned groups = ctl.tile[(cnt >> 1) & 7].y & 255u;
                     const bool part = groups != 0xFFu || it.partial(a, u);
                     constexpr int NB = D / 32;
                     float mx = 0.0f;  // the tile's largest finite scale: every warp looks for itself, four at a time
@@ -990,7 +1004,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
             if (!ok) break;
             const bool two = it.tokens > pa.tile_tokens, active = x == 0 || two;
             const bool row_live = whole_row && tok < it.tokens;
-            const int p = it.p_min + tok, p0 = it.p_min + x * pa.tile_tokens;  // of the row, the tile
+            const int p = it.p_min + tok;
             float M = row_live ? -INFINITY : 0.0f, l = 0.0f;  // rows beyond the item's ask for nothing
             if (active) {
                 float sc = sc0;
@@ -1004,7 +1018,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                     if (!(ok = warp_wait(&ctl.s_full[b], parity, abort))) break;
                     fence_after();
                     float shift = 0.0f;  // log2 of the values' unit (Q8_0)
-                    const unsigned groups = *(volatile unsigned *)&ctl.pages[at];
+                    const int2 info = tile_info(&ctl.tile[at]);
                     if (Q8) {
                         const unsigned cv = ck + 1;
                         if (!(ok = warp_wait(&ctl.ready[cv % C::kSlots], (cv / C::kSlots) & 1, abort))) break;
@@ -1012,12 +1026,11 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                         sc = fmaxf(sc0 * back * ex2(*(volatile float *)&ctl.unit[0][at]), kLeast);
                         shift = *(volatile float *)&ctl.unit[1][at];
                     }
-                    const int u = it.tile(i), j0 = u * kTile;
-                    const bool part = groups != 0xFFu || it.partial(a, u, p0, p0 + pa.tile_tokens - 1);
-                    // columns [c_lo, c_hi] and [0, c_sink) are visible
-                    const int c_hi = min(p, it.end - 1) - j0;
-                    const int c_lo = a.window ? max(p - a.window + 1 - j0, 0) : 0, c_sink = a.window ? a.sinks - j0 : 0;
-                    if (part) {  // hidden scores become -inf in place
+                    if (info.y >> (8 + x) & 1) {  // hidden scores become -inf in place
+                        // columns [c_lo, c_hi] and [0, c_sink) are visible
+                        const int j0 = info.x, groups = info.y;
+                        const int c_hi = min(p, it.end - 1) - j0;
+                        const int c_lo = a.window ? max(p - a.window + 1 - j0, 0) : 0, c_sink = a.window ? a.sinks - j0 : 0;
 #pragma unroll 1
                         for (int c0 = 0; c0 < kTile; c0 += 32) {
                             uint32_t v[32];
@@ -1184,7 +1197,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                 ok = warp_wait(&ctl.decided, shared++ & 1, abort);
                 if (ok && *(volatile int *)&ctl.last && row_live) {
                     __threadfence();
-                    constexpr int J = Q8 ? 32 : 64;  // columns at a time: J / 4 loads in flight, J sums
+                    constexpr int J = Q8 || D == 64 ? 32 : 64;  // columns at a time: J / 4 loads in flight, J sums
 #pragma unroll 1
                     for (int cc = 0; cc < D; cc += J) {
                         float o[J], m2 = -INFINITY, l2 = 0.0f;
