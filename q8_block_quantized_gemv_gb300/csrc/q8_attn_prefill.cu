@@ -868,26 +868,33 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                         if (!(ok = warp_wait(&ctl.full[s], par, abort))) break;
                         const unsigned groups = ctl.tile[(cnt >> 1) & 7].y & 255u;
                         if (kv && (groups != 0xFFu || it.partial(a, u))) {
+                            // Thread ht takes chunk ht % CH of every RS-th key, eight loads in flight.
                             bool found = false;
-                            for (int e = ht; e < kTile * CH; e += HT) {
-                                const int c = e / CH, ch = e % CH;
-                                uint4 *at = reinterpret_cast<uint4 *>(op + (ch / 8) * kTile * 128 + c * 128 + (ch % 8) * 16);
-                                if (!live(c, groups)) {
-                                    *at = make_uint4(0u, 0u, 0u, 0u);
-                                    continue;
-                                }
-                                uint4 v = *at;
-                                uint32_t w[4] = {v.x, v.y, v.z, v.w}, bad = 0u;
+                            constexpr int RS = HT / CH, B = 8;
+                            static_assert(kTile % (RS * B) == 0, "");
+                            uint4 *at = reinterpret_cast<uint4 *>(op + (ht % CH / 8) * kTile * 128 + ht / CH * 128 + ht % 8 * 16);
+#pragma unroll 1
+                            for (int y = 0; y < kTile / RS; y += B) {
+                                uint4 v[B];
 #pragma unroll
-                                for (int k = 0; k < 4; ++k) bad |= ((w[k] & 0x7FFF7FFFu) + 0x00800080u) & 0x80008000u;
-                                if (bad) {
-                                    found = true;
+                                for (int z = 0; z < B; ++z) v[z] = at[(y + z) * RS * 8];
 #pragma unroll
-                                    for (int k = 0; k < 4; ++k) {
-                                        const uint32_t b = ((w[k] & 0x7FFF7FFFu) + 0x00800080u) & 0x80008000u;
-                                        w[k] &= ~((b >> 15) * 0xFFFFu);
+                                for (int z = 0; z < B; ++z) {
+                                    const int c = (y + z) * RS + ht / CH;
+                                    if (!live(c, groups)) {
+                                        at[(y + z) * RS * 8] = make_uint4(0u, 0u, 0u, 0u);
+                                        continue;
                                     }
-                                    *at = make_uint4(w[0], w[1], w[2], w[3]);
+                                    const auto odd = [](uint32_t w) {  // the halves that are not finite, in their top bits
+                                        return ((w & 0x7FFF7FFFu) + 0x00800080u) & 0x80008000u;
+                                    };
+                                    const uint32_t b[4] = {odd(v[z].x), odd(v[z].y), odd(v[z].z), odd(v[z].w)};
+                                    if (b[0] | b[1] | b[2] | b[3]) {
+                                        found = true;
+                                        at[(y + z) * RS * 8] = make_uint4(
+                                            v[z].x & ~((b[0] >> 15) * 0xFFFFu), v[z].y & ~((b[1] >> 15) * 0xFFFFu),
+                                            v[z].z & ~((b[2] >> 15) * 0xFFFFu), v[z].w & ~((b[3] >> 15) * 0xFFFFu));
+                                    }
                                 }
                             }
                             if (found) *(volatile int *)&ctl.poison = 1;
@@ -1031,18 +1038,24 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                         const int j0 = info.x, groups = info.y;
                         const int c_hi = min(p, it.end - 1) - j0;
                         const int c_lo = a.window ? max(p - a.window + 1 - j0, 0) : 0, c_sink = a.window ? a.sinks - j0 : 0;
+                        // By 32 columns: most are seen by all 32 rows of the warp, or by none.
 #pragma unroll 1
                         for (int c0 = 0; c0 < kTile; c0 += 32) {
-                            uint32_t v[32];
-                            tm_ld32(ts + c0, v);
                             // bits: columns c0 .. of this row that it sees
-                            const uint32_t up = bits_below(c_hi + 1 - c0);
-                            uint32_t see = up & (~bits_below(c_lo - c0) | bits_below(c_sink - c0));
+                            uint32_t see = bits_below(c_hi + 1 - c0) & (~bits_below(c_lo - c0) | bits_below(c_sink - c0));
                             see &= ((groups >> (c0 / 16) & 1u) ? 0xFFFFu : 0u) |
                                    ((groups >> (c0 / 16 + 1) & 1u) ? 0xFFFF0000u : 0u);
-                            tm_wait_ld();
+                            if (__all_sync(0xffffffffu, see == ~0u)) continue;
+                            uint32_t v[32];
+                            if (__any_sync(0xffffffffu, see != 0u)) {
+                                tm_ld32(ts + c0, v);
+                                tm_wait_ld();
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) v[k] = (see >> k & 1u) ? v[k] : 0xFF800000u;
+                                for (int k = 0; k < 32; ++k) v[k] = (see >> k & 1u) ? v[k] : 0xFF800000u;
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) v[k] = 0xFF800000u;
+                            }
                             tm_st32(ts + c0, v);
                         }
                         tm_wait_st();
