@@ -208,14 +208,6 @@ __device__ __forceinline__ void tm_ld32(uint32_t a, uint32_t (&v)[32]) {
           "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
         : "r"(a));
 }
-__device__ __forceinline__ void tm_ld16(uint32_t a, uint32_t (&v)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15}, [%16];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-        : "r"(a));
-}
 __device__ __forceinline__ void tm_st32(uint32_t a, const uint32_t (&v)[32]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
@@ -306,6 +298,70 @@ __device__ __forceinline__ int2 tile_info(const int2 *p) {
     int2 v;
     asm volatile("ld.shared.v2.s32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(saddr(p)) : "memory");
     return v;
+}
+
+// The scores at ts that their row does not see become -inf in place: it sees columns c_lo .. c_hi and 0 .. c_sink - 1
+// of the 16-column groups that have a bit.
+__device__ __forceinline__ void hide_scores_here(uint32_t ts, int c_hi, int c_lo, int c_sink, unsigned groups) {
+    // By 32 columns: most are seen by all 32 rows of the warp, or by none.
+#pragma unroll 1
+    for (int c0 = 0; c0 < kTile; c0 += 32) {
+        uint32_t see = bits_below(c_hi + 1 - c0) & (~bits_below(c_lo - c0) | bits_below(c_sink - c0));
+        see &= ((groups >> (c0 / 16) & 1u) ? 0xFFFFu : 0u) | ((groups >> (c0 / 16 + 1) & 1u) ? 0xFFFF0000u : 0u);
+        if (__all_sync(0xffffffffu, see == ~0u)) continue;
+        uint32_t v[32];
+        if (__any_sync(0xffffffffu, see != 0u)) {
+            tm_ld32(ts + c0, v);
+            tm_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] = (see >> k & 1u) ? v[k] : 0xFF800000u;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] = 0xFF800000u;
+        }
+        tm_st32(ts + c0, v);
+    }
+    tm_wait_st();
+}
+
+// As a function of its own it leaves the softmax's loop to the tiles without any: a prompt of 8192 rows with heads of
+// 128 takes 347 us, 351 with it inline; heads of 64 and a window, where every third tile has some, 67 us and 63 inline.
+__device__ __noinline__ void hide_scores_call(uint32_t ts, int c_hi, int c_lo, int c_sink, unsigned groups) {
+    hide_scores_here(ts, c_hi, c_lo, c_sink, groups);
+}
+template <int D>
+__device__ __forceinline__ void hide_scores(uint32_t ts, int c_hi, int c_lo, int c_sink, unsigned groups) {
+    if (D == 64) hide_scores_here(ts, c_hi, c_lo, c_sink, groups);
+    else hide_scores_call(ts, c_hi, c_lo, c_sink, groups);
+}
+// A row's largest score, and n columns of a row times f: the rare part of a softmax step, out of its loop too.
+__device__ __noinline__ float max_score(uint32_t ts) {
+    float mx = -INFINITY;
+#pragma unroll 1
+    for (int c0 = 0; c0 < kTile; c0 += 64) {
+        uint32_t v[2][32];
+        tm_ld32(ts + c0, v[0]);
+        tm_ld32(ts + c0 + 32, v[1]);
+        tm_wait_ld();
+        mx = max3(mx, max32(v[0]), max32(v[1]));
+    }
+    return mx;
+}
+__device__ __noinline__ void scale_columns(uint32_t to, int n, float f) {
+#pragma unroll 1
+    for (int c0 = 0; c0 < n; c0 += 32) {
+        uint32_t o[32];
+        tm_ld32(to + c0, o);
+        tm_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+        tm_st32(to + c0, o);
+    }
+}
+
+// a / b for a >= 0, b > 0: a 64-bit division is some 100 instructions, and hardly ever needed.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+    return (unsigned long long)(a | b) >> 32 ? a / b : (long long)((unsigned)a / (unsigned)b);
 }
 
 struct PrefillArgs {
@@ -439,7 +495,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
         bar_init(&ctl.q_full, Q8 ? C::kHelpers : 1);
         bar_init(&ctl.q_empty, 1);
         bar_init(&ctl.drain, 1);
-        bar_init(&ctl.joined, 256);
+        bar_init(&ctl.joined, 8);
         bar_init(&ctl.decided, 1);
         for (int i = 0; i < C::kBufs; ++i) {
             bar_init(&ctl.s_full[i], 1);
@@ -530,7 +586,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
             total += ctl.scan[w];
         }
         total *= a.kv_heads;
-        span = max((total + gridDim.x - 1) / gridDim.x, 4ll + C::kItemCost);
+        span = max(quotient(total + gridDim.x - 1, gridDim.x), 4ll + C::kItemCost);
         b0 = span * blockIdx.x;
         b1 = min(total, b0 + span);
         if (b0 < b1 && ahead * a.kv_heads <= b0 && b0 < (ahead + keys) * a.kv_heads) {
@@ -556,7 +612,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
         it.qt = ctl.first_qt;
         request_of(a, it);
         q_tile_of(pa, it);
-        it.h = (int)((b0 - ctl.first_start) / cost_of(pa, it));
+        it.h = (int)quotient(b0 - ctl.first_start, cost_of(pa, it));
         it.start = ctl.first_start + it.h * cost_of(pa, it) + pa.item_cost;
     }
     // An item's tiles [i0, i1) that fall into this span; none of the last item's when only its fixed cost does.
@@ -1033,32 +1089,11 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                         sc = fmaxf(sc0 * back * ex2(*(volatile float *)&ctl.unit[0][at]), kLeast);
                         shift = *(volatile float *)&ctl.unit[1][at];
                     }
-                    if (info.y >> (8 + x) & 1) {  // hidden scores become -inf in place
+                    if (info.y >> (8 + x) & 1) {
                         // columns [c_lo, c_hi] and [0, c_sink) are visible
-                        const int j0 = info.x, groups = info.y;
-                        const int c_hi = min(p, it.end - 1) - j0;
-                        const int c_lo = a.window ? max(p - a.window + 1 - j0, 0) : 0, c_sink = a.window ? a.sinks - j0 : 0;
-                        // By 32 columns: most are seen by all 32 rows of the warp, or by none.
-#pragma unroll 1
-                        for (int c0 = 0; c0 < kTile; c0 += 32) {
-                            // bits: columns c0 .. of this row that it sees
-                            uint32_t see = bits_below(c_hi + 1 - c0) & (~bits_below(c_lo - c0) | bits_below(c_sink - c0));
-                            see &= ((groups >> (c0 / 16) & 1u) ? 0xFFFFu : 0u) |
-                                   ((groups >> (c0 / 16 + 1) & 1u) ? 0xFFFF0000u : 0u);
-                            if (__all_sync(0xffffffffu, see == ~0u)) continue;
-                            uint32_t v[32];
-                            if (__any_sync(0xffffffffu, see != 0u)) {
-                                tm_ld32(ts + c0, v);
-                                tm_wait_ld();
-#pragma unroll
-                                for (int k = 0; k < 32; ++k) v[k] = (see >> k & 1u) ? v[k] : 0xFF800000u;
-                            } else {
-#pragma unroll
-                                for (int k = 0; k < 32; ++k) v[k] = 0xFF800000u;
-                            }
-                            tm_st32(ts + c0, v);
-                        }
-                        tm_wait_st();
+                        const int j0 = info.x;
+                        hide_scores<D>(ts, min(p, it.end - 1) - j0, a.window ? max(p - a.window + 1 - j0, 0) : 0,
+                                       a.window ? a.sinks - j0 : 0, info.y);
                     }
                     // The weights are taken against the running maximum as it stands: a row's maximum is only looked
                     // for where their sum shows that a score passed it too far (or there is none yet).
@@ -1083,14 +1118,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                     };
                     for (int again = __any_sync(0xffffffffu, M == -INFINITY) ? 1 : 0;; again = 1) {
                         if (again) {
-                            float mx = -INFINITY;
-#pragma unroll 1
-                            for (int c0 = 0; c0 < kTile; c0 += 32) {
-                                uint32_t v[32];
-                                tm_ld32(ts + c0, v);
-                                tm_wait_ld();
-                                mx = fmaxf(mx, max32(v));
-                            }
+                            float mx = max_score(ts);
                             mx = mx == -INFINITY ? mx : fmaf(mx, sc, shift);
                             const float now = fmaxf(M, mx), f = now == M ? 1.0f : ex2(M - now);  // 0 from -inf
                             M = now;
@@ -1103,15 +1131,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                                     if (!(ok = warp_wait(&ctl.step[n & 7], (n >> 3) & 1, abort))) break;
                                     fence_after();
                                 }
-#pragma unroll 1
-                                for (int c0 = 0; c0 < D; c0 += 16) {
-                                    uint32_t o[16];
-                                    tm_ld16(to + c0, o);
-                                    tm_wait_ld();
-#pragma unroll
-                                    for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                                    tm_st16(to + c0, o);
-                                }
+                                scale_columns(to, D, f);
                             }
                         }
                         const float off = shift - (M == -INFINITY ? 0.0f : M);
@@ -1158,7 +1178,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
             ++seg;
             // ---- the segment's end ----
             const long long last_unit = it.start + it.n - 1;
-            const int c0 = (int)(it.start / span), c1 = (int)(last_unit / span);
+            const int c0 = (int)quotient(it.start, span), c1 = (int)quotient(last_unit, span);
             const bool wide = (((uintptr_t)a.out | (uintptr_t)(2 * a.ldo)) & 31) == 0;
             const bool poison = *(volatile int *)&ctl.poison != 0;
             float *base = reinterpret_cast<float *>(a.work + kPrefillPartAt);
@@ -1196,20 +1216,22 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
             fence_before();
             if (c0 != c1 && ok) {
                 // ---- shared with other CTAs: the last to arrive adds the parts in span order ----
-                __threadfence();
-                bar_arrive(&ctl.joined);
+                // (one thread's fence covers what the barrier has ordered before it)
+                __syncwarp();
+                if (lane == 0) bar_arrive(&ctl.joined);
                 if (tid == 0 && bar_wait(&ctl.joined, shared & 1, abort)) {
                     int *count = reinterpret_cast<int *>(a.work + kPrefillCounterAt) + c0;
                     __threadfence();
                     const int seen = atomicAdd(count, 1);
                     ctl.last = seen == c1 - c0;
-                    if (seen == c1 - c0) *count = 0;
-                    __threadfence();
+                    if (seen == c1 - c0) {
+                        *count = 0;
+                        __threadfence();
+                    }
                     bar_arrive(&ctl.decided);
                 }
                 ok = warp_wait(&ctl.decided, shared++ & 1, abort);
                 if (ok && *(volatile int *)&ctl.last && row_live) {
-                    __threadfence();
                     constexpr int J = Q8 || D == 64 ? 32 : 64;  // columns at a time: J / 4 loads in flight, J sums
 #pragma unroll 1
                     for (int cc = 0; cc < D; cc += J) {
