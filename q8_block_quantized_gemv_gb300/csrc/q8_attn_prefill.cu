@@ -60,11 +60,12 @@ template <int D, bool Q8> struct Cfg {
     static constexpr int kRaw = Q8 ? kTile * D + kTile * (D / 32) * 4 : 0;
     static constexpr int kSlots = Q8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 10);
     static constexpr int kRawSlots = Q8 ? (D == 128 ? 3 : 4) : 0;
-    static constexpr int kHelpers = Q8 ? 4 : 2;            // warps
+    static constexpr int kHelpers = Q8 ? 6 : 2;            // warps
     static constexpr int kThreads = 32 * (kHelpWarp + kHelpers);
     // What an item costs beside its tiles, in tiles: loading Q, the pipe's fill and drain, the epilogue.  Without it the
-    // CTAs of a long prompt's first rows, 44 short items each, took 835,000 clocks where the others took 740,000.
-    static constexpr int kItemCost = Q8 ? 2 : 4;
+    // CTAs of a long prompt's first rows, 44 short items each, took 835,000 clocks where the others took 740,000.  Over a
+    // Q8_0 cache, 2, 3 and 4 take 640, 582 and 570 us for a prompt of 8192 rows.
+    static constexpr int kItemCost = Q8 ? 4 : 4;
     static constexpr int kRing = 2 * kOp;                  // after Q's two tiles
     static constexpr int kRawAt = kRing + kSlots * kOp;
     static constexpr int kCtl = kRawAt + kRawSlots * kRaw;
@@ -91,7 +92,6 @@ template <int D, bool Q8> struct Control {
     int first_r, first_qt;
     long long first_start;
     long long scan[20];
-    float qscale[2][Q8 ? kRows : 1];  // Q8_0: the powers of two that undo the rows' fp16 scaling, by segment parity
 };
 static_assert(sizeof(Control<128, true>) <= 4096 && sizeof(Control<128, false>) <= 2048, "");
 
@@ -300,6 +300,40 @@ __device__ __forceinline__ int2 tile_info(const int2 *p) {
     return v;
 }
 
+// A row of Q to fp16, in place, by one thread: times a power of two that takes its largest magnitude to [2^9, 2^10), which
+// the result undoes.  Out of line, for the registers of the softmax's loop.
+template <int D> __device__ __noinline__ float row_to_half(unsigned char *row, int swizzle) {
+    uint4 *at = reinterpret_cast<uint4 *>(row);
+    uint32_t mx = 0u;
+#pragma unroll 1  // short code: what a CTA runs once or a few times waits for its instructions
+    for (int c0 = 0; c0 < D / 8; c0 += 8) {
+        uint4 v[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) v[c] = at[(c0 / 8) * kTile * 8 + (c ^ swizzle)];
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            mx = __vmaxu2(__vmaxu2(mx, __vmaxu2(v[c].x & 0x7FFF7FFFu, v[c].y & 0x7FFF7FFFu)),
+                          __vmaxu2(v[c].z & 0x7FFF7FFFu, v[c].w & 0x7FFF7FFFu));
+    }
+    const int ex = min(max((int)(max(mx & 0xFFFFu, mx >> 16) >> 7), 1), 254), up = min(127 + 9 - ex, 126);
+    const float f = __uint_as_float((uint32_t)(up + 127) << 23);
+#pragma unroll 1
+    for (int c0 = 0; c0 < D / 8; c0 += 8) {
+        uint4 v[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) v[c] = at[(c0 / 8) * kTile * 8 + (c ^ swizzle)];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                w[k] = f16x2(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xFFFF0000u) * f);
+            at[(c0 / 8) * kTile * 8 + (c ^ swizzle)] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+    return __uint_as_float((uint32_t)(127 - up) << 23);
+}
+
 // The scores at ts that their row does not see become -inf in place: it sees columns c_lo .. c_hi and 0 .. c_sink - 1
 // of the 16-column groups that have a bit.
 __device__ __forceinline__ void hide_scores_here(uint32_t ts, int c_hi, int c_lo, int c_sink, unsigned groups) {
@@ -492,7 +526,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
             bar_init(&ctl.raw_empty[i], C::kHelpers);
         }
         bar_init(&ctl.q_raw, 1);
-        bar_init(&ctl.q_full, Q8 ? C::kHelpers : 1);
+        bar_init(&ctl.q_full, Q8 ? 8 : 1);
         bar_init(&ctl.q_empty, 1);
         bar_init(&ctl.drain, 1);
         bar_init(&ctl.joined, 8);
@@ -696,8 +730,8 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                             const int u = it.tile(i), pb = it.p_min + pa.tile_tokens;
                             const bool gone = groups != 0xFFu;
                             ctl.tile[(cnt >> 1) & 7] = make_int2(
-                                u * kTile, (int)groups | (gone || it.partial(a, u, it.p_min, pb - 1) ? 256 : 0) |
-                                               (gone || it.partial(a, u, pb, pb + pa.tile_tokens - 1) ? 512 : 0));
+                                u * kTile, (int)groups | (gone || it.partial(a, u, it.p_min, min(pb - 1, it.p_max)) ? 256 : 0) |
+                                               (pb <= it.p_max && (gone || it.partial(a, u, pb, it.p_max)) ? 512 : 0));
                         }
                         const unsigned bytes = __popc(groups) * 16 * (Q8 ? D + D / 32 * 4 : 2 * D);
                         bar_arrive_tx(full, bytes);
@@ -874,7 +908,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
         }
         __syncwarp();
     } else if (warp >= kHelpWarp) {
-        // ---- Q, and what the tiles need before the MMAs ----
+        // ---- what the tiles need before the MMAs ----
         const int ht = tid - 32 * kHelpWarp;
         constexpr int HT = 32 * C::kHelpers;
         unsigned cnt = 0, seg = 0;
@@ -882,33 +916,6 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
         for (; more; advance()) {
             if (!ok) break;
             constexpr int CH = D / 8;  // 16-byte chunks of an operand row
-            if (Q8) {  // Q to fp16, in place
-                if (!(ok = warp_wait(&ctl.q_raw, seg & 1, abort))) break;
-#pragma unroll 4
-                for (int e = ht; e < kRows * CH; e += HT) {
-                    const int x = e / CH, c = e % CH;
-                    uint4 *at = reinterpret_cast<uint4 *>(smem + (x / kTile) * C::kOp + (c / 8) * kTile * 128 +
-                                                          (x % kTile) * 128 + (((c & 7) ^ (x & 7)) << 4));
-                    const uint4 v = *at;
-                    uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                    uint32_t mx = 0u;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) mx = max(mx, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
-#pragma unroll
-                    for (int o = 1; o < CH; o <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                    // times a power of two that takes the row's largest magnitude to [2^9, 2^10)
-                    const int ex = min(max((int)(mx >> 7), 1), 254), up = min(127 + 9 - ex, 126);
-                    const float f = __uint_as_float((uint32_t)(up + 127) << 23);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        w[k] = f16x2(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xFFFF0000u) * f);
-                    *at = make_uint4(w[0], w[1], w[2], w[3]);
-                    if (c == 0) ctl.qscale[seg & 1][Q8 ? x : 0] = __uint_as_float((uint32_t)(127 - up) << 23);
-                }
-                fence_async();
-                __syncwarp();
-                if (lane == 0) bar_arrive(&ctl.q_full);
-            }
             int v_ex = 0;
             for (int i = i0; i < i1 && ok; ++i) {
                 const int u = it.tile(i), j0 = u * kTile;
@@ -920,10 +927,11 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                 for (int kv = 0; kv < 2 && ok; ++kv, ++cnt) {
                     const unsigned s = cnt % C::kSlots, par = (cnt / C::kSlots) & 1;
                     unsigned char *op = smem + C::kRing + s * C::kOp;
-                    if (!Q8) {
+                    if constexpr (!Q8) {
                         if (!(ok = warp_wait(&ctl.full[s], par, abort))) break;
-                        const unsigned groups = ctl.tile[(cnt >> 1) & 7].y & 255u;
-                        if (kv && (groups != 0xFFu || it.partial(a, u))) {
+                        const int info = ctl.tile[(cnt >> 1) & 7].y;
+                        const unsigned groups = info & 255u;
+                        if (kv && (info & 768)) {
                             // Thread ht takes chunk ht % CH of every RS-th key, eight loads in flight.
                             bool found = false;
                             constexpr int RS = HT / CH, B = 8;
@@ -968,70 +976,85 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                     if (!(ok = warp_wait(&ctl.raw_full[rs], rpar, abort))) break;
                     const unsigned char *raw = smem + C::kRawAt + rs * C::kRaw;
                     const float *scl = reinterpret_cast<const float *>(raw + kTile * D);
-                    const unsigned groups = ctl.tile[(cnt >> 1) & 7].y & 255u;
-                    const bool part = groups != 0xFFu || it.partial(a, u);
+                    const int info = ctl.tile[(cnt >> 1) & 7].y;
+                    const unsigned groups = info & 255u;
+                    const bool part = (info & 768) != 0;
                     constexpr int NB = D / 32;
-                    float mx = 0.0f;  // the tile's largest finite scale: every warp looks for itself, four at a time
+                    // The tile's largest finite scale, by its bits: every warp looks for itself, four at a time.
+                    uint32_t mx = 0u;
 #pragma unroll
                     for (int y = 0; y < kTile * NB / 128; ++y) {
-                        const int e = (y * 32 + lane) * 4;
-                        const float4 f = *reinterpret_cast<const float4 *>(scl + e);
-                        float m = fmaxf(fmaxf(fabsf(f.x), fabsf(f.y)), fmaxf(fabsf(f.z), fabsf(f.w)));
-                        if (part || !(m < INFINITY)) {  // one by one, what somebody sees and is finite
-                            m = 0.0f;
-                            const float g[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-                            for (int w = 0; w < 4; ++w)
-                                if (fabsf(g[w]) < INFINITY && (!part || live((e + w) / NB, groups))) m = fmaxf(m, fabsf(g[w]));
-                        }
-                        mx = fmaxf(mx, m);
+                        const uint4 f = *reinterpret_cast<const uint4 *>(scl + (y * 32 + lane) * 4);
+                        mx = max(mx, max(max(f.x & 0x7FFFFFFFu, f.y & 0x7FFFFFFFu), max(f.z & 0x7FFFFFFFu, f.w & 0x7FFFFFFFu)));
                     }
-#pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                    mx = __reduce_max_sync(0xffffffffu, mx);
+                    if (part || mx >= 0x7F800000u) {  // one by one, what somebody sees and is finite
+                        mx = 0u;
+#pragma unroll 1
+                        for (int e = lane; e < kTile * NB; e += 32) {
+                            const uint32_t m = __float_as_uint(scl[e]) & 0x7FFFFFFFu;
+                            if (m < 0x7F800000u && (!part || live(e / NB, groups))) mx = max(mx, m);
+                        }
+                        mx = __reduce_max_sync(0xffffffffu, mx);
+                    }
                     // The values' unit only grows within a segment, and neither is below 2^-63, so that a tile of
                     // zeros does not take the row sums, which are kept apart from the units, out of fp32's range.
-                    int ex = min(max((int)(__float_as_uint(mx) >> 23), 64), 252);
+                    int ex = min(max((int)(mx >> 23), 64), 252);
                     if (kv) ex = v_ex = max(v_ex, ex);
                     const float down = __uint_as_float((uint32_t)(254 - ex) << 23);  // 2^-(ex - 127)
                     bool found = false;
                     // Thread ht takes 16 codes of rows r0, r0 + HT / RC, ...: a step of whole swizzle periods, so that
                     // all addresses are its first ones plus constants.
                     constexpr int RC = D / 16, RS = HT / RC;  // chunks of 16 codes a row, rows a pass
-                    static_assert(RS % 8 == 0 && kTile % RS == 0, "");
+                    static_assert(RS % 8 == 0, "");
                     const int ch = ht % RC, r0 = ht / RC;
                     const unsigned char *src = raw + r0 * D + ch * 16;
                     const float *sc = scl + r0 * NB + ch / 2;
                     unsigned char *to = op + (ch / 4) * kTile * 128 + r0 * 128;
-                    const bool swap = (ch >> 2) & 1;  // the two halves of a quarter warp write different banks
+                    // Two threads of a quarter warp that read the same chunk's place write its halves in turn, so that
+                    // they write different banks.
+                    const bool swap = (ch >> 2) & 1;
                     const int da = (((2 * ch) & 7) ^ (r0 & 7)) * 16, db = da ^ 16;
                     unsigned char *first = to + (swap ? db : da), *second = to + (swap ? da : db);
+                    constexpr int B = 3;  // rows at a time, so that their loads are in flight together
 #pragma unroll
-                    for (int y = 0; y < kTile / RS; ++y) {
-                        float f = sc[y * RS * NB] * down;
-                        uint4 v = *reinterpret_cast<const uint4 *>(src + y * RS * D);
+                    for (int y = 0; y * RS < kTile; y += B) {
+                        uint4 v[B];
+                        float f[B];
+#pragma unroll
+                        for (int z = 0; z < B; ++z) {
+                            if ((y + z + 1) * RS > kTile && r0 + (y + z) * RS >= kTile) break;
+                            v[z] = *reinterpret_cast<const uint4 *>(src + (y + z) * RS * D);
+                            f[z] = sc[(y + z) * RS * NB] * down;
+                        }
                         if (part) {
-                            const bool see = live(r0 + y * RS, groups);
-                            if (!see || (kv && !(fabsf(f) < INFINITY))) {
-                                found = found || see;
-                                v = make_uint4(0u, 0u, 0u, 0u);
-                                f = 0.0f;
+#pragma unroll
+                            for (int z = 0; z < B; ++z) {
+                                const bool see = live(r0 + (y + z) * RS, groups);
+                                if (r0 + (y + z) * RS < kTile && (!see || (kv && !(fabsf(f[z]) < INFINITY)))) {
+                                    found = found || see;
+                                    v[z] = make_uint4(0u, 0u, 0u, 0u);
+                                    f[z] = 0.0f;
+                                }
                             }
                         }
-                        const __half2 f2 = __float2half2_rn(f);
-                        const uint32_t w[4] = {v.x ^ 0x80808080u, v.y ^ 0x80808080u, v.z ^ 0x80808080u, v.w ^ 0x80808080u};
-                        uint32_t h[8];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
+                        for (int z = 0; z < B; ++z) {
+                            if ((y + z + 1) * RS > kTile && r0 + (y + z) * RS >= kTile) break;
+                            const __half2 f2 = __float2half2_rn(f[z]);
+                            const uint32_t w[4] = {(swap ? v[z].z : v[z].x) ^ 0x80808080u, (swap ? v[z].w : v[z].y) ^ 0x80808080u,
+                                                   (swap ? v[z].x : v[z].z) ^ 0x80808080u, (swap ? v[z].y : v[z].w) ^ 0x80808080u};
+                            uint32_t h[8];
 #pragma unroll
-                            for (int z = 0; z < 2; ++z) {
-                                const uint32_t b = __byte_perm(w[k], 0x64646464u, z ? 0x4342 : 0x4140);
+                            for (int k = 0; k < 8; ++k) {
+                                const uint32_t b = __byte_perm(w[k / 2], 0x64646464u, k % 2 ? 0x4342 : 0x4140);
                                 const __half2 q = __hmul2(__hsub2(*reinterpret_cast<const __half2 *>(&b),
                                                                   __half2half2(__ushort_as_half(0x6480))), f2);
-                                h[2 * k + z] = *reinterpret_cast<const uint32_t *>(&q);
+                                h[k] = *reinterpret_cast<const uint32_t *>(&q);
                             }
-                        const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-                        *reinterpret_cast<uint4 *>(first + y * RS * 128) = swap ? hi : lo;
-                        *reinterpret_cast<uint4 *>(second + y * RS * 128) = swap ? lo : hi;
+                            *reinterpret_cast<uint4 *>(first + (y + z) * RS * 128) = make_uint4(h[0], h[1], h[2], h[3]);
+                            *reinterpret_cast<uint4 *>(second + (y + z) * RS * 128) = make_uint4(h[4], h[5], h[6], h[7]);
+                        }
                     }
                     if (found) *(volatile int *)&ctl.poison = 1;
                     if (ht == 0) ctl.unit[kv][(cnt >> 1) & 7] = (float)(ex - 127);
@@ -1069,6 +1092,14 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
             const bool row_live = whole_row && tok < it.tokens;
             const int p = it.p_min + tok;
             float M = row_live ? -INFINITY : 0.0f, l = 0.0f;  // rows beyond the item's ask for nothing
+            float back = 1.0f;
+            if constexpr (Q8) {
+                if (!(ok = warp_wait(&ctl.q_raw, seg & 1, abort))) break;
+                if (row_live) back = row_to_half<D>(smem + x * C::kOp + y * 128, y & 7);
+                fence_async();
+                __syncwarp();
+                if (lane == 0) bar_arrive(&ctl.q_full);
+            }
             if (active) {
                 float sc = sc0;
                 for (int i = i0; i < i1 && ok; ++i) {
@@ -1085,7 +1116,6 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                     if (Q8) {
                         const unsigned cv = ck + 1;
                         if (!(ok = warp_wait(&ctl.ready[cv % C::kSlots], (cv / C::kSlots) & 1, abort))) break;
-                        const float back = *(volatile float *)&ctl.qscale[seg & 1][Q8 ? rx : 0];
                         sc = fmaxf(sc0 * back * ex2(*(volatile float *)&ctl.unit[0][at]), kLeast);
                         shift = *(volatile float *)&ctl.unit[1][at];
                     }
