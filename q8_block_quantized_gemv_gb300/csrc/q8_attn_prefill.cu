@@ -15,8 +15,8 @@
 // the rest load Q and prepare values:
 //   bf16 cache: K and V tiles arrive by TMA straight in the MMA's 128-byte swizzle; the helpers (two warps) look through
 //     the V tiles that some row does not see whole, and clear what nobody sees;
-//   Q8_0 cache: codes and scales arrive by bulk copies, and the helpers (four warps) turn them into fp16 operands,
-//     code * scale / unit with one power of two `unit` a tile, and Q into fp16 with one a row: 11 significant bits.
+//   Q8_0 cache: codes and scales arrive by bulk copies, and the helpers (six warps) turn them into fp16 operands,
+//     code * scale / unit with one power of two `unit` a tile, as the softmax threads do Q with one a row: 11 significant bits.
 //     (bf16 operands would cost the scores and values 8-bit roundings: measured 0.0029 against 0.0017 relative error.)
 //
 // The tiles of all items are one list, cut into equal spans, one for each CTA (one CTA per SM); an item that crosses
@@ -65,7 +65,7 @@ template <int D, bool Q8> struct Cfg {
     // What an item costs beside its tiles, in tiles: loading Q, the pipe's fill and drain, the epilogue.  Without it the
     // CTAs of a long prompt's first rows, 44 short items each, took 835,000 clocks where the others took 740,000.  Over a
     // Q8_0 cache, 2, 3 and 4 take 640, 582 and 570 us for a prompt of 8192 rows.
-    static constexpr int kItemCost = Q8 ? 4 : 4;
+    static constexpr int kItemCost = 4;
     static constexpr int kRing = 2 * kOp;                  // after Q's two tiles
     static constexpr int kRawAt = kRing + kSlots * kOp;
     static constexpr int kCtl = kRawAt + kRawSlots * kRaw;
