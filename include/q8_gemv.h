@@ -19,7 +19,8 @@
  *
  * Conventions shared by every entry point:
  *   - The caller owns every buffer and the library allocates no memory.  Its only state is read-only caches (per
- *     device: SM count, resident clusters), the device fault words (q8_device_fault), the planner overrides of
+ *     device: SM count, resident clusters, which kernels may use their shared memory; the address of the driver's
+ *     tensor-map encoder), the device fault words (q8_device_fault), the planner overrides of
  *     q8_set_tuning, the residual norm's 64 static completion counters (used only by its one-launch fold; see
  *     q8_gemv_residual_norm for the limit this puts on overlapping calls) and the 32 static counters of
  *     q8_gemv_residual_norm_noalloc (see there).

@@ -3,9 +3,9 @@
 // Every visible key and value is read once for all query heads of its cache head, 4 flops a byte and head: HBM bounds
 // the kernel until contexts are so short that latency does.  So the work is cut by bytes, not by requests: the visible
 // tokens of all (request, cache head) items in a row are a list of 16-token units, and each CTA (one per SM) takes an
-// equal contiguous span of it, computed on the device from lens.  Its 8 warps take the span's units in turn, each
-// with a ring of its own in shared memory filled by cp.async (prefetch runs on across items; no CTA barrier but at an
-// item's end), a running maximum and sum, and accumulators in registers.
+// equal contiguous span of it, computed on the device from lens.  Its 8 warps (12 over a Q8_0 cache, up to 8 heads to a
+// cache head) take the span's units in turn, each with a ring of its own in shared memory filled by cp.async (prefetch
+// runs on across items; no CTA barrier but at an item's end), a running maximum and sum, and accumulators in registers.
 //
 // Products run transposed on mma.sync m16n8k16, as 16 tokens (or 16 of the head's values) by 8 query heads: a unit's
 // S^T = K Q^T, then O^T += V^T P^T, so up to 8 heads sharing a cache head cost what one does.  tcgen05 has nothing to
@@ -14,6 +14,13 @@
 // At an item's end the warps' parts are summed through shared memory in warp order.  An item that crosses spans
 // leaves parts in the workspace; the CTA that arrives last (a counter per first CTA, left at zero) adds them in span
 // order, so the result does not depend on who was last.
+//
+// Measured, heads of 128, 32 over 8 cache heads: one request of 131,072 tokens, bf16, 84 us = 6.4 TB/s (95% of a copy's
+// rate); 15 requests with 81,000 tokens in all, Q8_0, 43 us = 4.4 TB/s.  There a unit costs about 580 instructions (the
+// codes' way to fp16, the scales), 145 for each of the SM's schedulers, and 200 clocks of the SM's share of the memory, and
+// neither is full: 54% of the issue slots, 65% of the bandwidth.  8 warps take 44 us, 16 with their 128 registers 56.
+// Heads of 64, 24 over 8, a window of 4,096 in 64 requests: 89 us = 6.0 TB/s.  One request of 203 tokens, 32 heads: 5.2
+// us, the chain from its length over table, keys and sums to the output.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -25,7 +32,7 @@ namespace q8 {
 namespace {
 
 constexpr int kUnit = 16;  // tokens of a unit; a page holds whole units
-constexpr int kMinSpan = 16;
+constexpr int kMinSpan = 16;  // units: two a warp, below which a further CTA would cost more to join than it takes over
 constexpr int kWholeUnits = 64;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;  // log2: the running maximum moves when a score passes it by more than this

@@ -16,8 +16,8 @@
 //   bf16 cache: K and V tiles arrive by TMA straight in the MMA's 128-byte swizzle; the helpers (two warps) look through
 //     the V tiles that some row does not see whole, and clear what nobody sees;
 //   Q8_0 cache: codes and scales arrive by bulk copies, and the helpers (six warps) turn them into fp16 operands,
-//     code * scale / unit with one power of two `unit` a tile, as the softmax threads do Q with one a row: 11 significant bits.
-//     (bf16 operands would cost the scores and values 8-bit roundings: measured 0.0029 against 0.0017 relative error.)
+//     code * scale / unit with one power of two `unit` a tile, as the softmax threads do Q with one a row: 11 significant
+//     bits.  (bf16 operands would cost the scores and values 8-bit roundings: measured 0.0029 against 0.0017 relative error.)
 //
 // The tiles of all items are one list, cut into equal spans, one for each CTA (one CTA per SM); an item that crosses
 // spans leaves fp32 parts in the workspace, which the CTA that arrives last adds in span order.
@@ -27,6 +27,15 @@
 // the end (a rare, slow walk).
 //
 // Every wait is bounded (about two seconds); one that runs out records a fault, and the CTA drains and returns.
+//
+// Measured, 32 heads of 128 over 8 cache heads: a prompt of 8,192 rows 347 us over a bf16 cache = 1.58 PFLOP/s (81% of a
+// large bf16 product's rate: the MMAs wait for the softmax some of the time, 66% of the tensor pipe's cycles are taken),
+// 570 us over a Q8_0 cache, where a tile goes through five hands (codes, conversion, S, softmax, O) and nothing is full:
+// 27% of the tensor pipe's cycles and 38% of the issue slots in a chunk of 509 rows, which takes 66 us (1.5 us more with
+// four conversion warps; as long with the conversion finished in registers before its operand's place is free, or with
+// the values' place given back before the keys').
+// 512 rows after 4,096 tokens, 32 cache heads: 51 us.  A call's fixed part is 11 us: the cut of the list 2, the first Q
+// and keys 3, a join 4 and the launch.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -13,7 +13,7 @@ namespace {
 // The work is two prefix sums over R requests (new rows, new pages) and one lookup for each row and each new page: a
 // few hundred KB at the most, so latency bounds it.  One launch, no CTA waits for another: every CTA takes both prefix
 // sums over all R requests for itself (R lengths from L2, the sums in shared memory), then its share of the rows and
-// of the new pages, each found by a binary search in the sums.
+// of the new pages, each found by a binary search in the sums.  (16 requests 3.5 us; 1,500 requests with 30,011 rows 4.7 us.)
 struct SlotArgs {
     const int *cached, *fresh, *free_pages, *head;
     int *table, *lens, *row_start, *positions, *next_head;
@@ -114,7 +114,8 @@ __global__ void __launch_bounds__(kSlotThreads) slots_kernel(SlotArgs a) {
 // memory bounds it once there are enough rows, and latency before that -- if a value costs few enough instructions.
 // A lane holds eight values of a head, as two chunks of four: with the half layout a chunk and its partner rotary_dim
 // / 2 on, so that the rotation needs no other lane; otherwise two neighbours.  (Four values a lane and shuffles for the
-// partners took twice the instructions: 82 us for 8191 rows of 32 + 2 x 8 heads, 55 us now.)
+// partners took twice the instructions: 82 us for 8191 rows of 32 + 2 x 8 heads, 55 us now, 5.5 TB/s, with 55% of the
+// issue slots taken; 16 rows of 32 + 2 x 32 heads take 1.9 us.)
 struct AppendArgs {
     const float *q, *k, *v, *qg, *kg, *table;
     const int *positions;
