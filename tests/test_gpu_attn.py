@@ -130,7 +130,7 @@ def queries(torch, rows, heads, dim, seed, pad=0):
     return x.cuda(), x.float().numpy().astype(np.float64)[:, :heads * dim].reshape(rows, heads, dim)
 
 
-def judge(got, want, tol):
+def agree(got, want, tol):
     got = got.float().cpu().numpy().astype(np.float64).reshape(want.shape)
     assert np.all(np.isfinite(got))
     over = np.abs(got - want) - tol
@@ -186,7 +186,7 @@ def test_decode(dev, work, kind, lens, heads, kv_heads, dim, page, window, sinks
     q, qn = queries(dev, len(lens), heads, dim, 12)
     scale = dim ** -0.5
     got = q8.attn_decode(q, p.cache, p.table_dev, p.lens_dev, window=window, sinks=sinks, workspace=work)
-    judge(got, *expected(p, qn, list(range(len(lens) + 1)), scale, window, sinks))
+    agree(got, *expected(p, qn, list(range(len(lens) + 1)), scale, window, sinks))
 
 
 def hide(torch, p, window, sinks):
@@ -213,7 +213,7 @@ def test_decode_long_split(dev, work, kind):
     p = Paged(dev, lens, 2, 128, 64, kind, 21, junk="inf", extra_width=2)
     q, qn = queries(dev, len(lens), 8, 128, 22)
     got = q8.attn_decode(q, p.cache, p.table_dev, p.lens_dev, scale=0.1, workspace=work)
-    judge(got, *expected(p, qn, list(range(5)), 0.1, 0, 0))
+    agree(got, *expected(p, qn, list(range(5)), 0.1, 0, 0))
     for ws in (work, None):
         again = q8.attn_decode(q, p.cache, p.table_dev, p.lens_dev, scale=0.1, workspace=ws)
         assert dev.equal(got.view(dev.int16), again.view(dev.int16))
@@ -261,7 +261,7 @@ def test_decode_strides_stream_and_missing_pages(dev, work, kind):
         for h in range(heads):
             a, t16, t8 = reference(qn[r:r + 1, h], p.k[r][:, h // 3], p.v[r][:, h // 3], ok, dim ** -0.5)
             o[r, h], tol[r, h] = a, t16 if kind == "bf16" else t8
-    judge(out[:, :heads * dim], o, tol)
+    agree(out[:, :heads * dim], o, tol)
     assert torch.all(out[:, heads * dim:] == 7.0) and not np.any(out[2, :heads * dim].float().cpu().numpy())
 
 
@@ -277,7 +277,7 @@ def test_decode_length_beyond_table(dev, work):
         o, tol = np.zeros((1, 2, 64)), np.zeros((1, 2, 64))
         for h in range(2):
             o[0, h], tol[0, h], _ = reference(qn[:, h], p.k[0][:, 0], p.v[0][:, 0], ok, 64 ** -0.5)
-        judge(got, o, tol)
+        agree(got, o, tol)
 
 
 def test_offsets_past_32_bits(dev, work):
@@ -308,9 +308,9 @@ def test_offsets_past_32_bits(dev, work):
     ok = np.tril(np.ones((n, n), dtype=bool))
     for h in range(heads):
         o[:, h], tol[:, h], _ = reference(qn[:, h], k[:, h], v[:, h], ok, dim ** -0.5)
-    judge(q8.attn_decode(q[-1:], cache, table, lens, workspace=work), o[-1:], tol[-1:])
+    agree(q8.attn_decode(q[-1:], cache, table, lens, workspace=work), o[-1:], tol[-1:])
     starts = torch.tensor([0, n], dtype=torch.int32, device="cuda")
-    judge(q8.attn_prefill(q, cache, table, lens, starts, workspace=work), o, tol)
+    agree(q8.attn_prefill(q, cache, table, lens, starts, workspace=work), o, tol)
 
 
 # ---- prefill --------------------------------------------------------------------------------------------------------
@@ -341,7 +341,7 @@ def test_prefill(dev, work, kind, lens, counts, pad, heads, kv_heads, dim, page,
     q, qn = queries(dev, starts[-1] + pad, heads, dim, 72)
     got = q8.attn_prefill(q, p.cache, p.table_dev, p.lens_dev, dev.tensor(starts, dtype=dev.int32, device="cuda"),
                           window=window, sinks=sinks, workspace=work)
-    judge(got, *expected(p, qn, starts, dim ** -0.5, window, sinks))
+    agree(got, *expected(p, qn, starts, dim ** -0.5, window, sinks))
     assert not pad or not np.any(got[starts[-1]:].float().cpu().numpy())
 
 
@@ -355,7 +355,7 @@ def test_prefill_long_context(dev, work, kind):
     q, qn = queries(dev, 200, 8, 128, 82)
     sd = dev.tensor(starts, dtype=dev.int32, device="cuda")
     got = q8.attn_prefill(q, p.cache, p.table_dev, p.lens_dev, sd, workspace=work)
-    judge(got, *expected(p, qn, starts, 128 ** -0.5, 0, 0))
+    agree(got, *expected(p, qn, starts, 128 ** -0.5, 0, 0))
     again = q8.attn_prefill(q, p.cache, p.table_dev, p.lens_dev, sd)
     assert dev.equal(got.view(dev.int16), again.view(dev.int16))
 
@@ -404,8 +404,8 @@ def test_prefill_matches_decode(dev, work):
     b = q8.attn_prefill(q, p.cache, p.table_dev, p.lens_dev, dev.arange(5, dtype=dev.int32, device="cuda"),
                         workspace=work)
     o, tol = expected(p, qn, list(range(5)), 128 ** -0.5, 0, 0)
-    judge(a, o, tol)
-    judge(b, o, tol)
+    agree(a, o, tol)
+    agree(b, o, tol)
 
 
 # ---- slots ----------------------------------------------------------------------------------------------------------
