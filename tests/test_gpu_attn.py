@@ -489,7 +489,10 @@ def plain_append(x, gamma, eps, table, pos, rot, interleaved):
 @pytest.mark.parametrize("rows,heads,kv_heads,dim,page,rot,interleaved,norm", [
     (1, 1, 1, 128, 16, 128, False, "qk"), (3, 8, 2, 64, 48, 64, True, "none"), (16, 32, 32, 128, 16, 64, False, "q"),
     (37, 5, 1, 64, 16, 16, True, "k"), (130, 12, 4, 128, 32, 96, False, "qk"), (130, 12, 4, 128, 32, 104, True, "qk"),
-    (9, 3, 3, 64, 16, 0, False, "none"), (9, 3, 3, 64, 16, 8, False, "qk"), (1000, 7, 7, 64, 64, 40, False, "qk")])
+    (9, 3, 3, 64, 16, 0, False, "none"), (9, 3, 3, 64, 16, 8, False, "qk"), (1000, 7, 7, 64, 64, 40, False, "qk"),
+    # enough values for four heads a lane group, head counts that end inside one
+    (601, 13, 5, 128, 16, 128, False, "qk"), (601, 13, 5, 128, 16, 72, True, "q"), (1103, 11, 7, 64, 48, 64, False, "k"),
+    (1103, 11, 7, 64, 48, 24, True, "qk"), (1103, 13, 6, 64, 48, 0, False, "none")])
 def test_append(dev, kind, rows, heads, kv_heads, dim, page, rot, interleaved, norm):
     import q8_block_quantized_gemv_gb300 as q8
     torch = dev
