@@ -72,9 +72,10 @@ template <int D, bool Q8> struct Cfg {
     static constexpr int kHelpers = Q8 ? 6 : 2;            // warps
     static constexpr int kThreads = 32 * (kHelpWarp + kHelpers);
     // What an item costs beside its tiles, in tiles: loading Q, the pipe's fill and drain, the epilogue.  Without it the
-    // CTAs of a long prompt's first rows, 44 short items each, took 835,000 clocks where the others took 740,000.  Over a
-    // Q8_0 cache, 2, 3 and 4 take 640, 582 and 570 us for a prompt of 8192 rows.
-    static constexpr int kItemCost = 4;
+    // CTAs of a long prompt's first rows, 44 short items each, took 835,000 clocks where the others took 740,000.  2, 3, 4
+    // and 6 take 368, 348, 347 and 358 us for a prompt of 8192 rows, 51.6, 50.3, 51.3 and 50.3 for a chunk of 512, 63.0,
+    // 62.0, 63.2 and 63.9 under a window; over a Q8_0 cache 2, 3 and 4 take 640, 582 and 570 us for the prompt.
+    static constexpr int kItemCost = Q8 ? 4 : 3;
     static constexpr int kRing = 2 * kOp;                  // after Q's two tiles
     static constexpr int kRawAt = kRing + kSlots * kOp;
     static constexpr int kCtl = kRawAt + kRawSlots * kRaw;
