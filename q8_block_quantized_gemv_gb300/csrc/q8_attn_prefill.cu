@@ -415,9 +415,11 @@ struct PrefillArgs {
     int item_cost;   // in key tiles
 };
 
-// Two query tiles of one cache head: tokens tok0 .. tok0 + tokens - 1 of request r, tile_tokens to a tile; row y of a tile is token y / group, head y % group of those that share the cache head.  The
-// item's key tiles are [0, us) for the sinks and [ul, ul + n - us).  In the list
-// an item takes item_cost + n places, the tiles last.
+// Two query tiles of one cache head: tokens tok0 .. tok0 + tokens - 1 of request r, tile_tokens to a tile; row y of a tile
+// is token y / group, head y % group of those that share the cache head.  The item's key tiles are us from key 0 for the
+// sinks, and n - us from key ul.  A window's first tile starts with the run of its first key, not at a whole tile: a prompt
+// of 4097 rows, window 1024, takes 59 us, 61.5 from whole tiles.  In the list an item takes item_cost + n places, the tiles
+// last.
 struct Item {
     int r, qt, h;
     long long start;  // of its tiles in the list, the fixed cost behind it
@@ -425,23 +427,23 @@ struct Item {
     int tok0, tokens;
     int p_min, p_max, end, lo, us, ul, n;
 
-    __device__ __forceinline__ int tile(int i) const { return i < us ? i : ul + (i - us); }
-    // Whether some row of the item does not see all of tile u, pages aside.
-    __device__ __forceinline__ bool partial(const AttnArgs &a, int u) const { return partial(a, u, p_min, p_max); }
+    __device__ __forceinline__ int tile(int i) const { return i < us ? i * kTile : ul + (i - us) * kTile; }  // its first key
+    // Whether some row of the item does not see all of the tile from key j0, pages aside.
+    __device__ __forceinline__ bool partial(const AttnArgs &a, int j0) const { return partial(a, j0, p_min, p_max); }
     // The same for its rows at positions p0 .. p1.
-    __device__ __forceinline__ bool partial(const AttnArgs &a, int u, int p0, int p1) const {
-        const int j0 = u * kTile;
+    __device__ __forceinline__ bool partial(const AttnArgs &a, int j0, int p0, int p1) const {
         return j0 + kTile > end || j0 + kTile - 1 > p0 || (a.window && p1 - j0 >= a.window && j0 + kTile > a.sinks);
     }
 };
 // Key tiles that rows at positions p_min .. p_max visit.
-__device__ __forceinline__ void span_of(const AttnArgs &a, Item &x) {
+__device__ __forceinline__ void span_of(const PrefillArgs &pa, Item &x) {
+    const AttnArgs &a = pa.a;
     x.end = min(max(x.p_max + 1, 0), a.width * a.page_size);
     x.lo = a.window ? min(max(x.p_min - a.window + 1, 0), x.end) : 0;
     const int sinks = a.window ? min(a.sinks, x.lo) : 0;
     x.us = (sinks + kTile - 1) / kTile;
-    x.ul = max(x.lo / kTile, x.us);
-    x.n = x.us + max(0, (x.end + kTile - 1) / kTile - x.ul);
+    x.ul = max(x.lo & -pa.run, x.us * kTile);
+    x.n = x.us + (max(x.end - x.ul, 0) + kTile - 1) / kTile;
 }
 __device__ __forceinline__ void request_of(const int *row_start, const int *lens, int rows, Item &x) {
     const int t0 = min(max(row_start[x.r], 0), rows), t1 = min(max(row_start[x.r + 1], t0), rows);
@@ -458,7 +460,7 @@ __device__ __forceinline__ void q_tile_of(const PrefillArgs &pa, Item &x) {
     x.tokens = min(2 * pa.tile_tokens, x.all - x.tok0);
     x.p_min = x.pos0 + x.tok0;
     x.p_max = x.p_min + x.tokens - 1;
-    span_of(pa.a, x);
+    span_of(pa, x);
 }
 __device__ __forceinline__ long long cost_of(const PrefillArgs &pa, const Item &x) {
     return x.n ? x.n + pa.item_cost : 0;
@@ -489,17 +491,17 @@ __device__ __forceinline__ bool sees(const AttnArgs &a, int p, int j) {
 template <int D, bool Q8>
 __device__ __noinline__ void add_nonfinite(const AttnArgs &a, const Item it, int i0, int i1, int p, int c0, float *o) {
     for (int i = i0; i < i1; ++i) {
-        const int u = it.tile(i);
+        const int j0 = it.tile(i);
         for (int c = 0; c < kTile; ++c) {
-            const int j = u * kTile + c;
+            const int j = j0 + c;
             if (j >= it.end) break;
             if (!sees(a, p, j)) continue;
             const int page = a.table[(size_t)it.r * a.pitch + j / a.page_size];
             if (page < 0 || page >= a.pages) continue;
             // only tiles that some row does not see whole were cleared
-            bool cleared = it.partial(a, u);
+            bool cleared = it.partial(a, j0);
             for (int b = 0; b < kTile / 16 && !cleared; ++b) {
-                const int pg = a.table[(size_t)it.r * a.pitch + (u * kTile + 16 * b) / a.page_size];
+                const int pg = a.table[(size_t)it.r * a.pitch + (j0 + 16 * b) / a.page_size];
                 cleared = pg < 0 || pg >= a.pages;
             }
             if (!cleared) break;
@@ -708,7 +710,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
             const int *row = a.table + (size_t)it.r * a.pitch;
             int page = -1, off = 0;
             auto look = [&](int i) {
-                const int j = it.tile(i) * kTile + lane * pa.run;
+                const int j = it.tile(i) + lane * pa.run;
                 page = -1;
                 if (lane < runs && j < it.end) {
                     page = row[j / a.page_size];
@@ -737,11 +739,11 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                     if (!Q8) slot_used(s, steps + (i - i0) + kv);
                     if (lane == 0) {
                         if (kv == 0) {
-                            const int u = it.tile(i), pb = it.p_min + pa.tile_tokens;
+                            const int j0 = it.tile(i), pb = it.p_min + pa.tile_tokens;
                             const bool gone = groups != 0xFFu;
                             ctl.tile[(cnt >> 1) & 7] = make_int2(
-                                u * kTile, (int)groups | (gone || it.partial(a, u, it.p_min, min(pb - 1, it.p_max)) ? 256 : 0) |
-                                               (pb <= it.p_max && (gone || it.partial(a, u, pb, it.p_max)) ? 512 : 0));
+                                j0, (int)groups | (gone || it.partial(a, j0, it.p_min, min(pb - 1, it.p_max)) ? 256 : 0) |
+                                               (pb <= it.p_max && (gone || it.partial(a, j0, pb, it.p_max)) ? 512 : 0));
                         }
                         const unsigned bytes = __popc(groups) * 16 * (Q8 ? D + D / 32 * 4 : 2 * D);
                         bar_arrive_tx(full, bytes);
@@ -928,7 +930,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
             constexpr int CH = D / 8;  // 16-byte chunks of an operand row
             int v_ex = 0;
             for (int i = i0; i < i1 && ok; ++i) {
-                const int u = it.tile(i), j0 = u * kTile;
+                const int j0 = it.tile(i);
                 // a key that some row of the item may see
                 auto live = [&](int c, unsigned groups) {
                     const int j = j0 + c;
@@ -1337,7 +1339,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
             x.r = lo;
             request_of(a, x);
             x.p_min = x.p_max = x.pos0 + (row - x.row0);
-            span_of(a, x);
+            span_of(pa, x);
         }
         if (x.n == 0)
             for (int e = 0; e < a.heads * D / 8; ++e)
