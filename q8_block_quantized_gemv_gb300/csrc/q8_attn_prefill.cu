@@ -93,7 +93,7 @@ template <int D, bool Q8> struct Control {
     uint64_t s_full[3], p_ready[3];            // by score buffer: scores computed, weights written
     uint64_t o_full[2], joined, decided;
     // Of key tile number n of this CTA at n & 7 (no role is more than five tiles behind the requests):
-    // its first key, and bits: which 16-token groups lie on a page (0-7); whether some row of tile A (8) or B (9) does
+    // its first place, and bits: which 16-token groups lie on a page (0-7); whether some row of tile A (8) or B (9) does
     // not see all of it
     int2 tile[8];
     float unit[2][8];   // Q8_0: log2 of the keys' and the values' unit
@@ -416,23 +416,28 @@ struct PrefillArgs {
 };
 
 // Two query tiles of one cache head: tokens tok0 .. tok0 + tokens - 1 of request r, tile_tokens to a tile; row y of a tile
-// is token y / group, head y % group of those that share the cache head.  The item's key tiles are us from key 0 for the
-// sinks, and n - us from key ul.  A window's first tile starts with the run of its first key, not at a whole tile: a prompt
-// of 4097 rows, window 1024, takes 59 us, 61.5 from whole tiles.  In the list an item takes item_cost + n places, the tiles
-// last.
+// is token y / group, head y % group of those that share the cache head.  The item's keys are a list cut into tiles: the
+// first `sinks` places hold the sinks (whole runs), the others keys from the window's first run on, place v key v + jump.
+// (Whole tiles for the sinks and for the window, from multiples of 128, took 61.5 us for a prompt of 4097 rows, window
+// 1024, 4 sinks; the window from its first run 59; the one list @A.)  In the list of all items an item takes item_cost + n
+// places, the tiles last.
 struct Item {
     int r, qt, h;
     long long start;  // of its tiles in the list, the fixed cost behind it
     int row0, all, pos0;  // the request's first row, its rows, the position of its first row
     int tok0, tokens;
-    int p_min, p_max, end, lo, us, ul, n;
+    int p_min, p_max, end, lo, sinks, jump, n;
 
-    __device__ __forceinline__ int tile(int i) const { return i < us ? i * kTile : ul + (i - us) * kTile; }  // its first key
-    // Whether some row of the item does not see all of the tile from key j0, pages aside.
-    __device__ __forceinline__ bool partial(const AttnArgs &a, int j0) const { return partial(a, j0, p_min, p_max); }
+    __device__ __forceinline__ int key(int v) const { return v < sinks ? v : v + jump; }
+    // Whether some row of the item does not see all of the tile from place v0, pages aside.
+    __device__ __forceinline__ bool partial(const AttnArgs &a, int v0) const { return partial(a, v0, p_min, p_max); }
     // The same for its rows at positions p0 .. p1.
-    __device__ __forceinline__ bool partial(const AttnArgs &a, int j0, int p0, int p1) const {
-        return j0 + kTile > end || j0 + kTile - 1 > p0 || (a.window && p1 - j0 >= a.window && j0 + kTile > a.sinks);
+    __device__ __forceinline__ bool partial(const AttnArgs &a, int v0, int p0, int p1) const {
+        const int last = key(v0 + kTile - 1);
+        if (last >= end || last > p0) return true;
+        if (!a.window) return false;
+        if (v0 < sinks && min(sinks, v0 + kTile) > a.sinks) return true;  // a run that sinks end inside
+        return last >= a.sinks && p1 - key(max(v0, sinks)) >= a.window;
     }
 };
 // Key tiles that rows at positions p_min .. p_max visit.
@@ -440,10 +445,11 @@ __device__ __forceinline__ void span_of(const PrefillArgs &pa, Item &x) {
     const AttnArgs &a = pa.a;
     x.end = min(max(x.p_max + 1, 0), a.width * a.page_size);
     x.lo = a.window ? min(max(x.p_min - a.window + 1, 0), x.end) : 0;
-    const int sinks = a.window ? min(a.sinks, x.lo) : 0;
-    x.us = (sinks + kTile - 1) / kTile;
-    x.ul = max(x.lo & -pa.run, x.us * kTile);
-    x.n = x.us + (max(x.end - x.ul, 0) + kTile - 1) / kTile;
+    const int ul = x.lo & -pa.run, sinks = a.window ? min(a.sinks, ul) : 0;
+    x.sinks = (sinks + pa.run - 1) & -pa.run;  // not past ul, which is whole runs too
+    x.jump = sinks == a.sinks ? ul - x.sinks : 0;
+    if (!x.jump) x.sinks = 0;  // no gap: one stretch of keys
+    x.n = (max(x.end - x.jump, 0) + kTile - 1) / kTile;
 }
 __device__ __forceinline__ void request_of(const int *row_start, const int *lens, int rows, Item &x) {
     const int t0 = min(max(row_start[x.r], 0), rows), t1 = min(max(row_start[x.r + 1], t0), rows);
@@ -491,17 +497,17 @@ __device__ __forceinline__ bool sees(const AttnArgs &a, int p, int j) {
 template <int D, bool Q8>
 __device__ __noinline__ void add_nonfinite(const AttnArgs &a, const Item it, int i0, int i1, int p, int c0, float *o) {
     for (int i = i0; i < i1; ++i) {
-        const int j0 = it.tile(i);
+        const int v0 = i * kTile;
         for (int c = 0; c < kTile; ++c) {
-            const int j = j0 + c;
+            const int j = it.key(v0 + c);
             if (j >= it.end) break;
             if (!sees(a, p, j)) continue;
             const int page = a.table[(size_t)it.r * a.pitch + j / a.page_size];
             if (page < 0 || page >= a.pages) continue;
             // only tiles that some row does not see whole were cleared
-            bool cleared = it.partial(a, j0);
+            bool cleared = it.partial(a, v0);
             for (int b = 0; b < kTile / 16 && !cleared; ++b) {
-                const int pg = a.table[(size_t)it.r * a.pitch + (j0 + 16 * b) / a.page_size];
+                const int pg = a.table[(size_t)it.r * a.pitch + it.key(v0 + 16 * b) / a.page_size];
                 cleared = pg < 0 || pg >= a.pages;
             }
             if (!cleared) break;
@@ -710,7 +716,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
             const int *row = a.table + (size_t)it.r * a.pitch;
             int page = -1, off = 0;
             auto look = [&](int i) {
-                const int j = it.tile(i) + lane * pa.run;
+                const int j = it.key(i * kTile + lane * pa.run);
                 page = -1;
                 if (lane < runs && j < it.end) {
                     page = row[j / a.page_size];
@@ -739,11 +745,11 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                     if (!Q8) slot_used(s, steps + (i - i0) + kv);
                     if (lane == 0) {
                         if (kv == 0) {
-                            const int j0 = it.tile(i), pb = it.p_min + pa.tile_tokens;
+                            const int v0 = i * kTile, pb = it.p_min + pa.tile_tokens;
                             const bool gone = groups != 0xFFu;
                             ctl.tile[(cnt >> 1) & 7] = make_int2(
-                                j0, (int)groups | (gone || it.partial(a, j0, it.p_min, min(pb - 1, it.p_max)) ? 256 : 0) |
-                                               (pb <= it.p_max && (gone || it.partial(a, j0, pb, it.p_max)) ? 512 : 0));
+                                v0, (int)groups | (gone || it.partial(a, v0, it.p_min, min(pb - 1, it.p_max)) ? 256 : 0) |
+                                               (pb <= it.p_max && (gone || it.partial(a, v0, pb, it.p_max)) ? 512 : 0));
                         }
                         const unsigned bytes = __popc(groups) * 16 * (Q8 ? D + D / 32 * 4 : 2 * D);
                         bar_arrive_tx(full, bytes);
@@ -930,10 +936,10 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
             constexpr int CH = D / 8;  // 16-byte chunks of an operand row
             int v_ex = 0;
             for (int i = i0; i < i1 && ok; ++i) {
-                const int j0 = it.tile(i);
+                const int v0 = i * kTile;
                 // a key that some row of the item may see
                 auto live = [&](int c, unsigned groups) {
-                    const int j = j0 + c;
+                    const int j = it.key(v0 + c);
                     return (groups >> (c >> 4) & 1u) && j < it.end && (j >= it.lo || j < a.sinks);
                 };
                 for (int kv = 0; kv < 2 && ok; ++kv, ++cnt) {
@@ -1133,9 +1139,9 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                     }
                     if (info.y >> (8 + x) & 1) {
                         // columns [c_lo, c_hi] and [0, c_sink) are visible
-                        const int j0 = info.x;
+                        const int j0 = info.x + it.jump;
                         hide_scores<D>(ts, min(p, it.end - 1) - j0, a.window ? max(p - a.window + 1 - j0, 0) : 0,
-                                       a.window ? a.sinks - j0 : 0, info.y);
+                                       a.window ? a.sinks - info.x : 0, info.y);
                     }
                     // The weights are taken against the running maximum as it stands: a row's maximum is only looked
                     // for where their sum shows that a score passed it too far (or there is none yet).

@@ -329,6 +329,13 @@ PREFILL = [
     ([530], [200], 0, 2, 2, 128, 16, 1, 0),
     ([400], [400], 0, 2, 1, 128, 16, 37, 130),
     ([900, 33, 64], [64, 33, 1], 5, 4, 4, 64, 128, 5000, 2),
+    # sinks that end inside a run, at a tile's end, past a tile; a gap of one run, of none, inside the chunk
+    ([700, 230], [90, 200], 0, 4, 2, 128, 16, 75, 17),
+    ([800], [130], 0, 3, 1, 64, 48, 200, 128),
+    ([900, 170], [140, 20], 1, 2, 1, 128, 32, 96, 129),
+    ([1000], [64], 0, 4, 4, 64, 128, 33, 300),
+    ([333], [100], 0, 2, 1, 64, 64, 170, 64),
+    ([640], [256], 0, 4, 2, 128, 128, 129, 1),
 ]
 
 
