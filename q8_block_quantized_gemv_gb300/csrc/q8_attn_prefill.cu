@@ -28,7 +28,7 @@
 //
 // Every wait is bounded (about two seconds); one that runs out records a fault, and the CTA drains and returns.
 //
-// Measured, 32 heads of 128 over 8 cache heads: a prompt of 8,192 rows 347 us over a bf16 cache = 1.58 PFLOP/s (81% of a
+// Measured, 32 heads of 128 over 8 cache heads: a prompt of 8,192 rows 348 us over a bf16 cache = 1.58 PFLOP/s (81% of a
 // large bf16 product's rate: the MMAs wait for the softmax some of the time, 66% of the tensor pipe's cycles are taken),
 // 570 us over a Q8_0 cache, where a tile goes through five hands (codes, conversion, S, softmax, O) and nothing is full:
 // 27% of the tensor pipe's cycles and 38% of the issue slots in a chunk of 509 rows, which takes 66 us (1.5 us more with
@@ -74,7 +74,7 @@ template <int D, bool Q8> struct Cfg {
     // What an item costs beside its tiles, in tiles: loading Q, the pipe's fill and drain, the epilogue.  Without it the
     // CTAs of a long prompt's first rows, 44 short items each, took 835,000 clocks where the others took 740,000.  2, 3, 4
     // and 6 take 368, 348, 347 and 358 us for a prompt of 8192 rows, 51.6, 50.3, 51.3 and 50.3 for a chunk of 512, 63.0,
-    // 62.0, 63.2 and 63.9 under a window; over a Q8_0 cache 2, 3 and 4 take 640, 582 and 570 us for the prompt.
+    // 62.0, 63.2 and 63.9 under a window (before its sinks and keys were one list); over a Q8_0 cache 2, 3 and 4 take 640, 582 and 570 us for the prompt.
     static constexpr int kItemCost = Q8 ? 4 : 3;
     static constexpr int kRing = 2 * kOp;                  // after Q's two tiles
     static constexpr int kRawAt = kRing + kSlots * kOp;
@@ -419,7 +419,8 @@ struct PrefillArgs {
 // is token y / group, head y % group of those that share the cache head.  The item's keys are a list cut into tiles: the
 // first `sinks` places hold the sinks (whole runs), the others keys from the window's first run on, place v key v + jump.
 // (Whole tiles for the sinks and for the window, from multiples of 128, took 61.5 us for a prompt of 4097 rows, window
-// 1024, 4 sinks; the window from its first run 59; the one list @A.)  In the list of all items an item takes item_cost + n
+// 1024, 4 sinks; the window from its first run 59; the one list 54.  Calls without a window take 1 to 2 us longer with it:
+// a chunk of 512 rows 50 and 51, a prompt of 8192 rows 346 and 348.)  In the list of all items an item takes item_cost + n
 // places, the tiles last.
 struct Item {
     int r, qt, h;
