@@ -53,6 +53,7 @@ constexpr int kRows = 256;   // query rows of an item
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMmaWarp = 8, kLoadWarp = 9, kHelpWarp = 10;
 constexpr unsigned kTmemColumns = 512;
+constexpr unsigned kSteps = 16;  // a power of two above 10 (see Control::step)
 constexpr uint32_t kColP = 64;   // the weights (16 bits) over the upper half of their scores
 constexpr unsigned kFaultAttnWait = 8u;
 
@@ -87,7 +88,10 @@ template <int D, bool Q8> struct Cfg {
 template <int D, bool Q8> struct Control {
     using C = Cfg<D, Q8>;
     uint64_t full[10], ready[10];              // operand ring: landed, usable
-    uint64_t step[8];                          // a step's MMAs are done, and with them what it used is free
+    // A step's MMAs are done, and with them what it used is free.  Who waits for a step must not find its barrier a whole
+    // turn further on: the loads wait for what a place held up to five tiles ago (ten places), and in items of one tile,
+    // whose first scores are a step of their own, the MMAs are up to ten steps past that by then.
+    uint64_t step[kSteps];
     uint64_t raw_full[4], raw_empty[4];        // raw ring (Q8_0)
     uint64_t q_raw, q_full, q_empty, drain;  // q_raw: landed, before the conversion (Q8_0)
     uint64_t s_full[3], p_ready[3];            // by score buffer: scores computed, weights written
@@ -539,7 +543,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
             bar_init(&ctl.full[i], 1);
             bar_init(&ctl.ready[i], C::kHelpers);
         }
-        for (int i = 0; i < 8; ++i) bar_init(&ctl.step[i], 1);
+        for (unsigned i = 0; i < kSteps; ++i) bar_init(&ctl.step[i], 1);
         for (int i = 0; i < C::kRawSlots; ++i) {
             bar_init(&ctl.raw_full[i], 1);
             bar_init(&ctl.raw_empty[i], C::kHelpers);
@@ -690,7 +694,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
     unsigned steps = 0, last_step = 0;
     auto slot_free = [&](unsigned s) {
         const unsigned n = __shfl_sync(0xffffffffu, last_step, s);
-        return warp_wait(&ctl.step[n & 7], (n >> 3) & 1, abort);
+        return warp_wait(&ctl.step[n % kSteps], n / kSteps & 1, abort);
     };
     auto slot_used = [&](unsigned s, unsigned step) {
         if (lane == (int)s) last_step = step;
@@ -846,7 +850,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                     issue_s(0, buffer(b + 2 * n), key1);
                     if (n == 0 && two) issue_s(1, buffer(b + 1), key1);
                     if (n + 1 == AHEAD || i0 + n + 1 == i1) {
-                        commit(&ctl.step[steps & 7]);
+                        commit(&ctl.step[steps % kSteps]);
                         if (i1 - i0 == 1) commit(&ctl.q_empty);
                     }
                 }
@@ -912,7 +916,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                         } else if (keys) {
                             issue_s(0, bb, key2);
                         }
-                        commit(&ctl.step[steps & 7]);
+                        commit(&ctl.step[steps % kSteps]);
                         if (i + 2 == i1) commit(&ctl.q_empty);
                     }
                     __syncwarp();
@@ -1177,7 +1181,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                                 // rest once that tile's turns are done.
                                 if (C::kBufs == 3) {
                                     const unsigned n = steps + (i - i0);
-                                    if (!(ok = warp_wait(&ctl.step[n & 7], (n >> 3) & 1, abort))) break;
+                                    if (!(ok = warp_wait(&ctl.step[n % kSteps], n / kSteps & 1, abort))) break;
                                     fence_after();
                                 }
                                 scale_columns(to, D, f);

@@ -336,6 +336,11 @@ PREFILL = [
     ([1000], [64], 0, 4, 4, 64, 128, 33, 300),
     ([333], [100], 0, 2, 1, 64, 64, 170, 64),
     ([640], [256], 0, 4, 2, 128, 128, 129, 1),
+    # many items of one tile, and of two, for each CTA: operand places are reused many steps later
+    ([17] * 60, [17] * 60, 0, 32, 32, 64, 16, 0, 0),
+    ([17] * 60, [17] * 60, 0, 32, 32, 128, 16, 0, 0),
+    ([140] * 30, [140] * 30, 0, 48, 48, 64, 16, 0, 0),
+    ([9, 33, 1, 128, 140] * 12, [9, 20, 1, 128, 140] * 12, 0, 32, 32, 64, 32, 0, 0),
 ]
 
 
