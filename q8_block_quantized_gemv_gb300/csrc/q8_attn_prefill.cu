@@ -96,6 +96,7 @@ template <int D, bool Q8> struct Control {
     uint64_t q_raw, q_full, q_empty, drain;  // q_raw: landed, before the conversion (Q8_0)
     uint64_t s_full[3], p_ready[3];            // by score buffer: scores computed, weights written
     uint64_t o_full[2], joined, decided;
+    uint64_t idle;  // a segment in which tile B has no rows: its warps have seen the end of A's
     // Of key tile number n of this CTA at n & 7 (no role is more than five tiles behind the requests):
     // its first place, and bits: which 16-token groups lie on a page (0-7); whether some row of tile A (8) or B (9) does
     // not see all of it
@@ -559,6 +560,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
             bar_init(&ctl.p_ready[i], 4);
         }
         for (int i = 0; i < 2; ++i) bar_init(&ctl.o_full[i], 1);
+        bar_init(&ctl.idle, 4);
         ctl.abort = 0;
         ctl.poison = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -1106,7 +1108,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
         constexpr float kMostSum = Q8 ? 32768.0f : 1.15292150e18f;  // 2^15, 2^60
         constexpr float kLeast = 1.17549435e-38f;  // a factor of 0 would make NaN of a hidden score's -inf
         const float sc0 = fmaxf(fabsf(a.scale) * kLog2e, kLeast);
-        unsigned cnt = 0, ocnt = 0, shared = 0, seg = 0;
+        unsigned cnt = 0, ocnt = 0, shared = 0, idles = 0, seg = 0;
         unsigned job = 0, sbits = 0;  // the buffer of A's next scores; the score barriers' phases
         bool ok = true;
         for (; more; advance()) {
@@ -1216,6 +1218,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                     if (lane == 0) bar_arrive(&ctl.p_ready[b]);
                 }
                 if (ok) ok = warp_wait(&ctl.o_full[x], ocnt++ & 1, abort);
+                if (ok && !two) ok = warp_wait(&ctl.idle, idles++ & 1, abort);
                 fence_after();
             } else {
                 // Tile B without rows keeps count of the buffers, and does not run ahead: a barrier tells a phase from the
@@ -1224,7 +1227,9 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                     sbits ^= 1u << job;
                     if (C::kBufs == 3) job = job == 0 ? 2u : job - 1;
                 }
+                // A waits for it in turn: it must not be two ends further on when this warp looks.
                 ok = warp_wait(&ctl.o_full[0], seg & 1, abort);
+                if (lane == 0) bar_arrive(&ctl.idle);
             }
             steps += i1 - i0 + 1;
             cnt += 2 * (i1 - i0);
