@@ -28,10 +28,10 @@
 //
 // Every wait is bounded (about two seconds); one that runs out records a fault, and the CTA drains and returns.
 //
-// Measured, 32 heads of 128 over 8 cache heads: a prompt of 8,192 rows 348 us over a bf16 cache = 1.58 PFLOP/s (81% of a
+// Measured, 32 heads of 128 over 8 cache heads: a prompt of 8,192 rows 353 us over a bf16 cache = 1.56 PFLOP/s (80% of a
 // large bf16 product's rate: the MMAs wait for the softmax some of the time, 66% of the tensor pipe's cycles are taken),
 // 570 us over a Q8_0 cache, where a tile goes through five hands (codes, conversion, S, softmax, O) and nothing is full:
-// 27% of the tensor pipe's cycles and 38% of the issue slots in a chunk of 509 rows, which takes 66 us (1.5 us more with
+// 27% of the tensor pipe's cycles and 38% of the issue slots in a chunk of 509 rows, which takes 67 us (1.5 us more with
 // four conversion warps; as long with the conversion finished in registers before its operand's place is free, or with
 // the values' place given back before the keys').
 // 512 rows after 4,096 tokens, 32 cache heads: 51 us.  A call's fixed part is 11 us: the cut of the list 2, the first Q
@@ -1108,7 +1108,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
         constexpr float kMostSum = Q8 ? 32768.0f : 1.15292150e18f;  // 2^15, 2^60
         constexpr float kLeast = 1.17549435e-38f;  // a factor of 0 would make NaN of a hidden score's -inf
         const float sc0 = fmaxf(fabsf(a.scale) * kLog2e, kLeast);
-        unsigned cnt = 0, ocnt = 0, shared = 0, idles = 0, seg = 0;
+        unsigned cnt = 0, ends = 0, shared = 0, seg = 0;  // ends: the phases of o_full (bit 0) and idle (bit 1)
         unsigned job = 0, sbits = 0;  // the buffer of A's next scores; the score barriers' phases
         bool ok = true;
         for (; more; advance()) {
@@ -1217,8 +1217,9 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                     __syncwarp();
                     if (lane == 0) bar_arrive(&ctl.p_ready[b]);
                 }
-                if (ok) ok = warp_wait(&ctl.o_full[x], ocnt++ & 1, abort);
-                if (ok && !two) ok = warp_wait(&ctl.idle, idles++ & 1, abort);
+                if (ok) ok = warp_wait(&ctl.o_full[x], ends & 1, abort);
+                if (ok && !two) ok = warp_wait(&ctl.idle, ends >> 1 & 1, abort);
+                ends ^= two ? 1u : 3u;
                 fence_after();
             } else {
                 // Tile B without rows keeps count of the buffers, and does not run ahead: a barrier tells a phase from the
@@ -1227,7 +1228,8 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                     sbits ^= 1u << job;
                     if (C::kBufs == 3) job = job == 0 ? 2u : job - 1;
                 }
-                // A waits for it in turn: it must not be two ends further on when this warp looks.
+                // A waits for it in turn: it must not be two ends further on when this warp looks.  (Its wait, needed only
+                // then, costs all calls 1%: a prompt of 8192 rows 350 and 353 us.)
                 ok = warp_wait(&ctl.o_full[0], seg & 1, abort);
                 if (lane == 0) bar_arrive(&ctl.idle);
             }
