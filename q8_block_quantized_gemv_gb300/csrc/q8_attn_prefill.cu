@@ -87,7 +87,11 @@ template <int D, bool Q8> struct Cfg {
 // Control block in shared memory.
 template <int D, bool Q8> struct Control {
     using C = Cfg<D, Q8>;
-    uint64_t full[10], ready[10];              // operand ring: landed, usable
+    // Operands: landed, usable.  Over a Q8_0 cache `ready` goes by place of the ring.  Over a bf16 cache both go by key
+    // tile, at most five of which are on their way: keys are full[n % 5], values full[5 + n % 5] and, after the helpers,
+    // ready[n % 5].  So a barrier's every phase has the same waiters: one that places shared between keys, which the
+    // helpers have no business with, and values could complete twice before a helper had looked.
+    uint64_t full[10], ready[10];
     // A step's MMAs are done, and with them what it used is free.  Who waits for a step must not find its barrier a whole
     // turn further on: the loads wait for what a place held up to five tiles ago (ten places), and in items of one tile,
     // whose first scores are a step of their own, the MMAs are up to ten steps past that by then.
@@ -541,9 +545,9 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
     const int tid = threadIdx.x, lane = tid & 31, warp = (int)uniform(tid >> 5);
     if (tid == 0) {
         for (int i = 0; i < C::kSlots; ++i) {
-            bar_init(&ctl.full[i], 1);
             bar_init(&ctl.ready[i], C::kHelpers);
         }
+        for (int i = 0; i < 10; ++i) bar_init(&ctl.full[i], 1);
         for (unsigned i = 0; i < kSteps; ++i) bar_init(&ctl.step[i], 1);
         for (int i = 0; i < C::kRawSlots; ++i) {
             bar_init(&ctl.raw_full[i], 1);
@@ -701,6 +705,15 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
     auto slot_used = [&](unsigned s, unsigned step) {
         if (lane == (int)s) last_step = step;
     };
+    // The landing of load number c (keys of tile c / 2, or its values), and the phase: bf16 operands, or raw Q8_0 data.
+    auto landed = [&](unsigned c) {
+        if constexpr (Q8) return &ctl.raw_full[c % C::kRawSlots];
+        else return &ctl.full[(c & 1) * 5 + (c >> 1) % 5];
+    };
+    auto landed_phase = [](unsigned c) {
+        if constexpr (Q8) return c / C::kRawSlots & 1;
+        else return (c >> 1) / 5 & 1;
+    };
     if (warp == kLoadWarp) {
         // ---- keys and values: lane i requests run i of each tile ----
         const int runs = kTile / pa.run, per = pa.run / 16;
@@ -743,7 +756,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                 for (int kv = 0; kv < 2; ++kv, ++cnt) {
                     const unsigned slots = Q8 ? C::kRawSlots : C::kSlots;
                     const unsigned s = cnt % slots, turn = cnt / slots;
-                    uint64_t *full = Q8 ? &ctl.raw_full[s] : &ctl.full[s];
+                    uint64_t *full = landed(cnt);
                     if (cnt >= slots) {
                         if (Q8) ok = warp_wait(&ctl.raw_empty[s], (turn - 1) & 1, abort);
                         else ok = slot_free(s);
@@ -787,8 +800,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
             const unsigned slots = Q8 ? C::kRawSlots : C::kSlots;
             for (unsigned c = cnt > slots ? cnt - slots : 0; c < cnt; ++c) {
                 const uint64_t t0 = now_ns();
-                while (!bar_try(Q8 ? &ctl.raw_full[c % slots] : &ctl.full[c % slots], (c / slots) & 1) &&
-                       now_ns() - t0 < 2000000000ull) {
+                while (!bar_try(landed(c), landed_phase(c)) && now_ns() - t0 < 2000000000ull) {
                 }
             }
             const uint64_t t0 = now_ns();
@@ -809,17 +821,24 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
         const uint32_t v_desc = desc128_low(saddr(smem + C::kRing), kTile * 128);
         constexpr int AHEAD = C::kBufs - 1;  // key tiles that A's scores are ahead of its O
         unsigned seg = 0, steps = 0, pbits = 0;              // pbits: the weight barriers' phases
-        unsigned kslot = 0, kphase = 0, vslot = 1, vphase = 0;  // of the next keys to wait for, the next values
+        // Of the next keys to wait for, the next values: place (Q8_0) or tile modulo 5 (bf16), and phase.
+        unsigned knext = 0, kphase = 0, vnext = Q8 ? 1 : 0, vphase = 0;
         unsigned jobs = 0;                                   // the buffer of A's next O
         bool ok = true;
-        auto two_on = [](unsigned &slot, unsigned &phase) {
-            slot += 2;
-            if (slot >= C::kSlots) {
-                slot -= C::kSlots;
+        auto tile_on = [](unsigned &next, unsigned &phase) {
+            constexpr unsigned by = Q8 ? 2 : 1, around = Q8 ? C::kSlots : 5;
+            next += by;
+            if (next >= around) {
+                next -= around;
                 phase ^= 1;
             }
         };
-        auto key_bar = [&]() { return Q8 ? &ctl.ready[kslot] : &ctl.full[kslot]; };
+        auto key_bar = [&]() { return Q8 ? &ctl.ready[knext] : &ctl.full[knext]; };
+        auto place_of = [](unsigned next, unsigned kv) {  // in the ring
+            if constexpr (Q8) return next;
+            const unsigned s = 2 * next + kv;
+            return s >= C::kSlots ? s - C::kSlots : s;
+        };
         auto issue_s = [&](int x, unsigned b, unsigned slot) {  // one lane
             const uint32_t qd = q_desc + x * (C::kOp >> 4), kd = k_desc + slot * (C::kOp >> 4);
 #pragma unroll
@@ -844,8 +863,8 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
             unsigned key1 = 0;  // slot of the keys that B's next scores need
             for (int n = 0; n < AHEAD && i0 + n < i1; ++n) {
                 if (!(ok = warp_wait(key_bar(), kphase, abort))) break;
-                key1 = uniform(kslot);
-                two_on(kslot, kphase);
+                key1 = uniform(place_of(knext, 0));
+                tile_on(knext, kphase);
                 const unsigned b = uniform(jobs);
                 fence_after();
                 if (elect()) {
@@ -861,22 +880,23 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
             if (!ok) break;
             ++steps;
             for (int i = i0; i < i1; ++i) {
-                const unsigned u = uniform(vslot | (jobs << 8)), vs = u & 255u, ba = u >> 8, bb = buffer(ba + 1);
+                const unsigned u = uniform(vnext | (jobs << 8)), vn = u & 255u, ba = u >> 8, bb = buffer(ba + 1);
+                const unsigned vs = place_of(vn, 1);
                 const uint32_t more_o = i > i0;
                 // ---- A ----
                 {
                     const bool keys = C::kBufs == 2 && i + 1 < i1;  // two buffers: A's next scores in this turn
                     uint64_t *const pbar = &ctl.p_ready[ba], *const kbar = keys ? key_bar() : pbar;
                     const unsigned pp = pbits >> ba & 1u, kp = keys ? kphase : pp;
-                    if (!look3(pbar, pp, &ctl.ready[vs], vphase, kbar, kp)) {
-                        if (!(ok = warp_wait(&ctl.ready[vs], vphase, abort))) break;
+                    if (!look3(pbar, pp, &ctl.ready[vn], vphase, kbar, kp)) {
+                        if (!(ok = warp_wait(&ctl.ready[vn], vphase, abort))) break;
                         if (!(ok = warp_wait(kbar, kp, abort))) break;
                         if (!(ok = warp_wait(pbar, pp, abort))) break;
                     }
                     pbits ^= 1u << ba;
                     if (keys) {
-                        key1 = uniform(kslot);
-                        two_on(kslot, kphase);
+                        key1 = uniform(place_of(knext, 0));
+                        tile_on(knext, kphase);
                     }
                     fence_after();
                     if (elect()) {
@@ -904,8 +924,8 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                     }
                     unsigned key2 = 0;
                     if (keys) {
-                        key2 = uniform(kslot);
-                        two_on(kslot, kphase);
+                        key2 = uniform(place_of(knext, 0));
+                        tile_on(knext, kphase);
                     }
                     fence_after();
                     if (elect()) {
@@ -924,7 +944,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                     __syncwarp();
                     if (keys) key1 = key2;
                 }
-                two_on(vslot, vphase);
+                tile_on(vnext, vphase);
                 if (C::kBufs == 3) jobs = buffer(jobs + 2);
                 ++steps;
             }
@@ -950,13 +970,14 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                     return (groups >> (c >> 4) & 1u) && j < it.end && (j >= it.lo || j < a.sinks);
                 };
                 for (int kv = 0; kv < 2 && ok; ++kv, ++cnt) {
-                    const unsigned s = cnt % C::kSlots, par = (cnt / C::kSlots) & 1;
+                    const unsigned s = cnt % C::kSlots;
                     unsigned char *op = smem + C::kRing + s * C::kOp;
                     if constexpr (!Q8) {
-                        if (!(ok = warp_wait(&ctl.full[s], par, abort))) break;
+                        if (!kv) continue;  // keys go to the MMAs as they are
+                        if (!(ok = warp_wait(landed(cnt), landed_phase(cnt), abort))) break;
                         const int info = ctl.tile[(cnt >> 1) & 7].y;
                         const unsigned groups = info & 255u;
-                        if (kv && (info & 768)) {
+                        if (info & 768) {
                             // Thread ht takes chunk ht % CH of every RS-th key, eight loads in flight.
                             bool found = false;
                             constexpr int RS = HT / CH, B = 8;
@@ -990,15 +1011,14 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                             fence_async();
                         }
                         __syncwarp();
-                        if (lane == 0) bar_arrive(&ctl.ready[s]);
+                        if (lane == 0) bar_arrive(&ctl.ready[(cnt >> 1) % 5]);
                         continue;
                     }
                     // Q8_0: codes and scales to fp16
                     const unsigned rs = cnt % (C::kRawSlots ? C::kRawSlots : 1);
-                    const unsigned rpar = (cnt / (C::kRawSlots ? C::kRawSlots : 1)) & 1;
                     if (cnt >= (unsigned)C::kSlots && !(ok = slot_free(s))) break;
                     slot_used(s, steps + (i - i0) + kv);
-                    if (!(ok = warp_wait(&ctl.raw_full[rs], rpar, abort))) break;
+                    if (!(ok = warp_wait(landed(cnt), landed_phase(cnt), abort))) break;
                     const unsigned char *raw = smem + C::kRawAt + rs * C::kRaw;
                     const float *scl = reinterpret_cast<const float *>(raw + kTile * D);
                     const int info = ctl.tile[(cnt >> 1) & 7].y;

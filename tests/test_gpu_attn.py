@@ -624,3 +624,34 @@ def test_refuses_mismatched_tensors(dev, work):
     with pytest.raises(q8.Q8Error) as e:  # rows not 16-byte aligned
         q8.attn_decode(torch.zeros((2, 260), dtype=torch.bfloat16, device="cuda"), cache, table, lens, q_heads=4, **ok)
     assert e.value.status == 3
+
+
+# ---- requests without rows ------------------------------------------------------------------------------------------
+
+def scattered(torch, work, R, kind, dim, seed, every):
+    """R requests, nearly all without rows (some with tokens in the cache), a short chunk every so many."""
+    import q8_block_quantized_gemv_gb300 as q8
+    rng = np.random.default_rng(seed)
+    lens, counts = [0] * R, [0] * R
+    for r in [*range(3, R, every), R - 1]:
+        counts[r] = int(rng.integers(1, 40))
+        lens[r] = counts[r] + int(rng.integers(0, 200))
+    for r in range(5, R, 7 * every):
+        if not counts[r]:
+            lens[r] = 20
+    p = Paged(torch, lens, 2, dim, 32, kind, seed)
+    starts = [0, *np.cumsum(counts).tolist()]
+    q, qn = queries(torch, starts[-1] + 2, 4, dim, seed + 1)
+    sd = torch.tensor(starts, dtype=torch.int32, device="cuda")
+    got = q8.attn_prefill(q, p.cache, p.table_dev, p.lens_dev, sd, workspace=work)
+    agree(got, *expected(p, qn, starts, dim ** -0.5, 0, 0))
+    assert q8.device_fault() == 0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "q8"])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_prefill_long_walks_between_items(dev, work, kind, dim):
+    """Hundreds of requests without rows between two that have some: the kernel's warps walk over them one by one, at
+    speeds of their own."""
+    scattered(dev, work, 9000, kind, dim, 111, 250)
+    scattered(dev, work, 1200, kind, dim, 112, 11)
