@@ -82,6 +82,10 @@ template <int D, bool Q8> struct Cfg {
     static constexpr int kCtl = kRawAt + kRawSlots * kRaw;
     static constexpr int kSmem = kCtl + (Q8 ? 4096 : 2048);
     static_assert(kSmem <= 226 * 1024, "");
+    // The list of items is cut before the operands come, in their place: the requests' sums of query tiles (R + 1), then,
+    // for up to kCopied requests, copies of row_start (R + 1) and lens (R), which otherwise are read where they are.
+    static constexpr int kCopied = (kCtl / 4 - 2) / 3;
+    static_assert((Q8_MAX_REQUESTS + 1) * 4 <= kCtl && (3 * kCopied + 2) * 4 <= kCtl, "the list ends before the control block");
 };
 
 // Control block in shared memory.
@@ -583,10 +587,15 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
     constexpr int T = C::kThreads;
     long long total = 0, b0 = 0, b1 = 0, span = 1;
     {
-        int *starts = qsum + a.R + 1, *lens = starts + a.R + 1;  // copies: what follows looks at them over and over
-        for (int r = tid; r <= a.R; r += T) {
-            starts[r] = a.row_start[r];
-            if (r < a.R) lens[r] = a.lens[r];
+        const int *starts = a.row_start, *lens = a.lens;
+        if (a.R <= C::kCopied) {  // what follows looks at them over and over
+            int *s = qsum + a.R + 1, *l = s + a.R + 1;
+            for (int r = tid; r <= a.R; r += T) {
+                s[r] = a.row_start[r];
+                if (r < a.R) l[r] = a.lens[r];
+            }
+            starts = s;
+            lens = l;
         }
         __syncthreads();
         const int each = (a.R + T - 1) / T, ra = min(a.R, tid * each), rb = min(a.R, ra + each);

@@ -655,3 +655,11 @@ def test_prefill_long_walks_between_items(dev, work, kind, dim):
     speeds of their own."""
     scattered(dev, work, 9000, kind, dim, 111, 250)
     scattered(dev, work, 1200, kind, dim, 112, 11)
+
+
+@pytest.mark.parametrize("dim,kind,R", [
+    # The list of requests is cut in shared memory: the most that have copies of their lengths beside it, and more.
+    (64, "q8", 13994), (64, "q8", 13995), (64, "q8", 14336), (64, "q8", 16384), (64, "bf16", 16383), (64, "bf16", 16384),
+    (128, "q8", 16384), (128, "bf16", 16384)])
+def test_prefill_most_requests(dev, work, dim, kind, R):
+    scattered(dev, work, R, kind, dim, R, 400)
