@@ -1,7 +1,8 @@
 """Python binding of libq8gemv, the GB300 Q8_0 block-quantized GEMV library.
 
 Argument marshalling only: every step of the product runs in the library's CUDA kernels (device entry points) or its
-C++ host code (repack, quantize).  PyTorch supplies device memory and streams.  The names follow the C ABI in
+C++ host code (repack, quantize).  PyTorch supplies device memory and streams: a call with ``stream=`` runs there, what
+it allocates is allocated there, and the caller orders its inputs' writes before it.  The names follow the C ABI in
 ``include/q8_gemv.h``:
 
 * :func:`gemv` -- ``q8_gemv`` / ``q8_gemv_ex``: y[r, n] = sum_b s[b, n] sum_i x[r, 32b+i] q[32b+i, n]
@@ -146,6 +147,21 @@ def _stream_of(stream, device):
     return _raw_stream(device.index)
 
 
+def _new(shape, dtype, device, stream=None, zeroed=False, returned=True):
+    """A tensor for a call that runs on ``stream`` (None: the current stream).  It is allocated, and zeroed, on that
+    stream: memory that other work of the current stream may still be using does not go to a kernel that nothing orders
+    behind it.  A returned tensor may be used on the current stream as well, once that waits for ``stream``, and freed."""
+    import torch
+    make = torch.zeros if zeroed else torch.empty
+    if stream is None or _stream_handle(stream) == _stream_of(None, device):
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(_stream_handle(stream), device=device)):
+        out = make(shape, dtype=dtype, device=device)
+    if returned:
+        out.record_stream(torch.cuda.current_stream(device))
+    return out
+
+
 def tiled_n(N: int) -> int:
     return lib().q8_tiled_n(N)
 
@@ -196,7 +212,7 @@ def quantize_act(x, out: QuantAct | None = None, stream=None) -> QuantAct:
     if nbytes < 0:
         raise ValueError("K must be a positive multiple of 32")
     if out is None:
-        out = QuantAct(torch.empty((nbytes,), dtype=torch.uint8, device=x.device), m, K)
+        out = QuantAct(_new((nbytes,), torch.uint8, x.device, stream), m, K)
     elif out.shape != (m, K) or out.buf.numel() != nbytes:
         raise ValueError("out must be a QuantAct of the same shape")
     _check(lib().q8_quantize_act(x.data_ptr(), out.data_ptr(), m, K, _stream_handle(stream)), "q8_quantize_act")
@@ -253,7 +269,7 @@ def gemv(x, q, s, N: int, y=None, variant: str = "auto", constant_weights: bool 
     import torch
     m, K, Np = _check_operands(x, q, s, N, tiled)
     if y is None:
-        y = torch.empty((m, Np), dtype=torch.float32, device=x.device)
+        y = _new((m, Np), torch.float32, x.device, stream)
     elif y.dtype != torch.float32 or y.shape != (m, Np) or not y.is_contiguous() or not y.is_cuda:
         raise ValueError("y must be a contiguous fp32 CUDA tensor [m, Np]")
     _check(lib().q8_gemv_ex(x.data_ptr(), q.data_ptr(), s.data_ptr(), y.data_ptr(), m, K, N, VARIANTS[variant],
@@ -270,7 +286,7 @@ def gemv_argmax(x, q, s, N: int, idx=None, logits=None, constant_weights: bool =
     import torch
     m, K, Np = _check_operands(x, q, s, N, tiled)
     if idx is None:
-        idx = torch.empty((m,), dtype=torch.int64, device=x.device)
+        idx = _new((m,), torch.int64, x.device, stream)
     elif idx.dtype != torch.int64 or idx.numel() < m or not idx.is_contiguous() or not idx.is_cuda:
         raise ValueError("idx must be a contiguous int64 CUDA tensor of m elements")
     lp = None
@@ -301,8 +317,8 @@ def tile_device(q, s, N: int, stream=None):
     import torch
     K = q.shape[0]
     Nt = tiled_n(N)
-    qt = torch.empty((K * Nt,), dtype=torch.int8, device=q.device)
-    st = torch.empty(((K // Q8_BLOCK) * Nt,), dtype=torch.float32, device=q.device)
+    qt = _new((K * Nt,), torch.int8, q.device, stream)
+    st = _new(((K // Q8_BLOCK) * Nt,), torch.float32, q.device, stream)
     _check(lib().q8_tile_device(q.data_ptr(), s.data_ptr(), K, N, qt.data_ptr(), st.data_ptr(),
                                 _stream_handle(stream)), "q8_tile_device")
     return qt, st
@@ -320,7 +336,7 @@ def gemv_parts(x, weights, ys=None, constant_weights: bool = False, tiled: bool 
     for i, (q, s, N) in enumerate(weights):
         _check_operands(x, q, s, N, tiled)
         Np = padded_n(N)
-        y = ys[i] if ys is not None else torch.empty((m, Np), dtype=torch.float32, device=x.device)
+        y = ys[i] if ys is not None else _new((m, Np), torch.float32, x.device, stream)
         if y.dtype != torch.float32 or y.shape != (m, Np) or not y.is_contiguous() or not y.is_cuda:
             raise ValueError("each y must be a contiguous fp32 CUDA tensor [m, Np]")
         arr[i] = _Part(q.data_ptr(), s.data_ptr(), y.data_ptr(), N)
@@ -349,10 +365,10 @@ def plan_glu_launches(m: int, K: int, N: int, q8_act: bool = False) -> int:
     return n
 
 
-def _q8_out(out_q8, m, Np, device):
+def _q8_out(out_q8, m, Np, device, stream):
     import torch
     if out_q8 is None:
-        return QuantAct(torch.empty((act_bytes(m, Np),), dtype=torch.uint8, device=device), m, Np)
+        return QuantAct(_new((act_bytes(m, Np),), torch.uint8, device, stream), m, Np)
     if out_q8.shape != (m, Np) or out_q8.buf.numel() != act_bytes(m, Np):
         raise ValueError("out_q8 must be a QuantAct of [m, Np]")
     return out_q8
@@ -369,12 +385,12 @@ def gemv_glu(x, gate, up, N: int, out=None, out_bf16=None, want=("f32",), consta
     m, K, Np = _check_operands(x, gate[0], gate[1], N, True)
     _check_operands(x, up[0], up[1], N, True)
     if out is None and "f32" in want:
-        out = torch.empty((m, Np), dtype=torch.float32, device=x.device)
+        out = _new((m, Np), torch.float32, x.device, stream)
     if out_bf16 is None and "bf16" in want:
-        out_bf16 = torch.empty((m, Np), dtype=torch.bfloat16, device=x.device)
+        out_bf16 = _new((m, Np), torch.bfloat16, x.device, stream)
     q8out = out_q8 is not None or "q8" in want
     if q8out:
-        out_q8 = _q8_out(out_q8, m, Np, x.device)
+        out_q8 = _q8_out(out_q8, m, Np, x.device, stream)
     if out is not None and (out.dtype != torch.float32 or out.shape != (m, Np) or not out.is_contiguous()):
         raise ValueError("out must be a contiguous fp32 CUDA tensor [m, Np]")
     if out_bf16 is not None and (out_bf16.dtype != torch.bfloat16 or out_bf16.shape != (m, Np)
@@ -401,12 +417,12 @@ def gemv_residual_norm(x, q, s, N: int, residual, gamma, eps: float, h=None, out
     if gamma.dtype != torch.float32 or gamma.numel() < N or not gamma.is_contiguous():
         raise ValueError("gamma must be a contiguous fp32 CUDA tensor of at least N values")
     if h is None:
-        h = torch.empty((m, Np), dtype=torch.float32, device=x.device)
+        h = _new((m, Np), torch.float32, x.device, stream)
     if out_bf16 is None and "bf16" in want:
-        out_bf16 = torch.empty((m, Np), dtype=torch.bfloat16, device=x.device)
+        out_bf16 = _new((m, Np), torch.bfloat16, x.device, stream)
     q8out = out_q8 is not None or "q8" in want
     if q8out:
-        out_q8 = _q8_out(out_q8, m, Np, x.device)
+        out_q8 = _q8_out(out_q8, m, Np, x.device, stream)
     _check(lib().q8_gemv_residual_norm_ex(x.data_ptr(), q.data_ptr(), s.data_ptr(), residual.data_ptr(),
                                           gamma.data_ptr(), float(eps), h.data_ptr(),
                                           out_bf16.data_ptr() if out_bf16 is not None else None,
@@ -550,9 +566,9 @@ def kv_slots(cached, fresh, table, free_pages, page_size: int, rows: int, head=N
     dev = cached.device
     if out is None:
         i32 = torch.int32  # tensors of their own: cheaper than views of one
-        lens, starts = torch.empty(R, dtype=i32, device=dev), torch.empty(R + 1, dtype=i32, device=dev)
-        positions, next_head = torch.empty(rows, dtype=i32, device=dev), torch.empty(1, dtype=i32, device=dev)
-        slots = torch.empty(rows, dtype=torch.int64, device=dev)
+        lens, starts = _new(R, i32, dev, stream), _new(R + 1, i32, dev, stream)
+        positions, next_head = _new(rows, i32, dev, stream), _new(1, i32, dev, stream)
+        slots = _new(rows, torch.int64, dev, stream)
         out = {"table": table, "lens": lens, "row_start": starts, "positions": positions, "slots": slots,
                "head": next_head}
         lp, sp, pp, hp = lens.data_ptr(), starts.data_ptr(), positions.data_ptr(), next_head.data_ptr()
@@ -642,7 +658,7 @@ def rope_append(q, k, v, cache: KVCache, positions, slots, table=None, q_heads: 
             raise ValueError("table must be a contiguous fp32 CUDA tensor [positions, rotary_dim]")
         tp, (limit, rot) = table.data_ptr(), table.shape
     if out is None:
-        out = torch.empty((rows, n), dtype=torch.bfloat16, device=q.device)
+        out = _new((rows, n), torch.bfloat16, q.device, stream)
         op, ldo = out.data_ptr(), n
     else:
         if out.shape[0] != rows:
@@ -670,7 +686,7 @@ def attn_workspace(device="cuda"):
     return torch.zeros((_workspace_bytes,), dtype=torch.uint8, device=device)
 
 
-def _attn(q, cache, R, table, lens, q_heads, scale, out, workspace):
+def _attn(q, cache, R, table, lens, q_heads, scale, out, workspace, stream):
     import torch
     shape = q.shape
     if q_heads is None:
@@ -679,14 +695,15 @@ def _attn(q, cache, R, table, lens, q_heads, scale, out, workspace):
     qp, ldq = _rows2("q", q, torch.bfloat16, max(n, 1))
     tp, width, pitch = _table_of(table, R)
     if out is None:
-        out = torch.empty((shape[0], n), dtype=torch.bfloat16, device=q.device)
+        out = _new((shape[0], n), torch.bfloat16, q.device, stream)
         op, ldo = out.data_ptr(), n
     else:
         if out.shape[0] != shape[0]:
             raise ValueError("out must have q's rows")
         op, ldo = _rows2("out", out, torch.bfloat16, max(n, 1))
     if workspace is None:
-        workspace = attn_workspace(q.device)
+        workspace = _new((int(lib().q8_attn_workspace_bytes()),), torch.uint8, q.device, stream, zeroed=True,
+                         returned=False)  # of this call alone: its stream's again when the call returns
     elif not workspace.is_cuda or not workspace.is_contiguous() or \
             workspace.nbytes < (_workspace_bytes or lib().q8_attn_workspace_bytes()):
         raise ValueError("workspace must come from attn_workspace")
@@ -699,11 +716,11 @@ def attn_decode(q, cache: KVCache, table, lens, q_heads: int | None = None, scal
     """Attention of one new token a request over its pages (q8_attn_decode): q bf16 [R, >= q_heads * dim], block table
     int32 [R, width], lens int32 [R] (the new token included; 0: an idle row, which gets zeros).  ``window``: keys that
     far back or more are hidden (0: none), but for the first ``sinks``.  ``scale`` defaults to dim ** -0.5.
-    ``workspace``: :func:`attn_workspace`, one per stream (None: allocated and zeroed for this call).  Returns bf16
+    ``workspace``: :func:`attn_workspace`, one per stream (None: allocated and zeroed for this call, on its stream).  Returns bf16
     [R, q_heads * dim], the output projection's activation."""
     R = q.shape[0]
     qp, ldq, kv, tp, width, pitch, lp, op, ldo, q_heads, scale, out, workspace = \
-        _attn(q, cache, R, table, lens, q_heads, scale, out, workspace)
+        _attn(q, cache, R, table, lens, q_heads, scale, out, workspace, stream)
     if R == 0:
         return out
     st = lib().q8_attn_decode(qp, ldq, kv, tp, width, pitch, lp, op, ldo, R, q_heads, scale, window, sinks,
@@ -720,7 +737,7 @@ def attn_prefill(q, cache: KVCache, table, lens, row_start, q_heads: int | None 
     [R].  Rows past row_start[R] get zeros.  Other arguments as :func:`attn_decode`."""
     R, rows = lens.numel(), q.shape[0]
     qp, ldq, kv, tp, width, pitch, lp, op, ldo, q_heads, scale, out, workspace = \
-        _attn(q, cache, R, table, lens, q_heads, scale, out, workspace)
+        _attn(q, cache, R, table, lens, q_heads, scale, out, workspace, stream)
     if rows == 0:
         return out
     st = lib().q8_attn_prefill(qp, ldq, kv, tp, width, pitch, lp, _ints("row_start", row_start, R + 1), op, ldo, rows,
