@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_kernel(AppendArgs a)
                        fmaf(y.x, y.x, fmaf(y.y, y.y, fmaf(y.z, y.z, y.w * y.w)));
 #pragma unroll
             for (int o = 1; o < L; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            if ((is_q && a.qg) || (is_k && a.kg)) {
+            if (pos >= 0 && ((is_q && a.qg) || (is_k && a.kg))) {  // padding stays 0 whatever eps and gamma are
                 const float rs = rsqrtf(ss * (1.0f / D) + a.eps);
                 const float4 g0 = is_q ? gq[0] : gk[0], g1 = is_q ? gq[1] : gk[1];
                 x.x *= rs * g0.x; x.y *= rs * g0.y; x.z *= rs * g0.z; x.w *= rs * g0.w;

@@ -663,3 +663,35 @@ def test_prefill_long_walks_between_items(dev, work, kind, dim):
     (128, "q8", 16384), (128, "bf16", 16384)])
 def test_prefill_most_requests(dev, work, dim, kind, R):
     scattered(dev, work, R, kind, dim, R, 400)
+
+
+# ---- zeros, infinities and scales far apart -------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kind", ["bf16", "q8"])
+@pytest.mark.parametrize("dim,rot,interleaved,rows", [(64, 64, False, 9), (128, 32, True, 40), (128, 0, False, 700)])
+def test_append_padding_rows_are_zeros(dev, kind, dim, rot, interleaved, rows):
+    """Padding rows' q are zeros whatever the norm would make of nothing: eps = 0 (0 / 0), gammas that are not finite."""
+    import q8_block_quantized_gemv_gb300 as q8
+    torch, heads, kv_heads, page = dev, 20, 4, 16
+    rng = np.random.default_rng(dim + rows)
+    xs = [rng.standard_normal((rows, n * dim)).astype(np.float32) for n in (heads, kv_heads, kv_heads)]
+    pos = rng.integers(0, 100, rows).astype(np.int32)
+    pos[[0, rows // 2, rows - 1]] = -1, -7, -(2 ** 31)
+    gq, gk = ((0.5 + rng.random(dim)).astype(np.float32) for _ in range(2))
+    table = q8.rope_table(100, rot) if rot else None
+    live = pos >= 0
+    for bad in (0.5, np.inf, np.nan):
+        gq[dim - 1] = gk[dim - 1] = bad
+        cache = q8.KVCache.empty(-(-rows // page), kv_heads, page, dim, kind)
+        out = torch.full((rows, heads * dim), 9.0, dtype=torch.bfloat16, device="cuda")
+        q8.rope_append(*(torch.from_numpy(x).cuda() for x in xs), cache, torch.from_numpy(pos).cuda(),
+                       torch.arange(rows, device="cuda"), table=table, interleaved=interleaved,
+                       q_gamma=torch.from_numpy(gq).cuda(), k_gamma=torch.from_numpy(gk).cuda(), eps=0.0, out=out)
+        got = out.float().cpu().numpy().astype(np.float64).reshape(rows, heads, dim)
+        assert not np.any(got[~live]) and not np.any(np.isnan(got[~live]))
+        with np.errstate(invalid="ignore"):
+            want, mag = plain_append(xs[0].astype(np.float64).reshape(rows, heads, dim), gq, 0.0,
+                                     table.cpu().numpy() if rot else None, np.where(live, pos, 0), rot, interleaved)
+        fine = np.isfinite(want) & live[:, None, None]
+        fp = (dim / 4 + 16) * 2.0 ** -24
+        assert np.all(np.abs(got[fine] - want[fine]) <= (U * np.abs(want) + 1.01 * fp * mag + 2.0 ** -133)[fine])
