@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, Q8, NT>::kWarps, 1) attn_decode_ke
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
                         p[n][x] = s[n][x] - m[n][x & 1];
-                        above = above || p[n][x] > kSlack;
+                        above = above || !(p[n][x] <= kSlack);  // true of -inf less -inf, while all scores were -inf
                     }
                 if (__any_sync(0xffffffffu, above)) {
 #pragma unroll

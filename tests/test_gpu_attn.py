@@ -695,3 +695,42 @@ def test_append_padding_rows_are_zeros(dev, kind, dim, rot, interleaved, rows):
         fine = np.isfinite(want) & live[:, None, None]
         fp = (dim / 4 + 16) * 2.0 ** -24
         assert np.all(np.abs(got[fine] - want[fine]) <= (U * np.abs(want) + 1.01 * fp * mag + 2.0 ** -133)[fine])
+
+
+def below_all(torch, p, r, first, count):
+    """Keys [first, first + count) of request r: scores of -inf from queries that are positive in the first 32 values."""
+    for j in range(first, first + count):
+        page, off = int(p.table[r, j // p.page]), j % p.page
+        if p.kind == "bf16":
+            p.cache.k[page, :, off, 0] = -float("inf")
+        else:
+            p.cache.k[page, :, off, :32] = -127
+            p.cache.k_scale[page, :, off, 0] = float("inf")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "q8"])
+@pytest.mark.parametrize("heads,kv_heads,dim", [(2, 2, 128), (6, 2, 64), (20, 1, 128), (40, 2, 64)])
+@pytest.mark.parametrize("first", [0, 70])
+def test_decode_scores_of_minus_infinity(dev, work, kind, heads, kv_heads, dim, first):
+    """Keys with a score of -inf weigh nothing, as many of them as there may be before (and after) the first finite one."""
+    import q8_block_quantized_gemv_gb300 as q8
+    torch, lens, page = dev, [700, 3000, 29], 16
+    p = Paged(dev, lens, kv_heads, dim, page, kind, 121 + heads)
+    q, qn = queries(dev, 3, heads, dim, 122)
+    v = q.view(3, heads, dim)
+    v[..., :32] = v[..., :32].abs() + 0.5
+    qn = q.float().cpu().numpy().astype(np.float64).reshape(3, heads, dim)
+    gone = {0: (first, 600), 1: (first, 2900), 2: (first if first < 29 else 0, 20)}
+    for r, (at, n) in gone.items():
+        below_all(torch, p, r, at, n)
+    o, tol = np.zeros(qn.shape), np.zeros(qn.shape)
+    for r, n in enumerate(lens):
+        ok = np.ones((1, n), dtype=bool)
+        ok[0, gone[r][0]:gone[r][0] + gone[r][1]] = False
+        for h in range(heads):
+            g = h // (heads // kv_heads)
+            a, t16, t8 = reference(qn[r:r + 1, h], p.k[r][:, g], p.v[r][:, g], ok, dim ** -0.5)
+            o[r, h], tol[r, h] = a, t16 if kind == "bf16" else t8
+    agree(q8.attn_decode(q, p.cache, p.table_dev, p.lens_dev, workspace=work), o, tol)
+    starts = torch.arange(4, dtype=torch.int32, device="cuda")
+    agree(q8.attn_prefill(q, p.cache, p.table_dev, p.lens_dev, starts, workspace=work), o, tol)
