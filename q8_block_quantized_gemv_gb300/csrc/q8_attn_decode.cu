@@ -191,6 +191,26 @@ __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
     return d;
 }
 
+// The fp16 pair of (p0, p1) * d * per.
+__device__ __forceinline__ uint32_t weights_f16x2(float p0, float p1, float d, const uint32_t (&per)[2]) {
+    float w0, w1;
+    asm("{\n .reg .b64 p, d, u;\n mov.b64 p, {%2, %3};\n mov.b64 d, {%4, %4};\n mov.b64 u, {%5, %6};\n"
+        " mul.rn.f32x2 p, p, d;\n mul.rn.f32x2 p, p, u;\n mov.b64 {%0, %1}, p;\n}"
+        : "=f"(w0), "=f"(w1) : "f"(p0), "f"(p1), "f"(d), "r"(per[0]), "r"(per[1]));
+    return f16x2(w0, w1);
+}
+
+// 2^-n, 0 below the smallest normal.
+__device__ __forceinline__ float two_to_minus(int n) { return n > 126 ? 0.0f : __uint_as_float((uint32_t)(127 - n) << 23); }
+// The 32 values of a block that belong to head x of a lane's two, times f.
+__device__ __forceinline__ void scale_block(float (&lo)[4], float (&hi)[4], int x, float f) {
+    lo[x] *= f;
+    lo[x + 2] *= f;
+    hi[x] *= f;
+    hi[x + 2] *= f;
+}
+constexpr int kMostPer = 253;  // exponent field of 2^126, the largest power of two with a normal reciprocal
+
 // x / d for x < 2^27 as (x * mul) >> shift.  mul = ceil(2^shift / d) with 2^shift >= 2^27 d is off by less than one
 // part in 2^27, so the quotient is exact, and x * mul < 2^56.
 struct UnitDiv {
@@ -393,11 +413,14 @@ __global__ void __launch_bounds__(32 * Cfg<D, Q8, NT>::kWarps, 1) attn_decode_ke
             float off[NT][Q8 ? NB : 1][2];
             float sc[NT][2];  // scale * log2(e) of this lane's two heads (2t, 2t + 1)
             float m[NT][2], l[NT][2], o[NT][KS][4];
-            // Over a Q8_0 cache o's 32 values of block b are in units of unit[b], a power of two that follows the
-            // largest value scale met: the weights p * scale / unit then stay within fp16's range.
-            float unit[Q8 ? NB : 1], per_unit[Q8 ? NB : 1];
+            // Over a Q8_0 cache a head's 32 values of block b in o are in units of 1 / per[n][b], a power of two that
+            // follows the largest p * scale met: the weights p * scale * per then keep fp16's 11 bits down to 2^-22 of
+            // the largest, however far apart the scales of tokens that weigh much and little are.
+            uint32_t per[NT][Q8 ? NB : 1][2];  // as fp32 bits
 #pragma unroll
-            for (int b = 0; b < (Q8 ? NB : 1); ++b) unit[b] = per_unit[b] = 0.0f;
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int b = 0; b < (Q8 ? NB : 1); ++b) per[n][b][0] = per[n][b][1] = kMostPer << 23;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const uint16_t *qr = a.q + (size_t)c.r * a.ldq + (size_t)(head0 + 8 * n + g) * D;
@@ -547,15 +570,27 @@ __global__ void __launch_bounds__(32 * Cfg<D, Q8, NT>::kWarps, 1) attn_decode_ke
                             float mx = fmaxf(s[n][x], s[n][x + 2]);
 #pragma unroll
                             for (int sh = 4; sh < 32; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
+                            if (Q8) mx = ceilf(mx);  // maxima are whole numbers: what follows takes powers of two
                             mx = fmaxf(mx, m[n][x]);
-                            const float f = mx == m[n][x] ? 1.0f : ex2(m[n][x] - mx);
-                            m[n][x] = mx;
-                            l[n][x] *= f;
+                            if (!Q8) {
+                                const float f = mx == m[n][x] ? 1.0f : ex2(m[n][x] - mx);
+                                l[n][x] *= f;
 #pragma unroll
-                            for (int k = 0; k < KS; ++k) {
-                                o[n][k][x] *= f;
-                                o[n][k][x + 2] *= f;
+                                for (int k = 0; k < KS; ++k) {
+                                    o[n][k][x] *= f;
+                                    o[n][k][x + 2] *= f;
+                                }
+                            } else if (mx != m[n][x]) {  // o stays, its units shrink with the weights
+                                const int down = (int)fminf(mx - m[n][x], 1024.0f);
+                                l[n][x] *= two_to_minus(down);
+#pragma unroll
+                                for (int b = 0; b < NB; ++b) {
+                                    const int e = (int)(per[n][b][x] >> 23) + down;
+                                    if (e > kMostPer) scale_block(o[n][2 * b], o[n][2 * b + 1], x, two_to_minus(e - kMostPer));
+                                    per[n][b][x] = (uint32_t)min(e, kMostPer) << 23;
+                                }
                             }
+                            m[n][x] = mx;
                             const float m0 = mx == -INFINITY ? 0.0f : mx;  // nothing seen yet: weights 0
                             p[n][x] = s[n][x] - m0;
                             p[n][x + 2] = s[n][x + 2] - m0;
@@ -586,36 +621,44 @@ __global__ void __launch_bounds__(32 * Cfg<D, Q8, NT>::kWarps, 1) attn_decode_ke
                         for (int n = 0; n < NT; ++n) mma_bf16(o[n][k], vf, pf[n][0], pf[n][1]);
                     }
                 } else {
-                    // The codes are exact in fp16; the tokens' scales go to the weights, p * scale / unit, rounded to
-                    // fp16 (11 bits; below 2^-14 of the unit they lose bits that do not reach the result).
+                    // The codes are exact in fp16; the tokens' scales go to the weights, p * scale * per, rounded to fp16.
                     float da[NB], db[NB];
                     load_scales<NB>(da, at + sr + C::kScales);
                     load_scales<NB>(db, at + sr + C::kScales + 2 * NB * 4);
-                    bool big = false;
+                    uint32_t wa[NT][NB], wb[NT][NB];  // of tokens ja and jb
+                    auto weigh = [&]() {
+                        __half2 top = __float2half2_rn(0.0f);
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) big = big || fmaxf(fabsf(da[b]), fabsf(db[b])) > 4.0f * unit[b];
-                    if (__any_sync(0xffffffffu, big)) {
+                        for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int b = 0; b < NB; ++b) {
-                            float mx = fmaxf(fabsf(da[b]), fabsf(db[b]));
-#pragma unroll
-                            for (int sh = 4; sh < 32; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
-                            if (mx > 4.0f * unit[b]) {
-                                // the power of two at or below the largest scale, within what has a reciprocal
-                                const float now = __uint_as_float(
-                                    min(max(__float_as_uint(mx) & 0x7F800000u, 0x01000000u), 0x7E000000u));
-                                const float f = unit[b] * (1.0f / now);
-#pragma unroll
-                                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                                    for (int x = 0; x < 4; ++x) {
-                                        o[n][2 * b][x] *= f;
-                                        o[n][2 * b + 1][x] *= f;
-                                    }
-                                unit[b] = now;
-                                per_unit[b] = 1.0f / now;
+                            for (int b = 0; b < NB; ++b) {
+                                wa[n][b] = weights_f16x2(p[n][0], p[n][1], da[b], per[n][b]);
+                                wb[n][b] = weights_f16x2(p[n][2], p[n][3], db[b], per[n][b]);
+                                top = __hmax2(top, __habs2(*reinterpret_cast<const __half2 *>(&wa[n][b])));
+                                top = __hmax2(top, __habs2(*reinterpret_cast<const __half2 *>(&wb[n][b])));
                             }
-                        }
+                        // some weight above 2^15 (0x7800; infinity is 0x7C00)
+                        return ((*reinterpret_cast<const uint32_t *>(&top) + 0x07FF07FFu) & 0x80008000u) != 0u;
+                    };
+                    if (__any_sync(0xffffffffu, weigh())) {
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                                for (int x = 0; x < 2; ++x) {
+                                    float mx = fmaxf(p[n][x] * fabsf(da[b]), p[n][x + 2] * fabsf(db[b]));
+#pragma unroll
+                                    for (int sh = 4; sh < 32; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
+                                    const int old = (int)(per[n][b][x] >> 23);
+                                    if (mx * __uint_as_float(per[n][b][x]) > 32768.0f) {
+                                        // the largest weight comes to [2^8, 2^9)
+                                        const int e = 127 + 127 + 8 - (int)(__float_as_uint(mx) >> 23);
+                                        scale_block(o[n][2 * b], o[n][2 * b + 1], x, two_to_minus(old - e));
+                                        per[n][b][x] = (uint32_t)e << 23;
+                                    }
+                                }
+                        weigh();
                     }
 #pragma unroll
                     for (int b = 0; b < NB; ++b) {
@@ -627,11 +670,10 @@ __global__ void __launch_bounds__(32 * Cfg<D, Q8, NT>::kWarps, 1) attn_decode_ke
                                                 codes_f16x2<2>(w[1])};
                         const uint32_t v1[4] = {codes_f16x2<0>(w[2]), codes_f16x2<0>(w[3]), codes_f16x2<2>(w[2]),
                                                 codes_f16x2<2>(w[3])};
-                        const float fa = da[b] * per_unit[b], fb = db[b] * per_unit[b];
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
-                            const uint32_t q0 = transposed8x8(f16x2(p[n][0] * fa, p[n][1] * fa));
-                            const uint32_t q1 = transposed8x8(f16x2(p[n][2] * fb, p[n][3] * fb));
+                            const uint32_t q0 = transposed8x8(wa[n][b]);
+                            const uint32_t q1 = transposed8x8(wb[n][b]);
                             mma_f16(o[n][2 * b], v0, q0, q1);
                             mma_f16(o[n][2 * b + 1], v1, q0, q1);
                         }
@@ -650,7 +692,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, Q8, NT>::kWarps, 1) attn_decode_ke
                     float *row = po + (8 * n + 2 * t + x) * D;
 #pragma unroll
                     for (int k = 0; k < KS; ++k) {
-                        const float f = Q8 ? unit[Q8 ? k / 2 : 0] : 1.0f;
+                        const float f = Q8 ? __uint_as_float(0x7F000000u - per[n][Q8 ? k / 2 : 0][x]) : 1.0f;
                         row[16 * k + g] = o[n][k][x] * f;
                         row[16 * k + g + 8] = o[n][k][x + 2] * f;
                     }

@@ -734,3 +734,80 @@ def test_decode_scores_of_minus_infinity(dev, work, kind, heads, kv_heads, dim, 
     agree(q8.attn_decode(q, p.cache, p.table_dev, p.lens_dev, workspace=work), o, tol)
     starts = torch.arange(4, dtype=torch.int32, device="cuda")
     agree(q8.attn_prefill(q, p.cache, p.table_dev, p.lens_dev, starts, workspace=work), o, tol)
+
+
+def value_scales(torch, p, r, factor):
+    """Request r's value scales times factor [len, kv_heads, dim / 32], powers of two: in the cache and in p.v."""
+    n, f = p.lens[r], torch.from_numpy(factor.astype(np.float32)).cuda()
+    j = torch.arange(n, device="cuda")
+    pages = p.table_dev[r].long()[j // p.page]
+    p.cache.v_scale[pages, :, j % p.page] = p.cache.v_scale[pages, :, j % p.page] * f
+    p.v[r] = p.v[r] * np.repeat(factor, 32, axis=2)
+
+
+def far_apart(torch, lens, kv_heads, dim, page, how, seed):
+    """A Q8_0 cache whose value scales lie far apart, and the keys of each request that weigh something.
+
+    ("unseen", e): a tenth of the keys have scores some hundred below the others', weights of nothing, and value scales
+    2^e times theirs; ("sink", e): one key has all the weight, and a value scale 2^-e of the others'; ("blocks", e): the
+    blocks of a head in turn 2^-e, 1 and 2^e; ("all", e): every scale times 2^-e to 2^e."""
+    what, e = how
+    p = Paged(torch, lens, kv_heads, dim, page, "q8", seed)
+    rng = np.random.default_rng(seed + 1)
+    keep = []
+    for r, n in enumerate(lens):
+        shape = (n, kv_heads, dim // 32)
+        factor, ok = np.ones(shape), np.ones(n, dtype=bool)
+        if what in ("unseen", "sink"):
+            if what == "unseen":
+                ok[rng.permutation(n)[:n // 10]] = False
+                odd, code = np.nonzero(~ok)[0], -127
+                factor[~ok] = 2.0 ** e
+            else:
+                at = int(rng.integers(n // 2, n))
+                ok[:] = False
+                ok[at] = True
+                odd, code = [at], 127
+                factor[at] = 2.0 ** -e
+            for j in odd:
+                pg, off = int(p.table[r, j // page]), j % page
+                p.cache.k[pg, :, off, :32] = code
+                p.cache.k_scale[pg, :, off, 0] = 1.0
+                p.k[r][j, :, :32] = code
+        elif what == "blocks":
+            factor[:] = 2.0 ** (e * (np.arange(dim // 32) % 3 - 1))
+        else:
+            factor = 2.0 ** rng.integers(-e, e + 1, shape)
+        value_scales(torch, p, r, factor)
+        keep.append(ok)
+    return p, keep
+
+
+FAR = [("unseen", 14), ("unseen", 20), ("unseen", 26), ("unseen", 60), ("sink", 14), ("sink", 22), ("blocks", 9),
+       ("blocks", 14), ("all", 8), ("all", 13), ("all", 30)]
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim", [(8, 2, 128), (12, 1, 64)])
+@pytest.mark.parametrize("how", FAR)
+def test_decode_value_scales_far_apart(dev, work, how, heads, kv_heads, dim):
+    """What a token's value scale is has no bearing on how well the others' values are added up."""
+    import q8_block_quantized_gemv_gb300 as q8
+    p, keep = far_apart(dev, [1500, 5000, 333], kv_heads, dim, 32, how, 131 + heads)
+    q, _ = queries(dev, 3, heads, dim, 132)
+    v = q.view(3, heads, dim)
+    v[..., :32] = v[..., :32].abs() + 0.5
+    qn = q.float().cpu().numpy().astype(np.float64).reshape(3, heads, dim)
+    o, tol = np.zeros(qn.shape), np.zeros(qn.shape)
+    for r in range(3):
+        for h in range(heads):
+            g = h // (heads // kv_heads)
+            o[r, h], _, tol[r, h] = reference(qn[r:r + 1, h], p.k[r][:, g], p.v[r][:, g], keep[r][None], dim ** -0.5)
+    agree_by_block(q8.attn_decode(q, p.cache, p.table_dev, p.lens_dev, workspace=work), o, tol)
+
+
+def agree_by_block(got, want, tol):
+    """agree, with the bound of the 2-norm for each block of 32 values: their sizes may be far apart."""
+    agree(got, want, tol)
+    diff = got.float().cpu().numpy().astype(np.float64).reshape(-1, 32) - want.reshape(-1, 32)
+    # 32 roundings of u / sqrt(3) at most: their 2-norm stays below u but for one block in many millions
+    assert np.all(np.linalg.norm(diff, axis=1) <= U * np.linalg.norm(want.reshape(-1, 32), axis=1))
