@@ -17,7 +17,10 @@
 //     the V tiles that some row does not see whole, and clear what nobody sees;
 //   Q8_0 cache: codes and scales arrive by bulk copies, and the helpers (six warps) turn them into fp16 operands,
 //     code * scale / unit with one power of two `unit` a tile, as the softmax threads do Q with one a row: 11 significant
-//     bits.  (bf16 operands would cost the scores and values 8-bit roundings: measured 0.0029 against 0.0017 relative error.)
+//     bits for scales down to 2^-21 of the tile's largest (for values, of the largest so far), fewer below.  For scores that is
+//     what fp32 sums of the largest keep.  An output block so small beside the largest values that it may have lost bits is
+//     computed again in fp32 by its row's thread (a rare, slow walk).  (bf16 operands would cost the scores and values 8-bit
+//     roundings: measured 0.0029 against 0.0017 relative error.)
 //
 // The tiles of all items are one list, cut into equal spans, one for each CTA (one CTA per SM); an item that crosses
 // spans leaves fp32 parts in the workspace, which the CTA that arrives last adds in span order.
@@ -111,7 +114,8 @@ template <int D, bool Q8> struct Control {
     int2 tile[8];
     float unit[2][8];   // Q8_0: log2 of the keys' and the values' unit
     uint32_t tmem;
-    int abort, poison, last;
+    int abort, last;
+    int poison, lost;   // values were cleared; or are below fp16's normal range (Q8_0)
     int first_r, first_qt;
     long long first_start;
     long long scan[20];
@@ -537,6 +541,38 @@ __device__ __noinline__ void add_nonfinite(const AttnArgs &a, const Item it, int
     }
 }
 
+// 32 of a row's values from column c0 once more, in fp32 from the Q8_0 cache itself, where none is as large as `least`.  The
+// row: token tok, head gh of those that share the cache head; M: its maximum as the softmax has it; o: times inv.
+template <int D>
+__device__ __noinline__ void attend_again(const AttnArgs &a, const Item it, int i0, int i1, int tok, int gh, float M, float inv,
+                                          float least, int c0, float *o) {
+    float most = 0.0f;
+    for (int d = 0; d < 32; ++d) most = fmaxf(most, fabsf(o[d]));
+    if (!(most < least) || isnan(o[0])) return;
+    const int p = it.p_min + tok;
+    const uint16_t *q = a.q + (size_t)(it.row0 + it.tok0 + tok) * a.ldq + (it.h * a.group + gh) * D;
+    for (int d = 0; d < 32; ++d) o[d] = 0.0f;
+    for (int v = i0 * kTile; v < i1 * kTile; ++v) {
+        const int j = it.key(v);
+        if (j >= it.end) break;
+        if (!sees(a, p, j)) continue;
+        const int page = a.table[(size_t)it.r * a.pitch + j / a.page_size];
+        if (page < 0 || page >= a.pages) continue;
+        const long long at = (long long)page * a.page_stride + ((long long)it.h * a.page_size + j % a.page_size) * D;
+        const float scale = a.vs[(at + c0) / 32];
+        if (!(fabsf(scale) < INFINITY)) continue;  // add_nonfinite's
+        float s = 0.0f;
+        for (int b = 0; b < D / 32; ++b) {
+            float sum = 0.0f;
+            for (int d = 32 * b; d < 32 * b + 32; ++d)
+                sum = fmaf(__uint_as_float((uint32_t)q[d] << 16), (float)static_cast<const signed char *>(a.k)[at + d], sum);
+            s = fmaf(sum, a.ks[at / 32 + b], s);
+        }
+        const float w = ex2(s * (a.scale * kLog2e) - M) * inv * scale;
+        for (int d = 0; d < 32; ++d) o[d] = fmaf(w, (float)static_cast<const signed char *>(a.v)[at + c0 + d], o[d]);
+    }
+}
+
 template <int D, bool Q8>
 __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
     prefill_kernel(const __grid_constant__ PrefillArgs pa, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -570,7 +606,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
         for (int i = 0; i < 2; ++i) bar_init(&ctl.o_full[i], 1);
         bar_init(&ctl.idle, 4);
         ctl.abort = 0;
-        ctl.poison = 0;
+        ctl.poison = ctl.lost = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 0) {
@@ -1051,12 +1087,14 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                         }
                         mx = __reduce_max_sync(0xffffffffu, mx);
                     }
-                    // The values' unit only grows within a segment, and neither is below 2^-63, so that a tile of
+                    // The values' unit only grows within a segment, and neither is below 2^-70, so that a tile of
                     // zeros does not take the row sums, which are kept apart from the units, out of fp32's range.
                     int ex = min(max((int)(mx >> 23), 64), 252);
                     if (kv) ex = v_ex = max(v_ex, ex);
-                    const float down = __uint_as_float((uint32_t)(254 - ex) << 23);  // 2^-(ex - 127)
-                    bool found = false;
+                    // The unit is 2^-7 of the largest scale's power of two: scale / unit is below 2^8, any int8 code times
+                    // it within fp16's range, and its smallest normal 2^-21 of the largest.
+                    const float down = __uint_as_float((uint32_t)(254 + 7 - ex) << 23);  // 2^-(ex - 7 - 127)
+                    bool found = false, lost = false;
                     // Thread ht takes 16 codes of rows r0, r0 + HT / RC, ...: a step of whole swizzle periods, so that
                     // all addresses are its first ones plus constants.
                     constexpr int RC = D / 16, RS = HT / RC;  // chunks of 16 codes a row, rows a pass
@@ -1096,6 +1134,8 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                         for (int z = 0; z < B; ++z) {
                             if ((y + z + 1) * RS > kTile && r0 + (y + z) * RS >= kTile) break;
                             const __half2 f2 = __float2half2_rn(f[z]);
+                            // not 0 and below 2^-14, fp16's smallest normal
+                            lost = lost || (__float_as_uint(f[z]) & 0x7FFFFFFFu) - 1u < 0x38800000u - 1u;
                             const uint32_t w[4] = {(swap ? v[z].z : v[z].x) ^ 0x80808080u, (swap ? v[z].w : v[z].y) ^ 0x80808080u,
                                                    (swap ? v[z].x : v[z].z) ^ 0x80808080u, (swap ? v[z].y : v[z].w) ^ 0x80808080u};
                             uint32_t h[8];
@@ -1111,7 +1151,8 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                         }
                     }
                     if (found) *(volatile int *)&ctl.poison = 1;
-                    if (ht == 0) ctl.unit[kv][(cnt >> 1) & 7] = (float)(ex - 127);
+                    if (kv && lost) *(volatile int *)&ctl.lost = 1;
+                    if (ht == 0) ctl.unit[kv][(cnt >> 1) & 7] = (float)(ex - 7 - 127);
                     fence_async();
                     __syncwarp();
                     if (lane == 0) {
@@ -1269,7 +1310,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
             const long long last_unit = it.start + it.n - 1;
             const int c0 = (int)quotient(it.start, span), c1 = (int)quotient(last_unit, span);
             const bool wide = (((uintptr_t)a.out | (uintptr_t)(2 * a.ldo)) & 31) == 0;
-            const bool poison = *(volatile int *)&ctl.poison != 0;
+            const bool poison = *(volatile int *)&ctl.poison != 0, rare = poison || (Q8 && *(volatile int *)&ctl.lost);
             float *base = reinterpret_cast<float *>(a.work + kPrefillPartAt);
             uint16_t *orow = a.out + (size_t)(it.row0 + it.tok0 + (row_live ? tok : 0)) * a.ldo + (it.h * a.group + gh) * D;
             float *part = base + ((long long)blockIdx.x * 2 + (it.start >= b0)) * kPrefillPartFloats;
@@ -1283,11 +1324,16 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                     float o[32];
 #pragma unroll
                     for (int k = 0; k < 32; ++k) o[k] = __uint_as_float(v[k]) * inv;
-                    if (poison && row_live) {
+                    if (rare && row_live) {
                         float extra[32];
 #pragma unroll
                         for (int k = 0; k < 32; ++k) extra[k] = o[k];
-                        add_nonfinite<D, Q8>(a, it, i0, i1, p, cc, extra);
+                        // values below fp16's normal range are off by 2^-18 units at most, a sum of them by l 2^-18
+                        if (Q8 && *(volatile int *)&ctl.lost) {
+                            const float shift = *(volatile float *)&ctl.unit[1][(cnt / 2 - 1) & 7];  // of the last tile
+                            attend_again<D>(a, it, i0, i1, tok, gh, M, inv, l * inv * ex2(shift - 8.0f), cc, extra);
+                        }
+                        if (poison) add_nonfinite<D, Q8>(a, it, i0, i1, p, cc, extra);
 #pragma unroll
                         for (int k = 0; k < 32; ++k) o[k] = extra[k];
                     }

@@ -811,3 +811,50 @@ def agree_by_block(got, want, tol):
     diff = got.float().cpu().numpy().astype(np.float64).reshape(-1, 32) - want.reshape(-1, 32)
     # 32 roundings of u / sqrt(3) at most: their 2-norm stays below u but for one block in many millions
     assert np.all(np.linalg.norm(diff, axis=1) <= U * np.linalg.norm(want.reshape(-1, 32), axis=1))
+
+
+def far_expected(p, qn, starts, keep):
+    """Results, tolerances, and the 2-norms of each element's terms, w_j v_j, for causal rows.  Where a row sees keys that
+    `keep` names, or the others, one kind has no weight to speak of and is left out of the sums."""
+    rows, heads, dim = qn.shape
+    o, tol, terms = np.zeros(qn.shape), np.zeros(qn.shape), np.zeros(qn.shape)
+    group = heads // p.kv_heads
+    for r, n in enumerate(p.lens):
+        t0, t1 = starts[r], starts[r + 1]
+        for t in range(t0, t1):
+            causal = seen(n - (t1 - t0) + t - t0, n, 0, 0)
+            ok = causal & keep[r] if (causal & keep[r]).any() else causal
+            j = np.nonzero(ok)[0]
+            for h in range(heads):
+                k, v = p.k[r][:, h // group], p.v[r][:, h // group]
+                o[t, h], _, tol[t, h] = (x[0] for x in reference(qn[t:t + 1, h], k, v, ok[None], dim ** -0.5))
+                w = np.exp(k[j] @ qn[t, h] * dim ** -0.5 - (k[j] @ qn[t, h]).max() * dim ** -0.5)
+                terms[t, h] = np.sqrt(((w / w.sum())[:, None] ** 2 * v[j] ** 2).sum(0))
+    return o, tol, terms
+
+
+@pytest.mark.parametrize("heads,kv_heads,dim", [(4, 2, 128), (6, 1, 64)])
+@pytest.mark.parametrize("how", FAR)
+def test_prefill_value_scales_far_apart(dev, work, how, heads, kv_heads, dim):
+    """The same for a chunk behind a context, a whole prompt (whose first rows see little of a tile that others see whole),
+    and a few rows of a context split over many CTAs.
+
+    Element by element as everywhere; and each block of 32 values on its own: a value is rounded twice and a weight once to
+    11 bits, scores by some 2^-11 of their size: random, less than u = 2^-8 of the terms' 2-norm together, and the result
+    to bf16, u of it."""
+    import q8_block_quantized_gemv_gb300 as q8
+    lens, counts = [700, 150, 2500], [70, 150, 5]
+    p, keep = far_apart(dev, lens, kv_heads, dim, 32, how, 141 + heads)
+    starts = [0, *np.cumsum(counts).tolist()]
+    q, _ = queries(dev, starts[-1], heads, dim, 142)
+    v = q.view(-1, heads, dim)
+    v[..., :32] = v[..., :32].abs() + 0.5
+    qn = q.float().cpu().numpy().astype(np.float64).reshape(-1, heads, dim)
+    o, tol, terms = far_expected(p, qn, starts, keep)
+    got = q8.attn_prefill(q, p.cache, p.table_dev, p.lens_dev, dev.tensor(starts, dtype=dev.int32, device="cuda"),
+                          workspace=work)
+    agree(got, o, tol)
+    off = np.linalg.norm(got.float().cpu().numpy().astype(np.float64).reshape(-1, 32) - o.reshape(-1, 32), axis=1)
+    allowed = U * (np.linalg.norm(o.reshape(-1, 32), axis=1) + np.linalg.norm(terms.reshape(-1, 32), axis=1))
+    assert np.all(off <= allowed), (off / allowed).max()
+    assert q8.device_fault() == 0
