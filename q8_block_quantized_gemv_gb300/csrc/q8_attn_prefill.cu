@@ -462,7 +462,7 @@ struct Item {
 __device__ __forceinline__ void span_of(const PrefillArgs &pa, Item &x) {
     const AttnArgs &a = pa.a;
     x.end = min(max(x.p_max + 1, 0), a.width * a.page_size);
-    x.lo = a.window ? min(max(x.p_min - a.window + 1, 0), x.end) : 0;
+    x.lo = a.window ? min(max(max(x.p_min, 0) - a.window + 1, 0), x.end) : 0;  // a position may be negative, a window 2^31 - 1
     const int ul = x.lo & -pa.run, sinks = a.window ? min(a.sinks, ul) : 0;
     x.sinks = (sinks + pa.run - 1) & -pa.run;  // not past ul, which is whole runs too
     x.jump = sinks == a.sinks ? ul - x.sinks : 0;
@@ -1217,7 +1217,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                     if (info.y >> (8 + x) & 1) {
                         // columns [c_lo, c_hi] and [0, c_sink) are visible
                         const int j0 = info.x + it.jump;
-                        hide_scores<D>(ts, min(p, it.end - 1) - j0, a.window ? max(p - a.window + 1 - j0, 0) : 0,
+                        hide_scores<D>(ts, min(p, it.end - 1) - j0, a.window ? max(max(p, 0) - (a.window - 1), j0) - j0 : 0,
                                        a.window ? a.sinks - info.x : 0, info.y);
                     }
                     // The weights are taken against the running maximum as it stands: a row's maximum is only looked

@@ -858,3 +858,19 @@ def test_prefill_value_scales_far_apart(dev, work, how, heads, kv_heads, dim):
     allowed = U * (np.linalg.norm(o.reshape(-1, 32), axis=1) + np.linalg.norm(terms.reshape(-1, 32), axis=1))
     assert np.all(off <= allowed), (off / allowed).max()
     assert q8.device_fault() == 0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "q8"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("window,sinks", [(2 ** 31 - 1, 0), (2 ** 31 - 4, 3), (40, 2), (1, 0)])
+def test_prefill_rows_before_the_first_key(dev, work, kind, dim, window, sinks):
+    """Chunks longer than their requests: rows at negative positions see nothing, the others what the window lets them,
+    the widest one that the argument holds too."""
+    import q8_block_quantized_gemv_gb300 as q8
+    lens, counts = [10, 40, 0, 333], [20, 171, 5, 400]
+    p = Paged(dev, lens, 2, dim, 16, kind, 151)
+    starts = [0, *np.cumsum(counts).tolist()]
+    q, qn = queries(dev, starts[-1], 6, dim, 152)
+    got = q8.attn_prefill(q, p.cache, p.table_dev, p.lens_dev, dev.tensor(starts, dtype=dev.int32, device="cuda"),
+                          window=window, sinks=sinks, workspace=work)
+    agree(got, *expected(p, qn, starts, dim ** -0.5, window, sinks))
