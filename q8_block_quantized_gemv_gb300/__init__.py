@@ -627,7 +627,7 @@ def _rows2(name, x, dtype, cols):
     shape = x.shape
     if not x.is_cuda or x.dtype != dtype or len(shape) != 2 or shape[1] < cols or x.stride(1) != 1:
         raise ValueError(f"{name} must be a 2-D {dtype} CUDA tensor of at least {cols} columns, unit column stride")
-    return x.data_ptr(), x.stride(0) if shape[0] > 1 else shape[1]
+    return x.data_ptr(), x.stride(0) if shape[0] > 1 else cols  # one row has no pitch
 
 
 def rope_append(q, k, v, cache: KVCache, positions, slots, table=None, q_heads: int | None = None,

@@ -874,3 +874,26 @@ def test_prefill_rows_before_the_first_key(dev, work, kind, dim, window, sinks):
     got = q8.attn_prefill(q, p.cache, p.table_dev, p.lens_dev, dev.tensor(starts, dtype=dev.int32, device="cuda"),
                           window=window, sinks=sinks, workspace=work)
     agree(got, *expected(p, qn, starts, dim ** -0.5, window, sinks))
+
+
+@pytest.mark.parametrize("extra", [1, 3, 40])
+def test_one_row_of_any_width(dev, work, extra):
+    """A single row's column count is no pitch: any number beyond the heads' is taken, in inputs and in out."""
+    import q8_block_quantized_gemv_gb300 as q8
+    torch, heads, dim = dev, 4, 64
+    p = Paged(torch, [77], 2, dim, 16, "bf16", 161)
+    q, qn = queries(torch, 1, heads, dim, 162, pad=extra)
+    want, tol = expected(p, qn, [0, 1], dim ** -0.5, 0, 0)
+    starts = torch.arange(2, dtype=torch.int32, device="cuda")
+    wide = lambda dt: torch.full((1, heads * dim + extra), 7.0, dtype=dt, device="cuda")  # noqa: E731
+    for call in (lambda o: q8.attn_decode(q, p.cache, p.table_dev, p.lens_dev, q_heads=heads, out=o, workspace=work),
+                 lambda o: q8.attn_prefill(q, p.cache, p.table_dev, p.lens_dev, starts, q_heads=heads, out=o, workspace=work)):
+        out = wide(torch.bfloat16)
+        call(out)
+        agree(out[:, :heads * dim], want, tol)
+        assert torch.all(out[:, heads * dim:] == 7.0)
+    x = [torch.randn((1, n * dim + extra), device="cuda") for n in (heads, 2, 2)]
+    at = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = wide(torch.bfloat16)
+    q8.rope_append(*x, q8.KVCache.empty(1, 2, 16, dim), at, at.long(), q_heads=heads, out=out)
+    assert torch.equal(out[:, :heads * dim], x[0][:, :heads * dim].bfloat16()) and torch.all(out[:, heads * dim:] == 7.0)
