@@ -511,7 +511,7 @@ class KVCache:
         for x, shape, ps in ((k, k.shape, stride), (v, k.shape, stride)) + (
                 ((k_scale, (*k.shape[:3], dim // Q8_BLOCK), stride // Q8_BLOCK),
                  (v_scale, (*k.shape[:3], dim // Q8_BLOCK), stride // Q8_BLOCK)) if q8 or v_scale is not None else ()):
-            if x is None or not x.is_cuda or x.device != k.device or tuple(x.shape) != tuple(shape):
+            if x is None or not x.is_cuda or x.get_device() != k.get_device() or tuple(x.shape) != tuple(shape):
                 raise ValueError("k, v and the scales must be CUDA tensors of one device, the scales [..., dim / 32]")
             if pages and not x[0].is_contiguous() or (pages > 1 and x.stride(0) != ps):
                 raise ValueError("a page must be contiguous, and the pages of k, v and the scales equally far apart")
@@ -522,7 +522,7 @@ class KVCache:
         self.pages, self.heads, self.page_size, self.dim, self.device = pages, heads, page_size, dim, k.device
         self._c = _KV(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if q8 else None,
                       v_scale.data_ptr() if q8 else None, stride, pages, heads, page_size, dim)
-        self._ref = ctypes.addressof(self._c)
+        self._ref, self._index = ctypes.addressof(self._c), k.get_device()
 
     @classmethod
     def empty(cls, pages: int, heads: int, page_size: int, dim: int, dtype: str = "bf16", device="cuda"):
@@ -538,19 +538,24 @@ class KVCache:
                    *(torch.zeros(sshape, dtype=torch.float32, device=device) for _ in range(2)))
 
 
-def _ints(name, t, n=None):
+# The tensors of one call are on one device: `index` is the cache's, or the first tensor's (-1: on the CPU).
+
+def _ints(name, t, index, n=None):
     import torch
-    if not t.is_cuda or t.dtype != torch.int32 or not t.is_contiguous() or (n is not None and t.numel() != n):
-        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor" + (f" of {n} values" if n is not None else ""))
+    if index < 0 or t.get_device() != index or t.dtype != torch.int32 or not t.is_contiguous() or \
+            (n is not None and t.numel() != n):
+        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor" + (f" of {n} values" if n is not None else "") +
+                         ", on the device of the others")
     return t.data_ptr()
 
 
-def _table_of(table, R):
+def _table_of(table, R, index):
     import torch
     shape = table.shape
-    if not table.is_cuda or table.dtype != torch.int32 or len(shape) != 2 or shape[0] != R or \
+    if table.get_device() != index or table.dtype != torch.int32 or len(shape) != 2 or shape[0] != R or \
             (shape[1] > 1 and table.stride(1) != 1):
-        raise ValueError(f"the block table must be an int32 CUDA tensor [{R}, width] with unit column stride")
+        raise ValueError(f"the block table must be an int32 CUDA tensor [{R}, width] with unit column stride, on the device "
+                         "of the others")
     return table.data_ptr(), shape[1], table.stride(0) if R > 1 else shape[1]
 
 
@@ -560,10 +565,9 @@ def kv_slots(cached, fresh, table, free_pages, page_size: int, rows: int, head=N
     place.  Returns a dict of CUDA tensors: table, lens int32 [R], row_start int32 [R + 1], positions int32 [rows],
     slots int64 [rows] (rows past the total: -1), head int32 [1], the next step's.  ``out``: such a dict to write."""
     import torch
-    R = cached.numel()
-    c, f = _ints("cached", cached), _ints("fresh", fresh, R)
-    t, width, pitch = _table_of(table, R)
-    dev = cached.device
+    R, index, dev = cached.numel(), cached.get_device(), cached.device
+    c, f = _ints("cached", cached, index), _ints("fresh", fresh, index, R)
+    t, width, pitch = _table_of(table, R, index)
     if out is None:
         i32 = torch.int32  # tensors of their own: cheaper than views of one
         lens, starts = _new(R, i32, dev, stream), _new(R + 1, i32, dev, stream)
@@ -574,13 +578,13 @@ def kv_slots(cached, fresh, table, free_pages, page_size: int, rows: int, head=N
         lp, sp, pp, hp = lens.data_ptr(), starts.data_ptr(), positions.data_ptr(), next_head.data_ptr()
     else:
         slots = out["slots"]
-        if slots.dtype != torch.int64 or slots.numel() != rows or not slots.is_contiguous() or not slots.is_cuda \
-                or out["table"] is not table:
+        if slots.dtype != torch.int64 or slots.numel() != rows or not slots.is_contiguous() \
+                or slots.get_device() != index or out["table"] is not table:
             raise ValueError("out must hold this table and contiguous CUDA tensors of the sizes kv_slots returns")
-        lp, sp = _ints("lens", out["lens"], R), _ints("row_start", out["row_start"], R + 1)
-        hp, pp = _ints("head", out["head"], 1), _ints("positions", out["positions"], rows)
-    st = lib().q8_kv_slots(c, f, R, page_size, _ints("free_pages", free_pages), free_pages.numel(),
-                           None if head is None else _ints("head", head, 1), t, width, pitch, rows, lp, sp, pp,
+        lp, sp = _ints("lens", out["lens"], index, R), _ints("row_start", out["row_start"], index, R + 1)
+        hp, pp = _ints("head", out["head"], index, 1), _ints("positions", out["positions"], index, rows)
+    st = lib().q8_kv_slots(c, f, R, page_size, _ints("free_pages", free_pages, index), free_pages.numel(),
+                           None if head is None else _ints("head", head, index, 1), t, width, pitch, rows, lp, sp, pp,
                            slots.data_ptr(), hp, _stream_of(stream, dev))
     if st:
         raise Q8Error(st, "q8_kv_slots")
@@ -623,10 +627,11 @@ def rope_table(positions: int, rotary_dim: int, base: float = 10000.0, scaling=N
     return torch.from_numpy(both.astype(np.float32)).to(device)
 
 
-def _rows2(name, x, dtype, cols):
+def _rows2(name, x, dtype, cols, index):
     shape = x.shape
-    if not x.is_cuda or x.dtype != dtype or len(shape) != 2 or shape[1] < cols or x.stride(1) != 1:
-        raise ValueError(f"{name} must be a 2-D {dtype} CUDA tensor of at least {cols} columns, unit column stride")
+    if x.get_device() != index or x.dtype != dtype or len(shape) != 2 or shape[1] < cols or x.stride(1) != 1:
+        raise ValueError(f"{name} must be a 2-D {dtype} CUDA tensor of at least {cols} columns, unit column stride, on the "
+                         "cache's device")
     return x.data_ptr(), x.stride(0) if shape[0] > 1 else cols  # one row has no pitch
 
 
@@ -637,24 +642,24 @@ def rope_append(q, k, v, cache: KVCache, positions, slots, table=None, q_heads: 
     slots int64 [rows] (:func:`kv_slots`); ``table``: :func:`rope_table`, its width the rotated part of a head (None:
     no rotation).  Returns q, bf16 [rows, q_heads * dim]."""
     import torch
-    dim, f32 = cache.dim, torch.float32
+    dim, f32, index = cache.dim, torch.float32, cache._index
     if q_heads is None:
-        q_heads = q.shape[1] // dim
+        q_heads = q.shape[-1] // dim
     rows, n, m = q.shape[0], q_heads * dim, cache.heads * dim
-    qp, ldq = _rows2("q", q, f32, max(n, 1))
-    kp, ldk = _rows2("k", k, f32, m)
-    vp, ldv = _rows2("v", v, f32, m)
+    qp, ldq = _rows2("q", q, f32, max(n, 1), index)
+    kp, ldk = _rows2("k", k, f32, m, index)
+    vp, ldv = _rows2("v", v, f32, m, index)
     if k.shape[0] != rows or v.shape[0] != rows:
         raise ValueError("q, k and v must have the same rows")
-    if not slots.is_cuda or slots.dtype != torch.int64 or slots.numel() != rows or not slots.is_contiguous():
+    if slots.get_device() != index or slots.dtype != torch.int64 or slots.numel() != rows or not slots.is_contiguous():
         raise ValueError("slots must be a contiguous int64 CUDA tensor of one value a row")
-    pos = _ints("positions", positions, rows)
+    pos = _ints("positions", positions, index, rows)
     for g in (q_gamma, k_gamma):
-        if g is not None and (not g.is_cuda or g.dtype != f32 or g.numel() != dim or not g.is_contiguous()):
+        if g is not None and (g.get_device() != index or g.dtype != f32 or g.numel() != dim or not g.is_contiguous()):
             raise ValueError("a gamma must be a contiguous fp32 CUDA tensor of dim values")
     tp, limit, rot = None, 0, 0
     if table is not None:
-        if not table.is_cuda or table.dtype != f32 or table.dim() != 2 or not table.is_contiguous():
+        if table.get_device() != index or table.dtype != f32 or table.dim() != 2 or not table.is_contiguous():
             raise ValueError("table must be a contiguous fp32 CUDA tensor [positions, rotary_dim]")
         tp, (limit, rot) = table.data_ptr(), table.shape
     if out is None:
@@ -663,7 +668,7 @@ def rope_append(q, k, v, cache: KVCache, positions, slots, table=None, q_heads: 
     else:
         if out.shape[0] != rows:
             raise ValueError("out must have q's rows")
-        op, ldo = _rows2("out", out, torch.bfloat16, max(n, 1))
+        op, ldo = _rows2("out", out, torch.bfloat16, max(n, 1), index)
     if rows == 0:
         return out
     st = lib().q8_rope_append(qp, ldq, kp, ldk, vp, ldv, None if q_gamma is None else q_gamma.data_ptr(),
@@ -688,26 +693,26 @@ def attn_workspace(device="cuda"):
 
 def _attn(q, cache, R, table, lens, q_heads, scale, out, workspace, stream):
     import torch
-    shape = q.shape
+    shape, index = q.shape, cache._index
     if q_heads is None:
-        q_heads = shape[1] // cache.dim
+        q_heads = shape[-1] // cache.dim
     n = q_heads * cache.dim
-    qp, ldq = _rows2("q", q, torch.bfloat16, max(n, 1))
-    tp, width, pitch = _table_of(table, R)
+    qp, ldq = _rows2("q", q, torch.bfloat16, max(n, 1), index)
+    tp, width, pitch = _table_of(table, R, index)
     if out is None:
         out = _new((shape[0], n), torch.bfloat16, q.device, stream)
         op, ldo = out.data_ptr(), n
     else:
         if out.shape[0] != shape[0]:
             raise ValueError("out must have q's rows")
-        op, ldo = _rows2("out", out, torch.bfloat16, max(n, 1))
+        op, ldo = _rows2("out", out, torch.bfloat16, max(n, 1), index)
     if workspace is None:
         workspace = _new((int(lib().q8_attn_workspace_bytes()),), torch.uint8, q.device, stream, zeroed=True,
                          returned=False)  # of this call alone: its stream's again when the call returns
-    elif not workspace.is_cuda or not workspace.is_contiguous() or \
+    elif workspace.get_device() != index or not workspace.is_contiguous() or \
             workspace.nbytes < (_workspace_bytes or lib().q8_attn_workspace_bytes()):
         raise ValueError("workspace must come from attn_workspace")
-    return (qp, ldq, cache._ref, tp, width, pitch, _ints("lens", lens, R), op, ldo, q_heads,
+    return (qp, ldq, cache._ref, tp, width, pitch, _ints("lens", lens, index, R), op, ldo, q_heads,
             cache.dim ** -0.5 if scale is None else scale, out, workspace)
 
 
@@ -740,7 +745,7 @@ def attn_prefill(q, cache: KVCache, table, lens, row_start, q_heads: int | None 
         _attn(q, cache, R, table, lens, q_heads, scale, out, workspace, stream)
     if rows == 0:
         return out
-    st = lib().q8_attn_prefill(qp, ldq, kv, tp, width, pitch, lp, _ints("row_start", row_start, R + 1), op, ldo, rows,
+    st = lib().q8_attn_prefill(qp, ldq, kv, tp, width, pitch, lp, _ints("row_start", row_start, cache._index, R + 1), op, ldo, rows,
                                R, q_heads, scale, window, sinks, workspace.data_ptr(),
                                _stream_of(stream, cache.device))
     if st:

@@ -170,3 +170,48 @@ def test_binding_refuses_cpu_tensors(lib):
     i = torch.zeros(2, dtype=torch.int32)
     with pytest.raises(ValueError):
         q8.kv_slots(i, i, torch.zeros((2, 2), dtype=torch.int32), i, 16, 2)
+
+
+def test_binding_refuses_tensors_of_another_device(lib):
+    """Every tensor of a call is held to the cache's device, or to that of ``cached``: by tensors that say where they are."""
+    torch = pytest.importorskip("torch")
+
+    class On(torch.Tensor):
+        where = 0
+
+        def get_device(self):
+            return self.where
+
+        is_cuda = True
+
+    class Elsewhere(On):
+        where = 1
+
+    def on(shape, dtype, cls=On):
+        return torch.zeros(shape, dtype=dtype).as_subclass(cls)
+
+    b16, f32, i32, i64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+    kv = (2, 2, 16, 64)
+    cache = q8.KVCache(on(kv, b16), on(kv, b16))
+    with pytest.raises(ValueError):
+        q8.KVCache(on(kv, b16), on(kv, b16, Elsewhere))
+    attn = dict(q=((3, 128), b16), table=((3, 2), i32), lens=((3,), i32), out=((3, 128), b16),
+                workspace=((lib.q8_attn_workspace_bytes(),), torch.uint8))
+    chunk = dict(attn, row_start=((4,), i32))
+    append = dict(q=((3, 128), f32), k=((3, 128), f32), v=((3, 128), f32), positions=((3,), i32), slots=((3,), i64),
+                  table=((9, 64), f32), q_gamma=((64,), f32), k_gamma=((64,), f32), out=((3, 128), b16))
+    slots = dict(cached=((3,), i32), fresh=((3,), i32), table=((3, 2), i32), free_pages=((5,), i32), head=((1,), i32))
+    calls = [(q8.attn_decode, attn, dict(cache=cache)), (q8.attn_prefill, chunk, dict(cache=cache)),
+             (q8.rope_append, append, dict(cache=cache)), (q8.kv_slots, slots, dict(page_size=16, rows=3))]
+    for call, tensors, rest in calls:
+        for name in tensors:
+            args = {n: on(*a, Elsewhere if n == name else On) for n, a in tensors.items()}
+            with pytest.raises(ValueError, match="device|attn_workspace|contiguous"):
+                call(**args, **rest)
+    for name in ("lens", "row_start", "positions", "slots", "head"):
+        table = on((3, 2), i32)
+        out = dict(table=table, lens=on(3, i32), row_start=on(4, i32), positions=on(3, i32), slots=on(3, i64),
+                   head=on(1, i32))
+        out[name] = out[name].as_subclass(Elsewhere)
+        with pytest.raises(ValueError):
+            q8.kv_slots(on(3, i32), on(3, i32), table, on(5, i32), 16, 3, out=out)
