@@ -716,6 +716,11 @@ def _attn(q, cache, R, table, lens, q_heads, scale, out, workspace, stream):
             cache.dim ** -0.5 if scale is None else scale, out, workspace)
 
 
+def _int32(n):
+    """A window's or sinks' length as the library's 32-bit int: past 2^31 they reach any position all the same."""
+    return max(-1, min(n, 0x7FFFFFFF))
+
+
 def attn_decode(q, cache: KVCache, table, lens, q_heads: int | None = None, scale: float | None = None,
                 window: int = 0, sinks: int = 0, out=None, workspace=None, stream=None):
     """Attention of one new token a request over its pages (q8_attn_decode): q bf16 [R, >= q_heads * dim], block table
@@ -728,8 +733,8 @@ def attn_decode(q, cache: KVCache, table, lens, q_heads: int | None = None, scal
         _attn(q, cache, R, table, lens, q_heads, scale, out, workspace, stream)
     if R == 0:
         return out
-    st = lib().q8_attn_decode(qp, ldq, kv, tp, width, pitch, lp, op, ldo, R, q_heads, scale, window, sinks,
-                              workspace.data_ptr(), _stream_of(stream, cache.device))
+    st = lib().q8_attn_decode(qp, ldq, kv, tp, width, pitch, lp, op, ldo, R, q_heads, scale, _int32(window),
+                              _int32(sinks), workspace.data_ptr(), _stream_of(stream, cache.device))
     if st:
         raise Q8Error(st, "q8_attn_decode")
     return out
@@ -746,7 +751,7 @@ def attn_prefill(q, cache: KVCache, table, lens, row_start, q_heads: int | None 
     if rows == 0:
         return out
     st = lib().q8_attn_prefill(qp, ldq, kv, tp, width, pitch, lp, _ints("row_start", row_start, cache._index, R + 1), op, ldo, rows,
-                               R, q_heads, scale, window, sinks, workspace.data_ptr(),
+                               R, q_heads, scale, _int32(window), _int32(sinks), workspace.data_ptr(),
                                _stream_of(stream, cache.device))
     if st:
         raise Q8Error(st, "q8_attn_prefill")

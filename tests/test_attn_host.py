@@ -215,3 +215,10 @@ def test_binding_refuses_tensors_of_another_device(lib):
         out[name] = out[name].as_subclass(Elsewhere)
         with pytest.raises(ValueError):
             q8.kv_slots(on(3, i32), on(3, i32), table, on(5, i32), 16, 3, out=out)
+
+
+def test_binding_keeps_long_windows_long(lib):
+    """Windows and sinks beyond 32 bits reach the library as the longest it takes, not as their low 32 bits."""
+    assert [q8._int32(n) for n in (0, 1, 2 ** 31 - 1, 2 ** 31, 2 ** 32, 2 ** 32 + 5, 10 ** 30)] == \
+        [0, 1] + [2 ** 31 - 1] * 5
+    assert q8._int32(-1) == -1 and q8._int32(-2 ** 32) == -1  # refused there

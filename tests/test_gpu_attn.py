@@ -897,3 +897,17 @@ def test_one_row_of_any_width(dev, work, extra):
     out = wide(torch.bfloat16)
     q8.rope_append(*x, q8.KVCache.empty(1, 2, 16, dim), at, at.long(), q_heads=heads, out=out)
     assert torch.equal(out[:, :heads * dim], x[0][:, :heads * dim].bfloat16()) and torch.all(out[:, heads * dim:] == 7.0)
+
+
+def test_windows_beyond_32_bits(dev, work):
+    import q8_block_quantized_gemv_gb300 as q8
+    p = Paged(dev, [90], 2, 64, 16, "bf16", 171)
+    q, qn = queries(dev, 30, 4, 64, 172)
+    starts = dev.tensor([0, 30], dtype=dev.int32, device="cuda")
+    for window, sinks, like in ((2 ** 32 + 5, 0, (0, 0)), (2 ** 40, 3, (0, 0)), (7, 2 ** 33, (0, 0)), (7, 2 ** 31 + 1, (0, 0))):
+        o, tol = expected(p, qn, [0, 30], 64 ** -0.5, *like)
+        agree(q8.attn_prefill(q, p.cache, p.table_dev, p.lens_dev, starts, window=window, sinks=sinks, workspace=work), o, tol)
+        got = q8.attn_decode(q[-1:], p.cache, p.table_dev, p.lens_dev, window=window, sinks=sinks, workspace=work)
+        agree(got, o[-1:], tol[-1:])
+    with pytest.raises(q8.Q8Error):
+        q8.attn_decode(q[-1:], p.cache, p.table_dev, p.lens_dev, window=-2 ** 32, workspace=work)
