@@ -62,6 +62,9 @@ class Server:
     """The cache, block table and workspaces of ``requests`` conversations over one model."""
 
     def __init__(self, model, requests, pages, page_size=64, cache="bf16", window=0, sinks=0):
+        if not 1 <= requests <= CHUNK:
+            raise ValueError(f"1 to {CHUNK} requests: every step has a row of each")
+        self.lengths = [0] * requests  # as self.cached, on the host
         self.model, self.R, self.page_size, self.window, self.sinks = model, requests, page_size, window, sinks
         self.caches = [q8.KVCache.empty(pages, model.kv_heads, page_size, model.dim, cache) for _ in model.layers]
         self.table = torch.full((requests, pages), -1, dtype=torch.int32, device="cuda")
@@ -72,6 +75,16 @@ class Server:
         self.logits = torch.empty((requests, q8.padded_n(model.vocab)), device="cuda")
         self.workspace = q8.attn_workspace()
         self.graph = None
+
+    def make_room(self, counts):
+        """Count counts[r] more tokens for request r; refused where pages or the rotation table's positions run out (what
+        the kernels then do, tokens without a place and NaN, is for steps that cannot ask)."""
+        lengths = [n + more for n, more in zip(self.lengths, counts)]
+        if sum(-(-n // self.page_size) for n in lengths) > self.free.numel():
+            raise ValueError("not enough pages for that many tokens")
+        if max(lengths) > self.model.rope.shape[0]:
+            raise ValueError("more tokens than the rotation table has positions")
+        self.lengths = lengths
 
     def step(self, tokens, fresh, decode):
         """One step over tokens [rows], fresh[r] of them request r's next; leaves each request's next token in
@@ -102,6 +115,9 @@ class Server:
         """The prompts (lists of token ids), as many rows a step as fit; every request's last chunk comes in the last
         step, so that self.tokens and self.logits are those of all requests.  Returns the first new tokens."""
         left = [list(p) for p in prompts]
+        if len(left) != self.R or not all(left):
+            raise ValueError("a prompt of one token or more for each request")
+        self.make_room([len(p) for p in left])
         while any(left):
             room, take = CHUNK, []
             for i, p in enumerate(left):
@@ -117,6 +133,7 @@ class Server:
 
     def decode(self, count):
         """``count`` more greedy tokens of every request, [count, requests]; the step is captured once and replayed."""
+        self.make_room([count] * self.R)
         out = torch.empty((count, self.R), dtype=torch.int64, device="cuda")
         start = 0
         if self.graph is None and count:

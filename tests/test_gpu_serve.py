@@ -99,3 +99,31 @@ def test_the_command_runs(serve, monkeypatch, capsys):
     serve.main()
     out = capsys.readouterr().out
     assert "prefill: 189 tokens of 3 prompts" in out and "decode: 2 steps of 3 requests" in out
+
+
+def test_what_a_server_refuses(serve):
+    """More requests than a step has rows (their last rows would never come together), prompts without a token (whose last
+    row is another's), more tokens than pages or positions."""
+    m = serve.Model(layers=1, width=256, heads=2, kv_heads=1, dim=64, ffn=416, vocab=99, positions=40, seed=5)
+    for requests in (0, serve.CHUNK + 1):
+        with pytest.raises(ValueError):
+            serve.Server(m, requests, 8, 16)
+    server = serve.Server(m, 2, 4, 16)
+    for prompts in ([[1]], [[1], []], [[1], [2], [3]], [[1] * 41, [2]], [[1] * 33, [2] * 17]):
+        with pytest.raises(ValueError):
+            server.prefill(prompts)
+    first = server.prefill([[1] * 30, [2] * 3])
+    assert server.cached.tolist() == [30, 3] and first.numel() == 2
+    server.decode(10)
+    with pytest.raises(ValueError):  # the 41st position
+        server.decode(1)
+    assert server.cached.tolist() == [40, 13] and torch.isfinite(server.logits[:, :99]).all()
+
+
+def test_as_many_requests_as_a_step_has_rows(serve):
+    m = serve.Model(layers=1, width=256, heads=2, kv_heads=1, dim=64, ffn=416, vocab=99, positions=40, seed=5)
+    server = serve.Server(m, serve.CHUNK, 2 * serve.CHUNK, 16)
+    prompts = [[r % 99] * (1 + r % 3) for r in range(serve.CHUNK)]
+    server.prefill(prompts)
+    server.decode(2)
+    assert server.cached.tolist() == [len(p) + 2 for p in prompts]
