@@ -129,7 +129,7 @@ struct AppendArgs {
 };
 
 constexpr int kAppendWarps = 4;
-constexpr long long kAppendWide = 3ll << 19;  // values
+constexpr long long kAppendWide = 3ll << 19;  // values (launch_append_type)
 
 __device__ __forceinline__ uint2 pack_bf16x4(float4 v) {
     const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
@@ -321,13 +321,16 @@ template <int D, bool I, bool Q8> cudaError_t launch_append_type(const AppendArg
         const long long per = (256 / D) * n, warps = a.rows * ((total + per - 1) / per);
         return dim3((unsigned)((warps + kAppendWarps - 1) / kAppendWarps), 1, 1);
     };
-    // One head a lane group while the rows are few (latency: all of it in flight at once anyway), four once there are
-    // enough to fill the SMs several times.  One against four, heads of 128: 16 rows of 32 + 2 x 32 heads 1.9 and 2.4 us,
-    // 64 rows 2.3 and 2.5, 128 rows (3 2^19 values) 2.8 and 2.7, 256 rows 4.9 and 3.6; 8191 rows of 32 + 2 x 8 heads with
-    // norms 74 and 55.
-    if ((long long)a.rows * total * D < kAppendWide)
-        return kv_launch(append_kernel<D, I, Q8, 1>, grid(1), 32 * kAppendWarps, 0, stream, a);
-    return kv_launch(append_kernel<D, I, Q8, 4>, grid(4), 32 * kAppendWarps, 0, stream, a);
+    // One head a lane group while the rows are few (latency: all of it in flight at once anyway), over a bf16 cache four once
+    // there are enough to fill the SMs several times.  One against four, 32 + 2 x 8 heads, halves, without and with norms:
+    // heads of 128, 16 rows 1.9 and 2.3 us (2.0 and 2.9), 256 rows (3 2^19 values) 2.8 and 2.7 (3.2 and 3.4), 512 rows 5.2
+    // and 4.2 (5.8 and 5.1), 8191 rows 69 and 51 (74 and 56); heads of 64, 512 rows (as many values) 2.8 and 2.8 (3.3 and
+    // 3.4), 1024 rows 5.2 and 4.1 (6.0 and 5.2).  Over a Q8_0 cache, whose scales take more instructions than the loads wait
+    // for, four are slower everywhere: 16 rows of heads of 128 2.6 and 5.5, 512 rows 6.8 and 7.6, 8191 rows 79 and 88.
+    if (!Q8)
+        if ((long long)a.rows * total * D >= kAppendWide)
+            return kv_launch(append_kernel<D, I, false, 4>, grid(4), 32 * kAppendWarps, 0, stream, a);
+    return kv_launch(append_kernel<D, I, Q8, 1>, grid(1), 32 * kAppendWarps, 0, stream, a);
 }
 
 template <int D> cudaError_t launch_append(const AppendArgs &a, bool interleaved, bool q8, cudaStream_t stream) {
