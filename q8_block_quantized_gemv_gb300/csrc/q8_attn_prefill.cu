@@ -385,14 +385,16 @@ __device__ __forceinline__ void hide_scores_here(uint32_t ts, int c_hi, int c_lo
     tm_wait_st();
 }
 
-// As a function of its own it leaves the softmax's loop to the tiles without any: a prompt of 8192 rows with heads of
-// 128 takes 347 us, 351 with it inline; heads of 64 and a window, where every third tile has some, 67 us and 63 inline.
+// Over a bf16 cache, where the softmax's loop is what the tensor cores wait for, as a function of its own, which leaves the
+// loop to the tiles without any; over a Q8_0 cache inline.  Own and inline, 4,096 rows, 32 heads over 8, without and with a
+// window of 1,024: bf16, heads of 128 117 and 120 us (window 87 and 88), heads of 64 91 and 95 (70 and 69); Q8_0, heads of
+// 128 195 and 194 (137 and 136), heads of 64 140 and 139 (102 and 100).
 __device__ __noinline__ void hide_scores_call(uint32_t ts, int c_hi, int c_lo, int c_sink, unsigned groups) {
     hide_scores_here(ts, c_hi, c_lo, c_sink, groups);
 }
-template <int D>
+template <bool Q8>
 __device__ __forceinline__ void hide_scores(uint32_t ts, int c_hi, int c_lo, int c_sink, unsigned groups) {
-    if (D == 64) hide_scores_here(ts, c_hi, c_lo, c_sink, groups);
+    if (Q8) hide_scores_here(ts, c_hi, c_lo, c_sink, groups);
     else hide_scores_call(ts, c_hi, c_lo, c_sink, groups);
 }
 // A row's largest score, and n columns of a row times f: the rare part of a softmax step, out of its loop too.
@@ -1217,7 +1219,7 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
                     if (info.y >> (8 + x) & 1) {
                         // columns [c_lo, c_hi] and [0, c_sink) are visible
                         const int j0 = info.x + it.jump;
-                        hide_scores<D>(ts, min(p, it.end - 1) - j0, a.window ? max(max(p, 0) - (a.window - 1), j0) - j0 : 0,
+                        hide_scores<Q8>(ts, min(p, it.end - 1) - j0, a.window ? max(max(p, 0) - (a.window - 1), j0) - j0 : 0,
                                        a.window ? a.sinks - info.x : 0, info.y);
                     }
                     // The weights are taken against the running maximum as it stands: a row's maximum is only looked
