@@ -402,9 +402,16 @@ int64_t q8_attn_workspace_bytes(void);
  *   out[r] = sum_j w_j v_j,   w = softmax over the visible j of scale * (q[r] . k_j)
  * where request r's token has position p = lens[r] - 1 and key j < lens[r] is visible when
  *   window == 0, or p - j < window, or j < sinks
- * and its page is in the table.  A row that sees nothing (lens[r] <= 0) gets zeros.  Scores, softmax statistics and
- * sums are fp32; the result is rounded once to bf16.  What is not visible is not read into the result, whatever its
- * bits.
+ * and its page is in the table.  A row that sees nothing (lens[r] <= 0) gets zeros.  What is not visible is not read
+ * into the result, whatever its bits.  Scores, softmax statistics and sums are fp32.  On the way to them, and from them:
+ *   - the weights w_j are rounded before they multiply v: over a bf16 cache to bf16 (each off by 2^-8 of itself at most);
+ *     over a Q8_0 cache to fp16, decode w_j times v's scale (2^-11 of itself down to 2^-22 of the head's largest such
+ *     product in the block of 32 values, 2^-33 of that below), prefill w_j (2^-11 of itself down to 2^-14 of the row's
+ *     largest, 2^-25 of that below);
+ *   - prefill over a Q8_0 cache takes code * scale in fp16 (two roundings of 2^-11 down to 2^-21 of the largest scale at
+ *     hand; blocks of the result that smaller ones could show in are computed from fp32);
+ *   - the result is rounded to bf16.
+ * In all some 2e-3 of the result in its 2-norm, most of it that last rounding.
  *   q, out  device, bf16 [R][ldq], [R][ldo]: heads at column head * dim; q_heads a multiple of cache->heads
  *   block_table  device, int32 [R][table_width], rows table_pitch apart      lens  device, int32 [R]
  *   window >= 0, sinks >= 0 (ignored when window is 0); scale finite

@@ -1,9 +1,10 @@
 // q8_attn_decode: attention of one new token a request over the paged cache, split over the cache's length and joined.
 //
-// Every visible key and value is read once for all query heads of its cache head, 4 flops a byte and head: HBM bounds
-// the kernel until contexts are so short that latency does.  So the work is cut by bytes, not by requests: the visible
-// tokens of all (request, cache head) items in a row are a list of 16-token units, and each CTA (one per SM) takes an
-// equal contiguous span of it, computed on the device from lens.  Its 8 warps (12 over a Q8_0 cache, up to 8 heads to a
+// Every visible key and value is read once for up to 16 query heads of its cache head (once more for each further 16), 4
+// flops a byte and head: HBM bounds the kernel until contexts are so short that latency does.  So the work is cut by bytes,
+// not by requests: the visible tokens of all items in a row -- an item is a request's cache head with 8 or 16 of its query
+// heads -- are a list of 16-token units, and each CTA (one per SM) takes an equal contiguous span of it, computed on the
+// device from lens.  Its 8 warps (12 over a Q8_0 cache, up to 8 heads to a
 // cache head) take the span's units in turn, each with a ring of its own in shared memory filled by cp.async (prefetch
 // runs on across items; no CTA barrier but at an item's end), a running maximum and sum, and accumulators in registers.
 //
@@ -246,7 +247,9 @@ __global__ void __launch_bounds__(32 * Cfg<D, Q8, NT>::kWarps, 1) attn_decode_ke
     Cursor c;                // the item being computed
     // ---- few short items: one a CTA, nothing to join ----
     // Splitting an item costs its CTAs a round through memory to hand their parts over, some 3 us; 64 units are 8 a
-    // warp.  (32 heads of one request of 203 tokens: 11.5 us split, 5.2 us whole.)
+    // warp.  (One request of 203 tokens, 32 heads of 128: 11.5 us split, 5.2 us whole.  32 heads over 8, one request of 1,008
+    // tokens 10.6 and 8.5, 1,500 tokens 10.9 and 10.7, 2,048 tokens 8.3 and 12.9; 16 requests of 1,008 tokens 14.0 and 9.1, of
+    // 2,048 26.1 and 22.6; Q8_0, one of 1,008 14.6 and 11.8, of 2,048 10.7 and 16.9; heads of 64 are alike.)
     bool whole_items = (long long)a.R * tiles <= gridDim.x;
     if (whole_items)  // at most a request a thread: a.R <= gridDim.x < the block
         whole_items = !__syncthreads_or(tid < a.R && seen_of(a, a.lens[tid]).n > kWholeUnits);

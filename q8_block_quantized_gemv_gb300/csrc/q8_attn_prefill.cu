@@ -9,7 +9,9 @@
 //     P = 2^(S scale log2(e) - m), rounded to 16 bits, written over S in tensor memory
 //     O += P V (P read from tensor memory, V from shared memory, fp32 O in tensor memory)
 // with a running m that only moves when weights against it grow past what their type and the sums take (2^15 in fp16,
-// 2^60 in bf16; then the row's O is rescaled in place).
+// 2^60 in bf16; then the row's O is rescaled in place).  The weights multiply V with 16 bits, as that product wants them: bf16's
+// 8 significant ones over a bf16 cache, whose range they share; over a Q8_0 cache fp16's 11 down to 2^-14 of the row's
+// largest and fewer below.  Their sum is fp32.
 //
 // Warps: 0-3 and 4-7 the softmax of tiles A and B, one row a thread; 8 issues the MMAs; 9 requests keys and values;
 // the rest load Q and prepare values:
@@ -31,10 +33,10 @@
 //
 // Every wait is bounded (about two seconds); one that runs out records a fault, and the CTA drains and returns.
 //
-// Measured, 32 heads of 128 over 8 cache heads: a prompt of 8,192 rows 353 us over a bf16 cache = 1.56 PFLOP/s (80% of a
+// Measured, 32 heads of 128 over 8 cache heads: a prompt of 8,192 rows 352 us over a bf16 cache = 1.56 PFLOP/s (80% of a
 // large bf16 product's rate: the MMAs wait for the softmax some of the time, 66% of the tensor pipe's cycles are taken),
 // 570 us over a Q8_0 cache, where a tile goes through five hands (codes, conversion, S, softmax, O) and nothing is full:
-// 27% of the tensor pipe's cycles and 38% of the issue slots in a chunk of 509 rows, which takes 67 us (1.5 us more with
+// 27% of the tensor pipe's cycles and 38% of the issue slots in a chunk of 509 rows, which takes 68 us (1.5 us more with
 // four conversion warps; as long with the conversion finished in registers before its operand's place is free, or with
 // the values' place given back before the keys').
 // 512 rows after 4,096 tokens, 32 cache heads: 51 us.  A call's fixed part is 11 us: the cut of the list 2, the first Q
@@ -76,9 +78,12 @@ template <int D, bool Q8> struct Cfg {
     static constexpr int kHelpers = Q8 ? 6 : 2;            // warps
     static constexpr int kThreads = 32 * (kHelpWarp + kHelpers);
     // What an item costs beside its tiles, in tiles: loading Q, the pipe's fill and drain, the epilogue.  Without it the
-    // CTAs of a long prompt's first rows, 44 short items each, took 835,000 clocks where the others took 740,000.  2, 3, 4
-    // and 6 take 368, 348, 347 and 358 us for a prompt of 8192 rows, 51.6, 50.3, 51.3 and 50.3 for a chunk of 512, 63.0,
-    // 62.0, 63.2 and 63.9 under a window (before its sinks and keys were one list); over a Q8_0 cache 2, 3 and 4 take 640, 582 and 570 us for the prompt.
+    // CTAs of a long prompt's first rows, 44 short items each, took 835,000 clocks where the others took 740,000.  2, 3, 4, 5
+    // and 6, heads of 128, 32 over 8: a prompt of 4,096 rows takes 121, 116, 116, 119 and 119 us, under a window of 1,024 87
+    // each, 512 rows of 9 requests 44, 41, 41, 41 and 41; over a Q8_0 cache 220, 204, 193, 195 and 196, 138, 136, 136, 139 and
+    // 139, 61, 56, 56, 58 and 58.  Heads of 64 are alike.  Prompts of full heads, 32 over 32, would have more (bf16 145, 134,
+    // 129, 128 and 130; Q8_0 260, 246, 232, 216 and 214), their 512 rows of 9 requests less (70, 71, 72, 73 and 75; 105, 97, 98,
+    // 98 and 99).
     static constexpr int kItemCost = Q8 ? 4 : 3;
     static constexpr int kRing = 2 * kOp;                  // after Q's two tiles
     static constexpr int kRawAt = kRing + kSlots * kOp;
