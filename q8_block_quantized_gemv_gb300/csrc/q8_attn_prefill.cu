@@ -9,7 +9,7 @@
 //     P = 2^(S scale log2(e) - m), rounded to 16 bits, written over S in tensor memory
 //     O += P V (P read from tensor memory, V from shared memory, fp32 O in tensor memory)
 // with a running m that only moves when weights against it grow past what their type and the sums take (2^15 in fp16,
-// 2^60 in bf16; then the row's O is rescaled in place).  The weights multiply V with 16 bits, as that product wants them: bf16's
+// 2^32 in bf16; then the row's O is rescaled in place).  The weights multiply V with 16 bits, as that product wants them: bf16's
 // 8 significant ones over a bf16 cache, whose range they share; over a Q8_0 cache fp16's 11 down to 2^-14 of the row's
 // largest and fewer below.  Their sum is fp32.
 //
@@ -1180,9 +1180,9 @@ __global__ void __launch_bounds__(Cfg<D, Q8>::kThreads, 1)
         const bool whole_row = y < pa.tile_tokens * a.group;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         const uint32_t to = tmem + lanes + C::kColO + x * D;
-        // The largest sum of a row's 128 weights: below fp16's largest value, and for bf16 weights, which have fp32's
-        // range, far below where a row's sums could overflow.
-        constexpr float kMostSum = Q8 ? 32768.0f : 1.15292150e18f;  // 2^15, 2^60
+        // The largest sum of a row's 128 weights: below fp16's largest value; for bf16 weights, which have fp32's range,
+        // such that sums over values of up to 2^90 do not overflow on the way to a result that does not.
+        constexpr float kMostSum = Q8 ? 32768.0f : 4294967296.0f;  // 2^15, 2^32
         constexpr float kLeast = 1.17549435e-38f;  // a factor of 0 would make NaN of a hidden score's -inf
         const float sc0 = fmaxf(fabsf(a.scale) * kLog2e, kLeast);
         unsigned cnt = 0, ends = 0, shared = 0, seg = 0;  // ends: the phases of o_full (bit 0) and idle (bit 1)

@@ -911,3 +911,27 @@ def test_windows_beyond_32_bits(dev, work):
         agree(got, o[-1:], tol[-1:])
     with pytest.raises(q8.Q8Error):
         q8.attn_decode(q[-1:], p.cache, p.table_dev, p.lens_dev, window=-2 ** 32, workspace=work)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_prefill_large_values_and_rising_scores(dev, work, dim):
+    """Values of 2^88 and weights that rise by 18 powers of two with every 128 keys: the sums stay finite, as the result is."""
+    import q8_block_quantized_gemv_gb300 as q8
+    torch, n, rows, heads, page = dev, 2000, 200, 4, 32
+    p = Paged(torch, [n], 2, dim, page, "bf16", 181)
+    q, _ = queries(torch, rows, heads, dim, 182)
+    q.view(rows, heads, dim)[..., 0] = 1.0
+    qn = q.float().cpu().numpy().astype(np.float64).reshape(rows, heads, dim)
+    scale = dim ** -0.5
+    pages = p.table_dev[0].long()[torch.arange(n, device="cuda") // page]
+    off = torch.arange(n, device="cuda") % page
+    rise = (torch.arange(n, device="cuda") / 128 * 18 * np.log(2) / scale).bfloat16()
+    p.cache.k[pages, :, off, 0] = rise[:, None]
+    p.cache.v[pages, :, off] *= 2.0 ** 88
+    p.k[0][:, :, 0] = rise.double().cpu().numpy()[:, None]
+    p.v[0] = p.v[0] * 2.0 ** 88
+    o, tol = expected(p, qn, [0, rows], scale, 0, 0)
+    starts = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    agree(q8.attn_prefill(q, p.cache, p.table_dev, p.lens_dev, starts, scale=scale, workspace=work), o, tol)
+    got = q8.attn_decode(q[-1:], p.cache, p.table_dev, p.lens_dev, scale=scale, workspace=work)
+    agree(got, o[-1:], tol[-1:])
