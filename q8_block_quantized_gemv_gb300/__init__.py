@@ -604,6 +604,11 @@ def rope_table(positions: int, rotary_dim: int, base: float = 10000.0, scaling=N
     import torch
     if rotary_dim % 2 or rotary_dim < 2 or positions < 1:
         raise ValueError("rotary_dim must be even and positive, positions at least 1")
+    numbers = [float(x) for x in (base, *(scaling[1:] if scaling else ()))]
+    if not all(np.isfinite(x) and x > 0 for x in numbers):
+        raise ValueError("base and the numbers of scaling must be finite and positive")
+    if scaling and not {"linear": 2, "ntk": 2, "parts": 3}.get(scaling[0], 0) <= len(scaling):
+        raise ValueError(f"scaling {scaling[0]!r} needs more numbers")
     i = np.arange(rotary_dim // 2, dtype=np.float64)
     amplitude = 1.0
     kind = scaling[0] if scaling else None

@@ -222,3 +222,14 @@ def test_binding_keeps_long_windows_long(lib):
     assert [q8._int32(n) for n in (0, 1, 2 ** 31 - 1, 2 ** 31, 2 ** 32, 2 ** 32 + 5, 10 ** 30)] == \
         [0, 1] + [2 ** 31 - 1] * 5
     assert q8._int32(-1) == -1 and q8._int32(-2 ** 32) == -1  # refused there
+
+
+@pytest.mark.parametrize("base,scaling", [
+    (0.0, None), (-1.0, None), (float("nan"), None), (1e4, ("linear", 0.0)), (1e4, ("linear", -2.0)), (1e4, ("linear",)),
+    (1e4, ("ntk", float("inf"))), (1e4, ("parts", 4.0)), (1e4, ("parts", 4.0, 0.0)), (1e4, ("parts", 4.0, 2048.0, 0.0, 1.0)),
+    (1e4, ("parts", 4.0, 2048.0, 32.0, float("nan"))), (1e4, ("other", 2.0))])
+def test_rope_table_refusals(base, scaling):
+    """What would fill the table with NaN, or is not there."""
+    pytest.importorskip("torch")
+    with pytest.raises(ValueError):
+        q8.rope_table(10, 8, base, scaling, device="cpu")
