@@ -17,9 +17,9 @@
 // order, so the result does not depend on who was last.
 //
 // Measured, heads of 128, 32 over 8 cache heads: one request of 131,072 tokens, bf16, 84 us = 6.4 TB/s (95% of a copy's
-// rate); 15 requests with 81,000 tokens in all, Q8_0, 43 us = 4.4 TB/s.  There a unit costs about 580 instructions (the
-// codes' way to fp16, the scales), 145 for each of the SM's schedulers, and 200 clocks of the SM's share of the memory, and
-// neither is full: 54% of the issue slots, 65% of the bandwidth.  8 warps take 44 us, 16 with their 128 registers 56.
+// rate); 15 requests with 81,000 tokens in all, Q8_0, 43 us = 4.4 TB/s.  There a unit costs about 550 instructions (the
+// codes' way to fp16, the scales), 137 for each of the SM's schedulers, and 200 clocks of the SM's share of the memory, and
+// neither is full: 51% of the issue slots, 64% of the bandwidth.  8 warps take 44 us, 16 with their 128 registers 56.
 // Heads of 64, 24 over 8, a window of 4,096 in 64 requests: 89 us = 6.0 TB/s.  One request of 203 tokens, 32 heads: 5.2
 // us, the chain from its length over table, keys and sums to the output.
 #include <cuda_bf16.h>

@@ -33,9 +33,9 @@
 //
 // Every wait is bounded (about two seconds); one that runs out records a fault, and the CTA drains and returns.
 //
-// Measured, 32 heads of 128 over 8 cache heads: a prompt of 8,192 rows 352 us over a bf16 cache = 1.56 PFLOP/s (80% of a
-// large bf16 product's rate: the MMAs wait for the softmax some of the time, 66% of the tensor pipe's cycles are taken),
-// 570 us over a Q8_0 cache, where a tile goes through five hands (codes, conversion, S, softmax, O) and nothing is full:
+// Measured, 32 heads of 128 over 8 cache heads: a prompt of 8,192 rows 351 us over a bf16 cache = 1.56 PFLOP/s (80% of a
+// large bf16 product's rate: the MMAs wait for the softmax some of the time, 68% of the tensor pipe's cycles are taken),
+// 581 us over a Q8_0 cache, where a tile goes through five hands (codes, conversion, S, softmax, O) and nothing is full:
 // 27% of the tensor pipe's cycles and 38% of the issue slots in a chunk of 509 rows, which takes 68 us (1.5 us more with
 // four conversion warps; as long with the conversion finished in registers before its operand's place is free, or with
 // the values' place given back before the keys').
