@@ -433,6 +433,123 @@ q8_status q8_attn_prefill(const void *q, int ldq, const q8_kv_cache *cache, cons
                           int table_pitch, const int *lens, const int *row_start, void *out, int ldo, int rows, int R,
                           int q_heads, float scale, int window, int sinks, void *workspace, q8_stream_t stream);
 
+/* ---------------------------------------------------------------------------------------------------------------
+ * Weights of 4 bits with group scales, and the choice of the next token: the products of a decode or prefill step over
+ * half the bytes of Q8_0, and what follows the last of them.  No counterpart on the pages.
+ * ------------------------------------------------------------------------------------------------------------- */
+
+/* A 4-bit weight: codes c in 0..15, and for each group of `group` consecutive rows of a column a 16-bit scale s and a
+ * zero point z:
+ *     W[k, n] = s[k / group, n] * (c[k, n] - z[k / group, n])
+ *   group  32, 64 or 128; K a multiple of it
+ *   flags  Q8_W4_ZEROS: the zero points are given (without it z = 8 everywhere); Q8_W4_BF16: the scales are bf16 (without
+ *          it fp16)
+ * As a checkpoint has it ("plain"):
+ *   codes   uint8 [K/2][N]: row 2i of column n in the low four bits of codes[i][n], row 2i + 1 in the high ones
+ *   scales  fp16 or bf16 [K/group][N]        zeros  uint8 [K/group][N], 0..127
+ * As the products read it ("tiled", q8_w4_tile): strips of 32 columns, of a strip one unit for each group in the order of
+ * K, unit (strip, g) at (strip * (K/group) + g) * U bytes, U = 16 * group + 64 (+ 32 with Q8_W4_ZEROS):
+ *   codes   words of 8 rows of one column, rows 8t + 2p and 8t + 2p + 1 of a 32-row block in bits 4p .. 4p + 3 and
+ *           16 + 4p .. 16 + 4p + 3 (p = 0..3).  With column 16j + 8h + i of the strip (j, h = 0, 1; i = 0..7) and block b of
+ *           the group, the word is number 2 (b % 2) + h of the 16 bytes at 512 (2 (b / 2) + j) + 16 (4i + t), or with
+ *           group 32 number h of the 8 bytes at 256 j + 8 (4i + t)
+ *   scales  32 of 16 bits, in column order        zeros  32 bytes, in column order (Q8_W4_ZEROS)
+ * Columns at or past N of the last strip hold code 0, scale 0 and zero point 0.
+ * q8_w4_bytes(K, N, group, flags): the tiled form's bytes; -1 for sizes or flags that are not a weight's. */
+typedef struct {
+    const void *w; /* device, tiled, 16-byte aligned */
+    int N, group;
+    unsigned int flags;
+} q8_weight4;
+
+#define Q8_W4_ZEROS 1u
+#define Q8_W4_BF16 2u
+
+int64_t q8_w4_bytes(int K, int N, int group, unsigned int flags);
+
+/* Plain -> tiled, on the host, and on the device enqueued on `stream` (w 16-byte aligned there, scales 2-byte; w may not
+ * overlap an input).  zeros is NULL exactly when flags has no Q8_W4_ZEROS.  The low seven bits of a zero point count.
+ * Errors: Q8_ERR_ARG (NULL pointers, zeros against flags, unknown flags, overlaps), Q8_ERR_SHAPE, Q8_ERR_ALIGN. */
+q8_status q8_w4_tile(const uint8_t *codes, const void *scales, const uint8_t *zeros, int K, int N, int group,
+                     unsigned int flags, void *w);
+q8_status q8_w4_tile_device(const uint8_t *codes, const void *scales, const uint8_t *zeros, int K, int N, int group,
+                            unsigned int flags, void *w, q8_stream_t stream);
+
+/* Host repack of GGML-style Q4_0 checkpoint blocks into the plain form (group 32, z = 8, fp16 scales): N * (K/32) blocks of
+ * 18 bytes, column-major by block as q8_repack_f16's, each a little-endian binary16 scale and 16 bytes, byte i holding row
+ * i of the block in its low and row 16 + i in its high four bits.  Q8_ERR_NOT_Q8_0 for a scale that is not finite. */
+q8_status q8_w4_repack(const void *blocks, int K, int N, uint8_t *codes, uint16_t *scales);
+
+/* y_p = x . W_p for every part p, 1 <= nparts <= Q8_MAX_PARTS; all parts have the same K, group and flags.
+ *   x  device, bf16 [m][K], 16-byte aligned, 1 <= m <= Q8_MAX_CHUNK        y  host array of device pointers, fp32
+ *   [m][q8_padded_n(N_p)] (written, 0 in the pad columns), 16-byte aligned, none overlapping an input or another y
+ *   flags  Q8_FLAG_CONSTANT_WEIGHTS or 0
+ * Codes less zero points and activations enter the tensor cores exactly (bf16); a group's sums are fp32, scaled in fp32
+ * and added in fp32 in an order fixed for (m, K, N, group) and the device: each output is within
+ * 1e-5 * sum |x s (c - z)| of the real number, and repeated calls give identical bits.
+ * Up to 16 rows run as streams of the weight, more on tcgen05 (one launch either way).
+ * Errors: Q8_ERR_ARG (NULL pointers, unknown flags, parts that differ in group or flags, overlaps), Q8_ERR_SHAPE (m, K, N,
+ * group, nparts), Q8_ERR_ALIGN, Q8_ERR_CUDA. */
+q8_status q8_gemv4_parts(const void *x, const q8_weight4 *weights, float *const *y, int nparts, int m, int K,
+                         unsigned int flags, q8_stream_t stream);
+
+/* The same for one weight. */
+q8_status q8_gemv4(const void *x, const q8_weight4 *weight, float *y, int m, int K, unsigned int flags,
+                   q8_stream_t stream);
+
+/* The gated pair: out = silu(x . Wg) * (x . Wu), silu(g) = g / (1 + exp(-g)), as q8_gemv_glu; gate and up have the same N,
+ * group and flags.  out fp32 [m][Np], out_bf16 bf16 [m][Np] (rounded to nearest even), either may be NULL; pads 0.  One
+ * launch.  Other arguments and errors as q8_gemv4_parts. */
+q8_status q8_gemv4_glu(const void *x, const q8_weight4 *gate, const q8_weight4 *up, float *out, void *out_bf16, int m,
+                       int K, unsigned int flags, q8_stream_t stream);
+
+/* The product, the residual add and the next RMS norm, as q8_gemv_residual_norm (its arguments and aliasing: h may be
+ * residual itself): h = residual + x . W, out = h / sqrt(mean(h^2) + eps) * gamma.  Two launches. */
+q8_status q8_gemv4_residual_norm(const void *x, const q8_weight4 *weight, const float *residual, const float *gamma,
+                                 float eps, float *h, void *out_bf16, int m, int K, unsigned int flags,
+                                 q8_stream_t stream);
+
+/* What a step does to its logits before a token is chosen.  Every pointer may be NULL: that rule is then left out.  All are
+ * device pointers, aligned to their type. */
+typedef struct {
+    const float *repetition, *frequency, *presence, *temperature; /* fp32 [m] */
+    const void *history;   /* int32 (int64 with history_wide) [m][history_pitch]: the tokens of each row's request */
+    const int *lengths;    /* int32 [m]: how many of them there are (required with history) */
+    const int *prompts;    /* int32 [m]: how many of those are prompt, not answer (NULL: none) */
+    const int *bias_ids;   /* int32 [m][bias_width]: tokens with a bias; ids outside 0..N-1 are unused places */
+    const float *bias;     /* fp32 [m][bias_width]: their biases (required with bias_ids) */
+    const int *mask;       /* int32 [mask_count][mask_pitch]: bit n % 32 of word n / 32 set: token n is allowed */
+    const int *mask_rows;  /* int32 [m]: the mask of each row, none outside 0..mask_count-1 (NULL: row r has mask r) */
+    const float *noise;    /* fp32 [m][noise_pitch]: added for the choice alone */
+    int history_width, history_pitch, history_wide, bias_width, mask_count, mask_pitch, noise_pitch;
+} q8_choice;
+
+#define Q8_MAX_HISTORY 1048575
+#define Q8_MAX_BIAS 2047
+
+/* The rules on logits, and the token chosen.  For token n < N of row r, in fp32, each step rounded once:
+ *     v = logits[r][n]
+ *     v = v > 0 ? v / repetition : v * repetition        if n stands anywhere in history[r][0 .. lengths[r])
+ *     v = v - frequency * c                              c = how often n stands in history[r][prompts[r] .. lengths[r])
+ *     v = v - presence                                   if c > 0
+ *     v = v + bias                                       if n is among bias_ids[r] (at several places: the last one counts)
+ *     v = v / temperature                                if temperature > 0
+ *     out[r][n] = v, or -inf where the row's mask has no bit for n (whatever v is, NaN too)
+ *     idx[r] = the lowest n with the largest score among the tokens that the mask allows, -1 if it allows none;
+ *              score = v + noise[r][n] where temperature > 0, else v
+ * A NaN is larger than +inf, and -0 equals +0, as in q8_gemv_argmax.  With Gumbel noise (-log(-log(u)), u uniform) idx is a
+ * sample of softmax(v); a temperature of 0 (or none) is greedy.  A negative or NaN temperature counts as 0.  Without
+ * temperature (NULL) the noise is not added.
+ *   logits  device, fp32 [m][ldl]      out  device, fp32 [m][ldo], or NULL (only idx is written); may be logits itself with
+ *   idx     device, int64 [m]                ldo == ldl (in place), and may not overlap an input otherwise
+ *   1 <= m <= 65535, 1 <= N < 2^31 - 1024, pitches at least N (history_pitch >= history_width, mask_pitch >= ceil(N / 32))
+ *   history_width <= Q8_MAX_HISTORY, bias_width <= Q8_MAX_BIAS, both >= 1 where given
+ * Lengths beyond history_width count as it, negative ones as 0, as do prompts; tokens of the history outside 0..N-1 are
+ * passed over.  repetition is expected positive.  One launch.
+ * Errors: Q8_ERR_ARG (NULL pointers, a rule without its companion, overlaps), Q8_ERR_SHAPE, Q8_ERR_ALIGN, Q8_ERR_CUDA. */
+q8_status q8_choose(const float *logits, int ldl, const q8_choice *rules, float *out, int ldo, int64_t *idx, int m, int N,
+                    q8_stream_t stream);
+
 /* Reads the device fault word of the current device: nonzero when a kernel's bounded wait on a pipeline barrier ran
  * out (bit 0: a consumer waited about two seconds for a stage's data; bit 1: the producer waited as long for a free
  * stage; bit 2: a wait of the prefill GEMM ran out; bit 3: one of q8_attn_prefill, whose workspace has to be

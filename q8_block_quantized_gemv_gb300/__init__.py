@@ -14,6 +14,11 @@ it allocates is allocated there, and the caller orders its inputs' writes before
 * :class:`KVCache`, :func:`kv_slots`, :func:`rope_table`, :func:`rope_append`, :func:`attn_decode`,
   :func:`attn_prefill` -- what lies between the q/k/v products and the output projection: a paged key-value cache
   (bf16 or Q8_0), its block tables and slots, the append with norms and rotation, and the attention over it;
+* :class:`Weight4`, :func:`gemv4`, :func:`gemv4_parts`, :func:`gemv4_glu`, :func:`gemv4_residual_norm` -- the products
+  over weights of 4 bits with a scale (and a zero point) for each group of 32, 64 or 128 rows; :func:`repack4` makes them
+  from checkpoint blocks;
+* :func:`choose` -- ``q8_choose``: penalties for repeated tokens, biases, temperature and grammar masks on the logits, and
+  the token chosen;
 * :func:`repack` -- ``q8_repack``: 36-byte checkpoint blocks -> (q, s) on the host;
 * :func:`quantize` -- ``q8_quantize``: the Q8_0 rule of "from_q8.rs" ``quantize`` on the host.
 
@@ -73,6 +78,15 @@ SIGNATURES = {
     "q8_attn_workspace_bytes": (ctypes.c_int64, []),
     "q8_attn_decode": (_I, [_P, _I, _P, _P, _I, _I, _P, _P, _I, _I, _I, ctypes.c_float, _I, _I, _P, _P]),
     "q8_attn_prefill": (_I, [_P, _I, _P, _P, _I, _I, _P, _P, _P, _I, _I, _I, _I, ctypes.c_float, _I, _I, _P, _P]),
+    "q8_w4_bytes": (ctypes.c_int64, [_I, _I, _I, ctypes.c_uint]),
+    "q8_w4_tile": (_I, [_P, _P, _P, _I, _I, _I, ctypes.c_uint, _P]),
+    "q8_w4_tile_device": (_I, [_P, _P, _P, _I, _I, _I, ctypes.c_uint, _P, _P]),
+    "q8_w4_repack": (_I, [_P, _I, _I, _P, _P]),
+    "q8_gemv4": (_I, [_P, _P, _P, _I, _I, ctypes.c_uint, _P]),
+    "q8_gemv4_parts": (_I, [_P, _P, _P, _I, _I, _I, ctypes.c_uint, _P]),
+    "q8_gemv4_glu": (_I, [_P, _P, _P, _P, _P, _I, _I, ctypes.c_uint, _P]),
+    "q8_gemv4_residual_norm": (_I, [_P, _P, _P, _P, ctypes.c_float, _P, _P, _I, _I, ctypes.c_uint, _P]),
+    "q8_choose": (_I, [_P, _I, _P, _P, _I, _P, _I, _I, _P]),
 }
 
 
@@ -761,6 +775,267 @@ def attn_prefill(q, cache: KVCache, table, lens, row_start, q_heads: int | None 
     if st:
         raise Q8Error(st, "q8_attn_prefill")
     return out
+
+
+class _W4(ctypes.Structure):
+    _fields_ = [("w", _P), ("N", _I), ("group", _I), ("flags", ctypes.c_uint)]
+
+
+class Weight4:
+    """A weight of 4-bit codes with group scales, laid out for the products (q8_w4_tile_device): value = scale * (code -
+    zero).  From CUDA tensors as a checkpoint has them: ``codes`` uint8 [K/2, N] (row 2i in the low half of byte row i),
+    ``scales`` float16 or bfloat16 [K/group, N] with group 32, 64 or 128, ``zeros`` uint8 [K/group, N] of 0..127 (None: 8
+    everywhere).  Keeps its own copy, ``buf``; :func:`tile4` lays it out on the host, :meth:`of_tiled` takes that."""
+
+    def __init__(self, codes, scales, zeros=None, stream=None):
+        import torch
+        for name, t in (("codes", codes), ("scales", scales), ("zeros", zeros)):
+            if t is not None and (not t.is_cuda or t.get_device() != codes.get_device() or t.dim() != 2
+                                  or not t.is_contiguous()):
+                raise ValueError(f"{name} must be a contiguous 2-D CUDA tensor, on the device of the others")
+        if codes.dtype != torch.uint8 or scales.dtype not in (torch.float16, torch.bfloat16) or \
+                (zeros is not None and zeros.dtype != torch.uint8):
+            raise TypeError("codes and zeros must be uint8, scales float16 or bfloat16")
+        K, N = 2 * codes.shape[0], codes.shape[1]
+        groups = scales.shape[0]
+        if scales.shape[1] != N or (zeros is not None and zeros.shape != scales.shape) or not groups or K % groups:
+            raise ValueError("scales and zeros must be [K / group, N], codes [K / 2, N]")
+        flags = (FLAG_W4_ZEROS if zeros is not None else 0) | (FLAG_W4_BF16 if scales.dtype == torch.bfloat16 else 0)
+        size = int(lib().q8_w4_bytes(K, N, K // groups, flags))
+        if size < 0:
+            raise ValueError("a group is 32, 64 or 128 rows")
+        self._keep(_new((size,), torch.uint8, codes.device, stream), K, N, K // groups, flags)
+        _check(lib().q8_w4_tile_device(codes.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr(), K,
+                                       N, self.group, flags, self.buf.data_ptr(), _stream_of(stream, codes.device)),
+               "q8_w4_tile_device")
+
+    @classmethod
+    def of_tiled(cls, buf, K: int, N: int, group: int, zeros: bool = False, bf16_scales: bool = False):
+        """A weight whose tiled form (uint8 CUDA tensor, 16-byte aligned) is at hand."""
+        import torch
+        flags = (FLAG_W4_ZEROS if zeros else 0) | (FLAG_W4_BF16 if bf16_scales else 0)
+        size = int(lib().q8_w4_bytes(K, N, group, flags))
+        if size < 0 or not buf.is_cuda or buf.dtype != torch.uint8 or not buf.is_contiguous() or buf.numel() != size:
+            raise ValueError(f"buf must be a contiguous uint8 CUDA tensor of {size} bytes")
+        self = cls.__new__(cls)
+        self._keep(buf, K, N, group, flags)
+        return self
+
+    def _keep(self, buf, K, N, group, flags):
+        self.buf, self.K, self.N, self.Np, self.group, self.flags = buf, K, N, padded_n(N), group, flags
+        self.device, self._index = buf.device, buf.get_device()
+        self._c = _W4(buf.data_ptr(), N, group, flags)
+        self._ref = ctypes.addressof(self._c)
+
+
+FLAG_W4_ZEROS = 1
+FLAG_W4_BF16 = 2
+
+
+def tile4(codes, scales, zeros=None, bf16_scales: bool = False):
+    """Host: numpy arrays in the plain form (scales as 16-bit words) -> the tiled bytes (q8_w4_tile)."""
+    codes = np.ascontiguousarray(codes, dtype=np.uint8)
+    scales = np.ascontiguousarray(scales).view(np.uint16)
+    if zeros is not None:
+        zeros = np.ascontiguousarray(zeros, dtype=np.uint8)
+    K, N, groups = 2 * codes.shape[0], codes.shape[1], scales.shape[0]
+    if scales.shape[1] != N or (zeros is not None and zeros.shape != scales.shape) or not groups or K % groups:
+        raise ValueError("scales and zeros must be [K / group, N], codes [K / 2, N]")
+    flags = (FLAG_W4_ZEROS if zeros is not None else 0) | (FLAG_W4_BF16 if bf16_scales else 0)
+    out = np.empty(max(int(lib().q8_w4_bytes(K, N, K // groups, flags)), 1), dtype=np.uint8)
+    _check(lib().q8_w4_tile(codes.ctypes.data, scales.ctypes.data, None if zeros is None else zeros.ctypes.data, K, N,
+                            K // groups, flags, out.ctypes.data), "q8_w4_tile")
+    return out
+
+
+def repack4(blocks, K: int, N: int):
+    """(codes uint8 [K/2, N], scales float16 [K/32, N]) from N * K/32 Q4_0 checkpoint blocks of 18 bytes (host)."""
+    raw = np.frombuffer(bytes(blocks), dtype=np.uint8) if not isinstance(blocks, np.ndarray) else \
+        np.ascontiguousarray(blocks).view(np.uint8).reshape(-1)
+    if K > 0 and N > 0 and raw.size != N * (K // Q8_BLOCK) * 18:
+        raise ValueError("block buffer size does not match K and N")
+    codes = np.empty((max(K // 2, 1), max(N, 1)), dtype=np.uint8)
+    scales = np.empty((max(K // Q8_BLOCK, 1), max(N, 1)), dtype=np.float16)
+    _check(lib().q8_w4_repack(raw.ctypes.data, K, N, codes.ctypes.data, scales.ctypes.data), "q8_w4_repack")
+    return codes, scales
+
+
+def _x4(x, w):
+    """The rows of activation x, checked against weight w."""
+    import torch
+    shape = x.shape
+    if x.dtype != torch.bfloat16 or len(shape) != 2 or shape[1] != w.K or x.get_device() != w._index \
+            or not x.is_contiguous():
+        raise ValueError(f"x must be a contiguous bfloat16 tensor [m, {w.K}] on the weight's device")
+    return shape[0]
+
+
+def _out4(name, t, m, w, dtype):
+    if t.dtype != dtype or tuple(t.shape) != (m, w.Np) or t.get_device() != w._index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor [{m}, {w.Np}] on the weight's device")
+    return t
+
+
+def gemv4(x, w: Weight4, y=None, constant_weights: bool = False, stream=None):
+    """y = x . W over a 4-bit weight (q8_gemv4): x bf16 [m, K], 1 <= m <= 512; returns y, fp32 [m, Np] (columns N .. Np-1
+    are 0).  constant_weights: as for :func:`gemv`."""
+    import torch
+    m = _x4(x, w)
+    y = _new((m, w.Np), torch.float32, w.device, stream) if y is None else _out4("y", y, m, w, torch.float32)
+    st = lib().q8_gemv4(x.data_ptr(), w._ref, y.data_ptr(), m, w.K, 1 if constant_weights else 0,
+                        _stream_of(stream, w.device))
+    if st:
+        raise Q8Error(st, "q8_gemv4")
+    return y
+
+
+def gemv4_parts(x, weights, ys=None, constant_weights: bool = False, stream=None):
+    """Several products of one activation in one call (q8_gemv4_parts); the weights have the same K, group and flags.
+    Returns the list of outputs, fp32 [m, Np_p]."""
+    import torch
+    n = len(weights)
+    if not 1 <= n <= 8:
+        raise ValueError("1 to 8 weights")
+    if ys is not None and len(ys) != n:
+        raise ValueError("an output for each weight")
+    m = _x4(x, weights[0])
+    arr, outs, to = (_W4 * n)(), [], (_P * n)()
+    for i, w in enumerate(weights):
+        if w.K != weights[0].K or w._index != weights[0]._index:
+            raise ValueError("the weights must have the same K and device")
+        y = _new((m, w.Np), torch.float32, w.device, stream) if ys is None else _out4("y", ys[i], m, w, torch.float32)
+        arr[i], to[i] = w._c, y.data_ptr()
+        outs.append(y)
+    st = lib().q8_gemv4_parts(x.data_ptr(), ctypes.addressof(arr), ctypes.addressof(to), n, m, weights[0].K,
+                              1 if constant_weights else 0, _stream_of(stream, weights[0].device))
+    if st:
+        raise Q8Error(st, "q8_gemv4_parts")
+    return outs
+
+
+def gemv4_glu(x, gate: Weight4, up: Weight4, out=None, out_bf16=None, want=("f32",), constant_weights: bool = False,
+              stream=None):
+    """The gated pair (q8_gemv4_glu): silu(x . Wg) * (x . Wu).  ``want``: which outputs to allocate when not given, "f32"
+    and/or "bf16" ([m, Np]).  Returns (out, out_bf16), either None when not requested."""
+    import torch
+    m = _x4(x, gate)
+    if up.K != gate.K or up._index != gate._index:
+        raise ValueError("gate and up must have the same K and device")
+    if out is not None:
+        _out4("out", out, m, gate, torch.float32)
+    elif "f32" in want:
+        out = _new((m, gate.Np), torch.float32, gate.device, stream)
+    if out_bf16 is not None:
+        _out4("out_bf16", out_bf16, m, gate, torch.bfloat16)
+    elif "bf16" in want:
+        out_bf16 = _new((m, gate.Np), torch.bfloat16, gate.device, stream)
+    st = lib().q8_gemv4_glu(x.data_ptr(), gate._ref, up._ref, None if out is None else out.data_ptr(),
+                            None if out_bf16 is None else out_bf16.data_ptr(), m, gate.K, 1 if constant_weights else 0,
+                            _stream_of(stream, gate.device))
+    if st:
+        raise Q8Error(st, "q8_gemv4_glu")
+    return out, out_bf16
+
+
+def gemv4_residual_norm(x, w: Weight4, residual, gamma, eps: float, h=None, out_bf16=None, constant_weights: bool = False,
+                        stream=None):
+    """A projection, the residual add and the following RMS norm (q8_gemv4_residual_norm): h = residual + x . W, out =
+    h / sqrt(mean(h^2) + eps) * gamma.  Returns (h fp32 [m, Np], out bf16 [m, Np]); ``h`` may be ``residual`` (in place)."""
+    import torch
+    m = _x4(x, w)
+    _out4("residual", residual, m, w, torch.float32)
+    if gamma.dtype != torch.float32 or gamma.numel() < w.N or not gamma.is_contiguous() or gamma.get_device() != w._index:
+        raise ValueError("gamma must be a contiguous fp32 tensor of at least N values on the weight's device")
+    h = _new((m, w.Np), torch.float32, w.device, stream) if h is None else _out4("h", h, m, w, torch.float32)
+    if out_bf16 is None:
+        out_bf16 = _new((m, w.Np), torch.bfloat16, w.device, stream)
+    else:
+        _out4("out_bf16", out_bf16, m, w, torch.bfloat16)
+    st = lib().q8_gemv4_residual_norm(x.data_ptr(), w._ref, residual.data_ptr(), gamma.data_ptr(), eps, h.data_ptr(),
+                                      out_bf16.data_ptr(), m, w.K, 1 if constant_weights else 0,
+                                      _stream_of(stream, w.device))
+    if st:
+        raise Q8Error(st, "q8_gemv4_residual_norm")
+    return h, out_bf16
+
+
+class _Choice(ctypes.Structure):
+    _fields_ = [(n, _P) for n in ("repetition", "frequency", "presence", "temperature", "history", "lengths", "prompts",
+                                  "bias_ids", "bias", "mask", "mask_rows", "noise")] + \
+               [(n, _I) for n in ("history_width", "history_pitch", "history_wide", "bias_width", "mask_count",
+                                  "mask_pitch", "noise_pitch")]
+
+
+def _pitched(name, t, dtypes, rows, cols, index):
+    """A 2-D tensor's pointer and row pitch: unit column stride, `rows` rows (None: any), at least `cols` columns."""
+    shape = t.shape
+    if t.get_device() != index or t.dtype not in dtypes or len(shape) != 2 or (rows is not None and shape[0] != rows) \
+            or shape[1] < cols or (shape[1] > 1 and t.stride(1) != 1) or (shape[0] > 1 and t.stride(0) < shape[1]):
+        raise ValueError(f"{name} must be a 2-D {dtypes[0]} CUDA tensor of {rows if rows is not None else 'any'} rows and at "
+                         f"least {cols} columns, unit column stride, on the device of the logits")
+    return t.data_ptr(), t.stride(0) if shape[0] > 1 else shape[1]
+
+
+def choose(logits, N: int | None = None, out=None, repetition=None, frequency=None, presence=None, temperature=None,
+           history=None, lengths=None, prompts=None, bias_ids=None, bias=None, mask=None, mask_rows=None, noise=None,
+           idx=None, stream=None):
+    """Penalties for repeated tokens, biases, temperature and grammar masks on the logits, and the token chosen
+    (q8_choose): logits fp32 [m, >= N] (N defaults to the columns).  Returns idx, int64 [m]: the first maximum among the
+    allowed tokens, -1 where the mask allows none.
+
+    out: fp32 [m, >= N] that receives the logits after the rules (``logits`` itself: in place; None: not written).
+    repetition, frequency, presence, temperature: fp32 [m].  history: int32 or int64 [m, width], of which the first
+    ``lengths`` (int32 [m]) tokens of a row count, the first ``prompts`` (int32 [m]) of those as prompt: repetition looks at
+    all of them, frequency and presence at the others.  bias_ids int32 and bias fp32 [m, count]: tokens with a bias, ids
+    outside the vocabulary are unused places.  mask: int32 [masks, >= ceil(N / 32)], a set bit n % 32 of word n / 32 allows
+    token n; mask_rows int32 [m]: the mask of each row, -1 for none (default: mask r for row r).  noise: fp32 [m, >= N], added
+    for the choice where the temperature is above 0 (Gumbel noise samples softmax(out))."""
+    import torch
+    f32, i32 = torch.float32, torch.int32
+    index = logits.get_device()
+    if index < 0:
+        raise ValueError("logits must be a CUDA tensor")
+    m = logits.shape[0]
+    if N is None:
+        N = logits.shape[-1]
+    lp, ldl = _pitched("logits", logits, (f32,), m, N, index)
+    c = _Choice()
+    for name, t, dtype in (("repetition", repetition, f32), ("frequency", frequency, f32), ("presence", presence, f32),
+                           ("temperature", temperature, f32), ("lengths", lengths, i32), ("prompts", prompts, i32),
+                           ("mask_rows", mask_rows, i32)):
+        if t is not None:
+            if t.get_device() != index or t.dtype != dtype or t.numel() != m or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of {m} values on the logits' device")
+            setattr(c, name, t.data_ptr())
+    if history is not None and history.shape[-1]:
+        c.history, c.history_pitch = _pitched("history", history, (i32, torch.int64), m, 1, index)
+        c.history_width, c.history_wide = history.shape[1], int(history.dtype == torch.int64)
+    if bias is not None and bias_ids is None:
+        raise ValueError("bias needs bias_ids")
+    if history is not None and lengths is None:
+        raise ValueError("history needs lengths")
+    if bias_ids is not None and bias_ids.shape[-1]:
+        for name, t, dtype in (("bias_ids", bias_ids, i32), ("bias", bias, f32)):
+            if t is None or t.get_device() != index or t.dtype != dtype or t.shape != (m, bias_ids.shape[-1]) \
+                    or not t.is_contiguous():
+                raise ValueError("bias_ids int32 and bias float32 must be contiguous [m, count], on the logits' device")
+        c.bias_ids, c.bias, c.bias_width = bias_ids.data_ptr(), bias.data_ptr(), bias_ids.shape[1]
+    if mask is not None:
+        c.mask, c.mask_pitch = _pitched("mask", mask, (i32,), None, (N + 31) // 32, index)
+        c.mask_count = mask.shape[0]
+    if noise is not None:
+        c.noise, c.noise_pitch = _pitched("noise", noise, (f32,), m, N, index)
+    op, ldo = (None, 0) if out is None else _pitched("out", out, (f32,), m, N, index)
+    if idx is None:
+        idx = _new((m,), torch.int64, logits.device, stream)
+    elif idx.dtype != torch.int64 or idx.numel() != m or not idx.is_contiguous() or idx.get_device() != index:
+        raise ValueError("idx must be a contiguous int64 CUDA tensor of m values on the logits' device")
+    if m == 0:
+        return idx
+    st = lib().q8_choose(lp, ldl, ctypes.addressof(c), op, ldo, idx.data_ptr(), m, N, _stream_of(stream, logits.device))
+    if st:
+        raise Q8Error(st, "q8_choose")
+    return idx
 
 
 def residual_norm_launches() -> int:
