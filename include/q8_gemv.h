@@ -553,7 +553,7 @@ q8_status q8_choose(const float *logits, int ldl, const q8_choice *rules, float 
 /* Reads the device fault word of the current device: nonzero when a kernel's bounded wait on a pipeline barrier ran
  * out (bit 0: a consumer waited about two seconds for a stage's data; bit 1: the producer waited as long for a free
  * stage; bit 2: a wait of the prefill GEMM ran out; bit 3: one of q8_attn_prefill, whose workspace has to be
- * zeroed again) and the kernel finished early -- that call's outputs are then
+ * zeroed again; bit 4: one of the products over 4-bit weights) and the kernel finished early -- that call's outputs are then
  * wrong.  Synchronous with respect to the
  * device.  `clear` != 0 resets the word to 0.  Returns Q8_ERR_ARG for a NULL `fault`, Q8_ERR_CUDA on a CUDA error. */
 q8_status q8_device_fault(unsigned int *fault, int clear);

@@ -8,6 +8,7 @@
 #include "../../include/q8_gemv.h"
 #include "q8_attn.h"
 #include "q8_launch.h"
+#include "q8_w4.h"
 
 namespace q8 {
 void set_last_cuda_error(int e);  // q8_host.cpp
@@ -646,12 +647,13 @@ extern "C" q8_status q8_gemv_residual_norm(const void *x, const int8_t *q, const
 
 extern "C" q8_status q8_device_fault(unsigned int *fault, int clear) {
     if (!fault) return Q8_ERR_ARG;
-    unsigned gemm = 0, attn = 0;
+    unsigned gemm = 0, attn = 0, w4 = 0;
     cudaError_t e = q8::read_fault_word(fault, clear != 0);
     if (e == cudaSuccess) e = q8::read_gemm_fault(&gemm, clear != 0);
     if (e == cudaSuccess) e = q8::read_attn_fault(&attn, clear != 0);
+    if (e == cudaSuccess) e = q8::read_w4_fault(&w4, clear != 0);
     if (e != cudaSuccess) return cuda_fail(e);
-    *fault |= gemm | attn;
+    *fault |= gemm | attn | w4;
     return Q8_OK;
 }
 

@@ -94,8 +94,9 @@ void add_part(q8::W4Args *a, const q8_weight4 *w, float *y) {
 }
 
 q8_status launch(const q8::W4Args &a, unsigned flags, q8_stream_t stream) {
-    const cudaError_t e =
-        q8::launch_w4_stream(a, (flags & Q8_FLAG_CONSTANT_WEIGHTS) != 0, (cudaStream_t)stream);
+    const bool constant = (flags & Q8_FLAG_CONSTANT_WEIGHTS) != 0;
+    const cudaError_t e = a.m <= q8::kW4StreamRows ? q8::launch_w4_stream(a, constant, (cudaStream_t)stream)
+                                                   : q8::launch_w4_gemm(a, constant, (cudaStream_t)stream);
     return e == cudaSuccess ? Q8_OK : kv_cuda_fail(e);
 }
 

@@ -1,67 +1,362 @@
-// Products over 4-bit weights, first form: a warp computes one strip of 32 columns for eight rows, a lane a column, on the
-// CUDA cores.  Right for every size; neither reads the weight once for all rows nor fills the SMs.
+// Products of up to 16 rows over 4-bit weights: every warp streams its own run of units and contracts them on the tensor
+// cores with exact bf16 operands.
+//
+// y[r, n] = sum_g s[g, n] * sum_{k in g} x[r, k] (c[k, n] - z[g, n]).  At 4.1 to 4.75 bits a weight the call is bound by the
+// bytes of the weight; what has to keep up with them is the conversion, 11 instructions for 8 codes (three shifts, four
+// ands-and-ors under a bf16 exponent, four packed subtracts), which is why each code is converted once for all rows.
+//
+//   - A strip of 32 columns belongs to a warp, in chunks of 128 rows (one, two or four units, contiguous), fetched by one
+//     bulk copy each into the warp's own ring of shared memory.  Only the warp's lane 0 waits for nothing and asks for all
+//     of it: no other warp is involved.
+//   - The weights are the MMA's A operand (m16n8k16: 16 columns of W), the activations B (8 rows).  The order of the
+//     reduction is free, so a lane's four k-pairs of two MMAs are the 8 rows of one stored word, and its activations 16
+//     consecutive bytes.  With the activations as A half of every MMA would be empty rows for m <= 8.
+//   - A group's sums start from zero and are folded with its scales into an fp32 carry; c - z and x are exact in bf16.
+//   - A CTA's eight warps are cw strips times kw runs of K; the kw warps of one run share its activations (a ring of their
+//     own, m bulk copies of 256 bytes a chunk).  The runs' carries are added in shared memory in order, then, where the
+//     strips are too few for the SMs and K is split over a cluster, those of its CTAs in rank order.
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 
-#include "q8_w4.h"
+#include <atomic>
+
+#include <stdlib.h>
+#include "q8_attn.h"
+#include "q8_launch.h"
+#include "q8_w4_device.cuh"
 
 namespace q8 {
+
+__device__ unsigned int g_w4_fault = 0;
+
 namespace {
 
-constexpr int kRows = 8;
+constexpr int kWarps4 = 8;
+constexpr int kThreads4 = 32 * kWarps4;
+constexpr int kChunk = 128;              // rows of K in a stage
+constexpr int kXPitch4 = 2 * kChunk + 64;  // bytes between activation rows in a stage: 64 past a multiple of 128, so that
+                                         // the 16-byte loads of two rows and four lanes fall on all banks
+struct Stream4 {
+    int cw;      // strips of a CTA (the gated pair: of both weights); 8 / cw runs of K
+    int depth;   // stages of a ring
+    int ks;      // CTAs of a cluster splitting K
+    int prefetch;
+};
 
-__device__ __forceinline__ float scale_value(uint16_t s, int bf16) {
-    return bf16 ? __uint_as_float((uint32_t)s << 16) : __half2float(__ushort_as_half(s));
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ void product(const W4Args &a, const unsigned char *strip, int row0, int c, float (&acc)[kRows]) {
-    for (int r = 0; r < kRows; ++r) acc[r] = 0.0f;
-    for (int g = 0; g < a.K / a.group; ++g, strip += a.unit) {
-        const int zero = a.zeros ? strip[16 * a.group + 64 + c] : 8;
-        float part[kRows] = {};
-        for (int b = 0; b < a.group / 32; ++b)
-            for (int t = 0; t < 4; ++t) {
-                const uint32_t w = *reinterpret_cast<const uint32_t *>(strip + w4_word(a.group, b, t, c));
-                const uint16_t *x = a.x + (size_t)row0 * a.K + g * a.group + 32 * b + 8 * t;
-                for (int i = 0; i < 8; ++i) {
-                    const float v = (float)((int)((w >> (4 * (i >> 1) + 16 * (i & 1))) & 15u) - zero);
-                    for (int r = 0; r < kRows; ++r)
-                        if (row0 + r < a.m) part[r] = fmaf(__uint_as_float((uint32_t)x[(size_t)r * a.K + i] << 16), v, part[r]);
-                }
+// One 32-row block of a strip: word[j][h] of tile j, columns 16j + g and 16j + 8 + g; xb[nt] the lane's 8 activations.
+template <int NT>
+__device__ __forceinline__ void block32(float (&d)[2][NT][4], const uint32_t (&word)[2][2], const uint32_t (&zero)[2][2],
+                                        const uint4 (&xb)[NT]) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const uint32_t lo[4] = {w4_pair<0>(word[j][0], zero[j][0]), w4_pair<0>(word[j][1], zero[j][1]),
+                                w4_pair<1>(word[j][0], zero[j][0]), w4_pair<1>(word[j][1], zero[j][1])};
+        const uint32_t hi[4] = {w4_pair<2>(word[j][0], zero[j][0]), w4_pair<2>(word[j][1], zero[j][1]),
+                                w4_pair<3>(word[j][0], zero[j][0]), w4_pair<3>(word[j][1], zero[j][1])};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_bf16(d[j][nt], lo, xb[nt].x, xb[nt].y);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_bf16(d[j][nt], hi, xb[nt].z, xb[nt].w);
+    }
+}
+
+template <int G, int NT>
+__global__ void __launch_bounds__(kThreads4, 2) stream4_kernel(const __grid_constant__ W4Args a, const Stream4 p) {
+    namespace cg = cooperative_groups;
+    constexpr int CG = kChunk / G;  // groups of a chunk
+    extern __shared__ __align__(128) unsigned char smem4[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int cw = p.cw, kw = kWarps4 / cw, depth = p.depth;
+    const int cwi = warp & (cw - 1), kwi = warp / cw;
+    const int stage = CG * a.unit, xstage = a.m * kXPitch4;
+    unsigned char *ring = smem4 + warp * depth * stage;
+    unsigned char *xring = smem4 + kWarps4 * depth * stage + kwi * depth * xstage;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem4 + depth * (kWarps4 * stage + kw * xstage));
+    uint64_t *wfull = bars + warp * depth, *xfull = bars + (kWarps4 + kwi) * depth, *xempty = xfull + kw * depth;
+
+    // the CTA's tile: cw strips of one part, or cw / 2 of the gate and of the up projection, in turn
+    const bool pair = a.epi == kW4Glu;
+    const int width = pair ? cw / 2 : cw;  // strips of output
+    int part = 0, tile = blockIdx.x;
+    if (!pair)
+        for (int first = 0, tiles;; ++part, tile -= tiles, first = a.part[part - 1].strip_end) {
+            tiles = (a.part[part].strip_end - first + cw - 1) / cw;
+            if (tile < tiles || part + 1 == a.nparts) break;
+        }
+    const W4Part &mine = a.part[pair ? cwi & 1 : part];
+    const int strips = mine.Np / kW4Strip, strip = tile * width + (pair ? cwi >> 1 : cwi);
+    const int live = min(cw, (pair ? 2 : 1) * (strips - tile * width));  // warps of a run with a strip
+
+    // the warp's run of chunks
+    const int groups = a.K / G, chunks = (groups + CG - 1) / CG, runs = kw * p.ks;
+    const int run = blockIdx.y * kw + kwi;
+    const int c0 = (int)((long long)chunks * run / runs);
+    const int n = cwi < live ? (int)((long long)chunks * (run + 1) / runs) - c0 : 0;
+    const unsigned char *src = mine.w + ((size_t)strip * groups + (size_t)c0 * CG) * a.unit;
+    auto groups_of = [&](int i) { return min(CG, groups - (c0 + i) * CG); };
+    auto ask_w = [&](int i) {  // lane 0
+        const unsigned bytes = (unsigned)(groups_of(i) * a.unit);
+        uint64_t *bar = wfull + i % depth;
+        w4_arrive_tx(bar, bytes);
+        w4_copy(ring + (i % depth) * stage, src + (size_t)i * stage, bytes, bar);
+    };
+    auto ask_x = [&](int i) {  // the run's first warp, all lanes
+        const unsigned bytes = (unsigned)(groups_of(i) * G * 2);
+        uint64_t *bar = xfull + i % depth;
+        if (lane == 0) w4_arrive_tx(bar, bytes * a.m);
+        __syncwarp();
+        if (lane < a.m)
+            w4_copy(xring + (i % depth) * xstage + lane * kXPitch4, a.x + (size_t)lane * a.K + (size_t)(c0 + i) * kChunk,
+                    bytes, bar);
+    };
+
+    if (lane == 0) {
+        for (int s = 0; s < depth; ++s) {
+            w4_bar_init(wfull + s, 1);
+            if (cwi == 0) {
+                w4_bar_init(xfull + s, 1);
+                w4_bar_init(xempty + s, live);
             }
-        const float s = scale_value(*reinterpret_cast<const uint16_t *>(strip + 16 * a.group + 2 * c), a.bf16);
-        for (int r = 0; r < kRows; ++r) acc[r] = fmaf(s, part[r], acc[r]);
+        }
+        w4_bar_fence();
+        if (p.prefetch)
+            for (int i = 0; i < depth && i < n; ++i) ask_w(i);
     }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (cwi == 0) {
+        __syncwarp();
+        for (int i = 0; i < depth && i < n; ++i) ask_x(i);
+    }
+    if (lane == 0 && !p.prefetch)
+        for (int i = 0; i < depth && i < n; ++i) ask_w(i);
+    __syncthreads();
+
+    float acc[2][NT][4] = {};
+    bool xlive[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) xlive[nt] = 8 * nt + g < a.m;
+    bool ok = true;
+    int slot = 0, i = 0, asked = min(depth, n);  // chunks of x asked for
+    unsigned phase = 0;
+    for (; i < n; ++i) {
+        if (cwi == 0 && i > 0 && i - 1 + depth < n) {  // the place of the chunk before: all of the run are past it, or nearly
+            if (!(ok = __all_sync(0xffffffffu, w4_wait(xempty + (i - 1) % depth, ((i - 1) / depth) & 1)))) break;
+            ask_x(i - 1 + depth);
+            asked = i + depth;
+        }
+        if (!(ok = __all_sync(0xffffffffu, w4_wait(xfull + slot, phase) && w4_wait(wfull + slot, phase)))) break;
+        const unsigned char *st = ring + slot * stage;
+        const unsigned char *xs = xring + slot * xstage + g * kXPitch4 + 16 * t;
+        const int here = groups_of(i);
+#pragma unroll
+        for (int q = 0; q < CG; ++q) {
+            if (CG > 1 && q >= here) break;
+            const unsigned char *u = st + q * a.unit;
+            uint32_t zero[2][2] = {{kRaisedEight, kRaisedEight}, {kRaisedEight, kRaisedEight}};
+            if (a.zeros) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) zero[j][h] = w4_raised_zero(u[16 * G + 64 + 16 * j + 8 * h + g]);
+            }
+            float d[2][NT][4] = {};
+#pragma unroll
+            for (int b = 0; b < G / 32; b += 2) {
+                uint32_t w0[2][2], w1[2][2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (G == 32) {
+                        const uint2 v = *reinterpret_cast<const uint2 *>(u + 256 * j + 8 * lane);
+                        w0[j][0] = v.x, w0[j][1] = v.y;
+                    } else {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(u + 512 * (b + j) + 16 * lane);
+                        w0[j][0] = v.x, w0[j][1] = v.y, w1[j][0] = v.z, w1[j][1] = v.w;
+                    }
+                }
+                uint4 x0[NT], x1[NT];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const unsigned char *row = xs + 8 * nt * kXPitch4 + 2 * (q * G + 32 * b);
+                    x0[nt] = x1[nt] = make_uint4(0u, 0u, 0u, 0u);
+                    if (xlive[nt]) {
+                        x0[nt] = *reinterpret_cast<const uint4 *>(row);
+                        if (G > 32) x1[nt] = *reinterpret_cast<const uint4 *>(row + 64);
+                    }
+                }
+                block32<NT>(d, w0, zero, x0);
+                if (G > 32) block32<NT>(d, w1, zero, x1);
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float s =
+                        w4_scale(*reinterpret_cast<const uint16_t *>(u + 16 * G + 2 * (16 * j + 8 * h + g)), a.bf16);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        acc[j][nt][2 * h] = fmaf(s, d[j][nt][2 * h], acc[j][nt][2 * h]);
+                        acc[j][nt][2 * h + 1] = fmaf(s, d[j][nt][2 * h + 1], acc[j][nt][2 * h + 1]);
+                    }
+                }
+        }
+        __syncwarp();
+        if (lane == 0) {
+            if (i + depth < n) ask_w(i + depth);
+            w4_arrive(xempty + slot);
+        }
+        if (++slot == depth) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+    if (!ok && lane == 0) {  // what was asked for lands (or two more seconds pass for each) before the memory is used again
+        atomicOr(&g_w4_fault, kW4Fault);
+        for (int j = i; j < n && j < i + depth; ++j) w4_wait_long(wfull + j % depth, (j / depth) & 1);
+        if (cwi == 0)
+            for (int j = i; j < asked; ++j) w4_wait_long(xfull + j % depth, (j / depth) & 1);
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    __syncthreads();
+
+    // carries [kw][m][pitch] (a pitch of 4 past a multiple of 32 spreads a fragment's rows over the banks), their sum
+    const int cols = 32 * cw, pitch = cols + 4, rows = a.m;
+    float *red = reinterpret_cast<float *>(smem4);
+    float *sum = red + kw * rows * pitch;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int r = 8 * nt + 2 * t + (e & 1);
+                if (r < rows) red[(kwi * rows + r) * pitch + 32 * cwi + 16 * j + 8 * (e >> 1) + g] = acc[j][nt][e];
+            }
+    __syncthreads();
+    for (int i = threadIdx.x; i < rows * (cols / 4); i += kThreads4) {
+        const int r = i / (cols / 4), c = 4 * (i - r * (cols / 4));
+        float4 v = *reinterpret_cast<const float4 *>(red + r * pitch + c);
+        for (int k = 1; k < kw; ++k) {
+            const float4 o = *reinterpret_cast<const float4 *>(red + (k * rows + r) * pitch + c);
+            v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+        }
+        *reinterpret_cast<float4 *>(sum + r * cols + c) = v;
+    }
+    cg::cluster_group cluster = cg::this_cluster();
+    if (p.ks > 1)
+        cluster.sync();
+    else
+        __syncthreads();
+
+    // a rank's share of the output's columns, four a thread
+    const int share = 8 * width, k0 = share * (int)blockIdx.y / p.ks, k1 = share * ((int)blockIdx.y + 1) / p.ks;
+    const W4Part &to = a.part[part];
+    for (int i = threadIdx.x; i < rows * (k1 - k0); i += kThreads4) {
+        const int r = i / (k1 - k0), c = 4 * (k0 + i - r * (k1 - k0));
+        const int out = tile * width * kW4Strip + c;
+        if (out >= to.Np) continue;
+        auto total = [&](int at) {
+            return p.ks > 1 ? cluster_sum4(cluster, sum, at, 0, 1, p.ks) : *reinterpret_cast<const float4 *>(sum + at);
+        };
+        const float4 v4 = total(r * cols + (pair ? (c >> 5) * 64 + (c & 31) : c));
+        float v[4] = {v4.x, v4.y, v4.z, v4.w};
+        const size_t at = (size_t)r * to.Np + out;
+        if (pair) {
+            const float4 u4 = total(r * cols + (c >> 5) * 64 + 32 + (c & 31));
+            const float u[4] = {u4.x, u4.y, u4.z, u4.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = v[e] / (1.0f + expf(-v[e])) * u[e];
+        }
+        if (a.epi == kW4Residual) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (out + e < to.N) v[e] += a.res[at + e];
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (out + e >= to.N) v[e] = 0.0f;
+        if (to.y) *reinterpret_cast<float4 *>(to.y + at) = make_float4(v[0], v[1], v[2], v[3]);
+        if (a.ybf) {
+            __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
+            *reinterpret_cast<uint2 *>(a.ybf + at) =
+                make_uint2(*reinterpret_cast<uint32_t *>(&lo), *reinterpret_cast<uint32_t *>(&hi));
+        }
+    }
+    if (p.ks > 1) cluster_sync_after_reads();
 }
 
-__global__ void __launch_bounds__(128) simple_kernel(const __grid_constant__ W4Args a) {
-    const int c = threadIdx.x & 31, strips = a.epi == kW4Glu ? a.part[0].strip_end : a.part[a.nparts - 1].strip_end;
-    const int strip = blockIdx.x * 4 + (threadIdx.x >> 5), row0 = blockIdx.y * kRows;
-    if (strip >= strips) return;
-    int p = 0;
-    while (strip >= a.part[p].strip_end) ++p;
-    const int local = strip - (p ? a.part[p - 1].strip_end : 0), n = local * kW4Strip + c;
-    const size_t at = (size_t)local * (a.K / a.group) * a.unit;
-    float acc[kRows], up[kRows];
-    product(a, a.part[p].w + at, row0, c, acc);
-    if (a.epi == kW4Glu) product(a, a.part[1].w + at, row0, c, up);
-    for (int r = 0; r < kRows && row0 + r < a.m; ++r) {
-        const size_t to = (size_t)(row0 + r) * a.part[p].Np + n;
-        float v = acc[r];
-        if (a.epi == kW4Glu) v = v / (1.0f + expf(-v)) * up[r];
-        if (a.epi == kW4Residual && n < a.part[p].N) v += a.res[to];
-        if (n >= a.part[p].N) v = 0.0f;
-        if (a.part[p].y) a.part[p].y[to] = v;
-        if (a.ybf) a.ybf[to] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+constexpr int kMaxSmem4 = 227 * 1024;
+
+int smem_bytes(const W4Args &a, const Stream4 &p) {
+    const int kw = kWarps4 / p.cw;
+    const int ring = p.depth * (kWarps4 * (kChunk / a.group) * a.unit + kw * a.m * kXPitch4 + (kWarps4 + 2 * kw) * 8);
+    const int ends = a.m * (kw * (32 * p.cw + 4) + 32 * p.cw) * 4;
+    return ring > ends ? ring : ends;
+}
+
+int tiles_of(const W4Args &a, int cw) {
+    if (a.epi == kW4Glu) return (a.part[0].strip_end + cw / 2 - 1) / (cw / 2);
+    int tiles = 0;
+    for (int i = 0; i < a.nparts; ++i) tiles += (a.part[i].strip_end - (i ? a.part[i - 1].strip_end : 0) + cw - 1) / cw;
+    return tiles;
+}
+
+template <int G, int NT> cudaError_t launch_kernel(const W4Args &a, const Stream4 &p, cudaStream_t stream) {
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t e = kv_allow_smem(stream4_kernel<G, NT>, kMaxSmem4, &allowed);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)tiles_of(a, p.cw), (unsigned)p.ks, 1);
+    cfg.blockDim = dim3(kThreads4, 1, 1);
+    cfg.dynamicSmemBytes = (size_t)smem_bytes(a, p);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (p.ks > 1) {
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = 1;
+        attr[1].val.clusterDim.y = (unsigned)p.ks;
+        attr[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
     }
+    return cudaLaunchKernelEx(&cfg, stream4_kernel<G, NT>, a, p);
 }
 
 }  // namespace
 
-cudaError_t launch_w4_stream(const W4Args &a, bool, cudaStream_t stream) {
-    const int strips = a.epi == kW4Glu ? a.part[0].strip_end : a.part[a.nparts - 1].strip_end;
-    simple_kernel<<<dim3((unsigned)(strips + 3) / 4, (unsigned)(a.m + kRows - 1) / kRows), 128, 0, stream>>>(a);
-    return cudaGetLastError();
+cudaError_t read_w4_fault(unsigned *out, bool clear) {
+    cudaError_t e = cudaMemcpyFromSymbol(out, g_w4_fault, sizeof(unsigned));
+    if (e != cudaSuccess || !clear) return e;
+    const unsigned zero = 0;
+    return cudaMemcpyToSymbol(g_w4_fault, &zero, sizeof(unsigned));
+}
+
+cudaError_t launch_w4_stream(const W4Args &a, bool constant_weights, cudaStream_t stream) {
+    int sms = 0;
+    cudaError_t e = sm_count_of_device(&sms);
+    if (e != cudaSuccess) return e;
+    Stream4 p = {a.m <= 8 ? 1 : 2, 4, 1, constant_weights};
+    if (a.epi == kW4Glu && p.cw < 2) p.cw = 2;
+    if (const char *v = getenv("W4_CW")) p.cw = atoi(v);
+    if (const char *v = getenv("W4_D")) p.depth = atoi(v);
+    const int tiles = tiles_of(a, p.cw), chunks = (a.K + kChunk - 1) / kChunk, kw = kWarps4 / p.cw;
+    while (p.ks < 8 && 2 * p.ks * tiles <= 2 * sms && 2 * p.ks * kw <= chunks) p.ks *= 2;
+    if (const char *v = getenv("W4_KS")) p.ks = atoi(v);
+    while (p.depth > 1 && smem_bytes(a, p) > kMaxSmem4 / 2 - 1024) --p.depth;
+    const bool wide = a.m > 8;
+    switch (a.group) {
+        case 32: return wide ? launch_kernel<32, 2>(a, p, stream) : launch_kernel<32, 1>(a, p, stream);
+        case 64: return wide ? launch_kernel<64, 2>(a, p, stream) : launch_kernel<64, 1>(a, p, stream);
+        default: return wide ? launch_kernel<128, 2>(a, p, stream) : launch_kernel<128, 1>(a, p, stream);
+    }
 }
 
 }  // namespace q8
