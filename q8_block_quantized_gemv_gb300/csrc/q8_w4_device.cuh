@@ -8,21 +8,24 @@
 
 namespace q8 {
 
-// Rows 8t + 2p and 8t + 2p + 1 of a word as the bf16 pair 128 + c: bf16's mantissa unit at 128 is 1, so the four bits go
-// under the exponent as they are.
-template <int P> __device__ __forceinline__ uint32_t w4_raised(uint32_t w) {
+// Rows 8t + 2P and 8t + 2P + 1 of a word as the exact bf16 pair (c - z) / 64.  The byte v under a zero exponent is the bf16
+// number v * 2^-133 (subnormals and the binade after them are one arithmetic progression), so four bits where they stand,
+// in the low or the high half of the byte, are c * 2^-133 or c * 2^-129: one packed fma times 2^127 or 2^123 less z / 64
+// is exact (|c - z| <= 127 has 7 bits).  Eight codes cost one shift, four ands and four fmas; putting each pair under the
+// exponent of 128 and subtracting takes three shifts.  `zero` holds -z / 64 twice.
+template <int P> __device__ __forceinline__ uint32_t w4_pair(uint32_t w, uint32_t zero) {
+    const uint32_t v = (P >= 2 ? w >> 8 : w) & (P & 1 ? 0x00F000F0u : 0x000F000Fu);
     uint32_t d;
-    asm("lop3.b32 %0, %1, 0x000F000F, 0x43004300, 0xEA;" : "=r"(d) : "r"(P ? w >> (4 * P) : w));
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(v), "r"(P & 1 ? 0x7D007D00u : 0x7F007F00u), "r"(zero));
     return d;
 }
-// ... less the pair 128 + z: c - z, exact (|c - z| <= 127 has at most 7 bits).
-template <int P> __device__ __forceinline__ uint32_t w4_pair(uint32_t w, uint32_t raised_zero) {
+constexpr float kW4Unit = 64.0f;            // what the products are short of
+constexpr uint32_t kW4Eight = 0xBE00BE00u;  // -8 / 64
+__device__ __forceinline__ uint32_t w4_zero(unsigned char z) {  // 2 - (128 + z) / 64
     uint32_t d;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(w4_raised<P>(w)), "r"(raised_zero));
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"((0x4300u | z) * 0x10001u), "r"(0xBC80BC80u), "r"(0x40004000u));
     return d;
 }
-constexpr uint32_t kRaisedEight = 0x43084308u;  // the pair 128 + 8
-__device__ __forceinline__ uint32_t w4_raised_zero(unsigned char z) { return (0x4300u | z) * 0x10001u; }
 
 // A scale's value: bf16 is the top half of an fp32.
 __device__ __forceinline__ float w4_scale(uint16_t s, int bf16) {
@@ -57,20 +60,15 @@ __device__ __forceinline__ bool w4_look(uint64_t *bar, unsigned parity) {
     return done != 0;
 }
 // Waits for the phase of the given parity, two seconds at most; false when that time ran out.
-__device__ __noinline__ bool w4_wait_long(uint64_t *bar, unsigned parity);
 __device__ __forceinline__ bool w4_wait(uint64_t *bar, unsigned parity) {
-    return w4_look(bar, parity) || w4_wait_long(bar, parity);
-}
-__device__ __noinline__ bool w4_wait_long(uint64_t *bar, unsigned parity) {
+    if (w4_look(bar, parity)) return true;
     uint64_t t0, t;
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
-    for (unsigned n = 1;; ++n) {
+    do {
         if (w4_look(bar, parity)) return true;
-        if ((n & 63u) == 0) {
-            asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-            if (t - t0 > 2000000000ull) return false;
-        }
-    }
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    } while (t - t0 < 2000000000ull);
+    return false;
 }
 
 }  // namespace q8

@@ -2,19 +2,20 @@
 // cores with exact bf16 operands.
 //
 // y[r, n] = sum_g s[g, n] * sum_{k in g} x[r, k] (c[k, n] - z[g, n]).  At 4.1 to 4.75 bits a weight the call is bound by the
-// bytes of the weight; what has to keep up with them is the conversion, 11 instructions for 8 codes (three shifts, four
-// ands-and-ors under a bf16 exponent, four packed subtracts), which is why each code is converted once for all rows.
+// bytes of the weight; what has to keep up with them is the conversion (w4_pair: 9 instructions for 8 codes), which is why
+// each code is converted once for all rows.
 //
-//   - A strip of 32 columns belongs to a warp, in chunks of 128 rows (one, two or four units, contiguous), fetched by one
-//     bulk copy each into the warp's own ring of shared memory.  Only the warp's lane 0 waits for nothing and asks for all
-//     of it: no other warp is involved.
+//   - A CTA's eight warps split K; the warps share nothing before the end.  A warp's work comes in stages of 128 rows of S
+//     strips of 32 columns (of a strip one, two or four units, contiguous) and those rows' activations, bulk copies into
+//     a ring of its own, one barrier a stage.
 //   - The weights are the MMA's A operand (m16n8k16: 16 columns of W), the activations B (8 rows).  The order of the
 //     reduction is free, so a lane's four k-pairs of two MMAs are the 8 rows of one stored word, and its activations 16
-//     consecutive bytes.  With the activations as A half of every MMA would be empty rows for m <= 8.
-//   - A group's sums start from zero and are folded with its scales into an fp32 carry; c - z and x are exact in bf16.
-//   - A CTA's eight warps are cw strips times kw runs of K; the kw warps of one run share its activations (a ring of their
-//     own, m bulk copies of 256 bytes a chunk).  The runs' carries are added in shared memory in order, then, where the
-//     strips are too few for the SMs and K is split over a cluster, those of its CTAs in rank order.
+//     consecutive bytes.  With the activations as A half of every MMA would be empty rows for m <= 8.  Rows past m are
+//     columns of B that nothing reads: they repeat the last row.
+//   - A group's sums start from zero and are folded with its scales into an fp32 carry; (c - z) / 64 and x are exact in bf16.
+//   - S strips share the activations' way from L2, which at m = 16 are as long as two strips' codes.
+//   - The warps' carries are added in shared memory in order, then, where the strips are too few for the SMs and K is split
+//     over a cluster, those of its CTAs in rank order.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -37,9 +38,8 @@ constexpr int kChunk = 128;              // rows of K in a stage
 constexpr int kXPitch4 = 2 * kChunk + 64;  // bytes between activation rows in a stage: 64 past a multiple of 128, so that
                                          // the 16-byte loads of two rows and four lanes fall on all banks
 struct Stream4 {
-    int cw;      // strips of a CTA (the gated pair: of both weights); 8 / cw runs of K
-    int depth;   // stages of a ring
-    int ks;      // CTAs of a cluster splitting K
+    int depth;  // stages of a ring
+    int ks;     // CTAs of a cluster splitting K
     int prefetch;
 };
 
@@ -66,182 +66,172 @@ __device__ __forceinline__ void block32(float (&d)[2][NT][4], const uint32_t (&w
     }
 }
 
-template <int G, int NT>
-__global__ void __launch_bounds__(kThreads4, 2) stream4_kernel(const __grid_constant__ W4Args a, const Stream4 p) {
+// S strips a warp: of one part, or half of them of the gate and half of the up projection.
+template <int G, int NT, int S>
+__global__ void __launch_bounds__(kThreads4, NT * S == 1 ? 4 : NT * S == 2 ? 3 : 2)
+    stream4_kernel(const __grid_constant__ W4Args a, const Stream4 p) {
     namespace cg = cooperative_groups;
     constexpr int CG = kChunk / G;  // groups of a chunk
     extern __shared__ __align__(128) unsigned char smem4[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int cw = p.cw, kw = kWarps4 / cw, depth = p.depth;
-    const int cwi = warp & (cw - 1), kwi = warp / cw;
-    const int stage = CG * a.unit, xstage = a.m * kXPitch4;
+    const int depth = p.depth;
+    const int chunk = CG * a.unit, stage = S * chunk + a.m * kXPitch4;
     unsigned char *ring = smem4 + warp * depth * stage;
-    unsigned char *xring = smem4 + kWarps4 * depth * stage + kwi * depth * xstage;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem4 + depth * (kWarps4 * stage + kw * xstage));
-    uint64_t *wfull = bars + warp * depth, *xfull = bars + (kWarps4 + kwi) * depth, *xempty = xfull + kw * depth;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem4 + kWarps4 * depth * stage) + warp * depth;
 
-    // the CTA's tile: cw strips of one part, or cw / 2 of the gate and of the up projection, in turn
+    // the CTA's tile: S strips of one part, or S / 2 of the gate and of the up projection
     const bool pair = a.epi == kW4Glu;
-    const int width = pair ? cw / 2 : cw;  // strips of output
+    const int width = pair ? S / 2 : S;  // strips of output
     int part = 0, tile = blockIdx.x;
     if (!pair)
         for (int first = 0, tiles;; ++part, tile -= tiles, first = a.part[part - 1].strip_end) {
-            tiles = (a.part[part].strip_end - first + cw - 1) / cw;
+            tiles = (a.part[part].strip_end - first + S - 1) / S;
             if (tile < tiles || part + 1 == a.nparts) break;
         }
-    const W4Part &mine = a.part[pair ? cwi & 1 : part];
-    const int strips = mine.Np / kW4Strip, strip = tile * width + (pair ? cwi >> 1 : cwi);
-    const int live = min(cw, (pair ? 2 : 1) * (strips - tile * width));  // warps of a run with a strip
+    const W4Part &to = a.part[part];
+    const int here = min(width, to.Np / kW4Strip - tile * width);  // strips that exist
 
     // the warp's run of chunks
-    const int groups = a.K / G, chunks = (groups + CG - 1) / CG, runs = kw * p.ks;
-    const int run = blockIdx.y * kw + kwi;
+    const int groups = a.K / G, chunks = (groups + CG - 1) / CG, runs = kWarps4 * p.ks;
+    const int run = blockIdx.y * kWarps4 + warp;
     const int c0 = (int)((long long)chunks * run / runs);
-    const int n = cwi < live ? (int)((long long)chunks * (run + 1) / runs) - c0 : 0;
-    const unsigned char *src = mine.w + ((size_t)strip * groups + (size_t)c0 * CG) * a.unit;
-    auto groups_of = [&](int i) { return min(CG, groups - (c0 + i) * CG); };
-    auto ask_w = [&](int i) {  // lane 0
-        const unsigned bytes = (unsigned)(groups_of(i) * a.unit);
-        uint64_t *bar = wfull + i % depth;
-        w4_arrive_tx(bar, bytes);
-        w4_copy(ring + (i % depth) * stage, src + (size_t)i * stage, bytes, bar);
+    const int n = (int)((long long)chunks * (run + 1) / runs) - c0;
+    const size_t strip_bytes = (size_t)groups * a.unit;
+    const size_t src = (size_t)tile * width * strip_bytes + (size_t)c0 * chunk;
+    auto groups_of = [&](int i) { return CG == 1 ? 1 : min(CG, groups - (c0 + i) * CG); };
+    // strip s of a stage is strip s of the tile, or s / 2 of the gate (even s) and of the up projection (odd)
+    auto ask_w = [&](int i, int slot) {  // lane 0: all bytes of the stage are announced, the weights' asked for
+        const int gr = groups_of(i);
+        const unsigned bytes = (unsigned)(gr * a.unit);
+        uint64_t *bar = full + slot;
+        w4_arrive_tx(bar, bytes * (pair ? 2 * here : here) + (unsigned)(gr * G * 2 * a.m));
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const int of = pair ? s >> 1 : s;
+            if (of < here)
+                w4_copy(ring + slot * stage + s * chunk,
+                        (pair && (s & 1) ? a.part[1].w : to.w) + src + of * strip_bytes + (size_t)i * chunk, bytes, bar);
+        }
     };
-    auto ask_x = [&](int i) {  // the run's first warp, all lanes
-        const unsigned bytes = (unsigned)(groups_of(i) * G * 2);
-        uint64_t *bar = xfull + i % depth;
-        if (lane == 0) w4_arrive_tx(bar, bytes * a.m);
-        __syncwarp();
+    auto ask_x = [&](int i, int slot) {  // lanes 0 .. m - 1, a row each
         if (lane < a.m)
-            w4_copy(xring + (i % depth) * xstage + lane * kXPitch4, a.x + (size_t)lane * a.K + (size_t)(c0 + i) * kChunk,
-                    bytes, bar);
+            w4_copy(ring + slot * stage + S * chunk + lane * kXPitch4,
+                    a.x + (size_t)lane * a.K + (size_t)(c0 + i) * kChunk, (unsigned)(groups_of(i) * G * 2), full + slot);
     };
 
     if (lane == 0) {
-        for (int s = 0; s < depth; ++s) {
-            w4_bar_init(wfull + s, 1);
-            if (cwi == 0) {
-                w4_bar_init(xfull + s, 1);
-                w4_bar_init(xempty + s, live);
-            }
-        }
+        for (int s = 0; s < depth; ++s) w4_bar_init(full + s, 1);
         w4_bar_fence();
         if (p.prefetch)
-            for (int i = 0; i < depth && i < n; ++i) ask_w(i);
+            for (int i = 0; i < depth && i < n; ++i) ask_w(i, i);
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (cwi == 0) {
-        __syncwarp();
-        for (int i = 0; i < depth && i < n; ++i) ask_x(i);
-    }
     if (lane == 0 && !p.prefetch)
-        for (int i = 0; i < depth && i < n; ++i) ask_w(i);
-    __syncthreads();
+        for (int i = 0; i < depth && i < n; ++i) ask_w(i, i);
+    __syncwarp();
+    for (int i = 0; i < depth && i < n; ++i) ask_x(i, i);
 
-    float acc[2][NT][4] = {};
-    bool xlive[NT];
+    float acc[S][2][NT][4] = {};
+    int xrow[NT];  // the lane's activation rows in a stage
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) xlive[nt] = 8 * nt + g < a.m;
-    bool ok = true;
-    int slot = 0, i = 0, asked = min(depth, n);  // chunks of x asked for
+    for (int nt = 0; nt < NT; ++nt) xrow[nt] = S * chunk + min(8 * nt + g, a.m - 1) * kXPitch4 + 16 * t;
+    int slot = 0, i = 0;
     unsigned phase = 0;
     for (; i < n; ++i) {
-        if (cwi == 0 && i > 0 && i - 1 + depth < n) {  // the place of the chunk before: all of the run are past it, or nearly
-            if (!(ok = __all_sync(0xffffffffu, w4_wait(xempty + (i - 1) % depth, ((i - 1) / depth) & 1)))) break;
-            ask_x(i - 1 + depth);
-            asked = i + depth;
-        }
-        if (!(ok = __all_sync(0xffffffffu, w4_wait(xfull + slot, phase) && w4_wait(wfull + slot, phase)))) break;
+        if (!__all_sync(0xffffffffu, w4_wait(full + slot, phase))) break;
         const unsigned char *st = ring + slot * stage;
-        const unsigned char *xs = xring + slot * xstage + g * kXPitch4 + 16 * t;
-        const int here = groups_of(i);
+        const int have = groups_of(i);
 #pragma unroll
         for (int q = 0; q < CG; ++q) {
-            if (CG > 1 && q >= here) break;
-            const unsigned char *u = st + q * a.unit;
-            uint32_t zero[2][2] = {{kRaisedEight, kRaisedEight}, {kRaisedEight, kRaisedEight}};
-            if (a.zeros) {
+            if (q >= have) break;
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+            for (int s = 0; s < S; ++s) {
+                const unsigned char *u = st + s * chunk + q * a.unit;
+                uint32_t zero[2][2] = {{kW4Eight, kW4Eight}, {kW4Eight, kW4Eight}};
+                if (a.zeros) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) zero[j][h] = w4_raised_zero(u[16 * G + 64 + 16 * j + 8 * h + g]);
-            }
-            float d[2][NT][4] = {};
+                    for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int b = 0; b < G / 32; b += 2) {
-                uint32_t w0[2][2], w1[2][2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    if (G == 32) {
-                        const uint2 v = *reinterpret_cast<const uint2 *>(u + 256 * j + 8 * lane);
-                        w0[j][0] = v.x, w0[j][1] = v.y;
-                    } else {
-                        const uint4 v = *reinterpret_cast<const uint4 *>(u + 512 * (b + j) + 16 * lane);
-                        w0[j][0] = v.x, w0[j][1] = v.y, w1[j][0] = v.z, w1[j][1] = v.w;
-                    }
+                        for (int h = 0; h < 2; ++h) zero[j][h] = w4_zero(u[16 * G + 64 + 16 * j + 8 * h + g]);
                 }
-                uint4 x0[NT], x1[NT];
+                float d[2][NT][4] = {};
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const unsigned char *row = xs + 8 * nt * kXPitch4 + 2 * (q * G + 32 * b);
-                    x0[nt] = x1[nt] = make_uint4(0u, 0u, 0u, 0u);
-                    if (xlive[nt]) {
+                for (int b = 0; b < G / 32; b += 2) {
+                    uint32_t w0[2][2], w1[2][2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        if (G == 32) {
+                            const uint2 v = *reinterpret_cast<const uint2 *>(u + 256 * j + 8 * lane);
+                            w0[j][0] = v.x, w0[j][1] = v.y;
+                        } else {
+                            const uint4 v = *reinterpret_cast<const uint4 *>(u + 512 * (b + j) + 16 * lane);
+                            w0[j][0] = v.x, w0[j][1] = v.y, w1[j][0] = v.z, w1[j][1] = v.w;
+                        }
+                    }
+                    uint4 x0[NT], x1[NT];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const unsigned char *row = st + xrow[nt] + 2 * (q * G + 32 * b);
                         x0[nt] = *reinterpret_cast<const uint4 *>(row);
                         if (G > 32) x1[nt] = *reinterpret_cast<const uint4 *>(row + 64);
                     }
+                    block32<NT>(d, w0, zero, x0);
+                    if (G > 32) block32<NT>(d, w1, zero, x1);
                 }
-                block32<NT>(d, w0, zero, x0);
-                if (G > 32) block32<NT>(d, w1, zero, x1);
-            }
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+                for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float s =
-                        w4_scale(*reinterpret_cast<const uint16_t *>(u + 16 * G + 2 * (16 * j + 8 * h + g)), a.bf16);
+                    for (int h = 0; h < 2; ++h) {
+                        const float f =
+                            w4_scale(*reinterpret_cast<const uint16_t *>(u + 16 * G + 2 * (16 * j + 8 * h + g)), a.bf16);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        acc[j][nt][2 * h] = fmaf(s, d[j][nt][2 * h], acc[j][nt][2 * h]);
-                        acc[j][nt][2 * h + 1] = fmaf(s, d[j][nt][2 * h + 1], acc[j][nt][2 * h + 1]);
+                        for (int nt = 0; nt < NT; ++nt) {
+                            acc[s][j][nt][2 * h] = fmaf(f, d[j][nt][2 * h], acc[s][j][nt][2 * h]);
+                            acc[s][j][nt][2 * h + 1] = fmaf(f, d[j][nt][2 * h + 1], acc[s][j][nt][2 * h + 1]);
+                        }
                     }
-                }
+            }
         }
         __syncwarp();
-        if (lane == 0) {
-            if (i + depth < n) ask_w(i + depth);
-            w4_arrive(xempty + slot);
+        if (i + depth < n) {
+            if (lane == 0) ask_w(i + depth, slot);
+            __syncwarp();
+            ask_x(i + depth, slot);
         }
         if (++slot == depth) {
             slot = 0;
             phase ^= 1;
         }
     }
-    if (!ok && lane == 0) {  // what was asked for lands (or two more seconds pass for each) before the memory is used again
+    if (i < n && lane == 0) {  // what was asked for lands (or two more seconds pass for each) before the memory is used again
         atomicOr(&g_w4_fault, kW4Fault);
-        for (int j = i; j < n && j < i + depth; ++j) w4_wait_long(wfull + j % depth, (j / depth) & 1);
-        if (cwi == 0)
-            for (int j = i; j < asked; ++j) w4_wait_long(xfull + j % depth, (j / depth) & 1);
+        for (int j = i; j < n && j < i + depth; ++j) w4_wait(full + j % depth, (j / depth) & 1);
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __syncthreads();
 
-    // carries [kw][m][pitch] (a pitch of 4 past a multiple of 32 spreads a fragment's rows over the banks), their sum
-    const int cols = 32 * cw, pitch = cols + 4, rows = a.m;
+    // carries [8][m][pitch] (a pitch of 4 past a multiple of 32 spreads a fragment's rows over the banks), their sum
+    constexpr int cols = 32 * S, pitch = cols + 4;
+    const int rows = a.m;
     float *red = reinterpret_cast<float *>(smem4);
-    float *sum = red + kw * rows * pitch;
+    float *sum = red + kWarps4 * rows * pitch;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int s = 0; s < S; ++s)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int r = 8 * nt + 2 * t + (e & 1);
-                if (r < rows) red[(kwi * rows + r) * pitch + 32 * cwi + 16 * j + 8 * (e >> 1) + g] = acc[j][nt][e];
-            }
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int r = 8 * nt + 2 * t + (e & 1);
+                    if (r < rows) red[(warp * rows + r) * pitch + 32 * s + 16 * j + 8 * (e >> 1) + g] = acc[s][j][nt][e];
+                }
     __syncthreads();
     for (int i = threadIdx.x; i < rows * (cols / 4); i += kThreads4) {
         const int r = i / (cols / 4), c = 4 * (i - r * (cols / 4));
-        float4 v = *reinterpret_cast<const float4 *>(red + r * pitch + c);
-        for (int k = 1; k < kw; ++k) {
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < kWarps4; ++k) {
             const float4 o = *reinterpret_cast<const float4 *>(red + (k * rows + r) * pitch + c);
             v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
         }
@@ -255,20 +245,25 @@ __global__ void __launch_bounds__(kThreads4, 2) stream4_kernel(const __grid_cons
 
     // a rank's share of the output's columns, four a thread
     const int share = 8 * width, k0 = share * (int)blockIdx.y / p.ks, k1 = share * ((int)blockIdx.y + 1) / p.ks;
-    const W4Part &to = a.part[part];
     for (int i = threadIdx.x; i < rows * (k1 - k0); i += kThreads4) {
         const int r = i / (k1 - k0), c = 4 * (k0 + i - r * (k1 - k0));
         const int out = tile * width * kW4Strip + c;
         if (out >= to.Np) continue;
-        auto total = [&](int at) {
-            return p.ks > 1 ? cluster_sum4(cluster, sum, at, 0, 1, p.ks) : *reinterpret_cast<const float4 *>(sum + at);
+        auto total = [&](int at, float (&v)[4]) {
+            float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
+            for (int k = 0; k < p.ks; ++k) {
+                const float4 o = *reinterpret_cast<const float4 *>(cluster.map_shared_rank(sum, k) + at);
+                f.x += o.x, f.y += o.y, f.z += o.z, f.w += o.w;
+            }
+            v[0] = kW4Unit * f.x, v[1] = kW4Unit * f.y, v[2] = kW4Unit * f.z, v[3] = kW4Unit * f.w;
         };
-        const float4 v4 = total(r * cols + (pair ? (c >> 5) * 64 + (c & 31) : c));
-        float v[4] = {v4.x, v4.y, v4.z, v4.w};
+        float v[4];
+        total(r * cols + (pair ? (c >> 5) * 64 + (c & 31) : c), v);
         const size_t at = (size_t)r * to.Np + out;
         if (pair) {
-            const float4 u4 = total(r * cols + (c >> 5) * 64 + 32 + (c & 31));
-            const float u[4] = {u4.x, u4.y, u4.z, u4.w};
+            float u[4];
+            total(r * cols + (c >> 5) * 64 + 32 + (c & 31), u);
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = v[e] / (1.0f + expf(-v[e])) * u[e];
         }
@@ -292,28 +287,27 @@ __global__ void __launch_bounds__(kThreads4, 2) stream4_kernel(const __grid_cons
 
 constexpr int kMaxSmem4 = 227 * 1024;
 
-int smem_bytes(const W4Args &a, const Stream4 &p) {
-    const int kw = kWarps4 / p.cw;
-    const int ring = p.depth * (kWarps4 * (kChunk / a.group) * a.unit + kw * a.m * kXPitch4 + (kWarps4 + 2 * kw) * 8);
-    const int ends = a.m * (kw * (32 * p.cw + 4) + 32 * p.cw) * 4;
+int smem_bytes(const W4Args &a, const Stream4 &p, int S) {
+    const int ring = kWarps4 * p.depth * (S * (kChunk / a.group) * a.unit + a.m * kXPitch4 + 8);
+    const int ends = a.m * (kWarps4 * (32 * S + 4) + 32 * S) * 4;
     return ring > ends ? ring : ends;
 }
 
-int tiles_of(const W4Args &a, int cw) {
-    if (a.epi == kW4Glu) return (a.part[0].strip_end + cw / 2 - 1) / (cw / 2);
+int tiles_of(const W4Args &a, int S) {
+    if (a.epi == kW4Glu) return (a.part[0].strip_end + S / 2 - 1) / (S / 2);
     int tiles = 0;
-    for (int i = 0; i < a.nparts; ++i) tiles += (a.part[i].strip_end - (i ? a.part[i - 1].strip_end : 0) + cw - 1) / cw;
+    for (int i = 0; i < a.nparts; ++i) tiles += (a.part[i].strip_end - (i ? a.part[i - 1].strip_end : 0) + S - 1) / S;
     return tiles;
 }
 
-template <int G, int NT> cudaError_t launch_kernel(const W4Args &a, const Stream4 &p, cudaStream_t stream) {
+template <int G, int NT, int S> cudaError_t launch_kernel(const W4Args &a, const Stream4 &p, cudaStream_t stream) {
     static std::atomic<uint64_t> allowed{0};
-    cudaError_t e = kv_allow_smem(stream4_kernel<G, NT>, kMaxSmem4, &allowed);
+    cudaError_t e = kv_allow_smem(stream4_kernel<G, NT, S>, kMaxSmem4, &allowed);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)tiles_of(a, p.cw), (unsigned)p.ks, 1);
+    cfg.gridDim = dim3((unsigned)tiles_of(a, S), (unsigned)p.ks, 1);
     cfg.blockDim = dim3(kThreads4, 1, 1);
-    cfg.dynamicSmemBytes = (size_t)smem_bytes(a, p);
+    cfg.dynamicSmemBytes = (size_t)smem_bytes(a, p, S);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -327,7 +321,12 @@ template <int G, int NT> cudaError_t launch_kernel(const W4Args &a, const Stream
         attr[1].val.clusterDim.z = 1;
         cfg.numAttrs = 2;
     }
-    return cudaLaunchKernelEx(&cfg, stream4_kernel<G, NT>, a, p);
+    return cudaLaunchKernelEx(&cfg, stream4_kernel<G, NT, S>, a, p);
+}
+
+template <int G> cudaError_t launch_group(const W4Args &a, const Stream4 &p, int S, cudaStream_t stream) {
+    if (a.m > 8) return S == 4 ? launch_kernel<G, 2, 4>(a, p, stream) : launch_kernel<G, 2, 2>(a, p, stream);
+    return S == 1 ? launch_kernel<G, 1, 1>(a, p, stream) : S == 2 ? launch_kernel<G, 1, 2>(a, p, stream) : launch_kernel<G, 1, 4>(a, p, stream);
 }
 
 }  // namespace
@@ -343,19 +342,19 @@ cudaError_t launch_w4_stream(const W4Args &a, bool constant_weights, cudaStream_
     int sms = 0;
     cudaError_t e = sm_count_of_device(&sms);
     if (e != cudaSuccess) return e;
-    Stream4 p = {a.m <= 8 ? 1 : 2, 4, 1, constant_weights};
-    if (a.epi == kW4Glu && p.cw < 2) p.cw = 2;
-    if (const char *v = getenv("W4_CW")) p.cw = atoi(v);
+    Stream4 p = {2, 1, constant_weights};
+    int S = a.m <= 4 ? 1 : a.m <= 8 ? 2 : 4;
+    if (a.epi == kW4Glu && S < 2) S = 2;
+    if (const char *v = getenv("W4_S")) S = atoi(v);
     if (const char *v = getenv("W4_D")) p.depth = atoi(v);
-    const int tiles = tiles_of(a, p.cw), chunks = (a.K + kChunk - 1) / kChunk, kw = kWarps4 / p.cw;
-    while (p.ks < 8 && 2 * p.ks * tiles <= 2 * sms && 2 * p.ks * kw <= chunks) p.ks *= 2;
+    const int tiles = tiles_of(a, S), chunks = (a.K + kChunk - 1) / kChunk;
+    while (p.ks < 8 && 2 * p.ks * tiles <= 2 * sms && 2 * p.ks * kWarps4 <= chunks) p.ks *= 2;
     if (const char *v = getenv("W4_KS")) p.ks = atoi(v);
-    while (p.depth > 1 && smem_bytes(a, p) > kMaxSmem4 / 2 - 1024) --p.depth;
-    const bool wide = a.m > 8;
+    while (p.depth > 1 && smem_bytes(a, p, S) > kMaxSmem4 - 1024) --p.depth;
     switch (a.group) {
-        case 32: return wide ? launch_kernel<32, 2>(a, p, stream) : launch_kernel<32, 1>(a, p, stream);
-        case 64: return wide ? launch_kernel<64, 2>(a, p, stream) : launch_kernel<64, 1>(a, p, stream);
-        default: return wide ? launch_kernel<128, 2>(a, p, stream) : launch_kernel<128, 1>(a, p, stream);
+        case 32: return launch_group<32>(a, p, S, stream);
+        case 64: return launch_group<64>(a, p, S, stream);
+        default: return launch_group<128>(a, p, S, stream);
     }
 }
 
