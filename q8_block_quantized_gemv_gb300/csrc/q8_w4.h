@@ -43,6 +43,7 @@ constexpr int kW4StreamRows = 16;  // most rows of a stream; more take the GEMM
 constexpr unsigned kW4Fault = 16u;  // bit of the fault word: a bounded wait ran out
 cudaError_t launch_w4_stream(const W4Args &a, bool constant_weights, cudaStream_t stream);  // q8_w4_stream.cu
 cudaError_t launch_w4_gemm(const W4Args &a, bool constant_weights, cudaStream_t stream);    // q8_w4_gemm.cu
-cudaError_t read_w4_fault(unsigned *out, bool clear);
+cudaError_t read_w4_fault(unsigned *out, bool clear);       // of both
+cudaError_t read_w4_gemm_fault(unsigned *out, bool clear);
 
 }  // namespace q8

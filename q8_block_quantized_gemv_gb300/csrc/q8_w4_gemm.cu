@@ -1,67 +1,550 @@
-// Products over 4-bit weights, first form: a warp computes one strip of 32 columns for eight rows, a lane a column, on the
-// CUDA cores.  Right for every size; neither reads the weight once for all rows nor fills the SMs.
+// Products of more than 16 rows over 4-bit weights on the 5th-generation tensor cores: one CTA computes 128 columns for up
+// to 256 rows over its range of K.
+//
+// The weights are the MMA's A operand (M = 128 columns of W), the activations B (N = up to 256 rows), so that one pass over
+// the weight and one conversion of it serve all rows of the tile, and each lane of the accumulator is one column: a group's
+// scale is one number for a thread that folds.  A group's sums (the codes less zero points and the activations exact in
+// bf16) go to a fresh accumulator in tensor memory and are folded with its scales into fp32 carries in registers.
+//
+// 16 warps, one CTA per SM, K in chunks of 128 rows and steps of 64:
+//   fold        warps 0-3 (FW = 1) or 0-7 (FW = 2): a thread reads its lane of a finished accumulator, times its column's
+//               scale (packed fp32x2), into at most 128 carries
+//   convert     the warps up to 11, in teams of four that take steps in turn: codes to bf16 in the 128-byte swizzle (two
+//               columns and two 32-row blocks a thread at a time; odd columns store their second block first, so that
+//               eight lanes' 16-byte stores fall on all banks)
+//   load        warp 12: units by bulk copies, activations by TMA (64 values x the tile's rows; rows past m are zeros)
+//   multiply    warp 13, converged, one lane elected for the instructions
+// FW = 1 where a thread's columns of both accumulators' rows are at most 128 in all (tiles of up to 128 rows; the gated
+// pair, which has two accumulators, up to 64); there the conversion is what bounds, and has eight warps for four.
+// Registers: the fold's 128 carries want 184 a thread; the others give theirs up (setmaxnreg; 512 x 128 in all).
+//
+// Where the tiles do not fill the SMs, K is split over a cluster, whose carries are added in rank order through shared
+// memory.  Every wait ends after two seconds: the CTA then stops, waits as long for what is in flight, and reports a fault.
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
+#include <stdlib.h>
 
-#include "q8_w4.h"
+#include <atomic>
+
+#include "q8_attn.h"
+#include "q8_launch.h"
+#include "q8_w4_device.cuh"
 
 namespace q8 {
 namespace {
 
-constexpr int kRows = 8;
+constexpr int kCols = 128;     // columns of W in a tile
+constexpr int kStepK = 64;     // rows of K in a step: 128 bytes of bf16
+constexpr int kChunkK = 128;   // rows of K in a raw stage
+constexpr int kThreadsG = 512;
+constexpr int kLoadWarpG = 12, kMmaWarpG = 13;
+constexpr int kOperand = kCols * kStepK * 2;  // 16 KB: one converted step of one weight
+constexpr int kMaxSmemG = 227 * 1024;
+constexpr int kMaxStages = 8, kMaxAcc = 4;
 
-__device__ __forceinline__ float scale_value(uint16_t s, int bf16) {
-    return bf16 ? __uint_as_float((uint32_t)s << 16) : __half2float(__ushort_as_half(s));
+__device__ unsigned int g_w4_gemm_fault = 0;
+
+struct Gemm4 {
+    int rows;    // of a tile, a multiple of 32 (FW = 2) or 16
+    int slots;   // stages of converted weights and activations
+    int raws;    // stages of units
+    int accs;    // accumulators
+    int ks;      // CTAs of a cluster splitting K
+    int prefetch;
+};
+
+struct Control {
+    uint64_t raw_full[kMaxStages], raw_empty[kMaxStages], x_full[kMaxStages], a_full[kMaxStages], slot_empty[kMaxStages];
+    uint64_t acc_full[kMaxAcc], acc_empty[kMaxAcc], drain;
+    uint32_t tmem;
+    int abort;
+};
+
+__device__ __forceinline__ bool wait(uint64_t *bar, unsigned parity, volatile int *abort) {
+    if (w4_look(bar, parity)) return true;
+    uint64_t t0, t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+    do {
+        if (w4_look(bar, parity)) return true;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    } while (!*abort && t - t0 < 2000000000ull);
+    if (!*abort) {
+        *abort = 1;
+        atomicOr(&g_w4_gemm_fault, kW4Fault);
+    }
+    return false;
+}
+// The same by a whole warp.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, unsigned parity, volatile int *abort) {
+    return __all_sync(0xffffffffu, wait(bar, parity, abort));
 }
 
-__device__ void product(const W4Args &a, const unsigned char *strip, int row0, int c, float (&acc)[kRows]) {
-    for (int r = 0; r < kRows; ++r) acc[r] = 0.0f;
-    for (int g = 0; g < a.K / a.group; ++g, strip += a.unit) {
-        const int zero = a.zeros ? strip[16 * a.group + 64 + c] : 8;
-        float part[kRows] = {};
-        for (int b = 0; b < a.group / 32; ++b)
-            for (int t = 0; t < 4; ++t) {
-                const uint32_t w = *reinterpret_cast<const uint32_t *>(strip + w4_word(a.group, b, t, c));
-                const uint16_t *x = a.x + (size_t)row0 * a.K + g * a.group + 32 * b + 8 * t;
-                for (int i = 0; i < 8; ++i) {
-                    const float v = (float)((int)((w >> (4 * (i >> 1) + 16 * (i & 1))) & 15u) - zero);
-                    for (int r = 0; r < kRows; ++r)
-                        if (row0 + r < a.m) part[r] = fmaf(__uint_as_float((uint32_t)x[(size_t)r * a.K + i] << 16), v, part[r]);
+__device__ __forceinline__ bool elect() {
+    uint32_t one;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(one));
+    return one != 0;
+}
+__device__ __forceinline__ void commit(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(w4_smem(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// Shared-memory descriptors of K-major operands in the 128-byte swizzle: rows of 128 bytes, groups of 8 rows 1024 bytes
+// apart (the high word), the address (the low one).
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr) { return ((addr & 0x3FFFFu) >> 4) | (1u << 16); }
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.b32 p, %4, 0;\n mov.b64 da, {%1, %5};\n"
+        " mov.b64 db, {%2, %5};\n tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t a, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(a));
+}
+__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tma_rows(void *dst, const CUtensorMap *map, int k, int row, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            w4_smem(dst)),
+        "l"(map), "r"(k), "r"(row), "r"(w4_smem(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ unsigned long long pack2(uint32_t lo, uint32_t hi) {
+    unsigned long long d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+    return d;
+}
+__device__ __forceinline__ void fma2(unsigned long long &d, unsigned long long a, unsigned long long b) {
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
+}
+__device__ __forceinline__ void unpack2(unsigned long long v, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+
+// Two columns (g and g + 8 of a 16-column tile) of rows 32 blk + 8t .. + 7 of a step, blk = first and then the other, as
+// they go into the operand: row n of 128 bytes, 16-byte chunk c at c ^ (n % 8).
+__device__ __forceinline__ void store8(unsigned char *row, int chunk, int g, uint32_t w, uint32_t zero) {
+    *reinterpret_cast<uint4 *>(row + ((chunk ^ g) << 4)) =
+        make_uint4(w4_pair<0>(w, zero), w4_pair<1>(w, zero), w4_pair<2>(w, zero), w4_pair<3>(w, zero));
+}
+
+template <int G, int P, int FW>
+__global__ void __launch_bounds__(kThreadsG, 1)
+    gemm4_kernel(const __grid_constant__ W4Args a, const Gemm4 p, const __grid_constant__ CUtensorMap xmap) {
+    namespace cg = cooperative_groups;
+    constexpr int CG = kChunkK / G;  // groups of a chunk
+    constexpr int kTeams = FW == 1 ? 2 : 1;
+    constexpr int kPerAcc = 8 / P;   // 16-row pieces of one accumulator that a folding thread holds at most
+    extern __shared__ __align__(1024) unsigned char smem_g[];
+    const int chunk_bytes = CG * a.unit, raw_bytes = P * 4 * chunk_bytes;
+    const int slot_bytes = P * kOperand + p.rows * 128;
+    unsigned char *slots = smem_g, *raws = smem_g + p.slots * slot_bytes;
+    Control &ctl = *reinterpret_cast<Control *>(raws + p.raws * raw_bytes);
+    volatile int *abort = &ctl.abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    // the tile: 128 columns of one part, or of the gate and of the up projection
+    int part = 0, tile = blockIdx.x;
+    if (P == 1)
+        for (int first = 0, tiles;; ++part, tile -= tiles, first = a.part[part - 1].strip_end) {
+            tiles = (a.part[part].strip_end - first + 3) / 4;
+            if (tile < tiles || part + 1 == a.nparts) break;
+        }
+    const W4Part &to = a.part[part];
+    const int strips = min(4, to.Np / kW4Strip - 4 * tile);  // that exist
+    const int row0 = blockIdx.y * p.rows;
+    const int groups = a.K / G, chunks = (groups + CG - 1) / CG;
+    const int c0 = (int)((long long)chunks * blockIdx.z / p.ks), c1 = (int)((long long)chunks * (blockIdx.z + 1) / p.ks);
+    const int rows_k = min(a.K, c1 * kChunkK) - c0 * kChunkK;  // of K in this CTA's range
+    const int n_chunks = c1 - c0, n_steps = (rows_k + kStepK - 1) / kStepK, n_groups = rows_k / G;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < p.raws; ++i) {
+            w4_bar_init(&ctl.raw_full[i], 1);
+            w4_bar_init(&ctl.raw_empty[i], 8 + 4 * FW);  // four converting warps for each of two steps, the folding warps
+        }
+        for (int i = 0; i < p.slots; ++i) {
+            w4_bar_init(&ctl.x_full[i], 1);
+            w4_bar_init(&ctl.a_full[i], 4);
+            w4_bar_init(&ctl.slot_empty[i], 1);
+        }
+        for (int i = 0; i < p.accs; ++i) {
+            w4_bar_init(&ctl.acc_full[i], 1);
+            w4_bar_init(&ctl.acc_empty[i], 4 * FW);
+        }
+        w4_bar_init(&ctl.drain, 1);
+        ctl.abort = 0;
+        w4_bar_fence();
+    }
+    if (warp == kMmaWarpG) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(w4_smem(&ctl.tmem)),
+                     "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = ctl.tmem;
+
+    // v: the product (and u: the up projection's) at (row, column n of the output)
+    auto finish = [&](int row, int n, float v, float u) {
+        const size_t at = (size_t)row * to.Np + n;
+        v *= kW4Unit;
+        if (P == 2) v = v / (1.0f + expf(-v)) * (kW4Unit * u);
+        if (a.epi == kW4Residual && n < to.N) v += a.res[at];
+        if (n >= to.N) v = 0.0f;
+        if (to.y) to.y[at] = v;
+        if (a.ybf) a.ybf[at] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+    };
+    const int half = p.rows / FW;  // rows of a folding thread
+    if (warp < 4 * FW) {
+        // ---- fold ----
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        unsigned long long acc[64];
+#pragma unroll
+        for (int i = 0; i < 64; ++i) acc[i] = 0ull;
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const int col0 = (warp >> 2) * half, pieces = half / 16;
+        int raw = 0, buf = 0;
+        unsigned raw_phase = 0, acc_phase = 0;
+        for (int gi = 0; gi < n_groups; ++gi) {
+            const int q = gi & (CG - 1);
+            if (q == 0 && !warp_wait(&ctl.raw_full[raw], raw_phase, abort)) break;
+            // strip 32 (warp % 4) of the tile is the warp's lanes
+            const unsigned char *u = raws + raw * raw_bytes + (warp & 3) * chunk_bytes + q * a.unit + 16 * G + 2 * lane;
+            unsigned long long s[P];
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const float f = w4_scale(*reinterpret_cast<const uint16_t *>(u + i * 4 * chunk_bytes), a.bf16);
+                s[i] = pack2(__float_as_uint(f), __float_as_uint(f));
+            }
+            if (!warp_wait(&ctl.acc_full[buf], acc_phase, abort)) break;
+            fence_after();
+            const uint32_t at = tmem + lanes + (uint32_t)(buf * P * p.rows + col0);
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+#pragma unroll
+                for (int c = 0; c < kPerAcc; c += 2)
+                    if (c < pieces) {
+                        uint32_t v0[16], v1[16];
+                        tmem_ld16(at + i * p.rows + 16 * c, v0);
+                        if (c + 1 < pieces) tmem_ld16(at + i * p.rows + 16 * c + 16, v1);
+                        tmem_wait();
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) fma2(acc[8 * (i * kPerAcc + c) + e], s[i], pack2(v0[2 * e], v0[2 * e + 1]));
+                        if (c + 1 < pieces) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                fma2(acc[8 * (i * kPerAcc + c + 1) + e], s[i], pack2(v1[2 * e], v1[2 * e + 1]));
+                        }
+                    }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                w4_arrive(&ctl.acc_empty[buf]);
+                if (q == CG - 1) w4_arrive(&ctl.raw_empty[raw]);
+            }
+            if (++buf == p.accs) buf = 0, acc_phase ^= 1;
+            if (q == CG - 1 && ++raw == p.raws) raw = 0, raw_phase ^= 1;
+        }
+        // The last group's sums are in: every MMA of the CTA is done, and with them every use of the slots.
+        if (p.ks == 1) {
+            const int n = tile * kCols + 32 * (warp & 3) + lane, first = row0 + (warp >> 2) * half;
+            if (n < to.Np && !*abort) {
+#pragma unroll
+                for (int c = 0; c < kPerAcc; ++c)
+                    if (16 * c < half) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            float v[2], u[2] = {0.0f, 0.0f};
+                            unpack2(acc[8 * c + e], v[0], v[1]);
+                            if (P == 2) unpack2(acc[8 * ((P - 1) * kPerAcc + c) + e], u[0], u[1]);
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                if (first + 16 * c + 2 * e + i < a.m) finish(first + 16 * c + 2 * e + i, n, v[i], u[i]);
+                        }
+                    }
+            }
+        } else if (!*abort) {
+            float *red = reinterpret_cast<float *>(smem_g);  // [P][rows][128]
+            const int n = 32 * (warp & 3) + lane, first = (warp >> 2) * half;
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+#pragma unroll
+                for (int c = 0; c < kPerAcc; ++c)
+                    if (16 * c < half) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            float v[2];
+                            unpack2(acc[8 * (i * kPerAcc + c) + e], v[0], v[1]);
+                            red[(i * p.rows + first + 16 * c + 2 * e) * kCols + n] = v[0];
+                            red[(i * p.rows + first + 16 * c + 2 * e + 1) * kCols + n] = v[1];
+                        }
+                    }
+        }
+    } else {
+        if (FW == 1)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        else
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp < kLoadWarpG) {
+            // ---- convert ----
+            const int team = (warp - 4 * FW) >> 2, strip = warp & 3, g = lane >> 2, t = lane & 3, odd = g & 1;
+            bool ok = true;
+            for (int j = team; j < n_steps; j += kTeams) {
+                const int i = j >> 1, raw = i % p.raws, slot = j % p.slots;
+                if (!(ok = warp_wait(&ctl.raw_full[raw], (i / p.raws) & 1, abort))) break;
+                if (j >= p.slots && !(ok = warp_wait(&ctl.slot_empty[slot], ((j / p.slots) - 1) & 1, abort))) break;
+#pragma unroll
+                for (int pp = 0; pp < P; ++pp) {
+                    const unsigned char *from = raws + raw * raw_bytes + (4 * pp + strip) * chunk_bytes;
+                    unsigned char *operand = slots + slot * slot_bytes + pp * kOperand + strip * 32 * 128 + g * 128;
+                    // the step's units: half of one, one, or two
+                    const unsigned char *u0 = from + (G == 128 ? 1024 * (j & 1) : G == 64 ? (j & 1) * a.unit : 2 * (j & 1) * a.unit);
+                    uint32_t zero[2][2][2];  // [block][tile][h]
+                    const unsigned char *z = (G == 128 ? from : u0) + 16 * G + 64 + g;
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int jj = 0; jj < 2; ++jj)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                zero[b][jj][h] = !a.zeros         ? kW4Eight
+                                                 : G > 32 && b == 1 ? zero[0][jj][h]
+                                                                    : w4_zero(z[b * a.unit + 16 * jj + 8 * h]);
+#pragma unroll
+                    for (int jj = 0; jj < 2; ++jj) {
+                        uint4 w;
+                        if (G == 32) {
+                            const uint2 lo = *reinterpret_cast<const uint2 *>(u0 + 256 * jj + 8 * lane);
+                            const uint2 hi = *reinterpret_cast<const uint2 *>(u0 + a.unit + 256 * jj + 8 * lane);
+                            w = make_uint4(lo.x, lo.y, hi.x, hi.y);
+                        } else {
+                            w = *reinterpret_cast<const uint4 *>(u0 + 512 * jj + 16 * lane);
+                        }
+                        const int first = odd ? 4 + t : t, second = first ^ 4;
+                        unsigned char *row = operand + 16 * jj * 128;
+                        store8(row, first, g, odd ? w.z : w.x, odd ? zero[1][jj][0] : zero[0][jj][0]);
+                        store8(row, second, g, odd ? w.x : w.z, odd ? zero[0][jj][0] : zero[1][jj][0]);
+                        store8(row + 8 * 128, first, g, odd ? w.w : w.y, odd ? zero[1][jj][1] : zero[0][jj][1]);
+                        store8(row + 8 * 128, second, g, odd ? w.y : w.w, odd ? zero[0][jj][1] : zero[1][jj][1]);
+                    }
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) {
+                    w4_arrive(&ctl.a_full[slot]);
+                    w4_arrive(&ctl.raw_empty[raw]);
                 }
             }
-        const float s = scale_value(*reinterpret_cast<const uint16_t *>(strip + 16 * a.group + 2 * c), a.bf16);
-        for (int r = 0; r < kRows; ++r) acc[r] = fmaf(s, part[r], acc[r]);
+        } else if (warp == kLoadWarpG) {
+            // ---- load (one lane) ----
+            if (lane == 0) {
+                const size_t strip_bytes = (size_t)groups * a.unit;
+                const unsigned char *src[P];
+#pragma unroll
+                for (int i = 0; i < P; ++i)
+                    src[i] = (i ? a.part[1].w : to.w) + (size_t)4 * tile * strip_bytes + (size_t)c0 * chunk_bytes;
+                auto ask_raw = [&](int i) {
+                    const int raw = i % p.raws;
+                    const unsigned bytes = (unsigned)(min(CG, groups - (c0 + i) * CG) * a.unit);
+                    w4_arrive_tx(&ctl.raw_full[raw], bytes * (unsigned)(P * strips));
+#pragma unroll
+                    for (int pp = 0; pp < P; ++pp)
+                        for (int s = 0; s < strips; ++s)
+                            w4_copy(raws + raw * raw_bytes + (4 * pp + s) * chunk_bytes,
+                                    src[pp] + s * strip_bytes + (size_t)i * chunk_bytes, bytes, &ctl.raw_full[raw]);
+                };
+                int asked = 0;  // chunks
+                if (p.prefetch)
+                    for (; asked < n_chunks && asked < p.raws; ++asked) ask_raw(asked);
+                asm volatile("griddepcontrol.wait;" ::: "memory");
+                bool ok = true;
+                int j = 0;
+                for (; j < n_steps && ok; ++j) {
+                    // units as far ahead as there is room, at every step
+                    while (asked < n_chunks && asked <= (j >> 1) + p.raws - 1) {
+                        if (asked >= p.raws && !(ok = wait(&ctl.raw_empty[asked % p.raws], ((asked / p.raws) - 1) & 1, abort)))
+                            break;
+                        ask_raw(asked++);
+                    }
+                    if (!ok) break;
+                    const int slot = j % p.slots;
+                    if (j >= p.slots && !(ok = wait(&ctl.slot_empty[slot], ((j / p.slots) - 1) & 1, abort))) break;
+                    w4_arrive_tx(&ctl.x_full[slot], (unsigned)p.rows * 128);
+                    tma_rows(slots + slot * slot_bytes + P * kOperand, &xmap, c0 * kChunkK + j * kStepK, row0,
+                             &ctl.x_full[slot]);
+                }
+                if (*abort) {  // what was asked for lands before the memory is used again
+                    for (int i = max(0, asked - p.raws); i < asked; ++i) w4_wait(&ctl.raw_full[i % p.raws], (i / p.raws) & 1);
+                    for (int i = max(0, j - p.slots); i < j; ++i) w4_wait(&ctl.x_full[i % p.slots], (i / p.slots) & 1);
+                }
+            }
+            __syncwarp();
+        } else if (warp == kMmaWarpG) {
+            // ---- multiply ----
+            const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(p.rows >> 3) << 17) |
+                                   ((uint32_t)(kCols >> 4) << 24);
+            int slot = 0, buf = 0;
+            unsigned slot_phase = 0, acc_phase = 1;  // a fresh barrier passes for the phase before its first
+            for (int j = 0; j < n_steps; ++j) {
+                if (!warp_wait(&ctl.x_full[slot], slot_phase, abort) || !warp_wait(&ctl.a_full[slot], slot_phase, abort)) break;
+                const int ksteps = min(4, (rows_k - j * kStepK) / 16);
+                const uint32_t base = desc_low(w4_smem(slots + slot * slot_bytes));
+                bool ok = true;
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const int in_group = (4 * (j & 1) + s) & (G / 16 - 1);
+                    if (s >= ksteps) break;
+                    if (in_group == 0 && !(ok = warp_wait(&ctl.acc_empty[buf], acc_phase, abort))) break;
+                    fence_after();
+                    if (elect()) {
+#pragma unroll
+                        for (int i = 0; i < P; ++i)
+                            mma(tmem + (uint32_t)((buf * P + i) * p.rows), base + ((i * kOperand + 32 * s) >> 4),
+                                base + ((P * kOperand + 32 * s) >> 4), idesc, in_group > 0);
+                        if (in_group == G / 16 - 1) commit(&ctl.acc_full[buf]);
+                    }
+                    __syncwarp();
+                    if (in_group == G / 16 - 1 && ++buf == p.accs) buf = 0, acc_phase ^= 1;
+                }
+                if (!ok) break;
+                if (elect()) commit(&ctl.slot_empty[slot]);
+                __syncwarp();
+                if (++slot == p.slots) slot = 0, slot_phase ^= 1;
+            }
+        }
+        asm volatile("griddepcontrol.wait;" ::: "memory");
     }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    // All MMAs are done (the last group's commit was waited for) and all copies have landed, unless the CTA stopped.
+    fence_before();
+    __syncthreads();
+    if (*abort && warp == kMmaWarpG) {
+        if (elect()) commit(&ctl.drain);
+        w4_wait(&ctl.drain, 0);
+    }
+    __syncthreads();
+    fence_after();
+
+    if (p.ks > 1) {  // a rank's share of the tile's rows, the ranks' carries added in order
+        const float *red = reinterpret_cast<float *>(smem_g);
+        cg::cluster_group cluster = cg::this_cluster();
+        cluster.sync();
+        const int live = min(p.rows, a.m - row0);
+        const int r0 = live * (int)blockIdx.z / p.ks, r1 = live * ((int)blockIdx.z + 1) / p.ks;
+        for (int i = threadIdx.x; i < (r1 - r0) * kCols; i += kThreadsG) {
+            const int r = r0 + i / kCols, c = i % kCols, n = tile * kCols + c;
+            if (n < to.Np && !*abort) {
+                float v = 0.0f, u = 0.0f;
+#pragma unroll 4
+                for (int k = 0; k < p.ks; ++k) v += cluster.map_shared_rank(red, k)[r * kCols + c];
+                if (P == 2) {
+#pragma unroll 4
+                    for (int k = 0; k < p.ks; ++k) u += cluster.map_shared_rank(red, k)[(p.rows + r) * kCols + c];
+                }
+                finish(row0 + r, n, v, u);
+            }
+        }
+        cluster_sync_after_reads();
+    }
+    if (warp == kMmaWarpG)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
 
-__global__ void __launch_bounds__(128) simple_kernel(const __grid_constant__ W4Args a) {
-    const int c = threadIdx.x & 31, strips = a.epi == kW4Glu ? a.part[0].strip_end : a.part[a.nparts - 1].strip_end;
-    const int strip = blockIdx.x * 4 + (threadIdx.x >> 5), row0 = blockIdx.y * kRows;
-    if (strip >= strips) return;
-    int p = 0;
-    while (strip >= a.part[p].strip_end) ++p;
-    const int local = strip - (p ? a.part[p - 1].strip_end : 0), n = local * kW4Strip + c;
-    const size_t at = (size_t)local * (a.K / a.group) * a.unit;
-    float acc[kRows], up[kRows];
-    product(a, a.part[p].w + at, row0, c, acc);
-    if (a.epi == kW4Glu) product(a, a.part[1].w + at, row0, c, up);
-    for (int r = 0; r < kRows && row0 + r < a.m; ++r) {
-        const size_t to = (size_t)(row0 + r) * a.part[p].Np + n;
-        float v = acc[r];
-        if (a.epi == kW4Glu) v = v / (1.0f + expf(-v)) * up[r];
-        if (a.epi == kW4Residual && n < a.part[p].N) v += a.res[to];
-        if (n >= a.part[p].N) v = 0.0f;
-        if (a.part[p].y) a.part[p].y[to] = v;
-        if (a.ybf) a.ybf[to] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+template <int G, int P, int FW>
+cudaError_t launch_kernel(const W4Args &a, const Gemm4 &p, int tiles, int smem, const CUtensorMap &map, cudaStream_t stream) {
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t e = kv_allow_smem(gemm4_kernel<G, P, FW>, kMaxSmemG, &allowed);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)tiles, (unsigned)((a.m + p.rows - 1) / p.rows), (unsigned)p.ks);
+    cfg.blockDim = dim3(kThreadsG, 1, 1);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (p.ks > 1) {
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = 1;
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = (unsigned)p.ks;
+        cfg.numAttrs = 2;
     }
+    return cudaLaunchKernelEx(&cfg, gemm4_kernel<G, P, FW>, a, p, map);
+}
+
+template <int G>
+cudaError_t launch_group(const W4Args &a, const Gemm4 &p, int fw, int tiles, int smem, const CUtensorMap &map,
+                         cudaStream_t stream) {
+    if (a.epi == kW4Glu)
+        return fw == 1 ? launch_kernel<G, 2, 1>(a, p, tiles, smem, map, stream)
+                       : launch_kernel<G, 2, 2>(a, p, tiles, smem, map, stream);
+    return fw == 1 ? launch_kernel<G, 1, 1>(a, p, tiles, smem, map, stream)
+                   : launch_kernel<G, 1, 2>(a, p, tiles, smem, map, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_w4_gemm(const W4Args &a, bool, cudaStream_t stream) {
-    const int strips = a.epi == kW4Glu ? a.part[0].strip_end : a.part[a.nparts - 1].strip_end;
-    simple_kernel<<<dim3((unsigned)(strips + 3) / 4, (unsigned)(a.m + kRows - 1) / kRows), 128, 0, stream>>>(a);
-    return cudaGetLastError();
+cudaError_t read_w4_gemm_fault(unsigned *out, bool clear) {
+    cudaError_t e = cudaMemcpyFromSymbol(out, g_w4_gemm_fault, sizeof(unsigned));
+    if (e != cudaSuccess || !clear) return e;
+    const unsigned zero = 0;
+    return cudaMemcpyToSymbol(g_w4_gemm_fault, &zero, sizeof(unsigned));
+}
+
+cudaError_t launch_w4_gemm(const W4Args &a, bool constant_weights, cudaStream_t stream) {
+    int sms = 0;
+    cudaError_t e = sm_count_of_device(&sms);
+    if (e != cudaSuccess) return e;
+    const int P = a.epi == kW4Glu ? 2 : 1, most = 256 / P;
+    Gemm4 p = {};
+    p.prefetch = constant_weights;
+    const int row_tiles = (a.m + most - 1) / most;
+    p.rows = ((a.m + row_tiles - 1) / row_tiles + 31) / 32 * 32;
+    const int fw = P * p.rows <= 128 ? 1 : 2;
+    int tiles = 0;
+    for (int i = 0; i < (P == 2 ? 1 : a.nparts); ++i)
+        tiles += (a.part[i].strip_end - (i ? a.part[i - 1].strip_end : 0) + 3) / 4;
+    const int chunks = (a.K + kChunkK - 1) / kChunkK, ctas = tiles * ((a.m + p.rows - 1) / p.rows);
+    double best = 1e300;
+    for (int k = 1; k <= 8 && k <= chunks; k *= 2) {
+        const double cost = (double)((ctas * k + sms - 1) / sms) * (8.0 + (double)((chunks + k - 1) / k));
+        if (cost < best - 1e-9) best = cost, p.ks = k;
+    }
+    if (const char *v = getenv("W4_GKS")) p.ks = atoi(v);
+    p.accs = 512 / (P * p.rows) < kMaxAcc ? 512 / (P * p.rows) : kMaxAcc;
+    const int raw = P * 4 * (kChunkK / a.group) * a.unit, slot = P * kOperand + p.rows * 128;
+    const int room = kMaxSmemG - (int)sizeof(Control);
+    p.raws = 3;
+    p.slots = (room - p.raws * raw) / slot;
+    if (p.slots > kMaxStages) p.slots = kMaxStages;
+    p.raws = (room - p.slots * slot) / raw;
+    if (p.raws > kMaxStages) p.raws = kMaxStages;
+    const int smem = p.slots * slot + p.raws * raw + (int)sizeof(Control);
+    CUtensorMap map;
+    if (!encode_bf16_rows(&map, a.x, a.m, a.K, kStepK, p.rows)) return cudaErrorNotSupported;
+    switch (a.group) {
+        case 32: return launch_group<32>(a, p, fw, tiles, smem, map, stream);
+        case 64: return launch_group<64>(a, p, fw, tiles, smem, map, stream);
+        default: return launch_group<128>(a, p, fw, tiles, smem, map, stream);
+    }
 }
 
 }  // namespace q8

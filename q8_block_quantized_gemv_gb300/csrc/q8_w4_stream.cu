@@ -332,7 +332,10 @@ template <int G> cudaError_t launch_group(const W4Args &a, const Stream4 &p, int
 }  // namespace
 
 cudaError_t read_w4_fault(unsigned *out, bool clear) {
-    cudaError_t e = cudaMemcpyFromSymbol(out, g_w4_fault, sizeof(unsigned));
+    unsigned gemm = 0;
+    cudaError_t e = read_w4_gemm_fault(&gemm, clear);
+    if (e == cudaSuccess) e = cudaMemcpyFromSymbol(out, g_w4_fault, sizeof(unsigned));
+    *out |= gemm;
     if (e != cudaSuccess || !clear) return e;
     const unsigned zero = 0;
     return cudaMemcpyToSymbol(g_w4_fault, &zero, sizeof(unsigned));
