@@ -12,7 +12,8 @@
 //   convert     the warps up to 11, in teams of four that take steps in turn: codes to bf16 in the 128-byte swizzle (two
 //               columns and two 32-row blocks a thread at a time; odd columns store their second block first, so that
 //               eight lanes' 16-byte stores fall on all banks)
-//   load        warp 12: units by bulk copies, activations by TMA (64 values x the tile's rows; rows past m are zeros)
+//   load        warp 12: units by bulk copies; warp 14: activations by TMA (64 values x the tile's rows; rows past m are
+//               zeros).  One warp for both kept the activations of a chunk behind the fold of the one before.
 //   multiply    warp 13, converged, one lane elected for the instructions
 // FW = 1 where a thread's columns of both accumulators' rows are at most 128 in all (tiles of up to 128 rows; the gated
 // pair, which has two accumulators, up to 64); there the conversion is what bounds, and has eight warps for four.
@@ -37,16 +38,18 @@ constexpr int kCols = 128;     // columns of W in a tile
 constexpr int kStepK = 64;     // rows of K in a step: 128 bytes of bf16
 constexpr int kChunkK = 128;   // rows of K in a raw stage
 constexpr int kThreadsG = 512;
-constexpr int kLoadWarpG = 12, kMmaWarpG = 13;
+constexpr int kLoadWarpG = 12, kMmaWarpG = 13, kXWarpG = 14;
 constexpr int kOperand = kCols * kStepK * 2;  // 16 KB: one converted step of one weight
 constexpr int kMaxSmemG = 227 * 1024;
 constexpr int kMaxStages = 8, kMaxAcc = 4;
+constexpr int kScaleStages = 4;  // chunks
 
 __device__ unsigned int g_w4_gemm_fault = 0;
 
 struct Gemm4 {
     int rows;    // of a tile, a multiple of 32 (FW = 2) or 16
-    int slots;   // stages of converted weights and activations
+    int ops;     // stages of converted weights
+    int xs;      // stages of activations
     int raws;    // stages of units
     int accs;    // accumulators
     int ks;      // CTAs of a cluster splitting K
@@ -54,7 +57,8 @@ struct Gemm4 {
 };
 
 struct Control {
-    uint64_t raw_full[kMaxStages], raw_empty[kMaxStages], x_full[kMaxStages], a_full[kMaxStages], slot_empty[kMaxStages];
+    uint64_t raw_full[kMaxStages], raw_empty[kMaxStages], x_full[kMaxStages], x_empty[kMaxStages];
+    uint64_t a_full[kMaxStages], a_empty[kMaxStages], s_full[kScaleStages], s_empty[kScaleStages];
     uint64_t acc_full[kMaxAcc], acc_empty[kMaxAcc], drain;
     uint32_t tmem;
     int abort;
@@ -147,9 +151,10 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     constexpr int kPerAcc = 8 / P;   // 16-row pieces of one accumulator that a folding thread holds at most
     extern __shared__ __align__(1024) unsigned char smem_g[];
     const int chunk_bytes = CG * a.unit, raw_bytes = P * 4 * chunk_bytes;
-    const int slot_bytes = P * kOperand + p.rows * 128;
-    unsigned char *slots = smem_g, *raws = smem_g + p.slots * slot_bytes;
-    Control &ctl = *reinterpret_cast<Control *>(raws + p.raws * raw_bytes);
+    const int x_bytes = p.rows * 128;
+    unsigned char *ops = smem_g, *xs = ops + p.ops * P * kOperand, *raws = xs + p.xs * x_bytes;
+    unsigned char *scales = raws + p.raws * raw_bytes;  // [stage][P][4 strips][CG][32] of 16 bits
+    Control &ctl = *reinterpret_cast<Control *>(scales + kScaleStages * P * 4 * CG * 64);
     volatile int *abort = &ctl.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -171,12 +176,19 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < p.raws; ++i) {
             w4_bar_init(&ctl.raw_full[i], 1);
-            w4_bar_init(&ctl.raw_empty[i], 8 + 4 * FW);  // four converting warps for each of two steps, the folding warps
+            w4_bar_init(&ctl.raw_empty[i], 8);  // four converting warps for each of two steps
         }
-        for (int i = 0; i < p.slots; ++i) {
+        for (int i = 0; i < kScaleStages; ++i) {
+            w4_bar_init(&ctl.s_full[i], 1);
+            w4_bar_init(&ctl.s_empty[i], 4 * FW);
+        }
+        for (int i = 0; i < p.xs; ++i) {
             w4_bar_init(&ctl.x_full[i], 1);
+            w4_bar_init(&ctl.x_empty[i], 1);
+        }
+        for (int i = 0; i < p.ops; ++i) {
             w4_bar_init(&ctl.a_full[i], 4);
-            w4_bar_init(&ctl.slot_empty[i], 1);
+            w4_bar_init(&ctl.a_empty[i], 1);
         }
         for (int i = 0; i < p.accs; ++i) {
             w4_bar_init(&ctl.acc_full[i], 1);
@@ -197,16 +209,6 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     fence_after();
     const uint32_t tmem = ctl.tmem;
 
-    // v: the product (and u: the up projection's) at (row, column n of the output)
-    auto finish = [&](int row, int n, float v, float u) {
-        const size_t at = (size_t)row * to.Np + n;
-        v *= kW4Unit;
-        if (P == 2) v = v / (1.0f + expf(-v)) * (kW4Unit * u);
-        if (a.epi == kW4Residual && n < to.N) v += a.res[at];
-        if (n >= to.N) v = 0.0f;
-        if (to.y) to.y[at] = v;
-        if (a.ybf) a.ybf[at] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
-    };
     const int half = p.rows / FW;  // rows of a folding thread
     if (warp < 4 * FW) {
         // ---- fold ----
@@ -217,17 +219,17 @@ __global__ void __launch_bounds__(kThreadsG, 1)
         for (int i = 0; i < 64; ++i) acc[i] = 0ull;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const int col0 = (warp >> 2) * half, pieces = half / 16;
-        int raw = 0, buf = 0;
-        unsigned raw_phase = 0, acc_phase = 0;
+        int st = 0, buf = 0;
+        unsigned s_phase = 0, acc_phase = 0;
         for (int gi = 0; gi < n_groups; ++gi) {
             const int q = gi & (CG - 1);
-            if (q == 0 && !warp_wait(&ctl.raw_full[raw], raw_phase, abort)) break;
-            // strip 32 (warp % 4) of the tile is the warp's lanes
-            const unsigned char *u = raws + raw * raw_bytes + (warp & 3) * chunk_bytes + q * a.unit + 16 * G + 2 * lane;
+            if (q == 0 && !warp_wait(&ctl.s_full[st], s_phase, abort)) break;
+            // strip (warp % 4) of the tile is the warp's lanes
+            const unsigned char *u = scales + (((st * P * 4 + (warp & 3)) * CG + q) * 32 + lane) * 2;
             unsigned long long s[P];
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-                const float f = w4_scale(*reinterpret_cast<const uint16_t *>(u + i * 4 * chunk_bytes), a.bf16);
+                const float f = w4_scale(*reinterpret_cast<const uint16_t *>(u + i * 4 * CG * 64), a.bf16);
                 s[i] = pack2(__float_as_uint(f), __float_as_uint(f));
             }
             if (!warp_wait(&ctl.acc_full[buf], acc_phase, abort)) break;
@@ -254,46 +256,30 @@ __global__ void __launch_bounds__(kThreadsG, 1)
             __syncwarp();
             if (lane == 0) {
                 w4_arrive(&ctl.acc_empty[buf]);
-                if (q == CG - 1) w4_arrive(&ctl.raw_empty[raw]);
+                if (q == CG - 1) w4_arrive(&ctl.s_empty[st]);
             }
             if (++buf == p.accs) buf = 0, acc_phase ^= 1;
-            if (q == CG - 1 && ++raw == p.raws) raw = 0, raw_phase ^= 1;
+            if (q == CG - 1 && ++st == kScaleStages) st = 0, s_phase ^= 1;
         }
-        // The last group's sums are in: every MMA of the CTA is done, and with them every use of the slots.
-        if (p.ks == 1) {
-            const int n = tile * kCols + 32 * (warp & 3) + lane, first = row0 + (warp >> 2) * half;
-            if (n < to.Np && !*abort) {
+        // The last group's sums are in: every MMA of the CTA is done, and with them every use of the operands, where the
+        // carries go now, [P][rows][128].  Straight from registers to the output, a store and a residual's load at a time,
+        // the same took 25 us for 256 rows.
+        float *red = reinterpret_cast<float *>(smem_g);
+        const int n = 32 * (warp & 3) + lane, first = (warp >> 2) * half;
 #pragma unroll
-                for (int c = 0; c < kPerAcc; ++c)
-                    if (16 * c < half) {
+        for (int i = 0; i < P; ++i)
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            float v[2], u[2] = {0.0f, 0.0f};
-                            unpack2(acc[8 * c + e], v[0], v[1]);
-                            if (P == 2) unpack2(acc[8 * ((P - 1) * kPerAcc + c) + e], u[0], u[1]);
+            for (int c = 0; c < kPerAcc; ++c)
+                if (16 * c < half) {
+                    float *to = red + (i * p.rows + first + 16 * c) * kCols + n;
 #pragma unroll
-                            for (int i = 0; i < 2; ++i)
-                                if (first + 16 * c + 2 * e + i < a.m) finish(first + 16 * c + 2 * e + i, n, v[i], u[i]);
-                        }
+                    for (int e = 0; e < 8; ++e) {
+                        float v[2];
+                        unpack2(acc[8 * (i * kPerAcc + c) + e], v[0], v[1]);
+                        to[2 * e * kCols] = v[0];
+                        to[(2 * e + 1) * kCols] = v[1];
                     }
-            }
-        } else if (!*abort) {
-            float *red = reinterpret_cast<float *>(smem_g);  // [P][rows][128]
-            const int n = 32 * (warp & 3) + lane, first = (warp >> 2) * half;
-#pragma unroll
-            for (int i = 0; i < P; ++i)
-#pragma unroll
-                for (int c = 0; c < kPerAcc; ++c)
-                    if (16 * c < half) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            float v[2];
-                            unpack2(acc[8 * (i * kPerAcc + c) + e], v[0], v[1]);
-                            red[(i * p.rows + first + 16 * c + 2 * e) * kCols + n] = v[0];
-                            red[(i * p.rows + first + 16 * c + 2 * e + 1) * kCols + n] = v[1];
-                        }
-                    }
-        }
+                }
     } else {
         if (FW == 1)
             asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
@@ -304,13 +290,13 @@ __global__ void __launch_bounds__(kThreadsG, 1)
             const int team = (warp - 4 * FW) >> 2, strip = warp & 3, g = lane >> 2, t = lane & 3, odd = g & 1;
             bool ok = true;
             for (int j = team; j < n_steps; j += kTeams) {
-                const int i = j >> 1, raw = i % p.raws, slot = j % p.slots;
+                const int i = j >> 1, raw = i % p.raws, op = j % p.ops;
                 if (!(ok = warp_wait(&ctl.raw_full[raw], (i / p.raws) & 1, abort))) break;
-                if (j >= p.slots && !(ok = warp_wait(&ctl.slot_empty[slot], ((j / p.slots) - 1) & 1, abort))) break;
+                if (j >= p.ops && !(ok = warp_wait(&ctl.a_empty[op], ((j / p.ops) - 1) & 1, abort))) break;
 #pragma unroll
                 for (int pp = 0; pp < P; ++pp) {
                     const unsigned char *from = raws + raw * raw_bytes + (4 * pp + strip) * chunk_bytes;
-                    unsigned char *operand = slots + slot * slot_bytes + pp * kOperand + strip * 32 * 128 + g * 128;
+                    unsigned char *operand = ops + (op * P + pp) * kOperand + strip * 32 * 128 + g * 128;
                     // the step's units: half of one, one, or two
                     const unsigned char *u0 = from + (G == 128 ? 1024 * (j & 1) : G == 64 ? (j & 1) * a.unit : 2 * (j & 1) * a.unit);
                     uint32_t zero[2][2][2];  // [block][tile][h]
@@ -345,85 +331,108 @@ __global__ void __launch_bounds__(kThreadsG, 1)
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) {
-                    w4_arrive(&ctl.a_full[slot]);
+                    w4_arrive(&ctl.a_full[op]);
                     w4_arrive(&ctl.raw_empty[raw]);
                 }
             }
         } else if (warp == kLoadWarpG) {
-            // ---- load (one lane) ----
+            // ---- load units (one lane) ----
             if (lane == 0) {
                 const size_t strip_bytes = (size_t)groups * a.unit;
                 const unsigned char *src[P];
 #pragma unroll
                 for (int i = 0; i < P; ++i)
                     src[i] = (i ? a.part[1].w : to.w) + (size_t)4 * tile * strip_bytes + (size_t)c0 * chunk_bytes;
-                auto ask_raw = [&](int i) {
+                if (!p.prefetch) asm volatile("griddepcontrol.wait;" ::: "memory");
+                int i = 0;
+                for (; i < n_chunks; ++i) {
                     const int raw = i % p.raws;
-                    const unsigned bytes = (unsigned)(min(CG, groups - (c0 + i) * CG) * a.unit);
+                    if (i >= p.raws && !wait(&ctl.raw_empty[raw], ((i / p.raws) - 1) & 1, abort)) break;
+                    const int have = min(CG, groups - (c0 + i) * CG), st = i % kScaleStages;
+                    const unsigned bytes = (unsigned)(have * a.unit);
                     w4_arrive_tx(&ctl.raw_full[raw], bytes * (unsigned)(P * strips));
 #pragma unroll
                     for (int pp = 0; pp < P; ++pp)
                         for (int s = 0; s < strips; ++s)
                             w4_copy(raws + raw * raw_bytes + (4 * pp + s) * chunk_bytes,
                                     src[pp] + s * strip_bytes + (size_t)i * chunk_bytes, bytes, &ctl.raw_full[raw]);
-                };
-                int asked = 0;  // chunks
-                if (p.prefetch)
-                    for (; asked < n_chunks && asked < p.raws; ++asked) ask_raw(asked);
-                asm volatile("griddepcontrol.wait;" ::: "memory");
-                bool ok = true;
-                int j = 0;
-                for (; j < n_steps && ok; ++j) {
-                    // units as far ahead as there is room, at every step
-                    while (asked < n_chunks && asked <= (j >> 1) + p.raws - 1) {
-                        if (asked >= p.raws && !(ok = wait(&ctl.raw_empty[asked % p.raws], ((asked / p.raws) - 1) & 1, abort)))
-                            break;
-                        ask_raw(asked++);
-                    }
-                    if (!ok) break;
-                    const int slot = j % p.slots;
-                    if (j >= p.slots && !(ok = wait(&ctl.slot_empty[slot], ((j / p.slots) - 1) & 1, abort))) break;
-                    w4_arrive_tx(&ctl.x_full[slot], (unsigned)p.rows * 128);
-                    tma_rows(slots + slot * slot_bytes + P * kOperand, &xmap, c0 * kChunkK + j * kStepK, row0,
-                             &ctl.x_full[slot]);
+                    // the scales once more, where they wait for the fold
+                    if (i >= kScaleStages && !wait(&ctl.s_empty[st], ((i / kScaleStages) - 1) & 1, abort)) break;
+                    w4_arrive_tx(&ctl.s_full[st], (unsigned)(have * P * strips * 64));
+#pragma unroll
+                    for (int pp = 0; pp < P; ++pp)
+                        for (int s = 0; s < strips; ++s)
+                            for (int q = 0; q < have; ++q)
+                                w4_copy(scales + (((st * P + pp) * 4 + s) * CG + q) * 64,
+                                        src[pp] + s * strip_bytes + (size_t)i * chunk_bytes + q * a.unit + 16 * G, 64,
+                                        &ctl.s_full[st]);
                 }
                 if (*abort) {  // what was asked for lands before the memory is used again
-                    for (int i = max(0, asked - p.raws); i < asked; ++i) w4_wait(&ctl.raw_full[i % p.raws], (i / p.raws) & 1);
-                    for (int i = max(0, j - p.slots); i < j; ++i) w4_wait(&ctl.x_full[i % p.slots], (i / p.slots) & 1);
+                    for (int k = max(0, i + 1 - p.raws); k <= i && k < n_chunks; ++k)
+                        w4_wait(&ctl.raw_full[k % p.raws], (k / p.raws) & 1);
+                    for (int k = max(0, i - kScaleStages); k < i; ++k)
+                        w4_wait(&ctl.s_full[k % kScaleStages], (k / kScaleStages) & 1);
                 }
+            }
+            __syncwarp();
+        } else if (warp == kXWarpG) {
+            // ---- load activations (one lane) ----
+            if (lane == 0) {
+                asm volatile("griddepcontrol.wait;" ::: "memory");
+                int j = 0;
+                for (; j < n_steps; ++j) {
+                    const int x = j % p.xs;
+                    if (j >= p.xs && !wait(&ctl.x_empty[x], ((j / p.xs) - 1) & 1, abort)) break;
+                    w4_arrive_tx(&ctl.x_full[x], (unsigned)x_bytes);
+                    tma_rows(xs + x * x_bytes, &xmap, c0 * kChunkK + j * kStepK, row0, &ctl.x_full[x]);
+                }
+                if (*abort)
+                    for (int k = max(0, j - p.xs); k < j; ++k) w4_wait(&ctl.x_full[k % p.xs], (k / p.xs) & 1);
             }
             __syncwarp();
         } else if (warp == kMmaWarpG) {
             // ---- multiply ----
             const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(p.rows >> 3) << 17) |
                                    ((uint32_t)(kCols >> 4) << 24);
-            int slot = 0, buf = 0;
-            unsigned slot_phase = 0, acc_phase = 1;  // a fresh barrier passes for the phase before its first
+            int op = 0, x = 0, buf = 0;
+            unsigned op_phase = 0, x_phase = 0, acc_phase = 1;  // a fresh barrier passes for the phase before its first
             for (int j = 0; j < n_steps; ++j) {
-                if (!warp_wait(&ctl.x_full[slot], slot_phase, abort) || !warp_wait(&ctl.a_full[slot], slot_phase, abort)) break;
+                if (!warp_wait(&ctl.x_full[x], x_phase, abort) || !warp_wait(&ctl.a_full[op], op_phase, abort)) break;
+                // the step's groups: a part of one, one, or two (of the last step perhaps only the first)
                 const int ksteps = min(4, (rows_k - j * kStepK) / 16);
-                const uint32_t base = desc_low(w4_smem(slots + slot * slot_bytes));
-                bool ok = true;
-#pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    const int in_group = (4 * (j & 1) + s) & (G / 16 - 1);
-                    if (s >= ksteps) break;
-                    if (in_group == 0 && !(ok = warp_wait(&ctl.acc_empty[buf], acc_phase, abort))) break;
-                    fence_after();
-                    if (elect()) {
-#pragma unroll
-                        for (int i = 0; i < P; ++i)
-                            mma(tmem + (uint32_t)((buf * P + i) * p.rows), base + ((i * kOperand + 32 * s) >> 4),
-                                base + ((P * kOperand + 32 * s) >> 4), idesc, in_group > 0);
-                        if (in_group == G / 16 - 1) commit(&ctl.acc_full[buf]);
-                    }
-                    __syncwarp();
-                    if (in_group == G / 16 - 1 && ++buf == p.accs) buf = 0, acc_phase ^= 1;
-                }
+                constexpr int kPer = G == 32 ? 2 : 4;  // MMAs of a group in a step
+                const bool fresh = G < 128 || (j & 1) == 0;
+                const int buf1 = buf + 1 == p.accs ? 0 : buf + 1;
+                bool ok = !fresh || warp_wait(&ctl.acc_empty[buf], acc_phase, abort);
+                if (G == 32 && ksteps > 2)
+                    ok = ok && warp_wait(&ctl.acc_empty[buf1], buf1 ? acc_phase : acc_phase ^ 1, abort);
                 if (!ok) break;
-                if (elect()) commit(&ctl.slot_empty[slot]);
+                const uint32_t da = __shfl_sync(0xffffffffu, desc_low(w4_smem(ops + op * P * kOperand)), 0);
+                const uint32_t db = __shfl_sync(0xffffffffu, desc_low(w4_smem(xs + x * x_bytes)), 0);
+                const uint32_t d0 = __shfl_sync(0xffffffffu, tmem + (uint32_t)(buf * P * p.rows), 0);
+                const uint32_t d1 = __shfl_sync(0xffffffffu, tmem + (uint32_t)(buf1 * P * p.rows), 0);
+                fence_after();
+                if (elect()) {
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        if (s < ksteps) {
+                            const uint32_t d = s < kPer ? d0 : d1;
+#pragma unroll
+                            for (int i = 0; i < P; ++i)
+                                mma(d + i * p.rows, da + ((i * kOperand + 32 * s) >> 4), db + (32 * s >> 4), idesc,
+                                    s % kPer > 0 || !fresh);
+                            if (G < 128 && s % kPer == kPer - 1) commit(&ctl.acc_full[s < kPer ? buf : buf1]);
+                        }
+                    if (G == 128 && !fresh) commit(&ctl.acc_full[buf]);
+                    commit(&ctl.a_empty[op]);
+                    commit(&ctl.x_empty[x]);
+                }
                 __syncwarp();
-                if (++slot == p.slots) slot = 0, slot_phase ^= 1;
+                if (G < 128 || !fresh)
+                    for (int i = 0; i < (G == 32 ? ksteps / 2 : 1); ++i)
+                        if (++buf == p.accs) buf = 0, acc_phase ^= 1;
+                if (++op == p.ops) op = 0, op_phase ^= 1;
+                if (++x == p.xs) x = 0, x_phase ^= 1;
             }
         }
         asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -440,27 +449,58 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     __syncthreads();
     fence_after();
 
-    if (p.ks > 1) {  // a rank's share of the tile's rows, the ranks' carries added in order
-        const float *red = reinterpret_cast<float *>(smem_g);
-        cg::cluster_group cluster = cg::this_cluster();
-        cluster.sync();
-        const int live = min(p.rows, a.m - row0);
-        const int r0 = live * (int)blockIdx.z / p.ks, r1 = live * ((int)blockIdx.z + 1) / p.ks;
-        for (int i = threadIdx.x; i < (r1 - r0) * kCols; i += kThreadsG) {
-            const int r = r0 + i / kCols, c = i % kCols, n = tile * kCols + c;
-            if (n < to.Np && !*abort) {
-                float v = 0.0f, u = 0.0f;
-#pragma unroll 4
-                for (int k = 0; k < p.ks; ++k) v += cluster.map_shared_rank(red, k)[r * kCols + c];
+    // A rank's share of the tile's rows, the ranks' carries added in order, four columns a thread.
+    const float *red = reinterpret_cast<float *>(smem_g);
+    cg::cluster_group cluster = cg::this_cluster();
+    if (p.ks > 1) cluster.sync();
+    const int live = min(p.rows, a.m - row0);
+    const int r0 = live * (int)blockIdx.z / p.ks, r1 = live * ((int)blockIdx.z + 1) / p.ks;
+    const int c = 4 * lane, n = tile * kCols + c;
+    if (n < to.Np && !*abort) {
+        auto total = [&](int r, float (&v)[4]) {
+            float4 f = *reinterpret_cast<const float4 *>(cluster.map_shared_rank(red, 0) + r * kCols + c);
+#pragma unroll 2
+            for (int k = 1; k < p.ks; ++k) {
+                const float4 o = *reinterpret_cast<const float4 *>(cluster.map_shared_rank(red, k) + r * kCols + c);
+                f.x += o.x, f.y += o.y, f.z += o.z, f.w += o.w;
+            }
+            v[0] = kW4Unit * f.x, v[1] = kW4Unit * f.y, v[2] = kW4Unit * f.z, v[3] = kW4Unit * f.w;
+        };
+        constexpr int kWarps = kThreadsG / 32, kTogether = 4;  // rows of a warp at a time
+        for (int r = r0 + warp; r < r1; r += kWarps * kTogether) {
+            float res[kTogether][4] = {};
+            if (a.epi == kW4Residual) {
+#pragma unroll
+                for (int i = 0; i < kTogether; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (r + i * kWarps < r1 && n + e < to.N)
+                            res[i][e] = __ldcg(a.res + (size_t)(row0 + r + i * kWarps) * to.Np + n + e);
+            }
+#pragma unroll
+            for (int i = 0; i < kTogether; ++i) {
+                if (r + i * kWarps >= r1) break;
+                float v[4];
+                total(r + i * kWarps, v);
                 if (P == 2) {
-#pragma unroll 4
-                    for (int k = 0; k < p.ks; ++k) u += cluster.map_shared_rank(red, k)[(p.rows + r) * kCols + c];
+                    float u[4];
+                    total(p.rows + r + i * kWarps, u);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = v[e] / (1.0f + expf(-v[e])) * u[e];
                 }
-                finish(row0 + r, n, v, u);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = n + e < to.N ? v[e] + res[i][e] : 0.0f;
+                const size_t at = (size_t)(row0 + r + i * kWarps) * to.Np + n;
+                if (to.y) *reinterpret_cast<float4 *>(to.y + at) = make_float4(v[0], v[1], v[2], v[3]);
+                if (a.ybf) {
+                    __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
+                    *reinterpret_cast<uint2 *>(a.ybf + at) =
+                        make_uint2(*reinterpret_cast<uint32_t *>(&lo), *reinterpret_cast<uint32_t *>(&hi));
+                }
             }
         }
-        cluster_sync_after_reads();
     }
+    if (p.ks > 1) cluster_sync_after_reads();
     if (warp == kMmaWarpG)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
@@ -530,14 +570,17 @@ cudaError_t launch_w4_gemm(const W4Args &a, bool constant_weights, cudaStream_t 
     }
     if (const char *v = getenv("W4_GKS")) p.ks = atoi(v);
     p.accs = 512 / (P * p.rows) < kMaxAcc ? 512 / (P * p.rows) : kMaxAcc;
-    const int raw = P * 4 * (kChunkK / a.group) * a.unit, slot = P * kOperand + p.rows * 128;
-    const int room = kMaxSmemG - (int)sizeof(Control);
-    p.raws = 3;
-    p.slots = (room - p.raws * raw) / slot;
-    if (p.slots > kMaxStages) p.slots = kMaxStages;
-    p.raws = (room - p.slots * slot) / raw;
+    const int raw = P * 4 * (kChunkK / a.group) * a.unit, op = P * kOperand, x = p.rows * 128;
+    const int fixed = (int)sizeof(Control) + kScaleStages * P * 4 * (kChunkK / a.group) * 64;
+    p.ops = 3;
+    p.xs = 4;
+    if (const char *v = getenv("W4_OPS")) p.ops = atoi(v);
+    if (const char *v = getenv("W4_XS")) p.xs = atoi(v);
+    const int slab = P * p.rows * kCols * 4;  // the carries, over operands and activations
+    p.raws = (kMaxSmemG - fixed - p.ops * op - p.xs * x) / raw;
     if (p.raws > kMaxStages) p.raws = kMaxStages;
-    const int smem = p.slots * slot + p.raws * raw + (int)sizeof(Control);
+    const int smem = fixed + p.ops * op + p.xs * x + p.raws * raw;
+    if (slab > p.ops * op + p.xs * x || p.raws < 2) return cudaErrorInvalidValue;
     CUtensorMap map;
     if (!encode_bf16_rows(&map, a.x, a.m, a.K, kStepK, p.rows)) return cudaErrorNotSupported;
     switch (a.group) {
