@@ -38,7 +38,7 @@ constexpr int kCols = 128;     // columns of W in a tile
 constexpr int kStepK = 64;     // rows of K in a step: 128 bytes of bf16
 constexpr int kChunkK = 128;   // rows of K in a raw stage
 constexpr int kThreadsG = 512;
-constexpr int kLoadWarpG = 12, kMmaWarpG = 13, kXWarpG = 14;
+constexpr int kConvertEnd = 12, kLoadWarp = 12, kMmaWarp = 13, kXWarp = 14;
 constexpr int kOperand = kCols * kStepK * 2;  // 16 KB: one converted step of one weight
 constexpr int kMaxSmemG = 227 * 1024;
 constexpr int kMaxStages = 8, kMaxAcc = 4;
@@ -48,8 +48,7 @@ __device__ unsigned int g_w4_gemm_fault = 0;
 
 struct Gemm4 {
     int rows;    // of a tile, a multiple of 32 (FW = 2) or 16
-    int ops;     // stages of converted weights
-    int xs;      // stages of activations
+    int slots;   // stages of converted weights and activations
     int raws;    // stages of units
     int accs;    // accumulators
     int ks;      // CTAs of a cluster splitting K
@@ -57,8 +56,8 @@ struct Gemm4 {
 };
 
 struct Control {
-    uint64_t raw_full[kMaxStages], raw_empty[kMaxStages], x_full[kMaxStages], x_empty[kMaxStages];
-    uint64_t a_full[kMaxStages], a_empty[kMaxStages], s_full[kScaleStages], s_empty[kScaleStages];
+    uint64_t raw_full[kMaxStages], raw_empty[kMaxStages], full[kMaxStages], empty[kMaxStages];
+    uint64_t s_full[kScaleStages], s_empty[kScaleStages];
     uint64_t acc_full[kMaxAcc], acc_empty[kMaxAcc], drain;
     uint32_t tmem;
     int abort;
@@ -147,12 +146,12 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     gemm4_kernel(const __grid_constant__ W4Args a, const Gemm4 p, const __grid_constant__ CUtensorMap xmap) {
     namespace cg = cooperative_groups;
     constexpr int CG = kChunkK / G;  // groups of a chunk
-    constexpr int kTeams = FW == 1 ? 2 : 1;
+    constexpr int kConvert = 4 * FW, kTeams = (kConvertEnd - kConvert) / 4;
     constexpr int kPerAcc = 8 / P;   // 16-row pieces of one accumulator that a folding thread holds at most
     extern __shared__ __align__(1024) unsigned char smem_g[];
     const int chunk_bytes = CG * a.unit, raw_bytes = P * 4 * chunk_bytes;
-    const int x_bytes = p.rows * 128;
-    unsigned char *ops = smem_g, *xs = ops + p.ops * P * kOperand, *raws = xs + p.xs * x_bytes;
+    const int x_bytes = p.rows * 128, slot_bytes = P * kOperand + x_bytes;
+    unsigned char *slots = smem_g, *raws = slots + p.slots * slot_bytes;
     unsigned char *scales = raws + p.raws * raw_bytes;  // [stage][P][4 strips][CG][32] of 16 bits
     Control &ctl = *reinterpret_cast<Control *>(scales + kScaleStages * P * 4 * CG * 64);
     volatile int *abort = &ctl.abort;
@@ -182,13 +181,9 @@ __global__ void __launch_bounds__(kThreadsG, 1)
             w4_bar_init(&ctl.s_full[i], 1);
             w4_bar_init(&ctl.s_empty[i], 4 * FW);
         }
-        for (int i = 0; i < p.xs; ++i) {
-            w4_bar_init(&ctl.x_full[i], 1);
-            w4_bar_init(&ctl.x_empty[i], 1);
-        }
-        for (int i = 0; i < p.ops; ++i) {
-            w4_bar_init(&ctl.a_full[i], 4);
-            w4_bar_init(&ctl.a_empty[i], 1);
+        for (int i = 0; i < p.slots; ++i) {
+            w4_bar_init(&ctl.full[i], 5);  // a team's four warps, the activations' announcement
+            w4_bar_init(&ctl.empty[i], 1);
         }
         for (int i = 0; i < p.accs; ++i) {
             w4_bar_init(&ctl.acc_full[i], 1);
@@ -198,7 +193,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
         ctl.abort = 0;
         w4_bar_fence();
     }
-    if (warp == kMmaWarpG) {
+    if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(w4_smem(&ctl.tmem)),
                      "r"(512)
                      : "memory");
@@ -285,18 +280,18 @@ __global__ void __launch_bounds__(kThreadsG, 1)
             asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         else
             asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        if (warp < kLoadWarpG) {
+        if (warp < kConvertEnd) {
             // ---- convert ----
-            const int team = (warp - 4 * FW) >> 2, strip = warp & 3, g = lane >> 2, t = lane & 3, odd = g & 1;
-            bool ok = true;
+            const int team = (warp - kConvert) >> 2, strip = warp & 3, g = lane >> 2, t = lane & 3, odd = g & 1;
+            int raw = 0, slot = team;
+            unsigned raw_phase = 0, phase = 1;  // a fresh barrier passes for the phase before its first
             for (int j = team; j < n_steps; j += kTeams) {
-                const int i = j >> 1, raw = i % p.raws, op = j % p.ops;
-                if (!(ok = warp_wait(&ctl.raw_full[raw], (i / p.raws) & 1, abort))) break;
-                if (j >= p.ops && !(ok = warp_wait(&ctl.a_empty[op], ((j / p.ops) - 1) & 1, abort))) break;
+                if (!warp_wait(&ctl.raw_full[raw], raw_phase, abort)) break;
+                if (!warp_wait(&ctl.empty[slot], phase, abort)) break;
 #pragma unroll
                 for (int pp = 0; pp < P; ++pp) {
                     const unsigned char *from = raws + raw * raw_bytes + (4 * pp + strip) * chunk_bytes;
-                    unsigned char *operand = ops + (op * P + pp) * kOperand + strip * 32 * 128 + g * 128;
+                    unsigned char *operand = slots + slot * slot_bytes + pp * kOperand + strip * 32 * 128 + g * 128;
                     // the step's units: half of one, one, or two
                     const unsigned char *u0 = from + (G == 128 ? 1024 * (j & 1) : G == 64 ? (j & 1) * a.unit : 2 * (j & 1) * a.unit);
                     uint32_t zero[2][2][2];  // [block][tile][h]
@@ -331,11 +326,13 @@ __global__ void __launch_bounds__(kThreadsG, 1)
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) {
-                    w4_arrive(&ctl.a_full[op]);
+                    w4_arrive(&ctl.full[slot]);
                     w4_arrive(&ctl.raw_empty[raw]);
                 }
+                if ((kTeams == 2 || (j & 1)) && ++raw == p.raws) raw = 0, raw_phase ^= 1;
+                if ((slot += kTeams) >= p.slots) slot -= p.slots, phase ^= 1;
             }
-        } else if (warp == kLoadWarpG) {
+        } else if (warp == kLoadWarp) {
             // ---- load units (one lane) ----
             if (lane == 0) {
                 const size_t strip_bytes = (size_t)groups * a.unit;
@@ -344,28 +341,31 @@ __global__ void __launch_bounds__(kThreadsG, 1)
                 for (int i = 0; i < P; ++i)
                     src[i] = (i ? a.part[1].w : to.w) + (size_t)4 * tile * strip_bytes + (size_t)c0 * chunk_bytes;
                 if (!p.prefetch) asm volatile("griddepcontrol.wait;" ::: "memory");
-                int i = 0;
+                int i = 0, raw = 0, st = 0;
+                unsigned raw_phase = 1, s_phase = 1;
                 for (; i < n_chunks; ++i) {
-                    const int raw = i % p.raws;
-                    if (i >= p.raws && !wait(&ctl.raw_empty[raw], ((i / p.raws) - 1) & 1, abort)) break;
-                    const int have = min(CG, groups - (c0 + i) * CG), st = i % kScaleStages;
+                    if (!wait(&ctl.raw_empty[raw], raw_phase, abort)) break;
+                    const int have = min(CG, groups - (c0 + i) * CG);
                     const unsigned bytes = (unsigned)(have * a.unit);
                     w4_arrive_tx(&ctl.raw_full[raw], bytes * (unsigned)(P * strips));
 #pragma unroll
                     for (int pp = 0; pp < P; ++pp)
                         for (int s = 0; s < strips; ++s)
-                            w4_copy(raws + raw * raw_bytes + (4 * pp + s) * chunk_bytes,
-                                    src[pp] + s * strip_bytes + (size_t)i * chunk_bytes, bytes, &ctl.raw_full[raw]);
+                            w4_copy(raws + raw * raw_bytes + (4 * pp + s) * chunk_bytes, src[pp] + s * strip_bytes, bytes,
+                                    &ctl.raw_full[raw]);
                     // the scales once more, where they wait for the fold
-                    if (i >= kScaleStages && !wait(&ctl.s_empty[st], ((i / kScaleStages) - 1) & 1, abort)) break;
+                    if (!wait(&ctl.s_empty[st], s_phase, abort)) break;
                     w4_arrive_tx(&ctl.s_full[st], (unsigned)(have * P * strips * 64));
 #pragma unroll
-                    for (int pp = 0; pp < P; ++pp)
+                    for (int pp = 0; pp < P; ++pp) {
                         for (int s = 0; s < strips; ++s)
                             for (int q = 0; q < have; ++q)
                                 w4_copy(scales + (((st * P + pp) * 4 + s) * CG + q) * 64,
-                                        src[pp] + s * strip_bytes + (size_t)i * chunk_bytes + q * a.unit + 16 * G, 64,
-                                        &ctl.s_full[st]);
+                                        src[pp] + s * strip_bytes + q * a.unit + 16 * G, 64, &ctl.s_full[st]);
+                        src[pp] += chunk_bytes;
+                    }
+                    if (++raw == p.raws) raw = 0, raw_phase ^= 1;
+                    if (++st == kScaleStages) st = 0, s_phase ^= 1;
                 }
                 if (*abort) {  // what was asked for lands before the memory is used again
                     for (int k = max(0, i + 1 - p.raws); k <= i && k < n_chunks; ++k)
@@ -375,29 +375,34 @@ __global__ void __launch_bounds__(kThreadsG, 1)
                 }
             }
             __syncwarp();
-        } else if (warp == kXWarpG) {
+        } else if (warp == kXWarp) {
             // ---- load activations (one lane) ----
             if (lane == 0) {
                 asm volatile("griddepcontrol.wait;" ::: "memory");
-                int j = 0;
+                int j = 0, slot = 0;
+                unsigned phase = 1;
                 for (; j < n_steps; ++j) {
-                    const int x = j % p.xs;
-                    if (j >= p.xs && !wait(&ctl.x_empty[x], ((j / p.xs) - 1) & 1, abort)) break;
-                    w4_arrive_tx(&ctl.x_full[x], (unsigned)x_bytes);
-                    tma_rows(xs + x * x_bytes, &xmap, c0 * kChunkK + j * kStepK, row0, &ctl.x_full[x]);
+                    if (!wait(&ctl.empty[slot], phase, abort)) break;
+                    w4_arrive_tx(&ctl.full[slot], (unsigned)x_bytes);
+                    tma_rows(slots + slot * slot_bytes + P * kOperand, &xmap, c0 * kChunkK + j * kStepK, row0,
+                             &ctl.full[slot]);
+                    if (++slot == p.slots) slot = 0, phase ^= 1;
                 }
+                // `full` waits for the teams too, which may have stopped: time for the copies in flight instead
                 if (*abort)
-                    for (int k = max(0, j - p.xs); k < j; ++k) w4_wait(&ctl.x_full[k % p.xs], (k / p.xs) & 1);
+                    for (int k = max(0, j - p.slots); k < j; ++k) w4_wait(&ctl.full[k % p.slots], (k / p.slots) & 1);
             }
             __syncwarp();
-        } else if (warp == kMmaWarpG) {
+        } else if (warp == kMmaWarp) {
             // ---- multiply ----
             const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(p.rows >> 3) << 17) |
                                    ((uint32_t)(kCols >> 4) << 24);
-            int op = 0, x = 0, buf = 0;
-            unsigned op_phase = 0, x_phase = 0, acc_phase = 1;  // a fresh barrier passes for the phase before its first
+            int slot = 0, buf = 0;
+            unsigned phase = 0, acc_phase = 1;
+            uint32_t da = __shfl_sync(0xffffffffu, desc_low(w4_smem(slots)), 0);  // the slot's operand; its activations
+            const uint32_t base = da, next = (uint32_t)slot_bytes >> 4, xat = (uint32_t)(P * kOperand) >> 4;
             for (int j = 0; j < n_steps; ++j) {
-                if (!warp_wait(&ctl.x_full[x], x_phase, abort) || !warp_wait(&ctl.a_full[op], op_phase, abort)) break;
+                if (!warp_wait(&ctl.full[slot], phase, abort)) break;
                 // the step's groups: a part of one, one, or two (of the last step perhaps only the first)
                 const int ksteps = min(4, (rows_k - j * kStepK) / 16);
                 constexpr int kPer = G == 32 ? 2 : 4;  // MMAs of a group in a step
@@ -407,10 +412,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
                 if (G == 32 && ksteps > 2)
                     ok = ok && warp_wait(&ctl.acc_empty[buf1], buf1 ? acc_phase : acc_phase ^ 1, abort);
                 if (!ok) break;
-                const uint32_t da = __shfl_sync(0xffffffffu, desc_low(w4_smem(ops + op * P * kOperand)), 0);
-                const uint32_t db = __shfl_sync(0xffffffffu, desc_low(w4_smem(xs + x * x_bytes)), 0);
-                const uint32_t d0 = __shfl_sync(0xffffffffu, tmem + (uint32_t)(buf * P * p.rows), 0);
-                const uint32_t d1 = __shfl_sync(0xffffffffu, tmem + (uint32_t)(buf1 * P * p.rows), 0);
+                const uint32_t d0 = tmem + (uint32_t)(buf * P * p.rows), d1 = tmem + (uint32_t)(buf1 * P * p.rows);
                 fence_after();
                 if (elect()) {
 #pragma unroll
@@ -419,20 +421,19 @@ __global__ void __launch_bounds__(kThreadsG, 1)
                             const uint32_t d = s < kPer ? d0 : d1;
 #pragma unroll
                             for (int i = 0; i < P; ++i)
-                                mma(d + i * p.rows, da + ((i * kOperand + 32 * s) >> 4), db + (32 * s >> 4), idesc,
+                                mma(d + i * p.rows, da + ((i * kOperand + 32 * s) >> 4), da + xat + (32 * s >> 4), idesc,
                                     s % kPer > 0 || !fresh);
                             if (G < 128 && s % kPer == kPer - 1) commit(&ctl.acc_full[s < kPer ? buf : buf1]);
                         }
                     if (G == 128 && !fresh) commit(&ctl.acc_full[buf]);
-                    commit(&ctl.a_empty[op]);
-                    commit(&ctl.x_empty[x]);
+                    commit(&ctl.empty[slot]);
                 }
                 __syncwarp();
                 if (G < 128 || !fresh)
                     for (int i = 0; i < (G == 32 ? ksteps / 2 : 1); ++i)
                         if (++buf == p.accs) buf = 0, acc_phase ^= 1;
-                if (++op == p.ops) op = 0, op_phase ^= 1;
-                if (++x == p.xs) x = 0, x_phase ^= 1;
+                da += next;
+                if (++slot == p.slots) slot = 0, phase ^= 1, da = base;
             }
         }
         asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -442,7 +443,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     // All MMAs are done (the last group's commit was waited for) and all copies have landed, unless the CTA stopped.
     fence_before();
     __syncthreads();
-    if (*abort && warp == kMmaWarpG) {
+    if (*abort && warp == kMmaWarp) {
         if (elect()) commit(&ctl.drain);
         w4_wait(&ctl.drain, 0);
     }
@@ -501,7 +502,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
         }
     }
     if (p.ks > 1) cluster_sync_after_reads();
-    if (warp == kMmaWarpG)
+    if (warp == kMmaWarp)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
 
@@ -570,17 +571,13 @@ cudaError_t launch_w4_gemm(const W4Args &a, bool constant_weights, cudaStream_t 
     }
     if (const char *v = getenv("W4_GKS")) p.ks = atoi(v);
     p.accs = 512 / (P * p.rows) < kMaxAcc ? 512 / (P * p.rows) : kMaxAcc;
-    const int raw = P * 4 * (kChunkK / a.group) * a.unit, op = P * kOperand, x = p.rows * 128;
+    const int raw = P * 4 * (kChunkK / a.group) * a.unit, slot = P * kOperand + p.rows * 128;
     const int fixed = (int)sizeof(Control) + kScaleStages * P * 4 * (kChunkK / a.group) * 64;
-    p.ops = 3;
-    p.xs = 4;
-    if (const char *v = getenv("W4_OPS")) p.ops = atoi(v);
-    if (const char *v = getenv("W4_XS")) p.xs = atoi(v);
-    const int slab = P * p.rows * kCols * 4;  // the carries, over operands and activations
-    p.raws = (kMaxSmemG - fixed - p.ops * op - p.xs * x) / raw;
+    p.slots = (kMaxSmemG - fixed - 3 * raw) / slot;  // at least 3, and 3 raw stages, for every size
+    if (p.slots > 5) p.slots = 5;
+    p.raws = (kMaxSmemG - fixed - p.slots * slot) / raw;
     if (p.raws > kMaxStages) p.raws = kMaxStages;
-    const int smem = fixed + p.ops * op + p.xs * x + p.raws * raw;
-    if (slab > p.ops * op + p.xs * x || p.raws < 2) return cudaErrorInvalidValue;
+    const int smem = fixed + p.slots * slot + p.raws * raw;
     CUtensorMap map;
     if (!encode_bf16_rows(&map, a.x, a.m, a.K, kStepK, p.rows)) return cudaErrorNotSupported;
     switch (a.group) {
