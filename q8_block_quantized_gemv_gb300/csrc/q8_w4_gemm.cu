@@ -38,11 +38,10 @@ constexpr int kCols = 128;     // columns of W in a tile
 constexpr int kStepK = 64;     // rows of K in a step: 128 bytes of bf16
 constexpr int kChunkK = 128;   // rows of K in a raw stage
 constexpr int kThreadsG = 512;
-constexpr int kConvertEnd = 12, kLoadWarp = 12, kMmaWarp = 13, kXWarp = 14;
+constexpr int kConvertEnd = 12, kLoadWarp = 12, kMmaWarp = 13, kXWarp = 14, kLoadUpWarp = 15;
 constexpr int kOperand = kCols * kStepK * 2;  // 16 KB: one converted step of one weight
 constexpr int kMaxSmemG = 227 * 1024;
 constexpr int kMaxStages = 8, kMaxAcc = 4;
-constexpr int kScaleStages = 4;  // chunks
 
 __device__ unsigned int g_w4_gemm_fault = 0;
 
@@ -57,7 +56,6 @@ struct Gemm4 {
 
 struct Control {
     uint64_t raw_full[kMaxStages], raw_empty[kMaxStages], full[kMaxStages], empty[kMaxStages];
-    uint64_t s_full[kScaleStages], s_empty[kScaleStages];
     uint64_t acc_full[kMaxAcc], acc_empty[kMaxAcc], drain;
     uint32_t tmem;
     int abort;
@@ -105,12 +103,41 @@ __device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t b, uint32_t
         "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
         : "memory");
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t a, uint32_t (&v)[16]) {
+// 16, 32 or 64 columns of the warp's lanes.
+__device__ __forceinline__ void tmem_ld16(uint32_t a, uint32_t *v) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
         "[%16];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(a));
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t *v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, "
+        "[%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(a));
+}
+__device__ __forceinline__ void tmem_ld64(uint32_t a, uint32_t *v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+        "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+        "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, "
+        "[%64];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31]),
+          "=r"(v[32]), "=r"(v[33]), "=r"(v[34]), "=r"(v[35]), "=r"(v[36]), "=r"(v[37]), "=r"(v[38]), "=r"(v[39]),
+          "=r"(v[40]), "=r"(v[41]), "=r"(v[42]), "=r"(v[43]), "=r"(v[44]), "=r"(v[45]), "=r"(v[46]), "=r"(v[47]),
+          "=r"(v[48]), "=r"(v[49]), "=r"(v[50]), "=r"(v[51]), "=r"(v[52]), "=r"(v[53]), "=r"(v[54]), "=r"(v[55]),
+          "=r"(v[56]), "=r"(v[57]), "=r"(v[58]), "=r"(v[59]), "=r"(v[60]), "=r"(v[61]), "=r"(v[62]), "=r"(v[63])
         : "r"(a));
 }
 __device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
@@ -146,14 +173,13 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     gemm4_kernel(const __grid_constant__ W4Args a, const Gemm4 p, const __grid_constant__ CUtensorMap xmap) {
     namespace cg = cooperative_groups;
     constexpr int CG = kChunkK / G;  // groups of a chunk
-    constexpr int kConvert = 4 * FW, kTeams = (kConvertEnd - kConvert) / 4;
+    constexpr int kConvert = 4 * FW, kTeam = FW == 1 ? 4 : 2;  // warps of a team, of two
     constexpr int kPerAcc = 8 / P;   // 16-row pieces of one accumulator that a folding thread holds at most
     extern __shared__ __align__(1024) unsigned char smem_g[];
     const int chunk_bytes = CG * a.unit, raw_bytes = P * 4 * chunk_bytes;
     const int x_bytes = p.rows * 128, slot_bytes = P * kOperand + x_bytes;
     unsigned char *slots = smem_g, *raws = slots + p.slots * slot_bytes;
-    unsigned char *scales = raws + p.raws * raw_bytes;  // [stage][P][4 strips][CG][32] of 16 bits
-    Control &ctl = *reinterpret_cast<Control *>(scales + kScaleStages * P * 4 * CG * 64);
+    Control &ctl = *reinterpret_cast<Control *>(raws + p.raws * raw_bytes);
     volatile int *abort = &ctl.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -174,15 +200,11 @@ __global__ void __launch_bounds__(kThreadsG, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < p.raws; ++i) {
-            w4_bar_init(&ctl.raw_full[i], 1);
-            w4_bar_init(&ctl.raw_empty[i], 8);  // four converting warps for each of two steps
-        }
-        for (int i = 0; i < kScaleStages; ++i) {
-            w4_bar_init(&ctl.s_full[i], 1);
-            w4_bar_init(&ctl.s_empty[i], 4 * FW);
+            w4_bar_init(&ctl.raw_full[i], P);
+            w4_bar_init(&ctl.raw_empty[i], 2 * kTeam + 4 * FW);  // a team for each of two steps, the folding warps
         }
         for (int i = 0; i < p.slots; ++i) {
-            w4_bar_init(&ctl.full[i], 5);  // a team's four warps, the activations' announcement
+            w4_bar_init(&ctl.full[i], kTeam + 1);  // a team, the activations' announcement
             w4_bar_init(&ctl.empty[i], 1);
         }
         for (int i = 0; i < p.accs; ++i) {
@@ -207,24 +229,24 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     const int half = p.rows / FW;  // rows of a folding thread
     if (warp < 4 * FW) {
         // ---- fold ----
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         asm volatile("griddepcontrol.wait;" ::: "memory");
         unsigned long long acc[64];
 #pragma unroll
         for (int i = 0; i < 64; ++i) acc[i] = 0ull;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const int col0 = (warp >> 2) * half, pieces = half / 16;
-        int st = 0, buf = 0;
-        unsigned s_phase = 0, acc_phase = 0;
+        int raw = 0, buf = 0;
+        unsigned raw_phase = 0, acc_phase = 0;
         for (int gi = 0; gi < n_groups; ++gi) {
             const int q = gi & (CG - 1);
-            if (q == 0 && !warp_wait(&ctl.s_full[st], s_phase, abort)) break;
+            if (q == 0 && !warp_wait(&ctl.raw_full[raw], raw_phase, abort)) break;
             // strip (warp % 4) of the tile is the warp's lanes
-            const unsigned char *u = scales + (((st * P * 4 + (warp & 3)) * CG + q) * 32 + lane) * 2;
+            const unsigned char *u = raws + raw * raw_bytes + (warp & 3) * chunk_bytes + q * a.unit + 16 * G + 2 * lane;
             unsigned long long s[P];
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-                const float f = w4_scale(*reinterpret_cast<const uint16_t *>(u + i * 4 * CG * 64), a.bf16);
+                const float f = w4_scale(*reinterpret_cast<const uint16_t *>(u + i * 4 * chunk_bytes), a.bf16);
                 s[i] = pack2(__float_as_uint(f), __float_as_uint(f));
             }
             if (!warp_wait(&ctl.acc_full[buf], acc_phase, abort)) break;
@@ -233,28 +255,35 @@ __global__ void __launch_bounds__(kThreadsG, 1)
 #pragma unroll
             for (int i = 0; i < P; ++i)
 #pragma unroll
-                for (int c = 0; c < kPerAcc; c += 2)
+                for (int c = 0; c < kPerAcc; c += 4)
                     if (c < pieces) {
-                        uint32_t v0[16], v1[16];
-                        tmem_ld16(at + i * p.rows + 16 * c, v0);
-                        if (c + 1 < pieces) tmem_ld16(at + i * p.rows + 16 * c + 16, v1);
+                        // as many columns at a look as there are registers for: a look costs its latency
+                        uint32_t v[64];
+                        const uint32_t from = at + i * p.rows + 16 * c;
+                        if (c + 4 <= pieces) {
+                            tmem_ld64(from, v);
+                        } else {
+                            tmem_ld16(from, v);
+                            if (c + 1 < pieces) tmem_ld16(from + 16, v + 16);
+                            if (c + 2 < pieces) tmem_ld16(from + 32, v + 32);
+                        }
                         tmem_wait();
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) fma2(acc[8 * (i * kPerAcc + c) + e], s[i], pack2(v0[2 * e], v0[2 * e + 1]));
-                        if (c + 1 < pieces) {
+                        for (int k = 0; k < 4; ++k)
+                            if (c + k < pieces) {
 #pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                fma2(acc[8 * (i * kPerAcc + c + 1) + e], s[i], pack2(v1[2 * e], v1[2 * e + 1]));
-                        }
+                                for (int e = 0; e < 8; ++e)
+                                    fma2(acc[8 * (i * kPerAcc + c + k) + e], s[i], pack2(v[16 * k + 2 * e], v[16 * k + 2 * e + 1]));
+                            }
                     }
             fence_before();
             __syncwarp();
             if (lane == 0) {
                 w4_arrive(&ctl.acc_empty[buf]);
-                if (q == CG - 1) w4_arrive(&ctl.s_empty[st]);
+                if (q == CG - 1) w4_arrive(&ctl.raw_empty[raw]);
             }
             if (++buf == p.accs) buf = 0, acc_phase ^= 1;
-            if (q == CG - 1 && ++st == kScaleStages) st = 0, s_phase ^= 1;
+            if (q == CG - 1 && ++raw == p.raws) raw = 0, raw_phase ^= 1;
         }
         // The last group's sums are in: every MMA of the CTA is done, and with them every use of the operands, where the
         // carries go now, [P][rows][128].  Straight from registers to the output, a store and a residual's load at a time,
@@ -277,19 +306,21 @@ __global__ void __launch_bounds__(kThreadsG, 1)
                 }
     } else {
         if (FW == 1)
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
         else
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         if (warp < kConvertEnd) {
             // ---- convert ----
-            const int team = (warp - kConvert) >> 2, strip = warp & 3, g = lane >> 2, t = lane & 3, odd = g & 1;
+            const int team = (warp - kConvert) / kTeam, strip0 = (warp & (kTeam - 1)) * (4 / kTeam);
+            const int g = lane >> 2, t = lane & 3, odd = g & 1;
             int raw = 0, slot = team;
             unsigned raw_phase = 0, phase = 1;  // a fresh barrier passes for the phase before its first
-            for (int j = team; j < n_steps; j += kTeams) {
+            for (int j = team; j < n_steps; j += 2) {  // a team has one step of every chunk
                 if (!warp_wait(&ctl.raw_full[raw], raw_phase, abort)) break;
                 if (!warp_wait(&ctl.empty[slot], phase, abort)) break;
 #pragma unroll
-                for (int pp = 0; pp < P; ++pp) {
+                for (int k = 0; k < P * (4 / kTeam); ++k) {
+                    const int pp = k % P, strip = strip0 + k / P;
                     const unsigned char *from = raws + raw * raw_bytes + (4 * pp + strip) * chunk_bytes;
                     unsigned char *operand = slots + slot * slot_bytes + pp * kOperand + strip * 32 * 128 + g * 128;
                     // the step's units: half of one, one, or two
@@ -329,50 +360,32 @@ __global__ void __launch_bounds__(kThreadsG, 1)
                     w4_arrive(&ctl.full[slot]);
                     w4_arrive(&ctl.raw_empty[raw]);
                 }
-                if ((kTeams == 2 || (j & 1)) && ++raw == p.raws) raw = 0, raw_phase ^= 1;
-                if ((slot += kTeams) >= p.slots) slot -= p.slots, phase ^= 1;
+                if (++raw == p.raws) raw = 0, raw_phase ^= 1;
+                if ((slot += 2) >= p.slots) slot -= p.slots, phase ^= 1;
             }
-        } else if (warp == kLoadWarp) {
-            // ---- load units (one lane) ----
+        } else if (warp == kLoadWarp || (P == 2 && warp == kLoadUpWarp)) {
+            // ---- load units (one lane; of the gated pair a warp for each weight: a bulk copy takes some 150 clocks) ----
             if (lane == 0) {
+                const int pp = warp == kLoadWarp ? 0 : 1;
                 const size_t strip_bytes = (size_t)groups * a.unit;
-                const unsigned char *src[P];
-#pragma unroll
-                for (int i = 0; i < P; ++i)
-                    src[i] = (i ? a.part[1].w : to.w) + (size_t)4 * tile * strip_bytes + (size_t)c0 * chunk_bytes;
+                const unsigned char *src =
+                    (pp ? a.part[1].w : to.w) + (size_t)4 * tile * strip_bytes + (size_t)c0 * chunk_bytes;
+                unsigned char *dst = raws + 4 * pp * chunk_bytes;
                 if (!p.prefetch) asm volatile("griddepcontrol.wait;" ::: "memory");
-                int i = 0, raw = 0, st = 0;
-                unsigned raw_phase = 1, s_phase = 1;
-                for (; i < n_chunks; ++i) {
+                int i = 0, raw = 0;
+                unsigned raw_phase = 1;
+                for (; i < n_chunks; ++i, src += chunk_bytes) {
                     if (!wait(&ctl.raw_empty[raw], raw_phase, abort)) break;
-                    const int have = min(CG, groups - (c0 + i) * CG);
-                    const unsigned bytes = (unsigned)(have * a.unit);
-                    w4_arrive_tx(&ctl.raw_full[raw], bytes * (unsigned)(P * strips));
+                    const unsigned bytes = (unsigned)(min(CG, groups - (c0 + i) * CG) * a.unit);
+                    w4_arrive_tx(&ctl.raw_full[raw], bytes * (unsigned)strips);
 #pragma unroll
-                    for (int pp = 0; pp < P; ++pp)
-                        for (int s = 0; s < strips; ++s)
-                            w4_copy(raws + raw * raw_bytes + (4 * pp + s) * chunk_bytes, src[pp] + s * strip_bytes, bytes,
-                                    &ctl.raw_full[raw]);
-                    // the scales once more, where they wait for the fold
-                    if (!wait(&ctl.s_empty[st], s_phase, abort)) break;
-                    w4_arrive_tx(&ctl.s_full[st], (unsigned)(have * P * strips * 64));
-#pragma unroll
-                    for (int pp = 0; pp < P; ++pp) {
-                        for (int s = 0; s < strips; ++s)
-                            for (int q = 0; q < have; ++q)
-                                w4_copy(scales + (((st * P + pp) * 4 + s) * CG + q) * 64,
-                                        src[pp] + s * strip_bytes + q * a.unit + 16 * G, 64, &ctl.s_full[st]);
-                        src[pp] += chunk_bytes;
-                    }
+                    for (int s = 0; s < 4; ++s)
+                        if (s < strips)
+                            w4_copy(dst + raw * raw_bytes + s * chunk_bytes, src + s * strip_bytes, bytes, &ctl.raw_full[raw]);
                     if (++raw == p.raws) raw = 0, raw_phase ^= 1;
-                    if (++st == kScaleStages) st = 0, s_phase ^= 1;
                 }
-                if (*abort) {  // what was asked for lands before the memory is used again
-                    for (int k = max(0, i + 1 - p.raws); k <= i && k < n_chunks; ++k)
-                        w4_wait(&ctl.raw_full[k % p.raws], (k / p.raws) & 1);
-                    for (int k = max(0, i - kScaleStages); k < i; ++k)
-                        w4_wait(&ctl.s_full[k % kScaleStages], (k / kScaleStages) & 1);
-                }
+                if (*abort)  // what was asked for lands before the memory is used again
+                    for (int k = max(0, i - p.raws); k < i; ++k) w4_wait(&ctl.raw_full[k % p.raws], (k / p.raws) & 1);
             }
             __syncwarp();
         } else if (warp == kXWarp) {
@@ -572,9 +585,9 @@ cudaError_t launch_w4_gemm(const W4Args &a, bool constant_weights, cudaStream_t 
     if (const char *v = getenv("W4_GKS")) p.ks = atoi(v);
     p.accs = 512 / (P * p.rows) < kMaxAcc ? 512 / (P * p.rows) : kMaxAcc;
     const int raw = P * 4 * (kChunkK / a.group) * a.unit, slot = P * kOperand + p.rows * 128;
-    const int fixed = (int)sizeof(Control) + kScaleStages * P * 4 * (kChunkK / a.group) * 64;
-    p.slots = (kMaxSmemG - fixed - 3 * raw) / slot;  // at least 3, and 3 raw stages, for every size
-    if (p.slots > 5) p.slots = 5;
+    const int fixed = (int)sizeof(Control);
+    p.slots = 3;
+    if (const char *v = getenv("W4_SLOTS")) p.slots = atoi(v);
     p.raws = (kMaxSmemG - fixed - p.slots * slot) / raw;
     if (p.raws > kMaxStages) p.raws = kMaxStages;
     const int smem = fixed + p.slots * slot + p.raws * raw;
