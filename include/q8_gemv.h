@@ -542,7 +542,7 @@ typedef struct {
  * temperature (NULL) the noise is not added.
  *   logits  device, fp32 [m][ldl]      out  device, fp32 [m][ldo], or NULL (only idx is written); may be logits itself with
  *   idx     device, int64 [m]                ldo == ldl (in place), and may not overlap an input otherwise
- *   1 <= m <= 65535, 1 <= N < 2^31 - 1024, pitches at least N (history_pitch >= history_width, mask_pitch >= ceil(N / 32))
+ *   1 <= m <= 65535, 1 <= N <= 2^30, pitches at least N (history_pitch >= history_width, mask_pitch >= ceil(N / 32))
  *   history_width <= Q8_MAX_HISTORY, bias_width <= Q8_MAX_BIAS, both >= 1 where given
  * Lengths beyond history_width count as it, negative ones as 0, as do prompts; tokens of the history outside 0..N-1 are
  * passed over.  repetition is expected positive.  One launch.

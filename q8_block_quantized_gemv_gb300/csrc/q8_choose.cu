@@ -1,5 +1,15 @@
-// The rules on logits and the token chosen, first form: one CTA a row, the counts of a window of the vocabulary at a time in
-// shared memory, the history read again for each window.
+// The rules on logits and the token chosen (formulas in q8_gemv.h): one cluster of up to eight CTAs a row, one pass over the
+// logits.
+//
+// 8 bytes a logit, 4 more with noise, bound a large step; what has to stay out of their way is the look-up of how often a
+// token was said.  Each CTA owns a slice of the vocabulary and holds one word for each of its tokens in shared memory: how
+// often it stands in the answer, whether it stands in the prompt, its place among the biases.  The words come from integer
+// atomics, whose order does not matter.  A history of up to kLocal tokens is read whole by every CTA of the row, which keeps
+// what falls into its slice and needs no word from the others; of a longer one each CTA reads its share and sends what it
+// finds to the owner through distributed shared memory.  A vocabulary beyond eight slices of kMostSlice takes several turns.
+// The first logits are asked for before the words are made.  Each step of a rule is one fp32 operation rounded once (no
+// contraction), so that the bits are those of any other implementation.
+#include <cooperative_groups.h>
 #include <limits.h>
 #include <math.h>
 
@@ -10,9 +20,11 @@ namespace q8 {
 namespace {
 
 constexpr int kThreadsC = 512;
-constexpr int kWindow = 8192;  // tokens whose counts are in shared memory at a time
+constexpr int kMostCtas = 8;
+constexpr int kMostSlice = 49152;  // 192 KB of words
+constexpr int kLocal = 8192;
 
-// A token's entry: how often it stands in the answer in the low 20 bits, its place among the biases + 1 in the next 11,
+// A token's word: how often it stands in the answer in the low 20 bits, its place among the biases + 1 in the next 11,
 // and whether it stands in the prompt.
 constexpr uint32_t kCount = 0xFFFFFu, kPrompt = 0x80000000u;
 
@@ -22,20 +34,61 @@ struct ChooseArgs {
     float *out;
     int64_t *idx;
     int ldl, ldo, N;
+    int slice;   // tokens of a CTA, a multiple of 128
+    bool words;  // whether any rule needs them
 };
 
-__device__ __forceinline__ int64_t token_at(const q8_choice &c, int r, int i) {
-    const size_t at = (size_t)r * c.history_pitch + i;
-    return c.history_wide ? static_cast<const int64_t *>(c.history)[at] : static_cast<const int *>(c.history)[at];
+struct Row {  // a row's numbers
+    float rep, freq, pres, temp;
+    bool hot;  // a temperature above 0
+    const float *bias;
+};
+
+// The rules on one logit; what is hidden is replaced by the caller.
+__device__ __forceinline__ float ruled(float v, uint32_t word, const Row &w) {
+    if (word) {
+        if (word & (kPrompt | kCount)) v = v > 0.0f ? __fdiv_rn(v, w.rep) : __fmul_rn(v, w.rep);
+        if (word & kCount) {
+            v = __fsub_rn(v, __fmul_rn(w.freq, (float)(word & kCount)));
+            v = __fsub_rn(v, w.pres);
+        }
+        const uint32_t place = (word & ~kPrompt) >> 20;
+        if (place) v = __fadd_rn(v, w.bias[place - 1]);
+    }
+    return w.hot ? __fdiv_rn(v, w.temp) : v;
 }
 
-__global__ void __launch_bounds__(kThreadsC) choose_kernel(const __grid_constant__ ChooseArgs a) {
-    __shared__ uint32_t entry[kWindow];
-    __shared__ unsigned long long best[kThreadsC / 32];
+// A score as a whole number of the same order: -0 as +0, NaN above all.
+__device__ __forceinline__ uint32_t order_of(float v) {
+    const uint32_t b = __float_as_uint(v + 0.0f);
+    return v != v ? 0xFFFFFFFFu : b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
+}
+
+// VEC: rows of logits, output and noise are 16-byte aligned, a thread takes four tokens in a row; else four that are
+// kThreadsC apart.
+template <bool VEC, bool WIDE>
+__global__ void __launch_bounds__(kThreadsC, 2) choose_kernel(const __grid_constant__ ChooseArgs a) {
+    namespace cg = cooperative_groups;
+    extern __shared__ __align__(16) uint32_t word_of[];
+    __shared__ unsigned long long best[kThreadsC / 32], of_rank[kMostCtas];
+    cg::cluster_group cluster = cg::this_cluster();
     const q8_choice &c = a.c;
-    const int r = blockIdx.x;
-    const float rep = c.repetition ? c.repetition[r] : 1.0f, freq = c.frequency ? c.frequency[r] : 0.0f;
-    const float pres = c.presence ? c.presence[r] : 0.0f, temp = c.temperature ? c.temperature[r] : 0.0f;
+    const int ctas = (int)gridDim.x, rank = (int)blockIdx.x, r = (int)blockIdx.y, slice = a.slice;
+    const int turn = ctas * slice;  // tokens of a turn
+    auto clear = [&](int count) {
+        for (int i = threadIdx.x; i < (count + 3) / 4; i += kThreadsC)
+            reinterpret_cast<uint4 *>(word_of)[i] = make_uint4(0u, 0u, 0u, 0u);
+    };
+    if (a.words) clear(min(slice, max(0, a.N - rank * slice)));
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    Row row;
+    row.rep = c.repetition ? c.repetition[r] : 1.0f;
+    row.freq = c.frequency ? c.frequency[r] : 0.0f;
+    row.pres = c.presence ? c.presence[r] : 0.0f;
+    row.temp = c.temperature ? c.temperature[r] : 0.0f;
+    row.hot = row.temp > 0.0f;
+    row.bias = c.bias ? c.bias + (size_t)r * c.bias_width : nullptr;
     int length = 0, prompt = 0;
     if (c.history) {
         length = min(max(c.lengths[r], 0), c.history_width);
@@ -43,59 +96,175 @@ __global__ void __launch_bounds__(kThreadsC) choose_kernel(const __grid_constant
     }
     const int mrow = c.mask ? (c.mask_rows ? c.mask_rows[r] : r) : -1;
     const int *mask = mrow >= 0 && mrow < c.mask_count ? c.mask + (size_t)mrow * c.mask_pitch : nullptr;
-    unsigned long long key = 0ull;
-    for (int n0 = 0; n0 < a.N; n0 += kWindow) {
-        const int count = min(kWindow, a.N - n0);
-        for (int i = threadIdx.x; i < count; i += kThreadsC) entry[i] = 0u;
-        __syncthreads();
-        if (c.bias_ids)
-            for (int i = threadIdx.x; i < c.bias_width; i += kThreadsC) {
-                const int n = c.bias_ids[(size_t)r * c.bias_width + i];
-                if (n >= n0 && n < n0 + count) atomicMax(&entry[n - n0], (uint32_t)(i + 1) << 20);
-            }
-        __syncthreads();
-        for (int i = threadIdx.x; i < length; i += kThreadsC) {
-            const int64_t n = token_at(c, r, i);
-            if (n >= n0 && n < n0 + count) {
-                if (i < prompt)
-                    atomicOr(&entry[n - n0], kPrompt);
-                else
-                    atomicAdd(&entry[n - n0], 1u);
+    const float *noise = c.noise && row.hot ? c.noise + (size_t)r * c.noise_pitch : nullptr;
+    const float *logits = a.logits + (size_t)r * a.ldl;
+    float *out = a.out ? a.out + (size_t)r * a.ldo : nullptr;
+    const size_t said = (size_t)r * c.history_pitch;
+    const bool far = length > kLocal && ctas > 1;  // a history that the CTAs share out
+    const bool any = a.words && (length > 0 || c.bias_ids);
+    // The CTAs of a cluster have all started when this is waited for, before the first write into another's memory (a
+    // history that is shared out has cluster-wide barriers of its own first).
+    if (!far) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+
+    auto load4 = [&](const float *p, int n, int end, float (&v)[4]) {  // the thread's tokens from n on
+        if (VEC && n + 4 <= end) {
+            const float4 f = __ldcs(reinterpret_cast<const float4 *>(p + n));
+            v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int at = n + (VEC ? e : e * kThreadsC);
+                v[e] = at < end ? __ldcs(p + at) : 0.0f;
             }
         }
-        __syncthreads();
-        for (int i = threadIdx.x; i < count; i += kThreadsC) {
-            const int n = n0 + i;
-            float v = a.logits[(size_t)r * a.ldl + n];
-            const uint32_t e = entry[i];
-            if (e & (kPrompt | kCount)) v = v > 0.0f ? __fdiv_rn(v, rep) : __fmul_rn(v, rep);
-            if (e & kCount) {
-                v = __fsub_rn(v, __fmul_rn(freq, (float)(e & kCount)));
-                v = __fsub_rn(v, pres);
+    };
+    uint32_t top = 0u;
+    int top_n = INT_MAX;  // the thread's best score and token: none yet
+    for (int base = 0; base < a.N; base += turn) {
+        const int first = base + rank * slice, end = min(a.N, first + slice);
+        constexpr int kTake = 4 * kThreadsC, kAhead = 2;  // tokens of the CTA at a time; as many times in flight
+        const int mine = first + (VEC ? 4 : 1) * (int)threadIdx.x;
+        float v[kAhead][4];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) load4(logits, mine + k * kTake, end, v[k]);
+        if (any) {
+            if (base > 0) {
+                __syncthreads();
+                clear(max(0, end - first));
             }
-            const uint32_t place = (e & ~kPrompt) >> 20;
-            if (place) v = __fadd_rn(v, c.bias[(size_t)r * c.bias_width + place - 1]);
-            if (temp > 0.0f) v = __fdiv_rn(v, temp);
-            const bool allowed = !mask || (mask[n >> 5] >> (n & 31)) & 1;
-            if (allowed) {
-                const float score = c.noise && temp > 0.0f ? __fadd_rn(v, c.noise[(size_t)r * c.noise_pitch + n]) : v;
-                const unsigned long long k = argmax_key(score, n);
-                key = k > key ? k : key;
+            __syncthreads();
+            if (c.bias_ids) {
+                for (int i = threadIdx.x; i < c.bias_width; i += kThreadsC) {
+                    const int n = c.bias_ids[(size_t)r * c.bias_width + i];
+                    if (n >= first && n < end) atomicMax(word_of + n - first, (uint32_t)(i + 1) << 20);
+                }
+                __syncthreads();
             }
-            if (a.out) a.out[(size_t)r * a.ldo + n] = allowed ? v : -INFINITY;
+            if (far) cluster.sync();  // every CTA's words are ready for the others
+            const int from = far ? (int)((long long)length * rank / ctas) : 0;
+            const int to = far ? (int)((long long)length * (rank + 1) / ctas) : length;
+            constexpr int kTokens = 8;  // of a thread in flight
+            for (int i0 = from + (int)threadIdx.x; i0 < to; i0 += kTokens * kThreadsC) {
+                long long n[kTokens];
+#pragma unroll
+                for (int k = 0; k < kTokens; ++k) {
+                    const int i = i0 + k * kThreadsC;
+                    n[k] = i >= to  ? -1
+                           : WIDE ? static_cast<const long long *>(c.history)[said + i]
+                                  : static_cast<const int *>(c.history)[said + i];
+                }
+#pragma unroll
+                for (int k = 0; k < kTokens; ++k) {
+                    const bool in_prompt = i0 + k * kThreadsC < prompt;
+                    uint32_t *w = nullptr;
+                    if (!far) {
+                        if (n[k] >= first && n[k] < end) w = word_of + (int)(n[k] - first);
+                    } else if (n[k] >= base && n[k] < min(a.N, base + turn)) {
+                        const int owner = (int)(n[k] - base) / slice;
+                        w = cluster.map_shared_rank(word_of, owner) + ((int)(n[k] - base) - owner * slice);
+                    }
+                    if (w) {
+                        if (in_prompt)
+                            atomicOr(w, kPrompt);
+                        else
+                            atomicAdd(w, 1u);
+                    }
+                }
+            }
+            if (far)
+                cluster.sync();
+            else
+                __syncthreads();
         }
-        __syncthreads();
+        for (int n0 = mine; n0 - mine + first < end; n0 += kAhead * kTake) {
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int n = n0 + k * kTake;
+                float x[4] = {v[k][0], v[k][1], v[k][2], v[k][3]}, g[4];
+                load4(logits, n + kAhead * kTake, end, v[k]);
+                if (noise) load4(noise, n, end, g);
+                if (n < end) {
+                    uint32_t words[4] = {0u, 0u, 0u, 0u};
+                    if (any) {
+                        if (VEC) {
+                            const uint4 w4 = *reinterpret_cast<const uint4 *>(word_of + (n - first));  // slices of whole 128s
+                            words[0] = w4.x, words[1] = w4.y, words[2] = w4.z, words[3] = w4.w;
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (n + e * kThreadsC < end) words[e] = word_of[n + e * kThreadsC - first];
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int at = n + (VEC ? e : e * kThreadsC);
+                        if (at >= end) continue;
+                        const bool allowed = !mask || ((mask[at >> 5] >> (at & 31)) & 1);
+                        x[e] = ruled(x[e], words[e], row);
+                        if (allowed) {
+                            const uint32_t o = order_of(noise ? __fadd_rn(x[e], g[e]) : x[e]);
+                            if (o > top || top_n == INT_MAX) top = o, top_n = at;  // tokens come in ascending order
+                        } else {
+                            x[e] = -INFINITY;
+                        }
+                    }
+                    if (out) {
+                        if (VEC && n + 4 <= end) {
+                            __stcs(reinterpret_cast<float4 *>(out + n), make_float4(x[0], x[1], x[2], x[3]));
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int at = n + (VEC ? e : e * kThreadsC);
+                                if (at < end) __stcs(out + at, x[e]);
+                            }
+                        }
+                    }
+                }
+            }
+        }
     }
+    // the row's best: the highest score, of equal ones the lowest token; 0 for none
+    unsigned long long key =
+        top_n == INT_MAX ? 0ull : ((unsigned long long)top << 32) | (unsigned long long)(0xFFFFFFFFu - (uint32_t)top_n);
     for (int o = 16; o > 0; o >>= 1) {
         const unsigned long long other = __shfl_xor_sync(0xffffffffu, key, o);
         key = other > key ? other : key;
     }
     if ((threadIdx.x & 31) == 0) best[threadIdx.x >> 5] = key;
     __syncthreads();
+    if (!far) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     if (threadIdx.x == 0) {
         for (int w = 1; w < kThreadsC / 32; ++w) key = best[w] > key ? best[w] : key;
+        cluster.map_shared_rank(of_rank, 0)[rank] = key;
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    cluster.sync();
+    if (rank == 0 && threadIdx.x == 0) {
+        key = of_rank[0];
+        for (int k = 1; k < ctas; ++k) key = of_rank[k] > key ? of_rank[k] : key;
         a.idx[r] = key ? (int64_t)(0xFFFFFFFFull - (key & 0xFFFFFFFFull)) : -1;
     }
+}
+
+template <bool VEC, bool WIDE> cudaError_t launch_choose(const ChooseArgs &a, int ctas, int m, cudaStream_t stream) {
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t e = kv_allow_smem(choose_kernel<VEC, WIDE>, 4 * kMostSlice, &allowed);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas, (unsigned)m, 1);
+    cfg.blockDim = dim3(kThreadsC, 1, 1);
+    cfg.dynamicSmemBytes = a.words ? 4 * (size_t)a.slice : 0;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)ctas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, choose_kernel<VEC, WIDE>, a);
 }
 
 }  // namespace
@@ -106,7 +275,7 @@ extern "C" q8_status q8_choose(const float *logits, int ldl, const q8_choice *ru
     using q8::kv_aligned;
     using q8::kv_overlap;
     if (!logits || !idx) return Q8_ERR_ARG;
-    if (m < 1 || m > 65535 || N < 1 || N >= INT_MAX - 1023 || ldl < N || (out && ldo < N)) return Q8_ERR_SHAPE;
+    if (m < 1 || m > 65535 || N < 1 || N > (1 << 30) || ldl < N || (out && ldo < N)) return Q8_ERR_SHAPE;
     q8::ChooseArgs a = {};
     if (rules) a.c = *rules;
     const q8_choice &c = a.c;
@@ -139,7 +308,18 @@ extern "C" q8_status q8_choose(const float *logits, int ldl, const q8_choice *ru
     a.ldl = ldl;
     a.ldo = ldo;
     a.N = N;
-    q8::choose_kernel<<<m, q8::kThreadsC, 0, (cudaStream_t)stream>>>(a);
-    const cudaError_t e = cudaGetLastError();
+    a.words = c.history || c.bias_ids;
+    // Eight CTAs a row, fewer where a slice would be less than 2048 tokens (one turn of a CTA's threads).
+    int ctas = 1;
+    while (ctas < q8::kMostCtas && ctas * 2048 < N) ctas *= 2;
+    const int slice = ((N + ctas - 1) / ctas + 127) / 128 * 128;
+    a.slice = slice < q8::kMostSlice ? slice : q8::kMostSlice;
+    auto quad = [](const void *p, int pitch) { return !p || (kv_aligned(p, 16) && pitch % 4 == 0); };
+    const bool vec = quad(logits, ldl) && quad(out, ldo) && quad(c.noise, c.noise_pitch);
+    const cudaStream_t cs = (cudaStream_t)stream;
+    const cudaError_t e = vec ? (c.history_wide ? q8::launch_choose<true, true>(a, ctas, m, cs)
+                                                : q8::launch_choose<true, false>(a, ctas, m, cs))
+                              : (c.history_wide ? q8::launch_choose<false, true>(a, ctas, m, cs)
+                                                : q8::launch_choose<false, false>(a, ctas, m, cs));
     return e == cudaSuccess ? Q8_OK : q8::kv_cuda_fail(e);
 }
