@@ -40,28 +40,33 @@ struct ChooseArgs {
 
 struct Row {  // a row's numbers
     float rep, freq, pres, temp;
-    bool hot;  // a temperature above 0
+    float inv, span;  // 1 / temp; the quotients that over_temperature makes without a division are of |v| in 1/span .. span
     const float *bias;
 };
 
-// The rules on one logit; what is hidden is replaced by the caller.
+// The rules of a word on a logit.
 __device__ __forceinline__ float ruled(float v, uint32_t word, const Row &w) {
-    if (word) {
-        if (word & (kPrompt | kCount)) v = v > 0.0f ? __fdiv_rn(v, w.rep) : __fmul_rn(v, w.rep);
-        if (word & kCount) {
-            v = __fsub_rn(v, __fmul_rn(w.freq, (float)(word & kCount)));
-            v = __fsub_rn(v, w.pres);
-        }
-        const uint32_t place = (word & ~kPrompt) >> 20;
-        if (place) v = __fadd_rn(v, w.bias[place - 1]);
+    if (word & (kPrompt | kCount)) v = v > 0.0f ? __fdiv_rn(v, w.rep) : __fmul_rn(v, w.rep);
+    if (word & kCount) {
+        v = __fsub_rn(v, __fmul_rn(w.freq, (float)(word & kCount)));
+        v = __fsub_rn(v, w.pres);
     }
-    return w.hot ? __fdiv_rn(v, w.temp) : v;
+    const uint32_t place = (word & ~kPrompt) >> 20;
+    if (place) v = __fadd_rn(v, w.bias[place - 1]);
+    return v;
 }
 
-// A score as a whole number of the same order: -0 as +0, NaN above all.
-__device__ __forceinline__ uint32_t order_of(float v) {
-    const uint32_t b = __float_as_uint(v + 0.0f);
-    return v != v ? 0xFFFFFFFFu : b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
+// v / temp, rounded once, for every logit of a row.  With y the correctly rounded 1 / temp, v y is within two units in the
+// last place, one correction by its remainder makes it one of the two nearest, whose remainder v - q temp is exact in one
+// fma, and q + remainder * y is then the correctly rounded quotient (Markstein's theorem), where nothing over- or
+// underflows.  Elsewhere, and for zeros, whose sign the remainder loses, the division itself.  A division of each logit took
+// more instructions than everything else.
+__device__ __forceinline__ float over_temperature(float v, const Row &w) {
+    float q = v * w.inv;
+    q = fmaf(fmaf(-q, w.temp, v), w.inv, q);
+    q = fmaf(fmaf(-q, w.temp, v), w.inv, q);
+    const float size = fabsf(v);
+    return size <= w.span && size * w.span >= 1.0f ? q : __fdiv_rn(v, w.temp);
 }
 
 // VEC: rows of logits, output and noise are 16-byte aligned, a thread takes four tokens in a row; else four that are
@@ -87,7 +92,9 @@ __global__ void __launch_bounds__(kThreadsC, 2) choose_kernel(const __grid_const
     row.freq = c.frequency ? c.frequency[r] : 0.0f;
     row.pres = c.presence ? c.presence[r] : 0.0f;
     row.temp = c.temperature ? c.temperature[r] : 0.0f;
-    row.hot = row.temp > 0.0f;
+    const bool hot = row.temp > 0.0f;
+    row.inv = __frcp_rn(row.temp);
+    row.span = row.temp >= 0x1p-20f && row.temp <= 0x1p20f ? 0x1p80f : 0.0f;  // 0: none
     row.bias = c.bias ? c.bias + (size_t)r * c.bias_width : nullptr;
     int length = 0, prompt = 0;
     if (c.history) {
@@ -96,7 +103,7 @@ __global__ void __launch_bounds__(kThreadsC, 2) choose_kernel(const __grid_const
     }
     const int mrow = c.mask ? (c.mask_rows ? c.mask_rows[r] : r) : -1;
     const int *mask = mrow >= 0 && mrow < c.mask_count ? c.mask + (size_t)mrow * c.mask_pitch : nullptr;
-    const float *noise = c.noise && row.hot ? c.noise + (size_t)r * c.noise_pitch : nullptr;
+    const float *noise = c.noise && hot ? c.noise + (size_t)r * c.noise_pitch : nullptr;
     const float *logits = a.logits + (size_t)r * a.ldl;
     float *out = a.out ? a.out + (size_t)r * a.ldo : nullptr;
     const size_t said = (size_t)r * c.history_pitch;
@@ -106,7 +113,12 @@ __global__ void __launch_bounds__(kThreadsC, 2) choose_kernel(const __grid_const
     // history that is shared out has cluster-wide barriers of its own first).
     if (!far) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 
-    auto load4 = [&](const float *p, int n, int end, float (&v)[4]) {  // the thread's tokens from n on
+    // Four tokens of a thread from n on: their logits, noise, and masks (bit e: token e is allowed)
+    struct Batch {
+        float x[4], g[4];
+        uint32_t allowed;
+    };
+    auto load4 = [&](const float *p, int n, int end, float (&v)[4]) {
         if (VEC && n + 4 <= end) {
             const float4 f = __ldcs(reinterpret_cast<const float4 *>(p + n));
             v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
@@ -118,15 +130,32 @@ __global__ void __launch_bounds__(kThreadsC, 2) choose_kernel(const __grid_const
             }
         }
     };
-    uint32_t top = 0u;
+    auto load = [&](int n, int end, Batch &b) {
+        load4(logits, n, end, b.x);
+        if (noise) load4(noise, n, end, b.g);
+        b.allowed = 15u;
+        if (mask) {
+            if (VEC) {
+                if (n < end) b.allowed = (uint32_t)mask[n >> 5] >> (n & 31);  // whose four are of one word
+            } else {
+                b.allowed = 0u;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int at = n + e * kThreadsC;
+                    if (at < end) b.allowed |= (((uint32_t)mask[at >> 5] >> (at & 31)) & 1u) << e;
+                }
+            }
+        }
+    };
+    float top = -INFINITY;
     int top_n = INT_MAX;  // the thread's best score and token: none yet
     for (int base = 0; base < a.N; base += turn) {
         const int first = base + rank * slice, end = min(a.N, first + slice);
         constexpr int kTake = 4 * kThreadsC, kAhead = 2;  // tokens of the CTA at a time; as many times in flight
         const int mine = first + (VEC ? 4 : 1) * (int)threadIdx.x;
-        float v[kAhead][4];
+        Batch ahead[kAhead];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) load4(logits, mine + k * kTake, end, v[k]);
+        for (int k = 0; k < kAhead; ++k) load(mine + k * kTake, end, ahead[k]);
         if (any) {
             if (base > 0) {
                 __syncthreads();
@@ -180,33 +209,43 @@ __global__ void __launch_bounds__(kThreadsC, 2) choose_kernel(const __grid_const
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
                 const int n = n0 + k * kTake;
-                float x[4] = {v[k][0], v[k][1], v[k][2], v[k][3]}, g[4];
-                load4(logits, n + kAhead * kTake, end, v[k]);
-                if (noise) load4(noise, n, end, g);
+                Batch now = ahead[k];
+                load(n + kAhead * kTake, end, ahead[k]);
                 if (n < end) {
-                    uint32_t words[4] = {0u, 0u, 0u, 0u};
+                    float(&x)[4] = now.x;
                     if (any) {
+                        uint32_t words[4];
                         if (VEC) {
                             const uint4 w4 = *reinterpret_cast<const uint4 *>(word_of + (n - first));  // slices of whole 128s
                             words[0] = w4.x, words[1] = w4.y, words[2] = w4.z, words[3] = w4.w;
                         } else {
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
-                                if (n + e * kThreadsC < end) words[e] = word_of[n + e * kThreadsC - first];
+                                words[e] = n + e * kThreadsC < end ? word_of[n + e * kThreadsC - first] : 0u;
+                        }
+                        if (words[0] | words[1] | words[2] | words[3]) {  // (past the end what they hold goes nowhere)
+#pragma unroll 1
+                            for (int e = 0; e < 4; ++e) {
+                                const uint32_t w = e == 0 ? words[0] : e == 1 ? words[1] : e == 2 ? words[2] : words[3];
+                                if (w) {
+                                    const float v = ruled(e == 0 ? x[0] : e == 1 ? x[1] : e == 2 ? x[2] : x[3], w, row);
+                                    if (e == 0) x[0] = v;
+                                    if (e == 1) x[1] = v;
+                                    if (e == 2) x[2] = v;
+                                    if (e == 3) x[3] = v;
+                                }
+                            }
                         }
                     }
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int at = n + (VEC ? e : e * kThreadsC);
-                        if (at >= end) continue;
-                        const bool allowed = !mask || ((mask[at >> 5] >> (at & 31)) & 1);
-                        x[e] = ruled(x[e], words[e], row);
-                        if (allowed) {
-                            const uint32_t o = order_of(noise ? __fadd_rn(x[e], g[e]) : x[e]);
-                            if (o > top || top_n == INT_MAX) top = o, top_n = at;  // tokens come in ascending order
-                        } else {
-                            x[e] = -INFINITY;
-                        }
+                        if (hot) x[e] = over_temperature(x[e], row);
+                        const bool allowed = (now.allowed >> e) & 1u;
+                        if (!allowed) x[e] = -INFINITY;
+                        const float score = noise ? __fadd_rn(x[e], now.g[e]) : x[e];
+                        // larger, or NaN where there was none, or the first (tokens come in ascending order)
+                        if (allowed && at < end && top == top && (!(score <= top) || top_n == INT_MAX)) top = score, top_n = at;
                     }
                     if (out) {
                         if (VEC && n + 4 <= end) {
@@ -224,8 +263,7 @@ __global__ void __launch_bounds__(kThreadsC, 2) choose_kernel(const __grid_const
         }
     }
     // the row's best: the highest score, of equal ones the lowest token; 0 for none
-    unsigned long long key =
-        top_n == INT_MAX ? 0ull : ((unsigned long long)top << 32) | (unsigned long long)(0xFFFFFFFFu - (uint32_t)top_n);
+    unsigned long long key = top_n == INT_MAX ? 0ull : argmax_key(top, top_n);
     for (int o = 16; o > 0; o >>= 1) {
         const unsigned long long other = __shfl_xor_sync(0xffffffffu, key, o);
         key = other > key ? other : key;

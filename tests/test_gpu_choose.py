@@ -167,6 +167,21 @@ def test_logits_of_any_kind():
     run(x, **rules)
 
 
+def test_quotients_are_rounded_once():
+    """Logits over temperatures of every kind, those just below a power of two among them, bit for bit the division's."""
+    m, N = 64, 40000
+    g = np.random.default_rng(30)
+    t = np.exp2(g.uniform(-3, 3, m)).astype(np.float32)
+    t[:8] = np.nextafter(np.exp2(np.arange(-4, 4)).astype(np.float32), np.float32(0))
+    t[8:16] = np.nextafter(np.exp2(np.arange(-4, 4)).astype(np.float32), np.float32(np.inf))
+    t[16:22] = [1.0, 2.0 ** -20, 2.0 ** 20, 2.0 ** -21, 2.0 ** 21, 1e-38]
+    x = (g.standard_normal((m, N)) * np.exp2(g.integers(-8, 8, (m, N)))).astype(np.float32)
+    x[:, ::50] = np.exp2(g.integers(-140, 127, (m, 800))).astype(np.float32)
+    x[:, 1::50] = np.nextafter(np.exp2(g.integers(-90, 90, (m, 800))).astype(np.float32), np.float32(0))
+    x[:, 2::50] = -x[:, 1::50]
+    run(x, temperature=t)
+
+
 def test_history_of_any_kind():
     """Tokens outside the vocabulary, lengths outside the buffer, a token said many times."""
     m, N, width = 6, 500, 400
