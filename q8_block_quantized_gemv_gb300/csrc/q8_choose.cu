@@ -13,13 +13,12 @@
 #include <limits.h>
 #include <math.h>
 
+#include "q8_attn.h"
 #include "q8_device.cuh"
-#include "q8_kv.h"
 
 namespace q8 {
 namespace {
 
-constexpr int kThreadsC = 512;
 constexpr int kMostCtas = 8;
 constexpr int kMostSlice = 49152;  // 192 KB of words
 constexpr int kLocal = 8192;
@@ -38,15 +37,39 @@ struct ChooseArgs {
     bool words;  // whether any rule needs them
 };
 
+struct Divisor {  // of many quotients
+    float by, inv, span;  // 1 / by; the quotients that need no division are of |v| in 1/span .. span (0: none)
+};
+__device__ __forceinline__ Divisor divisor(float by) {
+    return {by, __frcp_rn(by), by >= 0x1p-20f && by <= 0x1p20f ? 0x1p80f : 0.0f};
+}
+// v / by, rounded once, where |v| is in the divisor's span.  With y the correctly rounded 1 / by, v y is within two units in
+// the last place, one correction by its remainder makes it one of the two nearest, whose remainder v - q by is exact in one
+// fma, and q + remainder * y is then the correctly rounded quotient (Markstein's theorem), as nothing over- or underflows.
+// (Of a zero the remainder would lose the sign.)  A division of each logit took more instructions than everything else.
+__device__ __forceinline__ float quotient(float v, const Divisor &d) {
+    float q = v * d.inv;
+    q = fmaf(fmaf(-q, d.by, v), d.inv, q);
+    return fmaf(fmaf(-q, d.by, v), d.inv, q);
+}
+__device__ __forceinline__ bool in_span(float most, float least, const Divisor &d) {
+    return most <= d.span && least * d.span >= 1.0f;
+}
+
 struct Row {  // a row's numbers
-    float rep, freq, pres, temp;
-    float inv, span;  // 1 / temp; the quotients that over_temperature makes without a division are of |v| in 1/span .. span
+    Divisor rep, temp;
+    float freq, pres;
     const float *bias;
 };
 
 // The rules of a word on a logit.
 __device__ __forceinline__ float ruled(float v, uint32_t word, const Row &w) {
-    if (word & (kPrompt | kCount)) v = v > 0.0f ? __fdiv_rn(v, w.rep) : __fmul_rn(v, w.rep);
+    if (word & (kPrompt | kCount)) {
+        if (v > 0.0f)
+            v = in_span(v, v, w.rep) ? quotient(v, w.rep) : __fdiv_rn(v, w.rep.by);
+        else
+            v = __fmul_rn(v, w.rep.by);
+    }
     if (word & kCount) {
         v = __fsub_rn(v, __fmul_rn(w.freq, (float)(word & kCount)));
         v = __fsub_rn(v, w.pres);
@@ -56,45 +79,76 @@ __device__ __forceinline__ float ruled(float v, uint32_t word, const Row &w) {
     return v;
 }
 
-// v / temp, rounded once, for every logit of a row.  With y the correctly rounded 1 / temp, v y is within two units in the
-// last place, one correction by its remainder makes it one of the two nearest, whose remainder v - q temp is exact in one
-// fma, and q + remainder * y is then the correctly rounded quotient (Markstein's theorem), where nothing over- or
-// underflows.  Elsewhere, and for zeros, whose sign the remainder loses, the division itself.  A division of each logit took
-// more instructions than everything else.
-__device__ __forceinline__ float over_temperature(float v, const Row &w) {
-    float q = v * w.inv;
-    q = fmaf(fmaf(-q, w.temp, v), w.inv, q);
-    q = fmaf(fmaf(-q, w.temp, v), w.inv, q);
-    const float size = fabsf(v);
-    return size <= w.span && size * w.span >= 1.0f ? q : __fdiv_rn(v, w.temp);
+// Four logits over the row's temperature.
+__device__ __forceinline__ void over_temperature(float (&x)[4], const Divisor &t) {
+    float q[4], most = 0.0f, least = INFINITY, sum = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        q[e] = quotient(x[e], t);
+        most = fmaxf(most, fabsf(x[e]));
+        least = fminf(least, fabsf(x[e]));
+        sum += q[e];  // of a NaN among them the others do not tell
+    }
+    if (in_span(most, least, t) && sum == sum) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = q[e];
+    } else {
+#pragma unroll 1
+        for (int e = 0; e < 4; ++e) {
+            const float v = __fdiv_rn(x[0], t.by);  // the next in turn
+            x[0] = x[1], x[1] = x[2], x[2] = x[3], x[3] = v;
+        }
+    }
 }
 
-// VEC: rows of logits, output and noise are 16-byte aligned, a thread takes four tokens in a row; else four that are
-// kThreadsC apart.
-template <bool VEC, bool WIDE>
-__global__ void __launch_bounds__(kThreadsC, 2) choose_kernel(const __grid_constant__ ChooseArgs a) {
+// VEC: rows of logits, output and noise are 16-byte aligned, a thread takes four tokens in a row; else four that are T
+// apart.  T threads: 1024 where every CTA has an SM of its own, else 512, two an SM, of which one streams while the other
+// gathers its words.
+template <bool VEC, bool WIDE, int T>
+__global__ void __launch_bounds__(T, 1024 / T) choose_kernel(const __grid_constant__ ChooseArgs a) {
     namespace cg = cooperative_groups;
     extern __shared__ __align__(16) uint32_t word_of[];
-    __shared__ unsigned long long best[kThreadsC / 32], of_rank[kMostCtas];
+    __shared__ unsigned long long best[T / 32], of_rank[kMostCtas];
     cg::cluster_group cluster = cg::this_cluster();
     const q8_choice &c = a.c;
     const int ctas = (int)gridDim.x, rank = (int)blockIdx.x, r = (int)blockIdx.y, slice = a.slice;
     const int turn = ctas * slice;  // tokens of a turn
     auto clear = [&](int count) {
-        for (int i = threadIdx.x; i < (count + 3) / 4; i += kThreadsC)
+        for (int i = threadIdx.x; i < (count + 3) / 4; i += T)
             reinterpret_cast<uint4 *>(word_of)[i] = make_uint4(0u, 0u, 0u, 0u);
     };
     if (a.words) clear(min(slice, max(0, a.N - rank * slice)));
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
+    // What needs no other load first is asked for at once: a bias, the first tokens (those past the row's length are dropped
+    // when that is known).
+    constexpr int kTokens = 4;  // of a thread in flight
+    const size_t said = (size_t)r * c.history_pitch;
+    auto tokens = [&](int i0, int to, int (&n)[kTokens]) {  // -1 for none and for what is no token
+#pragma unroll
+        for (int k = 0; k < kTokens; ++k) {
+            const int i = i0 + k * T;
+            n[k] = -1;
+            if (i < to) {
+                if (WIDE) {
+                    const long long t = static_cast<const long long *>(c.history)[said + i];
+                    n[k] = t >= 0 && t < a.N ? (int)t : -1;
+                } else {
+                    n[k] = static_cast<const int *>(c.history)[said + i];
+                }
+            }
+        }
+    };
+    int early[kTokens];
+    tokens((int)threadIdx.x, c.history ? c.history_width : 0, early);
+    const int *bias_ids = c.bias_ids ? c.bias_ids + (size_t)r * c.bias_width : nullptr;
+    const int first_bias = bias_ids && (int)threadIdx.x < c.bias_width ? bias_ids[threadIdx.x] : -1;
     Row row;
-    row.rep = c.repetition ? c.repetition[r] : 1.0f;
+    row.rep = divisor(c.repetition ? c.repetition[r] : 1.0f);
+    row.temp = divisor(c.temperature ? c.temperature[r] : 0.0f);
     row.freq = c.frequency ? c.frequency[r] : 0.0f;
     row.pres = c.presence ? c.presence[r] : 0.0f;
-    row.temp = c.temperature ? c.temperature[r] : 0.0f;
-    const bool hot = row.temp > 0.0f;
-    row.inv = __frcp_rn(row.temp);
-    row.span = row.temp >= 0x1p-20f && row.temp <= 0x1p20f ? 0x1p80f : 0.0f;  // 0: none
+    const bool hot = row.temp.by > 0.0f;
     row.bias = c.bias ? c.bias + (size_t)r * c.bias_width : nullptr;
     int length = 0, prompt = 0;
     if (c.history) {
@@ -106,17 +160,18 @@ __global__ void __launch_bounds__(kThreadsC, 2) choose_kernel(const __grid_const
     const float *noise = c.noise && hot ? c.noise + (size_t)r * c.noise_pitch : nullptr;
     const float *logits = a.logits + (size_t)r * a.ldl;
     float *out = a.out ? a.out + (size_t)r * a.ldo : nullptr;
-    const size_t said = (size_t)r * c.history_pitch;
     const bool far = length > kLocal && ctas > 1;  // a history that the CTAs share out
     const bool any = a.words && (length > 0 || c.bias_ids);
+    const int from = far ? (int)((long long)length * rank / ctas) : 0;
+    const int to = far ? (int)((long long)length * (rank + 1) / ctas) : length;
     // The CTAs of a cluster have all started when this is waited for, before the first write into another's memory (a
     // history that is shared out has cluster-wide barriers of its own first).
     if (!far) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 
-    // Four tokens of a thread from n on: their logits, noise, and masks (bit e: token e is allowed)
+    // Four tokens of a thread from n on: their logits, noise, and masks' words (of four in a row the same)
     struct Batch {
         float x[4], g[4];
-        uint32_t allowed;
+        int mask[VEC ? 1 : 4];
     };
     auto load4 = [&](const float *p, int n, int end, float (&v)[4]) {
         if (VEC && n + 4 <= end) {
@@ -125,7 +180,7 @@ __global__ void __launch_bounds__(kThreadsC, 2) choose_kernel(const __grid_const
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int at = n + (VEC ? e : e * kThreadsC);
+                const int at = n + (VEC ? e : e * T);
                 v[e] = at < end ? __ldcs(p + at) : 0.0f;
             }
         }
@@ -133,25 +188,18 @@ __global__ void __launch_bounds__(kThreadsC, 2) choose_kernel(const __grid_const
     auto load = [&](int n, int end, Batch &b) {
         load4(logits, n, end, b.x);
         if (noise) load4(noise, n, end, b.g);
-        b.allowed = 15u;
-        if (mask) {
-            if (VEC) {
-                if (n < end) b.allowed = (uint32_t)mask[n >> 5] >> (n & 31);  // whose four are of one word
-            } else {
-                b.allowed = 0u;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int at = n + e * kThreadsC;
-                    if (at < end) b.allowed |= (((uint32_t)mask[at >> 5] >> (at & 31)) & 1u) << e;
-                }
-            }
+        for (int e = 0; e < (VEC ? 1 : 4); ++e) {
+            const int at = n + e * T;
+            b.mask[e] = mask && at < end ? mask[at >> 5] : -1;
         }
     };
+    // The thread's best score above -inf and its token, its first token whose score is NaN: none yet
     float top = -INFINITY;
-    int top_n = INT_MAX;  // the thread's best score and token: none yet
+    int top_n = INT_MAX, nan_n = INT_MAX;
     for (int base = 0; base < a.N; base += turn) {
         const int first = base + rank * slice, end = min(a.N, first + slice);
-        constexpr int kTake = 4 * kThreadsC, kAhead = 2;  // tokens of the CTA at a time; as many times in flight
+        constexpr int kTake = 4 * T, kAhead = 2;  // tokens of the CTA at a time; as many times in flight
         const int mine = first + (VEC ? 4 : 1) * (int)threadIdx.x;
         Batch ahead[kAhead];
 #pragma unroll
@@ -163,40 +211,39 @@ __global__ void __launch_bounds__(kThreadsC, 2) choose_kernel(const __grid_const
             }
             __syncthreads();
             if (c.bias_ids) {
-                for (int i = threadIdx.x; i < c.bias_width; i += kThreadsC) {
-                    const int n = c.bias_ids[(size_t)r * c.bias_width + i];
+                for (int i = threadIdx.x; i < c.bias_width; i += T) {
+                    const int n = i < T ? first_bias : bias_ids[i];
                     if (n >= first && n < end) atomicMax(word_of + n - first, (uint32_t)(i + 1) << 20);
                 }
                 __syncthreads();
             }
             if (far) cluster.sync();  // every CTA's words are ready for the others
-            const int from = far ? (int)((long long)length * rank / ctas) : 0;
-            const int to = far ? (int)((long long)length * (rank + 1) / ctas) : length;
-            constexpr int kTokens = 8;  // of a thread in flight
-            for (int i0 = from + (int)threadIdx.x; i0 < to; i0 += kTokens * kThreadsC) {
-                long long n[kTokens];
+            int next[kTokens];
+#pragma unroll
+            for (int k = 0; k < kTokens; ++k) next[k] = (int)threadIdx.x + k * T < to ? early[k] : -1;
+            if (far) tokens(from + (int)threadIdx.x, to, next);
+            for (int i0 = from + (int)threadIdx.x; i0 < to; i0 += kTokens * T) {
+                int n[kTokens];
+#pragma unroll
+                for (int k = 0; k < kTokens; ++k) n[k] = next[k];
+                tokens(i0 + kTokens * T, to, next);
 #pragma unroll
                 for (int k = 0; k < kTokens; ++k) {
-                    const int i = i0 + k * kThreadsC;
-                    n[k] = i >= to  ? -1
-                           : WIDE ? static_cast<const long long *>(c.history)[said + i]
-                                  : static_cast<const int *>(c.history)[said + i];
-                }
-#pragma unroll
-                for (int k = 0; k < kTokens; ++k) {
-                    const bool in_prompt = i0 + k * kThreadsC < prompt;
-                    uint32_t *w = nullptr;
-                    if (!far) {
-                        if (n[k] >= first && n[k] < end) w = word_of + (int)(n[k] - first);
-                    } else if (n[k] >= base && n[k] < min(a.N, base + turn)) {
-                        const int owner = (int)(n[k] - base) / slice;
-                        w = cluster.map_shared_rank(word_of, owner) + ((int)(n[k] - base) - owner * slice);
-                    }
-                    if (w) {
+                    const bool in_prompt = i0 + k * T < prompt;
+                    if (far) {
+                        if (n[k] >= base && n[k] < min(a.N, base + turn)) {
+                            const int owner = (n[k] - base) / slice;
+                            uint32_t *w = cluster.map_shared_rank(word_of, owner) + (n[k] - base - owner * slice);
+                            if (in_prompt)
+                                atomicOr(w, kPrompt);
+                            else
+                                atomicAdd(w, 1u);
+                        }
+                    } else if (n[k] >= first && n[k] < end) {
                         if (in_prompt)
-                            atomicOr(w, kPrompt);
+                            atomicOr(word_of + n[k] - first, kPrompt);
                         else
-                            atomicAdd(w, 1u);
+                            atomicAdd(word_of + n[k] - first, 1u);
                     }
                 }
             }
@@ -221,31 +268,45 @@ __global__ void __launch_bounds__(kThreadsC, 2) choose_kernel(const __grid_const
                         } else {
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
-                                words[e] = n + e * kThreadsC < end ? word_of[n + e * kThreadsC - first] : 0u;
+                                words[e] = n + e * T < end ? word_of[n + e * T - first] : 0u;
                         }
-                        if (words[0] | words[1] | words[2] | words[3]) {  // (past the end what they hold goes nowhere)
-#pragma unroll 1
-                            for (int e = 0; e < 4; ++e) {
-                                const uint32_t w = e == 0 ? words[0] : e == 1 ? words[1] : e == 2 ? words[2] : words[3];
-                                if (w) {
-                                    const float v = ruled(e == 0 ? x[0] : e == 1 ? x[1] : e == 2 ? x[2] : x[3], w, row);
-                                    if (e == 0) x[0] = v;
-                                    if (e == 1) x[1] = v;
-                                    if (e == 2) x[2] = v;
-                                    if (e == 3) x[3] = v;
-                                }
-                            }
+                        if (words[0] | words[1] | words[2] | words[3]) {  // (past the end they are zeros)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) x[e] = ruled(x[e], words[e], row);
                         }
                     }
+                    if (hot) over_temperature(x, row.temp);
+                    uint32_t seen = 0u;  // bit e: token e is there and allowed
+                    if (VEC) {
+                        seen = (uint32_t)now.mask[0] >> (n & 31);
+                        if (n + 4 > end) seen &= (1u << (end - n)) - 1u;
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int at = n + e * T;
+                            seen |= (at < end ? (uint32_t)now.mask[VEC ? 0 : e] >> (at & 31) & 1u : 0u) << e;
+                        }
+                    }
+                    float score[4], sum = 0.0f;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int at = n + (VEC ? e : e * kThreadsC);
-                        if (hot) x[e] = over_temperature(x[e], row);
-                        const bool allowed = (now.allowed >> e) & 1u;
-                        if (!allowed) x[e] = -INFINITY;
-                        const float score = noise ? __fadd_rn(x[e], now.g[e]) : x[e];
-                        // larger, or NaN where there was none, or the first (tokens come in ascending order)
-                        if (allowed && at < end && top == top && (!(score <= top) || top_n == INT_MAX)) top = score, top_n = at;
+                        if (!(seen >> e & 1u)) x[e] = -INFINITY;
+                        score[e] = noise ? __fadd_rn(x[e], now.g[e]) : x[e];
+                        sum += score[e];
+                    }
+                    if (sum == sum) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)  // tokens come in ascending order
+                            if (score[e] > top) top = score[e], top_n = n + (VEC ? e : e * T);
+                    } else {  // a NaN (or infinities of both signs)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int at = n + (VEC ? e : e * T);
+                            if (seen >> e & 1u) {
+                                if (score[e] > top) top = score[e], top_n = at;
+                                if (score[e] != score[e] && nan_n == INT_MAX) nan_n = at;
+                            }
+                        }
                     }
                     if (out) {
                         if (VEC && n + 4 <= end) {
@@ -253,7 +314,7 @@ __global__ void __launch_bounds__(kThreadsC, 2) choose_kernel(const __grid_const
                         } else {
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                const int at = n + (VEC ? e : e * kThreadsC);
+                                const int at = n + (VEC ? e : e * T);
                                 if (at < end) __stcs(out + at, x[e]);
                             }
                         }
@@ -263,7 +324,7 @@ __global__ void __launch_bounds__(kThreadsC, 2) choose_kernel(const __grid_const
         }
     }
     // the row's best: the highest score, of equal ones the lowest token; 0 for none
-    unsigned long long key = top_n == INT_MAX ? 0ull : argmax_key(top, top_n);
+    unsigned long long key = nan_n != INT_MAX ? argmax_key(NAN, nan_n) : top_n != INT_MAX ? argmax_key(top, top_n) : 0ull;
     for (int o = 16; o > 0; o >>= 1) {
         const unsigned long long other = __shfl_xor_sync(0xffffffffu, key, o);
         key = other > key ? other : key;
@@ -272,26 +333,45 @@ __global__ void __launch_bounds__(kThreadsC, 2) choose_kernel(const __grid_const
     __syncthreads();
     if (!far) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     if (threadIdx.x == 0) {
-        for (int w = 1; w < kThreadsC / 32; ++w) key = best[w] > key ? best[w] : key;
+        for (int w = 1; w < T / 32; ++w) key = best[w] > key ? best[w] : key;
         cluster.map_shared_rank(of_rank, 0)[rank] = key;
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    cluster.sync();
-    if (rank == 0 && threadIdx.x == 0) {
-        key = of_rank[0];
-        for (int k = 1; k < ctas; ++k) key = of_rank[k] > key ? of_rank[k] : key;
-        a.idx[r] = key ? (int64_t)(0xFFFFFFFFull - (key & 0xFFFFFFFFull)) : -1;
+    // The others leave once they have told the first CTA (nobody reads their memory any more).
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    if (rank != 0) return;
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    key = of_rank[0];
+    for (int k = 1; k < ctas; ++k) key = of_rank[k] > key ? of_rank[k] : key;
+    if (key == 0ull) {  // nothing above -inf: the first token that is allowed, if any is
+        __shared__ int lowest;
+        if (threadIdx.x == 0) lowest = mask ? INT_MAX : 0;
+        __syncthreads();
+        for (int i = threadIdx.x; mask && i <= (a.N - 1) >> 5; i += T) {
+            const uint32_t bits = (uint32_t)mask[i] & (32 * i + 32 > a.N ? (1u << (a.N & 31)) - 1u : ~0u);
+            if (bits) {
+                atomicMin(&lowest, 32 * i + __ffs((int)bits) - 1);
+                break;
+            }
+        }
+        __syncthreads();
+        if (threadIdx.x == 0) a.idx[r] = lowest == INT_MAX ? -1 : lowest;
+    } else if (threadIdx.x == 0) {
+        a.idx[r] = (int64_t)(0xFFFFFFFFull - (key & 0xFFFFFFFFull));
     }
 }
 
-template <bool VEC, bool WIDE> cudaError_t launch_choose(const ChooseArgs &a, int ctas, int m, cudaStream_t stream) {
+constexpr int choose_smem(int slice) { return 4 * slice; }
+
+template <bool VEC, bool WIDE, int T>
+cudaError_t launch_kernel(const ChooseArgs &a, int ctas, int m, int smem, cudaStream_t stream) {
     static std::atomic<uint64_t> allowed{0};
-    cudaError_t e = kv_allow_smem(choose_kernel<VEC, WIDE>, 4 * kMostSlice, &allowed);
+    cudaError_t e = kv_allow_smem(choose_kernel<VEC, WIDE, T>, choose_smem(kMostSlice), &allowed);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas, (unsigned)m, 1);
-    cfg.blockDim = dim3(kThreadsC, 1, 1);
-    cfg.dynamicSmemBytes = a.words ? 4 * (size_t)a.slice : 0;
+    cfg.blockDim = dim3(T, 1, 1);
+    cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -302,7 +382,18 @@ template <bool VEC, bool WIDE> cudaError_t launch_choose(const ChooseArgs &a, in
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, choose_kernel<VEC, WIDE>, a);
+    return cudaLaunchKernelEx(&cfg, choose_kernel<VEC, WIDE, T>, a);
+}
+
+template <bool VEC, bool WIDE> cudaError_t launch_choose(const ChooseArgs &a, int ctas, int m, cudaStream_t stream) {
+    int sms = 0;
+    const cudaError_t e = sm_count_of_device(&sms);
+    if (e != cudaSuccess) return e;
+    const int words = a.words ? choose_smem(a.slice) : 0;
+    // Where every CTA can have an SM of its own: a cluster's CTAs are put together on as few SMs as hold them, which these
+    // threads do not fit twice.
+    if ((long long)ctas * m <= sms) return launch_kernel<VEC, WIDE, 1024>(a, ctas, m, words, stream);
+    return launch_kernel<VEC, WIDE, 512>(a, ctas, m, words, stream);
 }
 
 }  // namespace
