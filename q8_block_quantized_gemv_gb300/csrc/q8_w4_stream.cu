@@ -21,7 +21,6 @@
 
 #include <atomic>
 
-#include <stdlib.h>
 #include "q8_attn.h"
 #include "q8_launch.h"
 #include "q8_w4_device.cuh"
@@ -37,7 +36,13 @@ constexpr int kThreads4 = 32 * kWarps4;
 constexpr int kChunk = 128;              // rows of K in a stage
 constexpr int kXPitch4 = 2 * kChunk + 64;  // bytes between activation rows in a stage: 64 past a multiple of 128, so that
                                          // the 16-byte loads of two rows and four lanes fall on all banks
+// A stage: the activations, whose boxes start on the 512 bytes that their swizzle repeats over, then the strips' units.
+__host__ __device__ constexpr int xbytes(int m, int xrows) { return xrows ? xrows * 2 * kChunk : m * kXPitch4; }
+__host__ __device__ constexpr int stage_bytes(int units, int m, int xrows) {
+    return (units + xbytes(m, xrows) + (xrows ? 511 : 15)) & (xrows ? ~511 : ~15);
+}
 struct Stream4 {
+    int xrows;  // rows of a box of activations; 0: rows are copied one by one
     int depth;  // stages of a ring
     int ks;     // CTAs of a cluster splitting K
     int prefetch;
@@ -69,13 +74,13 @@ __device__ __forceinline__ void block32(float (&d)[2][NT][4], const uint32_t (&w
 // S strips a warp: of one part, or half of them of the gate and half of the up projection.
 template <int G, int NT, int S>
 __global__ void __launch_bounds__(kThreads4, NT * S == 1 ? 4 : NT * S == 2 ? 3 : 2)
-    stream4_kernel(const __grid_constant__ W4Args a, const Stream4 p) {
+    stream4_kernel(const __grid_constant__ W4Args a, const Stream4 p, const __grid_constant__ CUtensorMap xmap) {
     namespace cg = cooperative_groups;
     constexpr int CG = kChunk / G;  // groups of a chunk
-    extern __shared__ __align__(128) unsigned char smem4[];
+    extern __shared__ __align__(1024) unsigned char smem4[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int depth = p.depth;
-    const int chunk = CG * a.unit, stage = S * chunk + a.m * kXPitch4;
+    const int chunk = CG * a.unit, stage = stage_bytes(S * chunk, a.m, p.xrows), wat = xbytes(a.m, p.xrows);
     unsigned char *ring = smem4 + warp * depth * stage;
     uint64_t *full = reinterpret_cast<uint64_t *>(smem4 + kWarps4 * depth * stage) + warp * depth;
 
@@ -104,19 +109,31 @@ __global__ void __launch_bounds__(kThreads4, NT * S == 1 ? 4 : NT * S == 2 ? 3 :
         const int gr = groups_of(i);
         const unsigned bytes = (unsigned)(gr * a.unit);
         uint64_t *bar = full + slot;
-        w4_arrive_tx(bar, bytes * (pair ? 2 * here : here) + (unsigned)(gr * G * 2 * a.m));
+        w4_arrive_tx(bar, bytes * (pair ? 2 * here : here) + (unsigned)(gr * G * 2 * (p.xrows ? p.xrows : a.m)));
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             const int of = pair ? s >> 1 : s;
             if (of < here)
-                w4_copy(ring + slot * stage + s * chunk,
+                w4_copy(ring + slot * stage + wat + s * chunk,
                         (pair && (s & 1) ? a.part[1].w : to.w) + src + of * strip_bytes + (size_t)i * chunk, bytes, bar);
         }
     };
-    auto ask_x = [&](int i, int slot) {  // lanes 0 .. m - 1, a row each
-        if (lane < a.m)
-            w4_copy(ring + slot * stage + S * chunk + lane * kXPitch4,
-                    a.x + (size_t)lane * a.K + (size_t)(c0 + i) * kChunk, (unsigned)(groups_of(i) * G * 2), full + slot);
+    // The stage's activations: m rows (lanes 0 .. m - 1) 64 bytes past a multiple of 128 apart, or boxes of 32 values of all
+    // rows in the 64-byte swizzle (lane 0).  Either way the 16-byte loads of two rows and four lanes fall on all banks.
+    auto ask_x = [&](int i, int slot) {
+        unsigned char *to = ring + slot * stage;
+        const int k0 = (c0 + i) * kChunk, rows_k = groups_of(i) * G;
+        if (p.xrows == 0) {
+            if (lane < a.m)
+                w4_copy(to + lane * kXPitch4, a.x + (size_t)lane * a.K + k0, (unsigned)(rows_k * 2), full + slot);
+        } else if (lane == 0) {
+            for (int b = 0; b < rows_k / 32; ++b)
+                asm volatile(
+                    "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
+                        "r"(w4_smem(to + b * p.xrows * 64)),
+                    "l"(&xmap), "r"(k0 + 32 * b), "r"(0), "r"(w4_smem(full + slot))
+                    : "memory");
+        }
     };
 
     if (lane == 0) {
@@ -132,9 +149,13 @@ __global__ void __launch_bounds__(kThreads4, NT * S == 1 ? 4 : NT * S == 2 ? 3 :
     for (int i = 0; i < depth && i < n; ++i) ask_x(i, i);
 
     float acc[S][2][NT][4] = {};
-    int xrow[NT];  // the lane's activation rows in a stage
+    int xrow[NT];  // where the lane's activations of 32-row block 0 are in a stage; xblock to the next
+    const int xblock = p.xrows ? p.xrows * 64 : 64;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) xrow[nt] = S * chunk + min(8 * nt + g, a.m - 1) * kXPitch4 + 16 * t;
+    for (int nt = 0; nt < NT; ++nt) {
+        const int r = 8 * nt + g;
+        xrow[nt] = p.xrows ? r * 64 + ((t ^ (r >> 1 & 3)) << 4) : min(r, a.m - 1) * kXPitch4 + 16 * t;
+    }
     int slot = 0, i = 0;
     unsigned phase = 0;
     for (; i < n; ++i) {
@@ -146,7 +167,7 @@ __global__ void __launch_bounds__(kThreads4, NT * S == 1 ? 4 : NT * S == 2 ? 3 :
             if (q >= have) break;
 #pragma unroll
             for (int s = 0; s < S; ++s) {
-                const unsigned char *u = st + s * chunk + q * a.unit;
+                const unsigned char *u = st + wat + s * chunk + q * a.unit;
                 uint32_t zero[2][2] = {{kW4Eight, kW4Eight}, {kW4Eight, kW4Eight}};
                 if (a.zeros) {
 #pragma unroll
@@ -171,9 +192,9 @@ __global__ void __launch_bounds__(kThreads4, NT * S == 1 ? 4 : NT * S == 2 ? 3 :
                     uint4 x0[NT], x1[NT];
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        const unsigned char *row = st + xrow[nt] + 2 * (q * G + 32 * b);
+                        const unsigned char *row = st + xrow[nt] + (q * (G / 32) + b) * xblock;
                         x0[nt] = *reinterpret_cast<const uint4 *>(row);
-                        if (G > 32) x1[nt] = *reinterpret_cast<const uint4 *>(row + 64);
+                        if (G > 32) x1[nt] = *reinterpret_cast<const uint4 *>(row + xblock);
                     }
                     block32<NT>(d, w0, zero, x0);
                     if (G > 32) block32<NT>(d, w1, zero, x1);
@@ -288,7 +309,7 @@ __global__ void __launch_bounds__(kThreads4, NT * S == 1 ? 4 : NT * S == 2 ? 3 :
 constexpr int kMaxSmem4 = 227 * 1024;
 
 int smem_bytes(const W4Args &a, const Stream4 &p, int S) {
-    const int ring = kWarps4 * p.depth * (S * (kChunk / a.group) * a.unit + a.m * kXPitch4 + 8);
+    const int ring = kWarps4 * p.depth * (stage_bytes(S * (kChunk / a.group) * a.unit, a.m, p.xrows) + 8);
     const int ends = a.m * (kWarps4 * (32 * S + 4) + 32 * S) * 4;
     return ring > ends ? ring : ends;
 }
@@ -300,7 +321,8 @@ int tiles_of(const W4Args &a, int S) {
     return tiles;
 }
 
-template <int G, int NT, int S> cudaError_t launch_kernel(const W4Args &a, const Stream4 &p, cudaStream_t stream) {
+template <int G, int NT, int S>
+cudaError_t launch_kernel(const W4Args &a, const Stream4 &p, const CUtensorMap &map, cudaStream_t stream) {
     static std::atomic<uint64_t> allowed{0};
     cudaError_t e = kv_allow_smem(stream4_kernel<G, NT, S>, kMaxSmem4, &allowed);
     if (e != cudaSuccess) return e;
@@ -321,12 +343,13 @@ template <int G, int NT, int S> cudaError_t launch_kernel(const W4Args &a, const
         attr[1].val.clusterDim.z = 1;
         cfg.numAttrs = 2;
     }
-    return cudaLaunchKernelEx(&cfg, stream4_kernel<G, NT, S>, a, p);
+    return cudaLaunchKernelEx(&cfg, stream4_kernel<G, NT, S>, a, p, map);
 }
 
-template <int G> cudaError_t launch_group(const W4Args &a, const Stream4 &p, int S, cudaStream_t stream) {
-    if (a.m > 8) return S == 4 ? launch_kernel<G, 2, 4>(a, p, stream) : launch_kernel<G, 2, 2>(a, p, stream);
-    return S == 1 ? launch_kernel<G, 1, 1>(a, p, stream) : S == 2 ? launch_kernel<G, 1, 2>(a, p, stream) : launch_kernel<G, 1, 4>(a, p, stream);
+template <int G>
+cudaError_t launch_group(const W4Args &a, const Stream4 &p, int S, const CUtensorMap &map, cudaStream_t stream) {
+    if (a.m > 8) return launch_kernel<G, 2, 2>(a, p, map, stream);
+    return S == 1 ? launch_kernel<G, 1, 1>(a, p, map, stream) : launch_kernel<G, 1, 2>(a, p, map, stream);
 }
 
 }  // namespace
@@ -345,19 +368,33 @@ cudaError_t launch_w4_stream(const W4Args &a, bool constant_weights, cudaStream_
     int sms = 0;
     cudaError_t e = sm_count_of_device(&sms);
     if (e != cudaSuccess) return e;
-    Stream4 p = {2, 1, constant_weights};
-    int S = a.m <= 4 ? 1 : a.m <= 8 ? 2 : 4;
-    if (a.epi == kW4Glu && S < 2) S = 2;
-    if (const char *v = getenv("W4_S")) S = atoi(v);
-    if (const char *v = getenv("W4_D")) p.depth = atoi(v);
+    // Strips a warp: two share the activations' way from L2 from five rows on, and where there are enough strips for a wave
+    // of such CTAs (4096 x 128256 at one row 56.8 -> 53.5 us); one otherwise, so that more warps share the weight.
+    Stream4 p = {a.m > 8 ? 16 : 0, 1, 1, constant_weights};
+    const bool pair = a.epi == kW4Glu;
+    const int strips = pair ? 2 * a.part[0].strip_end : a.part[a.nparts - 1].strip_end;
+    const int S = pair || a.m > 4 || strips >= 6 * sms ? 2 : 1;
+    const int fit = a.m > 8 ? 2 : S == 2 ? 3 : 4;  // CTAs an SM by their registers
+    // K is split while the CTAs fill no more than three quarters of what fits at once (512 CTAs where 608 fit were no faster
+    // than 256, and a second wave costs a whole one), and while each warp has a chunk.
     const int tiles = tiles_of(a, S), chunks = (a.K + kChunk - 1) / kChunk;
-    while (p.ks < 8 && 2 * p.ks * tiles <= 2 * sms && 2 * p.ks * kWarps4 <= chunks) p.ks *= 2;
-    if (const char *v = getenv("W4_KS")) p.ks = atoi(v);
-    while (p.depth > 1 && smem_bytes(a, p, S) > kMaxSmem4 - 1024) --p.depth;
+    while (p.ks < 8 && 2ll * p.ks * tiles * 4 <= 3ll * fit * sms && 2 * p.ks * kWarps4 <= chunks) p.ks *= 2;
+    // As many stages as leave room for the CTAs that an SM gets.
+    const long long ctas = (long long)tiles * p.ks;
+    const int each = (int)(ctas >= (long long)fit * sms ? fit : (ctas + sms - 1) / sms);
+    while (p.depth < 4 && p.depth * kWarps4 * p.ks < chunks) {
+        ++p.depth;
+        if (each * (smem_bytes(a, p, S) + 1024) > 228 * 1024) {
+            --p.depth;
+            break;
+        }
+    }
+    CUtensorMap map = {};
+    if (p.xrows && !encode_bf16_rows(&map, a.x, a.m, a.K, 32, p.xrows)) return cudaErrorNotSupported;
     switch (a.group) {
-        case 32: return launch_group<32>(a, p, S, stream);
-        case 64: return launch_group<64>(a, p, S, stream);
-        default: return launch_group<128>(a, p, S, stream);
+        case 32: return launch_group<32>(a, p, S, map, stream);
+        case 64: return launch_group<64>(a, p, S, map, stream);
+        default: return launch_group<128>(a, p, S, map, stream);
     }
 }
 
