@@ -28,6 +28,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 
@@ -825,7 +826,10 @@ class Weight4:
         self.buf, self.K, self.N, self.Np, self.group, self.flags = buf, K, N, padded_n(N), group, flags
         self.device, self._index = buf.device, buf.get_device()
         self._c = _W4(buf.data_ptr(), N, group, flags)
-        self._ref = ctypes.addressof(self._c)
+        self._ref, self._packed = ctypes.addressof(self._c), bytes(self._c)
+        # what every call needs, at hand: looking it up took a fifth of a small call's time
+        import torch
+        self._bf16, self._f32, self._empty = torch.bfloat16, torch.float32, torch.empty
 
 
 FLAG_W4_ZEROS = 1
@@ -862,16 +866,18 @@ def repack4(blocks, K: int, N: int):
 
 def _x4(x, w):
     """The rows of activation x, checked against weight w."""
-    import torch
     shape = x.shape
-    if x.dtype != torch.bfloat16 or len(shape) != 2 or shape[1] != w.K or x.get_device() != w._index \
+    if x.dtype is not w._bf16 or len(shape) != 2 or shape[1] != w.K or x.get_device() != w._index \
             or not x.is_contiguous():
         raise ValueError(f"x must be a contiguous bfloat16 tensor [m, {w.K}] on the weight's device")
     return shape[0]
 
 
-def _out4(name, t, m, w, dtype):
-    if t.dtype != dtype or tuple(t.shape) != (m, w.Np) or t.get_device() != w._index or not t.is_contiguous():
+def _out4(name, t, m, w, dtype, stream):
+    """An output [m, Np] of weight w: t, checked, or a new one."""
+    if t is None:
+        return w._empty((m, w.Np), dtype=dtype, device=w.device) if stream is None else _new((m, w.Np), dtype, w.device, stream)
+    if t.dtype is not dtype or tuple(t.shape) != (m, w.Np) or t.get_device() != w._index or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor [{m}, {w.Np}] on the weight's device")
     return t
 
@@ -879,9 +885,8 @@ def _out4(name, t, m, w, dtype):
 def gemv4(x, w: Weight4, y=None, constant_weights: bool = False, stream=None):
     """y = x . W over a 4-bit weight (q8_gemv4): x bf16 [m, K], 1 <= m <= 512; returns y, fp32 [m, Np] (columns N .. Np-1
     are 0).  constant_weights: as for :func:`gemv`."""
-    import torch
     m = _x4(x, w)
-    y = _new((m, w.Np), torch.float32, w.device, stream) if y is None else _out4("y", y, m, w, torch.float32)
+    y = _out4("y", y, m, w, w._f32, stream)
     st = lib().q8_gemv4(x.data_ptr(), w._ref, y.data_ptr(), m, w.K, 1 if constant_weights else 0,
                         _stream_of(stream, w.device))
     if st:
@@ -889,25 +894,26 @@ def gemv4(x, w: Weight4, y=None, constant_weights: bool = False, stream=None):
     return y
 
 
+_POINTERS = [struct.Struct(f"{n}Q") for n in range(9)]
+
+
 def gemv4_parts(x, weights, ys=None, constant_weights: bool = False, stream=None):
     """Several products of one activation in one call (q8_gemv4_parts); the weights have the same K, group and flags.
     Returns the list of outputs, fp32 [m, Np_p]."""
-    import torch
     n = len(weights)
     if not 1 <= n <= 8:
         raise ValueError("1 to 8 weights")
     if ys is not None and len(ys) != n:
         raise ValueError("an output for each weight")
-    m = _x4(x, weights[0])
-    arr, outs, to = (_W4 * n)(), [], (_P * n)()
-    for i, w in enumerate(weights):
-        if w.K != weights[0].K or w._index != weights[0]._index:
+    w0 = weights[0]
+    m, K, index = _x4(x, w0), w0.K, w0._index
+    for w in weights:
+        if w.K != K or w._index != index:
             raise ValueError("the weights must have the same K and device")
-        y = _new((m, w.Np), torch.float32, w.device, stream) if ys is None else _out4("y", ys[i], m, w, torch.float32)
-        arr[i], to[i] = w._c, y.data_ptr()
-        outs.append(y)
-    st = lib().q8_gemv4_parts(x.data_ptr(), ctypes.addressof(arr), ctypes.addressof(to), n, m, weights[0].K,
-                              1 if constant_weights else 0, _stream_of(stream, weights[0].device))
+    outs = [_out4("y", None if ys is None else ys[i], m, w, w._f32, stream) for i, w in enumerate(weights)]
+    st = lib().q8_gemv4_parts(x.data_ptr(), b"".join([w._packed for w in weights]),
+                              _POINTERS[n].pack(*[y.data_ptr() for y in outs]), n, m, K, 1 if constant_weights else 0,
+                              _stream_of(stream, w0.device))
     if st:
         raise Q8Error(st, "q8_gemv4_parts")
     return outs
@@ -917,18 +923,13 @@ def gemv4_glu(x, gate: Weight4, up: Weight4, out=None, out_bf16=None, want=("f32
               stream=None):
     """The gated pair (q8_gemv4_glu): silu(x . Wg) * (x . Wu).  ``want``: which outputs to allocate when not given, "f32"
     and/or "bf16" ([m, Np]).  Returns (out, out_bf16), either None when not requested."""
-    import torch
     m = _x4(x, gate)
     if up.K != gate.K or up._index != gate._index:
         raise ValueError("gate and up must have the same K and device")
-    if out is not None:
-        _out4("out", out, m, gate, torch.float32)
-    elif "f32" in want:
-        out = _new((m, gate.Np), torch.float32, gate.device, stream)
-    if out_bf16 is not None:
-        _out4("out_bf16", out_bf16, m, gate, torch.bfloat16)
-    elif "bf16" in want:
-        out_bf16 = _new((m, gate.Np), torch.bfloat16, gate.device, stream)
+    if out is not None or "f32" in want:
+        out = _out4("out", out, m, gate, gate._f32, stream)
+    if out_bf16 is not None or "bf16" in want:
+        out_bf16 = _out4("out_bf16", out_bf16, m, gate, gate._bf16, stream)
     st = lib().q8_gemv4_glu(x.data_ptr(), gate._ref, up._ref, None if out is None else out.data_ptr(),
                             None if out_bf16 is None else out_bf16.data_ptr(), m, gate.K, 1 if constant_weights else 0,
                             _stream_of(stream, gate.device))
@@ -941,16 +942,14 @@ def gemv4_residual_norm(x, w: Weight4, residual, gamma, eps: float, h=None, out_
                         stream=None):
     """A projection, the residual add and the following RMS norm (q8_gemv4_residual_norm): h = residual + x . W, out =
     h / sqrt(mean(h^2) + eps) * gamma.  Returns (h fp32 [m, Np], out bf16 [m, Np]); ``h`` may be ``residual`` (in place)."""
-    import torch
     m = _x4(x, w)
-    _out4("residual", residual, m, w, torch.float32)
-    if gamma.dtype != torch.float32 or gamma.numel() < w.N or not gamma.is_contiguous() or gamma.get_device() != w._index:
+    if residual is None:
+        raise ValueError("residual must be given")
+    _out4("residual", residual, m, w, w._f32, stream)
+    if gamma.dtype is not w._f32 or gamma.numel() < w.N or not gamma.is_contiguous() or gamma.get_device() != w._index:
         raise ValueError("gamma must be a contiguous fp32 tensor of at least N values on the weight's device")
-    h = _new((m, w.Np), torch.float32, w.device, stream) if h is None else _out4("h", h, m, w, torch.float32)
-    if out_bf16 is None:
-        out_bf16 = _new((m, w.Np), torch.bfloat16, w.device, stream)
-    else:
-        _out4("out_bf16", out_bf16, m, w, torch.bfloat16)
+    h = _out4("h", h, m, w, w._f32, stream)
+    out_bf16 = _out4("out_bf16", out_bf16, m, w, w._bf16, stream)
     st = lib().q8_gemv4_residual_norm(x.data_ptr(), w._ref, residual.data_ptr(), gamma.data_ptr(), eps, h.data_ptr(),
                                       out_bf16.data_ptr(), m, w.K, 1 if constant_weights else 0,
                                       _stream_of(stream, w.device))
@@ -966,14 +965,28 @@ class _Choice(ctypes.Structure):
                                   "mask_pitch", "noise_pitch")]
 
 
-def _pitched(name, t, dtypes, rows, cols, index):
-    """A 2-D tensor's pointer and row pitch: unit column stride, `rows` rows (None: any), at least `cols` columns."""
+_CHOICE = struct.Struct("12Q7i4x")  # the same, packed at a third of the time
+assert _CHOICE.size == ctypes.sizeof(_Choice)
+
+
+def _pitched(name, t, dtype, rows, cols, index):
+    """A 2-D tensor's pointer and row pitch: unit column stride, `rows` rows, at least `cols` columns."""
     shape = t.shape
-    if t.get_device() != index or t.dtype not in dtypes or len(shape) != 2 or (rows is not None and shape[0] != rows) \
-            or shape[1] < cols or (shape[1] > 1 and t.stride(1) != 1) or (shape[0] > 1 and t.stride(0) < shape[1]):
-        raise ValueError(f"{name} must be a 2-D {dtypes[0]} CUDA tensor of {rows if rows is not None else 'any'} rows and at "
-                         f"least {cols} columns, unit column stride, on the device of the logits")
-    return t.data_ptr(), t.stride(0) if shape[0] > 1 else shape[1]
+    if t.dtype is dtype and len(shape) == 2 and shape[0] == rows and shape[1] >= cols and t.get_device() == index:
+        pitch, unit = t.stride()
+        if (unit == 1 or shape[1] == 1) and (rows <= 1 or pitch >= shape[1]):
+            return t.data_ptr(), pitch if rows > 1 else shape[1]
+    raise ValueError(f"{name} must be a 2-D {dtype} CUDA tensor of {rows} rows and at least {cols} columns, unit column stride, "
+                     "on the device of the logits")
+
+
+def _row_values(name, t, dtype, m, index):
+    """The pointer of a value for each row; 0 for None."""
+    if t is None:
+        return 0
+    if t.dtype is not dtype or t.numel() != m or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of {m} values on the logits' device")
+    return t.data_ptr()
 
 
 def choose(logits, N: int | None = None, out=None, repetition=None, frequency=None, presence=None, temperature=None,
@@ -992,47 +1005,49 @@ def choose(logits, N: int | None = None, out=None, repetition=None, frequency=No
     for the choice where the temperature is above 0 (Gumbel noise samples softmax(out))."""
     import torch
     f32, i32 = torch.float32, torch.int32
-    index = logits.get_device()
-    if index < 0:
-        raise ValueError("logits must be a CUDA tensor")
-    m = logits.shape[0]
+    index, shape = logits.get_device(), logits.shape
+    if index < 0 or len(shape) != 2:
+        raise ValueError("logits must be a 2-D CUDA tensor")
+    m = shape[0]
     if N is None:
-        N = logits.shape[-1]
-    lp, ldl = _pitched("logits", logits, (f32,), m, N, index)
-    c = _Choice()
-    for name, t, dtype in (("repetition", repetition, f32), ("frequency", frequency, f32), ("presence", presence, f32),
-                           ("temperature", temperature, f32), ("lengths", lengths, i32), ("prompts", prompts, i32),
-                           ("mask_rows", mask_rows, i32)):
-        if t is not None:
-            if t.get_device() != index or t.dtype != dtype or t.numel() != m or not t.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of {m} values on the logits' device")
-            setattr(c, name, t.data_ptr())
-    if history is not None and history.shape[-1]:
-        c.history, c.history_pitch = _pitched("history", history, (i32, torch.int64), m, 1, index)
-        c.history_width, c.history_wide = history.shape[1], int(history.dtype == torch.int64)
-    if bias is not None and bias_ids is None:
+        N = shape[1]
+    lp, ldl = _pitched("logits", logits, f32, m, N, index)
+    op, ldo = (None, 0) if out is None else _pitched("out", out, f32, m, N, index)
+    hp = wide = hpitch = hwidth = bp = vp = bwidth = mp = mcount = mpitch = np_ = npitch = 0
+    if history is not None:
+        if lengths is None:
+            raise ValueError("history needs lengths")
+        if history.shape[-1]:
+            wide = history.dtype is torch.int64
+            hp, hpitch = _pitched("history", history, torch.int64 if wide else i32, m, 1, index)
+            hwidth = history.shape[1]
+    if bias_ids is not None:
+        bwidth = bias_ids.shape[-1]
+        if bias is None or bias_ids.dtype is not i32 or bias.dtype is not f32 or bias_ids.get_device() != index \
+                or bias.get_device() != index or tuple(bias_ids.shape) != (m, bwidth) or bias.shape != bias_ids.shape \
+                or not bias_ids.is_contiguous() or not bias.is_contiguous():
+            raise ValueError("bias_ids int32 and bias float32 must be contiguous [m, count], on the logits' device")
+        if bwidth:
+            bp, vp = bias_ids.data_ptr(), bias.data_ptr()
+    elif bias is not None:
         raise ValueError("bias needs bias_ids")
-    if history is not None and lengths is None:
-        raise ValueError("history needs lengths")
-    if bias_ids is not None and bias_ids.shape[-1]:
-        for name, t, dtype in (("bias_ids", bias_ids, i32), ("bias", bias, f32)):
-            if t is None or t.get_device() != index or t.dtype != dtype or t.shape != (m, bias_ids.shape[-1]) \
-                    or not t.is_contiguous():
-                raise ValueError("bias_ids int32 and bias float32 must be contiguous [m, count], on the logits' device")
-        c.bias_ids, c.bias, c.bias_width = bias_ids.data_ptr(), bias.data_ptr(), bias_ids.shape[1]
     if mask is not None:
-        c.mask, c.mask_pitch = _pitched("mask", mask, (i32,), None, (N + 31) // 32, index)
-        c.mask_count = mask.shape[0]
+        mcount = mask.shape[0]
+        mp, mpitch = _pitched("mask", mask, i32, mcount, (N + 31) // 32, index)
     if noise is not None:
-        c.noise, c.noise_pitch = _pitched("noise", noise, (f32,), m, N, index)
-    op, ldo = (None, 0) if out is None else _pitched("out", out, (f32,), m, N, index)
+        np_, npitch = _pitched("noise", noise, f32, m, N, index)
     if idx is None:
-        idx = _new((m,), torch.int64, logits.device, stream)
-    elif idx.dtype != torch.int64 or idx.numel() != m or not idx.is_contiguous() or idx.get_device() != index:
+        idx = torch.empty(m, dtype=torch.int64, device=logits.device) if stream is None else \
+            _new((m,), torch.int64, logits.device, stream)
+    elif idx.dtype is not torch.int64 or idx.numel() != m or not idx.is_contiguous() or idx.get_device() != index:
         raise ValueError("idx must be a contiguous int64 CUDA tensor of m values on the logits' device")
     if m == 0:
         return idx
-    st = lib().q8_choose(lp, ldl, ctypes.addressof(c), op, ldo, idx.data_ptr(), m, N, _stream_of(stream, logits.device))
+    c = _CHOICE.pack(_row_values("repetition", repetition, f32, m, index), _row_values("frequency", frequency, f32, m, index),
+                     _row_values("presence", presence, f32, m, index), _row_values("temperature", temperature, f32, m, index),
+                     hp, _row_values("lengths", lengths, i32, m, index), _row_values("prompts", prompts, i32, m, index), bp,
+                     vp, mp, _row_values("mask_rows", mask_rows, i32, m, index), np_, hwidth, hpitch, wide, bwidth, mcount, mpitch, npitch)
+    st = lib().q8_choose(lp, ldl, c, op, ldo, idx.data_ptr(), m, N, _stream_of(stream, logits.device))
     if st:
         raise Q8Error(st, "q8_choose")
     return idx
