@@ -23,7 +23,6 @@
 // memory.  Every wait ends after two seconds: the CTA then stops, waits as long for what is in flight, and reports a fault.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
-#include <stdlib.h>
 
 #include <atomic>
 
@@ -42,10 +41,12 @@ constexpr int kConvertEnd = 12, kLoadWarp = 12, kMmaWarp = 13, kXWarp = 14, kLoa
 constexpr int kOperand = kCols * kStepK * 2;  // 16 KB: one converted step of one weight
 constexpr int kMaxSmemG = 227 * 1024;
 constexpr int kMaxStages = 8, kMaxAcc = 4;
+constexpr int kMostSplit = 4;  // clusters of eight whole SMs find no place for all at once (61 rows of 2048 x 2048 13.3 -> 19.6 us)
 
 __device__ unsigned int g_w4_gemm_fault = 0;
 
 struct Gemm4 {
+    int tile0;   // the launch's first tile of columns
     int rows;    // of a tile, a multiple of 32 (FW = 2) or 16
     int slots;   // stages of converted weights and activations
     int raws;    // stages of units
@@ -103,24 +104,13 @@ __device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t b, uint32_t
         "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHigh)
         : "memory");
 }
-// 16, 32 or 64 columns of the warp's lanes.
+// 16 or 64 columns of the warp's lanes.
 __device__ __forceinline__ void tmem_ld16(uint32_t a, uint32_t *v) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
         "[%16];"
         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
           "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-        : "r"(a));
-}
-__device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t *v) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, "
-        "[%32];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
-          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
-          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
         : "r"(a));
 }
 __device__ __forceinline__ void tmem_ld64(uint32_t a, uint32_t *v) {
@@ -149,18 +139,6 @@ __device__ __forceinline__ void tma_rows(void *dst, const CUtensorMap *map, int 
         : "memory");
 }
 
-__device__ __forceinline__ unsigned long long pack2(uint32_t lo, uint32_t hi) {
-    unsigned long long d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
-    return d;
-}
-__device__ __forceinline__ void fma2(unsigned long long &d, unsigned long long a, unsigned long long b) {
-    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
-}
-__device__ __forceinline__ void unpack2(unsigned long long v, float &lo, float &hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-
 // Two columns (g and g + 8 of a 16-column tile) of rows 32 blk + 8t .. + 7 of a step, blk = first and then the other, as
 // they go into the operand: row n of 128 bytes, 16-byte chunk c at c ^ (n % 8).
 __device__ __forceinline__ void store8(unsigned char *row, int chunk, int g, uint32_t w, uint32_t zero) {
@@ -184,7 +162,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     // the tile: 128 columns of one part, or of the gate and of the up projection
-    int part = 0, tile = blockIdx.x;
+    int part = 0, tile = p.tile0 + blockIdx.x;
     if (P == 1)
         for (int first = 0, tiles;; ++part, tile -= tiles, first = a.part[part - 1].strip_end) {
             tiles = (a.part[part].strip_end - first + 3) / 4;
@@ -231,9 +209,9 @@ __global__ void __launch_bounds__(kThreadsG, 1)
         // ---- fold ----
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        unsigned long long acc[64];
+        float acc[128];
 #pragma unroll
-        for (int i = 0; i < 64; ++i) acc[i] = 0ull;
+        for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const int col0 = (warp >> 2) * half, pieces = half / 16;
         int raw = 0, buf = 0;
@@ -243,12 +221,9 @@ __global__ void __launch_bounds__(kThreadsG, 1)
             if (q == 0 && !warp_wait(&ctl.raw_full[raw], raw_phase, abort)) break;
             // strip (warp % 4) of the tile is the warp's lanes
             const unsigned char *u = raws + raw * raw_bytes + (warp & 3) * chunk_bytes + q * a.unit + 16 * G + 2 * lane;
-            unsigned long long s[P];
+            float s[P];
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-                const float f = w4_scale(*reinterpret_cast<const uint16_t *>(u + i * 4 * chunk_bytes), a.bf16);
-                s[i] = pack2(__float_as_uint(f), __float_as_uint(f));
-            }
+            for (int i = 0; i < P; ++i) s[i] = w4_scale(*reinterpret_cast<const uint16_t *>(u + i * 4 * chunk_bytes), a.bf16);
             if (!warp_wait(&ctl.acc_full[buf], acc_phase, abort)) break;
             fence_after();
             const uint32_t at = tmem + lanes + (uint32_t)(buf * P * p.rows + col0);
@@ -257,7 +232,8 @@ __global__ void __launch_bounds__(kThreadsG, 1)
 #pragma unroll
                 for (int c = 0; c < kPerAcc; c += 4)
                     if (c < pieces) {
-                        // as many columns at a look as there are registers for: a look costs its latency
+                        // as many columns at a look as there are registers for: beside everything else a look takes some 400
+                        // clocks, whether of 16 columns or of 64
                         uint32_t v[64];
                         const uint32_t from = at + i * p.rows + 16 * c;
                         if (c + 4 <= pieces) {
@@ -272,8 +248,10 @@ __global__ void __launch_bounds__(kThreadsG, 1)
                         for (int k = 0; k < 4; ++k)
                             if (c + k < pieces) {
 #pragma unroll
-                                for (int e = 0; e < 8; ++e)
-                                    fma2(acc[8 * (i * kPerAcc + c + k) + e], s[i], pack2(v[16 * k + 2 * e], v[16 * k + 2 * e + 1]));
+                                for (int e = 0; e < 16; ++e) {
+                                    float &to = acc[16 * (i * kPerAcc + c + k) + e];
+                                    to = fmaf(s[i], __uint_as_float(v[16 * k + e]), to);
+                                }
                             }
                     }
             fence_before();
@@ -297,12 +275,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
                 if (16 * c < half) {
                     float *to = red + (i * p.rows + first + 16 * c) * kCols + n;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        float v[2];
-                        unpack2(acc[8 * (i * kPerAcc + c) + e], v[0], v[1]);
-                        to[2 * e * kCols] = v[0];
-                        to[(2 * e + 1) * kCols] = v[1];
-                    }
+                    for (int e = 0; e < 16; ++e) to[e * kCols] = acc[16 * (i * kPerAcc + c) + e];
                 }
     } else {
         if (FW == 1)
@@ -576,28 +549,45 @@ cudaError_t launch_w4_gemm(const W4Args &a, bool constant_weights, cudaStream_t 
     int tiles = 0;
     for (int i = 0; i < (P == 2 ? 1 : a.nparts); ++i)
         tiles += (a.part[i].strip_end - (i ? a.part[i - 1].strip_end : 0) + 3) / 4;
-    const int chunks = (a.K + kChunkK - 1) / kChunkK, ctas = tiles * ((a.m + p.rows - 1) / p.rows);
-    double best = 1e300;
-    for (int k = 1; k <= 8 && k <= chunks; k *= 2) {
-        const double cost = (double)((ctas * k + sms - 1) / sms) * (8.0 + (double)((chunks + k - 1) / k));
-        if (cost < best - 1e-9) best = cost, p.ks = k;
-    }
-    if (const char *v = getenv("W4_GKS")) p.ks = atoi(v);
+    const int chunks = (a.K + kChunkK - 1) / kChunkK;
     p.accs = 512 / (P * p.rows) < kMaxAcc ? 512 / (P * p.rows) : kMaxAcc;
     const int raw = P * 4 * (kChunkK / a.group) * a.unit, slot = P * kOperand + p.rows * 128;
     const int fixed = (int)sizeof(Control);
-    p.slots = 3;
-    if (const char *v = getenv("W4_SLOTS")) p.slots = atoi(v);
+    p.slots = 3;  // four or five were no faster
     p.raws = (kMaxSmemG - fixed - p.slots * slot) / raw;
     if (p.raws > kMaxStages) p.raws = kMaxStages;
     const int smem = fixed + p.slots * slot + p.raws * raw;
+
+    // K splits, in chunks of a CTA's time, which beside its own takes some eight for its beginning and end: of all tiles; or
+    // the waves that are full unsplit and the tiles of the last one apart, split, in a launch of their own (512 rows of
+    // 4096 x 14336, 224 tiles on 152 SMs: see the measured table).
+    auto waves = [&](int t, int k) { return (double)(((long long)t * row_tiles * k + sms - 1) / sms); };
+    auto cost = [&](int t, int k) { return waves(t, k) * (8.0 + (double)((chunks + k - 1) / k)); };
+    auto best = [&](int t) {
+        int ks = 1;
+        for (int k = 2; k <= kMostSplit && k <= chunks; k *= 2)
+            if (cost(t, k) < cost(t, ks)) ks = k;
+        return ks;
+    };
+    int whole = (int)((long long)tiles * row_tiles / sms * sms / row_tiles);  // tiles of the full waves
+    const int all = best(tiles), rest = whole < tiles ? best(tiles - whole) : 1;
+    if (whole > 0 && whole < tiles && cost(whole, 1) + cost(tiles - whole, rest) < 0.95 * cost(tiles, all))
+        p.ks = 1;
+    else
+        p.ks = all, whole = tiles;
+
     CUtensorMap map;
     if (!encode_bf16_rows(&map, a.x, a.m, a.K, kStepK, p.rows)) return cudaErrorNotSupported;
-    switch (a.group) {
-        case 32: return launch_group<32>(a, p, fw, tiles, smem, map, stream);
-        case 64: return launch_group<64>(a, p, fw, tiles, smem, map, stream);
-        default: return launch_group<128>(a, p, fw, tiles, smem, map, stream);
+    for (int done = 0; done < tiles; done += whole, whole = tiles - done, p.ks = rest) {
+        p.tile0 = done;
+        switch (a.group) {
+            case 32: e = launch_group<32>(a, p, fw, whole, smem, map, stream); break;
+            case 64: e = launch_group<64>(a, p, fw, whole, smem, map, stream); break;
+            default: e = launch_group<128>(a, p, fw, whole, smem, map, stream); break;
+        }
+        if (e != cudaSuccess) return e;
     }
+    return cudaSuccess;
 }
 
 }  // namespace q8
