@@ -213,6 +213,13 @@ def test_the_longest_history():
     run(logits_of(1, 64, 15), history=history, lengths=lengths, frequency=np.float32([1e-3]))
 
 
+@pytest.mark.parametrize("N,width", [(500000, 20000), (393217, 8193), (131072, 8193)])
+def test_a_long_history_over_a_wide_vocabulary(N, width):
+    rules = everything(2, N, width, seed=18)
+    rules["history"][0, ::3] = N - 1
+    run(logits_of(2, N, 19), **rules)
+
+
 @pytest.mark.parametrize("count", [1, 300, 2047])
 def test_biases(count):
     m, N = 3, 4000

@@ -180,6 +180,57 @@ def test_residual_norm(m, K, N, group, zeros, place):
     assert np.all(np.abs(wide(out[:, :N].double()) - wide(normed)) <= bound)
 
 
+# Sizes whose tiles are one and a half waves or so: of more than 16 rows the last tiles then go apart, split over K.
+
+@pytest.mark.parametrize("m,group,sizes", [(512, 32, (14336,)), (300, 128, (4000, 5000, 3100)), (400, 64, (128, 11800, 33, 40)),
+                                           (140, 64, (21000,))])
+def test_parts_of_more_than_a_wave(m, group, sizes):
+    K = 640
+    ws = [plain_weight(K, n, group, group == 64, seed=n) for n in sizes]
+    x = rows(m, K)
+    for y, w in zip(q8.gemv4_parts(x, [q8.Weight4(*w) for w in ws]), ws):
+        check(y, x, dense(*w))
+
+
+@pytest.mark.parametrize("m,N", [(300, 8000), (129, 12001)])
+def test_gated_pair_of_more_than_a_wave(m, N):
+    K = 640
+    wg, wu = plain_weight(K, N, 64, True, seed=41), plain_weight(K, N, 64, True, seed=42)
+    x = rows(m, K)
+    out, bf = q8.gemv4_glu(x, q8.Weight4(*wg), q8.Weight4(*wu), want=("f32", "bf16"))
+    want, bound = silu_bound(*product(x, dense(*wg)), *product(x, dense(*wu)))
+    assert ((out[:, :N].double() - want).abs() - bound).max().item() <= 0
+    assert torch.equal(out.bfloat16(), bf) and not out[:, N:].any()
+
+
+def test_residual_norm_of_more_than_a_wave():
+    """In place, the sums in two launches before the norm: h is the residual and the product, the rest follows from h."""
+    m, K, N = 400, 640, 12001
+    w = plain_weight(K, N, 128, seed=43)
+    x, gamma = rows(m, K), 0.5 + torch.rand(N, device="cuda", generator=gen(44))
+    h = torch.zeros((m, q8.padded_n(N)), device="cuda")
+    h[:, :N] = torch.randn((m, N), device="cuda", generator=gen(45))
+    y, size = product(x, dense(*w))
+    want = h[:, :N].double() + y
+    _, out = q8.gemv4_residual_norm(x, q8.Weight4(*w), h, gamma, 1e-6, h=h)
+    assert ((h[:, :N].double() - want).abs() - TOL * size - 2.0 ** -24 * want.abs()).max().item() <= 0
+    got = h[:, :N].double()  # of these very sums: the mean's and the factors' fp32 roundings, then one to bf16
+    normed = got / (got.square().mean(1, keepdim=True) + 1e-6).sqrt() * gamma.double()
+    assert ((out[:, :N].double() - normed).abs() - (BF16 + 1e-5) * normed.abs()).max().item() <= 0
+    assert not h[:, N:].any() and not out[:, N:].any()
+
+
+@pytest.mark.parametrize("m", [1, 4, 5, 12])
+@pytest.mark.parametrize("group", [32, 128])
+def test_so_wide_that_a_warp_takes_two_strips(m, group):
+    K = 256
+    ws = [plain_weight(K, n, group, True, seed=n) for n in (30001, 1000, 29)]
+    x = rows(m, K)
+    for y, w in zip(q8.gemv4_parts(x, [q8.Weight4(*w) for w in ws]), ws):
+        check(y, x, dense(*w))
+    check(q8.gemv4(x, q8.Weight4(*ws[0])), x, dense(*ws[0]))
+
+
 @pytest.mark.parametrize("m", [1, 16, 77, 300])
 def test_same_bits_again_and_in_any_company(m):
     """A call gives the same bits again, and a row's bits do not depend on the other rows' values."""
