@@ -37,8 +37,9 @@ constexpr int kCols = 128;     // columns of W in a tile
 constexpr int kStepK = 64;     // rows of K in a step: 128 bytes of bf16
 constexpr int kChunkK = 128;   // rows of K in a raw stage
 constexpr int kThreadsG = 512;
-constexpr int kConvertEnd = 12, kLoadWarp = 12, kMmaWarp = 13, kXWarp = 14, kLoadUpWarp = 15;
-constexpr int kOperand = kCols * kStepK * 2;  // 16 KB: one converted step of one weight
+constexpr int kConvertEnd = 12, kLoadWarp = 12, kMmaWarp = 13, kXWarp = 14;
+constexpr int kOperand = kCols * kStepK * 2;  // 16 KB: one converted step
+constexpr int kMostRows = 256;
 constexpr int kMaxSmemG = 227 * 1024;
 constexpr int kMaxStages = 8, kMaxAcc = 4;
 constexpr int kMostSplit = 4;  // clusters of eight whole SMs find no place for all at once (61 rows of 2048 x 2048 13.3 -> 19.6 us)
@@ -47,7 +48,7 @@ __device__ unsigned int g_w4_gemm_fault = 0;
 
 struct Gemm4 {
     int tile0;   // the launch's first tile of columns
-    int rows;    // of a tile, a multiple of 32 (FW = 2) or 16
+    int rows;    // of a tile: kRows of the kernel
     int slots;   // stages of converted weights and activations
     int raws;    // stages of units
     int accs;    // accumulators
@@ -64,21 +65,28 @@ struct Control {
 
 __device__ __forceinline__ bool wait(uint64_t *bar, unsigned parity, volatile int *abort) {
     if (w4_look(bar, parity)) return true;
-    uint64_t t0, t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+    const long long t0 = clock64();
     do {
         if (w4_look(bar, parity)) return true;
-        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    } while (!*abort && t - t0 < 2000000000ull);
+    } while (!*abort && clock64() - t0 < 4000000000ll);
     if (!*abort) {
         *abort = 1;
         atomicOr(&g_w4_gemm_fault, kW4Fault);
     }
     return false;
 }
-// The same by a whole warp.
+// The same by a whole warp, without a branch that its lanes could take differently.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, unsigned parity, volatile int *abort) {
-    return __all_sync(0xffffffffu, wait(bar, parity, abort));
+    if (__all_sync(0xffffffffu, w4_look(bar, parity))) return true;
+    const long long t0 = clock64();
+    do {
+        if (__all_sync(0xffffffffu, w4_look(bar, parity))) return true;
+    } while (__all_sync(0xffffffffu, !*abort && clock64() - t0 < 4000000000ll));
+    if (!*abort) {
+        *abort = 1;
+        atomicOr(&g_w4_gemm_fault, kW4Fault);
+    }
+    return false;
 }
 
 __device__ __forceinline__ bool elect() {
@@ -130,6 +138,9 @@ __device__ __forceinline__ void tmem_ld64(uint32_t a, uint32_t *v) {
           "=r"(v[56]), "=r"(v[57]), "=r"(v[58]), "=r"(v[59]), "=r"(v[60]), "=r"(v[61]), "=r"(v[62]), "=r"(v[63])
         : "r"(a));
 }
+__device__ __forceinline__ void fma2(uint64_t &d, uint64_t a, uint32_t lo, uint32_t hi) {
+    asm("{\n .reg .b64 v;\n mov.b64 v, {%2, %3};\n fma.rn.f32x2 %0, %1, v, %0;\n}" : "+l"(d) : "l"(a), "r"(lo), "r"(hi));
+}
 __device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tma_rows(void *dst, const CUtensorMap *map, int k, int row, uint64_t *bar) {
     asm volatile(
@@ -146,31 +157,34 @@ __device__ __forceinline__ void store8(unsigned char *row, int chunk, int g, uin
         make_uint4(w4_pair<0>(w, zero), w4_pair<1>(w, zero), w4_pair<2>(w, zero), w4_pair<3>(w, zero));
 }
 
-template <int G, int P, int FW>
+template <int G, int FW, int PIECES>
 __global__ void __launch_bounds__(kThreadsG, 1)
     gemm4_kernel(const __grid_constant__ W4Args a, const Gemm4 p, const __grid_constant__ CUtensorMap xmap) {
     namespace cg = cooperative_groups;
     constexpr int CG = kChunkK / G;  // groups of a chunk
     constexpr int kConvert = 4 * FW, kTeam = FW == 1 ? 4 : 2;  // warps of a team, of two
-    constexpr int kPerAcc = 8 / P;   // 16-row pieces of one accumulator that a folding thread holds at most
+    constexpr int kLook = FW == 2 && PIECES == 8 ? 32 : 64;  // columns of tensor memory
+    constexpr int kRows = 16 * FW * PIECES, kHalf = 16 * PIECES;  // of the tile; of a folding thread
     extern __shared__ __align__(1024) unsigned char smem_g[];
-    const int chunk_bytes = CG * a.unit, raw_bytes = P * 4 * chunk_bytes;
-    const int x_bytes = p.rows * 128, slot_bytes = P * kOperand + x_bytes;
+    const int chunk_bytes = CG * a.unit, raw_bytes = 4 * chunk_bytes;
+    const int x_bytes = kRows * 128, slot_bytes = kOperand + x_bytes;
     unsigned char *slots = smem_g, *raws = slots + p.slots * slot_bytes;
     Control &ctl = *reinterpret_cast<Control *>(raws + p.raws * raw_bytes);
     volatile int *abort = &ctl.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    // the tile: 128 columns of one part, or of the gate and of the up projection
+    // the tile: four strips of one part, or two of the gate and then two of the up projection
+    const bool pair = a.epi == kW4Glu;
+    const int width = pair ? 2 : 4;  // strips of output
     int part = 0, tile = p.tile0 + blockIdx.x;
-    if (P == 1)
+    if (!pair)
         for (int first = 0, tiles;; ++part, tile -= tiles, first = a.part[part - 1].strip_end) {
             tiles = (a.part[part].strip_end - first + 3) / 4;
             if (tile < tiles || part + 1 == a.nparts) break;
         }
     const W4Part &to = a.part[part];
-    const int strips = min(4, to.Np / kW4Strip - 4 * tile);  // that exist
-    const int row0 = blockIdx.y * p.rows;
+    const int here = min(width, to.Np / kW4Strip - width * tile);  // strips that exist
+    const int row0 = blockIdx.y * kRows;
     const int groups = a.K / G, chunks = (groups + CG - 1) / CG;
     const int c0 = (int)((long long)chunks * blockIdx.z / p.ks), c1 = (int)((long long)chunks * (blockIdx.z + 1) / p.ks);
     const int rows_k = min(a.K, c1 * kChunkK) - c0 * kChunkK;  // of K in this CTA's range
@@ -178,7 +192,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < p.raws; ++i) {
-            w4_bar_init(&ctl.raw_full[i], P);
+            w4_bar_init(&ctl.raw_full[i], 1);
             w4_bar_init(&ctl.raw_empty[i], 2 * kTeam + 4 * FW);  // a team for each of two steps, the folding warps
         }
         for (int i = 0; i < p.slots; ++i) {
@@ -204,16 +218,15 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     fence_after();
     const uint32_t tmem = ctl.tmem;
 
-    const int half = p.rows / FW;  // rows of a folding thread
     if (warp < 4 * FW) {
         // ---- fold ----
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(FW == 1 ? 208 : 184));
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        float acc[128];
+        uint64_t acc[kHalf / 2];  // two rows each
 #pragma unroll
-        for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
+        for (int i = 0; i < kHalf / 2; ++i) acc[i] = 0;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-        const int col0 = (warp >> 2) * half, pieces = half / 16;
+        const int first = (warp >> 2) * kHalf;
         int raw = 0, buf = 0;
         unsigned raw_phase = 0, acc_phase = 0;
         for (int gi = 0; gi < n_groups; ++gi) {
@@ -221,39 +234,27 @@ __global__ void __launch_bounds__(kThreadsG, 1)
             if (q == 0 && !warp_wait(&ctl.raw_full[raw], raw_phase, abort)) break;
             // strip (warp % 4) of the tile is the warp's lanes
             const unsigned char *u = raws + raw * raw_bytes + (warp & 3) * chunk_bytes + q * a.unit + 16 * G + 2 * lane;
-            float s[P];
-#pragma unroll
-            for (int i = 0; i < P; ++i) s[i] = w4_scale(*reinterpret_cast<const uint16_t *>(u + i * 4 * chunk_bytes), a.bf16);
+            const float f = w4_scale(*reinterpret_cast<const uint16_t *>(u), a.bf16);
+            uint64_t s;
+            asm("mov.b64 %0, {%1, %1};" : "=l"(s) : "r"(__float_as_uint(f)));
             if (!warp_wait(&ctl.acc_full[buf], acc_phase, abort)) break;
             fence_after();
-            const uint32_t at = tmem + lanes + (uint32_t)(buf * P * p.rows + col0);
+            const uint32_t at = tmem + lanes + (uint32_t)(buf * kRows + first);
 #pragma unroll
-            for (int i = 0; i < P; ++i)
+            for (int c = 0; c < kHalf; c += kLook) {
+                uint32_t v[kLook];
+                if (kLook == 64 && c + 64 <= kHalf) {
+                    tmem_ld64(at + c, v);
+                } else {
 #pragma unroll
-                for (int c = 0; c < kPerAcc; c += 4)
-                    if (c < pieces) {
-                        // as many columns at a look as there are registers for: beside everything else a look takes some 400
-                        // clocks, whether of 16 columns or of 64
-                        uint32_t v[64];
-                        const uint32_t from = at + i * p.rows + 16 * c;
-                        if (c + 4 <= pieces) {
-                            tmem_ld64(from, v);
-                        } else {
-                            tmem_ld16(from, v);
-                            if (c + 1 < pieces) tmem_ld16(from + 16, v + 16);
-                            if (c + 2 < pieces) tmem_ld16(from + 32, v + 32);
-                        }
-                        tmem_wait();
+                    for (int k = 0; k < kLook; k += 16)
+                        if (c + k < kHalf) tmem_ld16(at + c + k, v + k);
+                }
+                tmem_wait();
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (c + k < pieces) {
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) {
-                                    float &to = acc[16 * (i * kPerAcc + c + k) + e];
-                                    to = fmaf(s[i], __uint_as_float(v[16 * k + e]), to);
-                                }
-                            }
-                    }
+                for (int k = 0; k < kLook; k += 2)
+                    if (c + k < kHalf) fma2(acc[(c + k) / 2], s, v[k], v[k + 1]);
+            }
             fence_before();
             __syncwarp();
             if (lane == 0) {
@@ -267,21 +268,11 @@ __global__ void __launch_bounds__(kThreadsG, 1)
         // carries go now, [P][rows][128].  Straight from registers to the output, a store and a residual's load at a time,
         // the same took 25 us for 256 rows.
         float *red = reinterpret_cast<float *>(smem_g);
-        const int n = 32 * (warp & 3) + lane, first = (warp >> 2) * half;
+        float *to = red + first * kCols + 32 * (warp & 3) + lane;
 #pragma unroll
-        for (int i = 0; i < P; ++i)
-#pragma unroll
-            for (int c = 0; c < kPerAcc; ++c)
-                if (16 * c < half) {
-                    float *to = red + (i * p.rows + first + 16 * c) * kCols + n;
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) to[e * kCols] = acc[16 * (i * kPerAcc + c) + e];
-                }
+        for (int e = 0; e < kHalf; ++e) to[e * kCols] = __uint_as_float((uint32_t)(e & 1 ? acc[e / 2] >> 32 : acc[e / 2]));
     } else {
-        if (FW == 1)
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-        else
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FW == 1 ? 96 : 72));
         if (warp < kConvertEnd) {
             // ---- convert ----
             const int team = (warp - kConvert) / kTeam, strip0 = (warp & (kTeam - 1)) * (4 / kTeam);
@@ -292,10 +283,10 @@ __global__ void __launch_bounds__(kThreadsG, 1)
                 if (!warp_wait(&ctl.raw_full[raw], raw_phase, abort)) break;
                 if (!warp_wait(&ctl.empty[slot], phase, abort)) break;
 #pragma unroll
-                for (int k = 0; k < P * (4 / kTeam); ++k) {
-                    const int pp = k % P, strip = strip0 + k / P;
-                    const unsigned char *from = raws + raw * raw_bytes + (4 * pp + strip) * chunk_bytes;
-                    unsigned char *operand = slots + slot * slot_bytes + pp * kOperand + strip * 32 * 128 + g * 128;
+                for (int k = 0; k < 4 / kTeam; ++k) {
+                    const int strip = strip0 + k;
+                    const unsigned char *from = raws + raw * raw_bytes + strip * chunk_bytes;
+                    unsigned char *operand = slots + slot * slot_bytes + strip * 32 * 128 + g * 128;
                     // the step's units: half of one, one, or two
                     const unsigned char *u0 = from + (G == 128 ? 1024 * (j & 1) : G == 64 ? (j & 1) * a.unit : 2 * (j & 1) * a.unit);
                     uint32_t zero[2][2][2];  // [block][tile][h]
@@ -336,25 +327,26 @@ __global__ void __launch_bounds__(kThreadsG, 1)
                 if (++raw == p.raws) raw = 0, raw_phase ^= 1;
                 if ((slot += 2) >= p.slots) slot -= p.slots, phase ^= 1;
             }
-        } else if (warp == kLoadWarp || (P == 2 && warp == kLoadUpWarp)) {
-            // ---- load units (one lane; of the gated pair a warp for each weight: a bulk copy takes some 150 clocks) ----
+        } else if (warp == kLoadWarp) {
+            // ---- load units (one lane) ----
             if (lane == 0) {
-                const int pp = warp == kLoadWarp ? 0 : 1;
                 const size_t strip_bytes = (size_t)groups * a.unit;
-                const unsigned char *src =
-                    (pp ? a.part[1].w : to.w) + (size_t)4 * tile * strip_bytes + (size_t)c0 * chunk_bytes;
-                unsigned char *dst = raws + 4 * pp * chunk_bytes;
+                const size_t at = (size_t)tile * width * strip_bytes + (size_t)c0 * chunk_bytes;
                 if (!p.prefetch) asm volatile("griddepcontrol.wait;" ::: "memory");
                 int i = 0, raw = 0;
                 unsigned raw_phase = 1;
-                for (; i < n_chunks; ++i, src += chunk_bytes) {
+                for (; i < n_chunks; ++i) {
                     if (!wait(&ctl.raw_empty[raw], raw_phase, abort)) break;
                     const unsigned bytes = (unsigned)(min(CG, groups - (c0 + i) * CG) * a.unit);
-                    w4_arrive_tx(&ctl.raw_full[raw], bytes * (unsigned)strips);
+                    w4_arrive_tx(&ctl.raw_full[raw], bytes * (unsigned)(pair ? 2 * here : here));
 #pragma unroll
-                    for (int s = 0; s < 4; ++s)
-                        if (s < strips)
-                            w4_copy(dst + raw * raw_bytes + s * chunk_bytes, src + s * strip_bytes, bytes, &ctl.raw_full[raw]);
+                    for (int s = 0; s < 4; ++s) {
+                        const int of = pair ? s & 1 : s;
+                        if (of < here)
+                            w4_copy(raws + raw * raw_bytes + s * chunk_bytes,
+                                    (pair && s > 1 ? a.part[1].w : to.w) + at + of * strip_bytes + (size_t)i * chunk_bytes,
+                                    bytes, &ctl.raw_full[raw]);
+                    }
                     if (++raw == p.raws) raw = 0, raw_phase ^= 1;
                 }
                 if (*abort)  // what was asked for lands before the memory is used again
@@ -370,7 +362,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
                 for (; j < n_steps; ++j) {
                     if (!wait(&ctl.empty[slot], phase, abort)) break;
                     w4_arrive_tx(&ctl.full[slot], (unsigned)x_bytes);
-                    tma_rows(slots + slot * slot_bytes + P * kOperand, &xmap, c0 * kChunkK + j * kStepK, row0,
+                    tma_rows(slots + slot * slot_bytes + kOperand, &xmap, c0 * kChunkK + j * kStepK, row0,
                              &ctl.full[slot]);
                     if (++slot == p.slots) slot = 0, phase ^= 1;
                 }
@@ -381,12 +373,12 @@ __global__ void __launch_bounds__(kThreadsG, 1)
             __syncwarp();
         } else if (warp == kMmaWarp) {
             // ---- multiply ----
-            const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(p.rows >> 3) << 17) |
+            const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kRows >> 3) << 17) |
                                    ((uint32_t)(kCols >> 4) << 24);
             int slot = 0, buf = 0;
             unsigned phase = 0, acc_phase = 1;
             uint32_t da = __shfl_sync(0xffffffffu, desc_low(w4_smem(slots)), 0);  // the slot's operand; its activations
-            const uint32_t base = da, next = (uint32_t)slot_bytes >> 4, xat = (uint32_t)(P * kOperand) >> 4;
+            const uint32_t base = da, next = (uint32_t)slot_bytes >> 4, xat = (uint32_t)kOperand >> 4;
             for (int j = 0; j < n_steps; ++j) {
                 if (!warp_wait(&ctl.full[slot], phase, abort)) break;
                 // the step's groups: a part of one, one, or two (of the last step perhaps only the first)
@@ -398,17 +390,13 @@ __global__ void __launch_bounds__(kThreadsG, 1)
                 if (G == 32 && ksteps > 2)
                     ok = ok && warp_wait(&ctl.acc_empty[buf1], buf1 ? acc_phase : acc_phase ^ 1, abort);
                 if (!ok) break;
-                const uint32_t d0 = tmem + (uint32_t)(buf * P * p.rows), d1 = tmem + (uint32_t)(buf1 * P * p.rows);
+                const uint32_t d0 = tmem + (uint32_t)(buf * kRows), d1 = tmem + (uint32_t)(buf1 * kRows);
                 fence_after();
                 if (elect()) {
 #pragma unroll
                     for (int s = 0; s < 4; ++s)
-                        if (s < ksteps) {
-                            const uint32_t d = s < kPer ? d0 : d1;
-#pragma unroll
-                            for (int i = 0; i < P; ++i)
-                                mma(d + i * p.rows, da + ((i * kOperand + 32 * s) >> 4), da + xat + (32 * s >> 4), idesc,
-                                    s % kPer > 0 || !fresh);
+                        if (G > 32 || s < ksteps) {
+                            mma(s < kPer ? d0 : d1, da + (32 * s >> 4), da + xat + (32 * s >> 4), idesc, s % kPer > 0 || !fresh);
                             if (G < 128 && s % kPer == kPer - 1) commit(&ctl.acc_full[s < kPer ? buf : buf1]);
                         }
                     if (G == 128 && !fresh) commit(&ctl.acc_full[buf]);
@@ -440,44 +428,46 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     const float *red = reinterpret_cast<float *>(smem_g);
     cg::cluster_group cluster = cg::this_cluster();
     if (p.ks > 1) cluster.sync();
-    const int live = min(p.rows, a.m - row0);
+    const int live = min(kRows, a.m - row0);
     const int r0 = live * (int)blockIdx.z / p.ks, r1 = live * ((int)blockIdx.z + 1) / p.ks;
-    const int c = 4 * lane, n = tile * kCols + c;
+    const int of_row = pair ? 16 : 32;  // lanes
+    const int c = 4 * (lane % of_row), n = tile * width * kW4Strip + c;
     if (n < to.Np && !*abort) {
-        auto total = [&](int r, float (&v)[4]) {
-            float4 f = *reinterpret_cast<const float4 *>(cluster.map_shared_rank(red, 0) + r * kCols + c);
+        auto total = [&](int at, float (&v)[4]) {
+            float4 f = *reinterpret_cast<const float4 *>(cluster.map_shared_rank(red, 0) + at);
 #pragma unroll 2
             for (int k = 1; k < p.ks; ++k) {
-                const float4 o = *reinterpret_cast<const float4 *>(cluster.map_shared_rank(red, k) + r * kCols + c);
+                const float4 o = *reinterpret_cast<const float4 *>(cluster.map_shared_rank(red, k) + at);
                 f.x += o.x, f.y += o.y, f.z += o.z, f.w += o.w;
             }
             v[0] = kW4Unit * f.x, v[1] = kW4Unit * f.y, v[2] = kW4Unit * f.z, v[3] = kW4Unit * f.w;
         };
-        constexpr int kWarps = kThreadsG / 32, kTogether = 4;  // rows of a warp at a time
-        for (int r = r0 + warp; r < r1; r += kWarps * kTogether) {
+        constexpr int kTogether = 4;  // rows of a thread at a time
+        const int apart = kThreadsG / of_row;
+        for (int r = r0 + (int)threadIdx.x / of_row; r < r1; r += apart * kTogether) {
             float res[kTogether][4] = {};
             if (a.epi == kW4Residual) {
 #pragma unroll
                 for (int i = 0; i < kTogether; ++i)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (r + i * kWarps < r1 && n + e < to.N)
-                            res[i][e] = __ldcg(a.res + (size_t)(row0 + r + i * kWarps) * to.Np + n + e);
+                        if (r + i * apart < r1 && n + e < to.N)
+                            res[i][e] = __ldcg(a.res + (size_t)(row0 + r + i * apart) * to.Np + n + e);
             }
 #pragma unroll
             for (int i = 0; i < kTogether; ++i) {
-                if (r + i * kWarps >= r1) break;
+                if (r + i * apart >= r1) break;
                 float v[4];
-                total(r + i * kWarps, v);
-                if (P == 2) {
+                total((r + i * apart) * kCols + c, v);
+                if (pair) {
                     float u[4];
-                    total(p.rows + r + i * kWarps, u);
+                    total((r + i * apart) * kCols + kCols / 2 + c, u);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) v[e] = v[e] / (1.0f + expf(-v[e])) * u[e];
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[e] = n + e < to.N ? v[e] + res[i][e] : 0.0f;
-                const size_t at = (size_t)(row0 + r + i * kWarps) * to.Np + n;
+                const size_t at = (size_t)(row0 + r + i * apart) * to.Np + n;
                 if (to.y) *reinterpret_cast<float4 *>(to.y + at) = make_float4(v[0], v[1], v[2], v[3]);
                 if (a.ybf) {
                     __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
@@ -492,10 +482,17 @@ __global__ void __launch_bounds__(kThreadsG, 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
 
-template <int G, int P, int FW>
+template <int G, int FW, int PIECES>
 cudaError_t launch_kernel(const W4Args &a, const Gemm4 &p, int tiles, int smem, const CUtensorMap &map, cudaStream_t stream) {
+    // the shares of setmaxnreg are of what the launch brings: a build that brings less is refused
+    static const cudaError_t brings = [] {
+        cudaFuncAttributes f;
+        const cudaError_t e = cudaFuncGetAttributes(&f, gemm4_kernel<G, FW, PIECES>);
+        return e != cudaSuccess ? e : f.numRegs < 128 ? cudaErrorNotSupported : cudaSuccess;
+    }();
+    if (brings != cudaSuccess) return brings;
     static std::atomic<uint64_t> allowed{0};
-    cudaError_t e = kv_allow_smem(gemm4_kernel<G, P, FW>, kMaxSmemG, &allowed);
+    cudaError_t e = kv_allow_smem(gemm4_kernel<G, FW, PIECES>, kMaxSmemG, &allowed);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)tiles, (unsigned)((a.m + p.rows - 1) / p.rows), (unsigned)p.ks);
@@ -514,17 +511,19 @@ cudaError_t launch_kernel(const W4Args &a, const Gemm4 &p, int tiles, int smem, 
         attr[1].val.clusterDim.z = (unsigned)p.ks;
         cfg.numAttrs = 2;
     }
-    return cudaLaunchKernelEx(&cfg, gemm4_kernel<G, P, FW>, a, p, map);
+    return cudaLaunchKernelEx(&cfg, gemm4_kernel<G, FW, PIECES>, a, p, map);
 }
 
 template <int G>
-cudaError_t launch_group(const W4Args &a, const Gemm4 &p, int fw, int tiles, int smem, const CUtensorMap &map,
-                         cudaStream_t stream) {
-    if (a.epi == kW4Glu)
-        return fw == 1 ? launch_kernel<G, 2, 1>(a, p, tiles, smem, map, stream)
-                       : launch_kernel<G, 2, 2>(a, p, tiles, smem, map, stream);
-    return fw == 1 ? launch_kernel<G, 1, 1>(a, p, tiles, smem, map, stream)
-                   : launch_kernel<G, 1, 2>(a, p, tiles, smem, map, stream);
+cudaError_t launch_group(const W4Args &a, const Gemm4 &p, int tiles, int smem, const CUtensorMap &map, cudaStream_t stream) {
+    switch (p.rows) {
+        case 32: return launch_kernel<G, 1, 2>(a, p, tiles, smem, map, stream);
+        case 64: return launch_kernel<G, 1, 4>(a, p, tiles, smem, map, stream);
+        case 128: return launch_kernel<G, 1, 8>(a, p, tiles, smem, map, stream);
+        case 160: return launch_kernel<G, 2, 5>(a, p, tiles, smem, map, stream);
+        case 192: return launch_kernel<G, 2, 6>(a, p, tiles, smem, map, stream);
+        default: return launch_kernel<G, 2, 8>(a, p, tiles, smem, map, stream);
+    }
 }
 
 }  // namespace
@@ -540,19 +539,17 @@ cudaError_t launch_w4_gemm(const W4Args &a, bool constant_weights, cudaStream_t 
     int sms = 0;
     cudaError_t e = sm_count_of_device(&sms);
     if (e != cudaSuccess) return e;
-    const int P = a.epi == kW4Glu ? 2 : 1, most = 256 / P;
     Gemm4 p = {};
     p.prefetch = constant_weights;
-    const int row_tiles = (a.m + most - 1) / most;
-    p.rows = ((a.m + row_tiles - 1) / row_tiles + 31) / 32 * 32;
-    const int fw = P * p.rows <= 128 ? 1 : 2;
-    int tiles = 0;
-    for (int i = 0; i < (P == 2 ? 1 : a.nparts); ++i)
-        tiles += (a.part[i].strip_end - (i ? a.part[i - 1].strip_end : 0) + 3) / 4;
+    const int row_tiles = (a.m + kMostRows - 1) / kMostRows;
+    const int rows = (a.m + row_tiles - 1) / row_tiles;
+    p.rows = rows <= 64 ? (rows + 31) / 32 * 32 : rows <= 128 ? 128 : rows <= 192 ? (rows + 31) / 32 * 32 : 256;
+    int tiles = a.epi == kW4Glu ? (a.part[0].strip_end + 1) / 2 : 0;
+    if (a.epi != kW4Glu)
+        for (int i = 0; i < a.nparts; ++i) tiles += (a.part[i].strip_end - (i ? a.part[i - 1].strip_end : 0) + 3) / 4;
     const int chunks = (a.K + kChunkK - 1) / kChunkK;
-    p.accs = 512 / (P * p.rows) < kMaxAcc ? 512 / (P * p.rows) : kMaxAcc;
-    const int raw = P * 4 * (kChunkK / a.group) * a.unit, slot = P * kOperand + p.rows * 128;
-    const int fixed = (int)sizeof(Control);
+    p.accs = 512 / p.rows < kMaxAcc ? 512 / p.rows : kMaxAcc;
+    const int raw = 4 * (kChunkK / a.group) * a.unit, slot = kOperand + p.rows * 128, fixed = (int)sizeof(Control);
     p.slots = 3;  // four or five were no faster
     p.raws = (kMaxSmemG - fixed - p.slots * slot) / raw;
     if (p.raws > kMaxStages) p.raws = kMaxStages;
@@ -581,9 +578,9 @@ cudaError_t launch_w4_gemm(const W4Args &a, bool constant_weights, cudaStream_t 
     for (int done = 0; done < tiles; done += whole, whole = tiles - done, p.ks = rest) {
         p.tile0 = done;
         switch (a.group) {
-            case 32: e = launch_group<32>(a, p, fw, whole, smem, map, stream); break;
-            case 64: e = launch_group<64>(a, p, fw, whole, smem, map, stream); break;
-            default: e = launch_group<128>(a, p, fw, whole, smem, map, stream); break;
+            case 32: e = launch_group<32>(a, p, whole, smem, map, stream); break;
+            case 64: e = launch_group<64>(a, p, whole, smem, map, stream); break;
+            default: e = launch_group<128>(a, p, whole, smem, map, stream); break;
         }
         if (e != cudaSuccess) return e;
     }
