@@ -50,6 +50,7 @@ __device__ __forceinline__ void w4_copy(void *dst, const void *src, unsigned byt
                  "l"(src), "r"(bytes), "r"(w4_smem(bar))
                  : "memory");
 }
+constexpr long long kW4Patience = 4000000000ll;  // clocks
 __device__ __forceinline__ bool w4_look(uint64_t *bar, unsigned parity) {
     uint32_t done;
     asm volatile(
@@ -59,15 +60,14 @@ __device__ __forceinline__ bool w4_look(uint64_t *bar, unsigned parity) {
         : "memory");
     return done != 0;
 }
-// Waits for the phase of the given parity, two seconds at most; false when that time ran out.
+// Waits for the phase of the given parity, some two seconds at most (of the SM's clock: reading the global timer first takes
+// 650 clocks); false when that time ran out.
 __device__ __forceinline__ bool w4_wait(uint64_t *bar, unsigned parity) {
     if (w4_look(bar, parity)) return true;
-    uint64_t t0, t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+    const long long t0 = clock64();
     do {
         if (w4_look(bar, parity)) return true;
-        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    } while (t - t0 < 2000000000ull);
+    } while (clock64() - t0 < kW4Patience);
     return false;
 }
 

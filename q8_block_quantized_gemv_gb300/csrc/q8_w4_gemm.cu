@@ -4,23 +4,33 @@
 // The weights are the MMA's A operand (M = 128 columns of W), the activations B (N = up to 256 rows), so that one pass over
 // the weight and one conversion of it serve all rows of the tile, and each lane of the accumulator is one column: a group's
 // scale is one number for a thread that folds.  A group's sums (the codes less zero points and the activations exact in
-// bf16) go to a fresh accumulator in tensor memory and are folded with its scales into fp32 carries in registers.
+// bf16) go to a fresh accumulator in tensor memory and are folded with its scales into fp32 carries in registers.  A gated
+// pair's tile is two strips of the gate and the same two of the up projection, 64 columns of output.
 //
 // 16 warps, one CTA per SM, K in chunks of 128 rows and steps of 64:
-//   fold        warps 0-3 (FW = 1) or 0-7 (FW = 2): a thread reads its lane of a finished accumulator, times its column's
-//               scale (packed fp32x2), into at most 128 carries
-//   convert     the warps up to 11, in teams of four that take steps in turn: codes to bf16 in the 128-byte swizzle (two
+//   fold        warps 0-3 (FW = 1) or 0-7 (FW = 2, half of the rows each): a thread reads its lane of a finished accumulator,
+//               times its column's scale (packed fp32x2), into at most 128 carries
+//   convert     the warps up to 11, in two teams that take steps in turn: codes to bf16 in the 128-byte swizzle (two
 //               columns and two 32-row blocks a thread at a time; odd columns store their second block first, so that
 //               eight lanes' 16-byte stores fall on all banks)
 //   load        warp 12: units by bulk copies; warp 14: activations by TMA (64 values x the tile's rows; rows past m are
 //               zeros).  One warp for both kept the activations of a chunk behind the fold of the one before.
-//   multiply    warp 13, converged, one lane elected for the instructions
-// FW = 1 where a thread's columns of both accumulators' rows are at most 128 in all (tiles of up to 128 rows; the gated
-// pair, which has two accumulators, up to 64); there the conversion is what bounds, and has eight warps for four.
-// Registers: the fold's 128 carries want 184 a thread; the others give theirs up (setmaxnreg; 512 x 128 in all).
+//   multiply    warp 13, converged, one lane elected for the instructions (a lane alone in the loop was 2 to 4% slower)
+// The fold's 128 carries and a look at tensor memory want 184 to 208 registers a thread; the others give theirs up (setmaxnreg,
+// of the launch's 512 x 128).
+//
+// What bounds it: up to 128 rows the latency of the hand-overs, a step's 450 clocks of waits and instructions of the multiplying
+// warp and 600 of a team, beside 200 of MMAs; beyond, shared memory (an MMA's operands, the converted codes, the
+// activations: 104 KB a step of 256 rows, 830 clocks at 128 bytes each, for 512 of MMAs) and, in groups of 32 and 64, the fold.
+// Hence waits without divergence and loops whose counts the compiler knows: with branches on the tile's rows 24 rows of
+// 4096 x 9000 in groups of 32 took 30 us, without 18, and, handing over four groups at a time, 13.4.  Measured: 512 rows of
+// 4096 x 14336, groups of 128, 49 us (1.22 PFLOP/s); the gated pair of 301 rows, 4096 x 14336, groups of 64, 93 us; 61 rows of
+// 2048 x 2048, groups of 32, with the norm 9.2 us.  The converted codes in tensor memory instead of shared memory (640 threads,
+// tiles of 160 rows) took 71 us for the first: a step then costs 600 clocks for 128 rows.
 //
 // Where the tiles do not fill the SMs, K is split over a cluster, whose carries are added in rank order through shared
-// memory.  Every wait ends after two seconds: the CTA then stops, waits as long for what is in flight, and reports a fault.
+// memory.  Every wait ends after some two seconds: the CTA then stops, waits as long for what is in flight, and reports a
+// fault.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -51,7 +61,7 @@ struct Gemm4 {
     int rows;    // of a tile: kRows of the kernel
     int slots;   // stages of converted weights and activations
     int raws;    // stages of units
-    int accs;    // accumulators
+    int accs;    // sets of accumulators
     int ks;      // CTAs of a cluster splitting K
     int prefetch;
 };
@@ -68,7 +78,7 @@ __device__ __forceinline__ bool wait(uint64_t *bar, unsigned parity, volatile in
     const long long t0 = clock64();
     do {
         if (w4_look(bar, parity)) return true;
-    } while (!*abort && clock64() - t0 < 4000000000ll);
+    } while (!*abort && clock64() - t0 < kW4Patience);
     if (!*abort) {
         *abort = 1;
         atomicOr(&g_w4_gemm_fault, kW4Fault);
@@ -81,7 +91,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, unsigned parity, volati
     const long long t0 = clock64();
     do {
         if (__all_sync(0xffffffffu, w4_look(bar, parity))) return true;
-    } while (__all_sync(0xffffffffu, !*abort && clock64() - t0 < 4000000000ll));
+    } while (__all_sync(0xffffffffu, !*abort && clock64() - t0 < kW4Patience));
     if (!*abort) {
         *abort = 1;
         atomicOr(&g_w4_gemm_fault, kW4Fault);
@@ -157,6 +167,15 @@ __device__ __forceinline__ void store8(unsigned char *row, int chunk, int g, uin
         make_uint4(w4_pair<0>(w, zero), w4_pair<1>(w, zero), w4_pair<2>(w, zero), w4_pair<3>(w, zero));
 }
 
+// Groups whose sums are handed to the fold at a time: as many of a chunk as fit twice into tensor memory, where tiles are small
+// (24 rows of 4096 x 9000 in groups of 32 18.4 -> 13.9 us, 64 rows 20.3 -> 17.5); one in tiles of 96 rows and more, whose sums
+// then take long to read (100 rows 26 -> 31 us with two).
+constexpr int groups_at_once(int G, int rows) {
+    int t = rows <= 64 ? kChunkK / G : 1;
+    while (t > 1 && 2 * t * rows > 512) t /= 2;
+    return t;
+}
+
 template <int G, int FW, int PIECES>
 __global__ void __launch_bounds__(kThreadsG, 1)
     gemm4_kernel(const __grid_constant__ W4Args a, const Gemm4 p, const __grid_constant__ CUtensorMap xmap) {
@@ -165,6 +184,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     constexpr int kConvert = 4 * FW, kTeam = FW == 1 ? 4 : 2;  // warps of a team, of two
     constexpr int kLook = FW == 2 && PIECES == 8 ? 32 : 64;  // columns of tensor memory
     constexpr int kRows = 16 * FW * PIECES, kHalf = 16 * PIECES;  // of the tile; of a folding thread
+    constexpr int T = groups_at_once(G, kRows);
     extern __shared__ __align__(1024) unsigned char smem_g[];
     const int chunk_bytes = CG * a.unit, raw_bytes = 4 * chunk_bytes;
     const int x_bytes = kRows * 128, slot_bytes = kOperand + x_bytes;
@@ -229,43 +249,48 @@ __global__ void __launch_bounds__(kThreadsG, 1)
         const int first = (warp >> 2) * kHalf;
         int raw = 0, buf = 0;
         unsigned raw_phase = 0, acc_phase = 0;
-        for (int gi = 0; gi < n_groups; ++gi) {
-            const int q = gi & (CG - 1);
-            if (q == 0 && !warp_wait(&ctl.raw_full[raw], raw_phase, abort)) break;
-            // strip (warp % 4) of the tile is the warp's lanes
-            const unsigned char *u = raws + raw * raw_bytes + (warp & 3) * chunk_bytes + q * a.unit + 16 * G + 2 * lane;
-            const float f = w4_scale(*reinterpret_cast<const uint16_t *>(u), a.bf16);
-            uint64_t s;
-            asm("mov.b64 %0, {%1, %1};" : "=l"(s) : "r"(__float_as_uint(f)));
+        for (int gi = 0; gi < n_groups;) {
+            if ((gi & (CG - 1)) == 0 && !warp_wait(&ctl.raw_full[raw], raw_phase, abort)) break;
             if (!warp_wait(&ctl.acc_full[buf], acc_phase, abort)) break;
             fence_after();
-            const uint32_t at = tmem + lanes + (uint32_t)(buf * kRows + first);
+            // strip (warp % 4) of the tile is the warp's lanes
+            const unsigned char *u =
+                raws + raw * raw_bytes + (warp & 3) * chunk_bytes + (gi & (CG - 1)) * a.unit + 16 * G + 2 * lane;
+            uint32_t at = tmem + lanes + (uint32_t)(buf * T * kRows + first);
+            const int end = min(gi + T, n_groups);
+            do {
+                const float f = w4_scale(*reinterpret_cast<const uint16_t *>(u), a.bf16);
+                uint64_t s;
+                asm("mov.b64 %0, {%1, %1};" : "=l"(s) : "r"(__float_as_uint(f)));
 #pragma unroll
-            for (int c = 0; c < kHalf; c += kLook) {
-                uint32_t v[kLook];
-                if (kLook == 64 && c + 64 <= kHalf) {
-                    tmem_ld64(at + c, v);
-                } else {
+                for (int c = 0; c < kHalf; c += kLook) {
+                    uint32_t v[kLook];
+                    if (kLook == 64 && c + 64 <= kHalf) {
+                        tmem_ld64(at + c, v);
+                    } else {
 #pragma unroll
-                    for (int k = 0; k < kLook; k += 16)
-                        if (c + k < kHalf) tmem_ld16(at + c + k, v + k);
+                        for (int k = 0; k < kLook; k += 16)
+                            if (c + k < kHalf) tmem_ld16(at + c + k, v + k);
+                    }
+                    tmem_wait();
+#pragma unroll
+                    for (int k = 0; k < kLook; k += 2)
+                        if (c + k < kHalf) fma2(acc[(c + k) / 2], s, v[k], v[k + 1]);
                 }
-                tmem_wait();
-#pragma unroll
-                for (int k = 0; k < kLook; k += 2)
-                    if (c + k < kHalf) fma2(acc[(c + k) / 2], s, v[k], v[k + 1]);
-            }
+                u += a.unit, at += kRows;
+            } while (++gi < end);
             fence_before();
             __syncwarp();
+            const bool chunk_done = (gi & (CG - 1)) == 0;
             if (lane == 0) {
                 w4_arrive(&ctl.acc_empty[buf]);
-                if (q == CG - 1) w4_arrive(&ctl.raw_empty[raw]);
+                if (chunk_done) w4_arrive(&ctl.raw_empty[raw]);
             }
             if (++buf == p.accs) buf = 0, acc_phase ^= 1;
-            if (q == CG - 1 && ++raw == p.raws) raw = 0, raw_phase ^= 1;
+            if (chunk_done && ++raw == p.raws) raw = 0, raw_phase ^= 1;
         }
         // The last group's sums are in: every MMA of the CTA is done, and with them every use of the operands, where the
-        // carries go now, [P][rows][128].  Straight from registers to the output, a store and a residual's load at a time,
+        // carries go now, [rows][128].  Straight from registers to the output, a store and a residual's load at a time,
         // the same took 25 us for 256 rows.
         float *red = reinterpret_cast<float *>(smem_g);
         float *to = red + first * kCols + 32 * (warp & 3) + lane;
@@ -380,31 +405,38 @@ __global__ void __launch_bounds__(kThreadsG, 1)
             uint32_t da = __shfl_sync(0xffffffffu, desc_low(w4_smem(slots)), 0);  // the slot's operand; its activations
             const uint32_t base = da, next = (uint32_t)slot_bytes >> 4, xat = (uint32_t)kOperand >> 4;
             for (int j = 0; j < n_steps; ++j) {
-                if (!warp_wait(&ctl.full[slot], phase, abort)) break;
-                // the step's groups: a part of one, one, or two (of the last step perhaps only the first)
-                const int ksteps = min(4, (rows_k - j * kStepK) / 16);
-                constexpr int kPer = G == 32 ? 2 : 4;  // MMAs of a group in a step
-                const bool fresh = G < 128 || (j & 1) == 0;
+                const int ksteps = G > 32 ? 4 : min(4, (rows_k - j * kStepK) / 16);
+                // a set of accumulators is of several steps, one, or half of one
+                constexpr int kSteps = T * G / kStepK, kSets = kSteps ? 1 : 2;
+                const int of = kSteps > 1 ? j & (kSteps - 1) : 0;  // the step in its set
                 const int buf1 = buf + 1 == p.accs ? 0 : buf + 1;
-                bool ok = !fresh || warp_wait(&ctl.acc_empty[buf], acc_phase, abort);
-                if (G == 32 && ksteps > 2)
-                    ok = ok && warp_wait(&ctl.acc_empty[buf1], buf1 ? acc_phase : acc_phase ^ 1, abort);
-                if (!ok) break;
-                const uint32_t d0 = tmem + (uint32_t)(buf * kRows), d1 = tmem + (uint32_t)(buf1 * kRows);
+                // (all looked at together where all are there)
+                const unsigned phase1 = buf1 ? acc_phase : acc_phase ^ 1;
+                const bool second = kSets == 2 && ksteps > 2;
+                bool there = w4_look(&ctl.full[slot], phase) & w4_look(&ctl.acc_empty[buf], acc_phase);
+                if (second) there &= w4_look(&ctl.acc_empty[buf1], phase1);
+                if (!__all_sync(0xffffffffu, there)) {
+                    bool ok = warp_wait(&ctl.full[slot], phase, abort) && warp_wait(&ctl.acc_empty[buf], acc_phase, abort);
+                    if (second) ok = ok && warp_wait(&ctl.acc_empty[buf1], phase1, abort);
+                    if (!ok) break;
+                }
+                const uint32_t d0 = tmem + (uint32_t)((buf * T + of * kStepK / G) * kRows), d1 = tmem + (uint32_t)(buf1 * kRows);
+                const bool done = of == kSteps - 1 || j + 1 == n_steps;
                 fence_after();
                 if (elect()) {
 #pragma unroll
                     for (int s = 0; s < 4; ++s)
                         if (G > 32 || s < ksteps) {
-                            mma(s < kPer ? d0 : d1, da + (32 * s >> 4), da + xat + (32 * s >> 4), idesc, s % kPer > 0 || !fresh);
-                            if (G < 128 && s % kPer == kPer - 1) commit(&ctl.acc_full[s < kPer ? buf : buf1]);
+                            const uint32_t d = s * 16 < G ? d0 : kSets == 2 ? d1 : d0 + kRows;
+                            mma(d, da + (32 * s >> 4), da + xat + (32 * s >> 4), idesc, 16 * s % G > 0 || (G > kStepK && of > 0));
+                            if (kSets == 2 && s % 2) commit(&ctl.acc_full[s < 2 ? buf : buf1]);
                         }
-                    if (G == 128 && !fresh) commit(&ctl.acc_full[buf]);
+                    if (kSets == 1 && done) commit(&ctl.acc_full[buf]);
                     commit(&ctl.empty[slot]);
                 }
                 __syncwarp();
-                if (G < 128 || !fresh)
-                    for (int i = 0; i < (G == 32 ? ksteps / 2 : 1); ++i)
+                if (kSets == 2 || done)
+                    for (int i = 0; i < (kSets == 2 ? ksteps / 2 : 1); ++i)
                         if (++buf == p.accs) buf = 0, acc_phase ^= 1;
                 da += next;
                 if (++slot == p.slots) slot = 0, phase ^= 1, da = base;
@@ -558,16 +590,17 @@ cudaError_t launch_w4_gemm(const W4Args &a, bool constant_weights, cudaStream_t 
     if (a.epi != kW4Glu)
         for (int i = 0; i < a.nparts; ++i) tiles += (a.part[i].strip_end - (i ? a.part[i - 1].strip_end : 0) + 3) / 4;
     const int chunks = (a.K + kChunkK - 1) / kChunkK;
-    p.accs = 512 / p.rows < kMaxAcc ? 512 / p.rows : kMaxAcc;
+    p.accs = 512 / (groups_at_once(a.group, p.rows) * p.rows);
+    if (p.accs > kMaxAcc) p.accs = kMaxAcc;
     const int raw = 4 * (kChunkK / a.group) * a.unit, slot = kOperand + p.rows * 128, fixed = (int)sizeof(Control);
-    p.slots = 3;  // four or five were no faster
+    p.slots = p.rows <= 64 ? 6 : 4;  // with three 64 rows of 4096 x 9000 took 13.8 us for 12.7, 512 of 4096 x 14336 51 for 49
     p.raws = (kMaxSmemG - fixed - p.slots * slot) / raw;
     if (p.raws > kMaxStages) p.raws = kMaxStages;
     const int smem = fixed + p.slots * slot + p.raws * raw;
 
     // K splits, in chunks of a CTA's time, which beside its own takes some eight for its beginning and end: of all tiles; or
     // the waves that are full unsplit and the tiles of the last one apart, split, in a launch of their own (512 rows of
-    // 4096 x 14336, 224 tiles on 152 SMs: see the measured table).
+    // 4096 x 14336, 224 tiles on 152 SMs, 62 -> 53 us).
     auto waves = [&](int t, int k) { return (double)(((long long)t * row_tiles * k + sms - 1) / sms); };
     auto cost = [&](int t, int k) { return waves(t, k) * (8.0 + (double)((chunks + k - 1) / k)); };
     auto best = [&](int t) {
