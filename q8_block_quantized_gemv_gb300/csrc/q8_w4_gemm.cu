@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     namespace cg = cooperative_groups;
     constexpr int CG = kChunkK / G;  // groups of a chunk
     constexpr int kConvert = 4 * FW, kTeam = FW == 1 ? 4 : 2;  // warps of a team, of two
-    constexpr int kLook = FW == 2 && PIECES == 8 ? 32 : 64;  // columns of tensor memory
+    constexpr int kLook = FW == 1 || PIECES < 5 ? 64 : PIECES == 5 ? 80 : PIECES == 6 ? 48 : 32;  // columns of tensor memory
     constexpr int kRows = 16 * FW * PIECES, kHalf = 16 * PIECES;  // of the tile; of a folding thread
     constexpr int T = groups_at_once(G, kRows);
     extern __shared__ __align__(1024) unsigned char smem_g[];
@@ -265,13 +265,11 @@ __global__ void __launch_bounds__(kThreadsG, 1)
 #pragma unroll
                 for (int c = 0; c < kHalf; c += kLook) {
                     uint32_t v[kLook];
-                    if (kLook == 64 && c + 64 <= kHalf) {
-                        tmem_ld64(at + c, v);
-                    } else {
+                    constexpr int kLong = kLook >= 64 && kHalf >= 64 ? 64 : 0;
+                    if (kLong && c + 64 <= kHalf) tmem_ld64(at + c, v);
 #pragma unroll
-                        for (int k = 0; k < kLook; k += 16)
-                            if (c + k < kHalf) tmem_ld16(at + c + k, v + k);
-                    }
+                    for (int k = 0; k < kLook; k += 16)
+                        if ((k >= kLong || c + 64 > kHalf) && c + k < kHalf) tmem_ld16(at + c + k, v + k);
                     tmem_wait();
 #pragma unroll
                     for (int k = 0; k < kLook; k += 2)
