@@ -487,7 +487,8 @@ q8_status q8_w4_repack(const void *blocks, int K, int N, uint8_t *codes, uint16_
  * Codes less zero points and activations enter the tensor cores exactly (bf16); a group's sums are fp32, scaled in fp32
  * and added in fp32 in an order fixed for (m, K, N, group) and the device: each output is within
  * 1e-5 * sum |x s (c - z)| of the real number, and repeated calls give identical bits.
- * Up to 16 rows run as streams of the weight, more on tcgen05 (one launch either way).
+ * Up to 16 rows run as a stream of the weight, one launch; more on tcgen05, one launch or two (the tiles of a last partial
+ * wave apart, with a K split of their own).
  * Errors: Q8_ERR_ARG (NULL pointers, unknown flags, parts that differ in group or flags, overlaps), Q8_ERR_SHAPE (m, K, N,
  * group, nparts), Q8_ERR_ALIGN, Q8_ERR_CUDA. */
 q8_status q8_gemv4_parts(const void *x, const q8_weight4 *weights, float *const *y, int nparts, int m, int K,
@@ -498,13 +499,14 @@ q8_status q8_gemv4(const void *x, const q8_weight4 *weight, float *y, int m, int
                    q8_stream_t stream);
 
 /* The gated pair: out = silu(x . Wg) * (x . Wu), silu(g) = g / (1 + exp(-g)), as q8_gemv_glu; gate and up have the same N,
- * group and flags.  out fp32 [m][Np], out_bf16 bf16 [m][Np] (rounded to nearest even), either may be NULL; pads 0.  One
- * launch.  Other arguments and errors as q8_gemv4_parts. */
+ * group and flags.  out fp32 [m][Np], out_bf16 bf16 [m][Np] (rounded to nearest even), either may be NULL; pads 0.
+ * Launches, other arguments and errors as q8_gemv4_parts. */
 q8_status q8_gemv4_glu(const void *x, const q8_weight4 *gate, const q8_weight4 *up, float *out, void *out_bf16, int m,
                        int K, unsigned int flags, q8_stream_t stream);
 
 /* The product, the residual add and the next RMS norm, as q8_gemv_residual_norm (its arguments and aliasing: h may be
- * residual itself): h = residual + x . W, out = h / sqrt(mean(h^2) + eps) * gamma.  Two launches. */
+ * residual itself): h = residual + x . W, out = h / sqrt(mean(h^2) + eps) * gamma.  The product's
+ * launches (as q8_gemv4_parts) and one more. */
 q8_status q8_gemv4_residual_norm(const void *x, const q8_weight4 *weight, const float *residual, const float *gamma,
                                  float eps, float *h, void *out_bf16, int m, int K, unsigned int flags,
                                  q8_stream_t stream);
