@@ -368,16 +368,22 @@ cudaError_t launch_w4_stream(const W4Args &a, bool constant_weights, cudaStream_
     int sms = 0;
     cudaError_t e = sm_count_of_device(&sms);
     if (e != cudaSuccess) return e;
-    // Strips a warp: two share the activations' way from L2 from five rows on, and where there are enough strips for a wave
-    // of such CTAs (4096 x 128256 at one row 56.8 -> 53.5 us); one otherwise, so that more warps share the weight.
+    // Strips a warp: two share the activations' way from L2 from five rows on, where there are enough strips for a wave of
+    // such CTAs (4096 x 128256 at one row 56.8 -> 53.5 us), and where the weight is large (14336 x 4096 in groups of 64, four
+    // rows 13.3 -> 10.5 us, two 11.6 -> 10.1; 4096 x 4096 in groups of 32, four rows 6.3 -> 5.8, but two 5.1 -> 6.0; one row of
+    // 4096 x 14336 8.5 -> 9.5); one otherwise, so that more warps share the weight (5120 x 1500, four rows 4.1 us, with two
+    // strips 4.9).
     Stream4 p = {a.m > 8 ? 16 : 0, 1, 1, constant_weights};
     const bool pair = a.epi == kW4Glu;
     const int strips = pair ? 2 * a.part[0].strip_end : a.part[a.nparts - 1].strip_end;
-    const int S = pair || a.m > 4 || strips >= 6 * sms ? 2 : 1;
+    const int chunks = (a.K + kChunk - 1) / kChunk;
+    const long long units = (long long)strips * chunks;
+    const bool large = a.m > 2 ? units >= 26ll * sms : units >= 54ll * sms && strips <= sms;
+    const int S = pair || a.m > 4 || strips >= 6 * sms || large ? 2 : 1;
     const int fit = a.m > 8 ? 2 : S == 2 ? 3 : 4;  // CTAs an SM by their registers
     // K is split while the CTAs fill no more than three quarters of what fits at once (512 CTAs where 608 fit were no faster
     // than 256, and a second wave costs a whole one), and while each warp has a chunk.
-    const int tiles = tiles_of(a, S), chunks = (a.K + kChunk - 1) / kChunk;
+    const int tiles = tiles_of(a, S);
     while (p.ks < 8 && 2ll * p.ks * tiles * 4 <= 3ll * fit * sms && 2 * p.ks * kWarps4 <= chunks) p.ks *= 2;
     // As many stages as leave room for the CTAs that an SM gets.
     const long long ctas = (long long)tiles * p.ks;

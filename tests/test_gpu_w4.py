@@ -231,6 +231,14 @@ def test_so_wide_that_a_warp_takes_two_strips(m, group):
     check(q8.gemv4(x, q8.Weight4(*ws[0])), x, dense(*ws[0]))
 
 
+@pytest.mark.parametrize("m", [1, 2, 3, 4])
+def test_few_rows_of_a_large_weight(m):
+    """Where two strips a warp are taken for the weight's size, odd strips and a K that ends inside a chunk among them."""
+    w = plain_weight(8224, 4040, 32, True, seed=46)
+    x = rows(m, 8224)
+    check(q8.gemv4(x, q8.Weight4(*w)), x, dense(*w))
+
+
 @pytest.mark.parametrize("m", [1, 16, 77, 300])
 def test_same_bits_again_and_in_any_company(m):
     """A call gives the same bits again, and a row's bits do not depend on the other rows' values."""
