@@ -7,6 +7,9 @@
 // atomics, whose order does not matter.  A history of up to kLocal tokens is read whole by every CTA of the row, which keeps
 // what falls into its slice and needs no word from the others; of a longer one each CTA reads its share and sends what it
 // finds to the owner through distributed shared memory.  A vocabulary beyond eight slices of kMostSlice takes several turns.
+// What else bounds it is instructions, 62% of the issue slots in a large step, and a CTA's beginning, when it makes its words and
+// streams nothing.  Measured: 256 rows of 128256, histories of 2001, 300 biases, masks and noise 103.5 us (3.8 TB/s of the 6.8
+// that a copy reaches), 16 rows with histories of 8191 21.3 us, one row of 32000 5.8 us.
 // The first logits are asked for before the words are made.  Each step of a rule is one fp32 operation rounded once (no
 // contraction), so that the bits are those of any other implementation.
 #include <cooperative_groups.h>

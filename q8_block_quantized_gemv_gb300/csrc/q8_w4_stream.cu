@@ -14,6 +14,9 @@
 //     columns of B that nothing reads: they repeat the last row.
 //   - A group's sums start from zero and are folded with its scales into an fp32 carry; (c - z) / 64 and x are exact in bf16.
 //   - S strips share the activations' way from L2, which at m = 16 are as long as two strips' codes.
+//   - Measured, groups of 128: one row of 4096 x 128256 53.5 us (5.1 TB/s of the 6.8 that a copy reaches; 70% of the issue
+//     slots: conversion, MMAs, and the beginning and end of each of the 2004 CTAs), the gated pair of 4096 x 14336 14.6 us
+//     (4.2 TB/s), 16 rows of 4096 x 6144 7.2 us; one row of 4096 x 4096 in groups of 32 4.8 us, nearly all of it latency.
 //   - The warps' carries are added in shared memory in order, then, where the strips are too few for the SMs and K is split
 //     over a cluster, those of its CTAs in rank order.
 #include <cooperative_groups.h>
