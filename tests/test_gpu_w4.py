@@ -239,6 +239,19 @@ def test_few_rows_of_a_large_weight(m):
     check(q8.gemv4(x, q8.Weight4(*w)), x, dense(*w))
 
 
+@pytest.mark.parametrize("m", [1, 7, 16, 17, 50, 70, 100, 140, 180, 250, 512])
+@pytest.mark.parametrize("group,K", [(32, 32), (32, 96), (32, 160), (32, 1056), (32, 2144), (64, 64), (64, 192), (64, 1088)])
+def test_depths_that_end_inside_a_chunk(m, group, K):
+    """One to three groups in the last chunk of 128 rows, with and without a split of K, beside whole numbers that must be exact."""
+    w = plain_weight(K, 200, group, True, seed=K)
+    x = rows(m, K)
+    check(q8.gemv4(x, q8.Weight4(*w)), x, dense(*w))
+    scales = torch.exp2(torch.randint(-3, 4, w[1].shape, device="cuda", generator=gen(m)).float()).half()
+    x = torch.randint(-8, 9, (m, K), device="cuda", generator=gen(m + 1)).to(torch.bfloat16)
+    want, _ = product(x, dense(w[0], scales, w[2]))
+    assert torch.equal(q8.gemv4(x, q8.Weight4(w[0], scales, w[2]))[:, :200].double(), want)
+
+
 @pytest.mark.parametrize("m", [1, 16, 77, 300])
 def test_same_bits_again_and_in_any_company(m):
     """A call gives the same bits again, and a row's bits do not depend on the other rows' values."""
