@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
                     const unsigned char *from = raws + raw * raw_bytes + strip * chunk_bytes;
                     unsigned char *operand = slots + slot * slot_bytes + strip * 32 * 128 + g * 128;
                     // the step's units: half of one, one, or two
-                    const unsigned char *u0 = from + (G == 128 ? 1024 * (j & 1) : G == 64 ? (j & 1) * a.unit : 2 * (j & 1) * a.unit);
+                    const unsigned char *u0 = from + (j & 1) * (G == 128 ? 1024 : G == 64 ? a.unit : 2 * a.unit);
                     uint32_t zero[2][2][2];  // [block][tile][h]
                     const unsigned char *z = (G == 128 ? from : u0) + 16 * G + 64 + g;
 #pragma unroll
