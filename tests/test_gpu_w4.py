@@ -252,6 +252,14 @@ def test_depths_that_end_inside_a_chunk(m, group, K):
     assert torch.equal(q8.gemv4(x, q8.Weight4(w[0], scales, w[2]))[:, :200].double(), want)
 
 
+@pytest.mark.parametrize("m,K,N,group", [(1, 1056, 60001, 32), (8, 2112, 61000, 64), (16, 4096, 60100, 128), (12, 160, 90000, 32)])
+def test_many_waves_of_streams(m, K, N, group):
+    w = plain_weight(K, N, group, True, seed=m)
+    x = rows(m, K)
+    for constant in (False, True):
+        check(q8.gemv4(x, q8.Weight4(*w), constant_weights=constant), x, dense(*w))
+
+
 @pytest.mark.parametrize("m", [1, 16, 77, 300])
 def test_same_bits_again_and_in_any_company(m):
     """A call gives the same bits again, and a row's bits do not depend on the other rows' values."""
