@@ -281,7 +281,7 @@ def main():
         torch.cuda.synchronize()
         return result, t[0].elapsed_time(t[1])
 
-    Server(model, 1, 1, a.page, a.cache).prefill([[0]])  # what initializes on first use
+    Server(model, 1, 1, a.page, a.cache, rules=rules).prefill([[0]])  # what initializes on first use
     first, ms = timed(lambda: server.prefill(prompts))
     print(f"prefill: {sum(map(len, prompts))} tokens of {a.requests} prompts in {ms:.2f} ms")
     few = min(2, a.tokens)
