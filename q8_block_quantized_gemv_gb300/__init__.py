@@ -131,6 +131,9 @@ def _check(status: int, where: str):
         raise Q8Error(status, where)
 
 
+_INT_MAX = 2 ** 31 - 1  # the library's sizes and row pitches are 32-bit: ctypes would pass the low bits of a larger one
+
+
 def padded_n(N: int) -> int:
     return lib().q8_padded_n(N)
 
@@ -571,7 +574,10 @@ def _table_of(table, R, index):
             (shape[1] > 1 and table.stride(1) != 1):
         raise ValueError(f"the block table must be an int32 CUDA tensor [{R}, width] with unit column stride, on the device "
                          "of the others")
-    return table.data_ptr(), shape[1], table.stride(0) if R > 1 else shape[1]
+    pitch = table.stride(0) if R > 1 else shape[1]
+    if pitch > _INT_MAX or R > _INT_MAX:
+        raise ValueError("the block table's rows are more than 2^31 - 1, or as far apart")
+    return table.data_ptr(), shape[1], pitch
 
 
 def kv_slots(cached, fresh, table, free_pages, page_size: int, rows: int, head=None, stream=None, out=None):
@@ -652,7 +658,10 @@ def _rows2(name, x, dtype, cols, index):
     if x.get_device() != index or x.dtype != dtype or len(shape) != 2 or shape[1] < cols or x.stride(1) != 1:
         raise ValueError(f"{name} must be a 2-D {dtype} CUDA tensor of at least {cols} columns, unit column stride, on the "
                          "cache's device")
-    return x.data_ptr(), x.stride(0) if shape[0] > 1 else cols  # one row has no pitch
+    pitch = x.stride(0) if shape[0] > 1 else cols  # one row has no pitch
+    if pitch > _INT_MAX or shape[0] > _INT_MAX:
+        raise ValueError(f"the rows of {name} are more than 2^31 - 1, or as far apart")
+    return x.data_ptr(), pitch
 
 
 def rope_append(q, k, v, cache: KVCache, positions, slots, table=None, q_heads: int | None = None,
@@ -802,7 +811,7 @@ class Weight4:
         if scales.shape[1] != N or (zeros is not None and zeros.shape != scales.shape) or not groups or K % groups:
             raise ValueError("scales and zeros must be [K / group, N], codes [K / 2, N]")
         flags = (FLAG_W4_ZEROS if zeros is not None else 0) | (FLAG_W4_BF16 if scales.dtype == torch.bfloat16 else 0)
-        size = int(lib().q8_w4_bytes(K, N, K // groups, flags))
+        size = _w4_bytes(K, N, K // groups, flags)
         if size < 0:
             raise ValueError("a group is 32, 64 or 128 rows")
         self._keep(_new((size,), torch.uint8, codes.device, stream), K, N, K // groups, flags)
@@ -815,7 +824,7 @@ class Weight4:
         """A weight whose tiled form (uint8 CUDA tensor, 16-byte aligned) is at hand."""
         import torch
         flags = (FLAG_W4_ZEROS if zeros else 0) | (FLAG_W4_BF16 if bf16_scales else 0)
-        size = int(lib().q8_w4_bytes(K, N, group, flags))
+        size = _w4_bytes(K, N, group, flags)
         if size < 0 or not buf.is_cuda or buf.dtype != torch.uint8 or not buf.is_contiguous() or buf.numel() != size:
             raise ValueError(f"buf must be a contiguous uint8 CUDA tensor of {size} bytes")
         self = cls.__new__(cls)
@@ -836,6 +845,11 @@ FLAG_W4_ZEROS = 1
 FLAG_W4_BF16 = 2
 
 
+def _w4_bytes(K, N, group, flags):
+    """q8_w4_bytes; -1 for sizes that are not the library's, those beyond its 32 bits among them."""
+    return int(lib().q8_w4_bytes(K, N, group, flags)) if all(0 < n <= _INT_MAX for n in (K, N, group)) else -1
+
+
 def tile4(codes, scales, zeros=None, bf16_scales: bool = False):
     """Host: numpy arrays in the plain form (scales as 16-bit words) -> the tiled bytes (q8_w4_tile)."""
     codes = np.ascontiguousarray(codes, dtype=np.uint8)
@@ -846,7 +860,9 @@ def tile4(codes, scales, zeros=None, bf16_scales: bool = False):
     if scales.shape[1] != N or (zeros is not None and zeros.shape != scales.shape) or not groups or K % groups:
         raise ValueError("scales and zeros must be [K / group, N], codes [K / 2, N]")
     flags = (FLAG_W4_ZEROS if zeros is not None else 0) | (FLAG_W4_BF16 if bf16_scales else 0)
-    out = np.empty(max(int(lib().q8_w4_bytes(K, N, K // groups, flags)), 1), dtype=np.uint8)
+    if max(K, N) > _INT_MAX:
+        raise ValueError("K and N must be less than 2^31")
+    out = np.empty(max(_w4_bytes(K, N, K // groups, flags), 1), dtype=np.uint8)
     _check(lib().q8_w4_tile(codes.ctypes.data, scales.ctypes.data, None if zeros is None else zeros.ctypes.data, K, N,
                             K // groups, flags, out.ctypes.data), "q8_w4_tile")
     return out
@@ -856,6 +872,8 @@ def repack4(blocks, K: int, N: int):
     """(codes uint8 [K/2, N], scales float16 [K/32, N]) from N * K/32 Q4_0 checkpoint blocks of 18 bytes (host)."""
     raw = np.frombuffer(bytes(blocks), dtype=np.uint8) if not isinstance(blocks, np.ndarray) else \
         np.ascontiguousarray(blocks).view(np.uint8).reshape(-1)
+    if max(abs(K), abs(N)) > _INT_MAX:
+        raise ValueError("K and N must be less than 2^31")
     if K > 0 and N > 0 and raw.size != N * (K // Q8_BLOCK) * 18:
         raise ValueError("block buffer size does not match K and N")
     codes = np.empty((max(K // 2, 1), max(N, 1)), dtype=np.uint8)
@@ -974,10 +992,12 @@ def _pitched(name, t, dtype, rows, cols, index):
     shape = t.shape
     if t.dtype is dtype and len(shape) == 2 and shape[0] == rows and shape[1] >= cols and t.get_device() == index:
         pitch, unit = t.stride()
-        if (unit == 1 or shape[1] == 1) and (rows <= 1 or pitch >= shape[1]):
-            return t.data_ptr(), pitch if rows > 1 else shape[1]
+        if rows <= 1:
+            pitch = shape[1]
+        if (unit == 1 or shape[1] == 1) and shape[1] <= pitch <= _INT_MAX and rows <= _INT_MAX:
+            return t.data_ptr(), pitch
     raise ValueError(f"{name} must be a 2-D {dtype} CUDA tensor of {rows} rows and at least {cols} columns, unit column stride, "
-                     "on the device of the logits")
+                     "rows less than 2^31 values apart, on the device of the logits")
 
 
 def _row_values(name, t, dtype, m, index):
@@ -1011,6 +1031,8 @@ def choose(logits, N: int | None = None, out=None, repetition=None, frequency=No
     m = shape[0]
     if N is None:
         N = shape[1]
+    if N < 1:
+        raise ValueError("N must be positive")
     lp, ldl = _pitched("logits", logits, f32, m, N, index)
     op, ldo = (None, 0) if out is None else _pitched("out", out, f32, m, N, index)
     hp = wide = hpitch = hwidth = bp = vp = bwidth = mp = mcount = mpitch = np_ = npitch = 0
