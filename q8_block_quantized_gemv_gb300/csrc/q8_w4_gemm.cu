@@ -30,7 +30,8 @@
 //
 // Where the tiles do not fill the SMs, K is split over a cluster, whose carries are added in rank order through shared
 // memory.  Every wait ends after some two seconds: the CTA then stops, waits as long for what is in flight, and reports a
-// fault.
+// fault.  No such clock starts while the kernel before may still run, however long that takes: a warp waits for its end
+// (griddepcontrol.wait) ahead of the first barrier that hangs on its results or on room that those free.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -302,7 +303,9 @@ __global__ void __launch_bounds__(kThreadsG, 1)
             const int g = lane >> 2, t = lane & 3, odd = g & 1;
             int raw = 0, slot = team;
             unsigned raw_phase = 0, phase = 1;  // a fresh barrier passes for the phase before its first
+            const int early = p.prefetch ? min(p.slots, 2 * p.raws) : 0;  // steps that need nothing of the kernel before
             for (int j = team; j < n_steps; j += 2) {  // a team has one step of every chunk
+                if (j >= early && j < early + 2) asm volatile("griddepcontrol.wait;" ::: "memory");
                 if (!warp_wait(&ctl.raw_full[raw], raw_phase, abort)) break;
                 if (!warp_wait(&ctl.empty[slot], phase, abort)) break;
 #pragma unroll
@@ -355,10 +358,11 @@ __global__ void __launch_bounds__(kThreadsG, 1)
             if (lane == 0) {
                 const size_t strip_bytes = (size_t)groups * a.unit;
                 const size_t at = (size_t)tile * width * strip_bytes + (size_t)c0 * chunk_bytes;
-                if (!p.prefetch) asm volatile("griddepcontrol.wait;" ::: "memory");
+                const int early = p.prefetch ? p.raws : 0;  // chunks that find an empty stage
                 int i = 0, raw = 0;
                 unsigned raw_phase = 1;
                 for (; i < n_chunks; ++i) {
+                    if (i == early) asm volatile("griddepcontrol.wait;" ::: "memory");
                     if (!wait(&ctl.raw_empty[raw], raw_phase, abort)) break;
                     const unsigned bytes = (unsigned)(min(CG, groups - (c0 + i) * CG) * a.unit);
                     w4_arrive_tx(&ctl.raw_full[raw], bytes * (unsigned)(pair ? 2 * here : here));
@@ -396,6 +400,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
             __syncwarp();
         } else if (warp == kMmaWarp) {
             // ---- multiply ----
+            asm volatile("griddepcontrol.wait;" ::: "memory");
             const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kRows >> 3) << 17) |
                                    ((uint32_t)(kCols >> 4) << 24);
             int slot = 0, buf = 0;
