@@ -469,6 +469,8 @@ int64_t q8_w4_bytes(int K, int N, int group, unsigned int flags);
 
 /* Plain -> tiled, on the host, and on the device enqueued on `stream` (w 16-byte aligned there, scales 2-byte; w may not
  * overlap an input).  zeros is NULL exactly when flags has no Q8_W4_ZEROS.  The low seven bits of a zero point count.
+ * On the device two launches, the second only to order what comes after: a product on `stream` may take the weight with
+ * Q8_FLAG_CONSTANT_WEIGHTS at once.
  * Errors: Q8_ERR_ARG (NULL pointers, zeros against flags, unknown flags, overlaps), Q8_ERR_SHAPE, Q8_ERR_ALIGN. */
 q8_status q8_w4_tile(const uint8_t *codes, const void *scales, const uint8_t *zeros, int K, int N, int group,
                      unsigned int flags, void *w);
@@ -483,7 +485,8 @@ q8_status q8_w4_repack(const void *blocks, int K, int N, uint8_t *codes, uint16_
 /* y_p = x . W_p for every part p, 1 <= nparts <= Q8_MAX_PARTS; all parts have the same K, group and flags.
  *   x  device, bf16 [m][K], 16-byte aligned, 1 <= m <= Q8_MAX_CHUNK        y  host array of device pointers, fp32
  *   [m][q8_padded_n(N_p)] (written, 0 in the pad columns), 16-byte aligned, none overlapping an input or another y
- *   flags  Q8_FLAG_CONSTANT_WEIGHTS or 0
+ *   flags  Q8_FLAG_CONSTANT_WEIGHTS (no work enqueued before this call on `stream` writes a weight's tiled form, other than
+ *          q8_w4_tile_device; the call may read it before that work has ended) or 0
  * Codes less zero points and activations enter the tensor cores exactly (bf16); a group's sums are fp32, scaled in fp32
  * and added in fp32 in an order fixed for (m, K, N, group) and the device: each output is within
  * 1e-5 * sum |x s (c - z)| of the real number, and repeated calls give identical bits.

@@ -795,7 +795,9 @@ class Weight4:
     """A weight of 4-bit codes with group scales, laid out for the products (q8_w4_tile_device): value = scale * (code -
     zero).  From CUDA tensors as a checkpoint has them: ``codes`` uint8 [K/2, N] (row 2i in the low half of byte row i),
     ``scales`` float16 or bfloat16 [K/group, N] with group 32, 64 or 128, ``zeros`` uint8 [K/group, N] of 0..127 (None: 8
-    everywhere).  Keeps its own copy, ``buf``; :func:`tile4` lays it out on the host, :meth:`of_tiled` takes that."""
+    everywhere).  Keeps its own copy, ``buf``; :func:`tile4` lays it out on the host, :meth:`of_tiled` takes that.  Products on the
+    same stream may take it with ``constant_weights`` at once; other work that writes ``buf`` (a copy into a tensor given to
+    :meth:`of_tiled`) has to have ended before such a call is made."""
 
     def __init__(self, codes, scales, zeros=None, stream=None):
         import torch

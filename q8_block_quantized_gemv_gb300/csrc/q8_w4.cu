@@ -59,6 +59,11 @@ __global__ void tile_kernel(const uint8_t *__restrict__ codes, const uint16_t *_
     tile_column(codes, scales, zeros, N, group, n < N ? (int)n : N, (int)(u % groups), c, w + u * unit);
 }
 
+// Nothing, behind tile_kernel: a kernel launched without the programmatic attribute starts when all before it has ended and its
+// writes are seen, so that a product that starts early starts behind those writes.  Behind tile_kernel itself its first
+// copies of a weight declared constant would be ordered by nothing.
+__global__ void tiled_kernel() {}
+
 // A product's weight against K; `first` is the call's first weight.
 q8_status check_weight(const q8_weight4 *w, const q8_weight4 *first, int K) {
     if (!w || !w->w || (w->flags & ~kWeightFlags) || w->group != first->group || w->flags != first->flags)
@@ -133,6 +138,7 @@ extern "C" q8_status q8_w4_tile_device(const uint8_t *codes, const void *scales,
     tile_kernel<<<(unsigned)((units + 7) / 8), 256, 0, (cudaStream_t)stream>>>(
         codes, static_cast<const uint16_t *>(scales), zeros, N, group, K / group, q8::w4_unit(group, zeros != nullptr),
         units, static_cast<unsigned char *>(w));
+    tiled_kernel<<<1, 32, 0, (cudaStream_t)stream>>>();
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? Q8_OK : kv_cuda_fail(e);
 }
