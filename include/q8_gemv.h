@@ -488,8 +488,11 @@ q8_status q8_w4_repack(const void *blocks, int K, int N, uint8_t *codes, uint16_
  *   flags  Q8_FLAG_CONSTANT_WEIGHTS (no work enqueued before this call on `stream` writes a weight's tiled form, other than
  *          q8_w4_tile_device; the call may read it before that work has ended) or 0
  * Codes less zero points and activations enter the tensor cores exactly (bf16); a group's sums are fp32, scaled in fp32
- * and added in fp32 in an order fixed for (m, K, N, group) and the device: each output is within
- * 1e-5 * sum |x s (c - z)| of the real number, and repeated calls give identical bits.
+ * and added in fp32 in a fixed order, so that repeated calls give identical bits.  Each output is within
+ * max(1e-5, (K / group + 64) * 2^-24) * sum |x s (c - z)| of the real number: one rounding a group where all of K is one
+ * carry's, and 64 for the sums within a group and the joins.  Equal terms, whose roundings do not cancel, measured a quarter
+ * of it (512 rows, K = 28672 in groups of 32: 1.3e-5; up to 16 rows, whose K is shared by warps, 2e-6 to 8e-6), random
+ * positive ones 3e-6 at most.
  * Up to 16 rows run as a stream of the weight, one launch; more on tcgen05, one launch or two (the tiles of a last partial
  * wave apart, with a K split of their own).
  * Errors: Q8_ERR_ARG (NULL pointers, unknown flags, parts that differ in group or flags, overlaps), Q8_ERR_SHAPE (m, K, N,
