@@ -488,7 +488,9 @@ q8_status q8_w4_repack(const void *blocks, int K, int N, uint8_t *codes, uint16_
  *   flags  Q8_FLAG_CONSTANT_WEIGHTS (no work enqueued before this call on `stream` writes a weight's tiled form, other than
  *          q8_w4_tile_device; the call may read it before that work has ended) or 0
  * Codes less zero points and activations enter the tensor cores exactly (bf16); a group's sums are fp32, scaled in fp32
- * and added in fp32 in a fixed order, so that repeated calls give identical bits.  Each output is within
+ * and added in fp32 in an order fixed for the entry point, m, K, the group, the widths of all the call's weights and the
+ * device: repeated calls give identical bits, whatever the other rows and weights hold.  (How K is split follows the tiles of the
+ * whole call, so that a weight alone and beside others may differ in the last bits.)  Each output is within
  * max(1e-5, (K / group + 64) * 2^-24) * sum |x s (c - z)| of the real number: one rounding a group where all of K is one
  * carry's, and 64 for the sums within a group and the joins.  Equal terms, whose roundings do not cancel, measured a quarter
  * of it (512 rows, K = 28672 in groups of 32: 1.3e-5; up to 16 rows, whose K is shared by warps, 2e-6 to 8e-6), random

@@ -67,3 +67,29 @@ def test_positive_terms(m, K, N, group):
         worst = max(worst, off(y[:, a:a + c.shape[1]], x.double() @ c, c.shape[1]))
     print(f"{m} x {K} x {N}, groups of {group}: {worst:.1f} of {units(K, group):.1f} units ({worst * 2 ** -24:.2e})")
     assert worst <= units(K, group)
+
+
+@pytest.mark.parametrize("m", [1, 5, 16, 30, 100, 300])
+@pytest.mark.parametrize("sizes", [(96, 1000, 33), (40, 9000, 600), (15000, 64, 8000)])
+def test_bits_follow_the_widths_of_the_call(m, sizes):
+    """A part's bits do not depend on what the other parts hold; alone it may be added up in another order, within the bound."""
+    K, group, u = 1024, 64, 2.0 ** -24
+    g = torch.Generator("cuda").manual_seed(m)
+
+    def weight(n):
+        codes = torch.randint(0, 256, (K // 2, n), dtype=torch.uint8, device="cuda", generator=g)
+        return codes, (torch.randn((K // group, n), device="cuda", generator=g) * 0.01).half()
+
+    x = torch.randn((m, K), device="cuda", generator=g).bfloat16()
+    plain = [weight(n) for n in sizes]
+    ws = [q8.Weight4(*w) for w in plain]
+    ys = q8.gemv4_parts(x, ws)
+    assert all(torch.equal(a, b) for a, b in zip(q8.gemv4_parts(x, ws), ys))
+    others = [q8.Weight4(*weight(n)) for n in sizes]
+    for i, n in enumerate(sizes):
+        assert torch.equal(q8.gemv4_parts(x, [ws[j] if j == i else w for j, w in enumerate(others)])[i], ys[i])
+        codes, scales = plain[i]
+        dense = (torch.stack([codes & 15, codes >> 4], 1).flatten(0, 1).double() - 8) * scales.double().repeat_interleave(group, 0)
+        want, size = x.double() @ dense, x.double().abs() @ dense.abs()
+        for y in (ys[i], q8.gemv4(x, ws[i])):
+            assert ((y[:, :n].double() - want).abs() <= units(K, group) * u * size).all()
