@@ -92,7 +92,9 @@ int q8_padded_n(int N);
  *   1 <= m <= 16 (1 <= m <= 512 over the tiled storage, Q8_MAX_CHUNK), K > 0, K % 32 == 0 ("from_q8.rs",
  *   `q8_gemv_applies`), N > 0.
  * y must not overlap x, q or s.  Every output n < Np is written; outputs n >= N are 0.0f.
- * Each y[r, n] equals the real-number product within 1e-5 * sum_b |s[b,n]| sum_i |x[r,32b+i] q[32b+i,n]|; the
+ * Each y[r, n] equals the real-number product within 1e-5 * sum_b |s[b,n]| sum_i |x[r,32b+i] q[32b+i,n]| for K up to
+ * 14336 (equal terms of 512 rows, whose roundings do not cancel, reach 6.7e-6 there), and beyond within
+ * (K / 32 + 64) * 2^-24 of that sum: the fp32 carry is rounded once a block (equal terms reach 1.3e-5 at K = 28672); the
  * summation order is fixed for a given (m, K, N) and device, so repeated calls give identical bits. */
 q8_status q8_gemv(const void *x, const int8_t *q, const float *s, float *y, int m, int K, int N, q8_stream_t stream);
 
