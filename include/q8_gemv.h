@@ -531,7 +531,8 @@ typedef struct {
     const int *bias_ids;   /* int32 [m][bias_width]: tokens with a bias; ids outside 0..N-1 are unused places */
     const float *bias;     /* fp32 [m][bias_width]: their biases (required with bias_ids) */
     const int *mask;       /* int32 [mask_count][mask_pitch]: bit n % 32 of word n / 32 set: token n is allowed */
-    const int *mask_rows;  /* int32 [m]: the mask of each row, none outside 0..mask_count-1 (NULL: row r has mask r) */
+    const int *mask_rows;  /* int32 [m]: the mask of each row, none outside 0..mask_count-1 (requires mask; NULL:
+                              row r has mask r, and there have to be m of them) */
     const float *noise;    /* fp32 [m][noise_pitch]: added for the choice alone */
     int history_width, history_pitch, history_wide, bias_width, mask_count, mask_pitch, noise_pitch;
 } q8_choice;

@@ -1023,8 +1023,9 @@ def choose(logits, N: int | None = None, out=None, repetition=None, frequency=No
     ``lengths`` (int32 [m]) tokens of a row count, the first ``prompts`` (int32 [m]) of those as prompt: repetition looks at
     all of them, frequency and presence at the others.  bias_ids int32 and bias fp32 [m, count]: tokens with a bias, ids
     outside the vocabulary are unused places.  mask: int32 [masks, >= ceil(N / 32)], a set bit n % 32 of word n / 32 allows
-    token n; mask_rows int32 [m]: the mask of each row, -1 for none (default: mask r for row r).  noise: fp32 [m, >= N], added
-    for the choice where the temperature is above 0 (Gumbel noise samples softmax(out))."""
+    token n; mask_rows int32 [m]: the mask of each row, none where it is outside 0 .. masks-1 (default: mask r for row r, of
+    which there have to be m).  noise: fp32 [m, >= N], added for the choice where the temperature is above 0 (Gumbel noise
+    samples softmax(out))."""
     import torch
     f32, i32 = torch.float32, torch.int32
     index, shape = logits.get_device(), logits.shape
@@ -1057,6 +1058,10 @@ def choose(logits, N: int | None = None, out=None, repetition=None, frequency=No
         raise ValueError("bias needs bias_ids")
     if mask is not None:
         mcount = mask.shape[0]
+        if m and mcount < (m if mask_rows is None else 1):
+            raise ValueError("a mask for each row, or mask_rows and at least one mask")
+    elif mask_rows is not None:
+        raise ValueError("mask_rows needs mask")
         mp, mpitch = _pitched("mask", mask, i32, mcount, (N + 31) // 32, index)
     if noise is not None:
         np_, npitch = _pitched("noise", noise, f32, m, N, index)

@@ -411,11 +411,11 @@ extern "C" q8_status q8_choose(const float *logits, int ldl, const q8_choice *ru
     q8::ChooseArgs a = {};
     if (rules) a.c = *rules;
     const q8_choice &c = a.c;
-    if ((c.history && !c.lengths) || (!c.bias_ids != !c.bias)) return Q8_ERR_ARG;
+    if ((c.history && !c.lengths) || (!c.bias_ids != !c.bias) || (c.mask_rows && !c.mask)) return Q8_ERR_ARG;
     if (c.history && (c.history_width < 1 || c.history_width > Q8_MAX_HISTORY || c.history_pitch < c.history_width))
         return Q8_ERR_SHAPE;
     if (c.bias_ids && (c.bias_width < 1 || c.bias_width > Q8_MAX_BIAS)) return Q8_ERR_SHAPE;
-    if (c.mask && (c.mask_count < 1 || c.mask_pitch < (N - 1) / 32 + 1)) return Q8_ERR_SHAPE;
+    if (c.mask && (c.mask_count < (c.mask_rows ? 1 : m) || c.mask_pitch < (N - 1) / 32 + 1)) return Q8_ERR_SHAPE;
     if (c.noise && c.noise_pitch < N) return Q8_ERR_SHAPE;
     const void *words[] = {logits, out, c.repetition, c.frequency, c.presence, c.temperature, c.lengths,
                            c.prompts, c.bias_ids, c.bias, c.mask, c.mask_rows, c.noise};
