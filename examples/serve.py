@@ -113,6 +113,10 @@ class Rules:
 
     def tensors(self, requests, vocab, most):
         """The arguments of choose for so many requests whose conversations have up to `most` tokens."""
+        if self.allowed is not None and (self.allowed.dtype != torch.bool or self.allowed.shape != (vocab,) or not self.allowed.any()):
+            # (choose would say -1, which the next step would look up as the last token)
+            raise ValueError(f"allowed must be bool [{vocab}] and allow a token")
+
         def rows(x):
             return torch.full((requests,), float(x), device="cuda")
 
