@@ -443,7 +443,7 @@ q8_status q8_attn_prefill(const void *q, int ldq, const q8_kv_cache *cache, cons
 /* A 4-bit weight: codes c in 0..15, and for each group of `group` consecutive rows of a column a 16-bit scale s and a
  * zero point z:
  *     W[k, n] = s[k / group, n] * (c[k, n] - z[k / group, n])
- *   group  32, 64 or 128; K a multiple of it
+ *   group  32, 64 or 128; K a multiple of it, at most 2^31 - 128
  *   flags  Q8_W4_ZEROS: the zero points are given (without it z = 8 everywhere); Q8_W4_BF16: the scales are bf16 (without
  *          it fp16)
  * As a checkpoint has it ("plain"):

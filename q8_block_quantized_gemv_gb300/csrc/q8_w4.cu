@@ -1,4 +1,5 @@
 // Weights of 4 bits with group scales: the tiled form, argument checks and the entry points of their products.
+#include <limits.h>
 #include <math.h>
 #include <string.h>
 
@@ -108,7 +109,8 @@ q8_status launch(const q8::W4Args &a, unsigned flags, q8_stream_t stream) {
 }  // namespace
 
 extern "C" int64_t q8_w4_bytes(int K, int N, int group, unsigned int flags) {
-    if ((group != 32 && group != 64 && group != 128) || K <= 0 || K % group != 0 || q8_padded_n(N) < 0 ||
+    // (the products count rows of K to the end of the last 128 in an int)
+    if ((group != 32 && group != 64 && group != 128) || K <= 0 || K > INT_MAX - 127 || K % group != 0 || q8_padded_n(N) < 0 ||
         (flags & ~kWeightFlags))
         return -1;
     return (int64_t)(q8_padded_n(N) / q8::kW4Strip) * (K / group) * q8::w4_unit(group, (flags & Q8_W4_ZEROS) != 0);

@@ -79,3 +79,14 @@ def test_weights(K, N):
     with pytest.raises(ValueError, match="2.31"):  # as its low bits this is K = 32, of a buffer made for less
         q8.repack4(b"", 32 - WRAP, 1)
     assert q8._w4_bytes(K, N, 32, 0) == -1 and q8._w4_bytes(32, 32, WRAP + 32, 0) == -1
+
+
+def test_depths_at_the_end_of_an_int():
+    """The products round K up to whole 128s."""
+    lib = q8.lib()
+    for K in (2 ** 31 - 32, 2 ** 31 - 64, 2 ** 31 - 96):
+        assert q8._w4_bytes(K, 32, 32, 0) == -1
+        w = q8._W4(1 << 33, 32, 32, 0)
+        assert lib.q8_gemv4(1 << 44, q8.ctypes.addressof(w), 1 << 45, 3, K, 0, None) == 2  # SHAPE
+    assert q8._w4_bytes(2 ** 31 - 128, 32, 128, 0) == (2 ** 24 - 1) * (16 * 128 + 64)
+    assert q8._w4_bytes(2 ** 31 - 128, 32, 32, 0) == (2 ** 26 - 4) * (16 * 32 + 64)
