@@ -1060,9 +1060,9 @@ def choose(logits, N: int | None = None, out=None, repetition=None, frequency=No
         mcount = mask.shape[0]
         if m and mcount < (m if mask_rows is None else 1):
             raise ValueError("a mask for each row, or mask_rows and at least one mask")
+        mp, mpitch = _pitched("mask", mask, i32, mcount, (N + 31) // 32, index)
     elif mask_rows is not None:
         raise ValueError("mask_rows needs mask")
-        mp, mpitch = _pitched("mask", mask, i32, mcount, (N + 31) // 32, index)
     if noise is not None:
         np_, npitch = _pitched("noise", noise, f32, m, N, index)
     if idx is None:
