@@ -9,7 +9,7 @@
 // finds to the owner through distributed shared memory.  A vocabulary beyond eight slices of kMostSlice takes several turns.
 // What else bounds it is instructions, 62% of the issue slots in a large step, and a CTA's beginning, when it makes its words and
 // streams nothing.  Measured: 256 rows of 128256, histories of 2001, 300 biases, masks and noise 103.5 us (3.8 TB/s of the 6.8
-// that a copy reaches), 16 rows with histories of 8191 21.3 us, one row of 32000 5.8 us.
+// that a copy reaches), 16 rows with histories of 8191 21.1 us, one row of 32000 5.8 us.
 // The first logits are asked for before the words are made.  Each step of a rule is one fp32 operation rounded once (no
 // contraction), so that the bits are those of any other implementation.
 #include <cooperative_groups.h>
@@ -24,6 +24,11 @@ namespace {
 
 constexpr int kMostCtas = 8;
 constexpr int kMostSlice = 49152;  // 192 KB of words
+// The longest history that every CTA of a row reads whole.  Sharing it out costs two cluster-wide barriers and atomics in other
+// SMs' memory.  Measured with 20 biases, masks and noise over 128256 tokens, read whole and shared out: one row with a history
+// of 2000 10.7 and 12.0 us, of 8191 12.3 and 15.4, of 16000 14.0 and 18.6; 16 rows 20.5 and 23.7, 23.7 and 30.8, 27.2 and 37.1;
+// 64 rows with 16000 45.4 and 65.1.  The two do not meet up to 32000 (16 rows 33.3 and 49.9): for lengths of 8193 to 32000 the
+// other side of this border would be the faster one.
 constexpr int kLocal = 8192;
 
 // A token's word: how often it stands in the answer in the low 20 bits, its place among the biases + 1 in the next 11,
@@ -441,7 +446,8 @@ extern "C" q8_status q8_choose(const float *logits, int ldl, const q8_choice *ru
     a.ldo = ldo;
     a.N = N;
     a.words = c.history || c.bias_ids;
-    // Eight CTAs a row, fewer where a slice would be less than 2048 tokens (one turn of a CTA's threads).
+    // Eight CTAs a row, fewer for vocabularies of up to 8192 tokens: doubled while a CTA would have more than 2048, so that
+    // slices are of more than 1024 (half a step of 512 threads, four tokens each).
     int ctas = 1;
     while (ctas < q8::kMostCtas && ctas * 2048 < N) ctas *= 2;
     const int slice = ((N + ctas - 1) / ctas + 127) / 128 * 128;

@@ -20,13 +20,16 @@
 // of the launch's 512 x 128).
 //
 // What bounds it: up to 128 rows the latency of the hand-overs, a step's 450 clocks of waits and instructions of the multiplying
-// warp and 600 of a team, beside 200 of MMAs; beyond, shared memory (an MMA's operands, the converted codes, the
-// activations: 104 KB a step of 256 rows, 830 clocks at 128 bytes each, for 512 of MMAs) and, in groups of 32 and 64, the fold.
-// Hence waits without divergence and loops whose counts the compiler knows: with branches on the tile's rows 24 rows of
-// 4096 x 9000 in groups of 32 took 30 us, without 18, and, handing over four groups at a time, 13.4.  Measured: 512 rows of
-// 4096 x 14336, groups of 128, 49 us (1.22 PFLOP/s); the gated pair of 301 rows, 4096 x 14336, groups of 64, 93 us; 61 rows of
-// 2048 x 2048, groups of 32, with the norm 9.2 us.  The converted codes in tensor memory instead of shared memory (640 threads,
-// tiles of 160 rows) took 71 us for the first: a step then costs 600 clocks for 128 rows.
+// warp and 600 of a team, beside 200 of MMAs.  Beyond, in groups of 32 and 64, the fold (256 rows of 4096 x 9000 in groups of
+// 32 40.9 us, with the fold left out 29.7; the gated pair of 301 rows in groups of 64 92.4 and 78.2, without conversion
+// 83.4); in groups of 128 no one part: 512 rows of 4096 x 14336 take 49.1 us, without conversion 44.5, without MMAs 46.8,
+// without activations 46.8, without the fold 47.7, and 32.9 with all four left out, of which the copies of the units, the
+// hand-overs and the two launches' beginnings and ends remain.  Hence waits without divergence and loops whose counts the
+// compiler knows: with branches on the tile's rows 24 rows of 4096 x 9000 in groups of 32 took 30 us, without 18, and, handing
+// over four groups at a time, 12.9.  Measured: 512 rows of 4096 x 14336, groups of 128, 49 us (1.22 PFLOP/s); the gated pair of
+// 301 rows, 4096 x 14336, groups of 64, 92 us; 61 rows of 2048 x 2048, groups of 32, with the norm 9.2 us.  The converted codes
+// in tensor memory instead of shared memory (640 threads, tiles of 160 rows) took 71 us for the first: a step then costs 600
+// clocks for 128 rows.
 //
 // Where the tiles do not fill the SMs, K is split over a cluster, whose carries are added in rank order through shared
 // memory.  Every wait ends after some two seconds: the CTA then stops, waits as long for what is in flight, and reports a
@@ -169,8 +172,8 @@ __device__ __forceinline__ void store8(unsigned char *row, int chunk, int g, uin
 }
 
 // Groups whose sums are handed to the fold at a time: as many of a chunk as fit twice into tensor memory, where tiles are small
-// (24 rows of 4096 x 9000 in groups of 32 18.4 -> 13.9 us, 64 rows 20.3 -> 17.5); one in tiles of 96 rows and more, whose sums
-// then take long to read (100 rows 26 -> 31 us with two).
+// (24 rows of 4096 x 9000 in groups of 32 18.3 -> 12.9 us, in groups of 64 12.6 -> 12.1; 64 rows 20.1 -> 15.1 and 15.0 -> 13.5);
+// one in tiles of 96 rows and more, whose sums then take long to read (100 rows 25.4 -> 31.9 us with two, 17.1 -> 19.0).
 constexpr int groups_at_once(int G, int rows) {
     int t = rows <= 64 ? kChunkK / G : 1;
     while (t > 1 && 2 * t * rows > 512) t /= 2;
@@ -549,9 +552,9 @@ cudaError_t launch_kernel(const W4Args &a, const Gemm4 &p, int tiles, int smem, 
     return cudaLaunchKernelEx(&cfg, gemm4_kernel<G, FW, PIECES>, a, p, map);
 }
 
-// Four warps fold where that is the lesser part, the groups long beside the rows: 64 rows of 4096 x 9000 take 13.7 us with four
-// and 15.9 with eight in groups of 128, 15.6 and 16.8 in groups of 64, 22.9 and 20.3 in groups of 32; 100 rows 15.8 and 17.4,
-// 20.1 and 18.2, 31.3 and 25.7.
+// Four warps fold where that is the lesser part, the groups long beside the rows: 24 rows of 4096 x 9000 take 11.6 us with four
+// and 12.9 with eight in groups of 128, 12.1 and 13.3 in groups of 64, 12.9 and 13.9 in groups of 32; 64 rows 12.7 and 13.7,
+// 13.5 and 14.4, 15.3 and 15.1; 100 rows 14.3 and 15.1, 19.2 and 17.1, 29.4 and 25.4.
 template <int G, int ROWS>
 cudaError_t launch_rows(const W4Args &a, const Gemm4 &p, int tiles, int smem, const CUtensorMap &map, cudaStream_t stream) {
     constexpr int FW = ROWS <= G ? 1 : 2;
@@ -596,7 +599,7 @@ cudaError_t launch_w4_gemm(const W4Args &a, bool constant_weights, cudaStream_t 
     p.accs = 512 / (groups_at_once(a.group, p.rows) * p.rows);
     if (p.accs > kMaxAcc) p.accs = kMaxAcc;
     const int raw = 4 * (kChunkK / a.group) * a.unit, slot = kOperand + p.rows * 128, fixed = (int)sizeof(Control);
-    p.slots = p.rows <= 64 ? 6 : 4;  // with three 64 rows of 4096 x 9000 took 13.8 us for 12.7, 512 of 4096 x 14336 51 for 49
+    p.slots = p.rows <= 64 ? 6 : 4;  // with three 64 rows of 4096 x 9000 took 13.6 us for 12.7, 512 of 4096 x 14336 51 for 49
     p.raws = (kMaxSmemG - fixed - p.slots * slot) / raw;
     if (p.raws > kMaxStages) p.raws = kMaxStages;
     const int smem = fixed + p.slots * slot + p.raws * raw;
