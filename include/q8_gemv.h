@@ -99,7 +99,8 @@ int q8_padded_n(int N);
 q8_status q8_gemv(const void *x, const int8_t *q, const float *s, float *y, int m, int K, int N, q8_stream_t stream);
 
 /* Flags of q8_gemv_ex. */
-#define Q8_FLAG_CONSTANT_WEIGHTS 1u /* no work enqueued before this call on `stream` writes q or s: the pipelined
+#define Q8_FLAG_CONSTANT_WEIGHTS 1u /* no work enqueued before this call on `stream` writes q or s, other than
+                                       q8_tile_device (which ends with a launch that orders what follows): the pipelined
                                        kernel may start streaming them before the previous kernel on the stream has
                                        finished (programmatic dependent launch); x and y are still ordered */
 

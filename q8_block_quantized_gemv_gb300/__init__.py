@@ -281,8 +281,8 @@ def gemv(x, q, s, N: int, y=None, variant: str = "auto", constant_weights: bool 
          stream=None):
     """y = x . W over the Q8_0 weight (q, s); returns y, fp32 [m, Np] (columns N .. Np-1 are 0).
 
-    constant_weights: nothing enqueued earlier on the stream writes q or s (Q8_FLAG_CONSTANT_WEIGHTS), so the
-    kernel may stream them before the previous kernel finishes.  tiled: q and s are in the tiled layout
+    constant_weights: nothing enqueued earlier on the stream, other than :func:`tile_device`, writes q or s
+    (Q8_FLAG_CONSTANT_WEIGHTS), so the kernel may stream them before the previous kernel finishes.  tiled: q and s are in the tiled layout
     (:func:`tile_device`, Q8_FLAG_TILED)."""
     import torch
     m, K, Np = _check_operands(x, q, s, N, tiled)

@@ -24,6 +24,10 @@ namespace {
 
 constexpr int kTileCols = 128;
 
+// Nothing, behind tile_values_kernel: a kernel launched without the programmatic attribute starts when all before it has ended
+// and its writes are seen, so that the first reads of a product that starts early are ordered behind those writes.
+__global__ void tiled_kernel() {}
+
 // One thread per 16-byte chunk of the tiled values (four rows of four columns); the first 8 threads of a unit also
 // write its scales.
 __global__ void tile_values_kernel(const int8_t *__restrict__ q, const float *__restrict__ s, int K, int N, int Np,
@@ -112,6 +116,10 @@ extern "C" q8_status q8_tile_device(const int8_t *q, const float *s, int K, int 
     cfg.blockDim = dim3(threads, 1, 1);
     cfg.stream = (cudaStream_t)stream;
     cudaError_t e = cudaLaunchKernelEx(&cfg, tile_values_kernel, q, s, K, N, Np, qt, st, chunks);
+    if (e == cudaSuccess) {
+        tiled_kernel<<<1, 32, 0, (cudaStream_t)stream>>>();
+        e = cudaGetLastError();
+    }
     if (e != cudaSuccess) {
         q8::set_last_cuda_error((int)e);
         return Q8_ERR_CUDA;

@@ -63,3 +63,31 @@ def test_a_constant_product_starts_behind_the_layout(m):
     starts, ends = {a for a, _, _ in edges}, {b for _, b, _ in edges}
     assert len(starts - ends) == 1 and len(ends - starts) == 1 and len(edges) == len(starts)  # a chain
     assert not all(p for _, _, p in edges)  # and does not reach back to the layout
+
+
+@pytest.mark.parametrize("m", [1, 16, 40])
+def test_the_same_over_q8_weights(m):
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    K, N = 256, 128
+    g = torch.Generator("cuda").manual_seed(m)
+    q = torch.randint(-127, 128, (K, N), dtype=torch.int8, device="cuda", generator=g)
+    s = torch.rand((K // 32, N), device="cuda", generator=g)
+    x = torch.randn((m, K), device="cuda", generator=g).bfloat16()
+    qt, st = q8.tile_device(q, s, N)
+    y = torch.empty((m, N), device="cuda")
+    side = torch.cuda.Stream()
+    q8.gemv(x, qt, st, N, y=y, tiled=True, constant_weights=True)
+    torch.cuda.synchronize()
+
+    def product():
+        q8.gemv(x, qt, st, N, y=y, tiled=True, constant_weights=True, stream=side)
+
+    def layout():
+        assert q8.lib().q8_tile_device(q.data_ptr(), s.data_ptr(), K, N, qt.data_ptr(), st.data_ptr(), side.cuda_stream) == 0
+
+    assert all(p for _, _, p in captured_edges(side, lambda: (product(), product())))
+    edges = captured_edges(side, lambda: (layout(), product()))
+    starts, ends = {a for a, _, _ in edges}, {b for _, b, _ in edges}
+    first = (starts - ends).pop()
+    assert [p for a, _, p in edges if a == first] == [False]  # nothing starts early behind the layout itself
