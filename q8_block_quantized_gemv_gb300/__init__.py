@@ -815,7 +815,7 @@ class Weight4:
         flags = (FLAG_W4_ZEROS if zeros is not None else 0) | (FLAG_W4_BF16 if scales.dtype == torch.bfloat16 else 0)
         size = _w4_bytes(K, N, K // groups, flags)
         if size < 0:
-            raise ValueError("a group is 32, 64 or 128 rows")
+            raise ValueError("a group is 32, 64 or 128 rows; K is at most 2^31 - 128, and N, rounded up to 32, less than 2^31")
         self._keep(_new((size,), torch.uint8, codes.device, stream), K, N, K // groups, flags)
         _check(lib().q8_w4_tile_device(codes.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr(), K,
                                        N, self.group, flags, self.buf.data_ptr(), _stream_of(stream, codes.device)),
